@@ -30,11 +30,21 @@ QMM_BF16 = 1
 STATUS_NAMES = {
     0: "QMM_OK", 1: "QMM_ERR_NULL", 2: "QMM_ERR_BITS", 3: "QMM_ERR_SHAPE",
     4: "QMM_ERR_ALIGN", 5: "QMM_ERR_UNSUPPORTED", 6: "QMM_ERR_CUDA",
-    8: "QMM_ERR_TIMEOUT", 9: "QMM_ERR_DEVICE",
+    8: "QMM_ERR_TIMEOUT", 9: "QMM_ERR_DEVICE", 10: "QMM_ERR_INDEX",
 }
 
 # C entry points and their ctypes signatures (must match include/qmm.h)
 _P, _I, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_L, _F = ctypes.c_int64, ctypes.c_float
+
+
+class PagedKV(ctypes.Structure):
+    """qmm_paged_kv of qmm.h: a paged key / value cache and the batch that uses it."""
+    _fields_ = [("k", _P), ("v", _P), ("page_stride", _L), ("slot_stride", _L), ("head_stride", _L),
+                ("block_table", _P), ("cu_q", _P), ("kv_len", _P), ("num_pages", _I), ("page_size", _I),
+                ("blocks", _I), ("batch", _I), ("tokens", _I), ("kv_heads", _I), ("head_dim", _I), ("dtype", _I)]
+
+
 SIGNATURES = {
     "qmm_pack": ([_P, _P, _I, _I, _I, _P, _P], _I),
     "qmm_unpack": ([_P, _P, _I, _I, _I, _P], _I),
@@ -50,6 +60,9 @@ SIGNATURES = {
     "qmm_repack_bytes": ([_I, _I, _I, _I], _SZ),
     "qmm_repack": ([_P, _P, _I, _I, _I, _I, _P], _I),
     "qmm_gemv_tile16": ([_P, _I, _P, _I, _I, _P, _P, _I, _P, _I, _I, _I, _I, _P], _I),
+    "qmm_kv_append": ([_P, _P, _L, _P, _L, _P, _L, _P, _I, _P, _I, _I, _I, _P], _I),
+    "qmm_paged_attn": ([_P, _P, _L, _I, _F, _I, _I, _P, _P, _I, _I, _P, _SZ, _P], _I),
+    "qmm_paged_attn_workspace": ([_I, _I, _I, _I], _SZ),
     "qmm_device_status": ([_P], _I),
     "qmm_watchdog_selftest": ([_P], _I),
     "qmm_status_string": ([_I], ctypes.c_char_p),
@@ -66,11 +79,13 @@ _FN = {}   # name -> the configured ctypes function, filled by load()
 FAST_PATH = os.path.join(_HERE, "lib", "_qmmfast" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 _FAST_NAMES = ("qmm_gemv", "qmm_gemm", "qmm_gemv_tile16")
 _call14 = None
+_fast_append = _fast_attn = None
 _ADDR = {}   # name -> function address for _call14, filled by load()
+_append_addr = _attn_addr = 0   # the same for the paged cache calls
 
 
 def _load_fastcall(lib):
-    global _call14
+    global _call14, _fast_append, _fast_attn, _append_addr, _attn_addr
     if not os.path.exists(FAST_PATH):
         return
     try:
@@ -82,6 +97,9 @@ def _load_fastcall(lib):
     for name in _FAST_NAMES:
         _ADDR[name] = ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
     _call14 = mod.call14
+    _append_addr = ctypes.cast(lib.qmm_kv_append, ctypes.c_void_p).value
+    _attn_addr = ctypes.cast(lib.qmm_paged_attn, ctypes.c_void_p).value
+    _fast_append, _fast_attn = mod.kv_append, mod.paged_attn
 
 
 class QmmError(RuntimeError):
@@ -393,6 +411,160 @@ def qmm_quantize_act(x, xq=None, sa=None):
     _check(load().qmm_quantize_act(_ptr(x), _ptr(xq), _ptr(sa), M, K, _stream(x.device)),
            "qmm_quantize_act")
     return xq, sa
+
+
+def _paged_checks(k_cache, v_cache, block_table, cu_q, kv_len, rows, kv_rows):
+    # the argument checks of the paged cache calls one by one, for the message
+    for name, t, dt, nd in (("k_cache", k_cache, None, 4), ("v_cache", v_cache, None, 4),
+                            ("block_table", block_table, torch.int32, 2), ("cu_q", cu_q, torch.int32, 1),
+                            ("kv_len", kv_len, torch.int32, 1)):
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.dim() != nd:
+            raise ValueError(f"{name} must have {nd} dimensions")
+        if dt is not None and (t.dtype != dt or not t.is_contiguous()):
+            raise ValueError(f"{name} must be contiguous {dt}")
+    if k_cache.dtype not in _DT:
+        raise ValueError("k_cache must be float16 or bfloat16")
+    if v_cache.dtype != k_cache.dtype or v_cache.shape != k_cache.shape or v_cache.stride() != k_cache.stride():
+        raise ValueError("k_cache and v_cache must have the same type, shape and strides")
+    if k_cache.stride(3) != 1:
+        raise ValueError("the cache's last dimension must be contiguous")
+    if cu_q.shape[0] != kv_len.shape[0] + 1 or block_table.shape[0] != kv_len.shape[0]:
+        raise ValueError("cu_q must have one entry more than kv_len, block_table as many rows")
+    D = k_cache.shape[3]
+    for name, t, heads in rows:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.dim() != 3 or t.shape[2] != D or t.dtype != k_cache.dtype:
+            raise ValueError(f"{name} must be [tokens][heads][{D}] of {k_cache.dtype}")
+        if heads is not None and t.shape[1] != heads:
+            raise ValueError(f"{name} must have {heads} heads")
+        if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != D):
+            raise ValueError(f"{name}: the heads of a token must be contiguous")
+        if t.shape[0] != rows[0][1].shape[0]:
+            raise ValueError(f"{name} must have as many tokens as {rows[0][0]}")
+
+
+def qmm_kv_append(k, v, k_cache, v_cache, block_table, cu_q, kv_len, q=None, q_out=None, cos_sin=None,
+                  interleaved=False):
+    """Stores new keys and values ([tokens][kv_heads][D], any token stride) in the
+    paged cache ([pages][page_size][kv_heads][D] by index, any strides with D
+    contiguous), keys rotated by their positions with the rows of cos_sin (fp32
+    [positions][rot], cosines then sines; None: no rotation).  Sequence b owns
+    tokens cu_q[b] .. cu_q[b+1]; kv_len[b] counts its keys with the new ones;
+    block_table[b] lists its pages.  With q ([tokens][q_heads][D]) the rotated
+    queries are returned (in q_out if given), else None.  See qmm_kv_append in
+    qmm.h."""
+    dt = k_cache.dtype
+    T, hk, D = k.shape
+    P = k_cache.shape[1]
+    ok = (k.is_cuda and v.is_cuda and k_cache.is_cuda and v_cache.is_cuda and block_table.is_cuda and cu_q.is_cuda
+          and kv_len.is_cuda and dt in _DT and k.dtype is dt and v.dtype is dt and v_cache.dtype is dt
+          and k_cache.dim() == 4 and v_cache.shape == k_cache.shape and v_cache.stride() == k_cache.stride()
+          and k_cache.shape[2] == hk and k_cache.shape[3] == D and k_cache.stride(3) == 1 and v.shape == k.shape
+          and k.stride(2) == 1 and v.stride(2) == 1 and (hk == 1 or (k.stride(1) == D and v.stride(1) == D))
+          and block_table.dtype is _I32 and cu_q.dtype is _I32 and kv_len.dtype is _I32
+          and block_table.is_contiguous() and cu_q.is_contiguous() and kv_len.is_contiguous()
+          and block_table.dim() == 2 and cu_q.dim() == 1 and kv_len.dim() == 1
+          and block_table.shape[0] == kv_len.shape[0] and cu_q.shape[0] == kv_len.shape[0] + 1)
+    if ok and q is not None:
+        ok = (q.is_cuda and q.dtype is dt and q.dim() == 3 and q.shape[0] == T and q.shape[2] == D
+              and q.stride(2) == 1 and (q.shape[1] == 1 or q.stride(1) == D))
+    if not ok:
+        rows = [("k", k, k_cache.shape[2]), ("v", v, k_cache.shape[2])] + ([("q", q, None)] if q is not None else [])
+        _paged_checks(k_cache, v_cache, block_table, cu_q, kv_len, rows, hk)
+        raise ValueError("qmm_kv_append: arguments do not match")
+    rot = rope_len = 0
+    if cos_sin is not None:
+        _dev(cos_sin, "cos_sin", torch.float32)
+        rope_len, rot = cos_sin.shape
+    heads = qs = 0
+    if q is not None:
+        heads, qs = q.shape[1], q.stride(0)
+        if q_out is None:
+            q_out = torch.empty((T, heads, D), dtype=dt, device=q.device)
+        else:
+            _dev(q_out, "q_out", dt, (T, heads, D))
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if _lib is None:
+        load()
+    s0, s1, s2, _ = k_cache.stride()
+    kv = (k_cache.data_ptr(), v_cache.data_ptr(), s0, s1, s2, block_table.data_ptr(), cu_q.data_ptr(),
+          kv_len.data_ptr(), k_cache.shape[0], P, block_table.shape[1], kv_len.shape[0], T, hk, D, _DT[dt])
+    args = (k.data_ptr(), k.stride(0), v.data_ptr(), v.stride(0), None if q is None else q.data_ptr(), qs,
+            None if q_out is None else q_out.data_ptr(), heads, None if cos_sin is None else cos_sin.data_ptr(), rot,
+            rope_len, 1 if interleaved else 0, _stream(k.get_device()))
+    st = (_fast_append(_append_addr, *kv, *args) if _fast_append is not None
+          else _FN["qmm_kv_append"](ctypes.byref(PagedKV(*kv)), *args))
+    if st:
+        raise QmmError(st, "qmm_kv_append")
+    return q_out
+
+
+_I32 = torch.int32
+_WS_BYTES = {}   # (device, q_heads, kv_heads, D, max_q) -> qmm_paged_attn_workspace
+
+
+def qmm_paged_attn_workspace(q_heads: int, kv_heads: int, head_dim: int, max_q: int) -> int:
+    """Bytes of scratch a qmm_paged_attn call of these sizes needs (0 for sizes it
+    does not take)."""
+    return int(load().qmm_paged_attn_workspace(q_heads, kv_heads, head_dim, max_q))
+
+
+def qmm_paged_attn(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q, max_kv=0, scale=None, causal=True,
+                   window=0, return_lse=False, out=None, workspace=None):
+    """Attention of the new tokens q ([tokens][q_heads][D], any token stride) over
+    the paged cache, which holds their own keys and values already (arguments as
+    for qmm_kv_append).  max_q: at least the longest sequence's new tokens; max_kv:
+    at least the longest kv_len (0: unknown); scale: 1/sqrt(D) if None; window: keys
+    a token sees, its own included (0: all).  Returns out ([tokens][q_heads][D]),
+    or (out, lse) with the fp32 log sums [tokens][q_heads].  workspace: uint8
+    scratch of qmm_paged_attn_workspace() bytes, allocated if None.  See
+    qmm_paged_attn in qmm.h."""
+    dt = q.dtype
+    T, heads, D = q.shape
+    hk = k_cache.shape[2]
+    if not (q.is_cuda and k_cache.is_cuda and v_cache.is_cuda and block_table.is_cuda and cu_q.is_cuda
+            and kv_len.is_cuda and dt in _DT and k_cache.dtype is dt and v_cache.dtype is dt and k_cache.dim() == 4
+            and v_cache.shape == k_cache.shape and v_cache.stride() == k_cache.stride() and k_cache.shape[3] == D
+            and k_cache.stride(3) == 1 and q.stride(2) == 1 and (heads == 1 or q.stride(1) == D)
+            and block_table.dtype is _I32 and cu_q.dtype is _I32 and kv_len.dtype is _I32
+            and block_table.is_contiguous() and cu_q.is_contiguous() and kv_len.is_contiguous()
+            and block_table.dim() == 2 and cu_q.dim() == 1 and kv_len.dim() == 1
+            and block_table.shape[0] == kv_len.shape[0] and cu_q.shape[0] == kv_len.shape[0] + 1):
+        _paged_checks(k_cache, v_cache, block_table, cu_q, kv_len, [("q", q, None)], hk)
+        raise ValueError("qmm_paged_attn: arguments do not match")
+    if out is None:
+        out = torch.empty((T, heads, D), dtype=dt, device=q.device)
+    else:
+        _dev(out, "out", dt, (T, heads, D))
+    lse = torch.empty((T, heads), dtype=torch.float32, device=q.device) if return_lse else None
+    if _lib is None:
+        load()
+    dev = q.get_device()
+    if workspace is None:
+        key = (dev, heads, hk, D, max_q)
+        nbytes = _WS_BYTES.get(key)
+        if nbytes is None:
+            nbytes = _WS_BYTES[key] = qmm_paged_attn_workspace(heads, hk, D, max_q)
+        workspace = torch.empty(max(nbytes, 16), dtype=_U8, device=q.device)
+    else:
+        _dev(workspace, "workspace", _U8)
+        nbytes = workspace.numel()
+    s0, s1, s2, _ = k_cache.stride()
+    kv = (k_cache.data_ptr(), v_cache.data_ptr(), s0, s1, s2, block_table.data_ptr(), cu_q.data_ptr(),
+          kv_len.data_ptr(), k_cache.shape[0], k_cache.shape[1], block_table.shape[1], kv_len.shape[0], T, hk, D,
+          _DT[dt])
+    args = (q.data_ptr(), q.stride(0), heads, D ** -0.5 if scale is None else scale, 1 if causal else 0, window,
+            out.data_ptr(), None if lse is None else lse.data_ptr(), max_q, max_kv, workspace.data_ptr(), nbytes,
+            _stream(dev))
+    st = (_fast_attn(_attn_addr, *kv, *args) if _fast_attn is not None
+          else _FN["qmm_paged_attn"](ctypes.byref(PagedKV(*kv)), *args))
+    if st:
+        raise QmmError(st, "qmm_paged_attn")
+    return (out, lse) if return_lse else out
 
 
 def qmm_device_status(stream=None) -> int:

@@ -12,6 +12,7 @@
 #include "gemv.h"
 #include "w4a8.h"
 #include "gemm.h"
+#include "paged.h"
 
 namespace qmm {
 
@@ -197,6 +198,32 @@ static qmm_status check_qmm_args(const void *x, const uint8_t *packed, int bits,
     return QMM_OK;
 }
 
+// Shared checks of the paged cache calls (everything that needs no device).  A
+// batch without tokens or sequences passes with the sizes alone.
+static qmm_status check_paged(const qmm_paged_kv *kv)
+{
+    if (!kv)
+        return QMM_ERR_NULL;
+    if (kv->batch < 0 || kv->tokens < 0 || kv->num_pages < 0 || kv->page_size < 1 || kv->blocks < 0 ||
+        kv->kv_heads < 1 || kv->head_dim < 1)
+        return QMM_ERR_SHAPE;
+    if (kv->dtype != QMM_F16 && kv->dtype != QMM_BF16)
+        return QMM_ERR_UNSUPPORTED;
+    if (kv->head_dim != 64 && kv->head_dim != 128)
+        return QMM_ERR_UNSUPPORTED;
+    if (kv->page_stride % 8 || kv->slot_stride % 8 || kv->head_stride % 8)
+        return QMM_ERR_ALIGN;
+    if (kv->batch == 0 || kv->tokens == 0)
+        return QMM_OK;
+    if (!kv->cu_q || !kv->kv_len || (kv->blocks > 0 && !kv->block_table) ||
+        (kv->blocks > 0 && kv->num_pages > 0 && (!kv->k || !kv->v)))
+        return QMM_ERR_NULL;
+    if (!aligned(kv->k, 16) || !aligned(kv->v, 16) || !aligned(kv->block_table, 4) || !aligned(kv->cu_q, 4) ||
+        !aligned(kv->kv_len, 4))
+        return QMM_ERR_ALIGN;
+    return QMM_OK;
+}
+
 }  // namespace qmm
 
 using namespace qmm;
@@ -217,6 +244,7 @@ const char *qmm_status_string(qmm_status s)
     case QMM_ERR_CUDA: return "CUDA runtime or launch failure";
     case QMM_ERR_TIMEOUT: return "device watchdog expired";
     case QMM_ERR_DEVICE: return "no usable sm_103a device";
+    case QMM_ERR_INDEX: return "an index in device memory is out of range";
     }
     return "unknown status";
 }
@@ -614,6 +642,99 @@ qmm_status qmm_quantize_act(const void *x, int8_t *xq, void *sa, int M, int K, c
         return from_cuda(cudaMemsetAsync(sa, 0, static_cast<size_t>(M) * 2, stream));
     return from_cuda(launch_quantize_act(static_cast<const uint16_t *>(x), xq, static_cast<uint16_t *>(sa),
                                          M, K, stream));
+}
+
+qmm_status qmm_kv_append(const qmm_paged_kv *kv, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                         const void *q, int64_t q_stride, void *q_out, int q_heads, const float *cos_sin, int rot,
+                         int rope_len, int interleaved, cudaStream_t stream)
+{
+    const qmm_status st = check_paged(kv);
+    if (st != QMM_OK)
+        return st;
+    if (rot < 0 || rot > kv->head_dim || rot % 16 || rope_len < 0 || q_heads < 0)
+        return QMM_ERR_SHAPE;
+    if (k_stride % 8 || v_stride % 8 || (q && q_stride % 8))
+        return QMM_ERR_ALIGN;
+    if (kv->batch == 0 || kv->tokens == 0)
+        return QMM_OK;
+    if (!k || !v || (rot > 0 && !cos_sin) || !q != !q_out)
+        return QMM_ERR_NULL;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(q, 16) || !aligned(q_out, 16) || !aligned(cos_sin, 16))
+        return QMM_ERR_ALIGN;
+    const DeviceFacts *f = device_facts();
+    if (!f || f->usable != QMM_OK)
+        return QMM_ERR_DEVICE;
+    AppendParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.kv = *kv;
+    p.k = static_cast<const uint16_t *>(k);
+    p.v = static_cast<const uint16_t *>(v);
+    p.q = static_cast<const uint16_t *>(q);
+    p.q_out = static_cast<uint16_t *>(q_out);
+    p.cos_sin = cos_sin;
+    p.status = f->status;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.q_stride = q_stride;
+    p.q_heads = q ? q_heads : 0;
+    p.rot = rot;
+    p.rope_len = rope_len;
+    p.interleaved = interleaved != 0;
+    return from_cuda(launch_kv_append(p, f->num_sms, stream));
+}
+
+size_t qmm_paged_attn_workspace(int q_heads, int kv_heads, int head_dim, int max_q)
+{
+    if (q_heads < 1 || kv_heads < 1 || q_heads % kv_heads || (head_dim != 64 && head_dim != 128) || max_q < 0)
+        return 0;
+    const DeviceFacts *f = device_facts();
+    if (!f || f->usable != QMM_OK)
+        return 0;
+    return attn_workspace_bytes(q_heads, kv_heads, head_dim, max_q, f->num_sms);
+}
+
+qmm_status qmm_paged_attn(const qmm_paged_kv *kv, const void *q, int64_t q_stride, int q_heads, float scale,
+                          int causal, int window, void *out, float *lse, int max_q, int max_kv, void *workspace,
+                          size_t workspace_bytes, cudaStream_t stream)
+{
+    const qmm_status st = check_paged(kv);
+    if (st != QMM_OK)
+        return st;
+    if (q_heads < 1 || q_heads % kv->kv_heads || window < 0 || (window > 0 && !causal) || max_q < 0 || max_kv < 0 ||
+        !(scale > 0.f) || !(scale <= 3.0e38f))
+        return QMM_ERR_SHAPE;
+    if (q_stride % 8)
+        return QMM_ERR_ALIGN;
+    if (kv->batch == 0 || kv->tokens == 0 || max_q == 0)
+        return QMM_OK;
+    if (!q || !out || !workspace)
+        return QMM_ERR_NULL;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 16) || !aligned(lse, 4))
+        return QMM_ERR_ALIGN;
+    // row tiles of the batch are counted in 32 bits
+    const int group = q_heads / kv->kv_heads;
+    if ((static_cast<long long>(max_q) * group / 16 + 1) * kv->batch > 0x7fffffffLL ||
+        static_cast<long long>(kv->tokens) * group > 0x7fffffffLL)
+        return QMM_ERR_UNSUPPORTED;
+    const DeviceFacts *f = device_facts();
+    if (!f || f->usable != QMM_OK)
+        return QMM_ERR_DEVICE;
+    if (workspace_bytes < attn_workspace_bytes(q_heads, kv->kv_heads, kv->head_dim, max_q, f->num_sms))
+        return QMM_ERR_SHAPE;
+    AttnParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.kv = *kv;
+    p.q = static_cast<const uint16_t *>(q);
+    p.out = static_cast<uint16_t *>(out);
+    p.lse = lse;
+    p.status = f->status;
+    p.q_stride = q_stride;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.q_heads = q_heads;
+    p.group = group;
+    p.causal = causal != 0;
+    p.window = window;
+    return from_cuda(attn_dispatch(p, max_q, max_kv, workspace, f->num_sms, stream));
 }
 
 qmm_status qmm_watchdog_selftest(cudaStream_t stream)

@@ -1,0 +1,596 @@
+// attn_chunk.cu -- attention over the paged cache for many query rows per key head
+// (chunks of a prompt, whole prompts), on the 5th-generation tensor cores.
+//
+//   S = Q K^T,  P = 2^(S scale log2(e) - m),  O += P V,  out = O / sum P
+//
+// A work item is 256 rows ((token, query head) pairs of one key head, so that a
+// key tile loaded once serves all query heads that share it) as two streams of 128
+// rows; the keys go by in tiles of 128.  Both products run on tcgen05 with their
+// accumulators in tensor memory: per stream S (128 x 128 fp32) and O (128 x D), all
+// 512 columns at D = 128.  P takes S's place as 16-bit values and is the second
+// product's left operand straight from tensor memory; V is its right operand as it
+// lies in the cache ([key][d], the "MN-major" form), so nothing is transposed.
+//
+// Roles.  Warps 0-3 and 4-7 are the softmax of streams 0 and 1, one thread per row:
+// no exchange between lanes at all.  Warp 8 issues the products; it starts stream
+// 1's while stream 0's softmax runs and the other way round.  Warps 9-11 bring K
+// and V tiles with 16-byte asynchronous copies into a ring of kRing slots: copies
+// and not tensor maps, because they take any page size and stride, and fill the
+// slots that nobody sees (past kv_len, before the window) with zeros, which the
+// product with V needs (0 x NaN).
+//
+// The running maximum is replaced only when it grows by more than 2^8: the output
+// accumulator in tensor memory is then read, scaled and written back by its
+// stream's own threads, a few times per item; S's arrival implies that the previous
+// product into O is complete, so that needs no barrier of its own.
+//
+// Bound by the tensor cores for long prompts: 4 D flops per (row, key) pair against
+// one exponential; at one row tile by the key tiles' traffic.
+#include "gemm.cuh"
+#include "paged.cuh"
+
+namespace qmm {
+
+namespace {
+
+constexpr int kSoftWarps = 4;                       // per stream
+constexpr int kIssueWarp = 2 * kSoftWarps;
+constexpr int kLoadWarp0 = kIssueWarp + 1;
+constexpr int kLoadWarps = 3;
+constexpr int kChunkThreads = 32 * (kLoadWarp0 + kLoadWarps);
+constexpr int kRing = 5;                            // K and V tiles in shared memory
+constexpr float kChunkGrow = 8.f;
+// registers per thread after the split: 256 x 208 + 128 x 88 = 384 x 168
+constexpr int kSoftRegs = 208, kOtherRegs = 88;
+static_assert(kChunkThreads == 384, "register split");
+
+using ChunkWalk = Walk<kChunkRows, kChunkKeys, kChunkSetup>;
+
+template <int D>
+struct ChunkLayout {
+    static constexpr int kTile = 128 * D * 2;       // 128 rows of D values: D / 64 halves of [128][64]
+    static constexpr int kOffQ = 0;                 // two streams
+    static constexpr int kOffRing = 2 * kTile;
+    static constexpr int kOffBar = kOffRing + kRing * kTile;
+    // ring full / empty, q_full[2], s_full[2], p_full[2], o_full[2], drain
+    static constexpr int kNumBars = 2 * kRing + 9;
+    static constexpr int kOffTmem = kOffBar + 8 * kNumBars;
+    static constexpr int kOffShare = kOffTmem + 16;
+    static constexpr int kOffRed = kOffShare + sizeof(Share);
+    static constexpr int kOffWalk = kOffRed + 8 * (kChunkThreads / 32);
+    static constexpr int kOffSeg = kOffWalk + sizeof(ChunkWalk) * (kChunkThreads / 32);
+    // two segments per softmax warp, one per other warp
+    static constexpr int kBytes = kOffSeg + sizeof(Segment) * (kIssueWarp + kChunkThreads / 32);
+    static_assert(kOffShare % 8 == 0 && sizeof(Share) % 8 == 0 && sizeof(ChunkWalk) % 8 == 0, "alignment");
+    static_assert(kBytes <= 227 * 1024, "shared memory per block");
+};
+
+// Tensor-memory columns of stream s: S and O.
+__device__ __forceinline__ uint32_t s_col(int s) { return static_cast<uint32_t>(s) * 128u; }
+__device__ __forceinline__ uint32_t o_col(int s) { return 256u + static_cast<uint32_t>(s) * 128u; }
+
+// Byte of 16-byte chunk c of row r in a tile: halves of 64 values, rows of 128
+// bytes, chunks permuted by the row (the 128-byte swizzle).
+__device__ __forceinline__ uint32_t sw_addr(int r, int c)
+{
+    return static_cast<uint32_t>((c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+// Descriptor of a [keys][64 d] tile read along d as the N index (MN-major, 128-byte
+// swizzle): 64-value blocks of N `kHalf` bytes apart, 8-key groups 1024 bytes apart.
+__device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t saddr, uint32_t half_bytes)
+{
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFF);
+    d |= static_cast<uint64_t>((half_bytes >> 4) & 0x3FFF) << 16;   // leading byte offset: next 64 of N
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;                    // stride byte offset: next 8 keys
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(2) << 61;
+    return d;
+}
+
+// D[tmem] (+)= A[tmem] * B[smem desc], kind::f16, one CTA
+__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// 32 tensor-memory columns of this thread's lane, without waiting
+__device__ __forceinline__ void tmem_ld32_start(uint32_t taddr, uint32_t *r)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+          "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// Ties 32 loaded registers to a point after the wait, so that no use moves above it.
+__device__ __forceinline__ void pin32(uint32_t *r)
+{
+    asm volatile(""
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+    asm volatile(""
+                 : "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                   "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                   "+r"(r[30]), "+r"(r[31]));
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+        "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+        "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kChunkThreads, 1)
+attn_chunk_kernel(const __grid_constant__ AttnParams p)
+{
+    using L = ChunkLayout<D>;
+    constexpr int kChunks = D / 8;                     // 16-byte chunks per row
+    constexpr int kRowsPerCopy = 32 / kChunks;
+    constexpr float kShift = BF16 ? 0.f : 7.f;
+
+    // the operand tiles' swizzle needs 1024-byte alignment, which the start of a
+    // block's shared memory has (there is no static part); checked below
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Share &share = *reinterpret_cast<Share *>(smem + L::kOffShare);
+    long long *red = reinterpret_cast<long long *>(smem + L::kOffRed);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::kOffBar);
+    uint64_t *empty = full + kRing;
+    uint64_t *q_full = empty + kRing, *s_full = q_full + 2, *p_full = s_full + 2, *o_full = p_full + 2;
+    uint64_t *drain = o_full + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kOffTmem);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (smem_u32(smem) & 1023u) {
+        if (threadIdx.x == 0)
+            record_error(p.status, QMM_ERR_ALIGN);
+        return;
+    }
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(&full[i], kLoadWarps);
+            mbar_init(&empty[i], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&q_full[s], kSoftWarps);
+            mbar_init(&s_full[s], 1);
+            mbar_init(&p_full[s], kSoftWarps);
+            mbar_init(&o_full[s], 1);
+        }
+        mbar_init(drain, 1);
+        fence_barrier_init();
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    }
+    if (warp == kIssueWarp)
+        tmem_alloc(tmem_slot, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!p.whole && threadIdx.x == 0)
+        p.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    find_share<kChunkRows, kChunkKeys, kChunkSetup, kChunkThreads>(p, red, &share);
+
+    bool ok = true;
+    // every warp walks the share on its own, its state in shared memory (lane 0
+    // steps): registers are short in the softmax warps
+    ChunkWalk &walk = reinterpret_cast<ChunkWalk *>(smem + L::kOffWalk)[warp];
+    Segment *segs = reinterpret_cast<Segment *>(smem + L::kOffSeg) + warp + min(warp, kIssueWarp);
+    if (lane == 0)
+        walk.begin(p, share);
+    auto next = [&](Segment &s) -> bool {
+        __syncwarp();
+        bool more = false;
+        if (lane == 0)
+            more = walk.next(p, s);
+        more = __shfl_sync(0xffffffffu, more ? 1 : 0, 0) != 0;
+        __syncwarp();            // the other lanes read the segment after this
+        return more;
+    };
+
+    if (warp < kIssueWarp) {
+        // ================= softmax of stream s: one row per thread =================
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+        const int s = warp / kSoftWarps, quarter = warp % kSoftWarps;
+        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+        const uint32_t ts = tmem + lanes + s_col(s), to = tmem + lanes + o_col(s);
+        uint8_t *qs = smem + L::kOffQ + s * L::kTile;
+        uint32_t ph = 0;         // parity of the next S
+        uint32_t oph = 0;        // parity of the next O
+        // the next segment that has rows for this stream
+        auto next_rows = [&](Segment &x) -> bool {
+            while (next(x))
+                if (x.r.rows > 128 * s)
+                    return true;
+            return false;
+        };
+        // this warp's 32 query rows into the operand tile (zeros past the item); every
+        // product that read the previous ones is complete
+        auto load_q = [&](const Segment &x) {
+            const int c = lane % kChunks;
+#pragma unroll 4
+            for (int e = 0; e < 32; e += kRowsPerCopy) {
+                const int row = quarter * 32 + e + lane / kChunks;
+                const int rr = x.r.row0 + 128 * s + row, tok = rr / p.group;
+                const bool in = 128 * s + row < x.r.rows;
+                const uint16_t *src = p.q;
+                if (in)
+                    src += (x.r.t0 + tok) * p.q_stride + static_cast<long long>(x.h * p.group + rr - tok * p.group) * D + 8 * c;
+                cp_async16_or_zero(smem_u32(qs + sw_addr(row, c)), src, in);
+            }
+            cp_async_commit();
+        };
+        auto q_ready = [&]() {
+            cp_async_wait_group<0>();
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&q_full[s]);
+        };
+        int cur = 0;
+        bool have = next_rows(segs[0]);
+        if (have) {
+            load_q(segs[0]);
+            q_ready();
+        }
+        while (have) {
+            const Segment &sg = segs[cur];
+            const RowTile &r = sg.r;
+            const int row = quarter * 32 + lane;
+            const int rr = r.row0 + 128 * s + row;
+            const int units = sg.units, kb0 = (r.unit0 + sg.off) * kChunkKeys;
+            const int2 see = row_keys(p, r, rr);
+            float mref = -INFINITY, l = 0.f;
+            for (int j = 0; j < units; ++j) {
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait(&s_full[s], ph, p.status))))
+                    break;
+                ph ^= 1u;
+                tc_fence_after();
+                uint32_t v[128];
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    tmem_ld32_start(ts + 32 * c, v + 32 * c);
+                tmem_ld_wait();
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    pin32(v + 32 * c);
+                const int kb = kb0 + j * kChunkKeys;
+                const int c_lo = see.x - kb, c_hi = see.y - kb;     // the columns this row sees
+                if (__any_sync(0xffffffffu, c_lo > 0 || c_hi < kChunkKeys - 1)) {
+#pragma unroll
+                    for (int c = 0; c < 128; ++c)
+                        if (c < c_lo || c > c_hi)
+                            v[c] = 0xff800000u;                     // -infinity
+                }
+                float mx[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    mx[c] = __uint_as_float(v[c]);
+#pragma unroll
+                for (int c = 4; c < 128; c += 4)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        mx[e] = fmaxf(mx[e], __uint_as_float(v[c + e]));
+                const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+                const bool up = m > mref + kChunkGrow;
+                if (__any_sync(0xffffffffu, up)) {
+                    const float a = up ? ex2(mref - m) : 1.f;
+                    mref = up ? m : mref;
+                    l *= a;
+                    if (j > 0) {
+#pragma unroll
+                        for (int c = 0; c < D; c += 32) {
+                            uint32_t o[32];
+                            tmem_ld32_start(to + c, o);
+                            tmem_ld_wait();
+                            pin32(o);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+                            tmem_st32(to + c, o);
+                        }
+                    }
+                }
+                const float neg = kShift - (mref == -INFINITY ? 0.f : mref);
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float p0 = ex2(fmaf(__uint_as_float(v[32 * c + 2 * e]), p.scale_log2, neg));
+                        const float p1 = ex2(fmaf(__uint_as_float(v[32 * c + 2 * e + 1]), p.scale_log2, neg));
+                        sum[(2 * e) & 3] += p0;
+                        sum[(2 * e + 1) & 3] += p1;
+                        w[e] = pack16<BF16>(p0, p1);
+                    }
+                    tmem_st16(ts + 16 * c, w);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&p_full[s]);
+            }
+            if (ok)
+                ok = __all_sync(0xffffffffu, mbar_wait(&o_full[s], oph, p.status));
+            oph ^= 1u;
+            if (!ok)
+                break;
+            tc_fence_after();
+            // the next segment's queries are under way while this one's rows go out
+            have = next_rows(segs[cur ^ 1]);
+            if (have)
+                load_q(segs[cur ^ 1]);
+            // rows to memory: the item's output, or this block's part of it
+            const bool live = 128 * s + row < r.rows;
+            const bool whole = is_whole(sg);
+            const int tok = rr / p.group;
+            const long long at = static_cast<long long>(r.t0 + tok) * p.q_heads + sg.h * p.group + rr - tok * p.group;
+            const long long pr = static_cast<long long>(part_slot(sg)) * kChunkRows + 128 * s + row;
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld32_start(to + c, o);
+                tmem_ld_wait();
+                pin32(o);
+                if (live && whole) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(p.out + at * D + c);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int f = 0; f < 4; ++f)
+                            w[f] = pack16<BF16>(__uint_as_float(o[8 * e + 2 * f]) * inv,
+                                                __uint_as_float(o[8 * e + 2 * f + 1]) * inv);
+                        dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                } else if (live) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(p.part_o + pr * D + c);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                }
+            }
+            if (live && whole && p.lse)
+                p.lse[at] = l > 0.f ? (mref - kShift + log2f(l)) * 0.6931471805599453f : -INFINITY;
+            if (live && !whole)
+                *reinterpret_cast<float2 *>(p.part_ml + pr * 2) = make_float2(mref, l);
+            tc_fence_before();   // the accumulators are read; the next P says so to the issuing warp
+            if (threadIdx.x == 0 && is_last_part(sg))
+                p.meta[blockIdx.x] = make_int4(sg.i, sg.h, sg.first, 0);
+            if (have)
+                q_ready();
+            cur ^= 1;
+        }
+        cp_async_wait_group<0>();
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp == kIssueWarp) {
+            // ================= product issue =================
+            {
+                const Segment &sg = segs[0];
+                const uint32_t id_qk = f16_idesc(BF16, 128, kChunkKeys);
+                const uint32_t id_pv = f16_idesc(BF16, 128, D) | (1u << 16);   // B is MN-major
+                const uint64_t q_desc = sw128_desc(smem_u32(smem + L::kOffQ));
+                const uint64_t k_desc = sw128_desc(smem_u32(smem + L::kOffRing));
+                const uint64_t v_desc = sw128_desc_mn(smem_u32(smem + L::kOffRing), 128 * 128);
+                int slot = 0;            // ring slot of the next tile (K_0 V_0 K_1 V_1 ...)
+                uint32_t par = 0;
+                uint32_t qph[2] = {0, 0}, pph[2] = {0, 0};
+                auto advance = [&]() {
+                    if (++slot == kRing) {
+                        slot = 0;
+                        par ^= 1u;
+                    }
+                };
+                // S of stream s from the K tile in slot ks
+                auto qk = [&](int s, int ks) {
+                    const uint64_t a = q_desc + ((s * L::kTile) >> 4), b = k_desc + ((ks * L::kTile) >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t step = (kk >> 2) * (128 * 128 / 16) + (kk & 3) * 2;
+                        tc_mma(tmem + s_col(s), a + step, b + step, id_qk, kk > 0 ? 1u : 0u);
+                    }
+                    tc_commit(&s_full[s]);
+                };
+                bool busy = false;
+                while (next(segs[0])) {
+                    if (lane != 0 || !ok)
+                        continue;
+                    const int ns = sg.r.rows > 128 ? 2 : 1;
+                    if (!(ok = mbar_wait(&full[slot], par, p.status)))
+                        continue;
+                    for (int s = 0; s < ns && ok; ++s) {
+                        if (!(ok = mbar_wait(&q_full[s], qph[s], p.status)))
+                            break;
+                        qph[s] ^= 1u;
+                        tc_fence_after();
+                        qk(s, slot);
+                        busy = true;
+                    }
+                    if (!ok)
+                        continue;
+                    tc_commit(&empty[slot]);
+                    advance();
+                    for (int j = 0; j < sg.units && ok; ++j) {
+                        const int vs = slot;
+                        if (!(ok = mbar_wait(&full[slot], par, p.status)))
+                            break;
+                        advance();
+                        const bool more = j + 1 < sg.units;
+                        for (int s = 0; s < ns; ++s) {
+                            if (!(ok = mbar_wait(&p_full[s], pph[s], p.status)))
+                                break;
+                            pph[s] ^= 1u;
+                            tc_fence_after();
+                            const uint64_t b = v_desc + ((vs * L::kTile) >> 4);
+#pragma unroll
+                            for (int kk = 0; kk < kChunkKeys / 16; ++kk)
+                                tc_mma_ts(tmem + o_col(s), tmem + s_col(s) + 8 * kk, b + kk * (2048 >> 4), id_pv,
+                                          kk > 0 || j > 0 ? 1u : 0u);
+                            if (s == ns - 1)
+                                tc_commit(&empty[vs]);
+                            if (more) {
+                                if (s == 0 && !(ok = mbar_wait(&full[slot], par, p.status)))
+                                    break;
+                                tc_fence_after();
+                                qk(s, slot);
+                            } else {
+                                tc_commit(&o_full[s]);
+                            }
+                        }
+                        if (ok && more) {
+                            tc_commit(&empty[slot]);
+                            advance();
+                        }
+                    }
+                }
+                // drain: every product issued has completed (each barrier phase that a
+                // softmax warp waits on covers the products before it; after a timeout
+                // wait for them here)
+                if (lane == 0 && busy && !ok) {
+                    tc_commit(drain);
+                    mbar_wait(drain, 0, p.status);
+                }
+            }
+            __syncwarp();
+        } else {
+            // ================= K and V tiles =================
+            constexpr int kGroups = kChunkKeys / kRowsPerCopy;      // warp-wide copies per tile
+            const int w = warp - kLoadWarp0;
+            const int sub = lane / kChunks, chunk = lane % kChunks;
+            const uint32_t ring = smem_u32(smem + L::kOffRing);
+            int issued = 0, signalled = 0;      // tiles
+            // tiles [signalled, upto) have landed: make them visible to the products
+            auto signal = [&](int upto) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    for (int i = signalled; i < upto; ++i)
+                        mbar_arrive(&full[i % kRing]);
+                signalled = upto;
+            };
+            const Segment &sg = segs[0];
+            while (ok && next(segs[0])) {
+                const RowTile r = sg.r;
+                const uint16_t *base[2] = {static_cast<const uint16_t *>(p.kv.k) + sg.h * p.kv.head_stride,
+                                           static_cast<const uint16_t *>(p.kv.v) + sg.h * p.kv.head_stride};
+                for (int j = 0; j < sg.units && ok; ++j) {
+                    const int kb = (r.unit0 + sg.off + j) * kChunkKeys;
+                    // the lane looks up the places of two of the rows this warp copies: copy i
+                    // (i = 0, 1, ...) covers rows kRowsPerCopy (w + kLoadWarps i) + (0 .. kRowsPerCopy)
+                    long long place[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int idx = lane + 32 * e;
+                        const int grp = w + kLoadWarps * (idx / kRowsPerCopy);
+                        const int key = kb + grp * kRowsPerCopy + idx % kRowsPerCopy;
+                        place[e] = grp < kGroups && key >= r.lo && key < r.hi ? key_offset(p.kv, r.b, key, p.status) : -1;
+                    }
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {           // K, then V
+                        const int slot = issued % kRing, round = issued / kRing;
+                        if (round > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait(&empty[slot], (round - 1) & 1, p.status))))
+                            break;
+                        const uint32_t dst = ring + slot * L::kTile;
+#pragma unroll 4
+                        for (int i = 0; w + kLoadWarps * i < kGroups; ++i) {
+                            const int idx = i * kRowsPerCopy + sub;
+                            const long long o0 = __shfl_sync(0xffffffffu, place[0], idx & 31);
+                            const long long o1 = __shfl_sync(0xffffffffu, place[1], idx & 31);
+                            const long long o = idx < 32 ? o0 : o1;
+                            const int row = (w + kLoadWarps * i) * kRowsPerCopy + sub;
+                            cp_async16_or_zero(dst + sw_addr(row, chunk), base[half] + (o >= 0 ? o : 0) + chunk * 8, o >= 0);
+                        }
+                        cp_async_commit();
+                        ++issued;
+                        // keep three tiles under way
+                        cp_async_wait_group<3>();
+                        if (issued - 3 > signalled)
+                            signal(issued - 3);
+                    }
+                }
+            }
+            cp_async_wait_group<0>();
+            signal(issued);
+        }
+    }
+
+    // teardown: every role is done (or gave up); release tensor memory
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kIssueWarp)
+        tmem_dealloc(tmem, 512);
+}
+
+template <int D, bool BF16>
+cudaError_t launch_chunk_attn(const AttnParams &p, int grid, cudaStream_t stream)
+{
+    constexpr int smem = ChunkLayout<D>::kBytes;
+    static SmemLimit limit;
+    if (const cudaError_t e = ensure_smem_limit(limit, attn_chunk_kernel<D, BF16>, smem, true); e != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kChunkThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_chunk_kernel<D, BF16>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_chunk(const AttnParams &p, int grid, cudaStream_t stream)
+{
+    const bool bf16 = p.kv.dtype == QMM_BF16;
+    if (p.kv.head_dim == 128)
+        return bf16 ? launch_chunk_attn<128, true>(p, grid, stream) : launch_chunk_attn<128, false>(p, grid, stream);
+    return bf16 ? launch_chunk_attn<64, true>(p, grid, stream) : launch_chunk_attn<64, false>(p, grid, stream);
+}
+
+}  // namespace qmm

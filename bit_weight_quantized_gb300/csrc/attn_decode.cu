@@ -1,0 +1,350 @@
+// attn_decode.cu -- attention over the paged cache for few query rows per key head
+// (single tokens, short drafts): at most 16 rows (token, query head of the key
+// head) per work item, which one m16 matrix-instruction tile holds.
+//
+//   s_j = scale <q, K_j>,  out = sum_j 2^(s_j' - m) V_j / sum_j 2^(s_j' - m),  s' = s log2(e)
+//
+// Bound by reading K and V once from HBM: every key costs 4 D bytes and at most
+// 16 * 4 D flops, far below the tensor cores' ratio, so mma.sync is enough and the
+// work is to keep reads in flight.  Each of a block's four warps walks its own 16
+// keys of every 64-key unit with its own ring of asynchronous copies (kStages x 16
+// keys of K and V), running maximum, sum and 16 x D fp32 output in registers: no
+// barrier and no exchange between warps until the segment ends.  Two blocks per SM
+// keep 2 x 4 warps x (kStages - 1) x 16 keys x 4 D bytes in flight (128 KB at
+// D = 128).  At the end of a segment the warps' results meet in shared memory.
+// Long axes are split over all blocks (find_share) and joined by the combine kernel.
+//
+// The running maximum is replaced only when it grows by more than 2^8 (the scale
+// factors stay within fp32 and fp16 range either way), so the output is rescaled
+// a few times per segment rather than in every tile.  fp16 weights are scaled by
+// 2^7: 2^(s' - m + 7) <= 2^15 stays finite and weights down to 2^-21 of the maximum
+// keep all their bits (fp16 loses bits below 2^-14).
+#include "paged.cuh"
+
+namespace qmm {
+
+namespace {
+
+constexpr int kDecWarps = 4;
+constexpr int kDecThreads = 32 * kDecWarps;
+constexpr int kDecStages = 3;
+constexpr int kWarpKeys = kDecodeKeys / kDecWarps;   // 16
+constexpr float kGrow = 8.f;                         // log2 of the growth that replaces the maximum
+
+template <int D>
+struct DecLayout {
+    static constexpr int kTile = kWarpKeys * D * 2;                       // 16 keys of K or V
+    static constexpr int kWarpBytes = kDecStages * 2 * kTile;
+    static constexpr int kOffQ = kDecWarps * kWarpBytes;
+    static constexpr int kBytes = kOffQ + kDecodeRows * D * 2;
+    static constexpr int kPitch = D + 8;                                  // floats per row of a warp's output
+    static_assert(kDecWarps * kDecodeRows * (kPitch + 2) * 4 <= kOffQ, "the warps' outputs reuse the rings");
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+template <bool BF16>
+__device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    if constexpr (BF16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+            "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        mma_f16_16816(d, a[0], a[1], a[2], a[3], b0, b1);
+}
+
+// Shared-memory byte of 16-byte chunk c of row r in a tile of D-value rows: chunks
+// are permuted by the row so that eight rows of one chunk column (one ldmatrix
+// matrix) lie in different banks.
+template <int D>
+__device__ __forceinline__ uint32_t tile_addr(int r, int c)
+{
+    return static_cast<uint32_t>(r * D * 2 + ((c ^ (r & 7)) << 4));
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kDecThreads, kDecodeBlocksPerSm)
+attn_decode_kernel(const __grid_constant__ AttnParams p)
+{
+    using L = DecLayout<D>;
+    constexpr int kChunks = D / 8;                 // 16-byte chunks per row
+    constexpr int kRowsPerCopy = 32 / kChunks;     // rows one warp-wide copy covers
+    constexpr int kCopies = kWarpKeys / kRowsPerCopy;
+    constexpr float kShift = BF16 ? 0.f : 7.f;
+
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ Share share;
+    __shared__ long long red[kDecWarps];
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g = lane >> 2, t = lane & 3;
+    if (tid == 0)
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    find_share<kDecodeRows, kDecodeKeys, kDecodeSetup, kDecThreads>(p, red, &share);
+
+    const uint32_t sbase = smem_u32(smem);
+    const uint32_t ring = sbase + warp * L::kWarpBytes;
+    const uint32_t qs = sbase + L::kOffQ;
+    // the lane's row and chunk in a warp-wide copy
+    const int crow = lane / kChunks, cchunk = lane % kChunks;
+    // its ldmatrix row and chunk: K (keys as the n index), V (transposed)
+    const int krow = (lane & 7) + ((lane >> 4) << 3), kch = (lane >> 3) & 1;
+    const int vrow = lane & 15, vch = lane >> 4;
+
+    if (!p.whole && tid == 0)
+        p.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
+
+    Walk<kDecodeRows, kDecodeKeys, kDecodeSetup> walk;
+    walk.begin(p, share);
+    Segment sg;
+    while (walk.next(p, sg)) {
+        const RowTile &r = sg.r;
+        const uint16_t *kbase = static_cast<const uint16_t *>(p.kv.k) + sg.h * p.kv.head_stride;
+        const uint16_t *vbase = static_cast<const uint16_t *>(p.kv.v) + sg.h * p.kv.head_stride;
+        const int key0 = (r.unit0 + sg.off) * kDecodeKeys + warp * kWarpKeys;   // the warp's first key
+
+        // offset of key (tile j, row lane & 15), or -1 where nothing is read
+        auto place = [&](int j) -> long long {
+            const int key = key0 + j * kDecodeKeys + (lane & 15);
+            return j < sg.units && key >= r.lo && key < r.hi ? key_offset(p.kv, r.b, key, p.status) : -1;
+        };
+        auto load = [&](int j, long long off) {
+            const uint32_t dst = ring + (j % kDecStages) * (2 * L::kTile);
+#pragma unroll
+            for (int c = 0; c < kCopies; ++c) {
+                const int row = c * kRowsPerCopy + crow;
+                const long long o = __shfl_sync(0xffffffffu, off, row);
+                const bool ok = o >= 0;
+                const long long e = (ok ? o : 0) + cchunk * 8;
+                cp_async16_or_zero(dst + tile_addr<D>(row, cchunk), kbase + e, ok);
+                cp_async16_or_zero(dst + L::kTile + tile_addr<D>(row, cchunk), vbase + e, ok);
+            }
+        };
+
+        long long ahead = place(0);
+#pragma unroll
+        for (int j = 0; j < kDecStages - 1; ++j) {
+            if (j < sg.units)
+                load(j, ahead);
+            cp_async_commit();
+            ahead = place(j + 1);
+        }
+
+        // queries: 16 rows, zero past the tile, to registers in fragment order
+        for (int e = tid; e < kDecodeRows * kChunks; e += kDecThreads) {
+            const int row = e / kChunks, c = e % kChunks;
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (row < r.rows) {
+                const int rr = r.row0 + row, tok = rr / p.group;
+                v = *reinterpret_cast<const uint4 *>(p.q + (r.t0 + tok) * p.q_stride +
+                                                     static_cast<long long>(sg.h * p.group + rr - tok * p.group) * D + 8 * c);
+            }
+            *reinterpret_cast<uint4 *>(smem + L::kOffQ + tile_addr<D>(row, c)) = v;
+        }
+        __syncthreads();
+        uint32_t qf[D / 16][4];
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+            ldsm4(qf[kk], qs + tile_addr<D>(lane & 15, 2 * kk + (lane >> 4)));
+
+        const int2 see0 = row_keys(p, r, r.row0 + g), see1 = row_keys(p, r, r.row0 + g + 8);
+        // keys that every row of the tile sees (rows past the tile do not count)
+        const int2 sa = row_keys(p, r, r.row0), sz = row_keys(p, r, r.row0 + r.rows - 1);
+        const int all_lo = sz.x, all_hi = sa.y;
+
+        float o[D / 8][4];
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                o[n][e] = 0.f;
+        float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+
+#pragma unroll 1
+        for (int j = 0; j < sg.units; ++j) {
+            if (j + kDecStages - 1 < sg.units)
+                load(j + kDecStages - 1, ahead);
+            cp_async_commit();
+            ahead = place(j + kDecStages);
+            cp_async_wait_group<kDecStages - 1>();
+            __syncwarp();
+            const int kb = key0 + j * kDecodeKeys;
+            if (kb < r.hi && kb + kWarpKeys > r.lo) {
+                const uint32_t ks = ring + (j % kDecStages) * (2 * L::kTile), vs = ks + L::kTile;
+                float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    uint32_t kf[4];
+                    ldsm4(kf, ks + tile_addr<D>(krow, 2 * kk + kch));
+                    mma16<BF16>(s[0], qf[kk], kf[0], kf[1]);
+                    mma16<BF16>(s[1], qf[kk], kf[2], kf[3]);
+                }
+                if (kb < all_lo || kb + kWarpKeys - 1 > all_hi) {
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int key = kb + 8 * n + 2 * t + e;
+                            if (key < see0.x || key > see0.y)
+                                s[n][e] = -INFINITY;
+                            if (key < see1.x || key > see1.y)
+                                s[n][2 + e] = -INFINITY;
+                        }
+                }
+                float x0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1])) * p.scale_log2;
+                float x1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3])) * p.scale_log2;
+                x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
+                x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
+                x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
+                x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
+                const bool up0 = x0 > m0 + kGrow, up1 = x1 > m1 + kGrow;
+                if (__any_sync(0xffffffffu, up0 || up1)) {
+                    const float a0 = up0 ? ex2(m0 - x0) : 1.f, a1 = up1 ? ex2(m1 - x1) : 1.f;
+                    m0 = up0 ? x0 : m0;
+                    m1 = up1 ? x1 : m1;
+                    l0 *= a0;
+                    l1 *= a1;
+#pragma unroll
+                    for (int n = 0; n < D / 8; ++n) {
+                        o[n][0] *= a0;
+                        o[n][1] *= a0;
+                        o[n][2] *= a1;
+                        o[n][3] *= a1;
+                    }
+                }
+                const float n0 = kShift - (m0 == -INFINITY ? 0.f : m0), n1 = kShift - (m1 == -INFINITY ? 0.f : m1);
+                uint32_t pf[4];
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const float p0 = ex2(fmaf(s[n][0], p.scale_log2, n0)), p1 = ex2(fmaf(s[n][1], p.scale_log2, n0));
+                    const float p2 = ex2(fmaf(s[n][2], p.scale_log2, n1)), p3 = ex2(fmaf(s[n][3], p.scale_log2, n1));
+                    l0 += p0 + p1;
+                    l1 += p2 + p3;
+                    pf[2 * n] = pack16<BF16>(p0, p1);
+                    pf[2 * n + 1] = pack16<BF16>(p2, p3);
+                }
+#pragma unroll
+                for (int n = 0; n < D / 16; ++n) {
+                    uint32_t vf[4];
+                    ldsm4_t(vf, vs + tile_addr<D>(vrow, 2 * n + vch));
+                    mma16<BF16>(o[2 * n], pf, vf[0], vf[1]);
+                    mma16<BF16>(o[2 * n + 1], pf, vf[2], vf[3]);
+                }
+            }
+            __syncwarp();   // every lane has read the slot before it is filled again
+        }
+        cp_async_wait_group<0>();
+#pragma unroll
+        for (int d = 1; d < 4; d <<= 1) {
+            l0 += __shfl_xor_sync(0xffffffffu, l0, d);
+            l1 += __shfl_xor_sync(0xffffffffu, l1, d);
+        }
+
+        // the warps' maxima, sums and outputs meet in shared memory (over the rings)
+        __syncthreads();
+        float *wo = reinterpret_cast<float *>(smem);
+        float *wml = wo + kDecWarps * kDecodeRows * L::kPitch;
+        {
+            float *w0 = wo + (warp * kDecodeRows + g) * L::kPitch, *w1 = w0 + 8 * L::kPitch;
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n) {
+                *reinterpret_cast<float2 *>(w0 + 8 * n + 2 * t) = make_float2(o[n][0], o[n][1]);
+                *reinterpret_cast<float2 *>(w1 + 8 * n + 2 * t) = make_float2(o[n][2], o[n][3]);
+            }
+            if (t == 0) {
+                *reinterpret_cast<float2 *>(wml + (warp * kDecodeRows + g) * 2) = make_float2(m0, l0);
+                *reinterpret_cast<float2 *>(wml + (warp * kDecodeRows + g + 8) * 2) = make_float2(m1, l1);
+            }
+        }
+        __syncthreads();
+        const bool whole = is_whole(sg);
+        const int slot = part_slot(sg);
+        for (int e = tid; e < r.rows * (D / 4); e += kDecThreads) {
+            const int row = e / (D / 4), c = 4 * (e % (D / 4));
+            float m = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kDecWarps; ++w)
+                m = fmaxf(m, wml[(w * kDecodeRows + row) * 2]);
+            const float base = m == -INFINITY ? 0.f : m;
+            float l = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kDecWarps; ++w) {
+                const float2 ml = *reinterpret_cast<const float2 *>(wml + (w * kDecodeRows + row) * 2);
+                const float a = ex2(ml.x - base);
+                const float4 v = *reinterpret_cast<const float4 *>(wo + (w * kDecodeRows + row) * L::kPitch + c);
+                l = fmaf(a, ml.y, l);
+                acc.x = fmaf(a, v.x, acc.x);
+                acc.y = fmaf(a, v.y, acc.y);
+                acc.z = fmaf(a, v.z, acc.z);
+                acc.w = fmaf(a, v.w, acc.w);
+            }
+            if (whole) {
+                const int rr = r.row0 + row, tok = rr / p.group;
+                const long long at = static_cast<long long>(r.t0 + tok) * p.q_heads + sg.h * p.group + rr - tok * p.group;
+                const float inv = l > 0.f ? 1.f / l : 0.f;
+                *reinterpret_cast<uint2 *>(p.out + at * D + c) =
+                    make_uint2(pack16<BF16>(acc.x * inv, acc.y * inv), pack16<BF16>(acc.z * inv, acc.w * inv));
+                if (p.lse && c == 0)
+                    p.lse[at] = l > 0.f ? (m - kShift + log2f(l)) * 0.6931471805599453f : -INFINITY;
+            } else {
+                *reinterpret_cast<float4 *>(p.part_o + (static_cast<long long>(slot) * kDecodeRows + row) * D + c) = acc;
+                if (c == 0)
+                    *reinterpret_cast<float2 *>(p.part_ml + (static_cast<long long>(slot) * kDecodeRows + row) * 2) =
+                        make_float2(m, l);
+            }
+        }
+        if (tid == 0 && is_last_part(sg))
+            p.meta[blockIdx.x] = make_int4(sg.i, sg.h, sg.first, 0);
+        __syncthreads();   // the rings and the query tile are free again
+    }
+}
+
+template <int D, bool BF16>
+cudaError_t launch_decode_attn(const AttnParams &p, int grid, cudaStream_t stream)
+{
+    constexpr int smem = DecLayout<D>::kBytes;
+    static SmemLimit limit;
+    if (const cudaError_t e = ensure_smem_limit(limit, attn_decode_kernel<D, BF16>, smem, true); e != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kDecThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_decode_kernel<D, BF16>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_decode(const AttnParams &p, int grid, cudaStream_t stream)
+{
+    const bool bf16 = p.kv.dtype == QMM_BF16;
+    if (p.kv.head_dim == 128)
+        return bf16 ? launch_decode_attn<128, true>(p, grid, stream) : launch_decode_attn<128, false>(p, grid, stream);
+    return bf16 ? launch_decode_attn<64, true>(p, grid, stream) : launch_decode_attn<64, false>(p, grid, stream);
+}
+
+}  // namespace qmm

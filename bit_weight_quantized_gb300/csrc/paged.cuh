@@ -1,0 +1,303 @@
+// paged.cuh -- device helpers of the paged key / value cache kernels: places in
+// the cache, asynchronous 16-byte copies, 16-bit conversions, and the split of an
+// attention call's work over the blocks.
+#pragma once
+
+#include "common.cuh"
+#include "paged.h"
+
+namespace qmm {
+
+namespace {
+
+// ---- small numeric helpers ------------------------------------------------------
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// fp32 -> two 16-bit values (lo = a), round to nearest even
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack16(float a, float b)
+{
+    uint32_t d;
+    if constexpr (BF16)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(b), "f"(a));
+    else
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(b), "f"(a));
+    return d;
+}
+
+template <bool BF16>
+__device__ __forceinline__ float lo16(uint32_t w)
+{
+    return BF16 ? __uint_as_float(w << 16) : f16_bits_to_f32(static_cast<uint16_t>(w));
+}
+
+template <bool BF16>
+__device__ __forceinline__ float hi16(uint32_t w)
+{
+    return BF16 ? __uint_as_float(w & 0xFFFF0000u) : f16_bits_to_f32(static_cast<uint16_t>(w >> 16));
+}
+
+// ---- asynchronous copies --------------------------------------------------------
+// 16 bytes global -> shared through L2; with ok == false 16 zero bytes (nothing is
+// read, `src` only has to be a valid address).
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void *src, bool ok)
+{
+    const int n = ok ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+template <int N>
+__device__ __forceinline__ void cp_async_wait_group()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// ---- the batch ----------------------------------------------------------------------
+// The new tokens of sequence b: first token and count, held to 0 .. tokens.
+__device__ __forceinline__ int2 seq_tokens(const qmm_paged_kv &kv, int b)
+{
+    const int t0 = min(max(kv.cu_q[b], 0), kv.tokens);
+    const int t1 = min(max(kv.cu_q[b + 1], t0), kv.tokens);
+    return make_int2(t0, t1 - t0);
+}
+
+// Keys of sequence b, held to what its row of the block table can hold.
+__device__ __forceinline__ int seq_keys(const qmm_paged_kv &kv, int b, int *status)
+{
+    const int n = kv.kv_len[b];
+    const long long most = static_cast<long long>(kv.blocks) * kv.page_size;
+    if (n > most) {
+        record_error(status, QMM_ERR_INDEX);
+        return static_cast<int>(most);
+    }
+    return max(n, 0);
+}
+
+// Element offset of (sequence b, key, head 0) in the cache, or -1 (recorded) for a
+// page number out of range.  key is in [0, blocks * page_size).
+__device__ __forceinline__ long long key_offset(const qmm_paged_kv &kv, int b, int key, int *status)
+{
+    const unsigned blk = static_cast<unsigned>(key) / static_cast<unsigned>(kv.page_size);
+    const int slot = key - static_cast<int>(blk) * kv.page_size;
+    const int page = kv.block_table[static_cast<long long>(b) * kv.blocks + blk];
+    if (page < 0 || page >= kv.num_pages) {
+        record_error(status, QMM_ERR_INDEX);
+        return -1;
+    }
+    return page * kv.page_stride + slot * kv.slot_stride;
+}
+
+// ---- the split of an attention call --------------------------------------------------
+// An item is one row tile of one sequence with one key head: ROWS consecutive rows
+// of the sequence's (token, query head of the key head) pairs, token-major, with the
+// keys [lo, hi) that any of them sees.  Its work is counted in units of KEYS keys
+// (aligned to KEYS), at least one so that rows without keys are written too.
+struct RowTile {
+    int b;          // sequence
+    int t0;         // its first new token
+    int n;          // its new tokens
+    int row0;       // first row of the tile
+    int rows;       // rows in the tile (0: the tile does not exist)
+    int kv;         // keys of the sequence
+    int lo, hi;     // keys some row of the tile sees
+    int unit0, units;
+};
+
+template <int ROWS, int KEYS>
+__device__ __forceinline__ RowTile row_tile(const AttnParams &p, int i)
+{
+    RowTile r;
+    r.b = i / p.row_tiles;
+    r.row0 = (i - r.b * p.row_tiles) * ROWS;
+    const int2 tn = seq_tokens(p.kv, r.b);
+    r.t0 = tn.x;
+    r.n = tn.y;
+    const long long all = static_cast<long long>(r.n) * p.group;
+    r.rows = static_cast<int>(min(static_cast<long long>(ROWS), max(0LL, all - r.row0)));
+    r.kv = seq_keys(p.kv, r.b, p.status);
+    r.lo = r.hi = r.unit0 = r.units = 0;
+    if (r.rows == 0)
+        return r;
+    const int first = r.kv - r.n + r.row0 / p.group;                       // position of the first row
+    const int last = r.kv - r.n + (r.row0 + r.rows - 1) / p.group;
+    r.hi = p.causal ? min(r.kv, max(0, last + 1)) : r.kv;
+    r.lo = p.window > 0 ? min(r.hi, max(0, first - p.window + 1)) : 0;
+    r.unit0 = r.lo / KEYS;
+    r.units = max(1, (r.hi + KEYS - 1) / KEYS - r.unit0);
+    return r;
+}
+
+// Visible keys [jmin, jmax] of row `row` (of the whole sequence) in the tile's
+// sequence; an empty range for rows past the tile.
+__device__ __forceinline__ int2 row_keys(const AttnParams &p, const RowTile &r, int row)
+{
+    if (row >= r.row0 + r.rows)
+        return make_int2(0, -1);
+    const int pos = r.kv - r.n + row / p.group;
+    return make_int2(p.window > 0 ? max(0, pos - p.window + 1) : 0, p.causal ? min(r.kv - 1, pos) : r.kv - 1);
+}
+
+// Where a block's share of the work starts.  All items of the call lie on one
+// line, row tiles in order, key heads within a row tile; an item is SETUP + units
+// long (SETUP: what starting and finishing an item costs, in units; its first unit
+// lies SETUP behind its start).  Block c takes the stretch [c * chunk, (c + 1) *
+// chunk), chunk = max(min_chunk, total / grid rounded up), so every block has the
+// same work however ragged the batch is.  An item that crosses a block's border
+// leaves partial results (at most two per block) that the combine kernel joins.
+// The split depends on the lengths alone, so results are the same run to run.
+struct Share {
+    long long at, end;       // the block's stretch
+    long long chunk;
+    long long start;         // where the item (i, h) that holds `at` starts
+    int i, h;                // row tile and key head of it
+};
+
+// Called by all THREADS threads of the block; `red` is scratch of THREADS / 32
+// words of 8 bytes, `out` the shared result.
+template <int ROWS, int KEYS, int SETUP, int THREADS>
+__device__ __forceinline__ void find_share(const AttnParams &p, long long *red, Share *out)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (p.whole) {   // block c holds item c
+        if (tid == 0) {
+            const int i = blockIdx.x / p.kv.kv_heads;
+            const RowTile r = row_tile<ROWS, KEYS>(p, i);
+            out->i = i;
+            out->h = blockIdx.x - i * p.kv.kv_heads;
+            out->at = out->start = 0;
+            out->end = r.units ? SETUP + r.units : 0;
+            out->chunk = 1LL << 40;
+            if (r.row0 == 0 && static_cast<long long>(r.n) * p.group > static_cast<long long>(p.row_tiles) * ROWS)
+                record_error(p.status, QMM_ERR_INDEX);
+        }
+        __syncthreads();
+        return;
+    }
+    const int tiles = p.kv.batch * p.row_tiles;
+    const int per = (tiles + THREADS - 1) / THREADS;
+    const int i0 = min(tiles, tid * per), i1 = min(tiles, i0 + per);
+    long long sum = 0;
+    for (int i = i0; i < i1; ++i) {
+        const RowTile r = row_tile<ROWS, KEYS>(p, i);
+        sum += static_cast<long long>(r.units ? SETUP + r.units : 0) * p.kv.kv_heads;
+        if (r.row0 == 0 && static_cast<long long>(r.n) * p.group > static_cast<long long>(p.row_tiles) * ROWS)
+            record_error(p.status, QMM_ERR_INDEX);   // more new tokens than max_q
+    }
+    long long incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o)
+            incl += v;
+    }
+    if (lane == 31)
+        red[warp] = incl;
+    if (tid == 0)
+        out->at = out->end = 0;
+    __syncthreads();
+    long long base = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+        const long long v = red[w];
+        if (w < warp)
+            base += v;
+        total += v;
+    }
+    const long long before = base + incl - sum;
+    const long long chunk = max(static_cast<long long>(p.min_chunk), (total + gridDim.x - 1) / gridDim.x);
+    const long long at = chunk * blockIdx.x;
+    if (tid == 0)
+        out->chunk = chunk;
+    if (at < total && before <= at && at < before + sum) {
+        long long start = before;
+        for (int i = i0; i < i1; ++i) {
+            const RowTile r = row_tile<ROWS, KEYS>(p, i);
+            const int len = r.units ? SETUP + r.units : 0;
+            const long long all = static_cast<long long>(len) * p.kv.kv_heads;
+            if (at < start + all) {
+                out->i = i;
+                out->h = static_cast<int>((at - start) / len);
+                out->start = start + static_cast<long long>(out->h) * len;
+                out->at = at;
+                out->end = min(total, at + chunk);
+                break;
+            }
+            start += all;
+        }
+    }
+    __syncthreads();
+}
+
+// One segment of a block's share: `units` >= 1 units from unit `off` of item (row
+// tile i, head h); `first`: the block that holds the item's unit 0.
+struct Segment {
+    RowTile r;
+    int i, h, off, units, first;
+};
+
+// Walks a share.  next() gives its segments in order.
+template <int ROWS, int KEYS, int SETUP>
+struct Walk {
+    long long at, end, chunk, start;
+    int i, h;
+    RowTile r;
+    __device__ __forceinline__ void begin(const AttnParams &p, const Share &s)
+    {
+        at = s.at;
+        end = s.end;
+        chunk = s.chunk;
+        start = s.start;
+        i = s.i;
+        h = s.h;
+        if (at < end)
+            r = row_tile<ROWS, KEYS>(p, i);
+    }
+    __device__ __forceinline__ bool next(const AttnParams &p, Segment &s)
+    {
+        while (at < end) {
+            const int len = SETUP + r.units;
+            if (at >= start + len) {   // on to the next item
+                start += len;
+                if (++h == p.kv.kv_heads) {
+                    h = 0;
+                    do {
+                        if (++i >= p.kv.batch * p.row_tiles)
+                            return false;   // not reached: the stretch ahead belongs to some tile
+                        r = row_tile<ROWS, KEYS>(p, i);
+                    } while (r.units == 0);
+                }
+                continue;
+            }
+            const long long to = min(end, start + len);
+            const int a = max(0, static_cast<int>(at - start) - SETUP), b = static_cast<int>(to - start) - SETUP;
+            at = to;
+            if (b <= a)
+                continue;              // only the item's start-up lies here
+            s.r = r;
+            s.i = i;
+            s.h = h;
+            s.off = a;
+            s.units = b - a;
+            s.first = static_cast<int>((start + SETUP) / chunk);
+            return true;
+        }
+        return false;
+    }
+};
+
+// Partial-result slot of a segment of block c: 1 where the item begins in c, else 0.
+__device__ __forceinline__ int part_slot(const Segment &s) { return 2 * static_cast<int>(blockIdx.x) + (s.off == 0 ? 1 : 0); }
+__device__ __forceinline__ bool is_whole(const Segment &s) { return s.units == s.r.units; }
+// Whether this block holds the last part, but not all, of the item.
+__device__ __forceinline__ bool is_last_part(const Segment &s) { return s.off > 0 && s.off + s.units == s.r.units; }
+
+}  // namespace
+
+}  // namespace qmm

@@ -1,0 +1,60 @@
+// paged.h -- host interface of the paged key / value cache kernels
+// (qmm_kv_append, qmm_paged_attn).
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "../../include/qmm.h"
+
+namespace qmm {
+
+struct AppendParams {
+    qmm_paged_kv kv;
+    const uint16_t *k, *v, *q;
+    uint16_t *q_out;
+    const float *cos_sin;          // fp32 [rope_len][rot]: cosines, then sines
+    int *status;
+    long long k_stride, v_stride, q_stride;
+    int q_heads, rot, rope_len, interleaved;
+};
+
+cudaError_t launch_kv_append(const AppendParams &p, int num_sms, cudaStream_t stream);
+
+struct AttnParams {
+    qmm_paged_kv kv;
+    const uint16_t *q;
+    uint16_t *out;
+    float *lse;                    // or nullptr
+    int *status;
+    float *part_o;                 // [2 grid][rows per tile][head_dim] partial outputs
+    float *part_ml;                // [2 grid][rows per tile][2] their maximum and sum
+    int4 *meta;                    // [grid] the item whose last part block c holds
+    long long q_stride;
+    float scale_log2;              // scale * log2(e): the softmax works in powers of two
+    int q_heads, group;            // query heads, query heads per key head
+    int causal, window;
+    int row_tiles;                 // row tiles per sequence (of the longest one)
+    int whole;                     // every item in one block: no partial results
+    int min_chunk;                 // work a block takes at least, in units
+};
+
+// Sizes of one kernel's work items: query rows per tile, keys per unit.
+constexpr int kDecodeRows = 16, kDecodeKeys = 64;
+constexpr int kChunkRows = 256, kChunkKeys = 128;
+// What starting and finishing an item costs, in units (see find_share).
+constexpr int kDecodeSetup = 1, kChunkSetup = 2;
+
+// Blocks of the decode kernel per SM (it is sized for two).
+constexpr int kDecodeBlocksPerSm = 2;
+
+cudaError_t launch_attn_decode(const AttnParams &p, int grid, cudaStream_t stream);
+cudaError_t launch_attn_chunk(const AttnParams &p, int grid, cudaStream_t stream);
+cudaError_t launch_attn_combine(const AttnParams &p, int grid, int rows, cudaStream_t stream);
+
+// Scratch of a call, and the whole call: kernel choice, split and launches.
+size_t attn_workspace_bytes(int q_heads, int kv_heads, int head_dim, int max_q, int num_sms);
+cudaError_t attn_dispatch(AttnParams &p, int max_q, long long max_kv, void *workspace, int num_sms,
+                          cudaStream_t stream);
+
+}  // namespace qmm

@@ -1,8 +1,8 @@
 /*
  * qmm.h -- C ABI of libqmm: FP16/BF16 activations x b-bit quantized weights
  * (b = 1..8), the integer-native W4A8 / W8A8 variants with their per-token
- * activation quantizer, and signed and float weight codes, on one GB300
- * (sm_103a).
+ * activation quantizer, signed and float weight codes, and the paged key / value
+ * cache with its attention, on one GB300 (sm_103a).
  *
  * The operation (Tilus review, lead and pith_extraction.core_discovery: a
  * matmul of FP16 activations by weights of any width from 1 to 8 bits that
@@ -25,7 +25,7 @@
  *    (host) are host memory.
  *  - fp16 / bf16 tensors are passed as void* holding 16-bit IEEE binary16 /
  *    bfloat16 bit patterns.  Matrices are dense and row-major with the
- *    shapes given; there are no stride arguments.
+ *    shapes given; only the key / value cache calls take strides.
  *  - Every call is asynchronous on `stream` (0 = the legacy default
  *    stream).  Argument errors are detected on the host before anything is
  *    launched and return a status without touching the device.  Launch
@@ -77,7 +77,8 @@ typedef enum {
     QMM_ERR_UNSUPPORTED = 5,  /* valid but not implemented (dtype, group, size) */
     QMM_ERR_CUDA = 6,         /* a CUDA runtime call or kernel launch failed     */
     QMM_ERR_TIMEOUT = 8,      /* device watchdog expired (see qmm_device_status) */
-    QMM_ERR_DEVICE = 9        /* no usable sm_103a device                       */
+    QMM_ERR_DEVICE = 9,       /* no usable sm_103a device                       */
+    QMM_ERR_INDEX = 10        /* an index in device memory is out of range (see qmm_device_status) */
 } qmm_status;
 
 typedef enum { QMM_F16 = 0, QMM_BF16 = 1 } qmm_dtype;
@@ -313,6 +314,108 @@ QMM_API qmm_status qmm_w8a8(const int8_t *xq, const void *sa, const int8_t *w8, 
  * QMM_ERR_DEVICE, QMM_ERR_CUDA; nothing is launched on an argument error. */
 QMM_API qmm_status qmm_quantize_act(const void *x, int8_t *xq, void *sa, int M, int K,
                                     cudaStream_t stream);
+
+/* ---- Paged key / value cache -------------------------------------------------
+ *
+ * What stands between the qkv product and the output product of a decoder
+ * layer: store the new tokens' keys and values, and attend over all of them.
+ *
+ * A batch of `batch` sequences brings `tokens` new tokens, packed one sequence
+ * after the other: sequence b owns tokens cu_q[b] .. cu_q[b+1] - 1 (n_b of them;
+ * possibly none), and kv_len[b] counts its keys WITH the new ones, so new token
+ * i of sequence b sits at position p = kv_len[b] - n_b + i.  Key j of sequence b
+ * lives in slot j % page_size of page block_table[b][j / page_size]; its head h
+ * is the head_dim consecutive values at
+ *     k + page * page_stride + slot * slot_stride + head * head_stride
+ * (and v + the same offset).  The strides cover both the heads-outside order
+ * [page][head][slot][d] and the heads-inside order [page][slot][head][d].
+ *
+ *   k, v         (device) 16-bit values of type `dtype`, 16-byte aligned; the
+ *                strides (in elements) are multiples of 8.
+ *   block_table  (device) int32 [batch][blocks], rows `blocks` apart.
+ *   cu_q         (device) int32 [batch + 1], cu_q[0] = 0, non-decreasing.
+ *   kv_len       (device) int32 [batch].  A token whose position is negative
+ *                (kv_len[b] < n_b, for example kv_len[b] = 0 in an unused place
+ *                of a padded batch) is padding.
+ *   page_size    any size >= 1.   head_dim: 64 or 128.   kv_heads >= 1.
+ * Tokens cu_q[batch] .. tokens - 1, if any, are padding too: nothing of them is
+ * read or written.
+ * The lengths, tables and page numbers are data in device memory, so the host
+ * cannot check them.  The kernels do: a page number outside [0, num_pages) or a
+ * position past the table (or past the rotation table) reads and writes nothing
+ * out of range, leaves the outputs that depend on it unspecified and records
+ * QMM_ERR_INDEX for qmm_device_status(). */
+typedef struct {
+    void *k, *v;                                       /* (device) the cache        */
+    int64_t page_stride, slot_stride, head_stride;     /* in elements               */
+    const int32_t *block_table, *cu_q, *kv_len;        /* (device)                  */
+    int num_pages, page_size, blocks;
+    int batch, tokens;
+    int kv_heads, head_dim;
+    int dtype;                                         /* qmm_dtype of every tensor */
+} qmm_paged_kv;
+
+/* Stores the new tokens' keys and values in the cache, rotated by their
+ * positions, and rotates the queries in the same pass (rotary positions):
+ *   a' = a cos - b sin,  b' = b cos + a sin     (fp32, one rounding to dtype)
+ * for the pairs (a, b) = (x[i], x[i + rot/2]), or (x[2i], x[2i + 1]) when
+ * `interleaved`, i < rot/2, with cos = cos_sin[p][i], sin = cos_sin[p][rot/2 + i]
+ * at the token's position p.  Elements rot .. head_dim - 1 and the values are
+ * copied.
+ *   kv       (host) the cache and the batch.
+ *   k, v     (device) [tokens][kv_heads][head_dim], tokens k_stride / v_stride
+ *            elements apart (views of a fused qkv product will do).
+ *   q        (device) [tokens][q_heads][head_dim], tokens q_stride apart, or NULL.
+ *   q_out    (device) dense [tokens][q_heads][head_dim] rotated queries (q_out
+ *            may be q itself when q is dense); NULL exactly when q is.
+ *   cos_sin  (device) fp32 [rope_len][rot]; NULL when rot = 0 (no rotation).
+ *   rot      0, or a multiple of 16 up to head_dim.
+ * All pointers 16-byte aligned, strides multiples of 8 elements.  Padding tokens
+ * are skipped: nothing is stored for them, their q_out rows are left as they
+ * were.  No two new tokens may share a slot.  Like the matmul calls it starts early (programmatic
+ * dependent launch) and touches no memory before the preceding kernel is done.
+ * Errors: QMM_ERR_SHAPE, QMM_ERR_NULL, QMM_ERR_ALIGN, QMM_ERR_UNSUPPORTED (head
+ * size, dtype), QMM_ERR_DEVICE, QMM_ERR_CUDA; on the device QMM_ERR_INDEX. */
+QMM_API qmm_status qmm_kv_append(const qmm_paged_kv *kv, const void *k, int64_t k_stride, const void *v,
+                                 int64_t v_stride, const void *q, int64_t q_stride, void *q_out, int q_heads,
+                                 const float *cos_sin, int rot, int rope_len, int interleaved,
+                                 cudaStream_t stream);
+
+/* Attention of the new tokens over the cache (which already holds their own keys
+ * and values): single tokens, drafts, chunks and whole prompts in one call.
+ * Query head h reads key head h / (q_heads / kv_heads).
+ *   s_j   = scale * <q, K_j>   over the visible keys j of the token at position p:
+ *           0 <= j < kv_len[b];  j <= p when `causal`;  j > p - window when window > 0
+ *   out   = sum_j exp(s_j - m) V_j / sum_j exp(s_j - m),   m = max_j s_j
+ *   lse   = m + ln sum_j exp(s_j - m)
+ * A row that sees no key (padding) gets out = 0 and lse = -infinity.  Scores, the
+ * running maximum, the sums and the accumulated output are fp32; the weights
+ * exp(s_j - m) are rounded to dtype for the product with V, and out once at the
+ * end.  Results are deterministic run to run.  Slots that no new token of the
+ * sequence sees (past kv_len, before the window) are not read: they may hold
+ * anything.  Values V_j that some of the new tokens see must be finite: a token
+ * that does not see such a key still multiplies it by zero.
+ *   q        (device) [tokens][q_heads][head_dim], tokens q_stride apart, 16-byte aligned.
+ *   out      (device) dense [tokens][q_heads][head_dim], dtype, 16-byte aligned.
+ *   lse      (device) fp32 [tokens][q_heads], or NULL.
+ *   scale    positive and finite.
+ *   window   0 (none) or the number of keys a token sees, its own included;
+ *            window > 0 needs causal.
+ *   max_q    at least the longest sequence's number of new tokens: it chooses the
+ *            kernel and sizes the split (a longer sequence records QMM_ERR_INDEX).
+ *   max_kv   at least the longest kv_len, or 0 if unknown: a hint for the split.
+ *   workspace  (device) 16-byte aligned scratch of at least
+ *            qmm_paged_attn_workspace() bytes; its contents need not survive, and
+ *            calls on one stream may share it.
+ * Starts early like the matmul calls; reads nothing before the preceding kernel
+ * is done.  Errors as for qmm_kv_append. */
+QMM_API qmm_status qmm_paged_attn(const qmm_paged_kv *kv, const void *q, int64_t q_stride, int q_heads,
+                                  float scale, int causal, int window, void *out, float *lse, int max_q,
+                                  int max_kv, void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Bytes of scratch a qmm_paged_attn call of these sizes needs on the current
+ * device (an upper bound over every batch), or 0 for sizes it does not take. */
+QMM_API size_t qmm_paged_attn_workspace(int q_heads, int kv_heads, int head_dim, int max_q);
 
 /* Synchronizes `stream`, then returns and clears the first device-side error
  * recorded by any qmm kernel on the current device (QMM_OK if none).  A
