@@ -79,13 +79,11 @@ _FN = {}   # name -> the configured ctypes function, filled by load()
 FAST_PATH = os.path.join(_HERE, "lib", "_qmmfast" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 _FAST_NAMES = ("qmm_gemv", "qmm_gemm", "qmm_gemv_tile16")
 _call14 = None
-_fast_append = _fast_attn = None
 _ADDR = {}   # name -> function address for _call14, filled by load()
-_append_addr = _attn_addr = 0   # the same for the paged cache calls
 
 
 def _load_fastcall(lib):
-    global _call14, _fast_append, _fast_attn, _append_addr, _attn_addr
+    global _call14
     if not os.path.exists(FAST_PATH):
         return
     try:
@@ -97,8 +95,28 @@ def _load_fastcall(lib):
     for name in _FAST_NAMES:
         _ADDR[name] = ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
     _call14 = mod.call14
+
+
+# The optional extension with the hot path of the paged cache calls
+# (csrc/pytorch_paged.cpp): their checks and allocations in C++.
+PAGED_PATH = os.path.join(_HERE, "lib", "_qmmpaged" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
+_fast_append = _fast_attn = None
+_append_addr = _attn_addr = _scratch_addr = 0   # function addresses for it, filled by load()
+
+
+def _load_paged(lib):
+    global _fast_append, _fast_attn, _append_addr, _attn_addr, _scratch_addr
+    if not os.path.exists(PAGED_PATH):
+        return
+    try:
+        spec = importlib.util.spec_from_file_location("_qmmpaged", PAGED_PATH)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+    except (ImportError, OSError):
+        return
     _append_addr = ctypes.cast(lib.qmm_kv_append, ctypes.c_void_p).value
     _attn_addr = ctypes.cast(lib.qmm_paged_attn, ctypes.c_void_p).value
+    _scratch_addr = ctypes.cast(lib.qmm_paged_attn_workspace, ctypes.c_void_p).value
     _fast_append, _fast_attn = mod.kv_append, mod.paged_attn
 
 
@@ -122,6 +140,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             fn.restype = res
             _FN[name] = fn
         _load_fastcall(lib)
+        _load_paged(lib)
         _lib = lib
     return _lib
 
@@ -413,8 +432,8 @@ def qmm_quantize_act(x, xq=None, sa=None):
     return xq, sa
 
 
-def _paged_checks(k_cache, v_cache, block_table, cu_q, kv_len, rows, kv_rows):
-    # the argument checks of the paged cache calls one by one, for the message
+def _paged_checks(k_cache, v_cache, block_table, cu_q, kv_len, rows):
+    # the argument checks of the paged cache calls, one by one
     for name, t, dt, nd in (("k_cache", k_cache, None, 4), ("v_cache", v_cache, None, 4),
                             ("block_table", block_table, torch.int32, 2), ("cu_q", cu_q, torch.int32, 1),
                             ("kv_len", kv_len, torch.int32, 1)):
@@ -446,6 +465,13 @@ def _paged_checks(k_cache, v_cache, block_table, cu_q, kv_len, rows, kv_rows):
             raise ValueError(f"{name} must have as many tokens as {rows[0][0]}")
 
 
+def _paged_kv(k_cache, v_cache, block_table, cu_q, kv_len, tokens):
+    s0, s1, s2, _ = k_cache.stride()
+    pages, page, hk, D = k_cache.shape
+    return PagedKV(_ptr(k_cache), _ptr(v_cache), s0, s1, s2, _ptr(block_table), _ptr(cu_q), _ptr(kv_len), pages, page,
+                   block_table.shape[1], kv_len.shape[0], tokens, hk, D, _DT[k_cache.dtype])
+
+
 def qmm_kv_append(k, v, k_cache, v_cache, block_table, cu_q, kv_len, q=None, q_out=None, cos_sin=None,
                   interleaved=False):
     """Stores new keys and values ([tokens][kv_heads][D], any token stride) in the
@@ -456,55 +482,35 @@ def qmm_kv_append(k, v, k_cache, v_cache, block_table, cu_q, kv_len, q=None, q_o
     block_table[b] lists its pages.  With q ([tokens][q_heads][D]) the rotated
     queries are returned (in q_out if given), else None.  See qmm_kv_append in
     qmm.h."""
-    dt = k_cache.dtype
-    T, hk, D = k.shape
-    P = k_cache.shape[1]
-    ok = (k.is_cuda and v.is_cuda and k_cache.is_cuda and v_cache.is_cuda and block_table.is_cuda and cu_q.is_cuda
-          and kv_len.is_cuda and dt in _DT and k.dtype is dt and v.dtype is dt and v_cache.dtype is dt
-          and k_cache.dim() == 4 and v_cache.shape == k_cache.shape and v_cache.stride() == k_cache.stride()
-          and k_cache.shape[2] == hk and k_cache.shape[3] == D and k_cache.stride(3) == 1 and v.shape == k.shape
-          and k.stride(2) == 1 and v.stride(2) == 1 and (hk == 1 or (k.stride(1) == D and v.stride(1) == D))
-          and block_table.dtype is _I32 and cu_q.dtype is _I32 and kv_len.dtype is _I32
-          and block_table.is_contiguous() and cu_q.is_contiguous() and kv_len.is_contiguous()
-          and block_table.dim() == 2 and cu_q.dim() == 1 and kv_len.dim() == 1
-          and block_table.shape[0] == kv_len.shape[0] and cu_q.shape[0] == kv_len.shape[0] + 1)
-    if ok and q is not None:
-        ok = (q.is_cuda and q.dtype is dt and q.dim() == 3 and q.shape[0] == T and q.shape[2] == D
-              and q.stride(2) == 1 and (q.shape[1] == 1 or q.stride(1) == D))
-    if not ok:
-        rows = [("k", k, k_cache.shape[2]), ("v", v, k_cache.shape[2])] + ([("q", q, None)] if q is not None else [])
-        _paged_checks(k_cache, v_cache, block_table, cu_q, kv_len, rows, hk)
-        raise ValueError("qmm_kv_append: arguments do not match")
-    rot = rope_len = 0
-    if cos_sin is not None:
-        _dev(cos_sin, "cos_sin", torch.float32)
-        rope_len, rot = cos_sin.shape
-    heads = qs = 0
-    if q is not None:
-        heads, qs = q.shape[1], q.stride(0)
-        if q_out is None:
-            q_out = torch.empty((T, heads, D), dtype=dt, device=q.device)
-        else:
-            _dev(q_out, "q_out", dt, (T, heads, D))
-    elif q_out is not None:
-        raise ValueError("q_out without q")
     if _lib is None:
         load()
-    s0, s1, s2, _ = k_cache.stride()
-    kv = (k_cache.data_ptr(), v_cache.data_ptr(), s0, s1, s2, block_table.data_ptr(), cu_q.data_ptr(),
-          kv_len.data_ptr(), k_cache.shape[0], P, block_table.shape[1], kv_len.shape[0], T, hk, D, _DT[dt])
-    args = (k.data_ptr(), k.stride(0), v.data_ptr(), v.stride(0), None if q is None else q.data_ptr(), qs,
-            None if q_out is None else q_out.data_ptr(), heads, None if cos_sin is None else cos_sin.data_ptr(), rot,
-            rope_len, 1 if interleaved else 0, _stream(k.get_device()))
-    st = (_fast_append(_append_addr, *kv, *args) if _fast_append is not None
-          else _FN["qmm_kv_append"](ctypes.byref(PagedKV(*kv)), *args))
-    if st:
-        raise QmmError(st, "qmm_kv_append")
+    if _fast_append is not None:
+        r = _fast_append(_append_addr, k, v, k_cache, v_cache, block_table, cu_q, kv_len, q, q_out, cos_sin, interleaved)
+        if type(r) is not int:
+            return r
+        if r > 0:
+            raise QmmError(r, "qmm_kv_append")
+    rows = [("k", k, k_cache.shape[2]), ("v", v, k_cache.shape[2])] + ([("q", q, None)] if q is not None else [])
+    _paged_checks(k_cache, v_cache, block_table, cu_q, kv_len, rows)
+    T, hk, D = k.shape
+    rot = rope_len = heads = 0
+    if cos_sin is not None:
+        _dev(cos_sin, "cos_sin", torch.float32)
+        if cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be [positions][rot]")
+        rope_len, rot = cos_sin.shape
+    if q is not None:
+        heads = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty((T, heads, D), dtype=q.dtype, device=q.device)
+        _dev(q_out, "q_out", q.dtype, (T, heads, D))
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    kv = _paged_kv(k_cache, v_cache, block_table, cu_q, kv_len, T)
+    _check(_lib.qmm_kv_append(ctypes.byref(kv), _ptr(k), k.stride(0), _ptr(v), v.stride(0), _ptr(q),
+                              0 if q is None else q.stride(0), _ptr(q_out), heads, _ptr(cos_sin), rot, rope_len,
+                              1 if interleaved else 0, _stream(k.device)), "qmm_kv_append")
     return q_out
-
-
-_I32 = torch.int32
-_WS_BYTES = {}   # (device, q_heads, kv_heads, D, max_q) -> qmm_paged_attn_workspace
 
 
 def qmm_paged_attn_workspace(q_heads: int, kv_heads: int, head_dim: int, max_q: int) -> int:
@@ -523,47 +529,31 @@ def qmm_paged_attn(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q, max_kv
     or (out, lse) with the fp32 log sums [tokens][q_heads].  workspace: uint8
     scratch of qmm_paged_attn_workspace() bytes, allocated if None.  See
     qmm_paged_attn in qmm.h."""
-    dt = q.dtype
-    T, heads, D = q.shape
-    hk = k_cache.shape[2]
-    if not (q.is_cuda and k_cache.is_cuda and v_cache.is_cuda and block_table.is_cuda and cu_q.is_cuda
-            and kv_len.is_cuda and dt in _DT and k_cache.dtype is dt and v_cache.dtype is dt and k_cache.dim() == 4
-            and v_cache.shape == k_cache.shape and v_cache.stride() == k_cache.stride() and k_cache.shape[3] == D
-            and k_cache.stride(3) == 1 and q.stride(2) == 1 and (heads == 1 or q.stride(1) == D)
-            and block_table.dtype is _I32 and cu_q.dtype is _I32 and kv_len.dtype is _I32
-            and block_table.is_contiguous() and cu_q.is_contiguous() and kv_len.is_contiguous()
-            and block_table.dim() == 2 and cu_q.dim() == 1 and kv_len.dim() == 1
-            and block_table.shape[0] == kv_len.shape[0] and cu_q.shape[0] == kv_len.shape[0] + 1):
-        _paged_checks(k_cache, v_cache, block_table, cu_q, kv_len, [("q", q, None)], hk)
-        raise ValueError("qmm_paged_attn: arguments do not match")
-    if out is None:
-        out = torch.empty((T, heads, D), dtype=dt, device=q.device)
-    else:
-        _dev(out, "out", dt, (T, heads, D))
-    lse = torch.empty((T, heads), dtype=torch.float32, device=q.device) if return_lse else None
     if _lib is None:
         load()
-    dev = q.get_device()
+    if scale is None:
+        scale = q.shape[-1] ** -0.5
+    if _fast_attn is not None:
+        r = _fast_attn(_attn_addr, _scratch_addr, q, k_cache, v_cache, block_table, cu_q, kv_len, max_q, max_kv, scale,
+                       causal, window, return_lse, out, workspace)
+        if type(r) is not int:
+            return r
+        if r > 0:
+            raise QmmError(r, "qmm_paged_attn")
+    _paged_checks(k_cache, v_cache, block_table, cu_q, kv_len, [("q", q, None)])
+    T, heads, D = q.shape
+    if out is None:
+        out = torch.empty((T, heads, D), dtype=q.dtype, device=q.device)
+    _dev(out, "out", q.dtype, (T, heads, D))
+    lse = torch.empty((T, heads), dtype=torch.float32, device=q.device) if return_lse else None
     if workspace is None:
-        key = (dev, heads, hk, D, max_q)
-        nbytes = _WS_BYTES.get(key)
-        if nbytes is None:
-            nbytes = _WS_BYTES[key] = qmm_paged_attn_workspace(heads, hk, D, max_q)
+        nbytes = qmm_paged_attn_workspace(heads, k_cache.shape[2], D, max_q)
         workspace = torch.empty(max(nbytes, 16), dtype=_U8, device=q.device)
-    else:
-        _dev(workspace, "workspace", _U8)
-        nbytes = workspace.numel()
-    s0, s1, s2, _ = k_cache.stride()
-    kv = (k_cache.data_ptr(), v_cache.data_ptr(), s0, s1, s2, block_table.data_ptr(), cu_q.data_ptr(),
-          kv_len.data_ptr(), k_cache.shape[0], k_cache.shape[1], block_table.shape[1], kv_len.shape[0], T, hk, D,
-          _DT[dt])
-    args = (q.data_ptr(), q.stride(0), heads, D ** -0.5 if scale is None else scale, 1 if causal else 0, window,
-            out.data_ptr(), None if lse is None else lse.data_ptr(), max_q, max_kv, workspace.data_ptr(), nbytes,
-            _stream(dev))
-    st = (_fast_attn(_attn_addr, *kv, *args) if _fast_attn is not None
-          else _FN["qmm_paged_attn"](ctypes.byref(PagedKV(*kv)), *args))
-    if st:
-        raise QmmError(st, "qmm_paged_attn")
+    _dev(workspace, "workspace", _U8)
+    kv = _paged_kv(k_cache, v_cache, block_table, cu_q, kv_len, T)
+    _check(_lib.qmm_paged_attn(ctypes.byref(kv), _ptr(q), q.stride(0), heads, scale, 1 if causal else 0, window,
+                               _ptr(out), _ptr(lse), max_q, max_kv, _ptr(workspace), workspace.numel(),
+                               _stream(q.device)), "qmm_paged_attn")
     return (out, lse) if return_lse else out
 
 

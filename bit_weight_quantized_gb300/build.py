@@ -79,9 +79,10 @@ def build(verbose: bool = False, force: bool = False, ptxas_verbose: bool = Fals
         if stale_headers or not os.path.exists(obj) or \
                 os.path.getmtime(obj) < os.path.getmtime(os.path.join(CSRC, src)):
             todo.append(src)
-    if todo:
-        with cf.ThreadPoolExecutor(max_workers=min(8, len(todo))) as ex:
-            list(ex.map(lambda s: _compile(s, verbose, ptxas_verbose), todo))
+    with cf.ThreadPoolExecutor(max_workers=8) as ex:
+        paged = ex.submit(build_paged, verbose)
+        list(ex.map(lambda s: _compile(s, verbose, ptxas_verbose), todo))
+        paged.result()
     objs = [os.path.join(BUILD, s[:-3] + ".o") for s in _sources()]
     if todo or not os.path.exists(LIB):
         tmp = LIB + f".{os.getpid()}.tmp"
@@ -121,6 +122,46 @@ def build_fastcall(verbose: bool = False) -> Optional[str]:
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(f"note: fast-call extension not built:\n{res.stderr}\n")
+        return None
+    if verbose and res.stderr:
+        sys.stderr.write(res.stderr)
+    os.replace(tmp, out)
+    return out
+
+
+PAGED_SRC = os.path.join(CSRC, "pytorch_paged.cpp")
+
+
+def paged_path() -> str:
+    """Where the paged cache calls' extension (csrc/pytorch_paged.cpp) is built."""
+    return os.path.join(LIBDIR, "_qmmpaged" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
+
+
+def build_paged(verbose: bool = False) -> Optional[str]:
+    """Compiles the paged cache calls' extension with the host C++ compiler against
+    torch's headers.  It is optional, like the fast-call extension: a failure here
+    only warns and the binding calls through ctypes."""
+    import torch
+    out = paged_path()
+    srcs = (PAGED_SRC, os.path.join(INCLUDE, "qmm.h"))
+    if os.path.exists(out) and os.path.getmtime(out) >= max(os.path.getmtime(s) for s in srcs):
+        return out
+    inc = sysconfig.get_paths().get("include", "")
+    troot = os.path.dirname(torch.__file__)
+    tinc, tlib = os.path.join(troot, "include"), os.path.join(troot, "lib")
+    cc = os.environ.get("CXX") or shutil.which("g++") or shutil.which("c++")
+    if not cc or not os.path.exists(os.path.join(inc, "Python.h")) or not os.path.isdir(tinc):
+        sys.stderr.write("note: paged cache extension not built (no C++ compiler or headers)\n")
+        return None
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    tmp = out + f".{os.getpid()}.tmp"
+    cmd = [cc, "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-isystem", inc, "-isystem", tinc,
+           "-isystem", os.path.join(tinc, "torch", "csrc", "api", "include"), "-isystem", cuda,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", PAGED_SRC, "-o", tmp,
+           "-L", tlib, f"-Wl,-rpath,{tlib}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        sys.stderr.write(f"note: paged cache extension not built:\n{res.stderr[-2000:]}\n")
         return None
     if verbose and res.stderr:
         sys.stderr.write(res.stderr)

@@ -52,8 +52,8 @@ struct ChunkLayout {
     static constexpr int kOffQ = 0;                 // two streams
     static constexpr int kOffRing = 2 * kTile;
     static constexpr int kOffBar = kOffRing + kRing * kTile;
-    // ring full / empty, q_full[2], s_full[2], p_full[2], o_full[2], drain
-    static constexpr int kNumBars = 2 * kRing + 9;
+    // ring full / empty, q_full[2], s_full[2], p_full[2][2 halves], o_full[2], drain
+    static constexpr int kNumBars = 2 * kRing + 11;
     static constexpr int kOffTmem = kOffBar + 8 * kNumBars;
     static constexpr int kOffShare = kOffTmem + 16;
     static constexpr int kOffRed = kOffShare + sizeof(Share);
@@ -155,6 +155,48 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r)
 
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// Two fp32 values in one 64-bit register: the FMA pipe takes both in one
+// instruction, which halves the softmax's issue slots there.
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi)
+{
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+    return d;
+}
+
+__device__ __forceinline__ void unpair(uint64_t v, float &lo, float &hi)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+__device__ __forceinline__ uint64_t mul2_f32(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kChunkThreads, 1)
 attn_chunk_kernel(const __grid_constant__ AttnParams p)
@@ -171,7 +213,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
     long long *red = reinterpret_cast<long long *>(smem + L::kOffRed);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::kOffBar);
     uint64_t *empty = full + kRing;
-    uint64_t *q_full = empty + kRing, *s_full = q_full + 2, *p_full = s_full + 2, *o_full = p_full + 2;
+    uint64_t *q_full = empty + kRing, *s_full = q_full + 2, *p_full = s_full + 2, *o_full = p_full + 4;
     uint64_t *drain = o_full + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kOffTmem);
 
@@ -189,7 +231,8 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
         for (int s = 0; s < 2; ++s) {
             mbar_init(&q_full[s], kSoftWarps);
             mbar_init(&s_full[s], 1);
-            mbar_init(&p_full[s], kSoftWarps);
+            mbar_init(&p_full[2 * s], kSoftWarps);
+            mbar_init(&p_full[2 * s + 1], kSoftWarps);
             mbar_init(&o_full[s], 1);
         }
         mbar_init(drain, 1);
@@ -277,6 +320,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
             const int units = sg.units, kb0 = (r.unit0 + sg.off) * kChunkKeys;
             const int2 see = row_keys(p, r, rr);
             float mref = -INFINITY, l = 0.f;
+            const uint64_t scale2 = pair(__float_as_uint(p.scale_log2), __float_as_uint(p.scale_log2));
             for (int j = 0; j < units; ++j) {
                 if (!(ok = __all_sync(0xffffffffu, mbar_wait(&s_full[s], ph, p.status))))
                     break;
@@ -300,14 +344,16 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                 }
                 float mx[4];
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    mx[c] = __uint_as_float(v[c]);
+                for (int e = 0; e < 4; ++e)
+                    mx[e] = __uint_as_float(v[e]);
 #pragma unroll
-                for (int c = 4; c < 128; c += 4)
+                for (int c = 4; c + 8 <= 128; c += 8)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        mx[e] = fmaxf(mx[e], __uint_as_float(v[c + e]));
-                const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+                        mx[e] = max3(mx[e], __uint_as_float(v[c + 2 * e]), __uint_as_float(v[c + 2 * e + 1]));
+                mx[0] = max3(mx[0], __uint_as_float(v[124]), __uint_as_float(v[125]));
+                mx[1] = max3(mx[1], __uint_as_float(v[126]), __uint_as_float(v[127]));
+                const float m = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * p.scale_log2;
                 const bool up = m > mref + kChunkGrow;
                 if (__any_sync(0xffffffffu, up)) {
                     const float a = up ? ex2(mref - m) : 1.f;
@@ -321,33 +367,45 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                             tmem_ld_wait();
                             pin32(o);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+                            for (int e = 0; e < 32; e += 2) {
+                                float x, y;
+                                unpair(mul2_f32(pair(o[e], o[e + 1]), pair(__float_as_uint(a), __float_as_uint(a))), x, y);
+                                o[e] = __float_as_uint(x);
+                                o[e + 1] = __float_as_uint(y);
+                            }
                             tmem_st32(to + c, o);
                         }
                     }
                 }
                 const float neg = kShift - (mref == -INFINITY ? 0.f : mref);
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint64_t neg2 = pair(__float_as_uint(neg), __float_as_uint(neg));
+                uint64_t sum[2] = {0, 0};
+                // weights, rounded to 16 bits for the second product; their first half
+                // is handed over while the second is computed
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     uint32_t w[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        const float p0 = ex2(fmaf(__uint_as_float(v[32 * c + 2 * e]), p.scale_log2, neg));
-                        const float p1 = ex2(fmaf(__uint_as_float(v[32 * c + 2 * e + 1]), p.scale_log2, neg));
-                        sum[(2 * e) & 3] += p0;
-                        sum[(2 * e + 1) & 3] += p1;
+                        float p0, p1;
+                        unpair(fma2(pair(v[32 * c + 2 * e], v[32 * c + 2 * e + 1]), scale2, neg2), p0, p1);
+                        p0 = ex2(p0);
+                        p1 = ex2(p1);
+                        sum[e & 1] = add2(sum[e & 1], pair(__float_as_uint(p0), __float_as_uint(p1)));
                         w[e] = pack16<BF16>(p0, p1);
                     }
                     tmem_st16(ts + 16 * c, w);
+                    if (c & 1) {
+                        tmem_st_wait();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(&p_full[2 * s + (c >> 1)]);
+                    }
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&p_full[s]);
+                float s0, s1;
+                unpair(add2(sum[0], sum[1]), s0, s1);
+                l += s0 + s1;
             }
             if (ok)
                 ok = __all_sync(0xffffffffu, mbar_wait(&o_full[s], oph, p.status));
@@ -458,15 +516,21 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                         advance();
                         const bool more = j + 1 < sg.units;
                         for (int s = 0; s < ns; ++s) {
-                            if (!(ok = mbar_wait(&p_full[s], pph[s], p.status)))
-                                break;
-                            pph[s] ^= 1u;
-                            tc_fence_after();
                             const uint64_t b = v_desc + ((vs * L::kTile) >> 4);
 #pragma unroll
-                            for (int kk = 0; kk < kChunkKeys / 16; ++kk)
-                                tc_mma_ts(tmem + o_col(s), tmem + s_col(s) + 8 * kk, b + kk * (2048 >> 4), id_pv,
-                                          kk > 0 || j > 0 ? 1u : 0u);
+                            for (int kk = 0; kk < kChunkKeys / 16; ++kk) {
+                                if (kk == 0 || kk == kChunkKeys / 32) {   // a half of the weights
+                                    if (ok)
+                                        ok = mbar_wait(&p_full[2 * s + (kk ? 1 : 0)], pph[s], p.status);
+                                    tc_fence_after();
+                                }
+                                if (ok)
+                                    tc_mma_ts(tmem + o_col(s), tmem + s_col(s) + 8 * kk, b + kk * (2048 >> 4), id_pv,
+                                              kk > 0 || j > 0 ? 1u : 0u);
+                            }
+                            if (!ok)
+                                break;
+                            pph[s] ^= 1u;
                             if (s == ns - 1)
                                 tc_commit(&empty[vs]);
                             if (more) {

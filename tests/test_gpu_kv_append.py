@@ -15,6 +15,16 @@ def q():
     return q
 
 
+@pytest.fixture(params=["extension", "ctypes"])
+def route(q, request, monkeypatch):
+    """Either route of the binding to the library."""
+    if request.param == "ctypes":
+        monkeypatch.setattr(q, "_fast_append", None)
+        monkeypatch.setattr(q, "_fast_attn", None)
+    elif q._fast_append is None:
+        pytest.skip("extension not built")
+
+
 def check(q, bt, rot, interleaved, with_q=True, in_place=False, seed=0):
     """Appends random tokens to bt and compares the whole cache."""
     g = torch.Generator(device="cuda")
@@ -109,7 +119,7 @@ def test_tokens_past_the_batch_are_padding(q):
     assert q.qmm_device_status() == 0
 
 
-def test_without_queries_and_in_place(q):
+def test_without_queries_and_in_place(q, route):
     check(q, Batch([4, 9], [4, 100], 8, 4, 64, "bf16", seed=2), 64, False, with_q=False)
     check(q, Batch([4, 9], [4, 100], 8, 4, 64, "bf16", seed=2), 64, False, in_place=True)
     check(q, Batch([4, 9], [4, 100], 8, 4, 64, "bf16", seed=2), 32, True, in_place=True)
@@ -150,7 +160,7 @@ def test_bad_indices_are_reported(q, what):
     assert int(changed.any(-1).sum()) == 4
 
 
-def test_append_then_attend(q):
+def test_append_then_attend(q, route):
     """The two calls as a decode loop makes them: token by token equals one chunk."""
     kv, n = 150, 21
     bt = Batch([n], [kv], 8, 2, 128, "bf16", seed=3)
@@ -172,7 +182,7 @@ def test_append_then_attend(q):
     assert ((one_by_one - whole.double()).abs() <= 4 * U[bt.dt] * (1 + whole.double().abs())).all()
 
 
-def test_refusals(q):
+def test_refusals(q, route):
     bt = Batch([2], [10], 4, 2, 64)
     k = torch.zeros(2, 2, 64, device="cuda", dtype=bt.dt)
     a = bt.args()

@@ -18,6 +18,15 @@ def q():
     return q
 
 
+@pytest.fixture(params=["extension", "ctypes"])
+def route(q, request, monkeypatch):
+    """Either route of the binding to the library."""
+    if request.param == "ctypes":
+        monkeypatch.setattr(q, "_fast_attn", None)
+    elif q._fast_attn is None:
+        pytest.skip("extension not built")
+
+
 def check(q, bt, scale=None, causal=True, window=0, max_kv=None, max_q=None, query=None):
     out, lse = q.qmm_paged_attn(bt.q if query is None else query, *bt.args(),
                                 max(bt.ql) if max_q is None else max_q, max(bt.kl) if max_kv is None else max_kv,
@@ -87,7 +96,7 @@ def test_rows_without_keys(q, n):
     check(q, bt, window=3)
 
 
-def test_no_tokens(q):
+def test_no_tokens(q, route):
     bt = Batch([0, 0], [5, 9], 4, 2, 64)
     assert q.qmm_paged_attn(bt.q, *bt.args(), 1, 9).shape == (0, 4, 64)
     assert q.qmm_device_status() == 0
@@ -176,7 +185,7 @@ def test_offsets_past_32_bits(q, n):
     check(q, bt)
 
 
-def test_query_views_and_given_buffers(q):
+def test_query_views_and_given_buffers(q, route):
     bt = Batch([5, 40], [100, 300], 8, 2, 64, "f16", seed=6)
     wide = torch.zeros(bt.T, 8 + 4, 64, dtype=bt.dt, device="cuda")
     wide[:, :8] = bt.q
@@ -251,7 +260,7 @@ def test_bad_indices_are_reported(q, n, what):
     assert q.qmm_device_status() == 0
 
 
-def test_refusals(q):
+def test_refusals(q, route):
     bt = Batch([2], [10], 4, 2, 64)
     a = bt.args()
     with pytest.raises(q.QmmError, match="SHAPE"):
