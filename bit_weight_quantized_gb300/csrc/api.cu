@@ -160,6 +160,43 @@ bool encode_u64_tmap(CUtensorMap *map, const void *base, long long cols, long lo
     return r == CUDA_SUCCESS;
 }
 
+void attn_set_tma(AttnParams &p)
+{
+    p.box = 0;
+    // one index for page and head: the page stride in head strides
+    long long step = 1, stride = p.kv.page_stride;
+    if (p.kv.kv_heads > 1) {
+        stride = p.kv.head_stride;
+        if (stride <= 0 || p.kv.page_stride % stride)
+            return;
+        step = p.kv.page_stride / stride;
+    }
+    // a box lies in one page and in one 128-key tile, and is whole 8-row groups of
+    // the swizzle: the largest power of two in both, at least 8
+    int box = 128;
+    while (p.kv.page_size % box)
+        box /= 2;
+    const long long rows = (p.kv.num_pages - 1LL) * step + p.kv.kv_heads;
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (box < 8 || !enc || p.kv.num_pages < 1 || step < 1 || rows > 0x7fffffffLL)
+        return;
+    const cuuint64_t dims[5] = {64, 8, static_cast<cuuint64_t>(p.kv.head_dim / 64),
+                                static_cast<cuuint64_t>(p.kv.page_size / 8), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[4] = {static_cast<cuuint64_t>(p.kv.slot_stride) * 2, 128,
+                                   static_cast<cuuint64_t>(p.kv.slot_stride) * 16, static_cast<cuuint64_t>(stride) * 2};
+    const cuuint32_t boxes[5] = {64, 8, static_cast<cuuint32_t>(p.kv.head_dim / 64), static_cast<cuuint32_t>(box / 8), 1};
+    const cuuint32_t one[5] = {1, 1, 1, 1, 1};
+    CUtensorMap *maps[2] = {&p.tmk, &p.tmv};
+    void *const base[2] = {p.kv.k, p.kv.v};
+    for (int i = 0; i < 2; ++i)
+        if (enc(maps[i], CU_TENSOR_MAP_DATA_TYPE_UINT16, 5, base[i], dims, strides, boxes, one,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return;
+    p.box = box;
+    p.page_step = static_cast<int>(step);
+}
+
 void skinny_set_tma(GemvParams &p)
 {
     p.tma = 0;

@@ -13,99 +13,195 @@ namespace qmm {
 
 namespace {
 
-constexpr int kCombineWarps = 4;
+// Part of block c: slot 2 c + 1 where the item begins (c == first), else 2 c.
+__device__ __forceinline__ long long part_of(int c, int first) { return 2LL * c + (c == first ? 1 : 0); }
 
-// Block (c, y): the item whose last part is in block c of the attention kernel
-// (meta[c]); one warp per row.
-template <int D, int ROWS, int KEYS, bool BF16>
-__global__ void __launch_bounds__(32 * kCombineWarps)
-attn_combine_kernel(const __grid_constant__ AttnParams p)
+__device__ __forceinline__ long long out_row(const AttnParams &p, int row, int t0, int h)
+{
+    const int tok = row / p.group;
+    return static_cast<long long>(t0 + tok) * p.q_heads + h * p.group + row - tok * p.group;
+}
+
+// Parts of the decode kernel, [16 rows][D].  Block (c, y): row y of the item whose last
+// part is in block c of the attention kernel (meta[c]).  A long axis leaves tens of
+// parts: the four warps take every fourth one each and meet in shared memory.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(128)
+join_decode_kernel(const __grid_constant__ AttnParams p)
 {
     constexpr float kShift = BF16 ? 0.f : 7.f;
     constexpr int kVec = D / 32;
+    __shared__ float so[4][D];
+    __shared__ float2 sml[4];
+    if (threadIdx.x == 0)
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int last = blockIdx.x, row = blockIdx.y;
+    const int4 mt = p.meta[2 * last];
+    if (mt.x < 0 || row >= mt.y)
+        return;
+    const int h = p.meta[2 * last + 1].x;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, first = mt.x;
+    float m = -INFINITY, l = 0.f, o[kVec];
+#pragma unroll
+    for (int e = 0; e < kVec; ++e)
+        o[e] = 0.f;
+    // eight parts at a time: their loads are under way together
+    for (int c0 = first + warp; c0 <= last; c0 += 32) {
+        float2 ml[8];
+        float v[8][kVec];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int c = c0 + 4 * u;
+            ml[u] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int e = 0; e < kVec; ++e)
+                v[u][e] = 0.f;
+            if (c <= last) {
+                const long long at = part_of(c, first) * kDecodeRows + row;
+                ml[u] = *reinterpret_cast<const float2 *>(p.part_ml + 2 * at);
+                const float *src = p.part_o + at * D + lane * kVec;
+                if constexpr (kVec == 4) {
+                    const float4 q = *reinterpret_cast<const float4 *>(src);
+                    v[u][0] = q.x; v[u][1] = q.y; v[u][2] = q.z; v[u][3] = q.w;
+                } else {
+                    const float2 q = *reinterpret_cast<const float2 *>(src);
+                    v[u][0] = q.x; v[u][1] = q.y;
+                }
+            }
+        }
+        float mn = m;
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            mn = fmaxf(mn, ml[u].x);
+        const float base = mn == -INFINITY ? 0.f : mn, a = ex2(m - base);
+        m = mn;
+        l *= a;
+#pragma unroll
+        for (int e = 0; e < kVec; ++e)
+            o[e] *= a;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const float w = ex2(ml[u].x - base);
+            l = fmaf(w, ml[u].y, l);
+#pragma unroll
+            for (int e = 0; e < kVec; ++e)
+                o[e] = fmaf(w, v[u][e], o[e]);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < kVec; ++e)
+        so[warp][lane * kVec + e] = o[e];
+    if (lane == 0)
+        sml[warp] = make_float2(m, l);
+    __syncthreads();
+    if (threadIdx.x * 2 < D) {
+        float mm = -INFINITY, ll = 0.f, o0 = 0.f, o1 = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+            mm = fmaxf(mm, sml[w].x);
+        const float base = mm == -INFINITY ? 0.f : mm;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const float a = ex2(sml[w].x - base);
+            ll = fmaf(a, sml[w].y, ll);
+            o0 = fmaf(a, so[w][2 * threadIdx.x], o0);
+            o1 = fmaf(a, so[w][2 * threadIdx.x + 1], o1);
+        }
+        const long long at = out_row(p, mt.z + row, mt.w, h);
+        const float inv = ll > 0.f ? 1.f / ll : 0.f;
+        reinterpret_cast<uint32_t *>(p.out + at * D)[threadIdx.x] = pack16<BF16>(o0 * inv, o1 * inv);
+        if (p.lse && threadIdx.x == 0)
+            p.lse[at] = ll > 0.f ? (mm - kShift + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+    }
+}
+
+// Parts of the chunk kernel, [D / 4][256 rows][4].  Block (c, y): rows 32 y .. 32 y + 31
+// of the item, one per lane; warp w takes values D / 8 w .. D / 8 (w + 1) of them.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(256)
+join_chunk_kernel(const __grid_constant__ AttnParams p)
+{
+    constexpr float kShift = BF16 ? 0.f : 7.f;
+    constexpr int kQuads = D / 32;      // groups of four values per thread
     if (threadIdx.x == 0)
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int last = blockIdx.x;
-    const int4 mt = p.meta[last];
-    if (mt.x < 0)
+    const int4 mt = p.meta[2 * last];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = 32 * blockIdx.y + lane;
+    if (mt.x < 0 || row >= mt.y)
         return;
-    const int lane = threadIdx.x & 31, first = mt.z;
-    const RowTile r = row_tile<ROWS, KEYS>(p, mt.x);
-    for (int row = blockIdx.y * kCombineWarps + (threadIdx.x >> 5); row < r.rows; row += gridDim.y * kCombineWarps) {
-        // part of block c: slot 2 c + 1 where the item begins (c == first), else 2 c
-        auto part = [&](int c) { return (2LL * c + (c == first ? 1 : 0)) * ROWS + row; };
-        float m = -INFINITY;
-        for (int c = first + lane; c <= last; c += 32)
-            m = fmaxf(m, p.part_ml[2 * part(c)]);
+    const int h = p.meta[2 * last + 1].x, first = mt.x;
+    float m = -INFINITY, l = 0.f;
+    float4 o[kQuads];
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1)
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-        const float base = m == -INFINITY ? 0.f : m;
-        float l = 0.f, o[kVec];
+    for (int e = 0; e < kQuads; ++e)
+        o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c0 = first; c0 <= last; c0 += 2) {   // two parts at a time
+        float2 ml[2];
+        float4 v[2][kQuads];
 #pragma unroll
-        for (int e = 0; e < kVec; ++e)
-            o[e] = 0.f;
-#pragma unroll 4
-        for (int c = first; c <= last; ++c) {
-            const float2 ml = *reinterpret_cast<const float2 *>(p.part_ml + 2 * part(c));
-            const float *src = p.part_o + part(c) * D + lane * kVec;
-            float v[kVec];
-            if constexpr (kVec == 4) {
-                const float4 q = *reinterpret_cast<const float4 *>(src);
-                v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
-            } else {
-                const float2 q = *reinterpret_cast<const float2 *>(src);
-                v[0] = q.x; v[1] = q.y;
+        for (int u = 0; u < 2; ++u) {
+            ml[u] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int e = 0; e < kQuads; ++e)
+                v[u][e] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (c0 + u <= last) {
+                const long long at = part_of(c0 + u, first);
+                ml[u] = *reinterpret_cast<const float2 *>(p.part_ml + 2 * (at * kChunkRows + row));
+#pragma unroll
+                for (int e = 0; e < kQuads; ++e)
+                    v[u][e] = *reinterpret_cast<const float4 *>(p.part_o + at * (kChunkRows * D) +
+                                                                ((warp * kQuads + e) * kChunkRows + row) * 4);
             }
-            const float w = ex2(ml.x - base);
-            l = fmaf(w, ml.y, l);
-#pragma unroll
-            for (int e = 0; e < kVec; ++e)
-                o[e] = fmaf(w, v[e], o[e]);
         }
-        const int rr = r.row0 + row, tok = rr / p.group;
-        const long long at = static_cast<long long>(r.t0 + tok) * p.q_heads + mt.y * p.group + rr - tok * p.group;
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        uint32_t w[kVec / 2];
+        const float mn = fmaxf(m, fmaxf(ml[0].x, ml[1].x)), base = mn == -INFINITY ? 0.f : mn;
+        const float a = ex2(m - base), w0 = ex2(ml[0].x - base), w1 = ex2(ml[1].x - base);
+        m = mn;
+        l = a * l + (w0 * ml[0].y + w1 * ml[1].y);
 #pragma unroll
-        for (int e = 0; e < kVec / 2; ++e)
-            w[e] = pack16<BF16>(o[2 * e] * inv, o[2 * e + 1] * inv);
-        uint16_t *dst = p.out + at * D + lane * kVec;
-        if constexpr (kVec == 4)
-            *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
-        else
-            *reinterpret_cast<uint32_t *>(dst) = w[0];
-        if (p.lse && lane == 0)
-            p.lse[at] = l > 0.f ? (m - kShift + log2f(l)) * 0.6931471805599453f : -INFINITY;
+        for (int e = 0; e < kQuads; ++e) {
+            o[e].x = a * o[e].x + (w0 * v[0][e].x + w1 * v[1][e].x);
+            o[e].y = a * o[e].y + (w0 * v[0][e].y + w1 * v[1][e].y);
+            o[e].z = a * o[e].z + (w0 * v[0][e].z + w1 * v[1][e].z);
+            o[e].w = a * o[e].w + (w0 * v[0][e].w + w1 * v[1][e].w);
+        }
     }
+    const long long at = out_row(p, mt.z + row, mt.w, h);
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    uint2 *dst = reinterpret_cast<uint2 *>(p.out + at * D + warp * (D / 8));
+#pragma unroll
+    for (int e = 0; e < kQuads; ++e)
+        dst[e] = make_uint2(pack16<BF16>(o[e].x * inv, o[e].y * inv), pack16<BF16>(o[e].z * inv, o[e].w * inv));
+    if (p.lse && warp == 0)
+        p.lse[at] = l > 0.f ? (m - kShift + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
-template <int D, int ROWS, int KEYS, bool BF16>
-cudaError_t launch_combine(const AttnParams &p, int grid, cudaStream_t stream)
+template <int D, bool BF16>
+cudaError_t launch_join(const AttnParams &p, int grid, bool few, int max_rows, cudaStream_t stream)
 {
     cudaLaunchConfig_t cfg = {};
-    const int tile_rows = std::min(ROWS, p.row_tiles * ROWS);
-    cfg.gridDim = dim3(grid, (tile_rows + 4 * kCombineWarps - 1) / (4 * kCombineWarps) * (ROWS > 16 ? 1 : 4));
-    cfg.blockDim = dim3(32 * kCombineWarps);
+    cfg.gridDim = few ? dim3(grid, max_rows) : dim3(grid, (max_rows + 31) / 32);
+    cfg.blockDim = dim3(few ? 128 : 256);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_combine_kernel<D, ROWS, KEYS, BF16>, p);
+    return few ? cudaLaunchKernelEx(&cfg, join_decode_kernel<D, BF16>, p)
+               : cudaLaunchKernelEx(&cfg, join_chunk_kernel<D, BF16>, p);
 }
 
-template <int ROWS, int KEYS>
-cudaError_t launch_combine_rows(const AttnParams &p, int grid, cudaStream_t stream)
+cudaError_t launch_attn_join(const AttnParams &p, int grid, bool few, int max_rows, cudaStream_t stream)
 {
     const bool bf16 = p.kv.dtype == QMM_BF16;
     if (p.kv.head_dim == 128)
-        return bf16 ? launch_combine<128, ROWS, KEYS, true>(p, grid, stream)
-                    : launch_combine<128, ROWS, KEYS, false>(p, grid, stream);
-    return bf16 ? launch_combine<64, ROWS, KEYS, true>(p, grid, stream)
-                : launch_combine<64, ROWS, KEYS, false>(p, grid, stream);
+        return bf16 ? launch_join<128, true>(p, grid, few, max_rows, stream)
+                    : launch_join<128, false>(p, grid, few, max_rows, stream);
+    return bf16 ? launch_join<64, true>(p, grid, few, max_rows, stream)
+                : launch_join<64, false>(p, grid, few, max_rows, stream);
 }
 
 // The decode kernel holds 16 query rows per key head.
@@ -116,7 +212,7 @@ int attn_grid(bool few, int num_sms) { return few ? kDecodeBlocksPerSm * num_sms
 size_t scratch_bytes(bool few, int head_dim, int num_sms)
 {
     const size_t g = attn_grid(few, num_sms), rows = few ? kDecodeRows : kChunkRows;
-    return g * 16 + 2 * g * rows * (head_dim + 2) * 4;
+    return g * 32 + 2 * g * rows * (head_dim + 2) * 4;
 }
 
 // Work a block takes at least, in units: below this a split costs more (a second kernel,
@@ -124,12 +220,6 @@ size_t scratch_bytes(bool few, int head_dim, int num_sms)
 constexpr int kMinDecodeUnits = 5, kMinChunkUnits = 4;
 
 }  // namespace
-
-cudaError_t launch_attn_combine(const AttnParams &p, int grid, int rows, cudaStream_t stream)
-{
-    return rows == kDecodeRows ? launch_combine_rows<kDecodeRows, kDecodeKeys>(p, grid, stream)
-                               : launch_combine_rows<kChunkRows, kChunkKeys>(p, grid, stream);
-}
 
 size_t attn_workspace_bytes(int q_heads, int kv_heads, int head_dim, int max_q, int num_sms)
 {
@@ -158,12 +248,15 @@ cudaError_t attn_dispatch(AttnParams &p, int max_q, long long max_kv, void *work
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     const size_t g = attn_grid(few, num_sms);
     p.meta = reinterpret_cast<int4 *>(ws);
-    p.part_ml = reinterpret_cast<float *>(ws + g * 16);
+    p.part_ml = reinterpret_cast<float *>(ws + g * 32);
     p.part_o = p.part_ml + 2 * g * rows * 2;
+    if (!few)
+        attn_set_tma(p);
     cudaError_t e = few ? launch_attn_decode(p, grid, stream) : launch_attn_chunk(p, grid, stream);
     if (e != cudaSuccess || p.whole)
         return e;
-    return launch_attn_combine(p, grid, rows, stream);
+    const long long max_rows = std::min(static_cast<long long>(rows), static_cast<long long>(max_q) * p.group);
+    return launch_attn_join(p, grid, few, static_cast<int>(max_rows), stream);
 }
 
 }  // namespace qmm

@@ -9,15 +9,20 @@
 // accumulators in tensor memory: per stream S (128 x 128 fp32) and O (128 x D), all
 // 512 columns at D = 128.  P takes S's place as 16-bit values and is the second
 // product's left operand straight from tensor memory; V is its right operand as it
-// lies in the cache ([key][d], the "MN-major" form), so nothing is transposed.
+// lies in the cache ([key][d], the "MN-major" form), so nothing is transposed.  An
+// item of at most 128 rows gives both streams the same rows and every other tile,
+// so that one stream's products still run under the other's softmax; stream 0 adds
+// up the two at the end, straight from tensor memory.
 //
 // Roles.  Warps 0-3 and 4-7 are the softmax of streams 0 and 1, one thread per row:
 // no exchange between lanes at all.  Warp 8 issues the products; it starts stream
 // 1's while stream 0's softmax runs and the other way round.  Warps 9-11 bring K
-// and V tiles with 16-byte asynchronous copies into a ring of kRing slots: copies
-// and not tensor maps, because they take any page size and stride, and fill the
-// slots that nobody sees (past kv_len, before the window) with zeros, which the
-// product with V needs (0 x NaN).
+// and V tiles into a ring of kRing slots: where the page size is a multiple of 8 by
+// tensor copies, one per page or part of a page that lies in the tile, all issued by
+// one warp (the other two clear the V rows that nobody sees: past kv_len, before the
+// window, where 0 x NaN would spoil the product); else by 16-byte asynchronous copies
+// that fill such rows with zeros.  Plain copies alone kept the three warps busy for
+// 6000 cycles a tile pair, three times the products' time.
 //
 // The running maximum is replaced only when it grows by more than 2^8: the output
 // accumulator in tensor memory is then read, scaled and written back by its
@@ -52,8 +57,9 @@ struct ChunkLayout {
     static constexpr int kOffQ = 0;                 // two streams
     static constexpr int kOffRing = 2 * kTile;
     static constexpr int kOffBar = kOffRing + kRing * kTile;
-    // ring full / empty, q_full[2], s_full[2], p_full[2][2 halves], o_full[2], drain
-    static constexpr int kNumBars = 2 * kRing + 11;
+    // ring full / empty / patch, q_full[2], s_full[2], p_full[2][2 halves], o_full[2],
+    // x_full, x_done, drain
+    static constexpr int kNumBars = 3 * kRing + 13;
     static constexpr int kOffTmem = kOffBar + 8 * kNumBars;
     static constexpr int kOffShare = kOffTmem + 16;
     static constexpr int kOffRed = kOffShare + sizeof(Share);
@@ -69,23 +75,32 @@ struct ChunkLayout {
 __device__ __forceinline__ uint32_t s_col(int s) { return static_cast<uint32_t>(s) * 128u; }
 __device__ __forceinline__ uint32_t o_col(int s) { return 256u + static_cast<uint32_t>(s) * 128u; }
 
-// Byte of 16-byte chunk c of row r in a tile: halves of 64 values, rows of 128
+// Byte of 16-byte chunk c of row r in a query tile: halves of 64 values, rows of 128
 // bytes, chunks permuted by the row (the 128-byte swizzle).
-__device__ __forceinline__ uint32_t sw_addr(int r, int c)
+__device__ __forceinline__ uint32_t q_addr(int r, int c)
 {
     return static_cast<uint32_t>((c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
-// Descriptor of a [keys][64 d] tile read along d as the N index (MN-major, 128-byte
-// swizzle): 64-value blocks of N `kHalf` bytes apart, 8-key groups 1024 bytes apart.
-__device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t saddr, uint32_t half_bytes)
+// The same in a K or V tile: groups of 8 keys, each [D / 64 halves][8 keys][64
+// values], so that one tensor copy brings both halves of a page's keys.
+template <int D>
+__device__ __forceinline__ uint32_t kv_addr(int r, int c)
+{
+    return static_cast<uint32_t>((r >> 3) * (D * 16) + (c >> 3) * 1024 + (r & 7) * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+// Operand descriptor with the 128-byte swizzle.  `stride`: bytes between groups of 8
+// rows (keys); `lead`: bytes between blocks of 64 values along the N index where the
+// tile is read along d (MN-major), unused otherwise.
+__device__ __forceinline__ uint64_t swizzled_desc(uint32_t saddr, uint32_t lead, uint32_t stride)
 {
     uint64_t d = 0;
     d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFF);
-    d |= static_cast<uint64_t>((half_bytes >> 4) & 0x3FFF) << 16;   // leading byte offset: next 64 of N
-    d |= static_cast<uint64_t>(1024 >> 4) << 32;                    // stride byte offset: next 8 keys
-    d |= static_cast<uint64_t>(1) << 46;
-    d |= static_cast<uint64_t>(2) << 61;
+    d |= static_cast<uint64_t>((lead >> 4) & 0x3FFF) << 16;
+    d |= static_cast<uint64_t>((stride >> 4) & 0x3FFF) << 32;
+    d |= static_cast<uint64_t>(1) << 46;                            // descriptor version (tcgen05)
+    d |= static_cast<uint64_t>(2) << 61;                            // 128-byte swizzle
     return d;
 }
 
@@ -101,6 +116,18 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint
         : "memory");
 }
 
+// True in one lane of the (converged) warp, the same one every time.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
 // 32 tensor-memory columns of this thread's lane, without waiting
 __device__ __forceinline__ void tmem_ld32_start(uint32_t taddr, uint32_t *r)
 {
@@ -114,6 +141,31 @@ __device__ __forceinline__ void tmem_ld32_start(uint32_t taddr, uint32_t *r)
           "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
           "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr));
+}
+
+// 5-D tiled load of a box into shared memory, completing on `bar`.
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const void *tmap, uint64_t *bar, int c3, int c4)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %3, %3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(0), "r"(c3), "r"(c4)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st2(uint32_t taddr, float a, float b)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(taddr), "f"(a), "f"(b) : "memory");
+}
+
+// two columns; complete on return
+__device__ __forceinline__ void tmem_ld2(uint32_t taddr, float &a, float &b)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : "=f"(a), "=f"(b)
+                 : "r"(taddr)
+                 : "memory");
 }
 
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
@@ -197,6 +249,9 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return d;
 }
 
+// An item of at most one stream's rows is shared by both streams, tile by tile.
+__device__ __forceinline__ bool in_two(const Segment &s) { return s.r.rows <= 128 && s.units > 1; }
+
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kChunkThreads, 1)
 attn_chunk_kernel(const __grid_constant__ AttnParams p)
@@ -213,8 +268,9 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
     long long *red = reinterpret_cast<long long *>(smem + L::kOffRed);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::kOffBar);
     uint64_t *empty = full + kRing;
-    uint64_t *q_full = empty + kRing, *s_full = q_full + 2, *p_full = s_full + 2, *o_full = p_full + 4;
-    uint64_t *drain = o_full + 2;
+    uint64_t *patch = empty + kRing;
+    uint64_t *q_full = patch + kRing, *s_full = q_full + 2, *p_full = s_full + 2, *o_full = p_full + 4;
+    uint64_t *x_full = o_full + 2, *x_done = x_full + 1, *drain = x_done + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kOffTmem);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -227,6 +283,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
         for (int i = 0; i < kRing; ++i) {
             mbar_init(&full[i], kLoadWarps);
             mbar_init(&empty[i], 1);
+            mbar_init(&patch[i], 1);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&q_full[s], kSoftWarps);
@@ -235,6 +292,8 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
             mbar_init(&p_full[2 * s + 1], kSoftWarps);
             mbar_init(&o_full[s], 1);
         }
+        mbar_init(x_full, kSoftWarps);
+        mbar_init(x_done, kSoftWarps);
         mbar_init(drain, 1);
         fence_barrier_init();
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -247,7 +306,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
     const uint32_t tmem = *tmem_slot;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (!p.whole && threadIdx.x == 0)
-        p.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
+        p.meta[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
     find_share<kChunkRows, kChunkKeys, kChunkSetup, kChunkThreads>(p, red, &share);
 
     bool ok = true;
@@ -276,16 +335,21 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
         uint8_t *qs = smem + L::kOffQ + s * L::kTile;
         uint32_t ph = 0;         // parity of the next S
         uint32_t oph = 0;        // parity of the next O
-        // the next segment that has rows for this stream
-        auto next_rows = [&](Segment &x) -> bool {
+        uint32_t xph = 0;        // parity of the next exchange between the streams
+        // the next segment this stream has a part in: rows of its own, or every other
+        // tile of an item of one stream's rows
+        auto next_part = [&](Segment &x) -> bool {
             while (next(x))
-                if (x.r.rows > 128 * s)
+                if (x.r.rows > 128 * s || in_two(x))
                     return true;
             return false;
         };
         // this warp's 32 query rows into the operand tile (zeros past the item); every
-        // product that read the previous ones is complete
+        // product that read the previous ones is complete.  Stream 1 has none where it
+        // shares stream 0's rows.
         auto load_q = [&](const Segment &x) {
+            if (s == 1 && x.r.rows <= 128)
+                return;
             const int c = lane % kChunks;
 #pragma unroll 4
             for (int e = 0; e < 32; e += kRowsPerCopy) {
@@ -295,11 +359,9 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                 const uint16_t *src = p.q;
                 if (in)
                     src += (x.r.t0 + tok) * p.q_stride + static_cast<long long>(x.h * p.group + rr - tok * p.group) * D + 8 * c;
-                cp_async16_or_zero(smem_u32(qs + sw_addr(row, c)), src, in);
+                cp_async16_or_zero(smem_u32(qs + q_addr(row, c)), src, in);
             }
             cp_async_commit();
-        };
-        auto q_ready = [&]() {
             cp_async_wait_group<0>();
             fence_proxy_async_smem();
             __syncwarp();
@@ -307,21 +369,22 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                 mbar_arrive(&q_full[s]);
         };
         int cur = 0;
-        bool have = next_rows(segs[0]);
-        if (have) {
+        bool have = next_part(segs[0]);
+        if (have)
             load_q(segs[0]);
-            q_ready();
-        }
         while (have) {
             const Segment &sg = segs[cur];
             const RowTile &r = sg.r;
-            const int row = quarter * 32 + lane;
-            const int rr = r.row0 + 128 * s + row;
+            const bool two = in_two(sg);
+            const int row = quarter * 32 + lane, trow = (two ? 0 : 128 * s) + row;   // row in the stream, in the item
+            const int rr = r.row0 + trow;
             const int units = sg.units, kb0 = (r.unit0 + sg.off) * kChunkKeys;
             const int2 see = row_keys(p, r, rr);
+            have = next_part(segs[cur ^ 1]);     // looked up while the first product runs
             float mref = -INFINITY, l = 0.f;
             const uint64_t scale2 = pair(__float_as_uint(p.scale_log2), __float_as_uint(p.scale_log2));
-            for (int j = 0; j < units; ++j) {
+            const int j0 = two ? s : 0, step = two ? 2 : 1;
+            for (int j = j0; j < units; j += step) {
                 if (!(ok = __all_sync(0xffffffffu, mbar_wait(&s_full[s], ph, p.status))))
                     break;
                 ph ^= 1u;
@@ -359,7 +422,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                     const float a = up ? ex2(mref - m) : 1.f;
                     mref = up ? m : mref;
                     l *= a;
-                    if (j > 0) {
+                    if (j > j0) {
 #pragma unroll
                         for (int c = 0; c < D; c += 32) {
                             uint32_t o[32];
@@ -413,25 +476,62 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
             if (!ok)
                 break;
             tc_fence_after();
-            // the next segment's queries are under way while this one's rows go out
-            have = next_rows(segs[cur ^ 1]);
-            if (have)
-                load_q(segs[cur ^ 1]);
+            // an item shared by both streams: stream 1 leaves its maximum and sum beside
+            // its output in tensor memory, stream 0 (same rows, same lanes) adds both up
+            float w0 = 1.f, w1 = 0.f;
+            if (two) {
+                const uint32_t tx = tmem + lanes + s_col(1), to1 = tmem + lanes + o_col(1);
+                if (s == 1) {
+                    tmem_st2(tx, mref, l);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(x_full);
+                    ok = __all_sync(0xffffffffu, mbar_wait(x_done, xph, p.status));
+                    xph ^= 1u;
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    cur ^= 1;
+                    if (have)
+                        load_q(segs[cur]);
+                    continue;
+                }
+                ok = __all_sync(0xffffffffu, mbar_wait(x_full, xph, p.status));
+                xph ^= 1u;
+                if (!ok)
+                    break;
+                tc_fence_after();
+                float m1, l1;
+                tmem_ld2(tx, m1, l1);
+                const float m = fmaxf(mref, m1), base = m == -INFINITY ? 0.f : m;
+                w0 = ex2(mref - base);
+                w1 = ex2(m1 - base);
+                mref = m;
+                l = w0 * l + w1 * l1;
+            }
             // rows to memory: the item's output, or this block's part of it
-            const bool live = 128 * s + row < r.rows;
             const bool whole = is_whole(sg);
-            const int tok = rr / p.group;
-            const long long at = static_cast<long long>(r.t0 + tok) * p.q_heads + sg.h * p.group + rr - tok * p.group;
-            const long long pr = static_cast<long long>(part_slot(sg)) * kChunkRows + 128 * s + row;
             const float inv = l > 0.f ? 1.f / l : 0.f;
+            float *part = p.part_o + static_cast<long long>(part_slot(sg)) * (kChunkRows * D) + 4 * trow;
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 uint32_t o[32];
                 tmem_ld32_start(to + c, o);
                 tmem_ld_wait();
                 pin32(o);
-                if (live && whole) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(p.out + at * D + c);
+                if (two) {
+                    uint32_t o1[32];
+                    tmem_ld32_start(tmem + lanes + o_col(1) + c, o1);
+                    tmem_ld_wait();
+                    pin32(o1);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        o[e] = __float_as_uint(w0 * __uint_as_float(o[e]) + w1 * __uint_as_float(o1[e]));
+                }
+                if (whole) {
+                    // through the stream's query tile, so that a warp stores whole rows
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         uint32_t w[4];
@@ -439,122 +539,164 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                         for (int f = 0; f < 4; ++f)
                             w[f] = pack16<BF16>(__uint_as_float(o[8 * e + 2 * f]) * inv,
                                                 __uint_as_float(o[8 * e + 2 * f + 1]) * inv);
-                        dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+                        *reinterpret_cast<uint4 *>(qs + q_addr(row, c / 8 + e)) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
-                } else if (live) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(p.part_o + pr * D + c);
+                } else if (trow < r.rows) {
+                    // parts lie [D / 4][rows][4], so that a warp's rows are consecutive
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        *reinterpret_cast<uint4 *>(part + (c / 4 + e) * (4 * kChunkRows)) =
+                            make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                 }
             }
-            if (live && whole && p.lse)
-                p.lse[at] = l > 0.f ? (mref - kShift + log2f(l)) * 0.6931471805599453f : -INFINITY;
-            if (live && !whole)
-                *reinterpret_cast<float2 *>(p.part_ml + pr * 2) = make_float2(mref, l);
             tc_fence_before();   // the accumulators are read; the next P says so to the issuing warp
+            __syncwarp();
+            if (two && lane == 0)
+                mbar_arrive(x_done);
+            if (whole) {
+                const int c = lane % kChunks;
+#pragma unroll 4
+                for (int e = 0; e < 32; e += kRowsPerCopy) {
+                    const int qrow = quarter * 32 + e + lane / kChunks;
+                    const int irow = trow - row + qrow, orow = r.row0 + irow, tok = orow / p.group;
+                    if (irow < r.rows)
+                        *reinterpret_cast<uint4 *>(p.out + (static_cast<long long>(r.t0 + tok) * p.q_heads +
+                                                            sg.h * p.group + orow - tok * p.group) * D + 8 * c) =
+                            *reinterpret_cast<const uint4 *>(qs + q_addr(qrow, c));
+                }
+                if (p.lse && trow < r.rows) {
+                    const int tok = rr / p.group;
+                    p.lse[static_cast<long long>(r.t0 + tok) * p.q_heads + sg.h * p.group + rr - tok * p.group] =
+                        l > 0.f ? (mref - kShift + log2f(l)) * 0.6931471805599453f : -INFINITY;
+                }
+                __syncwarp();    // the rows are read before the next queries replace them
+            } else if (trow < r.rows) {
+                *reinterpret_cast<float2 *>(p.part_ml + (static_cast<long long>(part_slot(sg)) * kChunkRows + trow) * 2) =
+                    make_float2(mref, l);
+            }
             if (threadIdx.x == 0 && is_last_part(sg))
-                p.meta[blockIdx.x] = make_int4(sg.i, sg.h, sg.first, 0);
-            if (have)
-                q_ready();
+                write_meta(p, sg);
             cur ^= 1;
+            if (have)
+                load_q(segs[cur]);
         }
-        cp_async_wait_group<0>();
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == kIssueWarp) {
             // ================= product issue =================
-            {
-                const Segment &sg = segs[0];
-                const uint32_t id_qk = f16_idesc(BF16, 128, kChunkKeys);
-                const uint32_t id_pv = f16_idesc(BF16, 128, D) | (1u << 16);   // B is MN-major
-                const uint64_t q_desc = sw128_desc(smem_u32(smem + L::kOffQ));
-                const uint64_t k_desc = sw128_desc(smem_u32(smem + L::kOffRing));
-                const uint64_t v_desc = sw128_desc_mn(smem_u32(smem + L::kOffRing), 128 * 128);
-                int slot = 0;            // ring slot of the next tile (K_0 V_0 K_1 V_1 ...)
-                uint32_t par = 0;
-                uint32_t qph[2] = {0, 0}, pph[2] = {0, 0};
-                auto advance = [&]() {
-                    if (++slot == kRing) {
-                        slot = 0;
-                        par ^= 1u;
-                    }
-                };
-                // S of stream s from the K tile in slot ks
-                auto qk = [&](int s, int ks) {
-                    const uint64_t a = q_desc + ((s * L::kTile) >> 4), b = k_desc + ((ks * L::kTile) >> 4);
+            // The whole warp runs this, one elected lane issues: with warp-uniform
+            // control flow the operand descriptors stay in uniform registers.  (A
+            // single lane's loop spent 70 to 170 cycles a product on moving them there,
+            // and bound the kernel: a product takes 64.)  A timed-out wait only skips
+            // the later waits: the loops run on, over data that nobody uses.
+            const uint32_t id_qk = f16_idesc(BF16, 128, kChunkKeys);
+            const uint32_t id_pv = f16_idesc(BF16, 128, D) | (1u << 16);   // B is MN-major
+            const uint64_t q_desc = swizzled_desc(smem_u32(smem + L::kOffQ), 16, 1024);
+            const uint64_t k_desc = swizzled_desc(smem_u32(smem + L::kOffRing), 16, D * 16);
+            const uint64_t v_desc = swizzled_desc(smem_u32(smem + L::kOffRing), 1024, D * 16);
+            unsigned tile0 = 0;          // ring tiles K_0 V_0 K_1 V_1 ... of the segments before
+            uint32_t qph = 0, pph = 0;   // parities, bit s for stream s
+            auto wait = [&](uint64_t *bar, uint32_t parity) {
+                if (ok)
+                    ok = mbar_wait(bar, parity, p.status);
+                tc_fence_after();
+            };
+            // waits for ring tile i of the segment and returns its slot
+            auto landed = [&](int i) -> int {
+                const unsigned at = tile0 + static_cast<unsigned>(i), slot = at % kRing;
+                wait(&full[slot], at / kRing & 1u);
+                return static_cast<int>(slot);
+            };
+            // S of stream s from query tile qt and the K tile in slot ks, whose last reader
+            // frees it
+            auto qk = [&](int s, int qt, int ks, bool last) {
+                const uint64_t a = q_desc + static_cast<uint32_t>((qt * L::kTile) >> 4);
+                const uint64_t b = k_desc + static_cast<uint32_t>((ks * L::kTile) >> 4);
+                if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t step = (kk >> 2) * (128 * 128 / 16) + (kk & 3) * 2;
-                        tc_mma(tmem + s_col(s), a + step, b + step, id_qk, kk > 0 ? 1u : 0u);
+                        tc_mma(tmem + s_col(s), a + (kk >> 2) * (128 * 128 / 16) + (kk & 3) * 2,
+                               b + (kk >> 2) * (1024 / 16) + (kk & 3) * 2, id_qk, kk > 0 ? 1u : 0u);
                     }
                     tc_commit(&s_full[s]);
-                };
-                bool busy = false;
-                while (next(segs[0])) {
-                    if (lane != 0 || !ok)
-                        continue;
-                    const int ns = sg.r.rows > 128 ? 2 : 1;
-                    if (!(ok = mbar_wait(&full[slot], par, p.status)))
-                        continue;
-                    for (int s = 0; s < ns && ok; ++s) {
-                        if (!(ok = mbar_wait(&q_full[s], qph[s], p.status)))
-                            break;
-                        qph[s] ^= 1u;
-                        tc_fence_after();
-                        qk(s, slot);
-                        busy = true;
-                    }
-                    if (!ok)
-                        continue;
-                    tc_commit(&empty[slot]);
-                    advance();
-                    for (int j = 0; j < sg.units && ok; ++j) {
-                        const int vs = slot;
-                        if (!(ok = mbar_wait(&full[slot], par, p.status)))
-                            break;
-                        advance();
-                        const bool more = j + 1 < sg.units;
-                        for (int s = 0; s < ns; ++s) {
-                            const uint64_t b = v_desc + ((vs * L::kTile) >> 4);
+                    if (last)
+                        tc_commit(&empty[ks]);
+                }
+                __syncwarp();
+            };
+            // O of stream s (+)= P V over one half of the tile's keys, V in slot vs
+            auto pv = [&](int s, int vs, int half, bool first) {
+                const uint64_t b = v_desc + static_cast<uint32_t>((vs * L::kTile) >> 4);
+                if (elect_one()) {
 #pragma unroll
-                            for (int kk = 0; kk < kChunkKeys / 16; ++kk) {
-                                if (kk == 0 || kk == kChunkKeys / 32) {   // a half of the weights
-                                    if (ok)
-                                        ok = mbar_wait(&p_full[2 * s + (kk ? 1 : 0)], pph[s], p.status);
-                                    tc_fence_after();
-                                }
-                                if (ok)
-                                    tc_mma_ts(tmem + o_col(s), tmem + s_col(s) + 8 * kk, b + kk * (2048 >> 4), id_pv,
-                                              kk > 0 || j > 0 ? 1u : 0u);
-                            }
-                            if (!ok)
-                                break;
-                            pph[s] ^= 1u;
+                    for (int e = 0; e < kChunkKeys / 32; ++e) {
+                        const int kk = half * (kChunkKeys / 32) + e;
+                        tc_mma_ts(tmem + o_col(s), tmem + s_col(s) + 8 * kk, b + kk * (2 * D * 16 / 16), id_pv,
+                                  e > 0 || !first ? 1u : 0u);
+                    }
+                }
+                __syncwarp();
+            };
+            auto commit = [&](uint64_t *bar) {
+                if (elect_one())
+                    tc_commit(bar);
+                __syncwarp();
+            };
+            // P V of stream s, half by half as its weights come
+            auto weigh = [&](int s, int vs, bool first) {
+                wait(&p_full[2 * s], pph >> s & 1u);
+                pv(s, vs, 0, first);
+                wait(&p_full[2 * s + 1], pph >> s & 1u);
+                pv(s, vs, 1, false);
+                pph ^= 1u << s;
+            };
+            while (next(segs[0])) {
+                const int ns = __shfl_sync(0xffffffffu, segs[0].r.rows > 128 ? 2 : 1, 0);
+                const int units = __shfl_sync(0xffffffffu, segs[0].units, 0);
+                if (ns == 1 && units > 1) {
+                    // one stream's rows: even tiles on stream 0, odd ones on stream 1
+                    wait(&q_full[0], qph & 1u);
+                    qph ^= 1u;
+                    qk(0, 0, landed(0), true);
+                    qk(1, 0, landed(2), true);
+                    for (int j = 0; j < units; ++j) {
+                        const int s = j & 1, vs = landed(2 * j + 1);
+                        weigh(s, vs, j < 2);
+                        commit(&empty[vs]);
+                        if (j + 2 < units)
+                            qk(s, 0, landed(2 * j + 4), true);
+                        else
+                            commit(&o_full[s]);
+                    }
+                } else {
+                    int ks = landed(0);
+                    for (int s = 0; s < ns; ++s) {
+                        wait(&q_full[s], qph >> s & 1u);
+                        qph ^= 1u << s;
+                        qk(s, s, ks, s == ns - 1);
+                    }
+                    for (int j = 0; j < units; ++j) {
+                        const int vs = landed(2 * j + 1);
+                        for (int s = 0; s < ns; ++s) {
+                            weigh(s, vs, j == 0);
                             if (s == ns - 1)
-                                tc_commit(&empty[vs]);
-                            if (more) {
-                                if (s == 0 && !(ok = mbar_wait(&full[slot], par, p.status)))
-                                    break;
-                                tc_fence_after();
-                                qk(s, slot);
+                                commit(&empty[vs]);
+                            if (j + 1 < units) {
+                                if (s == 0)
+                                    ks = landed(2 * j + 2);
+                                qk(s, s, ks, s == ns - 1);
                             } else {
-                                tc_commit(&o_full[s]);
+                                commit(&o_full[s]);
                             }
-                        }
-                        if (ok && more) {
-                            tc_commit(&empty[slot]);
-                            advance();
                         }
                     }
                 }
-                // drain: every product issued has completed (each barrier phase that a
-                // softmax warp waits on covers the products before it; after a timeout
-                // wait for them here)
-                if (lane == 0 && busy && !ok) {
-                    tc_commit(drain);
-                    mbar_wait(drain, 0, p.status);
-                }
+                tile0 += 2u * static_cast<unsigned>(units);
+            }
+            // after a timeout nobody has waited for the products: wait here
+            if (!__all_sync(0xffffffffu, ok)) {
+                commit(drain);
+                mbar_wait(drain, 0, p.status);
             }
             __syncwarp();
         } else {
@@ -564,46 +706,116 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
             const int sub = lane / kChunks, chunk = lane % kChunks;
             const uint32_t ring = smem_u32(smem + L::kOffRing);
             int issued = 0, signalled = 0;      // tiles
-            // tiles [signalled, upto) have landed: make them visible to the products
+            uint32_t copied = 0;                // bit i % 32: tile i came by plain copies
+            // plain-copied tiles in [signalled, upto) have landed: make them visible to
+            // the products
             auto signal = [&](int upto) {
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0)
                     for (int i = signalled; i < upto; ++i)
-                        mbar_arrive(&full[i % kRing]);
+                        if (copied >> (i & 31) & 1u)
+                            mbar_arrive(&full[i % kRing]);
                 signalled = upto;
             };
+            // tensor copies: lane x of the first loading warp brings box x of a tile
+            const bool boxes = p.box > 0 && lane * p.box < kChunkKeys;
+            uint32_t patched = 0;               // parities of the patch barriers, bit per slot
+            if (w == 0 && lane == 0 && p.box > 0) {
+                prefetch_tmap(&p.tmk);
+                prefetch_tmap(&p.tmv);
+            }
             const Segment &sg = segs[0];
             while (ok && next(segs[0])) {
                 const RowTile r = sg.r;
-                const uint16_t *base[2] = {static_cast<const uint16_t *>(p.kv.k) + sg.h * p.kv.head_stride,
-                                           static_cast<const uint16_t *>(p.kv.v) + sg.h * p.kv.head_stride};
-                for (int j = 0; j < sg.units && ok; ++j) {
-                    const int kb = (r.unit0 + sg.off + j) * kChunkKeys;
-                    // the lane looks up the places of two of the rows this warp copies: copy i
-                    // (i = 0, 1, ...) covers rows kRowsPerCopy (w + kLoadWarps i) + (0 .. kRowsPerCopy)
-                    long long place[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int idx = lane + 32 * e;
-                        const int grp = w + kLoadWarps * (idx / kRowsPerCopy);
-                        const int key = kb + grp * kRowsPerCopy + idx % kRowsPerCopy;
-                        place[e] = grp < kGroups && key >= r.lo && key < r.hi ? key_offset(p.kv, r.b, key, p.status) : -1;
+                const int h = sg.h, units = sg.units, kb0 = (r.unit0 + sg.off) * kChunkKeys;
+                const uint16_t *base[2] = {static_cast<const uint16_t *>(p.kv.k) + h * p.kv.head_stride,
+                                           static_cast<const uint16_t *>(p.kv.v) + h * p.kv.head_stride};
+                // place of the lane's box of tile j in the tensor map (x -1: nobody sees any
+                // of its keys), looked up one tile ahead
+                auto find_box = [&](int j) -> int2 {
+                    const int key = kb0 + j * kChunkKeys + lane * p.box;
+                    if (w != 0 || !boxes || j >= units || key >= r.hi || key + p.box <= r.lo)
+                        return make_int2(-1, 0);
+                    const int blk = static_cast<int>(static_cast<unsigned>(key) / static_cast<unsigned>(p.kv.page_size));
+                    const int page = p.kv.block_table[static_cast<long long>(r.b) * p.kv.blocks + blk];
+                    if (page < 0 || page >= p.kv.num_pages) {
+                        record_error(p.status, QMM_ERR_INDEX);
+                        return make_int2(-1, 0);
                     }
+                    return make_int2(page * p.page_step + h, (key - blk * p.kv.page_size) >> 3);
+                };
+                int2 at = find_box(0);
+                for (int j = 0; j < units && ok; ++j) {
+                    const int kb = kb0 + j * kChunkKeys;
+                    const bool edge = kb < r.lo || kb + kChunkKeys > r.hi;   // some keys are seen by nobody
+                    const int2 here = at;
+                    at = find_box(j + 1);
+                    // plain copies: the lane looks up the places of two of the rows this warp
+                    // copies: copy i (i = 0, 1, ...) covers rows kRowsPerCopy (w + kLoadWarps i) +
+                    // (0 .. kRowsPerCopy)
+                    long long place[2] = {-1, -1};
+                    if (p.box == 0) {
 #pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int idx = lane + 32 * e;
+                            const int grp = w + kLoadWarps * (idx / kRowsPerCopy);
+                            const int key = kb + grp * kRowsPerCopy + idx % kRowsPerCopy;
+                            if (grp < kGroups && key >= r.lo && key < r.hi)
+                                place[e] = key_offset(p.kv, r.b, key, p.status);
+                        }
+                    }
+#pragma unroll 1
                     for (int half = 0; half < 2; ++half) {           // K, then V
                         const int slot = issued % kRing, round = issued / kRing;
                         if (round > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait(&empty[slot], (round - 1) & 1, p.status))))
                             break;
                         const uint32_t dst = ring + slot * L::kTile;
+                        if (p.box > 0) {
+                            // V rows that nobody sees must be zero (0 x NaN): such a tile lands on
+                            // the patch barrier first, the other two warps clear the rows and only
+                            // then say that the slot is full
+                            const bool clear = half == 1 && edge;
+                            if (w == 0) {
+                                const bool mine = here.x >= 0;
+                                const uint32_t n = __popc(__ballot_sync(0xffffffffu, mine));
+                                uint64_t *bar = clear ? &patch[slot] : &full[slot];
+                                if (lane == 0) {
+                                    mbar_arrive_expect_tx(bar, n * static_cast<uint32_t>(p.box * D * 2));
+                                    if (clear)
+                                        mbar_arrive(&full[slot]);
+                                }
+                                __syncwarp();
+                                if (mine)
+                                    tma_load_5d(dst + lane * (p.box * D * 2), half ? &p.tmv : &p.tmk, bar, here.y, here.x);
+                            } else {
+                                if (clear) {
+                                    if (!(ok = __all_sync(0xffffffffu, mbar_wait(&patch[slot], patched >> slot & 1u, p.status))))
+                                        break;
+                                    uint8_t *tile = smem + L::kOffRing + slot * L::kTile;
+                                    for (int row = (w - 1) * kRowsPerCopy + sub; row < kChunkKeys; row += 2 * kRowsPerCopy)
+                                        if (kb + row < r.lo || kb + row >= r.hi)
+                                            *reinterpret_cast<uint4 *>(tile + kv_addr<D>(row, chunk)) = make_uint4(0u, 0u, 0u, 0u);
+                                    fence_proxy_async_smem();
+                                    __syncwarp();
+                                }
+                                if (lane == 0)
+                                    mbar_arrive(&full[slot]);
+                            }
+                            if (clear)
+                                patched ^= 1u << slot;
+                            copied &= ~(1u << (issued & 31));
+                        } else {
 #pragma unroll 4
-                        for (int i = 0; w + kLoadWarps * i < kGroups; ++i) {
-                            const int idx = i * kRowsPerCopy + sub;
-                            const long long o0 = __shfl_sync(0xffffffffu, place[0], idx & 31);
-                            const long long o1 = __shfl_sync(0xffffffffu, place[1], idx & 31);
-                            const long long o = idx < 32 ? o0 : o1;
-                            const int row = (w + kLoadWarps * i) * kRowsPerCopy + sub;
-                            cp_async16_or_zero(dst + sw_addr(row, chunk), base[half] + (o >= 0 ? o : 0) + chunk * 8, o >= 0);
+                            for (int i = 0; w + kLoadWarps * i < kGroups; ++i) {
+                                const int idx = i * kRowsPerCopy + sub;
+                                const long long o0 = __shfl_sync(0xffffffffu, place[0], idx & 31);
+                                const long long o1 = __shfl_sync(0xffffffffu, place[1], idx & 31);
+                                const long long o = idx < 32 ? o0 : o1;
+                                const int row = (w + kLoadWarps * i) * kRowsPerCopy + sub;
+                                cp_async16_or_zero(dst + kv_addr<D>(row, chunk), base[half] + (o >= 0 ? o : 0) + chunk * 8, o >= 0);
+                            }
+                            copied |= 1u << (issued & 31);
                         }
                         cp_async_commit();
                         ++issued;
@@ -616,6 +828,12 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
             }
             cp_async_wait_group<0>();
             signal(issued);
+            // no copy may still be landing when the block exits, also after a timeout
+            if (w == 0 && lane == 0)
+                for (int i = max(0, issued - kRing); i < issued; ++i)
+                    if (!mbar_wait(&full[i % kRing], (i / kRing) & 1, p.status))
+                        break;
+            __syncwarp();
         }
     }
 

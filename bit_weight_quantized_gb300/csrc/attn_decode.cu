@@ -12,7 +12,7 @@
 // barrier and no exchange between warps until the segment ends.  Two blocks per SM
 // keep 2 x 4 warps x (kStages - 1) x 16 keys x 4 D bytes in flight (128 KB at
 // D = 128).  At the end of a segment the warps' results meet in shared memory.
-// Long axes are split over all blocks (find_share) and joined by the combine kernel.
+// Long axes are split over all blocks (find_share) and joined by attn.cu.
 //
 // The running maximum is replaced only when it grows by more than 2^8 (the scale
 // factors stay within fp32 and fp16 range either way), so the output is rescaled
@@ -109,7 +109,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
     const int vrow = lane & 15, vch = lane >> 4;
 
     if (!p.whole && tid == 0)
-        p.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
+        p.meta[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
 
     Walk<kDecodeRows, kDecodeKeys, kDecodeSetup> walk;
     walk.begin(p, share);
@@ -312,7 +312,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
             }
         }
         if (tid == 0 && is_last_part(sg))
-            p.meta[blockIdx.x] = make_int4(sg.i, sg.h, sg.first, 0);
+            write_meta(p, sg);
         __syncthreads();   // the rings and the query tile are free again
     }
 }

@@ -150,7 +150,7 @@ __device__ __forceinline__ int2 row_keys(const AttnParams &p, const RowTile &r, 
 // lies SETUP behind its start).  Block c takes the stretch [c * chunk, (c + 1) *
 // chunk), chunk = max(min_chunk, total / grid rounded up), so every block has the
 // same work however ragged the batch is.  An item that crosses a block's border
-// leaves partial results (at most two per block) that the combine kernel joins.
+// leaves partial results (at most two per block) that a second kernel joins (attn.cu).
 // The split depends on the lengths alone, so results are the same run to run.
 struct Share {
     long long at, end;       // the block's stretch
@@ -297,6 +297,14 @@ __device__ __forceinline__ int part_slot(const Segment &s) { return 2 * static_c
 __device__ __forceinline__ bool is_whole(const Segment &s) { return s.units == s.r.units; }
 // Whether this block holds the last part, but not all, of the item.
 __device__ __forceinline__ bool is_last_part(const Segment &s) { return s.off > 0 && s.off + s.units == s.r.units; }
+
+// What the joining kernel needs of an item: its first block, its rows, first row and
+// token, and its key head.
+__device__ __forceinline__ void write_meta(const AttnParams &p, const Segment &s)
+{
+    p.meta[2 * blockIdx.x] = make_int4(s.first, s.r.rows, s.r.row0, s.r.t0);
+    p.meta[2 * blockIdx.x + 1] = make_int4(s.h, 0, 0, 0);
+}
 
 }  // namespace
 

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "../../include/qmm.h"
@@ -22,14 +23,19 @@ struct AppendParams {
 cudaError_t launch_kv_append(const AppendParams &p, int num_sms, cudaStream_t stream);
 
 struct AttnParams {
+    // the cache as [page and head][slot / 8][d / 64][slot % 8][d % 64] for tensor copies
+    // of `box` slots (chunk kernel; box = 0: no tensor copies); page i, head h is
+    // index i * page_step + h
+    alignas(64) CUtensorMap tmk, tmv;
+    int box, page_step;
     qmm_paged_kv kv;
     const uint16_t *q;
     uint16_t *out;
     float *lse;                    // or nullptr
     int *status;
-    float *part_o;                 // [2 grid][rows per tile][head_dim] partial outputs
+    float *part_o;                 // [2 grid] partial outputs of a row tile (unnormalized)
     float *part_ml;                // [2 grid][rows per tile][2] their maximum and sum
-    int4 *meta;                    // [grid] the item whose last part block c holds
+    int4 *meta;                    // [grid][2] the item whose last part block c holds
     long long q_stride;
     float scale_log2;              // scale * log2(e): the softmax works in powers of two
     int q_heads, group;            // query heads, query heads per key head
@@ -50,7 +56,9 @@ constexpr int kDecodeBlocksPerSm = 2;
 
 cudaError_t launch_attn_decode(const AttnParams &p, int grid, cudaStream_t stream);
 cudaError_t launch_attn_chunk(const AttnParams &p, int grid, cudaStream_t stream);
-cudaError_t launch_attn_combine(const AttnParams &p, int grid, int rows, cudaStream_t stream);
+
+// Sets p.box and the tensor maps where the cache takes tensor copies.
+void attn_set_tma(AttnParams &p);
 
 // Scratch of a call, and the whole call: kernel choice, split and launches.
 size_t attn_workspace_bytes(int q_heads, int kv_heads, int head_dim, int max_q, int num_sms);
