@@ -249,6 +249,28 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return d;
 }
 
+// Walks rows kStep apart as (token, query head of the key head), with one division
+// in all.
+struct RowCursor {
+    int tok, head, dt, dh, group;
+    __device__ __forceinline__ RowCursor(int row, int step, int g) : group(g)
+    {
+        tok = row / g;
+        head = row - tok * g;
+        dt = step / g;
+        dh = step - dt * g;
+    }
+    __device__ __forceinline__ void next()
+    {
+        tok += dt;
+        head += dh;
+        if (head >= group) {
+            head -= group;
+            ++tok;
+        }
+    }
+};
+
 // An item of at most one stream's rows is shared by both streams, tile by tile.
 __device__ __forceinline__ bool in_two(const Segment &s) { return s.r.rows <= 128 && s.units > 1; }
 
@@ -350,16 +372,16 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
         auto load_q = [&](const Segment &x) {
             if (s == 1 && x.r.rows <= 128)
                 return;
-            const int c = lane % kChunks;
-#pragma unroll 4
+            const int c = lane % kChunks, row0 = quarter * 32 + lane / kChunks;
+            const int left = x.r.rows - 128 * s;        // rows of the stream
+            RowCursor at(x.r.row0 + 128 * s + row0, kRowsPerCopy, p.group);
+            const uint16_t *base = p.q + x.r.t0 * p.q_stride + static_cast<long long>(x.h * p.group) * D + 8 * c;
+#pragma unroll
             for (int e = 0; e < 32; e += kRowsPerCopy) {
-                const int row = quarter * 32 + e + lane / kChunks;
-                const int rr = x.r.row0 + 128 * s + row, tok = rr / p.group;
-                const bool in = 128 * s + row < x.r.rows;
-                const uint16_t *src = p.q;
-                if (in)
-                    src += (x.r.t0 + tok) * p.q_stride + static_cast<long long>(x.h * p.group + rr - tok * p.group) * D + 8 * c;
-                cp_async16_or_zero(smem_u32(qs + q_addr(row, c)), src, in);
+                const int row = row0 + e;
+                cp_async16_or_zero(smem_u32(qs + q_addr(row, c)),
+                                   row < left ? base + at.tok * p.q_stride + at.head * D : p.q, row < left);
+                at.next();
             }
             cp_async_commit();
             cp_async_wait_group<0>();
@@ -554,15 +576,17 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
             if (two && lane == 0)
                 mbar_arrive(x_done);
             if (whole) {
-                const int c = lane % kChunks;
-#pragma unroll 4
+                const int c = lane % kChunks, row0 = quarter * 32 + lane / kChunks;
+                const int left = r.rows - (trow - row);
+                RowCursor at(r.row0 + trow - row + row0, kRowsPerCopy, p.group);
+                uint16_t *base = p.out + (static_cast<long long>(r.t0) * p.q_heads + sg.h * p.group) * D + 8 * c;
+                const int tstride = p.q_heads * D;
+#pragma unroll
                 for (int e = 0; e < 32; e += kRowsPerCopy) {
-                    const int qrow = quarter * 32 + e + lane / kChunks;
-                    const int irow = trow - row + qrow, orow = r.row0 + irow, tok = orow / p.group;
-                    if (irow < r.rows)
-                        *reinterpret_cast<uint4 *>(p.out + (static_cast<long long>(r.t0 + tok) * p.q_heads +
-                                                            sg.h * p.group + orow - tok * p.group) * D + 8 * c) =
-                            *reinterpret_cast<const uint4 *>(qs + q_addr(qrow, c));
+                    if (row0 + e < left)
+                        *reinterpret_cast<uint4 *>(base + static_cast<long long>(at.tok) * tstride + at.head * D) =
+                            *reinterpret_cast<const uint4 *>(qs + q_addr(row0 + e, c));
+                    at.next();
                 }
                 if (p.lse && trow < r.rows) {
                     const int tok = rr / p.group;
@@ -594,7 +618,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
             const uint64_t q_desc = swizzled_desc(smem_u32(smem + L::kOffQ), 16, 1024);
             const uint64_t k_desc = swizzled_desc(smem_u32(smem + L::kOffRing), 16, D * 16);
             const uint64_t v_desc = swizzled_desc(smem_u32(smem + L::kOffRing), 1024, D * 16);
-            unsigned tile0 = 0;          // ring tiles K_0 V_0 K_1 V_1 ... of the segments before
+            unsigned tile0 = 0;          // ring tiles of the segments before
             uint32_t qph = 0, pph = 0;   // parities, bit s for stream s
             auto wait = [&](uint64_t *bar, uint32_t parity) {
                 if (ok)
@@ -658,13 +682,13 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                     wait(&q_full[0], qph & 1u);
                     qph ^= 1u;
                     qk(0, 0, landed(0), true);
-                    qk(1, 0, landed(2), true);
+                    qk(1, 0, landed(1), true);
                     for (int j = 0; j < units; ++j) {
-                        const int s = j & 1, vs = landed(2 * j + 1);
+                        const int s = j & 1, vs = landed(j + 1 < units ? 2 * j + 2 : 2 * j + 1);
                         weigh(s, vs, j < 2);
                         commit(&empty[vs]);
                         if (j + 2 < units)
-                            qk(s, 0, landed(2 * j + 4), true);
+                            qk(s, 0, landed(2 * j + 3), true);
                         else
                             commit(&o_full[s]);
                     }
@@ -731,28 +755,33 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                 const int h = sg.h, units = sg.units, kb0 = (r.unit0 + sg.off) * kChunkKeys;
                 const uint16_t *base[2] = {static_cast<const uint16_t *>(p.kv.k) + h * p.kv.head_stride,
                                            static_cast<const uint16_t *>(p.kv.v) + h * p.kv.head_stride};
-                // place of the lane's box of tile j in the tensor map (x -1: nobody sees any
-                // of its keys), looked up one tile ahead
+                // page and slot / 8 of the lane's box of tile j (slot -1: nobody sees any of its
+                // keys).  Looked up one ring tile ahead, and not looked at before it is used:
+                // the warp would wait for the table's entry here.
                 auto find_box = [&](int j) -> int2 {
                     const int key = kb0 + j * kChunkKeys + lane * p.box;
                     if (w != 0 || !boxes || j >= units || key >= r.hi || key + p.box <= r.lo)
-                        return make_int2(-1, 0);
+                        return make_int2(0, -1);
                     const int blk = static_cast<int>(static_cast<unsigned>(key) / static_cast<unsigned>(p.kv.page_size));
-                    const int page = p.kv.block_table[static_cast<long long>(r.b) * p.kv.blocks + blk];
-                    if (page < 0 || page >= p.kv.num_pages) {
-                        record_error(p.status, QMM_ERR_INDEX);
-                        return make_int2(-1, 0);
-                    }
-                    return make_int2(page * p.page_step + h, (key - blk * p.kv.page_size) >> 3);
+                    return make_int2(p.kv.block_table[static_cast<long long>(r.b) * p.kv.blocks + blk],
+                                     (key - blk * p.kv.page_size) >> 3);
+                };
+                // ring tile i is tile (i >> 1)'s K or V (bit 0): K_0 V_0 K_1 V_1 ..., or, where
+                // both streams take turns, as they need them: K_0 K_1 V_0 K_2 V_1 ...
+                const bool two = in_two(sg);
+                auto ring_tile = [&](int i) -> int {
+                    if (!two || i == 0 || i == 2 * units - 1)
+                        return i;
+                    return i & 1 ? i + 1 : i - 1;
                 };
                 int2 at = find_box(0);
-                for (int j = 0; j < units && ok; ++j) {
-                    const int kb = kb0 + j * kChunkKeys;
+                for (int i = 0; i < 2 * units && ok; ++i) {
+                    const int j = ring_tile(i) >> 1, half = ring_tile(i) & 1, kb = kb0 + j * kChunkKeys;
                     const bool edge = kb < r.lo || kb + kChunkKeys > r.hi;   // some keys are seen by nobody
                     const int2 here = at;
-                    at = find_box(j + 1);
+                    at = find_box(i + 1 < 2 * units ? ring_tile(i + 1) >> 1 : units);
                     // plain copies: the lane looks up the places of two of the rows this warp
-                    // copies: copy i (i = 0, 1, ...) covers rows kRowsPerCopy (w + kLoadWarps i) +
+                    // copies: copy c (c = 0, 1, ...) covers rows kRowsPerCopy (w + kLoadWarps c) +
                     // (0 .. kRowsPerCopy)
                     long long place[2] = {-1, -1};
                     if (p.box == 0) {
@@ -765,65 +794,65 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                                 place[e] = key_offset(p.kv, r.b, key, p.status);
                         }
                     }
-#pragma unroll 1
-                    for (int half = 0; half < 2; ++half) {           // K, then V
-                        const int slot = issued % kRing, round = issued / kRing;
-                        if (round > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait(&empty[slot], (round - 1) & 1, p.status))))
-                            break;
-                        const uint32_t dst = ring + slot * L::kTile;
-                        if (p.box > 0) {
-                            // V rows that nobody sees must be zero (0 x NaN): such a tile lands on
-                            // the patch barrier first, the other two warps clear the rows and only
-                            // then say that the slot is full
-                            const bool clear = half == 1 && edge;
-                            if (w == 0) {
-                                const bool mine = here.x >= 0;
-                                const uint32_t n = __popc(__ballot_sync(0xffffffffu, mine));
-                                uint64_t *bar = clear ? &patch[slot] : &full[slot];
-                                if (lane == 0) {
-                                    mbar_arrive_expect_tx(bar, n * static_cast<uint32_t>(p.box * D * 2));
-                                    if (clear)
-                                        mbar_arrive(&full[slot]);
-                                }
-                                __syncwarp();
-                                if (mine)
-                                    tma_load_5d(dst + lane * (p.box * D * 2), half ? &p.tmv : &p.tmk, bar, here.y, here.x);
-                            } else {
-                                if (clear) {
-                                    if (!(ok = __all_sync(0xffffffffu, mbar_wait(&patch[slot], patched >> slot & 1u, p.status))))
-                                        break;
-                                    uint8_t *tile = smem + L::kOffRing + slot * L::kTile;
-                                    for (int row = (w - 1) * kRowsPerCopy + sub; row < kChunkKeys; row += 2 * kRowsPerCopy)
-                                        if (kb + row < r.lo || kb + row >= r.hi)
-                                            *reinterpret_cast<uint4 *>(tile + kv_addr<D>(row, chunk)) = make_uint4(0u, 0u, 0u, 0u);
-                                    fence_proxy_async_smem();
-                                    __syncwarp();
-                                }
-                                if (lane == 0)
+                    const int slot = issued % kRing, round = issued / kRing;
+                    if (round > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait(&empty[slot], (round - 1) & 1, p.status))))
+                        break;
+                    const uint32_t dst = ring + slot * L::kTile;
+                    if (p.box > 0) {
+                        // V rows that nobody sees must be zero (0 x NaN): such a tile lands on
+                        // the patch barrier first, the other two warps clear the rows and only
+                        // then say that the slot is full
+                        const bool clear = half == 1 && edge;
+                        if (w == 0) {
+                            const bool page_ok = here.x >= 0 && here.x < p.kv.num_pages, mine = here.y >= 0 && page_ok;
+                            if (here.y >= 0 && !page_ok)
+                                record_error(p.status, QMM_ERR_INDEX);
+                            const uint32_t n = __popc(__ballot_sync(0xffffffffu, mine));
+                            uint64_t *bar = clear ? &patch[slot] : &full[slot];
+                            if (lane == 0) {
+                                mbar_arrive_expect_tx(bar, n * static_cast<uint32_t>(p.box * D * 2));
+                                if (clear)
                                     mbar_arrive(&full[slot]);
                             }
-                            if (clear)
-                                patched ^= 1u << slot;
-                            copied &= ~(1u << (issued & 31));
+                            __syncwarp();
+                            if (mine)
+                                tma_load_5d(dst + lane * (p.box * D * 2), half ? &p.tmv : &p.tmk, bar, here.y,
+                                            here.x * p.page_step + h);
                         } else {
-#pragma unroll 4
-                            for (int i = 0; w + kLoadWarps * i < kGroups; ++i) {
-                                const int idx = i * kRowsPerCopy + sub;
-                                const long long o0 = __shfl_sync(0xffffffffu, place[0], idx & 31);
-                                const long long o1 = __shfl_sync(0xffffffffu, place[1], idx & 31);
-                                const long long o = idx < 32 ? o0 : o1;
-                                const int row = (w + kLoadWarps * i) * kRowsPerCopy + sub;
-                                cp_async16_or_zero(dst + kv_addr<D>(row, chunk), base[half] + (o >= 0 ? o : 0) + chunk * 8, o >= 0);
+                            if (clear) {
+                                if (!(ok = __all_sync(0xffffffffu, mbar_wait(&patch[slot], patched >> slot & 1u, p.status))))
+                                    break;
+                                uint8_t *tile = smem + L::kOffRing + slot * L::kTile;
+                                for (int row = (w - 1) * kRowsPerCopy + sub; row < kChunkKeys; row += 2 * kRowsPerCopy)
+                                    if (kb + row < r.lo || kb + row >= r.hi)
+                                        *reinterpret_cast<uint4 *>(tile + kv_addr<D>(row, chunk)) = make_uint4(0u, 0u, 0u, 0u);
+                                fence_proxy_async_smem();
+                                __syncwarp();
                             }
-                            copied |= 1u << (issued & 31);
+                            if (lane == 0)
+                                mbar_arrive(&full[slot]);
                         }
-                        cp_async_commit();
-                        ++issued;
-                        // keep three tiles under way
-                        cp_async_wait_group<3>();
-                        if (issued - 3 > signalled)
-                            signal(issued - 3);
+                        if (clear)
+                            patched ^= 1u << slot;
+                        copied &= ~(1u << (issued & 31));
+                    } else {
+#pragma unroll 4
+                        for (int c = 0; w + kLoadWarps * c < kGroups; ++c) {
+                            const int idx = c * kRowsPerCopy + sub;
+                            const long long o0 = __shfl_sync(0xffffffffu, place[0], idx & 31);
+                            const long long o1 = __shfl_sync(0xffffffffu, place[1], idx & 31);
+                            const long long o = idx < 32 ? o0 : o1;
+                            const int row = (w + kLoadWarps * c) * kRowsPerCopy + sub;
+                            cp_async16_or_zero(dst + kv_addr<D>(row, chunk), base[half] + (o >= 0 ? o : 0) + chunk * 8, o >= 0);
+                        }
+                        copied |= 1u << (issued & 31);
                     }
+                    cp_async_commit();
+                    ++issued;
+                    // keep three tiles under way
+                    cp_async_wait_group<3>();
+                    if (issued - 3 > signalled)
+                        signal(issued - 3);
                 }
             }
             cp_async_wait_group<0>();
