@@ -6,8 +6,9 @@
 // A work item is 256 rows ((token, query head) pairs of one key head, so that a
 // key tile loaded once serves all query heads that share it) as two streams of 128
 // rows; the keys go by in tiles of 128.  Both products run on tcgen05 with their
-// accumulators in tensor memory: per stream S (128 x 128 fp32) and O (128 x D), all
-// 512 columns at D = 128.  P takes S's place as 16-bit values and is the second
+// accumulators in tensor memory: per stream two buffers of S (128 x 64 fp32, the
+// halves of a key tile) and O (128 x D), all 512 columns at D = 128.  P takes S's
+// place as 16-bit values and is the second
 // product's left operand straight from tensor memory; V is its right operand as it
 // lies in the cache ([key][d], the "MN-major" form), so nothing is transposed.  An
 // item of at most 128 rows gives both streams the same rows and every other tile,
@@ -15,19 +16,18 @@
 // up the two at the end, straight from tensor memory.
 //
 // Roles.  Warps 0-3 and 4-7 are the softmax of streams 0 and 1, one thread per row:
-// no exchange between lanes at all.  Warp 8 issues the products; it starts stream
-// 1's while stream 0's softmax runs and the other way round.  Warps 9-11 bring K
-// and V tiles into a ring of kRing slots: where the page size is a multiple of 8 by
+// no exchange between lanes at all.  Warps 8 and 9 issue the
+// streams' products.  Warps 10 and 11 bring K and V tiles into a ring
+// each: where the page size is a multiple of 8 by
 // tensor copies, one per page or part of a page that lies in the tile, all issued by
-// one warp (the other two clear the V rows that nobody sees: past kv_len, before the
+// one warp (the other one clears the V rows that nobody sees: past kv_len, before the
 // window, where 0 x NaN would spoil the product); else by 16-byte asynchronous copies
-// that fill such rows with zeros.  Plain copies alone kept the three warps busy for
-// 6000 cycles a tile pair, three times the products' time.
+// that fill such rows with zeros.  Plain copies alone kept the loading warps busy
+// for 6000 cycles a tile pair, three times the products' time.
 //
 // The running maximum is replaced only when it grows by more than 2^8: the output
 // accumulator in tensor memory is then read, scaled and written back by its
-// stream's own threads, a few times per item; S's arrival implies that the previous
-// product into O is complete, so that needs no barrier of its own.
+// stream's own threads, a few times per item, once the last product into it is done.
 //
 // Bound by the tensor cores for long prompts: 4 D flops per (row, key) pair against
 // one exponential; at one row tile by the key tiles' traffic.
@@ -39,15 +39,12 @@ namespace qmm {
 namespace {
 
 constexpr int kSoftWarps = 4;                       // per stream
-constexpr int kIssueWarp = 2 * kSoftWarps;
-constexpr int kLoadWarp0 = kIssueWarp + 1;
-constexpr int kLoadWarps = 3;
+constexpr int kIssueWarp = 2 * kSoftWarps;          // one per stream
+constexpr int kLoadWarp0 = kIssueWarp + 2;
+constexpr int kLoadWarps = 2;
 constexpr int kChunkThreads = 32 * (kLoadWarp0 + kLoadWarps);
-constexpr int kRing = 5;                            // K and V tiles in shared memory
 constexpr float kChunkGrow = 8.f;
-// registers per thread after the split: 256 x 208 + 128 x 88 = 384 x 168
-constexpr int kSoftRegs = 208, kOtherRegs = 88;
-static_assert(kChunkThreads == 384, "register split");
+constexpr int kHalf = kChunkKeys / 2;               // keys per score buffer
 
 using ChunkWalk = Walk<kChunkRows, kChunkKeys, kChunkSetup>;
 
@@ -55,11 +52,13 @@ template <int D>
 struct ChunkLayout {
     static constexpr int kTile = 128 * D * 2;       // 128 rows of D values: D / 64 halves of [128][64]
     static constexpr int kOffQ = 0;                 // two streams
-    static constexpr int kOffRing = 2 * kTile;
-    static constexpr int kOffBar = kOffRing + kRing * kTile;
-    // ring full / empty / patch, q_full[2], s_full[2], p_full[2][2 halves], o_full[2],
-    // x_full, x_done, drain
-    static constexpr int kNumBars = 3 * kRing + 13;
+    static constexpr int kKRing = D == 64 ? 5 : 3, kVRing = D == 64 ? 5 : 2;   // tiles of each ring
+    static constexpr int kOffK = 2 * kTile;
+    static constexpr int kOffV = kOffK + kKRing * kTile;
+    static constexpr int kOffBar = kOffV + kVRing * kTile;
+    // full / empty of both rings, patch, q_full[2], then per stream and half s_full, p_full
+    // and o_full, x_full, x_done, drain[2], begun, taken
+    static constexpr int kNumBars = 2 * (kKRing + kVRing) + 21;
     static constexpr int kOffTmem = kOffBar + 8 * kNumBars;
     static constexpr int kOffShare = kOffTmem + 16;
     static constexpr int kOffRed = kOffShare + sizeof(Share);
@@ -71,8 +70,8 @@ struct ChunkLayout {
     static_assert(kBytes <= 227 * 1024, "shared memory per block");
 };
 
-// Tensor-memory columns of stream s: S and O.
-__device__ __forceinline__ uint32_t s_col(int s) { return static_cast<uint32_t>(s) * 128u; }
+// Tensor-memory columns of stream s: the score buffers of half h, and O.
+__device__ __forceinline__ uint32_t s_col(int s, int h = 0) { return static_cast<uint32_t>(s) * 128u + static_cast<uint32_t>(h) * 64u; }
 __device__ __forceinline__ uint32_t o_col(int s) { return 256u + static_cast<uint32_t>(s) * 128u; }
 
 // Byte of 16-byte chunk c of row r in a query tile: halves of 64 values, rows of 128
@@ -282,17 +281,21 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
     constexpr int kChunks = D / 8;                     // 16-byte chunks per row
     constexpr int kRowsPerCopy = 32 / kChunks;
     constexpr float kShift = BF16 ? 0.f : 7.f;
+    // Scores by half tiles: a half's buffer is filled again right behind the product
+    // that reads its weights, under the other half's softmax.  At D = 128 a product of
+    // 64 keys is bound by reading both operands from shared memory (6 KB in 32 cycles'
+    // work), so there the two buffers are filled at once.
+    constexpr bool kSplit = D == 64;
 
     // the operand tiles' swizzle needs 1024-byte alignment, which the start of a
     // block's shared memory has (there is no static part); checked below
     extern __shared__ __align__(1024) uint8_t smem[];
     Share &share = *reinterpret_cast<Share *>(smem + L::kOffShare);
     long long *red = reinterpret_cast<long long *>(smem + L::kOffRed);
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::kOffBar);
-    uint64_t *empty = full + kRing;
-    uint64_t *patch = empty + kRing;
-    uint64_t *q_full = patch + kRing, *s_full = q_full + 2, *p_full = s_full + 2, *o_full = p_full + 4;
-    uint64_t *x_full = o_full + 2, *x_done = x_full + 1, *drain = x_done + 1;
+    uint64_t *k_full = reinterpret_cast<uint64_t *>(smem + L::kOffBar), *k_empty = k_full + L::kKRing;
+    uint64_t *v_full = k_empty + L::kKRing, *v_empty = v_full + L::kVRing, *patch = v_empty + L::kVRing;
+    uint64_t *q_full = patch + 1, *s_full = q_full + 2, *p_full = s_full + 4, *o_full = p_full + 4;
+    uint64_t *x_full = o_full + 4, *x_done = x_full + 1, *drain = x_done + 1, *begun = drain + 2, *taken = begun + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kOffTmem);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -302,21 +305,29 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
         return;
     }
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kRing; ++i) {
-            mbar_init(&full[i], kLoadWarps);
-            mbar_init(&empty[i], 1);
-            mbar_init(&patch[i], 1);
+        for (int i = 0; i < L::kKRing; ++i) {
+            mbar_init(&k_full[i], 1);
+            mbar_init(&k_empty[i], 2);
         }
+        for (int i = 0; i < L::kVRing; ++i) {
+            mbar_init(&v_full[i], 1);
+            mbar_init(&v_empty[i], 2);
+        }
+        mbar_init(patch, 1);
         for (int s = 0; s < 2; ++s) {
             mbar_init(&q_full[s], kSoftWarps);
-            mbar_init(&s_full[s], 1);
-            mbar_init(&p_full[2 * s], kSoftWarps);
-            mbar_init(&p_full[2 * s + 1], kSoftWarps);
-            mbar_init(&o_full[s], 1);
+            for (int i = 2 * s; i < 2 * s + 2; ++i) {
+                mbar_init(&s_full[i], 1);
+                mbar_init(&p_full[i], kSoftWarps);
+                mbar_init(&o_full[i], 1);
+            }
         }
         mbar_init(x_full, kSoftWarps);
         mbar_init(x_done, kSoftWarps);
-        mbar_init(drain, 1);
+        mbar_init(&drain[0], 1);
+        mbar_init(&drain[1], 1);
+        mbar_init(begun, 1);
+        mbar_init(taken, 1);
         fence_barrier_init();
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     }
@@ -350,13 +361,11 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
 
     if (warp < kIssueWarp) {
         // ================= softmax of stream s: one row per thread =================
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
         const int s = warp / kSoftWarps, quarter = warp % kSoftWarps;
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         const uint32_t ts = tmem + lanes + s_col(s), to = tmem + lanes + o_col(s);
         uint8_t *qs = smem + L::kOffQ + s * L::kTile;
-        uint32_t ph = 0;         // parity of the next S
-        uint32_t oph = 0;        // parity of the next O
+        uint32_t ph = 0;         // parity of the next tile's barriers
         uint32_t xph = 0;        // parity of the next exchange between the streams
         // the next segment this stream has a part in: rows of its own, or every other
         // tile of an item of one stream's rows
@@ -406,95 +415,100 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
             float mref = -INFINITY, l = 0.f;
             const uint64_t scale2 = pair(__float_as_uint(p.scale_log2), __float_as_uint(p.scale_log2));
             const int j0 = two ? s : 0, step = two ? 2 : 1;
-            for (int j = j0; j < units; j += step) {
-                if (!(ok = __all_sync(0xffffffffu, mbar_wait(&s_full[s], ph, p.status))))
-                    break;
-                ph ^= 1u;
-                tc_fence_after();
-                uint32_t v[128];
+            for (int j = j0; j < units && ok; j += step) {
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    const int b = 2 * s + h;
+                    if (!(ok = __all_sync(0xffffffffu, mbar_wait(&s_full[b], ph, p.status))))
+                        break;
+                    tc_fence_after();
+                    uint32_t v[kHalf];
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    tmem_ld32_start(ts + 32 * c, v + 32 * c);
-                tmem_ld_wait();
+                    for (int c = 0; c < kHalf; c += 32)
+                        tmem_ld32_start(ts + 64 * h + c, v + c);
+                    tmem_ld_wait();
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    pin32(v + 32 * c);
-                const int kb = kb0 + j * kChunkKeys;
-                const int c_lo = see.x - kb, c_hi = see.y - kb;     // the columns this row sees
-                if (__any_sync(0xffffffffu, c_lo > 0 || c_hi < kChunkKeys - 1)) {
+                    for (int c = 0; c < kHalf; c += 32)
+                        pin32(v + c);
+                    const int kb = kb0 + j * kChunkKeys + h * kHalf;
+                    const int c_lo = see.x - kb, c_hi = see.y - kb;     // the columns this row sees
+                    if (__any_sync(0xffffffffu, c_lo > 0 || c_hi < kHalf - 1)) {
 #pragma unroll
-                    for (int c = 0; c < 128; ++c)
-                        if (c < c_lo || c > c_hi)
-                            v[c] = 0xff800000u;                     // -infinity
-                }
-                float mx[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    mx[e] = __uint_as_float(v[e]);
-#pragma unroll
-                for (int c = 4; c + 8 <= 128; c += 8)
+                        for (int c = 0; c < kHalf; ++c)
+                            if (c < c_lo || c > c_hi)
+                                v[c] = 0xff800000u;                     // -infinity
+                    }
+                    float mx[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        mx[e] = max3(mx[e], __uint_as_float(v[c + 2 * e]), __uint_as_float(v[c + 2 * e + 1]));
-                mx[0] = max3(mx[0], __uint_as_float(v[124]), __uint_as_float(v[125]));
-                mx[1] = max3(mx[1], __uint_as_float(v[126]), __uint_as_float(v[127]));
-                const float m = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * p.scale_log2;
-                const bool up = m > mref + kChunkGrow;
-                if (__any_sync(0xffffffffu, up)) {
-                    const float a = up ? ex2(mref - m) : 1.f;
-                    mref = up ? m : mref;
-                    l *= a;
-                    if (j > j0) {
+                        mx[e] = __uint_as_float(v[e]);
 #pragma unroll
-                        for (int c = 0; c < D; c += 32) {
-                            uint32_t o[32];
-                            tmem_ld32_start(to + c, o);
-                            tmem_ld_wait();
-                            pin32(o);
+                    for (int c = 4; c + 8 <= kHalf; c += 8)
 #pragma unroll
-                            for (int e = 0; e < 32; e += 2) {
-                                float x, y;
-                                unpair(mul2_f32(pair(o[e], o[e + 1]), pair(__float_as_uint(a), __float_as_uint(a))), x, y);
-                                o[e] = __float_as_uint(x);
-                                o[e + 1] = __float_as_uint(y);
+                        for (int e = 0; e < 4; ++e)
+                            mx[e] = max3(mx[e], __uint_as_float(v[c + 2 * e]), __uint_as_float(v[c + 2 * e + 1]));
+                    mx[0] = max3(mx[0], __uint_as_float(v[kHalf - 4]), __uint_as_float(v[kHalf - 3]));
+                    mx[1] = max3(mx[1], __uint_as_float(v[kHalf - 2]), __uint_as_float(v[kHalf - 1]));
+                    const float m = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * p.scale_log2;
+                    const bool up = m > mref + kChunkGrow;
+                    if (__any_sync(0xffffffffu, up)) {
+                        const float a = up ? ex2(mref - m) : 1.f;
+                        mref = up ? m : mref;
+                        l *= a;
+                        if (j > j0 || h) {
+                            // the product before this one is complete when its half says so
+                            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&o_full[b ^ 1], h ? ph : ph ^ 1u, p.status))))
+                                break;
+                            tc_fence_after();
+#pragma unroll
+                            for (int c = 0; c < D; c += 32) {
+                                uint32_t o[32];
+                                tmem_ld32_start(to + c, o);
+                                tmem_ld_wait();
+                                pin32(o);
+#pragma unroll
+                                for (int e = 0; e < 32; e += 2) {
+                                    float x, y;
+                                    unpair(mul2_f32(pair(o[e], o[e + 1]), pair(__float_as_uint(a), __float_as_uint(a))), x, y);
+                                    o[e] = __float_as_uint(x);
+                                    o[e + 1] = __float_as_uint(y);
+                                }
+                                tmem_st32(to + c, o);
                             }
-                            tmem_st32(to + c, o);
                         }
                     }
-                }
-                const float neg = kShift - (mref == -INFINITY ? 0.f : mref);
-                const uint64_t neg2 = pair(__float_as_uint(neg), __float_as_uint(neg));
-                uint64_t sum[2] = {0, 0};
-                // weights, rounded to 16 bits for the second product; their first half
-                // is handed over while the second is computed
+                    const float neg = kShift - (mref == -INFINITY ? 0.f : mref);
+                    const uint64_t neg2 = pair(__float_as_uint(neg), __float_as_uint(neg));
+                    // weights, rounded to 16 bits for the second product
+                    uint64_t sum[2] = {0, 0};
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t w[16];
+                    for (int c = 0; c < kHalf / 32; ++c) {
+                        uint32_t w[16];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        float p0, p1;
-                        unpair(fma2(pair(v[32 * c + 2 * e], v[32 * c + 2 * e + 1]), scale2, neg2), p0, p1);
-                        p0 = ex2(p0);
-                        p1 = ex2(p1);
-                        sum[e & 1] = add2(sum[e & 1], pair(__float_as_uint(p0), __float_as_uint(p1)));
-                        w[e] = pack16<BF16>(p0, p1);
+                        for (int e = 0; e < 16; ++e) {
+                            float p0, p1;
+                            unpair(fma2(pair(v[32 * c + 2 * e], v[32 * c + 2 * e + 1]), scale2, neg2), p0, p1);
+                            p0 = ex2(p0);
+                            p1 = ex2(p1);
+                            sum[e & 1] = add2(sum[e & 1], pair(__float_as_uint(p0), __float_as_uint(p1)));
+                            w[e] = pack16<BF16>(p0, p1);
+                        }
+                        tmem_st16(ts + 64 * h + 16 * c, w);
                     }
-                    tmem_st16(ts + 16 * c, w);
-                    if (c & 1) {
-                        tmem_st_wait();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive(&p_full[2 * s + (c >> 1)]);
-                    }
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&p_full[b]);
+                    float s0, s1;
+                    unpair(add2(sum[0], sum[1]), s0, s1);
+                    l += s0 + s1;
                 }
-                float s0, s1;
-                unpair(add2(sum[0], sum[1]), s0, s1);
-                l += s0 + s1;
+                ph ^= 1u;
             }
+            // the last product into O
             if (ok)
-                ok = __all_sync(0xffffffffu, mbar_wait(&o_full[s], oph, p.status));
-            oph ^= 1u;
+                ok = __all_sync(0xffffffffu, mbar_wait(&o_full[2 * s + 1], ph ^ 1u, p.status));
             if (!ok)
                 break;
             tc_fence_after();
@@ -605,262 +619,287 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                 load_q(segs[cur]);
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-        if (warp == kIssueWarp) {
+        if (warp < kLoadWarp0) {
             // ================= product issue =================
+            // Warp 8 issues stream 0's products and, for items that both streams share,
+            // stream 1's too; warp 9 issues stream 1's where it has rows of its own, after
+            // warp 8 has said that such an item begins.  (A warp that skipped tiles on its
+            // own could meet a ring barrier a phase early or late.)
             // The whole warp runs this, one elected lane issues: with warp-uniform
             // control flow the operand descriptors stay in uniform registers.  (A
-            // single lane's loop spent 70 to 170 cycles a product on moving them there,
-            // and bound the kernel: a product takes 64.)  A timed-out wait only skips
-            // the later waits: the loops run on, over data that nobody uses.
-            const uint32_t id_qk = f16_idesc(BF16, 128, kChunkKeys);
+            // single lane's loop spent 70 to 170 cycles a product on moving them there;
+            // one warp for both streams, at 50 cycles a product and 110 a wait, still
+            // bound the kernel.)  A timed-out wait only skips the later waits: the loops
+            // run on, over data that nobody uses.
+            const int me = warp - kIssueWarp;
+            const uint32_t id_qk = f16_idesc(BF16, 128, kSplit ? kHalf : kChunkKeys);
             const uint32_t id_pv = f16_idesc(BF16, 128, D) | (1u << 16);   // B is MN-major
             const uint64_t q_desc = swizzled_desc(smem_u32(smem + L::kOffQ), 16, 1024);
-            const uint64_t k_desc = swizzled_desc(smem_u32(smem + L::kOffRing), 16, D * 16);
-            const uint64_t v_desc = swizzled_desc(smem_u32(smem + L::kOffRing), 1024, D * 16);
-            unsigned tile0 = 0;          // ring tiles of the segments before
-            uint32_t qph = 0, pph = 0;   // parities, bit s for stream s
+            const uint64_t k_desc = swizzled_desc(smem_u32(smem + L::kOffK), 16, D * 16);
+            const uint64_t v_desc = swizzled_desc(smem_u32(smem + L::kOffV), 1024, D * 16);
+            unsigned tile0 = 0;          // key tiles of the segments before
+            uint32_t qph = 0;            // parity of this warp's q_full
+            uint32_t gph = 0;            // parity of `begun` (warp 9) or `taken` (warp 8)
+            bool any = false;            // warp 8: some item began before
+            uint32_t pph = 0;            // parities of p_full, bit per stream
             auto wait = [&](uint64_t *bar, uint32_t parity) {
                 if (ok)
                     ok = mbar_wait(bar, parity, p.status);
                 tc_fence_after();
             };
-            // waits for ring tile i of the segment and returns its slot
-            auto landed = [&](int i) -> int {
-                const unsigned at = tile0 + static_cast<unsigned>(i), slot = at % kRing;
-                wait(&full[slot], at / kRing & 1u);
+            // wait for K or V tile j of the segment and return its slot
+            auto k_landed = [&](int j) -> int {
+                const unsigned at = tile0 + static_cast<unsigned>(j), slot = at % L::kKRing;
+                wait(&k_full[slot], at / L::kKRing & 1u);
                 return static_cast<int>(slot);
             };
-            // S of stream s from query tile qt and the K tile in slot ks, whose last reader
-            // frees it
-            auto qk = [&](int s, int qt, int ks, bool last) {
+            auto v_landed = [&](int j) -> int {
+                const unsigned at = tile0 + static_cast<unsigned>(j), slot = at % L::kVRing;
+                wait(&v_full[slot], at / L::kVRing & 1u);
+                return static_cast<int>(slot);
+            };
+            // `arrivals` on a slot's barrier (it takes two: one from each warp, or both from the
+            // only one that reads the tile), when the products so far are done
+            auto release = [&](uint64_t *bar, int arrivals) {
+                tc_commit(bar);
+                if (arrivals == 2)
+                    tc_commit(bar);
+            };
+            // S of stream s, half h of the keys (or all of them), from query tile qt and the K
+            // tile in slot ks
+            auto qk = [&](int s, int qt, int ks, int h, int arrivals) {
                 const uint64_t a = q_desc + static_cast<uint32_t>((qt * L::kTile) >> 4);
-                const uint64_t b = k_desc + static_cast<uint32_t>((ks * L::kTile) >> 4);
+                const uint64_t b = k_desc + static_cast<uint32_t>((ks * L::kTile + (kSplit ? h * (L::kTile / 2) : 0)) >> 4);
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
-                        tc_mma(tmem + s_col(s), a + (kk >> 2) * (128 * 128 / 16) + (kk & 3) * 2,
+                        tc_mma(tmem + s_col(s, kSplit ? h : 0), a + (kk >> 2) * (128 * 128 / 16) + (kk & 3) * 2,
                                b + (kk >> 2) * (1024 / 16) + (kk & 3) * 2, id_qk, kk > 0 ? 1u : 0u);
                     }
-                    tc_commit(&s_full[s]);
-                    if (last)
-                        tc_commit(&empty[ks]);
+                    if (kSplit) {
+                        tc_commit(&s_full[2 * s + h]);
+                    } else {
+                        tc_commit(&s_full[2 * s]);
+                        tc_commit(&s_full[2 * s + 1]);
+                    }
+                    if (h == 1)
+                        release(&k_empty[ks], arrivals);
                 }
                 __syncwarp();
             };
-            // O of stream s (+)= P V over one half of the tile's keys, V in slot vs
-            auto pv = [&](int s, int vs, int half, bool first) {
-                const uint64_t b = v_desc + static_cast<uint32_t>((vs * L::kTile) >> 4);
+            // O of stream s (+)= P V over half h of the keys, V in slot vs, as soon as the weights are there
+            auto pv = [&](int s, int vs, int h, bool first, int arrivals) {
+                wait(&p_full[2 * s + h], pph >> s & 1u);
+                const uint64_t b = v_desc + static_cast<uint32_t>((vs * L::kTile + h * (L::kTile / 2)) >> 4);
                 if (elect_one()) {
 #pragma unroll
-                    for (int e = 0; e < kChunkKeys / 32; ++e) {
-                        const int kk = half * (kChunkKeys / 32) + e;
-                        tc_mma_ts(tmem + o_col(s), tmem + s_col(s) + 8 * kk, b + kk * (2 * D * 16 / 16), id_pv,
+                    for (int e = 0; e < kHalf / 16; ++e)
+                        tc_mma_ts(tmem + o_col(s), tmem + s_col(s, h) + 8 * e, b + e * (2 * D * 16 / 16), id_pv,
                                   e > 0 || !first ? 1u : 0u);
-                    }
+                    tc_commit(&o_full[2 * s + h]);
+                    if (h == 1)
+                        release(&v_empty[vs], arrivals);
                 }
                 __syncwarp();
-            };
-            auto commit = [&](uint64_t *bar) {
-                if (elect_one())
-                    tc_commit(bar);
-                __syncwarp();
-            };
-            // P V of stream s, half by half as its weights come
-            auto weigh = [&](int s, int vs, bool first) {
-                wait(&p_full[2 * s], pph >> s & 1u);
-                pv(s, vs, 0, first);
-                wait(&p_full[2 * s + 1], pph >> s & 1u);
-                pv(s, vs, 1, false);
-                pph ^= 1u << s;
             };
             while (next(segs[0])) {
                 const int ns = __shfl_sync(0xffffffffu, segs[0].r.rows > 128 ? 2 : 1, 0);
                 const int units = __shfl_sync(0xffffffffu, segs[0].units, 0);
-                if (ns == 1 && units > 1) {
-                    // one stream's rows: even tiles on stream 0, odd ones on stream 1
-                    wait(&q_full[0], qph & 1u);
+                const bool two = ns == 1 && units > 1;   // both streams, tile by tile in turn
+                if (ns == 2) {
+                    if (me == 1) {
+                        wait(begun, gph);
+                        gph ^= 1u;
+                        if (lane == 0)
+                            mbar_arrive(taken);
+                    }
+                    wait(&q_full[me], qph);
                     qph ^= 1u;
-                    qk(0, 0, landed(0), true);
-                    qk(1, 0, landed(1), true);
-                    for (int j = 0; j < units; ++j) {
-                        const int s = j & 1, vs = landed(j + 1 < units ? 2 * j + 2 : 2 * j + 1);
-                        weigh(s, vs, j < 2);
-                        commit(&empty[vs]);
-                        if (j + 2 < units)
-                            qk(s, 0, landed(2 * j + 3), true);
-                        else
-                            commit(&o_full[s]);
+                    if (me == 0) {
+                        if (any)
+                            wait(taken, gph);   // of the last such item: one signal at a time
+                        gph ^= any ? 1u : 0u;
+                        any = true;
+                        if (lane == 0)
+                            mbar_arrive(begun);
                     }
-                } else {
-                    int ks = landed(0);
-                    for (int s = 0; s < ns; ++s) {
-                        wait(&q_full[s], qph >> s & 1u);
-                        qph ^= 1u << s;
-                        qk(s, s, ks, s == ns - 1);
-                    }
+                    int ks = k_landed(0);
+                    if (kSplit)
+                        qk(me, me, ks, 0, 1);
+                    qk(me, me, ks, 1, 1);
                     for (int j = 0; j < units; ++j) {
-                        const int vs = landed(2 * j + 1);
-                        for (int s = 0; s < ns; ++s) {
-                            weigh(s, vs, j == 0);
-                            if (s == ns - 1)
-                                commit(&empty[vs]);
-                            if (j + 1 < units) {
-                                if (s == 0)
-                                    ks = landed(2 * j + 2);
-                                qk(s, s, ks, s == ns - 1);
-                            } else {
-                                commit(&o_full[s]);
-                            }
+                        const int vs = v_landed(j);
+                        const bool more = j + 1 < units;
+                        pv(me, vs, 0, j == 0, 1);
+                        if (kSplit && more) {
+                            ks = k_landed(j + 1);
+                            qk(me, me, ks, 0, 1);
                         }
+                        pv(me, vs, 1, false, 1);
+                        if (more) {
+                            if (!kSplit)
+                                ks = k_landed(j + 1);
+                            qk(me, me, ks, 1, 1);
+                        }
+                        pph ^= 3u;
                     }
+                } else if (me == 0) {
+                    // one stream's rows: tile by tile in turn on both; a single tile on stream 0
+                    const int step = two ? 2 : 1;
+                    wait(&q_full[0], qph);
+                    qph ^= 1u;
+                    for (int s = 0; s < step; ++s) {
+                        const int ks = k_landed(s);
+                        if (kSplit)
+                            qk(s, 0, ks, 0, 2);
+                        qk(s, 0, ks, 1, 2);
+                    }
+                    for (int j = 0; j < units; ++j) {
+                        const int s = two ? j & 1 : 0, vs = v_landed(j);
+                        const bool more = j + step < units;
+                        int ks = 0;
+                        pv(s, vs, 0, j < step, 2);
+                        if (kSplit && more) {
+                            ks = k_landed(j + 2);
+                            qk(s, 0, ks, 0, 2);
+                        }
+                        pv(s, vs, 1, false, 2);
+                        if (more) {
+                            if (!kSplit)
+                                ks = k_landed(j + 2);
+                            qk(s, 0, ks, 1, 2);
+                        }
+                        pph ^= 1u << s;
+                    }
+                } else if (two && (units >> 1 & 1)) {
+                    pph ^= 2u;           // stream 1's tiles, issued by warp 8
                 }
-                tile0 += 2u * static_cast<unsigned>(units);
+                tile0 += static_cast<unsigned>(units);
             }
             // after a timeout nobody has waited for the products: wait here
             if (!__all_sync(0xffffffffu, ok)) {
-                commit(drain);
-                mbar_wait(drain, 0, p.status);
+                if (elect_one())
+                    tc_commit(&drain[me]);
+                __syncwarp();
+                mbar_wait(&drain[me], 0, p.status);
             }
             __syncwarp();
         } else {
-            // ================= K and V tiles =================
-            constexpr int kGroups = kChunkKeys / kRowsPerCopy;      // warp-wide copies per tile
-            const int w = warp - kLoadWarp0;
+            // ================= K tiles (warp 10) and V tiles (warp 11) =================
+            constexpr int kCopies = kChunkKeys / kRowsPerCopy;      // warp-wide plain copies per tile
+            const bool is_v = warp != kLoadWarp0;
+            const int slots = is_v ? L::kVRing : L::kKRing;
+            uint64_t *full = is_v ? v_full : k_full, *empty = is_v ? v_empty : k_empty;
+            uint8_t *ring = smem + (is_v ? L::kOffV : L::kOffK);
+            const CUtensorMap *map = is_v ? &p.tmv : &p.tmk;
             const int sub = lane / kChunks, chunk = lane % kChunks;
-            const uint32_t ring = smem_u32(smem + L::kOffRing);
-            int issued = 0, signalled = 0;      // tiles
-            uint32_t copied = 0;                // bit i % 32: tile i came by plain copies
-            // plain-copied tiles in [signalled, upto) have landed: make them visible to
-            // the products
-            auto signal = [&](int upto) {
+            const int nbox = p.box > 0 ? kChunkKeys / p.box : 0;     // tensor copies per tile, at most 16
+            const uint32_t box_bytes = static_cast<uint32_t>(p.box * D * 2);
+            int slot = 0, issued = 0;
+            uint32_t par = 1;             // parity of the ring's empty barriers (none to wait for at first)
+            uint32_t patched = 0;         // parity of the patch barrier
+            int unsaid = -1;              // slot of a plain-copied tile that is not announced yet
+            auto announce = [&]() {
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0)
-                    for (int i = signalled; i < upto; ++i)
-                        if (copied >> (i & 31) & 1u)
-                            mbar_arrive(&full[i % kRing]);
-                signalled = upto;
+                    mbar_arrive(&full[unsaid]);
             };
-            // tensor copies: lane x of the first loading warp brings box x of a tile
-            const bool boxes = p.box > 0 && lane * p.box < kChunkKeys;
-            uint32_t patched = 0;               // parities of the patch barriers, bit per slot
-            if (w == 0 && lane == 0 && p.box > 0) {
-                prefetch_tmap(&p.tmk);
-                prefetch_tmap(&p.tmv);
-            }
+            if (lane == 0 && p.box > 0)
+                prefetch_tmap(map);
             const Segment &sg = segs[0];
             while (ok && next(segs[0])) {
                 const RowTile r = sg.r;
                 const int h = sg.h, units = sg.units, kb0 = (r.unit0 + sg.off) * kChunkKeys;
-                const uint16_t *base[2] = {static_cast<const uint16_t *>(p.kv.k) + h * p.kv.head_stride,
-                                           static_cast<const uint16_t *>(p.kv.v) + h * p.kv.head_stride};
-                // page and slot / 8 of the lane's box of tile j (slot -1: nobody sees any of its
-                // keys).  Looked up one ring tile ahead, and not looked at before it is used:
-                // the warp would wait for the table's entry here.
+                const uint16_t *base = static_cast<const uint16_t *>(is_v ? p.kv.v : p.kv.k) + h * p.kv.head_stride;
+                // page and slot / 8 of box `lane` of tile j (slot -1: nobody sees any of its
+                // keys).  Looked up one tile ahead, and not looked at before it is used: the
+                // warp would wait for the table's entry here.
                 auto find_box = [&](int j) -> int2 {
                     const int key = kb0 + j * kChunkKeys + lane * p.box;
-                    if (w != 0 || !boxes || j >= units || key >= r.hi || key + p.box <= r.lo)
+                    if (lane >= nbox || j >= units || key >= r.hi || key + p.box <= r.lo)
                         return make_int2(0, -1);
                     const int blk = static_cast<int>(static_cast<unsigned>(key) / static_cast<unsigned>(p.kv.page_size));
                     return make_int2(p.kv.block_table[static_cast<long long>(r.b) * p.kv.blocks + blk],
                                      (key - blk * p.kv.page_size) >> 3);
                 };
-                // ring tile i is tile (i >> 1)'s K or V (bit 0): K_0 V_0 K_1 V_1 ..., or, where
-                // both streams take turns, as they need them: K_0 K_1 V_0 K_2 V_1 ...
-                const bool two = in_two(sg);
-                auto ring_tile = [&](int i) -> int {
-                    if (!two || i == 0 || i == 2 * units - 1)
-                        return i;
-                    return i & 1 ? i + 1 : i - 1;
-                };
                 int2 at = find_box(0);
-                for (int i = 0; i < 2 * units && ok; ++i) {
-                    const int j = ring_tile(i) >> 1, half = ring_tile(i) & 1, kb = kb0 + j * kChunkKeys;
-                    const bool edge = kb < r.lo || kb + kChunkKeys > r.hi;   // some keys are seen by nobody
+                for (int j = 0; j < units; ++j) {
+                    const int kb = kb0 + j * kChunkKeys;
                     const int2 here = at;
-                    at = find_box(i + 1 < 2 * units ? ring_tile(i + 1) >> 1 : units);
-                    // plain copies: the lane looks up the places of two of the rows this warp
-                    // copies: copy c (c = 0, 1, ...) covers rows kRowsPerCopy (w + kLoadWarps c) +
-                    // (0 .. kRowsPerCopy)
-                    long long place[2] = {-1, -1};
-                    if (p.box == 0) {
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int idx = lane + 32 * e;
-                            const int grp = w + kLoadWarps * (idx / kRowsPerCopy);
-                            const int key = kb + grp * kRowsPerCopy + idx % kRowsPerCopy;
-                            if (grp < kGroups && key >= r.lo && key < r.hi)
-                                place[e] = key_offset(p.kv, r.b, key, p.status);
-                        }
-                    }
-                    const int slot = issued % kRing, round = issued / kRing;
-                    if (round > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait(&empty[slot], (round - 1) & 1, p.status))))
+                    at = find_box(j + 1);
+                    if (issued >= slots && !(ok = __all_sync(0xffffffffu, mbar_wait(&empty[slot], par, p.status))))
                         break;
-                    const uint32_t dst = ring + slot * L::kTile;
-                    if (p.box > 0) {
+                    uint8_t *tile = ring + slot * L::kTile;
+                    if (nbox > 0) {
                         // V rows that nobody sees must be zero (0 x NaN): such a tile lands on
-                        // the patch barrier first, the other two warps clear the rows and only
-                        // then say that the slot is full
-                        const bool clear = half == 1 && edge;
-                        if (w == 0) {
-                            const bool page_ok = here.x >= 0 && here.x < p.kv.num_pages, mine = here.y >= 0 && page_ok;
-                            if (here.y >= 0 && !page_ok)
-                                record_error(p.status, QMM_ERR_INDEX);
-                            const uint32_t n = __popc(__ballot_sync(0xffffffffu, mine));
-                            uint64_t *bar = clear ? &patch[slot] : &full[slot];
-                            if (lane == 0) {
-                                mbar_arrive_expect_tx(bar, n * static_cast<uint32_t>(p.box * D * 2));
-                                if (clear)
-                                    mbar_arrive(&full[slot]);
-                            }
+                        // the patch barrier, the warp clears the rows and then says that the slot
+                        // is full
+                        const bool clear = is_v && (kb < r.lo || kb + kChunkKeys > r.hi);
+                        const bool page_ok = here.x >= 0 && here.x < p.kv.num_pages;
+                        if (here.y >= 0 && !page_ok)
+                            record_error(p.status, QMM_ERR_INDEX);
+                        const uint32_t mine = __ballot_sync(0xffffffffu, here.y >= 0 && page_ok);
+                        uint64_t *bar = clear ? patch : &full[slot];
+                        if (elect_one())
+                            mbar_arrive_expect_tx(bar, static_cast<uint32_t>(__popc(mine)) * box_bytes);
+                        __syncwarp();
+                        // box by box, warp-uniform: lanes that issue side by side take turns
+                        // anyway, and at several times the cost
+                        const int row = here.x * p.page_step + h;
+                        for (int x = 0; x < nbox; ++x) {
+                            const int c3 = __shfl_sync(0xffffffffu, here.y, x), c4 = __shfl_sync(0xffffffffu, row, x);
+                            if ((mine >> x & 1u) && elect_one())
+                                tma_load_5d(smem_u32(tile) + static_cast<uint32_t>(x) * box_bytes, map, bar, c3, c4);
                             __syncwarp();
-                            if (mine)
-                                tma_load_5d(dst + lane * (p.box * D * 2), half ? &p.tmv : &p.tmk, bar, here.y,
-                                            here.x * p.page_step + h);
-                        } else {
-                            if (clear) {
-                                if (!(ok = __all_sync(0xffffffffu, mbar_wait(&patch[slot], patched >> slot & 1u, p.status))))
-                                    break;
-                                uint8_t *tile = smem + L::kOffRing + slot * L::kTile;
-                                for (int row = (w - 1) * kRowsPerCopy + sub; row < kChunkKeys; row += 2 * kRowsPerCopy)
-                                    if (kb + row < r.lo || kb + row >= r.hi)
-                                        *reinterpret_cast<uint4 *>(tile + kv_addr<D>(row, chunk)) = make_uint4(0u, 0u, 0u, 0u);
-                                fence_proxy_async_smem();
-                                __syncwarp();
-                            }
-                            if (lane == 0)
-                                mbar_arrive(&full[slot]);
                         }
-                        if (clear)
-                            patched ^= 1u << slot;
-                        copied &= ~(1u << (issued & 31));
+                        if (clear) {
+                            if (!(ok = __all_sync(0xffffffffu, mbar_wait(patch, patched, p.status))))
+                                break;
+                            patched ^= 1u;
+                            for (int q = sub; q < kChunkKeys; q += kRowsPerCopy)
+                                if (kb + q < r.lo || kb + q >= r.hi)
+                                    *reinterpret_cast<uint4 *>(tile + kv_addr<D>(q, chunk)) = make_uint4(0u, 0u, 0u, 0u);
+                            unsaid = slot;
+                            announce();
+                            unsaid = -1;
+                        }
                     } else {
-#pragma unroll 4
-                        for (int c = 0; w + kLoadWarps * c < kGroups; ++c) {
-                            const int idx = c * kRowsPerCopy + sub;
-                            const long long o0 = __shfl_sync(0xffffffffu, place[0], idx & 31);
-                            const long long o1 = __shfl_sync(0xffffffffu, place[1], idx & 31);
-                            const long long o = idx < 32 ? o0 : o1;
-                            const int row = (w + kLoadWarps * c) * kRowsPerCopy + sub;
-                            cp_async16_or_zero(dst + kv_addr<D>(row, chunk), base[half] + (o >= 0 ? o : 0) + chunk * 8, o >= 0);
+                        // plain copies; the lane looks up the places of kChunkKeys / 32 of the keys
+                        long long place[kChunkKeys / 32];
+#pragma unroll
+                        for (int e = 0; e < kChunkKeys / 32; ++e) {
+                            const int key = kb + 32 * e + lane;
+                            place[e] = key >= r.lo && key < r.hi ? key_offset(p.kv, r.b, key, p.status) : -1;
                         }
-                        copied |= 1u << (issued & 31);
+#pragma unroll
+                        for (int c = 0; c < kCopies; ++c) {
+                            const int q = c * kRowsPerCopy + sub;
+                            const long long o = __shfl_sync(0xffffffffu, place[c * kRowsPerCopy / 32], q & 31);
+                            cp_async16_or_zero(smem_u32(tile + kv_addr<D>(q, chunk)), base + (o >= 0 ? o : 0) + chunk * 8, o >= 0);
+                        }
+                        cp_async_commit();
+                        // the tile before this one has landed
+                        cp_async_wait_group<1>();
+                        if (unsaid >= 0)
+                            announce();
+                        unsaid = slot;
                     }
-                    cp_async_commit();
                     ++issued;
-                    // keep three tiles under way
-                    cp_async_wait_group<3>();
-                    if (issued - 3 > signalled)
-                        signal(issued - 3);
+                    if (++slot == slots) {
+                        slot = 0;
+                        par ^= 1u;
+                    }
                 }
             }
-            cp_async_wait_group<0>();
-            signal(issued);
+            if (unsaid >= 0) {
+                cp_async_wait_group<0>();
+                announce();
+            }
             // no copy may still be landing when the block exits, also after a timeout
-            if (w == 0 && lane == 0)
-                for (int i = max(0, issued - kRing); i < issued; ++i)
-                    if (!mbar_wait(&full[i % kRing], (i / kRing) & 1, p.status))
+            if (lane == 0)
+                for (int i = max(0, issued - slots); i < issued; ++i)
+                    if (!mbar_wait(&full[i % slots], (i / slots) & 1, p.status))
                         break;
             __syncwarp();
         }
