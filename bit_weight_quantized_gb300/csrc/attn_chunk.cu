@@ -415,97 +415,121 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
             float mref = -INFINITY, l = 0.f;
             const uint64_t scale2 = pair(__float_as_uint(p.scale_log2), __float_as_uint(p.scale_log2));
             const int j0 = two ? s : 0, step = two ? 2 : 1;
-            for (int j = j0; j < units && ok; j += step) {
-#pragma unroll 1
-                for (int h = 0; h < 2; ++h) {
-                    const int b = 2 * s + h;
-                    if (!(ok = __all_sync(0xffffffffu, mbar_wait(&s_full[b], ph, p.status))))
-                        break;
-                    tc_fence_after();
-                    uint32_t v[kHalf];
+            // keys that every row of the warp sees: halves inside need no mask
+            int all_lo = see.x, all_hi = trow < r.rows ? see.y : 0x7fffffff;
 #pragma unroll
-                    for (int c = 0; c < kHalf; c += 32)
-                        tmem_ld32_start(ts + 64 * h + c, v + c);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int c = 0; c < kHalf; c += 32)
-                        pin32(v + c);
-                    const int kb = kb0 + j * kChunkKeys + h * kHalf;
+            for (int d = 16; d > 0; d >>= 1) {
+                all_lo = max(all_lo, __shfl_xor_sync(0xffffffffu, all_lo, d));
+                all_hi = min(all_hi, __shfl_xor_sync(0xffffffffu, all_hi, d));
+            }
+            uint32_t v[kHalf];       // a half's scores; the next half's are on their way in early
+            auto scores = [&](int h, uint32_t parity) {
+                if (ok)
+                    ok = __all_sync(0xffffffffu, mbar_wait(&s_full[2 * s + h], parity, p.status));
+                tc_fence_after();
+            };
+            auto fetch = [&](int h, int c) { tmem_ld32_start(ts + 64 * h + 32 * c, v + 32 * c); };
+            // One half of key tile j.  The first half's loop brings in the second half's
+            // scores as its own are used up, the second half's the next tile's first half
+            // where that has a buffer of its own (kSplit).
+            auto half = [&](int j, int h) {
+                const int b = 2 * s + h;
+                const bool more = j + step < units;
+                const bool ahead = h == 0 || (kSplit && more);
+                tmem_ld_wait();
+                pin32(v);
+                pin32(v + 32);
+                const int kb = kb0 + j * kChunkKeys + h * kHalf;
+                if (kb < all_lo || kb + kHalf - 1 > all_hi) {
                     const int c_lo = see.x - kb, c_hi = see.y - kb;     // the columns this row sees
-                    if (__any_sync(0xffffffffu, c_lo > 0 || c_hi < kHalf - 1)) {
 #pragma unroll
-                        for (int c = 0; c < kHalf; ++c)
-                            if (c < c_lo || c > c_hi)
-                                v[c] = 0xff800000u;                     // -infinity
-                    }
-                    float mx[4];
+                    for (int c = 0; c < kHalf; ++c)
+                        if (c < c_lo || c > c_hi)
+                            v[c] = 0xff800000u;                         // -infinity
+                }
+                float mx[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    mx[e] = __uint_as_float(v[e]);
+#pragma unroll
+                for (int c = 4; c + 8 <= kHalf; c += 8)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        mx[e] = __uint_as_float(v[e]);
+                        mx[e] = max3(mx[e], __uint_as_float(v[c + 2 * e]), __uint_as_float(v[c + 2 * e + 1]));
+                mx[0] = max3(mx[0], __uint_as_float(v[kHalf - 4]), __uint_as_float(v[kHalf - 3]));
+                mx[1] = max3(mx[1], __uint_as_float(v[kHalf - 2]), __uint_as_float(v[kHalf - 1]));
+                const float m = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * p.scale_log2;
+                const bool up = m > mref + kChunkGrow;
+                if (__any_sync(0xffffffffu, up)) {
+                    const float a = up ? ex2(mref - m) : 1.f;
+                    mref = up ? m : mref;
+                    l *= a;
+                    if (j > j0 || h) {
+                        // the product before this one is complete when its half says so
+                        if (ok)
+                            ok = __all_sync(0xffffffffu, mbar_wait(&o_full[b ^ 1], h ? ph : ph ^ 1u, p.status));
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 32) {
+                            uint32_t o[32];
+                            tmem_ld32_start(to + c, o);
+                            tmem_ld_wait();
+                            pin32(o);
 #pragma unroll
-                    for (int c = 4; c + 8 <= kHalf; c += 8)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            mx[e] = max3(mx[e], __uint_as_float(v[c + 2 * e]), __uint_as_float(v[c + 2 * e + 1]));
-                    mx[0] = max3(mx[0], __uint_as_float(v[kHalf - 4]), __uint_as_float(v[kHalf - 3]));
-                    mx[1] = max3(mx[1], __uint_as_float(v[kHalf - 2]), __uint_as_float(v[kHalf - 1]));
-                    const float m = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * p.scale_log2;
-                    const bool up = m > mref + kChunkGrow;
-                    if (__any_sync(0xffffffffu, up)) {
-                        const float a = up ? ex2(mref - m) : 1.f;
-                        mref = up ? m : mref;
-                        l *= a;
-                        if (j > j0 || h) {
-                            // the product before this one is complete when its half says so
-                            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&o_full[b ^ 1], h ? ph : ph ^ 1u, p.status))))
-                                break;
-                            tc_fence_after();
-#pragma unroll
-                            for (int c = 0; c < D; c += 32) {
-                                uint32_t o[32];
-                                tmem_ld32_start(to + c, o);
-                                tmem_ld_wait();
-                                pin32(o);
-#pragma unroll
-                                for (int e = 0; e < 32; e += 2) {
-                                    float x, y;
-                                    unpair(mul2_f32(pair(o[e], o[e + 1]), pair(__float_as_uint(a), __float_as_uint(a))), x, y);
-                                    o[e] = __float_as_uint(x);
-                                    o[e + 1] = __float_as_uint(y);
-                                }
-                                tmem_st32(to + c, o);
-                            }
+                            for (int e = 0; e < 32; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+                            tmem_st32(to + c, o);
                         }
                     }
-                    const float neg = kShift - (mref == -INFINITY ? 0.f : mref);
-                    const uint64_t neg2 = pair(__float_as_uint(neg), __float_as_uint(neg));
-                    // weights, rounded to 16 bits for the second product
-                    uint64_t sum[2] = {0, 0};
-#pragma unroll
-                    for (int c = 0; c < kHalf / 32; ++c) {
-                        uint32_t w[16];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            float p0, p1;
-                            unpair(fma2(pair(v[32 * c + 2 * e], v[32 * c + 2 * e + 1]), scale2, neg2), p0, p1);
-                            p0 = ex2(p0);
-                            p1 = ex2(p1);
-                            sum[e & 1] = add2(sum[e & 1], pair(__float_as_uint(p0), __float_as_uint(p1)));
-                            w[e] = pack16<BF16>(p0, p1);
-                        }
-                        tmem_st16(ts + 64 * h + 16 * c, w);
-                    }
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(&p_full[b]);
-                    float s0, s1;
-                    unpair(add2(sum[0], sum[1]), s0, s1);
-                    l += s0 + s1;
                 }
+                const float neg = kShift - (mref == -INFINITY ? 0.f : mref);
+                const uint64_t neg2 = pair(__float_as_uint(neg), __float_as_uint(neg));
+                // weights, rounded to 16 bits for the second product
+                uint64_t sum[2] = {0, 0};
+#pragma unroll
+                for (int c = 0; c < kHalf / 32; ++c) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        float p0, p1;
+                        unpair(fma2(pair(v[32 * c + 2 * e], v[32 * c + 2 * e + 1]), scale2, neg2), p0, p1);
+                        p0 = ex2(p0);
+                        p1 = ex2(p1);
+                        sum[e & 1] = add2(sum[e & 1], pair(__float_as_uint(p0), __float_as_uint(p1)));
+                        w[e] = pack16<BF16>(p0, p1);
+                    }
+                    tmem_st16(ts + 64 * h + 16 * c, w);
+                    if (ahead) {
+                        if (c == 0)
+                            scores(h ^ 1, h ? ph ^ 1u : ph);
+                        fetch(h ^ 1, c);
+                    }
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&p_full[b]);
+                float s0, s1;
+                unpair(add2(sum[0], sum[1]), s0, s1);
+                l += s0 + s1;
+                if (!ahead && more) {
+                    scores(0, ph ^ 1u);
+                    fetch(0, 0);
+                    fetch(0, 1);
+                }
+            };
+            scores(0, ph);
+            fetch(0, 0);
+            fetch(0, 1);
+            for (int j = j0; j < units && ok; j += step) {
+                half(j, 0);
+                if (!ok)
+                    break;
+                half(j, 1);
                 ph ^= 1u;
             }
+            tmem_ld_wait();          // (after a timeout some may be under way)
             // the last product into O
             if (ok)
                 ok = __all_sync(0xffffffffu, mbar_wait(&o_full[2 * s + 1], ph ^ 1u, p.status));
