@@ -6,31 +6,33 @@
 // A work item is 256 rows ((token, query head) pairs of one key head, so that a
 // key tile loaded once serves all query heads that share it) as two streams of 128
 // rows; the keys go by in tiles of 128.  Both products run on tcgen05 with their
-// accumulators in tensor memory: per stream two buffers of S (128 x 64 fp32, the
-// halves of a key tile) and O (128 x D), all 512 columns at D = 128.  P takes S's
-// place as 16-bit values and is the second
+// accumulators in tensor memory: per stream S (128 x 128 fp32) and O (128 x D), all
+// 512 columns at D = 128.  P takes S's place as 16-bit values and is the second
 // product's left operand straight from tensor memory; V is its right operand as it
 // lies in the cache ([key][d], the "MN-major" form), so nothing is transposed.  An
-// item of at most 128 rows gives both streams the same rows and every other tile,
-// so that one stream's products still run under the other's softmax; stream 0 adds
-// up the two at the end, straight from tensor memory.
+// item of at most 128 rows gives both streams the same rows and every other tile;
+// stream 0 adds up the two at the end, straight from tensor memory.
 //
 // Roles.  Warps 0-3 and 4-7 are the softmax of streams 0 and 1, one thread per row:
-// no exchange between lanes at all.  Warps 8 and 9 issue the
-// streams' products.  Warps 10 and 11 bring K and V tiles into a ring
-// each: where the page size is a multiple of 8 by
-// tensor copies, one per page or part of a page that lies in the tile, all issued by
-// one warp (the other one clears the V rows that nobody sees: past kv_len, before the
-// window, where 0 x NaN would spoil the product); else by 16-byte asynchronous copies
-// that fill such rows with zeros.  Plain copies alone kept the loading warps busy
-// for 6000 cycles a tile pair, three times the products' time.
+// no exchange between lanes.  Warp 8 issues the products, one stream after the
+// other, so that one's products run under the other's softmax.  (A warp for each
+// stream let the two fall into step, with both softmaxes and then both products at
+// once: 240 instead of 190 us for 4096 x 4096 x 32 heads of 128.)  Warps 10 and 11
+// bring K and V tiles into a ring each: where the page size is a multiple of 8 by
+// tensor copies, one per page or part of a page that lies in the tile; else by
+// 16-byte asynchronous copies, which take any page size.  V rows that nobody sees
+// (past kv_len, before the window) are made zero, since 0 x NaN would spoil the
+// product.  Plain copies kept the loading warps busy for 6000 cycles a tile pair,
+// three times the products' time.
 //
 // The running maximum is replaced only when it grows by more than 2^8: the output
 // accumulator in tensor memory is then read, scaled and written back by its
-// stream's own threads, a few times per item, once the last product into it is done.
+// stream's own threads, a few times per item.  S's arrival says that the product
+// before it into O is complete, so that needs no signal of its own.
 //
-// Bound by the tensor cores for long prompts: 4 D flops per (row, key) pair against
-// one exponential; at one row tile by the key tiles' traffic.
+// Bound by the tensor cores at D = 128 (4096 x 4096 x 32 heads: 1480 TFLOP/s, 79% of
+// the measured bf16 rate; products and signals alone, the softmax left out, 1687), by
+// the softmax at D = 64 (844 and 1261).
 #include "gemm.cuh"
 #include "paged.cuh"
 
@@ -39,12 +41,15 @@ namespace qmm {
 namespace {
 
 constexpr int kSoftWarps = 4;                       // per stream
-constexpr int kIssueWarp = 2 * kSoftWarps;          // one per stream
-constexpr int kLoadWarp0 = kIssueWarp + 2;
-constexpr int kLoadWarps = 2;
-constexpr int kChunkThreads = 32 * (kLoadWarp0 + kLoadWarps);
+constexpr int kIssueWarp = 2 * kSoftWarps;
+constexpr int kLoadWarpK = kIssueWarp + 2, kLoadWarpV = kIssueWarp + 3;   // (warp 9 has no part)
+constexpr int kChunkThreads = 384;
 constexpr float kChunkGrow = 8.f;
-constexpr int kHalf = kChunkKeys / 2;               // keys per score buffer
+constexpr int kHalf = kChunkKeys / 2;               // the weights are handed over by halves of a tile
+// Registers per thread after the split: 256 x 200 + 128 x 104 = 384 x 168, what the
+// launch gives.
+constexpr int kSoftRegs = 200, kOtherRegs = 104;
+static_assert(256 * kSoftRegs + 128 * kOtherRegs == kChunkThreads * 168, "register split");
 
 using ChunkWalk = Walk<kChunkRows, kChunkKeys, kChunkSetup>;
 
@@ -56,9 +61,9 @@ struct ChunkLayout {
     static constexpr int kOffK = 2 * kTile;
     static constexpr int kOffV = kOffK + kKRing * kTile;
     static constexpr int kOffBar = kOffV + kVRing * kTile;
-    // full / empty of both rings, patch, q_full[2], then per stream and half s_full, p_full
-    // and o_full, x_full, x_done, drain[2], begun, taken
-    static constexpr int kNumBars = 2 * (kKRing + kVRing) + 21;
+    // full / empty of both rings, patch, per stream q_full, s_full, p_full (two halves) and
+    // o_full, x_full, x_done, drain
+    static constexpr int kNumBars = 2 * (kKRing + kVRing) + 14;
     static constexpr int kOffTmem = kOffBar + 8 * kNumBars;
     static constexpr int kOffShare = kOffTmem + 16;
     static constexpr int kOffRed = kOffShare + sizeof(Share);
@@ -70,8 +75,9 @@ struct ChunkLayout {
     static_assert(kBytes <= 227 * 1024, "shared memory per block");
 };
 
-// Tensor-memory columns of stream s: the score buffers of half h, and O.
-__device__ __forceinline__ uint32_t s_col(int s, int h = 0) { return static_cast<uint32_t>(s) * 128u + static_cast<uint32_t>(h) * 64u; }
+// Tensor-memory columns of stream s: S (and P, half h of it), and O.
+__device__ __forceinline__ uint32_t s_col(int s) { return static_cast<uint32_t>(s) * 128u; }
+__device__ __forceinline__ uint32_t p_col(int s, int h) { return s_col(s) + static_cast<uint32_t>(h) * 32u; }
 __device__ __forceinline__ uint32_t o_col(int s) { return 256u + static_cast<uint32_t>(s) * 128u; }
 
 // Byte of 16-byte chunk c of row r in a query tile: halves of 64 values, rows of 128
@@ -234,13 +240,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
     return d;
 }
 
-__device__ __forceinline__ uint64_t mul2_f32(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
     float d;
@@ -281,12 +280,6 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
     constexpr int kChunks = D / 8;                     // 16-byte chunks per row
     constexpr int kRowsPerCopy = 32 / kChunks;
     constexpr float kShift = BF16 ? 0.f : 7.f;
-    // Scores by half tiles: a half's buffer is filled again right behind the product
-    // that reads its weights, under the other half's softmax.  At D = 128 a product of
-    // 64 keys is bound by reading both operands from shared memory (6 KB in 32 cycles'
-    // work), so there the two buffers are filled at once.
-    constexpr bool kSplit = D == 64;
-
     // the operand tiles' swizzle needs 1024-byte alignment, which the start of a
     // block's shared memory has (there is no static part); checked below
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -294,8 +287,8 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
     long long *red = reinterpret_cast<long long *>(smem + L::kOffRed);
     uint64_t *k_full = reinterpret_cast<uint64_t *>(smem + L::kOffBar), *k_empty = k_full + L::kKRing;
     uint64_t *v_full = k_empty + L::kKRing, *v_empty = v_full + L::kVRing, *patch = v_empty + L::kVRing;
-    uint64_t *q_full = patch + 1, *s_full = q_full + 2, *p_full = s_full + 4, *o_full = p_full + 4;
-    uint64_t *x_full = o_full + 4, *x_done = x_full + 1, *drain = x_done + 1, *begun = drain + 2, *taken = begun + 1;
+    uint64_t *q_full = patch + 1, *s_full = q_full + 2, *p_full = s_full + 2, *o_full = p_full + 4;
+    uint64_t *x_full = o_full + 2, *x_done = x_full + 1, *drain = x_done + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kOffTmem);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -307,27 +300,23 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
     if (threadIdx.x == 0) {
         for (int i = 0; i < L::kKRing; ++i) {
             mbar_init(&k_full[i], 1);
-            mbar_init(&k_empty[i], 2);
+            mbar_init(&k_empty[i], 1);
         }
         for (int i = 0; i < L::kVRing; ++i) {
             mbar_init(&v_full[i], 1);
-            mbar_init(&v_empty[i], 2);
+            mbar_init(&v_empty[i], 1);
         }
         mbar_init(patch, 1);
         for (int s = 0; s < 2; ++s) {
             mbar_init(&q_full[s], kSoftWarps);
-            for (int i = 2 * s; i < 2 * s + 2; ++i) {
-                mbar_init(&s_full[i], 1);
-                mbar_init(&p_full[i], kSoftWarps);
-                mbar_init(&o_full[i], 1);
-            }
+            mbar_init(&s_full[s], 1);
+            mbar_init(&p_full[2 * s], kSoftWarps);
+            mbar_init(&p_full[2 * s + 1], kSoftWarps);
+            mbar_init(&o_full[s], 1);
         }
         mbar_init(x_full, kSoftWarps);
         mbar_init(x_done, kSoftWarps);
-        mbar_init(&drain[0], 1);
-        mbar_init(&drain[1], 1);
-        mbar_init(begun, 1);
-        mbar_init(taken, 1);
+        mbar_init(drain, 1);
         fence_barrier_init();
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     }
@@ -361,11 +350,13 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
 
     if (warp < kIssueWarp) {
         // ================= softmax of stream s: one row per thread =================
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
         const int s = warp / kSoftWarps, quarter = warp % kSoftWarps;
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         const uint32_t ts = tmem + lanes + s_col(s), to = tmem + lanes + o_col(s);
         uint8_t *qs = smem + L::kOffQ + s * L::kTile;
-        uint32_t ph = 0;         // parity of the next tile's barriers
+        uint32_t ph = 0;         // parity of the next S
+        uint32_t oph = 0;        // parity of the next O
         uint32_t xph = 0;        // parity of the next exchange between the streams
         // the next segment this stream has a part in: rows of its own, or every other
         // tile of an item of one stream's rows
@@ -422,28 +413,24 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                 all_lo = max(all_lo, __shfl_xor_sync(0xffffffffu, all_lo, d));
                 all_hi = min(all_hi, __shfl_xor_sync(0xffffffffu, all_hi, d));
             }
-            uint32_t v[kHalf];       // a half's scores; the next half's are on their way in early
-            auto scores = [&](int h, uint32_t parity) {
-                if (ok)
-                    ok = __all_sync(0xffffffffu, mbar_wait(&s_full[2 * s + h], parity, p.status));
+            for (int j = j0; j < units; j += step) {
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait(&s_full[s], ph, p.status))))
+                    break;
+                ph ^= 1u;
                 tc_fence_after();
-            };
-            auto fetch = [&](int h, int c) { tmem_ld32_start(ts + 64 * h + 32 * c, v + 32 * c); };
-            // One half of key tile j.  The first half's loop brings in the second half's
-            // scores as its own are used up, the second half's the next tile's first half
-            // where that has a buffer of its own (kSplit).
-            auto half = [&](int j, int h) {
-                const int b = 2 * s + h;
-                const bool more = j + step < units;
-                const bool ahead = h == 0 || (kSplit && more);
+                uint32_t v[kChunkKeys];
+#pragma unroll
+                for (int c = 0; c < kChunkKeys; c += 32)
+                    tmem_ld32_start(ts + c, v + c);
                 tmem_ld_wait();
-                pin32(v);
-                pin32(v + 32);
-                const int kb = kb0 + j * kChunkKeys + h * kHalf;
-                if (kb < all_lo || kb + kHalf - 1 > all_hi) {
+#pragma unroll
+                for (int c = 0; c < kChunkKeys; c += 32)
+                    pin32(v + c);
+                const int kb = kb0 + j * kChunkKeys;
+                if (kb < all_lo || kb + kChunkKeys - 1 > all_hi) {
                     const int c_lo = see.x - kb, c_hi = see.y - kb;     // the columns this row sees
 #pragma unroll
-                    for (int c = 0; c < kHalf; ++c)
+                    for (int c = 0; c < kChunkKeys; ++c)
                         if (c < c_lo || c > c_hi)
                             v[c] = 0xff800000u;                         // -infinity
                 }
@@ -452,23 +439,19 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                 for (int e = 0; e < 4; ++e)
                     mx[e] = __uint_as_float(v[e]);
 #pragma unroll
-                for (int c = 4; c + 8 <= kHalf; c += 8)
+                for (int c = 4; c + 8 <= kChunkKeys; c += 8)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         mx[e] = max3(mx[e], __uint_as_float(v[c + 2 * e]), __uint_as_float(v[c + 2 * e + 1]));
-                mx[0] = max3(mx[0], __uint_as_float(v[kHalf - 4]), __uint_as_float(v[kHalf - 3]));
-                mx[1] = max3(mx[1], __uint_as_float(v[kHalf - 2]), __uint_as_float(v[kHalf - 1]));
+                mx[0] = max3(mx[0], __uint_as_float(v[kChunkKeys - 4]), __uint_as_float(v[kChunkKeys - 3]));
+                mx[1] = max3(mx[1], __uint_as_float(v[kChunkKeys - 2]), __uint_as_float(v[kChunkKeys - 1]));
                 const float m = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * p.scale_log2;
                 const bool up = m > mref + kChunkGrow;
                 if (__any_sync(0xffffffffu, up)) {
                     const float a = up ? ex2(mref - m) : 1.f;
                     mref = up ? m : mref;
                     l *= a;
-                    if (j > j0 || h) {
-                        // the product before this one is complete when its half says so
-                        if (ok)
-                            ok = __all_sync(0xffffffffu, mbar_wait(&o_full[b ^ 1], h ? ph : ph ^ 1u, p.status));
-                        tc_fence_after();
+                    if (j > j0) {
 #pragma unroll 1
                         for (int c = 0; c < D; c += 32) {
                             uint32_t o[32];
@@ -484,10 +467,11 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                 }
                 const float neg = kShift - (mref == -INFINITY ? 0.f : mref);
                 const uint64_t neg2 = pair(__float_as_uint(neg), __float_as_uint(neg));
-                // weights, rounded to 16 bits for the second product
+                // weights, rounded to 16 bits for the second product; the first half of them
+                // is handed over while the second is computed
                 uint64_t sum[2] = {0, 0};
 #pragma unroll
-                for (int c = 0; c < kHalf / 32; ++c) {
+                for (int c = 0; c < kChunkKeys / 32; ++c) {
                     uint32_t w[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
@@ -498,41 +482,22 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                         sum[e & 1] = add2(sum[e & 1], pair(__float_as_uint(p0), __float_as_uint(p1)));
                         w[e] = pack16<BF16>(p0, p1);
                     }
-                    tmem_st16(ts + 64 * h + 16 * c, w);
-                    if (ahead) {
-                        if (c == 0)
-                            scores(h ^ 1, h ? ph ^ 1u : ph);
-                        fetch(h ^ 1, c);
+                    tmem_st16(ts + 16 * c, w);
+                    if (c & 1) {
+                        tmem_st_wait();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(&p_full[2 * s + (c >> 1)]);
                     }
                 }
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&p_full[b]);
                 float s0, s1;
                 unpair(add2(sum[0], sum[1]), s0, s1);
                 l += s0 + s1;
-                if (!ahead && more) {
-                    scores(0, ph ^ 1u);
-                    fetch(0, 0);
-                    fetch(0, 1);
-                }
-            };
-            scores(0, ph);
-            fetch(0, 0);
-            fetch(0, 1);
-            for (int j = j0; j < units && ok; j += step) {
-                half(j, 0);
-                if (!ok)
-                    break;
-                half(j, 1);
-                ph ^= 1u;
             }
-            tmem_ld_wait();          // (after a timeout some may be under way)
-            // the last product into O
             if (ok)
-                ok = __all_sync(0xffffffffu, mbar_wait(&o_full[2 * s + 1], ph ^ 1u, p.status));
+                ok = __all_sync(0xffffffffu, mbar_wait(&o_full[s], oph, p.status));
+            oph ^= 1u;
             if (!ok)
                 break;
             tc_fence_after();
@@ -643,29 +608,21 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                 load_q(segs[cur]);
         }
     } else {
-        if (warp < kLoadWarp0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp == kIssueWarp) {
             // ================= product issue =================
-            // Warp 8 issues stream 0's products and, for items that both streams share,
-            // stream 1's too; warp 9 issues stream 1's where it has rows of its own, after
-            // warp 8 has said that such an item begins.  (A warp that skipped tiles on its
-            // own could meet a ring barrier a phase early or late.)
             // The whole warp runs this, one elected lane issues: with warp-uniform
-            // control flow the operand descriptors stay in uniform registers.  (A
-            // single lane's loop spent 70 to 170 cycles a product on moving them there;
-            // one warp for both streams, at 50 cycles a product and 110 a wait, still
-            // bound the kernel.)  A timed-out wait only skips the later waits: the loops
+            // control flow the operand descriptors stay in uniform registers.  (A single
+            // lane's loop spent 70 to 170 cycles a product on moving them there; a
+            // product takes 64.)  A timed-out wait only skips the later waits: the loops
             // run on, over data that nobody uses.
-            const int me = warp - kIssueWarp;
-            const uint32_t id_qk = f16_idesc(BF16, 128, kSplit ? kHalf : kChunkKeys);
+            const uint32_t id_qk = f16_idesc(BF16, 128, kChunkKeys);
             const uint32_t id_pv = f16_idesc(BF16, 128, D) | (1u << 16);   // B is MN-major
             const uint64_t q_desc = swizzled_desc(smem_u32(smem + L::kOffQ), 16, 1024);
             const uint64_t k_desc = swizzled_desc(smem_u32(smem + L::kOffK), 16, D * 16);
             const uint64_t v_desc = swizzled_desc(smem_u32(smem + L::kOffV), 1024, D * 16);
             unsigned tile0 = 0;          // key tiles of the segments before
-            uint32_t qph = 0;            // parity of this warp's q_full
-            uint32_t gph = 0;            // parity of `begun` (warp 9) or `taken` (warp 8)
-            bool any = false;            // warp 8: some item began before
-            uint32_t pph = 0;            // parities of p_full, bit per stream
+            uint32_t qph = 0, pph = 0;   // parities of q_full and p_full, bit per stream
             auto wait = [&](uint64_t *bar, uint32_t parity) {
                 if (ok)
                     ok = mbar_wait(bar, parity, p.status);
@@ -682,136 +639,110 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                 wait(&v_full[slot], at / L::kVRing & 1u);
                 return static_cast<int>(slot);
             };
-            // `arrivals` on a slot's barrier (it takes two: one from each warp, or both from the
-            // only one that reads the tile), when the products so far are done
-            auto release = [&](uint64_t *bar, int arrivals) {
-                tc_commit(bar);
-                if (arrivals == 2)
-                    tc_commit(bar);
-            };
-            // S of stream s, half h of the keys (or all of them), from query tile qt and the K
-            // tile in slot ks
-            auto qk = [&](int s, int qt, int ks, int h, int arrivals) {
+            // S of stream s from query tile qt and the K tile in slot ks, whose last reader
+            // frees it
+            auto qk = [&](int s, int qt, int ks, bool last) {
                 const uint64_t a = q_desc + static_cast<uint32_t>((qt * L::kTile) >> 4);
-                const uint64_t b = k_desc + static_cast<uint32_t>((ks * L::kTile + (kSplit ? h * (L::kTile / 2) : 0)) >> 4);
+                const uint64_t b = k_desc + static_cast<uint32_t>((ks * L::kTile) >> 4);
                 if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        tc_mma(tmem + s_col(s, kSplit ? h : 0), a + (kk >> 2) * (128 * 128 / 16) + (kk & 3) * 2,
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        tc_mma(tmem + s_col(s), a + (kk >> 2) * (128 * 128 / 16) + (kk & 3) * 2,
                                b + (kk >> 2) * (1024 / 16) + (kk & 3) * 2, id_qk, kk > 0 ? 1u : 0u);
-                    }
-                    if (kSplit) {
-                        tc_commit(&s_full[2 * s + h]);
-                    } else {
-                        tc_commit(&s_full[2 * s]);
-                        tc_commit(&s_full[2 * s + 1]);
-                    }
-                    if (h == 1)
-                        release(&k_empty[ks], arrivals);
+                    tc_commit(&s_full[s]);
+                    if (last)
+                        tc_commit(&k_empty[ks]);
                 }
                 __syncwarp();
             };
-            // O of stream s (+)= P V over half h of the keys, V in slot vs, as soon as the weights are there
-            auto pv = [&](int s, int vs, int h, bool first, int arrivals) {
-                wait(&p_full[2 * s + h], pph >> s & 1u);
-                const uint64_t b = v_desc + static_cast<uint32_t>((vs * L::kTile + h * (L::kTile / 2)) >> 4);
-                if (elect_one()) {
+            // O of stream s (+)= P V, V in slot vs, half by half as the weights come
+            auto pv = [&](int s, int vs, bool first, bool last) {
 #pragma unroll
-                    for (int e = 0; e < kHalf / 16; ++e)
-                        tc_mma_ts(tmem + o_col(s), tmem + s_col(s, h) + 8 * e, b + e * (2 * D * 16 / 16), id_pv,
-                                  e > 0 || !first ? 1u : 0u);
-                    tc_commit(&o_full[2 * s + h]);
-                    if (h == 1)
-                        release(&v_empty[vs], arrivals);
+                for (int h = 0; h < 2; ++h) {
+                    wait(&p_full[2 * s + h], pph >> s & 1u);
+                    const uint64_t b = v_desc + static_cast<uint32_t>((vs * L::kTile + h * (L::kTile / 2)) >> 4);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int e = 0; e < kHalf / 16; ++e)
+                            tc_mma_ts(tmem + o_col(s), tmem + p_col(s, h) + 8 * e, b + e * (2 * D * 16 / 16), id_pv,
+                                      h > 0 || e > 0 || !first ? 1u : 0u);
+                        if (h == 1 && last)
+                            tc_commit(&v_empty[vs]);
+                    }
                 }
                 __syncwarp();
+                pph ^= 1u << s;
+            };
+            auto finish = [&](int s) {   // stream s's last product of the segment
+                if (elect_one())
+                    tc_commit(&o_full[s]);
+                __syncwarp();
+            };
+            auto q_landed = [&](int s) {
+                wait(&q_full[s], qph >> s & 1u);
+                qph ^= 1u << s;
             };
             while (next(segs[0])) {
                 const int ns = __shfl_sync(0xffffffffu, segs[0].r.rows > 128 ? 2 : 1, 0);
                 const int units = __shfl_sync(0xffffffffu, segs[0].units, 0);
-                const bool two = ns == 1 && units > 1;   // both streams, tile by tile in turn
-                if (ns == 2) {
-                    if (me == 1) {
-                        wait(begun, gph);
-                        gph ^= 1u;
-                        if (lane == 0)
-                            mbar_arrive(taken);
+                // (the streams' loops are unrolled: with constant streams a product issues
+                // in 50 cycles, with variable ones in 60, and this warp is on every tile's
+                // path)
+                if (ns == 1) {
+                    // one stream's rows: even tiles on stream 0, odd ones on stream 1
+                    q_landed(0);
+                    qk(0, 0, k_landed(0), true);
+                    if (units > 1)
+                        qk(1, 0, k_landed(1), true);
+                    for (int j0 = 0; j0 < units; j0 += 2) {
+#pragma unroll
+                        for (int s = 0; s < 2; ++s) {
+                            const int j = j0 + s;
+                            if (j < units) {
+                                pv(s, v_landed(j), j0 == 0, true);
+                                if (j + 2 < units)
+                                    qk(s, 0, k_landed(j + 2), true);
+                                else
+                                    finish(s);
+                            }
+                        }
                     }
-                    wait(&q_full[me], qph);
-                    qph ^= 1u;
-                    if (me == 0) {
-                        if (any)
-                            wait(taken, gph);   // of the last such item: one signal at a time
-                        gph ^= any ? 1u : 0u;
-                        any = true;
-                        if (lane == 0)
-                            mbar_arrive(begun);
-                    }
+                } else {
                     int ks = k_landed(0);
-                    if (kSplit)
-                        qk(me, me, ks, 0, 1);
-                    qk(me, me, ks, 1, 1);
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        q_landed(s);
+                        qk(s, s, ks, s == 1);
+                    }
                     for (int j = 0; j < units; ++j) {
                         const int vs = v_landed(j);
                         const bool more = j + 1 < units;
-                        pv(me, vs, 0, j == 0, 1);
-                        if (kSplit && more) {
-                            ks = k_landed(j + 1);
-                            qk(me, me, ks, 0, 1);
+#pragma unroll
+                        for (int s = 0; s < 2; ++s) {
+                            pv(s, vs, j == 0, s == 1);
+                            if (more) {
+                                if (s == 0)
+                                    ks = k_landed(j + 1);
+                                qk(s, s, ks, s == 1);
+                            } else {
+                                finish(s);
+                            }
                         }
-                        pv(me, vs, 1, false, 1);
-                        if (more) {
-                            if (!kSplit)
-                                ks = k_landed(j + 1);
-                            qk(me, me, ks, 1, 1);
-                        }
-                        pph ^= 3u;
                     }
-                } else if (me == 0) {
-                    // one stream's rows: tile by tile in turn on both; a single tile on stream 0
-                    const int step = two ? 2 : 1;
-                    wait(&q_full[0], qph);
-                    qph ^= 1u;
-                    for (int s = 0; s < step; ++s) {
-                        const int ks = k_landed(s);
-                        if (kSplit)
-                            qk(s, 0, ks, 0, 2);
-                        qk(s, 0, ks, 1, 2);
-                    }
-                    for (int j = 0; j < units; ++j) {
-                        const int s = two ? j & 1 : 0, vs = v_landed(j);
-                        const bool more = j + step < units;
-                        int ks = 0;
-                        pv(s, vs, 0, j < step, 2);
-                        if (kSplit && more) {
-                            ks = k_landed(j + 2);
-                            qk(s, 0, ks, 0, 2);
-                        }
-                        pv(s, vs, 1, false, 2);
-                        if (more) {
-                            if (!kSplit)
-                                ks = k_landed(j + 2);
-                            qk(s, 0, ks, 1, 2);
-                        }
-                        pph ^= 1u << s;
-                    }
-                } else if (two && (units >> 1 & 1)) {
-                    pph ^= 2u;           // stream 1's tiles, issued by warp 8
                 }
                 tile0 += static_cast<unsigned>(units);
             }
             // after a timeout nobody has waited for the products: wait here
             if (!__all_sync(0xffffffffu, ok)) {
                 if (elect_one())
-                    tc_commit(&drain[me]);
+                    tc_commit(drain);
                 __syncwarp();
-                mbar_wait(&drain[me], 0, p.status);
+                mbar_wait(drain, 0, p.status);
             }
             __syncwarp();
-        } else {
+        } else if (warp >= kLoadWarpK) {
             // ================= K tiles (warp 10) and V tiles (warp 11) =================
-            constexpr int kCopies = kChunkKeys / kRowsPerCopy;      // warp-wide plain copies per tile
-            const bool is_v = warp != kLoadWarp0;
+            const bool is_v = warp == kLoadWarpV;
             const int slots = is_v ? L::kVRing : L::kKRing;
             uint64_t *full = is_v ? v_full : k_full, *empty = is_v ? v_empty : k_empty;
             uint8_t *ring = smem + (is_v ? L::kOffV : L::kOffK);
@@ -889,18 +820,17 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                             unsaid = -1;
                         }
                     } else {
-                        // plain copies; the lane looks up the places of kChunkKeys / 32 of the keys
-                        long long place[kChunkKeys / 32];
-#pragma unroll
-                        for (int e = 0; e < kChunkKeys / 32; ++e) {
-                            const int key = kb + 32 * e + lane;
-                            place[e] = key >= r.lo && key < r.hi ? key_offset(p.kv, r.b, key, p.status) : -1;
-                        }
-#pragma unroll
-                        for (int c = 0; c < kCopies; ++c) {
-                            const int q = c * kRowsPerCopy + sub;
-                            const long long o = __shfl_sync(0xffffffffu, place[c * kRowsPerCopy / 32], q & 31);
-                            cp_async16_or_zero(smem_u32(tile + kv_addr<D>(q, chunk)), base + (o >= 0 ? o : 0) + chunk * 8, o >= 0);
+                        // plain copies, 32 keys at a time: the lane looks up the place of one
+#pragma unroll 1
+                        for (int e = 0; e < kChunkKeys; e += 32) {
+                            const int key = kb + e + lane;
+                            const long long place = key >= r.lo && key < r.hi ? key_offset(p.kv, r.b, key, p.status) : -1;
+#pragma unroll 4
+                            for (int c = 0; c < 32; c += kRowsPerCopy) {
+                                const long long o = __shfl_sync(0xffffffffu, place, c + sub);
+                                cp_async16_or_zero(smem_u32(tile + kv_addr<D>(e + c + sub, chunk)),
+                                                   base + (o >= 0 ? o : 0) + chunk * 8, o >= 0);
+                            }
                         }
                         cp_async_commit();
                         // the tile before this one has landed
