@@ -337,7 +337,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
     ChunkWalk &walk = reinterpret_cast<ChunkWalk *>(smem + L::kOffWalk)[warp];
     Segment *segs = reinterpret_cast<Segment *>(smem + L::kOffSeg) + warp + min(warp, kIssueWarp);
     if (lane == 0)
-        walk.begin(p, share);
+        walk.begin(share);
     auto next = [&](Segment &s) -> bool {
         __syncwarp();
         bool more = false;
@@ -602,7 +602,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                     make_float2(mref, l);
             }
             if (threadIdx.x == 0 && is_last_part(sg))
-                write_meta(p, sg);
+                write_meta<kChunkSetup>(p, sg, share.chunk);
             cur ^= 1;
             if (have)
                 load_q(segs[cur]);

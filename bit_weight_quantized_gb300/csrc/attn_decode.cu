@@ -112,7 +112,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
         p.meta[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
 
     Walk<kDecodeRows, kDecodeKeys, kDecodeSetup> walk;
-    walk.begin(p, share);
+    walk.begin(share);
     Segment sg;
     while (walk.next(p, sg)) {
         const RowTile &r = sg.r;
@@ -312,7 +312,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
             }
         }
         if (tid == 0 && is_last_part(sg))
-            write_meta(p, sg);
+            write_meta<kDecodeSetup>(p, sg, share.chunk);
         __syncthreads();   // the rings and the query tile are free again
     }
 }

@@ -157,7 +157,15 @@ struct Share {
     long long chunk;
     long long start;         // where the item (i, h) that holds `at` starts
     int i, h;                // row tile and key head of it
+    RowTile r;               // the row tile
 };
+
+// a / b for a >= 0, b > 0.  The line is nearly always shorter than 2^31, and a 64-bit
+// division is some 600 cycles on a path that every block waits for.
+__device__ __forceinline__ long long divide(long long a, long long b)
+{
+    return ((a | b) >> 31) == 0 ? static_cast<long long>(static_cast<unsigned>(a) / static_cast<unsigned>(b)) : a / b;
+}
 
 // Called by all THREADS threads of the block; `red` is scratch of THREADS / 32
 // words of 8 bytes, `out` the shared result.
@@ -170,6 +178,7 @@ __device__ __forceinline__ void find_share(const AttnParams &p, long long *red, 
             const int i = blockIdx.x / p.kv.kv_heads;
             const RowTile r = row_tile<ROWS, KEYS>(p, i);
             out->i = i;
+            out->r = r;
             out->h = blockIdx.x - i * p.kv.kv_heads;
             out->at = out->start = 0;
             out->end = r.units ? SETUP + r.units : 0;
@@ -211,7 +220,7 @@ __device__ __forceinline__ void find_share(const AttnParams &p, long long *red, 
         total += v;
     }
     const long long before = base + incl - sum;
-    const long long chunk = max(static_cast<long long>(p.min_chunk), (total + gridDim.x - 1) / gridDim.x);
+    const long long chunk = max(static_cast<long long>(p.min_chunk), divide(total + gridDim.x - 1, gridDim.x));
     const long long at = chunk * blockIdx.x;
     if (tid == 0)
         out->chunk = chunk;
@@ -223,7 +232,8 @@ __device__ __forceinline__ void find_share(const AttnParams &p, long long *red, 
             const long long all = static_cast<long long>(len) * p.kv.kv_heads;
             if (at < start + all) {
                 out->i = i;
-                out->h = static_cast<int>((at - start) / len);
+                out->r = r;
+                out->h = static_cast<int>(divide(at - start, len));
                 out->start = start + static_cast<long long>(out->h) * len;
                 out->at = at;
                 out->end = min(total, at + chunk);
@@ -235,11 +245,12 @@ __device__ __forceinline__ void find_share(const AttnParams &p, long long *red, 
     __syncthreads();
 }
 
-// One segment of a block's share: `units` >= 1 units from unit `off` of item (row
-// tile i, head h); `first`: the block that holds the item's unit 0.
+// One segment of a block's share: `units` >= 1 units from unit `off` of an item (row
+// tile r, head h) that starts at `start` of the line.
 struct Segment {
     RowTile r;
-    int i, h, off, units, first;
+    int h, off, units;
+    long long start;
 };
 
 // Walks a share.  next() gives its segments in order.
@@ -248,7 +259,7 @@ struct Walk {
     long long at, end, chunk, start;
     int i, h;
     RowTile r;
-    __device__ __forceinline__ void begin(const AttnParams &p, const Share &s)
+    __device__ __forceinline__ void begin(const Share &s)
     {
         at = s.at;
         end = s.end;
@@ -256,8 +267,7 @@ struct Walk {
         start = s.start;
         i = s.i;
         h = s.h;
-        if (at < end)
-            r = row_tile<ROWS, KEYS>(p, i);
+        r = s.r;
     }
     __device__ __forceinline__ bool next(const AttnParams &p, Segment &s)
     {
@@ -281,11 +291,10 @@ struct Walk {
             if (b <= a)
                 continue;              // only the item's start-up lies here
             s.r = r;
-            s.i = i;
             s.h = h;
             s.off = a;
             s.units = b - a;
-            s.first = static_cast<int>((start + SETUP) / chunk);
+            s.start = start;
             return true;
         }
         return false;
@@ -298,11 +307,12 @@ __device__ __forceinline__ bool is_whole(const Segment &s) { return s.units == s
 // Whether this block holds the last part, but not all, of the item.
 __device__ __forceinline__ bool is_last_part(const Segment &s) { return s.off > 0 && s.off + s.units == s.r.units; }
 
-// What the joining kernel needs of an item: its first block, its rows, first row and
-// token, and its key head.
-__device__ __forceinline__ void write_meta(const AttnParams &p, const Segment &s)
+// What the joining kernel needs of an item: its first block (the one that holds its
+// first unit), its rows, first row and token, and its key head.
+template <int SETUP>
+__device__ __forceinline__ void write_meta(const AttnParams &p, const Segment &s, long long chunk)
 {
-    p.meta[2 * blockIdx.x] = make_int4(s.first, s.r.rows, s.r.row0, s.r.t0);
+    p.meta[2 * blockIdx.x] = make_int4(static_cast<int>(divide(s.start + SETUP, chunk)), s.r.rows, s.r.row0, s.r.t0);
     p.meta[2 * blockIdx.x + 1] = make_int4(s.h, 0, 0, 0);
 }
 
