@@ -218,6 +218,7 @@ size_t scratch_bytes(bool few, int head_dim, int num_sms)
 // Work a block takes at least, in units: below this a split costs more (a second kernel,
 // the partial results) than the longer walk.
 constexpr int kMinDecodeUnits = 5, kMinChunkUnits = 6;
+constexpr int kMaxCluster = 8, kClusterUnits = 8;
 
 }  // namespace
 
@@ -240,9 +241,19 @@ cudaError_t attn_dispatch(AttnParams &p, int max_q, long long max_kv, void *work
     const long long longest = (max_kv + keys - 1) / keys;      // units of the longest item
     // one block per item where no item is long enough to be split
     p.whole = longest + setup <= p.min_chunk && items <= 0x7fffffff;
+    p.cluster = 1;
     int grid = attn_grid(few, num_sms);
+    // a cluster of blocks per item where all of them run at once and each block's
+    // stretch is short enough to cost less than the joining kernel
+    if (few && !p.whole)
+        for (int c = kMaxCluster; c > 1; c /= 2)
+            if (items * c <= grid && (longest + c - 1) / c <= kClusterUnits) {
+                p.cluster = c;
+                p.whole = 1;
+                break;
+            }
     if (p.whole)
-        grid = static_cast<int>(items);
+        grid = static_cast<int>(items) * p.cluster;
     else if (items * (longest + setup) < static_cast<long long>(grid) * p.min_chunk)
         grid = static_cast<int>((items * (longest + setup) + p.min_chunk - 1) / p.min_chunk);
     uint8_t *ws = static_cast<uint8_t *>(workspace);

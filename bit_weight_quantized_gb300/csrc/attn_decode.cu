@@ -7,12 +7,15 @@
 // Bound by reading K and V once from HBM: every key costs 4 D bytes and at most
 // 16 * 4 D flops, far below the tensor cores' ratio, so mma.sync is enough and the
 // work is to keep reads in flight.  Each of a block's four warps walks its own 16
-// keys of every 64-key unit with its own ring of asynchronous copies (kStages x 16
-// keys of K and V), running maximum, sum and 16 x D fp32 output in registers: no
+// keys of every 64-key unit with its own ring of asynchronous copies (16 keys of K
+// and V a stage), running maximum, sum and 16 x D fp32 output in registers: no
 // barrier and no exchange between warps until the segment ends.  Two blocks per SM
-// keep 2 x 4 warps x (kStages - 1) x 16 keys x 4 D bytes in flight (128 KB at
-// D = 128).  At the end of a segment the warps' results meet in shared memory.
-// Long axes are split over all blocks (find_share) and joined by attn.cu.
+// keep 128 KB (D = 128) or 160 KB (D = 64) in flight.  At the end of a segment the
+// warps' results meet in shared memory.
+//
+// Long axes are split over all blocks (find_share) and joined by a second kernel
+// (attn.cu).  Short ones, where that kernel's 3.5 us would count, go to a cluster of
+// up to eight blocks per item, which joins its parts through its blocks' shared memory.
 //
 // The running maximum is replaced only when it grows by more than 2^8 (the scale
 // factors stay within fp32 and fp16 range either way), so the output is rescaled
@@ -27,18 +30,20 @@ namespace {
 
 constexpr int kDecWarps = 4;
 constexpr int kDecThreads = 32 * kDecWarps;
-constexpr int kDecStages = 3;
 constexpr int kWarpKeys = kDecodeKeys / kDecWarps;   // 16
 constexpr float kGrow = 8.f;                         // log2 of the growth that replaces the maximum
 
 template <int D>
 struct DecLayout {
     static constexpr int kTile = kWarpKeys * D * 2;                       // 16 keys of K or V
-    static constexpr int kWarpBytes = kDecStages * 2 * kTile;
+    static constexpr int kStages = 384 / D;                               // 96 KB of rings per block
+    static constexpr int kWarpBytes = kStages * 2 * kTile;
     static constexpr int kOffQ = kDecWarps * kWarpBytes;
     static constexpr int kBytes = kOffQ + kDecodeRows * D * 2;
     static constexpr int kPitch = D + 8;                                  // floats per row of a warp's output
-    static_assert(kDecWarps * kDecodeRows * (kPitch + 2) * 4 <= kOffQ, "the warps' outputs reuse the rings");
+    static constexpr int kOffMl = kDecWarps * kDecodeRows * kPitch * 4;   // the warps' maxima and sums
+    static constexpr int kOffSum = kOffMl + kDecWarps * kDecodeRows * 8;  // the block's output, maxima and sums
+    static_assert(kOffSum + kDecodeRows * (D + 2) * 4 <= kOffQ, "the warps' outputs reuse the rings");
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr)
@@ -76,6 +81,36 @@ template <int D>
 __device__ __forceinline__ uint32_t tile_addr(int r, int c)
 {
     return static_cast<uint32_t>(r * D * 2 + ((c ^ (r & 7)) << 4));
+}
+
+// A shared-memory address of this block, in block `rank` of the cluster.
+__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, int rank)
+{
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+
+__device__ __forceinline__ float2 peer_load2(uint32_t addr)
+{
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float4 peer_load4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 template <int D, bool BF16>
@@ -116,6 +151,11 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
     Segment sg;
     while (walk.next(p, sg)) {
         const RowTile &r = sg.r;
+        if (p.cluster > 1) {   // the cluster's blocks take stretches of one item
+            const int rank = blockIdx.x % p.cluster, all = sg.units;
+            sg.off = rank * all / p.cluster;
+            sg.units = (rank + 1) * all / p.cluster - sg.off;
+        }
         const uint16_t *kbase = static_cast<const uint16_t *>(p.kv.k) + sg.h * p.kv.head_stride;
         const uint16_t *vbase = static_cast<const uint16_t *>(p.kv.v) + sg.h * p.kv.head_stride;
         const int key0 = (r.unit0 + sg.off) * kDecodeKeys + warp * kWarpKeys;   // the warp's first key
@@ -126,7 +166,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
             return j < sg.units && key >= r.lo && key < r.hi ? key_offset(p.kv, r.b, key, p.status) : -1;
         };
         auto load = [&](int j, long long off) {
-            const uint32_t dst = ring + (j % kDecStages) * (2 * L::kTile);
+            const uint32_t dst = ring + (j % L::kStages) * (2 * L::kTile);
 #pragma unroll
             for (int c = 0; c < kCopies; ++c) {
                 const int row = c * kRowsPerCopy + crow;
@@ -140,7 +180,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
 
         long long ahead = place(0);
 #pragma unroll
-        for (int j = 0; j < kDecStages - 1; ++j) {
+        for (int j = 0; j < L::kStages - 1; ++j) {
             if (j < sg.units)
                 load(j, ahead);
             cp_async_commit();
@@ -179,15 +219,15 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
 
 #pragma unroll 1
         for (int j = 0; j < sg.units; ++j) {
-            if (j + kDecStages - 1 < sg.units)
-                load(j + kDecStages - 1, ahead);
+            if (j + L::kStages - 1 < sg.units)
+                load(j + L::kStages - 1, ahead);
             cp_async_commit();
-            ahead = place(j + kDecStages);
-            cp_async_wait_group<kDecStages - 1>();
+            ahead = place(j + L::kStages);
+            cp_async_wait_group<L::kStages - 1>();
             __syncwarp();
             const int kb = key0 + j * kDecodeKeys;
             if (kb < r.hi && kb + kWarpKeys > r.lo) {
-                const uint32_t ks = ring + (j % kDecStages) * (2 * L::kTile), vs = ks + L::kTile;
+                const uint32_t ks = ring + (j % L::kStages) * (2 * L::kTile), vs = ks + L::kTile;
                 float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
@@ -260,7 +300,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
         // the warps' maxima, sums and outputs meet in shared memory (over the rings)
         __syncthreads();
         float *wo = reinterpret_cast<float *>(smem);
-        float *wml = wo + kDecWarps * kDecodeRows * L::kPitch;
+        float *wml = reinterpret_cast<float *>(smem + L::kOffMl);
         {
             float *w0 = wo + (warp * kDecodeRows + g) * L::kPitch, *w1 = w0 + 8 * L::kPitch;
 #pragma unroll
@@ -276,6 +316,16 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
         __syncthreads();
         const bool whole = is_whole(sg);
         const int slot = part_slot(sg);
+        // four finished values of a row to the output
+        auto store = [&](int row, int c, float m, float l, const float4 &acc) {
+            const int rr = r.row0 + row, tok = rr / p.group;
+            const long long at = static_cast<long long>(r.t0 + tok) * p.q_heads + sg.h * p.group + rr - tok * p.group;
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            *reinterpret_cast<uint2 *>(p.out + at * D + c) =
+                make_uint2(pack16<BF16>(acc.x * inv, acc.y * inv), pack16<BF16>(acc.z * inv, acc.w * inv));
+            if (p.lse && c == 0)
+                p.lse[at] = l > 0.f ? (m - kShift + log2f(l)) * 0.6931471805599453f : -INFINITY;
+        };
         for (int e = tid; e < r.rows * (D / 4); e += kDecThreads) {
             const int row = e / (D / 4), c = 4 * (e % (D / 4));
             float m = -INFINITY;
@@ -296,20 +346,45 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
                 acc.z = fmaf(a, v.z, acc.z);
                 acc.w = fmaf(a, v.w, acc.w);
             }
-            if (whole) {
-                const int rr = r.row0 + row, tok = rr / p.group;
-                const long long at = static_cast<long long>(r.t0 + tok) * p.q_heads + sg.h * p.group + rr - tok * p.group;
-                const float inv = l > 0.f ? 1.f / l : 0.f;
-                *reinterpret_cast<uint2 *>(p.out + at * D + c) =
-                    make_uint2(pack16<BF16>(acc.x * inv, acc.y * inv), pack16<BF16>(acc.z * inv, acc.w * inv));
-                if (p.lse && c == 0)
-                    p.lse[at] = l > 0.f ? (m - kShift + log2f(l)) * 0.6931471805599453f : -INFINITY;
+            if (p.cluster > 1) {
+                *reinterpret_cast<float4 *>(smem + L::kOffSum + (row * D + c) * 4) = acc;
+                if (c == 0)
+                    *reinterpret_cast<float2 *>(smem + L::kOffSum + (kDecodeRows * D + 2 * row) * 4) = make_float2(m, l);
+            } else if (whole) {
+                store(row, c, m, l, acc);
             } else {
                 *reinterpret_cast<float4 *>(p.part_o + (static_cast<long long>(slot) * kDecodeRows + row) * D + c) = acc;
                 if (c == 0)
                     *reinterpret_cast<float2 *>(p.part_ml + (static_cast<long long>(slot) * kDecodeRows + row) * 2) =
                         make_float2(m, l);
             }
+        }
+        if (p.cluster > 1) {
+            // the blocks' parts meet, each block joins its share of the values
+            cluster_sync();
+            const int rank = blockIdx.x % p.cluster;
+            for (int e = rank * kDecThreads + tid; e < r.rows * (D / 4); e += p.cluster * kDecThreads) {
+                const int row = e / (D / 4), c = 4 * (e % (D / 4));
+                const uint32_t ml_at = sbase + L::kOffSum + (kDecodeRows * D + 2 * row) * 4;
+                const uint32_t o_at = sbase + L::kOffSum + (row * D + c) * 4;
+                float m = -INFINITY, l = 0.f;
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int b = 0; b < p.cluster; ++b) {
+                    const float2 ml = peer_load2(peer_addr(ml_at, b));
+                    const float4 v = peer_load4(peer_addr(o_at, b));
+                    const float mn = fmaxf(m, ml.x), base = mn == -INFINITY ? 0.f : mn;
+                    const float w0 = ex2(m - base), w1 = ex2(ml.x - base);
+                    m = mn;
+                    l = w0 * l + w1 * ml.y;
+                    acc.x = w0 * acc.x + w1 * v.x;
+                    acc.y = w0 * acc.y + w1 * v.y;
+                    acc.z = w0 * acc.z + w1 * v.z;
+                    acc.w = w0 * acc.w + w1 * v.w;
+                }
+                store(row, c, m, l, acc);
+            }
+            cluster_sync();   // no block leaves while another still reads from it
+            return;
         }
         if (tid == 0 && is_last_part(sg))
             write_meta<kDecodeSetup>(p, sg, share.chunk);
@@ -329,11 +404,14 @@ cudaError_t launch_decode_attn(const AttnParams &p, int grid, cudaStream_t strea
     cfg.blockDim = dim3(kDecThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = p.cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = p.cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, attn_decode_kernel<D, BF16>, p);
 }
 

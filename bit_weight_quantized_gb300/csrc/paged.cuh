@@ -173,13 +173,13 @@ template <int ROWS, int KEYS, int SETUP, int THREADS>
 __device__ __forceinline__ void find_share(const AttnParams &p, long long *red, Share *out)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (p.whole) {   // block c holds item c
+    if (p.whole) {   // cluster (or block) c holds item c
         if (tid == 0) {
-            const int i = blockIdx.x / p.kv.kv_heads;
+            const int item = blockIdx.x / p.cluster, i = item / p.kv.kv_heads;
             const RowTile r = row_tile<ROWS, KEYS>(p, i);
             out->i = i;
             out->r = r;
-            out->h = blockIdx.x - i * p.kv.kv_heads;
+            out->h = item - i * p.kv.kv_heads;
             out->at = out->start = 0;
             out->end = r.units ? SETUP + r.units : 0;
             out->chunk = 1LL << 40;

@@ -41,7 +41,8 @@ struct AttnParams {
     int q_heads, group;            // query heads, query heads per key head
     int causal, window;
     int row_tiles;                 // row tiles per sequence (of the longest one)
-    int whole;                     // every item in one block: no partial results
+    int whole;                     // every item in one cluster: no partial results
+    int cluster;                   // blocks per cluster (decode kernel, whole items)
     int min_chunk;                 // work a block takes at least, in units
 };
 
