@@ -218,7 +218,7 @@ size_t scratch_bytes(bool few, int head_dim, int num_sms)
 // Work a block takes at least, in units: below this a split costs more (a second kernel,
 // the partial results) than the longer walk.
 constexpr int kMinDecodeUnits = 5, kMinChunkUnits = 6;
-constexpr int kMaxCluster = 8, kClusterUnits = 8;
+constexpr int kClusterUnits = 8;
 
 }  // namespace
 

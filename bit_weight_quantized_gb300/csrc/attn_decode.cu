@@ -149,13 +149,17 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
     Walk<kDecodeRows, kDecodeKeys, kDecodeSetup> walk;
     walk.begin(share);
     Segment sg;
-    while (walk.next(p, sg)) {
+    bool more = p.whole ? share.end > 0 : walk.next(p, sg);
+    if (p.whole && more) {   // the whole item; a cluster's blocks take a stretch each
+        const int rank = blockIdx.x % p.cluster, all = share.r.units;
+        sg.r = share.r;
+        sg.h = share.h;
+        sg.start = 0;
+        sg.off = rank * all / p.cluster;
+        sg.units = (rank + 1) * all / p.cluster - sg.off;
+    }
+    for (; more; more = !p.whole && walk.next(p, sg)) {
         const RowTile &r = sg.r;
-        if (p.cluster > 1) {   // the cluster's blocks take stretches of one item
-            const int rank = blockIdx.x % p.cluster, all = sg.units;
-            sg.off = rank * all / p.cluster;
-            sg.units = (rank + 1) * all / p.cluster - sg.off;
-        }
         const uint16_t *kbase = static_cast<const uint16_t *>(p.kv.k) + sg.h * p.kv.head_stride;
         const uint16_t *vbase = static_cast<const uint16_t *>(p.kv.v) + sg.h * p.kv.head_stride;
         const int key0 = (r.unit0 + sg.off) * kDecodeKeys + warp * kWarpKeys;   // the warp's first key
@@ -178,6 +182,16 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
             }
         };
 
+        // queries: 16 rows, zero past the tile
+        for (int e = tid; e < kDecodeRows * kChunks; e += kDecThreads) {
+            const int row = e / kChunks, c = e % kChunks, rr = r.row0 + row, tok = rr / p.group;
+            const bool in = row < r.rows;
+            const uint16_t *src = p.q;
+            if (in)
+                src += (r.t0 + tok) * p.q_stride + static_cast<long long>(sg.h * p.group + rr - tok * p.group) * D + 8 * c;
+            cp_async16_or_zero(qs + tile_addr<D>(row, c), src, in);
+        }
+        cp_async_commit();
         long long ahead = place(0);
 #pragma unroll
         for (int j = 0; j < L::kStages - 1; ++j) {
@@ -187,17 +201,9 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
             ahead = place(j + 1);
         }
 
-        // queries: 16 rows, zero past the tile, to registers in fragment order
-        for (int e = tid; e < kDecodeRows * kChunks; e += kDecThreads) {
-            const int row = e / kChunks, c = e % kChunks;
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (row < r.rows) {
-                const int rr = r.row0 + row, tok = rr / p.group;
-                v = *reinterpret_cast<const uint4 *>(p.q + (r.t0 + tok) * p.q_stride +
-                                                     static_cast<long long>(sg.h * p.group + rr - tok * p.group) * D + 8 * c);
-            }
-            *reinterpret_cast<uint4 *>(smem + L::kOffQ + tile_addr<D>(row, c)) = v;
-        }
+        // the queries have landed (the copies after them are still under way); to
+        // registers in fragment order
+        cp_async_wait_group<L::kStages - 1>();
         __syncthreads();
         uint32_t qf[D / 16][4];
 #pragma unroll
@@ -363,23 +369,35 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
             // the blocks' parts meet, each block joins its share of the values
             cluster_sync();
             const int rank = blockIdx.x % p.cluster;
-            for (int e = rank * kDecThreads + tid; e < r.rows * (D / 4); e += p.cluster * kDecThreads) {
+            for (int e = tid * p.cluster + rank; e < r.rows * (D / 4); e += p.cluster * kDecThreads) {
                 const int row = e / (D / 4), c = 4 * (e % (D / 4));
                 const uint32_t ml_at = sbase + L::kOffSum + (kDecodeRows * D + 2 * row) * 4;
                 const uint32_t o_at = sbase + L::kOffSum + (row * D + c) * 4;
                 float m = -INFINITY, l = 0.f;
                 float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int b = 0; b < p.cluster; ++b) {
-                    const float2 ml = peer_load2(peer_addr(ml_at, b));
-                    const float4 v = peer_load4(peer_addr(o_at, b));
-                    const float mn = fmaxf(m, ml.x), base = mn == -INFINITY ? 0.f : mn;
-                    const float w0 = ex2(m - base), w1 = ex2(ml.x - base);
-                    m = mn;
-                    l = w0 * l + w1 * ml.y;
-                    acc.x = w0 * acc.x + w1 * v.x;
-                    acc.y = w0 * acc.y + w1 * v.y;
-                    acc.z = w0 * acc.z + w1 * v.z;
-                    acc.w = w0 * acc.w + w1 * v.w;
+                float2 ml[kMaxCluster];      // all reads are under way together
+                float4 v[kMaxCluster];
+#pragma unroll
+                for (int b = 0; b < kMaxCluster; ++b) {
+                    ml[b] = make_float2(-INFINITY, 0.f);
+                    v[b] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (b < p.cluster) {
+                        ml[b] = peer_load2(peer_addr(ml_at, b));
+                        v[b] = peer_load4(peer_addr(o_at, b));
+                    }
+                }
+#pragma unroll
+                for (int b = 0; b < kMaxCluster; ++b)
+                    m = fmaxf(m, ml[b].x);
+                const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+                for (int b = 0; b < kMaxCluster; ++b) {
+                    const float w = ex2(ml[b].x - base);
+                    l = fmaf(w, ml[b].y, l);
+                    acc.x = fmaf(w, v[b].x, acc.x);
+                    acc.y = fmaf(w, v[b].y, acc.y);
+                    acc.z = fmaf(w, v[b].z, acc.z);
+                    acc.w = fmaf(w, v[b].w, acc.w);
                 }
                 store(row, c, m, l, acc);
             }

@@ -54,6 +54,9 @@ constexpr int kChunkRows = 256, kChunkKeys = 128;
 // with 2, 4 and 6.
 constexpr int kDecodeSetup = 1, kChunkSetup = 4;
 
+// Blocks per cluster of the decode kernel at most.
+constexpr int kMaxCluster = 8;
+
 // Blocks of the decode kernel per SM (it is sized for two).
 constexpr int kDecodeBlocksPerSm = 2;
 
