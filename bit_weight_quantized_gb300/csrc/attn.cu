@@ -230,7 +230,7 @@ size_t attn_workspace_bytes(int q_heads, int kv_heads, int head_dim, int max_q, 
 cudaError_t attn_dispatch(AttnParams &p, int max_q, long long max_kv, void *workspace, int num_sms, cudaStream_t stream)
 {
     const bool few = few_rows(max_q, p.group);
-    const int rows = few ? kDecodeRows : kChunkRows, keys = few ? kDecodeKeys : kChunkKeys;
+    const int rows = few ? kDecodeRows : kChunkRows, keys = few ? decode_keys(p.kv.head_dim) : kChunkKeys;
     const int setup = few ? kDecodeSetup : kChunkSetup;
     p.row_tiles = static_cast<int>((static_cast<long long>(max_q) * p.group + rows - 1) / rows);
     p.min_chunk = few ? kMinDecodeUnits : kMinChunkUnits;
@@ -242,6 +242,7 @@ cudaError_t attn_dispatch(AttnParams &p, int max_q, long long max_kv, void *work
     // one block per item where no item is long enough to be split
     p.whole = longest + setup <= p.min_chunk && items <= 0x7fffffff;
     p.cluster = 1;
+    p.same_page = p.kv.page_size % (keys / 4) == 0;   // four warps per decode block
     int grid = attn_grid(few, num_sms);
     // a cluster of blocks per item where all of them run at once and each block's
     // stretch is short enough to cost less than the joining kernel

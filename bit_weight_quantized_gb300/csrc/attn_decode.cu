@@ -7,10 +7,10 @@
 // Bound by reading K and V once from HBM: every key costs 4 D bytes and at most
 // 16 * 4 D flops, far below the tensor cores' ratio, so mma.sync is enough and the
 // work is to keep reads in flight.  Each of a block's four warps walks its own 16
-// keys of every 64-key unit with its own ring of asynchronous copies (16 keys of K
+// keys (D = 64: 32) of every unit with its own ring of asynchronous copies (8 KB of K
 // and V a stage), running maximum, sum and 16 x D fp32 output in registers: no
 // barrier and no exchange between warps until the segment ends.  Two blocks per SM
-// keep 128 KB (D = 128) or 160 KB (D = 64) in flight.  At the end of a segment the
+// keep 128 KB in flight.  At the end of a segment the
 // warps' results meet in shared memory.
 //
 // Long axes are split over all blocks (find_share) and joined by a second kernel
@@ -30,13 +30,14 @@ namespace {
 
 constexpr int kDecWarps = 4;
 constexpr int kDecThreads = 32 * kDecWarps;
-constexpr int kWarpKeys = kDecodeKeys / kDecWarps;   // 16
 constexpr float kGrow = 8.f;                         // log2 of the growth that replaces the maximum
 
 template <int D>
 struct DecLayout {
-    static constexpr int kTile = kWarpKeys * D * 2;                       // 16 keys of K or V
-    static constexpr int kStages = 384 / D;                               // 96 KB of rings per block
+    static constexpr int kKeys = decode_keys(D);                          // keys per unit
+    static constexpr int kWarpKeys = kKeys / kDecWarps;                   // a warp's keys of a unit
+    static constexpr int kTile = kWarpKeys * D * 2;                       // their K or V, 4 KB
+    static constexpr int kStages = 3;                                     // 96 KB of rings per block
     static constexpr int kWarpBytes = kStages * 2 * kTile;
     static constexpr int kOffQ = kDecWarps * kWarpBytes;
     static constexpr int kBytes = kOffQ + kDecodeRows * D * 2;
@@ -120,7 +121,8 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
     using L = DecLayout<D>;
     constexpr int kChunks = D / 8;                 // 16-byte chunks per row
     constexpr int kRowsPerCopy = 32 / kChunks;     // rows one warp-wide copy covers
-    constexpr int kCopies = kWarpKeys / kRowsPerCopy;
+    constexpr int kKeys = L::kKeys, kWarpKeys = L::kWarpKeys, kCopies = kWarpKeys / kRowsPerCopy;
+    constexpr int kSub = kWarpKeys / 16;           // 16-key steps of the matrix instructions per tile
     constexpr float kShift = BF16 ? 0.f : 7.f;
 
     extern __shared__ __align__(128) uint8_t smem[];
@@ -132,7 +134,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
     if (tid == 0)
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    find_share<kDecodeRows, kDecodeKeys, kDecodeSetup, kDecThreads>(p, red, &share);
+    find_share<kDecodeRows, kKeys, kDecodeSetup, kDecThreads>(p, red, &share);
 
     const uint32_t sbase = smem_u32(smem);
     const uint32_t ring = sbase + warp * L::kWarpBytes;
@@ -146,7 +148,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
     if (!p.whole && tid == 0)
         p.meta[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
 
-    Walk<kDecodeRows, kDecodeKeys, kDecodeSetup> walk;
+    Walk<kDecodeRows, kKeys, kDecodeSetup> walk;
     walk.begin(share);
     Segment sg;
     bool more = p.whole ? share.end > 0 : walk.next(p, sg);
@@ -162,15 +164,35 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
         const RowTile &r = sg.r;
         const uint16_t *kbase = static_cast<const uint16_t *>(p.kv.k) + sg.h * p.kv.head_stride;
         const uint16_t *vbase = static_cast<const uint16_t *>(p.kv.v) + sg.h * p.kv.head_stride;
-        const int key0 = (r.unit0 + sg.off) * kDecodeKeys + warp * kWarpKeys;   // the warp's first key
+        const int key0 = (r.unit0 + sg.off) * kKeys + warp * kWarpKeys;   // the warp's first key
 
-        // offset of key (tile j, row lane & 15), or -1 where nothing is read
+        // Where tile j lies, looked up one tile ahead: where a tile's keys share a page
+        // (p.same_page), the offset of the lane's first row; else that of row `lane`.
+        // -1: nothing is read.
         auto place = [&](int j) -> long long {
-            const int key = key0 + j * kDecodeKeys + (lane & 15);
-            return j < sg.units && key >= r.lo && key < r.hi ? key_offset(p.kv, r.b, key, p.status) : -1;
+            const int key = key0 + j * kKeys + (p.same_page ? 0 : lane % kWarpKeys);
+            if (j >= sg.units || key >= r.hi || (p.same_page ? key + kWarpKeys <= r.lo : key < r.lo))
+                return -1;
+            const long long off = key_offset(p.kv, r.b, key, p.status);
+            return p.same_page && off >= 0 ? off + crow * p.kv.slot_stride : off;
         };
         auto load = [&](int j, long long off) {
             const uint32_t dst = ring + (j % L::kStages) * (2 * L::kTile);
+            if (p.same_page) {
+                const int kb = key0 + j * kKeys;
+                const bool inside = off >= 0 && kb >= r.lo && kb + kWarpKeys <= r.hi;
+                const long long step = kRowsPerCopy * p.kv.slot_stride;
+                long long e = (off >= 0 ? off : 0) + cchunk * 8;
+#pragma unroll
+                for (int c = 0; c < kCopies; ++c) {
+                    const int row = c * kRowsPerCopy + crow, key = kb + row;
+                    const bool ok = inside || (off >= 0 && key >= r.lo && key < r.hi);
+                    cp_async16_or_zero(dst + tile_addr<D>(row, cchunk), kbase + (ok ? e : 0), ok);
+                    cp_async16_or_zero(dst + L::kTile + tile_addr<D>(row, cchunk), vbase + (ok ? e : 0), ok);
+                    e += step;
+                }
+                return;
+            }
 #pragma unroll
             for (int c = 0; c < kCopies; ++c) {
                 const int row = c * kRowsPerCopy + crow;
@@ -231,20 +253,27 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
             ahead = place(j + L::kStages);
             cp_async_wait_group<L::kStages - 1>();
             __syncwarp();
-            const int kb = key0 + j * kDecodeKeys;
+            const int kb = key0 + j * kKeys;
             if (kb < r.hi && kb + kWarpKeys > r.lo) {
                 const uint32_t ks = ring + (j % L::kStages) * (2 * L::kTile), vs = ks + L::kTile;
-                float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+                float s[2 * kSub][4];
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    uint32_t kf[4];
-                    ldsm4(kf, ks + tile_addr<D>(krow, 2 * kk + kch));
-                    mma16<BF16>(s[0], qf[kk], kf[0], kf[1]);
-                    mma16<BF16>(s[1], qf[kk], kf[2], kf[3]);
-                }
+                for (int n = 0; n < 2 * kSub; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        s[n][e] = 0.f;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+                    for (int u = 0; u < kSub; ++u) {
+                        uint32_t kf[4];
+                        ldsm4(kf, ks + tile_addr<D>(16 * u + krow, 2 * kk + kch));
+                        mma16<BF16>(s[2 * u], qf[kk], kf[0], kf[1]);
+                        mma16<BF16>(s[2 * u + 1], qf[kk], kf[2], kf[3]);
+                    }
                 if (kb < all_lo || kb + kWarpKeys - 1 > all_hi) {
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
+                    for (int n = 0; n < 2 * kSub; ++n)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const int key = kb + 8 * n + 2 * t + e;
@@ -254,8 +283,14 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
                                 s[n][2 + e] = -INFINITY;
                         }
                 }
-                float x0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1])) * p.scale_log2;
-                float x1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3])) * p.scale_log2;
+                float x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll
+                for (int n = 0; n < 2 * kSub; ++n) {
+                    x0 = fmaxf(x0, fmaxf(s[n][0], s[n][1]));
+                    x1 = fmaxf(x1, fmaxf(s[n][2], s[n][3]));
+                }
+                x0 *= p.scale_log2;
+                x1 *= p.scale_log2;
                 x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
                 x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
                 x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
@@ -276,23 +311,25 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
                     }
                 }
                 const float n0 = kShift - (m0 == -INFINITY ? 0.f : m0), n1 = kShift - (m1 == -INFINITY ? 0.f : m1);
-                uint32_t pf[4];
+                uint32_t pf[kSub][4];
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
+                for (int n = 0; n < 2 * kSub; ++n) {
                     const float p0 = ex2(fmaf(s[n][0], p.scale_log2, n0)), p1 = ex2(fmaf(s[n][1], p.scale_log2, n0));
                     const float p2 = ex2(fmaf(s[n][2], p.scale_log2, n1)), p3 = ex2(fmaf(s[n][3], p.scale_log2, n1));
                     l0 += p0 + p1;
                     l1 += p2 + p3;
-                    pf[2 * n] = pack16<BF16>(p0, p1);
-                    pf[2 * n + 1] = pack16<BF16>(p2, p3);
+                    pf[n / 2][2 * (n & 1)] = pack16<BF16>(p0, p1);
+                    pf[n / 2][2 * (n & 1) + 1] = pack16<BF16>(p2, p3);
                 }
 #pragma unroll
-                for (int n = 0; n < D / 16; ++n) {
-                    uint32_t vf[4];
-                    ldsm4_t(vf, vs + tile_addr<D>(vrow, 2 * n + vch));
-                    mma16<BF16>(o[2 * n], pf, vf[0], vf[1]);
-                    mma16<BF16>(o[2 * n + 1], pf, vf[2], vf[3]);
-                }
+                for (int u = 0; u < kSub; ++u)
+#pragma unroll
+                    for (int n = 0; n < D / 16; ++n) {
+                        uint32_t vf[4];
+                        ldsm4_t(vf, vs + tile_addr<D>(16 * u + vrow, 2 * n + vch));
+                        mma16<BF16>(o[2 * n], pf[u], vf[0], vf[1]);
+                        mma16<BF16>(o[2 * n + 1], pf[u], vf[2], vf[3]);
+                    }
             }
             __syncwarp();   // every lane has read the slot before it is filled again
         }

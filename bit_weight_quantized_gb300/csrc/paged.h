@@ -43,11 +43,13 @@ struct AttnParams {
     int row_tiles;                 // row tiles per sequence (of the longest one)
     int whole;                     // every item in one cluster: no partial results
     int cluster;                   // blocks per cluster (decode kernel, whole items)
+    int same_page;                 // every warp tile of the decode kernel lies in one page
     int min_chunk;                 // work a block takes at least, in units
 };
 
 // Sizes of one kernel's work items: query rows per tile, keys per unit.
-constexpr int kDecodeRows = 16, kDecodeKeys = 64;
+constexpr int kDecodeRows = 16;
+__host__ __device__ constexpr int decode_keys(int head_dim) { return head_dim == 64 ? 128 : 64; }   // 32 KB of K and V
 constexpr int kChunkRows = 256, kChunkKeys = 128;
 // What starting and finishing an item costs, in units (see find_share).  Chunk kernel:
 // about 9000 cycles against 2400 a unit; an 8192-token prompt takes 466, 361 and 368 us
