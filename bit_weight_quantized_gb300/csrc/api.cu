@@ -717,6 +717,7 @@ qmm_status qmm_kv_append(const qmm_paged_kv *kv, const void *k, int64_t k_stride
     p.rot = rot;
     p.rope_len = rope_len;
     p.interleaved = interleaved != 0;
+    p.by_page = fast_div(kv->page_size);
     return from_cuda(launch_kv_append(p, f->num_sms, stream));
 }
 

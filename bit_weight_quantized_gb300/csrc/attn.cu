@@ -18,7 +18,7 @@ __device__ __forceinline__ long long part_of(int c, int first) { return 2LL * c 
 
 __device__ __forceinline__ long long out_row(const AttnParams &p, int row, int t0, int h)
 {
-    const int tok = row / p.group;
+    const int tok = p.by_group(row);
     return static_cast<long long>(t0 + tok) * p.q_heads + h * p.group + row - tok * p.group;
 }
 
@@ -233,6 +233,9 @@ cudaError_t attn_dispatch(AttnParams &p, int max_q, long long max_kv, void *work
     const int rows = few ? kDecodeRows : kChunkRows, keys = few ? decode_keys(p.kv.head_dim) : kChunkKeys;
     const int setup = few ? kDecodeSetup : kChunkSetup;
     p.row_tiles = static_cast<int>((static_cast<long long>(max_q) * p.group + rows - 1) / rows);
+    p.by_group = fast_div(p.group);
+    p.by_tiles = fast_div(p.row_tiles);
+    p.by_page = fast_div(p.kv.page_size);
     p.min_chunk = few ? kMinDecodeUnits : kMinChunkUnits;
     const long long items = static_cast<long long>(p.kv.batch) * p.row_tiles * p.kv.kv_heads;
     const long long most = static_cast<long long>(p.kv.blocks) * p.kv.page_size;

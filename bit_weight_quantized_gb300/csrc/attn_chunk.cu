@@ -17,8 +17,8 @@
 // no exchange between lanes.  Warp 8 issues the products, one stream after the
 // other, so that one's products run under the other's softmax.  (A warp for each
 // stream let the two fall into step, with both softmaxes and then both products at
-// once: 240 instead of 190 us for 4096 x 4096 x 32 heads of 128.)  Warps 10 and 11
-// bring K and V tiles into a ring each: where the page size is a multiple of 8 by
+// once: 240 instead of 190 us for 4096 x 4096 x 32 heads of 128.)  Warp 9 finds the
+// segments of the block's share ahead of the others.  Warps 10 and 11 bring K and V tiles into a ring each: where the page size is a multiple of 8 by
 // tensor copies, one per page or part of a page that lies in the tile; else by
 // 16-byte asynchronous copies, which take any page size.  V rows that nobody sees
 // (past kv_len, before the window) are made zero, since 0 x NaN would spoil the
@@ -42,7 +42,8 @@ namespace {
 
 constexpr int kSoftWarps = 4;                       // per stream
 constexpr int kIssueWarp = 2 * kSoftWarps;
-constexpr int kLoadWarpK = kIssueWarp + 2, kLoadWarpV = kIssueWarp + 3;   // (warp 9 has no part)
+constexpr int kWalkWarp = kIssueWarp + 1, kLoadWarpV = kIssueWarp + 3;   // (K: the one between)
+constexpr int kSegs = 4;                            // segments found ahead
 constexpr int kChunkThreads = 384;
 constexpr float kChunkGrow = 8.f;
 constexpr int kHalf = kChunkKeys / 2;               // the weights are handed over by halves of a tile
@@ -62,16 +63,14 @@ struct ChunkLayout {
     static constexpr int kOffV = kOffK + kKRing * kTile;
     static constexpr int kOffBar = kOffV + kVRing * kTile;
     // full / empty of both rings, patch, per stream q_full, s_full, p_full (two halves) and
-    // o_full, x_full, x_done, drain
-    static constexpr int kNumBars = 2 * (kKRing + kVRing) + 14;
+    // o_full, x_full, x_done, drain, full / empty of the segments
+    static constexpr int kNumBars = 2 * (kKRing + kVRing) + 14 + 2 * kSegs;
     static constexpr int kOffTmem = kOffBar + 8 * kNumBars;
     static constexpr int kOffShare = kOffTmem + 16;
     static constexpr int kOffRed = kOffShare + sizeof(Share);
-    static constexpr int kOffWalk = kOffRed + 8 * (kChunkThreads / 32);
-    static constexpr int kOffSeg = kOffWalk + sizeof(ChunkWalk) * (kChunkThreads / 32);
-    // two segments per softmax warp, one per other warp
-    static constexpr int kBytes = kOffSeg + sizeof(Segment) * (kIssueWarp + kChunkThreads / 32);
-    static_assert(kOffShare % 8 == 0 && sizeof(Share) % 8 == 0 && sizeof(ChunkWalk) % 8 == 0, "alignment");
+    static constexpr int kOffSeg = kOffRed + 8 * (kChunkThreads / 32);
+    static constexpr int kBytes = kOffSeg + sizeof(Segment) * kSegs;
+    static_assert(kOffShare % 8 == 0 && sizeof(Share) % 8 == 0, "alignment");
     static_assert(kBytes <= 227 * 1024, "shared memory per block");
 };
 
@@ -247,16 +246,15 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return d;
 }
 
-// Walks rows kStep apart as (token, query head of the key head), with one division
-// in all.
+// Walks rows `step` apart as (token, query head of the key head).
 struct RowCursor {
     int tok, head, dt, dh, group;
-    __device__ __forceinline__ RowCursor(int row, int step, int g) : group(g)
+    __device__ __forceinline__ RowCursor(int row, int step, const AttnParams &p) : group(p.group)
     {
-        tok = row / g;
-        head = row - tok * g;
-        dt = step / g;
-        dh = step - dt * g;
+        tok = p.by_group(row);
+        head = row - tok * group;
+        dt = p.by_group(step);
+        dh = step - dt * group;
     }
     __device__ __forceinline__ void next()
     {
@@ -289,6 +287,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
     uint64_t *v_full = k_empty + L::kKRing, *v_empty = v_full + L::kVRing, *patch = v_empty + L::kVRing;
     uint64_t *q_full = patch + 1, *s_full = q_full + 2, *p_full = s_full + 2, *o_full = p_full + 4;
     uint64_t *x_full = o_full + 2, *x_done = x_full + 1, *drain = x_done + 1;
+    uint64_t *seg_full = drain + 1, *seg_empty = seg_full + kSegs;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kOffTmem);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -317,6 +316,10 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
         mbar_init(x_full, kSoftWarps);
         mbar_init(x_done, kSoftWarps);
         mbar_init(drain, 1);
+        for (int i = 0; i < kSegs; ++i) {
+            mbar_init(&seg_full[i], 1);
+            mbar_init(&seg_empty[i], 2 * kSoftWarps + 3);   // softmax, issue and loading warps
+        }
         fence_barrier_init();
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     }
@@ -332,20 +335,18 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
     find_share<kChunkRows, kChunkKeys, kChunkSetup, kChunkThreads>(p, red, &share);
 
     bool ok = true;
-    // every warp walks the share on its own, its state in shared memory (lane 0
-    // steps): registers are short in the softmax warps
-    ChunkWalk &walk = reinterpret_cast<ChunkWalk *>(smem + L::kOffWalk)[warp];
-    Segment *segs = reinterpret_cast<Segment *>(smem + L::kOffSeg) + warp + min(warp, kIssueWarp);
-    if (lane == 0)
-        walk.begin(share);
-    auto next = [&](Segment &s) -> bool {
+    // Warp 9 walks the share and puts the segments, numbered, into a ring of kSegs; one
+    // of no units ends them.  Every other warp goes through all of them.
+    Segment *segs = reinterpret_cast<Segment *>(smem + L::kOffSeg);
+    auto segment = [&](int n) -> const Segment & {
+        if (ok)
+            ok = __all_sync(0xffffffffu, mbar_wait(&seg_full[n % kSegs], n / kSegs & 1, p.status));
+        return segs[n % kSegs];
+    };
+    auto leave = [&](int n) {
         __syncwarp();
-        bool more = false;
         if (lane == 0)
-            more = walk.next(p, s);
-        more = __shfl_sync(0xffffffffu, more ? 1 : 0, 0) != 0;
-        __syncwarp();            // the other lanes read the segment after this
-        return more;
+            mbar_arrive(&seg_empty[n % kSegs]);
     };
 
     if (warp < kIssueWarp) {
@@ -358,23 +359,27 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
         uint32_t ph = 0;         // parity of the next S
         uint32_t oph = 0;        // parity of the next O
         uint32_t xph = 0;        // parity of the next exchange between the streams
-        // the next segment this stream has a part in: rows of its own, or every other
-        // tile of an item of one stream's rows
-        auto next_part = [&](Segment &x) -> bool {
-            while (next(x))
+        // the first segment from number n on that this stream has a part in: rows of its
+        // own, or every other tile of an item of one stream's rows; or the end (-1)
+        auto next_part = [&](int n) -> int {
+            for (;; ++n) {
+                const Segment &x = segment(n);
+                if (!ok || x.units == 0)
+                    return -1;
                 if (x.r.rows > 128 * s || in_two(x))
-                    return true;
-            return false;
+                    return n;
+                leave(n);
+            }
         };
         // this warp's 32 query rows into the operand tile (zeros past the item); every
         // product that read the previous ones is complete.  Stream 1 has none where it
         // shares stream 0's rows.
-        auto load_q = [&](const Segment &x) {
+        auto start_q = [&](const Segment &x) {
             if (s == 1 && x.r.rows <= 128)
                 return;
             const int c = lane % kChunks, row0 = quarter * 32 + lane / kChunks;
             const int left = x.r.rows - 128 * s;        // rows of the stream
-            RowCursor at(x.r.row0 + 128 * s + row0, kRowsPerCopy, p.group);
+            RowCursor at(x.r.row0 + 128 * s + row0, kRowsPerCopy, p);
             const uint16_t *base = p.q + x.r.t0 * p.q_stride + static_cast<long long>(x.h * p.group) * D + 8 * c;
 #pragma unroll
             for (int e = 0; e < 32; e += kRowsPerCopy) {
@@ -384,25 +389,29 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                 at.next();
             }
             cp_async_commit();
+        };
+        auto land_q = [&](const Segment &x) {
+            if (s == 1 && x.r.rows <= 128)
+                return;
             cp_async_wait_group<0>();
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&q_full[s]);
         };
-        int cur = 0;
-        bool have = next_part(segs[0]);
-        if (have)
-            load_q(segs[0]);
-        while (have) {
-            const Segment &sg = segs[cur];
-            const RowTile &r = sg.r;
+        int n = next_part(0);
+        if (n >= 0) {
+            start_q(segs[n % kSegs]);
+            land_q(segs[n % kSegs]);
+        }
+        while (n >= 0) {
+            const Segment &sg = segs[n % kSegs];
+            const RowTile r = sg.r;
             const bool two = in_two(sg);
             const int row = quarter * 32 + lane, trow = (two ? 0 : 128 * s) + row;   // row in the stream, in the item
             const int rr = r.row0 + trow;
             const int units = sg.units, kb0 = (r.unit0 + sg.off) * kChunkKeys;
             const int2 see = row_keys(p, r, rr);
-            have = next_part(segs[cur ^ 1]);     // looked up while the first product runs
             float mref = -INFINITY, l = 0.f;
             const uint64_t scale2 = pair(__float_as_uint(p.scale_log2), __float_as_uint(p.scale_log2));
             const int j0 = two ? s : 0, step = two ? 2 : 1;
@@ -518,9 +527,12 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                     if (!ok)
                         break;
                     tc_fence_after();
-                    cur ^= 1;
-                    if (have)
-                        load_q(segs[cur]);
+                    leave(n);
+                    n = next_part(n + 1);
+                    if (n >= 0) {
+                        start_q(segs[n % kSegs]);
+                        land_q(segs[n % kSegs]);
+                    }
                     continue;
                 }
                 ok = __all_sync(0xffffffffu, mbar_wait(x_full, xph, p.status));
@@ -538,41 +550,48 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
             }
             // rows to memory: the item's output, or this block's part of it
             const bool whole = is_whole(sg);
+            const int next = next_part(n + 1);
+            // (whole rows go through the query tile; else the next queries can come in now)
+            if (!whole && next >= 0)
+                start_q(segs[next % kSegs]);
             const float inv = l > 0.f ? 1.f / l : 0.f;
             float *part = p.part_o + static_cast<long long>(part_slot(sg)) * (kChunkRows * D) + 4 * trow;
-#pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-                uint32_t o[32];
-                tmem_ld32_start(to + c, o);
-                tmem_ld_wait();
-                pin32(o);
-                if (two) {
+            uint32_t o[D];
+#pragma unroll
+            for (int c = 0; c < D; c += 32)
+                tmem_ld32_start(to + c, o + c);
+            tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < D; c += 32)
+                pin32(o + c);
+            if (two) {
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
                     uint32_t o1[32];
                     tmem_ld32_start(tmem + lanes + o_col(1) + c, o1);
                     tmem_ld_wait();
                     pin32(o1);
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
-                        o[e] = __float_as_uint(w0 * __uint_as_float(o[e]) + w1 * __uint_as_float(o1[e]));
+                        o[c + e] = __float_as_uint(w0 * __uint_as_float(o[c + e]) + w1 * __uint_as_float(o1[e]));
                 }
-                if (whole) {
-                    // through the stream's query tile, so that a warp stores whole rows
+            }
+            if (whole) {
+                // through the stream's query tile, so that a warp stores whole rows
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint32_t w[4];
+                for (int c = 0; c < D / 8; ++c) {
+                    uint32_t w[4];
 #pragma unroll
-                        for (int f = 0; f < 4; ++f)
-                            w[f] = pack16<BF16>(__uint_as_float(o[8 * e + 2 * f]) * inv,
-                                                __uint_as_float(o[8 * e + 2 * f + 1]) * inv);
-                        *reinterpret_cast<uint4 *>(qs + q_addr(row, c / 8 + e)) = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
-                } else if (trow < r.rows) {
-                    // parts lie [D / 4][rows][4], so that a warp's rows are consecutive
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        *reinterpret_cast<uint4 *>(part + (c / 4 + e) * (4 * kChunkRows)) =
-                            make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    for (int f = 0; f < 4; ++f)
+                        w[f] = pack16<BF16>(__uint_as_float(o[8 * c + 2 * f]) * inv, __uint_as_float(o[8 * c + 2 * f + 1]) * inv);
+                    *reinterpret_cast<uint4 *>(qs + q_addr(row, c)) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
+            } else if (trow < r.rows) {
+                // parts lie [D / 4][rows][4], so that a warp's rows are consecutive
+#pragma unroll
+                for (int c = 0; c < D / 4; ++c)
+                    *reinterpret_cast<uint4 *>(part + c * (4 * kChunkRows)) =
+                        make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
             }
             tc_fence_before();   // the accumulators are read; the next P says so to the issuing warp
             __syncwarp();
@@ -581,7 +600,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
             if (whole) {
                 const int c = lane % kChunks, row0 = quarter * 32 + lane / kChunks;
                 const int left = r.rows - (trow - row);
-                RowCursor at(r.row0 + trow - row + row0, kRowsPerCopy, p.group);
+                RowCursor at(r.row0 + trow - row + row0, kRowsPerCopy, p);
                 uint16_t *base = p.out + (static_cast<long long>(r.t0) * p.q_heads + sg.h * p.group) * D + 8 * c;
                 const int tstride = p.q_heads * D;
 #pragma unroll
@@ -592,7 +611,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                     at.next();
                 }
                 if (p.lse && trow < r.rows) {
-                    const int tok = rr / p.group;
+                    const int tok = p.by_group(rr);
                     p.lse[static_cast<long long>(r.t0 + tok) * p.q_heads + sg.h * p.group + rr - tok * p.group] =
                         l > 0.f ? (mref - kShift + log2f(l)) * 0.6931471805599453f : -INFINITY;
                 }
@@ -603,9 +622,13 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
             }
             if (threadIdx.x == 0 && is_last_part(sg))
                 write_meta<kChunkSetup>(p, sg, share.chunk);
-            cur ^= 1;
-            if (have)
-                load_q(segs[cur]);
+            leave(n);
+            n = next;
+            if (n >= 0) {
+                if (whole)
+                    start_q(segs[n % kSegs]);
+                land_q(segs[n % kSegs]);
+            }
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -682,9 +705,13 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                 wait(&q_full[s], qph >> s & 1u);
                 qph ^= 1u << s;
             };
-            while (next(segs[0])) {
-                const int ns = __shfl_sync(0xffffffffu, segs[0].r.rows > 128 ? 2 : 1, 0);
-                const int units = __shfl_sync(0xffffffffu, segs[0].units, 0);
+            for (int n = 0;; ++n) {
+                const Segment &sg = segment(n);
+                const int ns = __shfl_sync(0xffffffffu, sg.r.rows > 128 ? 2 : 1, 0);
+                const int units = __shfl_sync(0xffffffffu, sg.units, 0);
+                if (!ok || units == 0)
+                    break;
+                leave(n);
                 // (the streams' loops are unrolled: with constant streams a product issues
                 // in 50 cycles, with variable ones in 60, and this warp is on every tile's
                 // path)
@@ -740,7 +767,24 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                 mbar_wait(drain, 0, p.status);
             }
             __syncwarp();
-        } else if (warp >= kLoadWarpK) {
+        } else if (warp == kWalkWarp) {
+            // ================= segments =================
+            if (lane == 0) {
+                ChunkWalk walk;
+                walk.begin(share);
+                bool more = true;
+                for (int n = 0; more; ++n) {
+                    Segment &x = segs[n % kSegs];
+                    if (n >= kSegs && !mbar_wait(&seg_empty[n % kSegs], (n / kSegs - 1) & 1, p.status))
+                        break;
+                    more = walk.next(p, x);
+                    if (!more)
+                        x.units = 0;
+                    mbar_arrive(&seg_full[n % kSegs]);
+                }
+            }
+            __syncwarp();
+        } else {
             // ================= K tiles (warp 10) and V tiles (warp 11) =================
             const bool is_v = warp == kLoadWarpV;
             const int slots = is_v ? L::kVRing : L::kKRing;
@@ -762,10 +806,13 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
             };
             if (lane == 0 && p.box > 0)
                 prefetch_tmap(map);
-            const Segment &sg = segs[0];
-            while (ok && next(segs[0])) {
+            for (int n = 0; ok; ++n) {
+                const Segment &sg = segment(n);
                 const RowTile r = sg.r;
                 const int h = sg.h, units = sg.units, kb0 = (r.unit0 + sg.off) * kChunkKeys;
+                if (!ok || units == 0)
+                    break;
+                leave(n);
                 const uint16_t *base = static_cast<const uint16_t *>(is_v ? p.kv.v : p.kv.k) + h * p.kv.head_stride;
                 // page and slot / 8 of box `lane` of tile j (slot -1: nobody sees any of its
                 // keys).  Looked up one tile ahead, and not looked at before it is used: the
@@ -774,7 +821,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                     const int key = kb0 + j * kChunkKeys + lane * p.box;
                     if (lane >= nbox || j >= units || key >= r.hi || key + p.box <= r.lo)
                         return make_int2(0, -1);
-                    const int blk = static_cast<int>(static_cast<unsigned>(key) / static_cast<unsigned>(p.kv.page_size));
+                    const int blk = p.by_page(key);
                     return make_int2(p.kv.block_table[static_cast<long long>(r.b) * p.kv.blocks + blk],
                                      (key - blk * p.kv.page_size) >> 3);
                 };
@@ -824,7 +871,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
 #pragma unroll 1
                         for (int e = 0; e < kChunkKeys; e += 32) {
                             const int key = kb + e + lane;
-                            const long long place = key >= r.lo && key < r.hi ? key_offset(p.kv, r.b, key, p.status) : -1;
+                            const long long place = key >= r.lo && key < r.hi ? key_offset(p.kv, p.by_page, r.b, key, p.status) : -1;
 #pragma unroll 4
                             for (int c = 0; c < 32; c += kRowsPerCopy) {
                                 const long long o = __shfl_sync(0xffffffffu, place, c + sub);

@@ -173,7 +173,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
             const int key = key0 + j * kKeys + (p.same_page ? 0 : lane % kWarpKeys);
             if (j >= sg.units || key >= r.hi || (p.same_page ? key + kWarpKeys <= r.lo : key < r.lo))
                 return -1;
-            const long long off = key_offset(p.kv, r.b, key, p.status);
+            const long long off = key_offset(p.kv, p.by_page, r.b, key, p.status);
             return p.same_page && off >= 0 ? off + crow * p.kv.slot_stride : off;
         };
         auto load = [&](int j, long long off) {
@@ -206,7 +206,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
 
         // queries: 16 rows, zero past the tile
         for (int e = tid; e < kDecodeRows * kChunks; e += kDecThreads) {
-            const int row = e / kChunks, c = e % kChunks, rr = r.row0 + row, tok = rr / p.group;
+            const int row = e / kChunks, c = e % kChunks, rr = r.row0 + row, tok = p.by_group(rr);
             const bool in = row < r.rows;
             const uint16_t *src = p.q;
             if (in)
@@ -361,7 +361,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
         const int slot = part_slot(sg);
         // four finished values of a row to the output
         auto store = [&](int row, int c, float m, float l, const float4 &acc) {
-            const int rr = r.row0 + row, tok = rr / p.group;
+            const int rr = r.row0 + row, tok = p.by_group(rr);
             const long long at = static_cast<long long>(r.t0 + tok) * p.q_heads + sg.h * p.group + rr - tok * p.group;
             const float inv = l > 0.f ? 1.f / l : 0.f;
             *reinterpret_cast<uint2 *>(p.out + at * D + c) =

@@ -139,7 +139,7 @@ kv_append_kernel(const __grid_constant__ AppendParams p)
         sn[0] = w0.x; sn[1] = w0.y; sn[2] = w0.z; sn[3] = w0.w;
         sn[4] = w1.x; sn[5] = w1.y; sn[6] = w1.z; sn[7] = w1.w;
     }
-    const long long place = key_offset(kv, seq, pos, p.status);
+    const long long place = key_offset(kv, p.by_page, seq, pos, p.status);
 
     while (h < heads) {
         // the next head's chunks are under way while this one turns

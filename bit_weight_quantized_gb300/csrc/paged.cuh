@@ -82,10 +82,11 @@ __device__ __forceinline__ int seq_keys(const qmm_paged_kv &kv, int b, int *stat
 
 // Element offset of (sequence b, key, head 0) in the cache, or -1 (recorded) for a
 // page number out of range.  key is in [0, blocks * page_size).
-__device__ __forceinline__ long long key_offset(const qmm_paged_kv &kv, int b, int key, int *status)
+__device__ __forceinline__ long long key_offset(const qmm_paged_kv &kv, const FastDiv &by_page, int b, int key,
+                                                int *status)
 {
-    const unsigned blk = static_cast<unsigned>(key) / static_cast<unsigned>(kv.page_size);
-    const int slot = key - static_cast<int>(blk) * kv.page_size;
+    const int blk = by_page(key);
+    const int slot = key - blk * kv.page_size;
     const int page = kv.block_table[static_cast<long long>(b) * kv.blocks + blk];
     if (page < 0 || page >= kv.num_pages) {
         record_error(status, QMM_ERR_INDEX);
@@ -114,7 +115,7 @@ template <int ROWS, int KEYS>
 __device__ __forceinline__ RowTile row_tile(const AttnParams &p, int i)
 {
     RowTile r;
-    r.b = i / p.row_tiles;
+    r.b = p.by_tiles(i);
     r.row0 = (i - r.b * p.row_tiles) * ROWS;
     const int2 tn = seq_tokens(p.kv, r.b);
     r.t0 = tn.x;
@@ -125,8 +126,8 @@ __device__ __forceinline__ RowTile row_tile(const AttnParams &p, int i)
     r.lo = r.hi = r.unit0 = r.units = 0;
     if (r.rows == 0)
         return r;
-    const int first = r.kv - r.n + r.row0 / p.group;                       // position of the first row
-    const int last = r.kv - r.n + (r.row0 + r.rows - 1) / p.group;
+    const int first = r.kv - r.n + p.by_group(r.row0);                     // position of the first row
+    const int last = r.kv - r.n + p.by_group(r.row0 + r.rows - 1);
     r.hi = p.causal ? min(r.kv, max(0, last + 1)) : r.kv;
     r.lo = p.window > 0 ? min(r.hi, max(0, first - p.window + 1)) : 0;
     r.unit0 = r.lo / KEYS;
@@ -140,7 +141,7 @@ __device__ __forceinline__ int2 row_keys(const AttnParams &p, const RowTile &r, 
 {
     if (row >= r.row0 + r.rows)
         return make_int2(0, -1);
-    const int pos = r.kv - r.n + row / p.group;
+    const int pos = r.kv - r.n + p.by_group(row);
     return make_int2(p.window > 0 ? max(0, pos - p.window + 1) : 0, p.causal ? min(r.kv - 1, pos) : r.kv - 1);
 }
 
@@ -193,8 +194,9 @@ __device__ __forceinline__ void find_share(const AttnParams &p, long long *red, 
     const int per = (tiles + THREADS - 1) / THREADS;
     const int i0 = min(tiles, tid * per), i1 = min(tiles, i0 + per);
     long long sum = 0;
+    RowTile r;
     for (int i = i0; i < i1; ++i) {
-        const RowTile r = row_tile<ROWS, KEYS>(p, i);
+        r = row_tile<ROWS, KEYS>(p, i);
         sum += static_cast<long long>(r.units ? SETUP + r.units : 0) * p.kv.kv_heads;
         if (r.row0 == 0 && static_cast<long long>(r.n) * p.group > static_cast<long long>(p.row_tiles) * ROWS)
             record_error(p.status, QMM_ERR_INDEX);   // more new tokens than max_q
@@ -227,7 +229,8 @@ __device__ __forceinline__ void find_share(const AttnParams &p, long long *red, 
     if (at < total && before <= at && at < before + sum) {
         long long start = before;
         for (int i = i0; i < i1; ++i) {
-            const RowTile r = row_tile<ROWS, KEYS>(p, i);
+            if (per > 1)
+                r = row_tile<ROWS, KEYS>(p, i);
             const int len = r.units ? SETUP + r.units : 0;
             const long long all = static_cast<long long>(len) * p.kv.kv_heads;
             if (at < start + all) {

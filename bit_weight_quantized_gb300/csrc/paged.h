@@ -10,6 +10,33 @@
 
 namespace qmm {
 
+// Division of 0 <= n < 2^31 by a number known at launch, as a high product and a shift
+// (Granlund and Montgomery, "Division by invariant integers using multiplication"): a
+// division by a variable is some 30 dependent instructions.  l = ceil(log2 d), mul =
+// ceil(2^(31 + l) / d) < 2^32: the product's error, n / 2^(31 + l), is below 1 / d.
+struct FastDiv {
+    uint32_t mul, shift, one;   // one: d = 1
+#ifdef __CUDACC__
+    __device__ __forceinline__ int operator()(int n) const
+    {
+        return one ? n : static_cast<int>(__umulhi(static_cast<uint32_t>(n), mul) >> shift);
+    }
+#endif
+};
+
+inline FastDiv fast_div(int d)
+{
+    FastDiv f = {0, 0, d == 1};
+    if (d > 1) {
+        int l = 1;
+        while ((1LL << l) < d)
+            ++l;
+        f.mul = static_cast<uint32_t>(((1ULL << (31 + l)) + static_cast<uint64_t>(d) - 1) / static_cast<uint64_t>(d));
+        f.shift = static_cast<uint32_t>(l - 1);
+    }
+    return f;
+}
+
 struct AppendParams {
     qmm_paged_kv kv;
     const uint16_t *k, *v, *q;
@@ -18,6 +45,7 @@ struct AppendParams {
     int *status;
     long long k_stride, v_stride, q_stride;
     int q_heads, rot, rope_len, interleaved;
+    FastDiv by_page;
 };
 
 cudaError_t launch_kv_append(const AppendParams &p, int num_sms, cudaStream_t stream);
@@ -41,6 +69,7 @@ struct AttnParams {
     int q_heads, group;            // query heads, query heads per key head
     int causal, window;
     int row_tiles;                 // row tiles per sequence (of the longest one)
+    FastDiv by_group, by_tiles, by_page;   // divisions by group, row_tiles, page_size
     int whole;                     // every item in one cluster: no partial results
     int cluster;                   // blocks per cluster (decode kernel, whole items)
     int same_page;                 // every warp tile of the decode kernel lies in one page
