@@ -215,10 +215,27 @@ size_t scratch_bytes(bool few, int head_dim, int num_sms)
     return g * 32 + 2 * g * rows * (head_dim + 2) * 4;
 }
 
-// Work a block takes at least, in units: below this a split costs more (a second kernel,
-// the partial results) than the longer walk.
+// Work a block takes at least, in units: below this a split costs more (a second
+// kernel, the partial results) than the longer walk.
 constexpr int kMinDecodeUnits = 5, kMinChunkUnits = 6;
+
+// Units a cluster's block takes at most (one token over 8000 keys: 18.9 us at 16 units,
+// 12.3 split over all blocks and joined).
 constexpr int kClusterUnits = 8;
+
+// Blocks per item of the decode kernel where every item gets a cluster (or block) of
+// its own: items short enough for one block, or a cluster per item where all of them run
+// at once and each block's stretch is short enough to cost less than the joining
+// kernel.  0: the axis is split over all blocks.
+int decode_cluster(long long items, long long longest, int grid)
+{
+    if (longest + kDecodeSetup <= kMinDecodeUnits && items <= 0x7fffffff)
+        return 1;
+    for (int c = kMaxCluster; c > 1; c /= 2)
+        if (items * c <= grid && (longest + c - 1) / c <= kClusterUnits)
+            return c;
+    return 0;
+}
 
 }  // namespace
 
@@ -229,33 +246,34 @@ size_t attn_workspace_bytes(int q_heads, int kv_heads, int head_dim, int max_q, 
 
 cudaError_t attn_dispatch(AttnParams &p, int max_q, long long max_kv, void *workspace, int num_sms, cudaStream_t stream)
 {
-    const bool few = few_rows(max_q, p.group);
-    const int rows = few ? kDecodeRows : kChunkRows, keys = few ? decode_keys(p.kv.head_dim) : kChunkKeys;
+    const long long most = static_cast<long long>(p.kv.blocks) * p.kv.page_size, q_rows = static_cast<long long>(max_q) * p.group;
+    if (max_kv <= 0 || max_kv > most)
+        max_kv = most;
+    // the decode kernel's items and the longest one's units
+    const int dkeys = decode_keys(p.kv.head_dim);
+    const long long dtiles = (q_rows + kDecodeRows - 1) / kDecodeRows;
+    const long long ditems = p.kv.batch * dtiles * p.kv.kv_heads, dunits = (max_kv + dkeys - 1) / dkeys;
+    // more rows go to it too where its items, sixteen rows each, all run at once: it
+    // starts faster and needs no join (64 tokens over 1000 keys 13.7 us against the chunk
+    // kernel's 18.9, 128 over 128 6.3 against 8.7; but 4 x 50 over 200, 416 items on 304
+    // blocks, 13.9 against 9.6, and 5 over 4000 of 32 sequences, split, 243 against 94)
+    const int dgrid = attn_grid(true, num_sms);
+    const int cluster = decode_cluster(ditems, dunits, dgrid);
+    const bool few = few_rows(max_q, p.group) || (cluster > 0 && ditems * cluster <= dgrid);
+    const int rows = few ? kDecodeRows : kChunkRows, keys = few ? dkeys : kChunkKeys;
     const int setup = few ? kDecodeSetup : kChunkSetup;
-    p.row_tiles = static_cast<int>((static_cast<long long>(max_q) * p.group + rows - 1) / rows);
+    p.row_tiles = static_cast<int>((q_rows + rows - 1) / rows);
     p.by_group = fast_div(p.group);
     p.by_tiles = fast_div(p.row_tiles);
     p.by_page = fast_div(p.kv.page_size);
+    p.same_page = p.kv.page_size % (keys / 4) == 0;   // four warps per decode block
     p.min_chunk = few ? kMinDecodeUnits : kMinChunkUnits;
     const long long items = static_cast<long long>(p.kv.batch) * p.row_tiles * p.kv.kv_heads;
-    const long long most = static_cast<long long>(p.kv.blocks) * p.kv.page_size;
-    if (max_kv <= 0 || max_kv > most)
-        max_kv = most;
-    const long long longest = (max_kv + keys - 1) / keys;      // units of the longest item
-    // one block per item where no item is long enough to be split
-    p.whole = longest + setup <= p.min_chunk && items <= 0x7fffffff;
-    p.cluster = 1;
-    p.same_page = p.kv.page_size % (keys / 4) == 0;   // four warps per decode block
+    const long long longest = (max_kv + keys - 1) / keys;
+    // one block or cluster per item where no item is long enough to be split over more
+    p.cluster = few && cluster > 0 ? cluster : 1;
+    p.whole = few ? cluster > 0 : longest + setup <= p.min_chunk && items <= 0x7fffffff;
     int grid = attn_grid(few, num_sms);
-    // a cluster of blocks per item where all of them run at once and each block's
-    // stretch is short enough to cost less than the joining kernel
-    if (few && !p.whole)
-        for (int c = kMaxCluster; c > 1; c /= 2)
-            if (items * c <= grid && (longest + c - 1) / c <= kClusterUnits) {
-                p.cluster = c;
-                p.whole = 1;
-                break;
-            }
     if (p.whole)
         grid = static_cast<int>(items) * p.cluster;
     else if (items * (longest + setup) < static_cast<long long>(grid) * p.min_chunk)
@@ -270,8 +288,7 @@ cudaError_t attn_dispatch(AttnParams &p, int max_q, long long max_kv, void *work
     cudaError_t e = few ? launch_attn_decode(p, grid, stream) : launch_attn_chunk(p, grid, stream);
     if (e != cudaSuccess || p.whole)
         return e;
-    const long long max_rows = std::min(static_cast<long long>(rows), static_cast<long long>(max_q) * p.group);
-    return launch_attn_join(p, grid, few, static_cast<int>(max_rows), stream);
+    return launch_attn_join(p, grid, few, static_cast<int>(std::min(static_cast<long long>(rows), q_rows)), stream);
 }
 
 }  // namespace qmm

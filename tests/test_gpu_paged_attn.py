@@ -28,6 +28,10 @@ def route(q, request, monkeypatch):
 
 
 def check(q, bt, scale=None, causal=True, window=0, max_kv=None, max_q=None, query=None):
+    """One call, and where the lengths leave the choice, one with a max_q so large that the
+    chunk kernel runs: both against the plain form."""
+    if max_q is None and max(bt.ql) > 1:
+        check(q, bt, scale, causal, window, max_kv, 4096, query)
     out, lse = q.qmm_paged_attn(bt.q if query is None else query, *bt.args(),
                                 max(bt.ql) if max_q is None else max_q, max(bt.kl) if max_kv is None else max_kv,
                                 scale=scale, causal=causal, window=window, return_lse=True)
