@@ -219,6 +219,12 @@ size_t scratch_bytes(bool few, int head_dim, int num_sms)
 // kernel, the partial results) than the longer walk.
 constexpr int kMinDecodeUnits = 5, kMinChunkUnits = 6;
 
+// Work of the longest item (setup and units) up to which blocks of the chunk kernel take
+// whole items: no joining kernel, against blocks of unequal work by up to one item.  8
+// sequences of up to 300 tokens over 400 keys: 26.9 us, split 31.6; 16 of 100 over 600:
+// 30.0, split 33.8.
+constexpr int kUnsplitWork = 10;
+
 // Units a cluster's block takes at most (one token over 8000 keys: 18.9 us at 16 units,
 // 12.3 split over all blocks and joined).
 constexpr int kClusterUnits = 8;
@@ -269,13 +275,18 @@ cudaError_t attn_dispatch(AttnParams &p, int max_q, long long max_kv, void *work
     p.same_page = p.kv.page_size % (keys / 4) == 0;   // four warps per decode block
     p.min_chunk = few ? kMinDecodeUnits : kMinChunkUnits;
     const long long items = static_cast<long long>(p.kv.batch) * p.row_tiles * p.kv.kv_heads;
-    const long long longest = (max_kv + keys - 1) / keys;
+    long long longest = (max_kv + keys - 1) / keys;
+    if (p.window > 0)   // the keys that a tile's tokens see between them
+        longest = std::min(longest, (static_cast<long long>(p.window) + rows / p.group + 1) / keys + 2);
     // one block or cluster per item where no item is long enough to be split over more
     p.cluster = few && cluster > 0 ? cluster : 1;
-    p.whole = few ? cluster > 0 : longest + setup <= p.min_chunk && items <= 0x7fffffff;
     int grid = attn_grid(few, num_sms);
-    if (p.whole)
+    p.whole = few ? cluster > 0 : items <= grid ? longest + setup <= p.min_chunk : longest + setup <= kUnsplitWork;
+    p.unsplit = !few && p.whole && items > grid;
+    if (p.whole && !p.unsplit)
         grid = static_cast<int>(items) * p.cluster;
+    else if (p.unsplit)
+        p.min_chunk = 1;
     else if (items * (longest + setup) < static_cast<long long>(grid) * p.min_chunk)
         grid = static_cast<int>((items * (longest + setup) + p.min_chunk - 1) / p.min_chunk);
     uint8_t *ws = static_cast<uint8_t *>(workspace);

@@ -152,7 +152,8 @@ __device__ __forceinline__ int2 row_keys(const AttnParams &p, const RowTile &r, 
 // chunk), chunk = max(min_chunk, total / grid rounded up), so every block has the
 // same work however ragged the batch is.  An item that crosses a block's border
 // leaves partial results (at most two per block) that a second kernel joins (attn.cu).
-// The split depends on the lengths alone, so results are the same run to run.
+// The split depends on the lengths alone, so results are the same run to run.  With
+// p.unsplit a block takes the items that start in its stretch, whole.
 struct Share {
     long long at, end;       // the block's stretch
     long long chunk;
@@ -174,7 +175,7 @@ template <int ROWS, int KEYS, int SETUP, int THREADS>
 __device__ __forceinline__ void find_share(const AttnParams &p, long long *red, Share *out)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (p.whole) {   // cluster (or block) c holds item c
+    if (p.whole && !p.unsplit) {   // cluster (or block) c holds item c
         if (tid == 0) {
             const int item = blockIdx.x / p.cluster, i = item / p.kv.kv_heads;
             const RowTile r = row_tile<ROWS, KEYS>(p, i);
@@ -211,7 +212,7 @@ __device__ __forceinline__ void find_share(const AttnParams &p, long long *red, 
     if (lane == 31)
         red[warp] = incl;
     if (tid == 0)
-        out->at = out->end = 0;
+        out->at = out->end = out->start = 0;
     __syncthreads();
     long long base = 0, total = 0;
 #pragma unroll
@@ -272,20 +273,42 @@ struct Walk {
         h = s.h;
         r = s.r;
     }
+    // on to the next item, which starts len further on
+    __device__ __forceinline__ bool advance(const AttnParams &p, int len)
+    {
+        start += len;
+        if (++h == p.kv.kv_heads) {
+            h = 0;
+            do {
+                if (++i >= p.kv.batch * p.row_tiles)
+                    return false;
+                r = row_tile<ROWS, KEYS>(p, i);
+            } while (r.units == 0);
+        }
+        return true;
+    }
     __device__ __forceinline__ bool next(const AttnParams &p, Segment &s)
     {
+        if (p.unsplit) {
+            while (at < end && start < at)       // began in an earlier block
+                if (!advance(p, SETUP + r.units))
+                    at = end;
+            if (at >= end || start >= end)
+                return false;
+            s.r = r;
+            s.h = h;
+            s.off = 0;
+            s.units = r.units;
+            s.start = start;
+            if (!advance(p, SETUP + r.units))
+                at = end;                        // that was the last item
+            return true;
+        }
         while (at < end) {
             const int len = SETUP + r.units;
-            if (at >= start + len) {   // on to the next item
-                start += len;
-                if (++h == p.kv.kv_heads) {
-                    h = 0;
-                    do {
-                        if (++i >= p.kv.batch * p.row_tiles)
-                            return false;   // not reached: the stretch ahead belongs to some tile
-                        r = row_tile<ROWS, KEYS>(p, i);
-                    } while (r.units == 0);
-                }
+            if (at >= start + len) {
+                if (!advance(p, len))
+                    return false;   // not reached: the stretch ahead belongs to some tile
                 continue;
             }
             const long long to = min(end, start + len);

@@ -70,7 +70,8 @@ struct AttnParams {
     int causal, window;
     int row_tiles;                 // row tiles per sequence (of the longest one)
     FastDiv by_group, by_tiles, by_page;   // divisions by group, row_tiles, page_size
-    int whole;                     // every item in one cluster: no partial results
+    int whole;                     // every item in one cluster or block: no partial results
+    int unsplit;                   // whole items, several per block (chunk kernel)
     int cluster;                   // blocks per cluster (decode kernel, whole items)
     int same_page;                 // every warp tile of the decode kernel lies in one page
     int min_chunk;                 // work a block takes at least, in units
