@@ -490,7 +490,8 @@ def qmm_kv_append(k, v, k_cache, v_cache, block_table, cu_q, kv_len, q=None, q_o
             return r
         if r > 0:
             raise QmmError(r, "qmm_kv_append")
-    rows = [("k", k, k_cache.shape[2]), ("v", v, k_cache.shape[2])] + ([("q", q, None)] if q is not None else [])
+    hk = k_cache.shape[2] if k_cache.dim() == 4 else None
+    rows = [("k", k, hk), ("v", v, hk)] + ([("q", q, None)] if q is not None else [])
     _paged_checks(k_cache, v_cache, block_table, cu_q, kv_len, rows)
     T, hk, D = k.shape
     rot = rope_len = heads = 0

@@ -248,7 +248,12 @@ static qmm_status check_paged(const qmm_paged_kv *kv)
         return QMM_ERR_UNSUPPORTED;
     if (kv->head_dim != 64 && kv->head_dim != 128)
         return QMM_ERR_UNSUPPORTED;
-    if (kv->page_stride % 8 || kv->slot_stride % 8 || kv->head_stride % 8)
+    // a stride counts only where there is more than one of what it separates
+    if ((kv->num_pages > 1 && kv->page_stride < 0) || (kv->page_size > 1 && kv->slot_stride < 0) ||
+        (kv->kv_heads > 1 && kv->head_stride < 0))
+        return QMM_ERR_SHAPE;
+    if ((kv->num_pages > 1 && kv->page_stride % 8) || (kv->page_size > 1 && kv->slot_stride % 8) ||
+        (kv->kv_heads > 1 && kv->head_stride % 8))
         return QMM_ERR_ALIGN;
     if (kv->batch == 0 || kv->tokens == 0)
         return QMM_OK;
@@ -690,7 +695,9 @@ qmm_status qmm_kv_append(const qmm_paged_kv *kv, const void *k, int64_t k_stride
         return st;
     if (rot < 0 || rot > kv->head_dim || rot % 16 || rope_len < 0 || q_heads < 0)
         return QMM_ERR_SHAPE;
-    if (k_stride % 8 || v_stride % 8 || (q && q_stride % 8))
+    if (kv->tokens > 1 && (k_stride < 0 || v_stride < 0 || (q && q_stride < 0)))
+        return QMM_ERR_SHAPE;
+    if (kv->tokens > 1 && (k_stride % 8 || v_stride % 8 || (q && q_stride % 8)))
         return QMM_ERR_ALIGN;
     if (kv->batch == 0 || kv->tokens == 0)
         return QMM_OK;
@@ -739,9 +746,9 @@ qmm_status qmm_paged_attn(const qmm_paged_kv *kv, const void *q, int64_t q_strid
     if (st != QMM_OK)
         return st;
     if (q_heads < 1 || q_heads % kv->kv_heads || window < 0 || (window > 0 && !causal) || max_q < 0 || max_kv < 0 ||
-        !(scale > 0.f) || !(scale <= 3.0e38f))
+        !(scale > 0.f) || !(scale <= 2.0e38f) || (kv->tokens > 1 && q_stride < 0))   // scale log2(e) is finite
         return QMM_ERR_SHAPE;
-    if (q_stride % 8)
+    if (kv->tokens > 1 && q_stride % 8)
         return QMM_ERR_ALIGN;
     if (kv->batch == 0 || kv->tokens == 0 || max_q == 0)
         return QMM_OK;

@@ -876,7 +876,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                             for (int c = 0; c < 32; c += kRowsPerCopy) {
                                 const long long o = __shfl_sync(0xffffffffu, place, c + sub);
                                 cp_async16_or_zero(smem_u32(tile + kv_addr<D>(e + c + sub, chunk)),
-                                                   base + (o >= 0 ? o : 0) + chunk * 8, o >= 0);
+                                                   o >= 0 ? base + o + chunk * 8 : p.q, o >= 0);
                             }
                         }
                         cp_async_commit();

@@ -182,13 +182,13 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
                 const int kb = key0 + j * kKeys;
                 const bool inside = off >= 0 && kb >= r.lo && kb + kWarpKeys <= r.hi;
                 const long long step = kRowsPerCopy * p.kv.slot_stride;
-                long long e = (off >= 0 ? off : 0) + cchunk * 8;
+                long long e = off + cchunk * 8;
 #pragma unroll
                 for (int c = 0; c < kCopies; ++c) {
                     const int row = c * kRowsPerCopy + crow, key = kb + row;
                     const bool ok = inside || (off >= 0 && key >= r.lo && key < r.hi);
-                    cp_async16_or_zero(dst + tile_addr<D>(row, cchunk), kbase + (ok ? e : 0), ok);
-                    cp_async16_or_zero(dst + L::kTile + tile_addr<D>(row, cchunk), vbase + (ok ? e : 0), ok);
+                    cp_async16_or_zero(dst + tile_addr<D>(row, cchunk), ok ? kbase + e : p.q, ok);
+                    cp_async16_or_zero(dst + L::kTile + tile_addr<D>(row, cchunk), ok ? vbase + e : p.q, ok);
                     e += step;
                 }
                 return;
@@ -198,9 +198,9 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
                 const int row = c * kRowsPerCopy + crow;
                 const long long o = __shfl_sync(0xffffffffu, off, row);
                 const bool ok = o >= 0;
-                const long long e = (ok ? o : 0) + cchunk * 8;
-                cp_async16_or_zero(dst + tile_addr<D>(row, cchunk), kbase + e, ok);
-                cp_async16_or_zero(dst + L::kTile + tile_addr<D>(row, cchunk), vbase + e, ok);
+                const long long e = o + cchunk * 8;
+                cp_async16_or_zero(dst + tile_addr<D>(row, cchunk), ok ? kbase + e : p.q, ok);
+                cp_async16_or_zero(dst + L::kTile + tile_addr<D>(row, cchunk), ok ? vbase + e : p.q, ok);
             }
         };
 

@@ -202,6 +202,27 @@ def test_query_views_and_given_buffers(q, route):
     assert torch.equal(a, out)
 
 
+# a size of one may come with any stride
+@pytest.mark.parametrize("n", [1, 40])
+def test_strides_of_single_things(q, n):
+    bt = Batch([n], [n + 100], 4, 1, 64, seed=4)
+    want = check(q, bt)
+    k, v = (torch.as_strided(t, t.shape, (t.stride(0), t.stride(1), 5, 1), t.storage_offset()) for t in (bt.k_cache, bt.v_cache))
+    bt.k_cache, bt.v_cache = k, v
+    assert torch.equal(check(q, bt), want)
+
+
+# a cache without a page holds no keys: nothing is read
+@pytest.mark.parametrize("n", [1, 40])
+def test_empty_pool(q, n):
+    bt = Batch([n], [0], 4, 2, 64, seed=4)
+    none = torch.empty(0, 16, 2, 64, dtype=bt.dt, device="cuda")
+    for max_q in (n, 4096):
+        out = q.qmm_paged_attn(bt.q, none, none, bt.table, bt.cu_q, bt.kv_len, max_q, 0)
+        torch.cuda.synchronize()
+        assert (out == 0).all() and q.qmm_device_status() == 0
+
+
 # the same batch, whatever the caller knows of its lengths; run to run equal
 @pytest.mark.parametrize("n", [1, 60])
 def test_hints_and_repeats(q, n):

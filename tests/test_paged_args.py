@@ -25,6 +25,10 @@ KV_CASES = [
     (dict(batch=-1), SHAPE), (dict(tokens=-1), SHAPE), (dict(num_pages=-1), SHAPE), (dict(page_size=0), SHAPE),
     (dict(blocks=-1), SHAPE), (dict(kv_heads=0), SHAPE), (dict(head_dim=0), SHAPE),
     (dict(head_dim=96), UNSUPPORTED), (dict(dtype=2), UNSUPPORTED),
+    (dict(page_stride=-8), SHAPE), (dict(slot_stride=-8), SHAPE), (dict(head_stride=-8), SHAPE),
+    # a stride of one thing is not looked at (valid calls stop at the missing device)
+    (dict(num_pages=1, page_stride=3), DEVICE), (dict(page_size=1, slot_stride=3), DEVICE),
+    (dict(kv_heads=1, head_stride=-3), DEVICE),
     (dict(page_stride=2044), ALIGN), (dict(slot_stride=4), ALIGN), (dict(head_stride=1), ALIGN),
     (dict(k=None), NULL), (dict(v=None), NULL), (dict(block_table=None), NULL), (dict(cu_q=None), NULL),
     (dict(kv_len=None), NULL), (dict(k=A + 8), ALIGN), (dict(v=A + 2), ALIGN), (dict(block_table=A + 2), ALIGN),
@@ -32,7 +36,7 @@ KV_CASES = [
 ]
 APPEND_CASES = [
     (dict(rot=8), SHAPE), (dict(rot=-16), SHAPE), (dict(rot=144), SHAPE), (dict(rope_len=-1), SHAPE),
-    (dict(q_heads=-1), SHAPE), (dict(k_stride=1), ALIGN), (dict(v_stride=4), ALIGN), (dict(q_stride=12), ALIGN),
+    (dict(q_heads=-1), SHAPE), (dict(k_stride=-8), SHAPE), (dict(q_stride=-8), SHAPE), (dict(k_stride=1), ALIGN), (dict(v_stride=4), ALIGN), (dict(q_stride=12), ALIGN),
     (dict(k=None), NULL), (dict(v=None), NULL), (dict(cos_sin=None), NULL), (dict(q=None), NULL),
     (dict(q_out=None), NULL), (dict(k=A + 8), ALIGN), (dict(v=A + 8), ALIGN), (dict(q=A + 8), ALIGN),
     (dict(q_out=A + 8), ALIGN), (dict(cos_sin=A + 4), ALIGN), (dict(cos_sin=None, rot=0), DEVICE),
@@ -41,7 +45,7 @@ APPEND_CASES = [
 ATTN_CASES = [
     (dict(q_heads=7), SHAPE), (dict(q_heads=0), SHAPE), (dict(window=-1), SHAPE), (dict(window=4, causal=0), SHAPE),
     (dict(max_q=-1), SHAPE), (dict(max_kv=-1), SHAPE), (dict(scale=0.0), SHAPE), (dict(scale=-1.0), SHAPE),
-    (dict(scale=float("nan")), SHAPE), (dict(scale=float("inf")), SHAPE), (dict(q_stride=20), ALIGN),
+    (dict(scale=float("nan")), SHAPE), (dict(scale=float("inf")), SHAPE), (dict(scale=3e38), SHAPE), (dict(q_stride=-8), SHAPE), (dict(q_stride=20), ALIGN),
     (dict(q=None), NULL), (dict(out=None), NULL), (dict(workspace=None), NULL), (dict(q=A + 4), ALIGN),
     (dict(out=A + 8), ALIGN), (dict(workspace=A + 8), ALIGN), (dict(lse=A + 2), ALIGN), (dict(max_q=0), 0),
 ]
