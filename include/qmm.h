@@ -36,7 +36,8 @@
  *    it.  Nothing in the library aborts, throws across the ABI or traps.
  *  - Outputs are written with round-to-nearest-even from fp32.
  *  - Overlap of consecutive calls.  qmm_gemv, qmm_gemm, qmm_w4a8, qmm_w8a8,
- *    qmm_gemv_float and qmm_quantize_act launch with programmatic dependent
+ *    qmm_gemv_float, qmm_quantize_act, qmm_kv_append and qmm_paged_attn launch with
+ *    programmatic dependent
  *    launch and let the next kernel on the stream start as soon as they start
  *    themselves.  The matmul calls read their weight arguments (packed / w4 /
  *    w8, scales / ws, zeros) BEFORE they wait for the preceding kernel;
