@@ -225,22 +225,32 @@ constexpr int kMinDecodeUnits = 5, kMinChunkUnits = 6;
 // 30.0, split 33.8.
 constexpr int kUnsplitWork = 10;
 
-// Units a cluster's block takes at most (one token over 8000 keys: 18.9 us at 16 units,
-// 12.3 split over all blocks and joined).
-constexpr int kClusterUnits = 8;
+// Units a block of a cluster takes at most, of four warps and (wide) of eight, twice the
+// keys: one token over 8000 keys 18.9 us at 16 units of four warps, 12.3 split over all
+// blocks and joined; four over 4000, 8 units, 12.9 against 14.6.
+constexpr int kClusterUnits = 8, kWideUnits = 4;
 
-// Blocks per item of the decode kernel where every item gets a cluster (or block) of
-// its own: items short enough for one block, or a cluster per item where all of them run
-// at once and each block's stretch is short enough to cost less than the joining
-// kernel.  0: the axis is split over all blocks.
-int decode_cluster(long long items, long long longest, int grid)
+// Blocks per item of the decode kernel, and their warps, where every item gets a cluster
+// (or block) of its own: clusters of the largest size that all run at once (eight
+// clusters of eight on 64 SMs do, sixteen on 128 do not: 12.0 us for 24 rows over 1000
+// keys, 7.9 in sixteen of four), each block's stretch short enough to cost less than the
+// joining kernel.  Eight warps a block where an SM is free for each: one token over 200
+// keys 5.5 us against 6.4 with four, over 2000 7.1 against 8.2.  Items short enough for
+// one block go there however many they are.  0: the axis is split over all blocks.
+int decode_cluster(const AttnParams &p, long long items, long long max_kv, int num_sms, int *warps)
 {
-    if (longest + kDecodeSetup <= kMinDecodeUnits && items <= 0x7fffffff)
-        return 1;
-    for (int c = kMaxCluster; c > 1; c /= 2)
-        if (items * c <= grid && (longest + c - 1) / c <= kClusterUnits)
-            return c;
-    return 0;
+    const bool bf16 = p.kv.dtype == QMM_BF16;
+    for (*warps = 8; *warps >= 4; *warps /= 2) {
+        const int keys = decode_keys(p.kv.head_dim, *warps), most = *warps == 8 ? kWideUnits : kClusterUnits;
+        const long long units = (max_kv + keys - 1) / keys, blocks = *warps == 8 ? num_sms : kDecodeBlocksPerSm * num_sms;
+        for (int c = kMaxCluster; c >= 1; c /= 2)
+            if (items * c <= blocks && (c == 1 || c / 2 < units) && (units + c - 1) / c <= most &&
+                (c == 1 || items <= attn_decode_clusters(p.kv.head_dim, bf16, *warps, c)))
+                return c;
+    }
+    *warps = 4;
+    const int keys = decode_keys(p.kv.head_dim, 4);
+    return (max_kv + keys - 1) / keys + kDecodeSetup <= kMinDecodeUnits && items <= 0x7fffffff ? 1 : 0;
 }
 
 }  // namespace
@@ -255,24 +265,23 @@ cudaError_t attn_dispatch(AttnParams &p, int max_q, long long max_kv, void *work
     const long long most = static_cast<long long>(p.kv.blocks) * p.kv.page_size, q_rows = static_cast<long long>(max_q) * p.group;
     if (max_kv <= 0 || max_kv > most)
         max_kv = most;
-    // the decode kernel's items and the longest one's units
-    const int dkeys = decode_keys(p.kv.head_dim);
-    const long long dtiles = (q_rows + kDecodeRows - 1) / kDecodeRows;
-    const long long ditems = p.kv.batch * dtiles * p.kv.kv_heads, dunits = (max_kv + dkeys - 1) / dkeys;
+    // the decode kernel's items
+    const long long dtiles = (q_rows + kDecodeRows - 1) / kDecodeRows, ditems = p.kv.batch * dtiles * p.kv.kv_heads;
+    int warps;
+    const int cluster = decode_cluster(p, ditems, max_kv, num_sms, &warps);
     // more rows go to it too where its items, sixteen rows each, all run at once: it
-    // starts faster and needs no join (64 tokens over 1000 keys 13.7 us against the chunk
+    // starts faster and needs no join (64 tokens over 1000 keys 13.6 us against the chunk
     // kernel's 18.9, 128 over 128 6.3 against 8.7; but 4 x 50 over 200, 416 items on 304
     // blocks, 13.9 against 9.6, and 5 over 4000 of 32 sequences, split, 243 against 94)
-    const int dgrid = attn_grid(true, num_sms);
-    const int cluster = decode_cluster(ditems, dunits, dgrid);
-    const bool few = few_rows(max_q, p.group) || (cluster > 0 && ditems * cluster <= dgrid);
-    const int rows = few ? kDecodeRows : kChunkRows, keys = few ? dkeys : kChunkKeys;
+    const bool few = few_rows(max_q, p.group) || (cluster > 0 && ditems * cluster <= kDecodeBlocksPerSm * num_sms);
+    const int rows = few ? kDecodeRows : kChunkRows, keys = few ? decode_keys(p.kv.head_dim, warps) : kChunkKeys;
     const int setup = few ? kDecodeSetup : kChunkSetup;
     p.row_tiles = static_cast<int>((q_rows + rows - 1) / rows);
     p.by_group = fast_div(p.group);
     p.by_tiles = fast_div(p.row_tiles);
     p.by_page = fast_div(p.kv.page_size);
-    p.same_page = p.kv.page_size % (keys / 4) == 0;   // four warps per decode block
+    p.warps = warps;
+    p.same_page = p.kv.page_size % (decode_keys(p.kv.head_dim, 4) / 4) == 0;
     p.min_chunk = few ? kMinDecodeUnits : kMinChunkUnits;
     const long long items = static_cast<long long>(p.kv.batch) * p.row_tiles * p.kv.kv_heads;
     long long longest = (max_kv + keys - 1) / keys;

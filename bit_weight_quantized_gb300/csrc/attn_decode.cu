@@ -6,44 +6,44 @@
 //
 // Bound by reading K and V once from HBM: every key costs 4 D bytes and at most
 // 16 * 4 D flops, far below the tensor cores' ratio, so mma.sync is enough and the
-// work is to keep reads in flight.  Each of a block's four warps walks its own 16
-// keys (D = 64: 32) of every unit with its own ring of asynchronous copies (8 KB of K
-// and V a stage), running maximum, sum and 16 x D fp32 output in registers: no
-// barrier and no exchange between warps until the segment ends.  Two blocks per SM
-// keep 128 KB in flight.  At the end of a segment the
-// warps' results meet in shared memory.
+// work is to keep reads in flight.  Each of a block's warps walks its own 16 keys
+// (D = 64: 32) of every unit with its own ring of asynchronous copies (8 KB of K and V
+// a stage), running maximum, sum and 16 x D fp32 output in registers: no barrier and
+// no exchange between warps until the segment ends, when their results meet in shared
+// memory.  Two blocks of four warps, or one of eight, per SM keep 128 KB in flight.
 //
 // Long axes are split over all blocks (find_share) and joined by a second kernel
 // (attn.cu).  Short ones, where that kernel's 3.5 us would count, go to a cluster of
-// up to eight blocks per item, which joins its parts through its blocks' shared memory.
+// up to eight blocks per item, which joins its parts through its blocks' shared memory;
+// blocks of eight warps halve its walk where an SM is free for each.
 //
 // The running maximum is replaced only when it grows by more than 2^8 (the scale
 // factors stay within fp32 and fp16 range either way), so the output is rescaled
 // a few times per segment rather than in every tile.  fp16 weights are scaled by
 // 2^7: 2^(s' - m + 7) <= 2^15 stays finite and weights down to 2^-21 of the maximum
 // keep all their bits (fp16 loses bits below 2^-14).
+#include <atomic>
+
 #include "paged.cuh"
 
 namespace qmm {
 
 namespace {
 
-constexpr int kDecWarps = 4;
-constexpr int kDecThreads = 32 * kDecWarps;
 constexpr float kGrow = 8.f;                         // log2 of the growth that replaces the maximum
 
-template <int D>
+template <int D, int WARPS>
 struct DecLayout {
-    static constexpr int kKeys = decode_keys(D);                          // keys per unit
-    static constexpr int kWarpKeys = kKeys / kDecWarps;                   // a warp's keys of a unit
+    static constexpr int kWarpKeys = decode_keys(D, 4) / 4;               // a warp's keys of a unit
+    static constexpr int kKeys = decode_keys(D, WARPS);                   // keys per unit
     static constexpr int kTile = kWarpKeys * D * 2;                       // their K or V, 4 KB
-    static constexpr int kStages = 3;                                     // 96 KB of rings per block
+    static constexpr int kStages = 3;                                     // 24 KB of rings per warp
     static constexpr int kWarpBytes = kStages * 2 * kTile;
-    static constexpr int kOffQ = kDecWarps * kWarpBytes;
+    static constexpr int kOffQ = WARPS * kWarpBytes;
     static constexpr int kBytes = kOffQ + kDecodeRows * D * 2;
     static constexpr int kPitch = D + 8;                                  // floats per row of a warp's output
-    static constexpr int kOffMl = kDecWarps * kDecodeRows * kPitch * 4;   // the warps' maxima and sums
-    static constexpr int kOffSum = kOffMl + kDecWarps * kDecodeRows * 8;  // the block's output, maxima and sums
+    static constexpr int kOffMl = WARPS * kDecodeRows * kPitch * 4;   // the warps' maxima and sums
+    static constexpr int kOffSum = kOffMl + WARPS * kDecodeRows * 8;  // the block's output, maxima and sums
     static_assert(kOffSum + kDecodeRows * (D + 2) * 4 <= kOffQ, "the warps' outputs reuse the rings");
 };
 
@@ -114,11 +114,13 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-template <int D, bool BF16>
-__global__ void __launch_bounds__(kDecThreads, kDecodeBlocksPerSm)
+// WARPS = 4: two blocks per SM; 8: one, for clusters where every block has an SM.
+template <int D, bool BF16, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? kDecodeBlocksPerSm : 1)
 attn_decode_kernel(const __grid_constant__ AttnParams p)
 {
-    using L = DecLayout<D>;
+    using L = DecLayout<D, WARPS>;
+    constexpr int kDecThreads = 32 * WARPS;
     constexpr int kChunks = D / 8;                 // 16-byte chunks per row
     constexpr int kRowsPerCopy = 32 / kChunks;     // rows one warp-wide copy covers
     constexpr int kKeys = L::kKeys, kWarpKeys = L::kWarpKeys, kCopies = kWarpKeys / kRowsPerCopy;
@@ -127,7 +129,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
 
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Share share;
-    __shared__ long long red[kDecWarps];
+    __shared__ long long red[WARPS];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;
@@ -373,13 +375,13 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
             const int row = e / (D / 4), c = 4 * (e % (D / 4));
             float m = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < kDecWarps; ++w)
+            for (int w = 0; w < WARPS; ++w)
                 m = fmaxf(m, wml[(w * kDecodeRows + row) * 2]);
             const float base = m == -INFINITY ? 0.f : m;
             float l = 0.f;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int w = 0; w < kDecWarps; ++w) {
+            for (int w = 0; w < WARPS; ++w) {
                 const float2 ml = *reinterpret_cast<const float2 *>(wml + (w * kDecodeRows + row) * 2);
                 const float a = ex2(ml.x - base);
                 const float4 v = *reinterpret_cast<const float4 *>(wo + (w * kDecodeRows + row) * L::kPitch + c);
@@ -447,27 +449,68 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
     }
 }
 
-template <int D, bool BF16>
-cudaError_t launch_decode_attn(const AttnParams &p, int grid, cudaStream_t stream)
+template <int D, bool BF16, int WARPS>
+cudaError_t decode_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute (&attr)[2], int grid, int cluster,
+                          cudaStream_t stream)
 {
-    constexpr int smem = DecLayout<D>::kBytes;
+    constexpr int smem = DecLayout<D, WARPS>::kBytes;
     static SmemLimit limit;
-    if (const cudaError_t e = ensure_smem_limit(limit, attn_decode_kernel<D, BF16>, smem, true); e != cudaSuccess)
+    if (const cudaError_t e = ensure_smem_limit(limit, attn_decode_kernel<D, BF16, WARPS>, smem, true); e != cudaSuccess)
         return e;
-    cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kDecThreads);
+    cfg.blockDim = dim3(32 * WARPS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = p.cluster;
+    attr[1].val.clusterDim.x = cluster;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = p.cluster > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, attn_decode_kernel<D, BF16>, p);
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaSuccess;
+}
+
+template <int D, bool BF16, int WARPS>
+cudaError_t launch_decode_attn(const AttnParams &p, int grid, cudaStream_t stream)
+{
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    if (const cudaError_t e = decode_config<D, BF16, WARPS>(cfg, attr, grid, p.cluster, stream); e != cudaSuccess)
+        return e;
+    return cudaLaunchKernelEx(&cfg, attn_decode_kernel<D, BF16, WARPS>, p);
+}
+
+// Clusters of 2, 4 or 8 blocks that run at once on the current device: fewer than its
+// blocks' number would give, since a cluster lies in one part of the device.
+template <int D, bool BF16, int WARPS>
+int active_clusters(int cluster)
+{
+    static std::atomic<int> known[64][4] = {};   // + 1; per device and log2 of the size
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
+        return 0;
+    std::atomic<int> &k = known[dev][cluster == 2 ? 1 : cluster == 4 ? 2 : 3];
+    if ((n = k.load(std::memory_order_relaxed)) > 0)
+        return n - 1;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    if (decode_config<D, BF16, WARPS>(cfg, attr, cluster, cluster, nullptr) != cudaSuccess)
+        return 0;
+    cfg.attrs = attr + 1;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, attn_decode_kernel<D, BF16, WARPS>, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        n = 0;
+    }
+    k.store(n + 1, std::memory_order_relaxed);
+    return n;
+}
+
+template <int D, bool BF16>
+cudaError_t launch_decode_width(const AttnParams &p, int grid, cudaStream_t stream)
+{
+    return p.warps == 8 ? launch_decode_attn<D, BF16, 8>(p, grid, stream) : launch_decode_attn<D, BF16, 4>(p, grid, stream);
 }
 
 }  // namespace
@@ -476,8 +519,17 @@ cudaError_t launch_attn_decode(const AttnParams &p, int grid, cudaStream_t strea
 {
     const bool bf16 = p.kv.dtype == QMM_BF16;
     if (p.kv.head_dim == 128)
-        return bf16 ? launch_decode_attn<128, true>(p, grid, stream) : launch_decode_attn<128, false>(p, grid, stream);
-    return bf16 ? launch_decode_attn<64, true>(p, grid, stream) : launch_decode_attn<64, false>(p, grid, stream);
+        return bf16 ? launch_decode_width<128, true>(p, grid, stream) : launch_decode_width<128, false>(p, grid, stream);
+    return bf16 ? launch_decode_width<64, true>(p, grid, stream) : launch_decode_width<64, false>(p, grid, stream);
+}
+
+int attn_decode_clusters(int head_dim, bool bf16, int warps, int cluster)
+{
+    if (head_dim == 128)
+        return warps == 8 ? (bf16 ? active_clusters<128, true, 8>(cluster) : active_clusters<128, false, 8>(cluster))
+                          : (bf16 ? active_clusters<128, true, 4>(cluster) : active_clusters<128, false, 4>(cluster));
+    return warps == 8 ? (bf16 ? active_clusters<64, true, 8>(cluster) : active_clusters<64, false, 8>(cluster))
+                      : (bf16 ? active_clusters<64, true, 4>(cluster) : active_clusters<64, false, 4>(cluster));
 }
 
 }  // namespace qmm

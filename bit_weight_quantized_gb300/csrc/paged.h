@@ -73,13 +73,15 @@ struct AttnParams {
     int whole;                     // every item in one cluster or block: no partial results
     int unsplit;                   // whole items, several per block (chunk kernel)
     int cluster;                   // blocks per cluster (decode kernel, whole items)
+    int warps;                     // of a block of the decode kernel: 4 or 8
     int same_page;                 // every warp tile of the decode kernel lies in one page
     int min_chunk;                 // work a block takes at least, in units
 };
 
 // Sizes of one kernel's work items: query rows per tile, keys per unit.
 constexpr int kDecodeRows = 16;
-__host__ __device__ constexpr int decode_keys(int head_dim) { return head_dim == 64 ? 128 : 64; }   // 32 KB of K and V
+// (decode kernel: 8 KB of K and V per warp)
+__host__ __device__ constexpr int decode_keys(int head_dim, int warps) { return (head_dim == 64 ? 32 : 16) * warps; }
 constexpr int kChunkRows = 256, kChunkKeys = 128;
 // What starting and finishing an item costs, in units (see find_share).  Chunk kernel:
 // about 9000 cycles against 2400 a unit; an 8192-token prompt takes 466, 361 and 368 us
@@ -91,6 +93,10 @@ constexpr int kMaxCluster = 8;
 
 // Blocks of the decode kernel per SM (it is sized for two).
 constexpr int kDecodeBlocksPerSm = 2;
+
+// Clusters of `cluster` (2, 4, 8) blocks of `warps` warps of the decode kernel that run at
+// once on the current device.
+int attn_decode_clusters(int head_dim, bool bf16, int warps, int cluster);
 
 cudaError_t launch_attn_decode(const AttnParams &p, int grid, cudaStream_t stream);
 cudaError_t launch_attn_chunk(const AttnParams &p, int grid, cudaStream_t stream);

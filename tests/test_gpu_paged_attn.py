@@ -113,6 +113,16 @@ def test_long_axis_is_split(q, n, kv, dtype):
     check(q, Batch([n], [kv], 8, 2, 128, dtype, page=64, seed=kv))
 
 
+# short axes: clusters of two to eight blocks of eight and of four warps, single blocks of
+# both, and axes that are split, by the number of sequences and of keys
+@pytest.mark.parametrize("batch", [1, 5, 13, 30, 70, 160])
+@pytest.mark.parametrize("D", [64, 128])
+def test_short_axes(q, batch, D):
+    for kv in (40, 190, 450, 1100, 2300, 4500):
+        if batch * kv <= 160000:
+            check(q, Batch([1] * batch, [max(1, kv - i % 3 * 31) for i in range(batch)], 8, 2, D, "bf16", seed=kv))
+
+
 # ragged batches: long and short items on the same blocks
 @pytest.mark.parametrize("n", [1, 48])
 def test_ragged(q, n):
