@@ -407,10 +407,16 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
         while (n >= 0) {
             const Segment &sg = segs[n % kSegs];
             const RowTile r = sg.r;
-            const bool two = in_two(sg);
+            const bool two = in_two(sg), whole = is_whole(sg);
             const int row = quarter * 32 + lane, trow = (two ? 0 : 128 * s) + row;   // row in the stream, in the item
             const int rr = r.row0 + trow;
-            const int units = sg.units, kb0 = (r.unit0 + sg.off) * kChunkKeys;
+            const int h = sg.h, units = sg.units, kb0 = (r.unit0 + sg.off) * kChunkKeys;
+            const int slot = part_slot(sg);
+            if (threadIdx.x == 0 && is_last_part(sg))
+                write_meta<kChunkSetup>(p, sg, share.chunk);
+            // (before the next part is looked for: segments that a stream has no part in
+            // may fill the ring in between)
+            leave(n);
             const int2 see = row_keys(p, r, rr);
             float mref = -INFINITY, l = 0.f;
             const uint64_t scale2 = pair(__float_as_uint(p.scale_log2), __float_as_uint(p.scale_log2));
@@ -527,7 +533,6 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                     if (!ok)
                         break;
                     tc_fence_after();
-                    leave(n);
                     n = next_part(n + 1);
                     if (n >= 0) {
                         start_q(segs[n % kSegs]);
@@ -549,13 +554,12 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                 l = w0 * l + w1 * l1;
             }
             // rows to memory: the item's output, or this block's part of it
-            const bool whole = is_whole(sg);
             const int next = next_part(n + 1);
             // (whole rows go through the query tile; else the next queries can come in now)
             if (!whole && next >= 0)
                 start_q(segs[next % kSegs]);
             const float inv = l > 0.f ? 1.f / l : 0.f;
-            float *part = p.part_o + static_cast<long long>(part_slot(sg)) * (kChunkRows * D) + 4 * trow;
+            float *part = p.part_o + static_cast<long long>(slot) * (kChunkRows * D) + 4 * trow;
             uint32_t o[D];
 #pragma unroll
             for (int c = 0; c < D; c += 32)
@@ -601,7 +605,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                 const int c = lane % kChunks, row0 = quarter * 32 + lane / kChunks;
                 const int left = r.rows - (trow - row);
                 RowCursor at(r.row0 + trow - row + row0, kRowsPerCopy, p);
-                uint16_t *base = p.out + (static_cast<long long>(r.t0) * p.q_heads + sg.h * p.group) * D + 8 * c;
+                uint16_t *base = p.out + (static_cast<long long>(r.t0) * p.q_heads + h * p.group) * D + 8 * c;
                 const int tstride = p.q_heads * D;
 #pragma unroll
                 for (int e = 0; e < 32; e += kRowsPerCopy) {
@@ -612,17 +616,14 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                 }
                 if (p.lse && trow < r.rows) {
                     const int tok = p.by_group(rr);
-                    p.lse[static_cast<long long>(r.t0 + tok) * p.q_heads + sg.h * p.group + rr - tok * p.group] =
+                    p.lse[static_cast<long long>(r.t0 + tok) * p.q_heads + h * p.group + rr - tok * p.group] =
                         l > 0.f ? (mref - kShift + log2f(l)) * 0.6931471805599453f : -INFINITY;
                 }
                 __syncwarp();    // the rows are read before the next queries replace them
             } else if (trow < r.rows) {
-                *reinterpret_cast<float2 *>(p.part_ml + (static_cast<long long>(part_slot(sg)) * kChunkRows + trow) * 2) =
+                *reinterpret_cast<float2 *>(p.part_ml + (static_cast<long long>(slot) * kChunkRows + trow) * 2) =
                     make_float2(mref, l);
             }
-            if (threadIdx.x == 0 && is_last_part(sg))
-                write_meta<kChunkSetup>(p, sg, share.chunk);
-            leave(n);
             n = next;
             if (n >= 0) {
                 if (whole)

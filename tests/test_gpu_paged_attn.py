@@ -123,6 +123,14 @@ def test_short_axes(q, batch, D):
             check(q, Batch([1] * batch, [max(1, kv - i % 3 * 31) for i in range(batch)], 8, 2, D, "bf16", seed=kv))
 
 
+# several items a block, of which the second 128 rows' warps have a part in few: a wide one
+# and then more one-tile items of at most 128 rows than are found ahead
+@pytest.mark.parametrize("D", [64, 128])
+def test_wide_items_between_narrow_ones(q, D):
+    ql = [200 if i % 3 == 0 else 90 + i % 39 for i in range(120)]
+    check(q, Batch(ql, ql, 8, 8, D, "f16", seed=7))
+
+
 # ragged batches: long and short items on the same blocks
 @pytest.mark.parametrize("n", [1, 48])
 def test_ragged(q, n):
