@@ -197,6 +197,23 @@ void attn_set_tma(AttnParams &p)
     p.page_step = static_cast<int>(step);
 }
 
+bool attn_set_q_tma(AttnParams &p)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    // (a single token's stride is not looked at)
+    const long long stride = p.kv.tokens > 1 ? p.q_stride : static_cast<long long>(p.q_heads) * p.kv.head_dim;
+    if (!enc || p.group > 128 || stride <= 0)
+        return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(p.kv.head_dim), static_cast<cuuint64_t>(p.q_heads),
+                                static_cast<cuuint64_t>(p.kv.tokens)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(p.kv.head_dim) * 2, static_cast<cuuint64_t>(stride) * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(p.group), static_cast<cuuint32_t>(128 / p.group)};
+    const cuuint32_t one[3] = {1, 1, 1};
+    return enc(&p.tmq, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<uint16_t *>(p.q), dims, strides, box, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 void skinny_set_tma(GemvParams &p)
 {
     p.tma = 0;

@@ -220,10 +220,10 @@ size_t scratch_bytes(bool few, int head_dim, int num_sms)
 constexpr int kMinDecodeUnits = 5, kMinChunkUnits = 6;
 
 // Work of the longest item (setup and units) up to which blocks of the chunk kernel take
-// whole items: no joining kernel, against blocks of unequal work by up to one item.  8
-// sequences of up to 300 tokens over 400 keys: 26.9 us, split 31.6; 16 of 100 over 600:
-// 30.0, split 33.8.
-constexpr int kUnsplitWork = 10;
+// whole items: no joining kernel, against blocks of unequal work by up to one item.  Four
+// sequences of up to 1000 tokens, work 10: 47.8 us, split 49.5; seven chunks with a
+// window of 1000, work 12: 35.6, split 36.8; prompts of 2048, work 18: 49.9, split 41.6.
+constexpr int kUnsplitWork = 12;
 
 // Units a block of a cluster takes at most, of four warps and (wide) of eight, twice the
 // keys: one token over 8000 keys 18.9 us at 16 units of four warps, 12.3 split over all
@@ -273,9 +273,13 @@ cudaError_t attn_dispatch(AttnParams &p, int max_q, long long max_kv, void *work
     // starts faster and needs no join (64 tokens over 1000 keys 13.6 us against the chunk
     // kernel's 18.9, 128 over 128 6.3 against 8.7; but 4 x 50 over 200, 416 items on 304
     // blocks, 13.9 against 9.6, and 5 over 4000 of 32 sequences, split, 243 against 94)
-    const bool few = few_rows(max_q, p.group) || (cluster > 0 && ditems * cluster <= kDecodeBlocksPerSm * num_sms);
-    const int rows = few ? kDecodeRows : kChunkRows, keys = few ? decode_keys(p.kv.head_dim, warps) : kChunkKeys;
+    // (and queries that the chunk kernel's tensor copies do not take: groups of over 128
+    // heads, strides of zero)
+    const bool few = few_rows(max_q, p.group) || (cluster > 0 && ditems * cluster <= kDecodeBlocksPerSm * num_sms) ||
+                     !attn_set_q_tma(p);
+    const int rows = few ? kDecodeRows : 2 * chunk_stream_rows(p.group), keys = few ? decode_keys(p.kv.head_dim, warps) : kChunkKeys;
     const int setup = few ? kDecodeSetup : kChunkSetup;
+    p.tile_rows = rows;
     p.row_tiles = static_cast<int>((q_rows + rows - 1) / rows);
     p.by_group = fast_div(p.group);
     p.by_tiles = fast_div(p.row_tiles);
@@ -302,7 +306,7 @@ cudaError_t attn_dispatch(AttnParams &p, int max_q, long long max_kv, void *work
     const size_t g = attn_grid(few, num_sms);
     p.meta = reinterpret_cast<int4 *>(ws);
     p.part_ml = reinterpret_cast<float *>(ws + g * 32);
-    p.part_o = p.part_ml + 2 * g * rows * 2;
+    p.part_o = p.part_ml + 2 * g * (few ? kDecodeRows : kChunkRows) * 2;
     if (!few)
         attn_set_tma(p);
     cudaError_t e = few ? launch_attn_decode(p, grid, stream) : launch_attn_chunk(p, grid, stream);

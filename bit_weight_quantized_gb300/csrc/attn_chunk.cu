@@ -5,25 +5,35 @@
 //
 // A work item is 256 rows ((token, query head) pairs of one key head, so that a
 // key tile loaded once serves all query heads that share it) as two streams of 128
-// rows; the keys go by in tiles of 128.  Both products run on tcgen05 with their
-// accumulators in tensor memory: per stream S (128 x 128 fp32) and O (128 x D), all
-// 512 columns at D = 128.  P takes S's place as 16-bit values and is the second
+// rows (or somewhat fewer, where the query heads per key head do not divide 128: a
+// stream holds whole tokens, so that one tensor copy per 64 values brings its queries);
+// the keys go by in tiles of 128.  Both products run on tcgen05 with their accumulators
+// in tensor memory: per stream S (128 x 128 fp32) and O (128 x D), all 512 columns at
+// D = 128.  P takes S's place as 16-bit values and is the second
 // product's left operand straight from tensor memory; V is its right operand as it
 // lies in the cache ([key][d], the "MN-major" form), so nothing is transposed.  An
-// item of at most 128 rows gives both streams the same rows and every other tile;
-// stream 0 adds up the two at the end, straight from tensor memory.
+// item of one stream's rows gives both streams the same rows and every other tile;
+// stream 0 adds up the two at the end, straight from tensor memory.  The next item's
+// queries are loaded, and its first scores computed, as soon as the last scores of this
+// one are there.
 //
 // Roles.  Warps 0-3 and 4-7 are the softmax of streams 0 and 1, one thread per row:
 // no exchange between lanes.  Warp 8 issues the products, one stream after the
 // other, so that one's products run under the other's softmax.  (A warp for each
 // stream let the two fall into step, with both softmaxes and then both products at
 // once: 240 instead of 190 us for 4096 x 4096 x 32 heads of 128.)  Warp 9 finds the
-// segments of the block's share ahead of the others.  Warps 10 and 11 bring K and V tiles into a ring each: where the page size is a multiple of 8 by
+// segments of the block's share ahead of the others and brings their queries.  Warps 10
+// and 11 bring K and V tiles into a ring each: where the page size is a multiple of 8 by
 // tensor copies, one per page or part of a page that lies in the tile; else by
 // 16-byte asynchronous copies, which take any page size.  V rows that nobody sees
 // (past kv_len, before the window) are made zero, since 0 x NaN would spoil the
 // product.  Plain copies kept the loading warps busy for 6000 cycles a tile pair,
-// three times the products' time.
+// three times the products' time; plain copies of 256 query rows 3000 of all eight
+// softmax warps' time, or 14000 of one warp's.
+//
+// Code that runs once per item costs some 6 cycles an instruction, since it has to be
+// fetched: masks and outputs go through loops of 32 columns (straight code for the mask
+// of a tile took 2500 cycles, the loop 1100 at most).
 //
 // The running maximum is replaced only when it grows by more than 2^8: the output
 // accumulator in tensor memory is then read, scaled and written back by its
@@ -52,7 +62,7 @@ constexpr int kHalf = kChunkKeys / 2;               // the weights are handed ov
 constexpr int kSoftRegs = 200, kOtherRegs = 104;
 static_assert(256 * kSoftRegs + 128 * kOtherRegs == kChunkThreads * 168, "register split");
 
-using ChunkWalk = Walk<kChunkRows, kChunkKeys, kChunkSetup>;
+using ChunkWalk = Walk<kChunkKeys, kChunkSetup>;
 
 template <int D>
 struct ChunkLayout {
@@ -62,14 +72,15 @@ struct ChunkLayout {
     static constexpr int kOffK = 2 * kTile;
     static constexpr int kOffV = kOffK + kKRing * kTile;
     static constexpr int kOffBar = kOffV + kVRing * kTile;
-    // full / empty of both rings, patch, per stream q_full, s_full, p_full (two halves) and
+    // full / empty of both rings, patch, per stream q_full, q_empty, s_full, p_full (two halves) and
     // o_full, x_full, x_done, drain, full / empty of the segments
-    static constexpr int kNumBars = 2 * (kKRing + kVRing) + 14 + 2 * kSegs;
+    static constexpr int kNumBars = 2 * (kKRing + kVRing) + 16 + 2 * kSegs;
     static constexpr int kOffTmem = kOffBar + 8 * kNumBars;
     static constexpr int kOffShare = kOffTmem + 16;
     static constexpr int kOffRed = kOffShare + sizeof(Share);
     static constexpr int kOffSeg = kOffRed + 8 * (kChunkThreads / 32);
-    static constexpr int kBytes = kOffSeg + sizeof(Segment) * kSegs;
+    static constexpr int kOffX = (kOffSeg + static_cast<int>(sizeof(Segment)) * kSegs + 7) / 8 * 8;   // stream 1's maxima and sums
+    static constexpr int kBytes = kOffX + 128 * 8;
     static_assert(kOffShare % 8 == 0 && sizeof(Share) % 8 == 0, "alignment");
     static_assert(kBytes <= 227 * 1024, "shared memory per block");
 };
@@ -79,14 +90,10 @@ __device__ __forceinline__ uint32_t s_col(int s) { return static_cast<uint32_t>(
 __device__ __forceinline__ uint32_t p_col(int s, int h) { return s_col(s) + static_cast<uint32_t>(h) * 32u; }
 __device__ __forceinline__ uint32_t o_col(int s) { return 256u + static_cast<uint32_t>(s) * 128u; }
 
-// Byte of 16-byte chunk c of row r in a query tile: halves of 64 values, rows of 128
-// bytes, chunks permuted by the row (the 128-byte swizzle).
-__device__ __forceinline__ uint32_t q_addr(int r, int c)
-{
-    return static_cast<uint32_t>((c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-}
+// Query tiles lie as halves of 64 values, rows of 128 bytes, chunks of 16 bytes permuted
+// by the row (the 128-byte swizzle).
 
-// The same in a K or V tile: groups of 8 keys, each [D / 64 halves][8 keys][64
+// Byte of chunk c of row r in a K or V tile: groups of 8 keys, each [D / 64 halves][8 keys][64
 // values], so that one tensor copy brings both halves of a page's keys.
 template <int D>
 __device__ __forceinline__ uint32_t kv_addr(int r, int c)
@@ -157,19 +164,13 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const void *tmap, uint
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_st2(uint32_t taddr, float a, float b)
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *tmap, uint64_t *bar, int c0, int c1, int c2)
 {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(taddr), "f"(a), "f"(b) : "memory");
-}
-
-// two columns; complete on return
-__device__ __forceinline__ void tmem_ld2(uint32_t taddr, float &a, float &b)
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];\n\t"
-                 "tcgen05.wait::ld.sync.aligned;"
-                 : "=f"(a), "=f"(b)
-                 : "r"(taddr)
-                 : "memory");
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
 }
 
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
@@ -246,29 +247,31 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return d;
 }
 
-// Walks rows `step` apart as (token, query head of the key head).
-struct RowCursor {
-    int tok, head, dt, dh, group;
-    __device__ __forceinline__ RowCursor(int row, int step, const AttnParams &p) : group(p.group)
-    {
-        tok = p.by_group(row);
-        head = row - tok * group;
-        dt = p.by_group(step);
-        dh = step - dt * group;
-    }
-    __device__ __forceinline__ void next()
-    {
-        tok += dt;
-        head += dh;
-        if (head >= group) {
-            head -= group;
-            ++tok;
+// Chunks (16 bytes) of a group of four lanes, lane q's own four in a: afterwards lane q
+// holds chunk q of the group's lanes in order.
+__device__ __forceinline__ void transpose4(uint32_t (&a)[4][4], int lane)
+{
+#pragma unroll
+    for (int d = 1; d <= 2; d <<= 1) {
+        const bool odd = lane & d;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            if (c & d)
+                continue;
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? a[c][f] : a[c + d][f], d);
+                if (odd)
+                    a[c][f] = got;
+                else
+                    a[c + d][f] = got;
+            }
         }
     }
-};
+}
 
 // An item of at most one stream's rows is shared by both streams, tile by tile.
-__device__ __forceinline__ bool in_two(const Segment &s) { return s.r.rows <= 128 && s.units > 1; }
+__device__ __forceinline__ bool in_two(const Segment &s, int stream_rows) { return s.r.rows <= stream_rows && s.units > 1; }
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kChunkThreads, 1)
@@ -285,7 +288,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
     long long *red = reinterpret_cast<long long *>(smem + L::kOffRed);
     uint64_t *k_full = reinterpret_cast<uint64_t *>(smem + L::kOffBar), *k_empty = k_full + L::kKRing;
     uint64_t *v_full = k_empty + L::kKRing, *v_empty = v_full + L::kVRing, *patch = v_empty + L::kVRing;
-    uint64_t *q_full = patch + 1, *s_full = q_full + 2, *p_full = s_full + 2, *o_full = p_full + 4;
+    uint64_t *q_full = patch + 1, *q_empty = q_full + 2, *s_full = q_empty + 2, *p_full = s_full + 2, *o_full = p_full + 4;
     uint64_t *x_full = o_full + 2, *x_done = x_full + 1, *drain = x_done + 1;
     uint64_t *seg_full = drain + 1, *seg_empty = seg_full + kSegs;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kOffTmem);
@@ -307,7 +310,8 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
         }
         mbar_init(patch, 1);
         for (int s = 0; s < 2; ++s) {
-            mbar_init(&q_full[s], kSoftWarps);
+            mbar_init(&q_full[s], 1);
+            mbar_init(&q_empty[s], 1);
             mbar_init(&s_full[s], 1);
             mbar_init(&p_full[2 * s], kSoftWarps);
             mbar_init(&p_full[2 * s + 1], kSoftWarps);
@@ -332,8 +336,9 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (!p.whole && threadIdx.x == 0)
         p.meta[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
-    find_share<kChunkRows, kChunkKeys, kChunkSetup, kChunkThreads>(p, red, &share);
+    find_share<kChunkKeys, kChunkSetup, kChunkThreads>(p, red, &share);
 
+    const int srows = chunk_stream_rows(p.group);   // a stream's rows
     bool ok = true;
     // Warp 9 walks the share and puts the segments, numbered, into a ring of kSegs; one
     // of no units ends them.  Every other warp goes through all of them.
@@ -355,74 +360,31 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
         const int s = warp / kSoftWarps, quarter = warp % kSoftWarps;
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         const uint32_t ts = tmem + lanes + s_col(s), to = tmem + lanes + o_col(s);
-        uint8_t *qs = smem + L::kOffQ + s * L::kTile;
+        float2 *x_ml = reinterpret_cast<float2 *>(smem + L::kOffX);
         uint32_t ph = 0;         // parity of the next S
         uint32_t oph = 0;        // parity of the next O
         uint32_t xph = 0;        // parity of the next exchange between the streams
-        // the first segment from number n on that this stream has a part in: rows of its
-        // own, or every other tile of an item of one stream's rows; or the end (-1)
-        auto next_part = [&](int n) -> int {
-            for (;; ++n) {
-                const Segment &x = segment(n);
-                if (!ok || x.units == 0)
-                    return -1;
-                if (x.r.rows > 128 * s || in_two(x))
-                    return n;
-                leave(n);
-            }
-        };
-        // this warp's 32 query rows into the operand tile (zeros past the item); every
-        // product that read the previous ones is complete.  Stream 1 has none where it
-        // shares stream 0's rows.
-        auto start_q = [&](const Segment &x) {
-            if (s == 1 && x.r.rows <= 128)
-                return;
-            const int c = lane % kChunks, row0 = quarter * 32 + lane / kChunks;
-            const int left = x.r.rows - 128 * s;        // rows of the stream
-            RowCursor at(x.r.row0 + 128 * s + row0, kRowsPerCopy, p);
-            const uint16_t *base = p.q + x.r.t0 * p.q_stride + static_cast<long long>(x.h * p.group) * D + 8 * c;
-#pragma unroll
-            for (int e = 0; e < 32; e += kRowsPerCopy) {
-                const int row = row0 + e;
-                cp_async16_or_zero(smem_u32(qs + q_addr(row, c)),
-                                   row < left ? base + at.tok * p.q_stride + at.head * D : p.q, row < left);
-                at.next();
-            }
-            cp_async_commit();
-        };
-        auto land_q = [&](const Segment &x) {
-            if (s == 1 && x.r.rows <= 128)
-                return;
-            cp_async_wait_group<0>();
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&q_full[s]);
-        };
-        int n = next_part(0);
-        if (n >= 0) {
-            start_q(segs[n % kSegs]);
-            land_q(segs[n % kSegs]);
-        }
-        while (n >= 0) {
-            const Segment &sg = segs[n % kSegs];
+        for (int n = 0;; ++n) {
+            const Segment &sg = segment(n);
             const RowTile r = sg.r;
-            const bool two = in_two(sg), whole = is_whole(sg);
-            const int row = quarter * 32 + lane, trow = (two ? 0 : 128 * s) + row;   // row in the stream, in the item
-            const int rr = r.row0 + trow;
-            const int h = sg.h, units = sg.units, kb0 = (r.unit0 + sg.off) * kChunkKeys;
-            const int slot = part_slot(sg);
+            const int h = sg.h, units = sg.units, kb0 = (r.unit0 + sg.off) * kChunkKeys, slot = part_slot(sg);
+            const bool two = in_two(sg, srows), whole = is_whole(sg);
+            if (!ok || units == 0)
+                break;
             if (threadIdx.x == 0 && is_last_part(sg))
                 write_meta<kChunkSetup>(p, sg, share.chunk);
-            // (before the next part is looked for: segments that a stream has no part in
-            // may fill the ring in between)
             leave(n);
+            if (r.rows <= srows * s && !two)
+                continue;                   // no rows of this stream's
+            const int row = quarter * 32 + lane, trow = (two ? 0 : srows * s) + row;   // row in the stream, in the item
+            const bool mine = row < srows && trow < r.rows;   // (the others hold anything)
+            const int rr = r.row0 + trow;
             const int2 see = row_keys(p, r, rr);
             float mref = -INFINITY, l = 0.f;
             const uint64_t scale2 = pair(__float_as_uint(p.scale_log2), __float_as_uint(p.scale_log2));
             const int j0 = two ? s : 0, step = two ? 2 : 1;
             // keys that every row of the warp sees: halves inside need no mask
-            int all_lo = see.x, all_hi = trow < r.rows ? see.y : 0x7fffffff;
+            int all_lo = mine ? see.x : 0, all_hi = mine ? see.y : 0x7fffffff;
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) {
                 all_lo = max(all_lo, __shfl_xor_sync(0xffffffffu, all_lo, d));
@@ -433,6 +395,30 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                     break;
                 ph ^= 1u;
                 tc_fence_after();
+                const int kb = kb0 + j * kChunkKeys;
+                if (kb < all_lo || kb + kChunkKeys - 1 > all_hi) {
+                    // Keys that the row does not see get the score -infinity.  In place and
+                    // in a loop: straight code for 128 columns, which few tiles run, took
+                    // 2500 cycles of instruction fetches.
+#pragma unroll 1
+                    for (int c = 0; c < kChunkKeys; c += 32) {
+                        if (kb + c >= all_lo && kb + c + 31 <= all_hi)
+                            continue;
+                        const int lo = see.x - kb - c, hi = see.y - kb - c;     // the columns this row sees
+                        const uint32_t bits = (hi >= 31 ? ~0u : hi < 0 ? 0u : (2u << hi) - 1u) &
+                                              (lo <= 0 ? ~0u : lo > 31 ? 0u : ~0u << lo);
+                        uint32_t x[32];
+                        tmem_ld32_start(ts + c, x);
+                        tmem_ld_wait();
+                        pin32(x);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!(bits >> e & 1u))
+                                x[e] = 0xff800000u;
+                        tmem_st32(ts + c, x);
+                    }
+                    tmem_st_wait();
+                }
                 uint32_t v[kChunkKeys];
 #pragma unroll
                 for (int c = 0; c < kChunkKeys; c += 32)
@@ -441,14 +427,6 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
 #pragma unroll
                 for (int c = 0; c < kChunkKeys; c += 32)
                     pin32(v + c);
-                const int kb = kb0 + j * kChunkKeys;
-                if (kb < all_lo || kb + kChunkKeys - 1 > all_hi) {
-                    const int c_lo = see.x - kb, c_hi = see.y - kb;     // the columns this row sees
-#pragma unroll
-                    for (int c = 0; c < kChunkKeys; ++c)
-                        if (c < c_lo || c > c_hi)
-                            v[c] = 0xff800000u;                         // -infinity
-                }
                 float mx[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
@@ -516,14 +494,12 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
             if (!ok)
                 break;
             tc_fence_after();
-            // an item shared by both streams: stream 1 leaves its maximum and sum beside
-            // its output in tensor memory, stream 0 (same rows, same lanes) adds both up
+            // an item shared by both streams: stream 1 leaves its maximum and sum in
+            // shared memory, stream 0 (same rows, same lanes) adds both up
             float w0 = 1.f, w1 = 0.f;
             if (two) {
-                const uint32_t tx = tmem + lanes + s_col(1), to1 = tmem + lanes + o_col(1);
                 if (s == 1) {
-                    tmem_st2(tx, mref, l);
-                    tmem_st_wait();
+                    x_ml[row] = make_float2(mref, l);
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0)
@@ -533,11 +509,6 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                     if (!ok)
                         break;
                     tc_fence_after();
-                    n = next_part(n + 1);
-                    if (n >= 0) {
-                        start_q(segs[n % kSegs]);
-                        land_q(segs[n % kSegs]);
-                    }
                     continue;
                 }
                 ok = __all_sync(0xffffffffu, mbar_wait(x_full, xph, p.status));
@@ -545,8 +516,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                 if (!ok)
                     break;
                 tc_fence_after();
-                float m1, l1;
-                tmem_ld2(tx, m1, l1);
+                const float m1 = x_ml[row].x, l1 = x_ml[row].y;
                 const float m = fmaxf(mref, m1), base = m == -INFINITY ? 0.f : m;
                 w0 = ex2(mref - base);
                 w1 = ex2(m1 - base);
@@ -554,81 +524,62 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                 l = w0 * l + w1 * l1;
             }
             // rows to memory: the item's output, or this block's part of it
-            const int next = next_part(n + 1);
-            // (whole rows go through the query tile; else the next queries can come in now)
-            if (!whole && next >= 0)
-                start_q(segs[next % kSegs]);
             const float inv = l > 0.f ? 1.f / l : 0.f;
             float *part = p.part_o + static_cast<long long>(slot) * (kChunkRows * D) + 4 * trow;
-            uint32_t o[D];
+            const int tok = p.by_group(rr), sub = lane & 3;
+            // this row's place in the output, and those of the group of four lanes
+            const long long place = mine ?
+                (static_cast<long long>(r.t0 + tok) * p.q_heads + h * p.group + rr - tok * p.group) * D : -1;
+            long long to_row[4];
 #pragma unroll
-            for (int c = 0; c < D; c += 32)
-                tmem_ld32_start(to + c, o + c);
-            tmem_ld_wait();
-#pragma unroll
-            for (int c = 0; c < D; c += 32)
-                pin32(o + c);
-            if (two) {
-#pragma unroll
-                for (int c = 0; c < D; c += 32) {
+            for (int i = 0; i < 4; ++i)
+                to_row[i] = __shfl_sync(0xffffffffu, place, (lane & ~3) + i);
+            // (a loop, for the sake of the instruction fetches: see above)
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld32_start(to + c, o);
+                tmem_ld_wait();
+                pin32(o);
+                if (two) {
                     uint32_t o1[32];
                     tmem_ld32_start(tmem + lanes + o_col(1) + c, o1);
                     tmem_ld_wait();
                     pin32(o1);
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
-                        o[c + e] = __float_as_uint(w0 * __uint_as_float(o[c + e]) + w1 * __uint_as_float(o1[e]));
+                        o[e] = __float_as_uint(w0 * __uint_as_float(o[e]) + w1 * __uint_as_float(o1[e]));
                 }
-            }
-            if (whole) {
-                // through the stream's query tile, so that a warp stores whole rows
+                if (whole) {
+                    // four lanes exchange their rows' pieces, so that each row's 64 bytes
+                    // are stored by lanes side by side
+                    uint32_t w[4][4];
 #pragma unroll
-                for (int c = 0; c < D / 8; ++c) {
-                    uint32_t w[4];
+                    for (int e = 0; e < 16; ++e)
+                        w[e >> 2][e & 3] = pack16<BF16>(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+                    transpose4(w, lane);
 #pragma unroll
-                    for (int f = 0; f < 4; ++f)
-                        w[f] = pack16<BF16>(__uint_as_float(o[8 * c + 2 * f]) * inv, __uint_as_float(o[8 * c + 2 * f + 1]) * inv);
-                    *reinterpret_cast<uint4 *>(qs + q_addr(row, c)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    for (int i = 0; i < 4; ++i)
+                        if (to_row[i] >= 0)
+                            *reinterpret_cast<uint4 *>(p.out + to_row[i] + c + 8 * sub) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+                } else if (mine) {
+                    // parts lie [D / 4][rows][4], so that a warp's rows are consecutive
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        *reinterpret_cast<uint4 *>(part + (c / 4 + e) * (4 * kChunkRows)) =
+                            make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                 }
-            } else if (trow < r.rows) {
-                // parts lie [D / 4][rows][4], so that a warp's rows are consecutive
-#pragma unroll
-                for (int c = 0; c < D / 4; ++c)
-                    *reinterpret_cast<uint4 *>(part + c * (4 * kChunkRows)) =
-                        make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
             }
             tc_fence_before();   // the accumulators are read; the next P says so to the issuing warp
             __syncwarp();
             if (two && lane == 0)
                 mbar_arrive(x_done);
-            if (whole) {
-                const int c = lane % kChunks, row0 = quarter * 32 + lane / kChunks;
-                const int left = r.rows - (trow - row);
-                RowCursor at(r.row0 + trow - row + row0, kRowsPerCopy, p);
-                uint16_t *base = p.out + (static_cast<long long>(r.t0) * p.q_heads + h * p.group) * D + 8 * c;
-                const int tstride = p.q_heads * D;
-#pragma unroll
-                for (int e = 0; e < 32; e += kRowsPerCopy) {
-                    if (row0 + e < left)
-                        *reinterpret_cast<uint4 *>(base + static_cast<long long>(at.tok) * tstride + at.head * D) =
-                            *reinterpret_cast<const uint4 *>(qs + q_addr(row0 + e, c));
-                    at.next();
-                }
-                if (p.lse && trow < r.rows) {
-                    const int tok = p.by_group(rr);
-                    p.lse[static_cast<long long>(r.t0 + tok) * p.q_heads + h * p.group + rr - tok * p.group] =
-                        l > 0.f ? (mref - kShift + log2f(l)) * 0.6931471805599453f : -INFINITY;
-                }
-                __syncwarp();    // the rows are read before the next queries replace them
-            } else if (trow < r.rows) {
-                *reinterpret_cast<float2 *>(p.part_ml + (static_cast<long long>(slot) * kChunkRows + trow) * 2) =
-                    make_float2(mref, l);
-            }
-            n = next;
-            if (n >= 0) {
-                if (whole)
-                    start_q(segs[n % kSegs]);
-                land_q(segs[n % kSegs]);
+            if (mine) {
+                if (!whole)
+                    *reinterpret_cast<float2 *>(p.part_ml + (static_cast<long long>(slot) * kChunkRows + trow) * 2) =
+                        make_float2(mref, l);
+                else if (p.lse)
+                    p.lse[place / D] = l > 0.f ? (mref - kShift + log2f(l)) * 0.6931471805599453f : -INFINITY;
             }
         }
     } else {
@@ -663,9 +614,9 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                 wait(&v_full[slot], at / L::kVRing & 1u);
                 return static_cast<int>(slot);
             };
-            // S of stream s from query tile qt and the K tile in slot ks, whose last reader
-            // frees it
-            auto qk = [&](int s, int qt, int ks, bool last) {
+            // S of stream s from query tile qt and the K tile in slot ks; the last readers
+            // free them
+            auto qk = [&](int s, int qt, int ks, bool last, bool last_q) {
                 const uint64_t a = q_desc + static_cast<uint32_t>((qt * L::kTile) >> 4);
                 const uint64_t b = k_desc + static_cast<uint32_t>((ks * L::kTile) >> 4);
                 if (elect_one()) {
@@ -676,6 +627,8 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                     tc_commit(&s_full[s]);
                     if (last)
                         tc_commit(&k_empty[ks]);
+                    if (last_q)
+                        tc_commit(&q_empty[qt]);
                 }
                 __syncwarp();
             };
@@ -708,20 +661,21 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
             };
             for (int n = 0;; ++n) {
                 const Segment &sg = segment(n);
-                const int ns = __shfl_sync(0xffffffffu, sg.r.rows > 128 ? 2 : 1, 0);
+                const int ns = __shfl_sync(0xffffffffu, sg.r.rows > srows ? 2 : 1, 0);
                 const int units = __shfl_sync(0xffffffffu, sg.units, 0);
                 if (!ok || units == 0)
                     break;
                 leave(n);
                 // (the streams' loops are unrolled: with constant streams a product issues
                 // in 50 cycles, with variable ones in 60, and this warp is on every tile's
-                // path)
+                // path; with a segment's first scores inside them, under a condition, 512 over
+                // 16384 keys took 98 us instead of 89)
                 if (ns == 1) {
                     // one stream's rows: even tiles on stream 0, odd ones on stream 1
                     q_landed(0);
-                    qk(0, 0, k_landed(0), true);
+                    qk(0, 0, k_landed(0), true, units == 1);
                     if (units > 1)
-                        qk(1, 0, k_landed(1), true);
+                        qk(1, 0, k_landed(1), true, units == 2);
                     for (int j0 = 0; j0 < units; j0 += 2) {
 #pragma unroll
                         for (int s = 0; s < 2; ++s) {
@@ -729,7 +683,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                             if (j < units) {
                                 pv(s, v_landed(j), j0 == 0, true);
                                 if (j + 2 < units)
-                                    qk(s, 0, k_landed(j + 2), true);
+                                    qk(s, 0, k_landed(j + 2), true, j + 3 == units);
                                 else
                                     finish(s);
                             }
@@ -740,7 +694,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
                         q_landed(s);
-                        qk(s, s, ks, s == 1);
+                        qk(s, s, ks, s == 1, units == 1);
                     }
                     for (int j = 0; j < units; ++j) {
                         const int vs = v_landed(j);
@@ -751,7 +705,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                             if (more) {
                                 if (s == 0)
                                     ks = k_landed(j + 1);
-                                qk(s, s, ks, s == 1);
+                                qk(s, s, ks, s == 1, j + 2 == units);
                             } else {
                                 finish(s);
                             }
@@ -769,20 +723,48 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
             }
             __syncwarp();
         } else if (warp == kWalkWarp) {
-            // ================= segments =================
+            // ================= segments and query rows =================
             if (lane == 0) {
                 ChunkWalk walk;
                 walk.begin(share);
+                prefetch_tmap(&p.tmq);
+                int found = 0;           // segments found
                 bool more = true;
-                for (int n = 0; more; ++n) {
-                    Segment &x = segs[n % kSegs];
-                    if (n >= kSegs && !mbar_wait(&seg_empty[n % kSegs], (n / kSegs - 1) & 1, p.status))
+                uint32_t uses[2] = {0, 0};   // of the query tiles
+                const int toks = 128 / p.group;
+                for (int n = 0;; ++n) {
+                    for (; more && found < n + (n == 0 ? 1 : kSegs); ++found) {
+                        Segment &x = segs[found % kSegs];
+                        if (found >= kSegs && !mbar_wait(&seg_empty[found % kSegs], (found / kSegs - 1) & 1, p.status)) {
+                            ok = false;
+                            break;
+                        }
+                        more = walk.next(p, x);
+                        if (!more)
+                            x.units = 0;
+                        mbar_arrive(&seg_full[found % kSegs]);
+                    }
+                    const Segment &sg = segs[n % kSegs];
+                    if (!ok || sg.units == 0)
                         break;
-                    more = walk.next(p, x);
-                    if (!more)
-                        x.units = 0;
-                    mbar_arrive(&seg_full[n % kSegs]);
+                    // its rows, whole tokens, into the query tiles (past the item: of whatever
+                    // comes next)
+                    const int ns = sg.r.rows > srows ? 2 : 1, tok = sg.r.t0 + p.by_group(sg.r.row0);
+                    for (int s = 0; s < ns && ok; ++s) {
+                        if (uses[s] > 0 && !(ok = mbar_wait(&q_empty[s], (uses[s] - 1) & 1u, p.status)))
+                            break;
+                        ++uses[s];
+                        mbar_arrive_expect_tx(&q_full[s], static_cast<uint32_t>(srows * D * 2));
+#pragma unroll
+                        for (int c = 0; c < D; c += 64)
+                            tma_load_3d(smem_u32(smem + L::kOffQ + s * L::kTile + c * 256), &p.tmq, &q_full[s], c,
+                                        sg.h * p.group, tok + s * toks);
+                    }
                 }
+                // no copy may still be landing when the block exits, also after a timeout
+                for (int s = 0; s < 2; ++s)
+                    if (uses[s] > 0)
+                        mbar_wait(&q_full[s], (uses[s] - 1) & 1u, p.status);
             }
             __syncwarp();
         } else {

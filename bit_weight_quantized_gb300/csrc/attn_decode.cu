@@ -136,7 +136,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
     if (tid == 0)
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    find_share<kDecodeRows, kKeys, kDecodeSetup, kDecThreads>(p, red, &share);
+    find_share<kKeys, kDecodeSetup, kDecThreads>(p, red, &share);
 
     const uint32_t sbase = smem_u32(smem);
     const uint32_t ring = sbase + warp * L::kWarpBytes;
@@ -150,7 +150,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
     if (!p.whole && tid == 0)
         p.meta[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
 
-    Walk<kDecodeRows, kKeys, kDecodeSetup> walk;
+    Walk<kKeys, kDecodeSetup> walk;
     walk.begin(share);
     Segment sg;
     bool more = p.whole ? share.end > 0 : walk.next(p, sg);

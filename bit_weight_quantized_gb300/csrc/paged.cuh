@@ -96,7 +96,7 @@ __device__ __forceinline__ long long key_offset(const qmm_paged_kv &kv, const Fa
 }
 
 // ---- the split of an attention call --------------------------------------------------
-// An item is one row tile of one sequence with one key head: ROWS consecutive rows
+// An item is one row tile of one sequence with one key head: tile_rows consecutive rows
 // of the sequence's (token, query head of the key head) pairs, token-major, with the
 // keys [lo, hi) that any of them sees.  Its work is counted in units of KEYS keys
 // (aligned to KEYS), at least one so that rows without keys are written too.
@@ -111,17 +111,17 @@ struct RowTile {
     int unit0, units;
 };
 
-template <int ROWS, int KEYS>
+template <int KEYS>
 __device__ __forceinline__ RowTile row_tile(const AttnParams &p, int i)
 {
     RowTile r;
     r.b = p.by_tiles(i);
-    r.row0 = (i - r.b * p.row_tiles) * ROWS;
+    r.row0 = (i - r.b * p.row_tiles) * p.tile_rows;
     const int2 tn = seq_tokens(p.kv, r.b);
     r.t0 = tn.x;
     r.n = tn.y;
     const long long all = static_cast<long long>(r.n) * p.group;
-    r.rows = static_cast<int>(min(static_cast<long long>(ROWS), max(0LL, all - r.row0)));
+    r.rows = static_cast<int>(min(static_cast<long long>(p.tile_rows), max(0LL, all - r.row0)));
     r.kv = seq_keys(p.kv, r.b, p.status);
     r.lo = r.hi = r.unit0 = r.units = 0;
     if (r.rows == 0)
@@ -171,21 +171,21 @@ __device__ __forceinline__ long long divide(long long a, long long b)
 
 // Called by all THREADS threads of the block; `red` is scratch of THREADS / 32
 // words of 8 bytes, `out` the shared result.
-template <int ROWS, int KEYS, int SETUP, int THREADS>
+template <int KEYS, int SETUP, int THREADS>
 __device__ __forceinline__ void find_share(const AttnParams &p, long long *red, Share *out)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (p.whole && !p.unsplit) {   // cluster (or block) c holds item c
         if (tid == 0) {
             const int item = blockIdx.x / p.cluster, i = item / p.kv.kv_heads;
-            const RowTile r = row_tile<ROWS, KEYS>(p, i);
+            const RowTile r = row_tile<KEYS>(p, i);
             out->i = i;
             out->r = r;
             out->h = item - i * p.kv.kv_heads;
             out->at = out->start = 0;
             out->end = r.units ? SETUP + r.units : 0;
             out->chunk = 1LL << 40;
-            if (r.row0 == 0 && static_cast<long long>(r.n) * p.group > static_cast<long long>(p.row_tiles) * ROWS)
+            if (r.row0 == 0 && static_cast<long long>(r.n) * p.group > static_cast<long long>(p.row_tiles) * p.tile_rows)
                 record_error(p.status, QMM_ERR_INDEX);
         }
         __syncthreads();
@@ -197,9 +197,9 @@ __device__ __forceinline__ void find_share(const AttnParams &p, long long *red, 
     long long sum = 0;
     RowTile r;
     for (int i = i0; i < i1; ++i) {
-        r = row_tile<ROWS, KEYS>(p, i);
+        r = row_tile<KEYS>(p, i);
         sum += static_cast<long long>(r.units ? SETUP + r.units : 0) * p.kv.kv_heads;
-        if (r.row0 == 0 && static_cast<long long>(r.n) * p.group > static_cast<long long>(p.row_tiles) * ROWS)
+        if (r.row0 == 0 && static_cast<long long>(r.n) * p.group > static_cast<long long>(p.row_tiles) * p.tile_rows)
             record_error(p.status, QMM_ERR_INDEX);   // more new tokens than max_q
     }
     long long incl = sum;
@@ -231,7 +231,7 @@ __device__ __forceinline__ void find_share(const AttnParams &p, long long *red, 
         long long start = before;
         for (int i = i0; i < i1; ++i) {
             if (per > 1)
-                r = row_tile<ROWS, KEYS>(p, i);
+                r = row_tile<KEYS>(p, i);
             const int len = r.units ? SETUP + r.units : 0;
             const long long all = static_cast<long long>(len) * p.kv.kv_heads;
             if (at < start + all) {
@@ -258,7 +258,7 @@ struct Segment {
 };
 
 // Walks a share.  next() gives its segments in order.
-template <int ROWS, int KEYS, int SETUP>
+template <int KEYS, int SETUP>
 struct Walk {
     long long at, end, chunk, start;
     int i, h;
@@ -282,7 +282,7 @@ struct Walk {
             do {
                 if (++i >= p.kv.batch * p.row_tiles)
                     return false;
-                r = row_tile<ROWS, KEYS>(p, i);
+                r = row_tile<KEYS>(p, i);
             } while (r.units == 0);
         }
         return true;

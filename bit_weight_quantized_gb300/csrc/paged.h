@@ -55,6 +55,7 @@ struct AttnParams {
     // of `box` slots (chunk kernel; box = 0: no tensor copies); page i, head h is
     // index i * page_step + h
     alignas(64) CUtensorMap tmk, tmv;
+    alignas(64) CUtensorMap tmq;   // the queries as [token][head][D], boxes of one stream's rows (chunk kernel)
     int box, page_step;
     qmm_paged_kv kv;
     const uint16_t *q;
@@ -68,6 +69,7 @@ struct AttnParams {
     float scale_log2;              // scale * log2(e): the softmax works in powers of two
     int q_heads, group;            // query heads, query heads per key head
     int causal, window;
+    int tile_rows;                 // rows per tile
     int row_tiles;                 // row tiles per sequence (of the longest one)
     FastDiv by_group, by_tiles, by_page;   // divisions by group, row_tiles, page_size
     int whole;                     // every item in one cluster or block: no partial results
@@ -83,10 +85,12 @@ constexpr int kDecodeRows = 16;
 // (decode kernel: 8 KB of K and V per warp)
 __host__ __device__ constexpr int decode_keys(int head_dim, int warps) { return (head_dim == 64 ? 32 : 16) * warps; }
 constexpr int kChunkRows = 256, kChunkKeys = 128;
+// (chunk kernel: whole tokens' rows, at most 128 in each of its two streams)
+__host__ __device__ constexpr int chunk_stream_rows(int group) { return 128 / group * group; }
 // What starting and finishing an item costs, in units (see find_share).  Chunk kernel:
-// about 9000 cycles against 2400 a unit; an 8192-token prompt takes 466, 361 and 368 us
-// with 2, 4 and 6.
-constexpr int kDecodeSetup = 1, kChunkSetup = 4;
+// about 5000 cycles against 2400 a unit; a 2048-token prompt takes 45.7, 41.6, 42.5 and
+// 42.9 us with 1 to 4, one of 8192 405, 338, 336 and 340.
+constexpr int kDecodeSetup = 1, kChunkSetup = 2;
 
 // Blocks per cluster of the decode kernel at most.
 constexpr int kMaxCluster = 8;
@@ -103,6 +107,8 @@ cudaError_t launch_attn_chunk(const AttnParams &p, int grid, cudaStream_t stream
 
 // Sets p.box and the tensor maps where the cache takes tensor copies.
 void attn_set_tma(AttnParams &p);
+// Tensor map of the queries (chunk kernel); false where there can be none.
+bool attn_set_q_tma(AttnParams &p);
 
 // Scratch of a call, and the whole call: kernel choice, split and launches.
 size_t attn_workspace_bytes(int q_heads, int kv_heads, int head_dim, int max_q, int num_sms);

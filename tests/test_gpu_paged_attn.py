@@ -72,7 +72,7 @@ def test_pages_and_layouts(q, page, layout, n):
     check(q, Batch([n, n, n], [n, n + 133, n + 470], 4, 2, 128, "f16", page=page, layout=layout, seed=page))
 
 
-@pytest.mark.parametrize("heads", [(1, 1), (3, 3), (6, 2), (7, 1), (16, 1), (17, 1), (64, 1), (40, 8), (32, 32)])
+@pytest.mark.parametrize("heads", [(1, 1), (3, 3), (6, 2), (7, 1), (16, 1), (17, 1), (64, 1), (40, 8), (32, 32), (100, 1), (128, 1), (258, 2)])
 @pytest.mark.parametrize("n", [1, 4, 50])
 def test_head_groups(q, heads, n):
     check(q, Batch([n, n], [n + 77, n + 300], *heads, 64, "bf16", seed=heads[0]))
@@ -221,6 +221,14 @@ def test_query_views_and_given_buffers(q, route):
 
 
 # a size of one may come with any stride
+# every token has the same queries: a stride of zero
+@pytest.mark.parametrize("n", [1, 60])
+def test_broadcast_queries(q, n):
+    bt = Batch([n, n], [n + 30, n + 400], 8, 2, 64, "bf16", seed=3)
+    bt.q = bt.q[:1].expand(bt.T, -1, -1)
+    check(q, bt)
+
+
 @pytest.mark.parametrize("n", [1, 40])
 def test_strides_of_single_things(q, n):
     bt = Batch([n], [n + 100], 4, 1, 64, seed=4)
