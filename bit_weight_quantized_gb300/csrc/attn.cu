@@ -225,26 +225,29 @@ constexpr int kMinDecodeUnits = 5, kMinChunkUnits = 6;
 // window of 1000, work 12: 35.6, split 36.8; prompts of 2048, work 18: 49.9, split 41.6.
 constexpr int kUnsplitWork = 12;
 
-// Units a block of a cluster takes at most, of four warps and (wide) of eight, twice the
-// keys: one token over 8000 keys 18.9 us at 16 units of four warps, 12.3 split over all
-// blocks and joined; four over 4000, 8 units, 12.9 against 14.6.
-constexpr int kClusterUnits = 8, kWideUnits = 4;
+// Whole items in clusters against a split over all blocks: a cluster's block walks
+// units / c, a split one units * items / blocks and the joining kernel's time, some 5
+// units; and not more than 12 units, since whole items are not balanced where lengths
+// differ.  One token over 8000 keys 11.6 us in clusters (8 units), 12.0 split; 16000 keys
+// (16) 18.9 and 14.6; eight over 3000 (12) 15.8 and 18.4.
+constexpr int kJoinUnits = 5, kMostUnits = 12;
 
 // Blocks per item of the decode kernel, and their warps, where every item gets a cluster
 // (or block) of its own: clusters of the largest size that all run at once (eight
 // clusters of eight on 64 SMs do, sixteen on 128 do not: 12.0 us for 24 rows over 1000
-// keys, 7.9 in sixteen of four), each block's stretch short enough to cost less than the
-// joining kernel.  Eight warps a block where an SM is free for each: one token over 200
-// keys 5.5 us against 6.4 with four, over 2000 7.1 against 8.2.  Items short enough for
-// one block go there however many they are.  0: the axis is split over all blocks.
+// keys, 7.9 in sixteen of four).  Eight warps a block where an SM is free for each: one
+// token over 2000 keys 6.2 us against 7.4 with four, over 4000 8.1 against 10.4.  Items
+// short enough for one block go there however many they are.  0: the axis is split over
+// all blocks.
 int decode_cluster(const AttnParams &p, long long items, long long max_kv, int num_sms, int *warps)
 {
     const bool bf16 = p.kv.dtype == QMM_BF16;
     for (*warps = 8; *warps >= 4; *warps /= 2) {
-        const int keys = decode_keys(p.kv.head_dim, *warps), most = *warps == 8 ? kWideUnits : kClusterUnits;
+        const int keys = decode_keys(p.kv.head_dim, *warps);
         const long long units = (max_kv + keys - 1) / keys, blocks = *warps == 8 ? num_sms : kDecodeBlocksPerSm * num_sms;
         for (int c = kMaxCluster; c >= 1; c /= 2)
-            if (items * c <= blocks && (c == 1 || c / 2 < units) && (units + c - 1) / c <= most &&
+            if (items * c <= blocks && (c == 1 || c / 2 < units) && (units + c - 1) / c <= kMostUnits &&
+                (units + c - 1) / c <= items * units / blocks + kJoinUnits &&
                 (c == 1 || items <= attn_decode_clusters(p.kv.head_dim, bf16, *warps, c)))
                 return c;
     }
@@ -270,8 +273,8 @@ cudaError_t attn_dispatch(AttnParams &p, int max_q, long long max_kv, void *work
     int warps;
     const int cluster = decode_cluster(p, ditems, max_kv, num_sms, &warps);
     // more rows go to it too where its items, sixteen rows each, all run at once: it
-    // starts faster and needs no join (64 tokens over 1000 keys 13.6 us against the chunk
-    // kernel's 18.9, 128 over 128 6.3 against 8.7; but 4 x 50 over 200, 416 items on 304
+    // starts faster and needs no join (64 tokens over 1000 keys 11.4 us against the chunk
+    // kernel's 18.3, 128 over 128 6.0 against 8.0; but 4 x 50 over 200, 416 items on 304
     // blocks, 13.9 against 9.6, and 5 over 4000 of 32 sequences, split, 243 against 94)
     // (and queries that the chunk kernel's tensor copies do not take: groups of over 128
     // heads, strides of zero)

@@ -14,8 +14,9 @@
 //
 // Long axes are split over all blocks (find_share) and joined by a second kernel
 // (attn.cu).  Short ones, where that kernel's 3.5 us would count, go to a cluster of
-// up to eight blocks per item, which joins its parts through its blocks' shared memory;
-// blocks of eight warps halve its walk where an SM is free for each.
+// up to eight blocks per item, each of which sends the others their share of its part to
+// join, from shared memory to shared memory; blocks of eight warps halve its walk where
+// an SM is free for each.  One token over 517 keys: 5.2 us.
 //
 // The running maximum is replaced only when it grows by more than 2^8 (the scale
 // factors stay within fp32 and fp16 range either way), so the output is rescaled
@@ -40,11 +41,14 @@ struct DecLayout {
     static constexpr int kStages = 3;                                     // 24 KB of rings per warp
     static constexpr int kWarpBytes = kStages * 2 * kTile;
     static constexpr int kOffQ = WARPS * kWarpBytes;
-    static constexpr int kBytes = kOffQ + kDecodeRows * D * 2;
+    // what the cluster's blocks send this one: [value / 4 / blocks][block] four values,
+    // [row][block] maximum and sum
+    static constexpr int kOffIn = kOffQ + kDecodeRows * D * 2;
+    static constexpr int kOffInMl = kOffIn + kDecodeRows * D * 4;
+    static constexpr int kBytes = kOffInMl + kDecodeRows * kMaxCluster * 8;
     static constexpr int kPitch = D + 8;                                  // floats per row of a warp's output
     static constexpr int kOffMl = WARPS * kDecodeRows * kPitch * 4;   // the warps' maxima and sums
-    static constexpr int kOffSum = kOffMl + WARPS * kDecodeRows * 8;  // the block's output, maxima and sums
-    static_assert(kOffSum + kDecodeRows * (D + 2) * 4 <= kOffQ, "the warps' outputs reuse the rings");
+    static_assert(kOffMl + WARPS * kDecodeRows * 8 <= kOffQ, "the warps' outputs reuse the rings");
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr)
@@ -92,27 +96,19 @@ __device__ __forceinline__ uint32_t peer_addr(uint32_t addr, int rank)
     return r;
 }
 
-__device__ __forceinline__ float2 peer_load2(uint32_t addr)
+__device__ __forceinline__ void peer_store2(uint32_t addr, float a, float b)
 {
-    float2 v;
-    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
-    return v;
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(a), "f"(b) : "memory");
 }
 
-__device__ __forceinline__ float4 peer_load4(uint32_t addr)
+__device__ __forceinline__ void peer_store4(uint32_t addr, const float4 &v)
 {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
                  : "memory");
-    return v;
 }
 
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // WARPS = 4: two blocks per SM; 8: one, for clusters where every block has an SM.
 template <int D, bool BF16, int WARPS>
@@ -135,6 +131,8 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
     const int g = lane >> 2, t = lane & 3;
     if (tid == 0)
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (p.cluster > 1)
+        cluster_arrive();   // (waited for before anything is sent to another block)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     find_share<kKeys, kDecodeSetup, kDecThreads>(p, red, &share);
 
@@ -162,21 +160,35 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
         sg.off = rank * all / p.cluster;
         sg.units = (rank + 1) * all / p.cluster - sg.off;
     }
+    if (!more && p.cluster > 1)
+        cluster_wait();
     for (; more; more = !p.whole && walk.next(p, sg)) {
         const RowTile &r = sg.r;
         const uint16_t *kbase = static_cast<const uint16_t *>(p.kv.k) + sg.h * p.kv.head_stride;
         const uint16_t *vbase = static_cast<const uint16_t *>(p.kv.v) + sg.h * p.kv.head_stride;
         const int key0 = (r.unit0 + sg.off) * kKeys + warp * kWarpKeys;   // the warp's first key
 
-        // Where tile j lies, looked up one tile ahead: where a tile's keys share a page
-        // (p.same_page), the offset of the lane's first row; else that of row `lane`.
-        // -1: nothing is read.
-        auto place = [&](int j) -> long long {
-            const int key = key0 + j * kKeys + (p.same_page ? 0 : lane % kWarpKeys);
-            if (j >= sg.units || key >= r.hi || (p.same_page ? key + kWarpKeys <= r.lo : key < r.lo))
+        // Where tile j lies: where a tile's keys share a page (p.same_page), the offset of
+        // the lane's first row; else that of row `lane`.  -1: nothing is read.  The page is
+        // looked up one tile ahead and not looked at before the tile is loaded: the warp
+        // would wait for the table's entry here.
+        auto key_of = [&](int j) { return key0 + j * kKeys + (p.same_page ? 0 : lane % kWarpKeys); };
+        auto reads = [&](int j) {
+            const int key = key_of(j);
+            return j < sg.units && key < r.hi && (p.same_page ? key + kWarpKeys : key + 1) > r.lo;
+        };
+        auto look_up = [&](int j) -> int {
+            return reads(j) ? p.kv.block_table[static_cast<long long>(r.b) * p.kv.blocks + p.by_page(key_of(j))] : 0;
+        };
+        auto place = [&](int j, int page) -> long long {
+            if (!reads(j))
                 return -1;
-            const long long off = key_offset(p.kv, p.by_page, r.b, key, p.status);
-            return p.same_page && off >= 0 ? off + crow * p.kv.slot_stride : off;
+            if (page < 0 || page >= p.kv.num_pages) {
+                record_error(p.status, QMM_ERR_INDEX);
+                return -1;
+            }
+            const int key = key_of(j), slot = key - p.by_page(key) * p.kv.page_size;
+            return page * p.kv.page_stride + (slot + (p.same_page ? crow : 0)) * p.kv.slot_stride;
         };
         auto load = [&](int j, long long off) {
             const uint32_t dst = ring + (j % L::kStages) * (2 * L::kTile);
@@ -206,6 +218,11 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
             }
         };
 
+        int page[L::kStages - 1];
+#pragma unroll
+        for (int j = 0; j < L::kStages - 1; ++j)
+            page[j] = look_up(j);
+        int ahead = look_up(L::kStages - 1);
         // queries: 16 rows, zero past the tile
         for (int e = tid; e < kDecodeRows * kChunks; e += kDecThreads) {
             const int row = e / kChunks, c = e % kChunks, rr = r.row0 + row, tok = p.by_group(rr);
@@ -216,13 +233,11 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
             cp_async16_or_zero(qs + tile_addr<D>(row, c), src, in);
         }
         cp_async_commit();
-        long long ahead = place(0);
 #pragma unroll
         for (int j = 0; j < L::kStages - 1; ++j) {
             if (j < sg.units)
-                load(j, ahead);
+                load(j, place(j, page[j]));
             cp_async_commit();
-            ahead = place(j + 1);
         }
 
         // the queries have landed (the copies after them are still under way); to
@@ -250,9 +265,9 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
 #pragma unroll 1
         for (int j = 0; j < sg.units; ++j) {
             if (j + L::kStages - 1 < sg.units)
-                load(j + L::kStages - 1, ahead);
+                load(j + L::kStages - 1, place(j + L::kStages - 1, ahead));
             cp_async_commit();
-            ahead = place(j + L::kStages);
+            ahead = look_up(j + L::kStages);
             cp_async_wait_group<L::kStages - 1>();
             __syncwarp();
             const int kb = key0 + j * kKeys;
@@ -359,6 +374,23 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
             }
         }
         __syncthreads();
+        const int rank = blockIdx.x % p.cluster, log2_blocks = 31 - __clz(p.cluster);
+        if (p.cluster > 1) {
+            cluster_wait();      // every block of the cluster has started
+            // the block's maxima and sums of all rows to every block
+            for (int e = tid; e < r.rows << log2_blocks; e += kDecThreads) {
+                const int row = e >> log2_blocks;
+                float m = -INFINITY, l = 0.f;
+#pragma unroll
+                for (int w = 0; w < WARPS; ++w)
+                    m = fmaxf(m, wml[(w * kDecodeRows + row) * 2]);
+                const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+                for (int w = 0; w < WARPS; ++w)
+                    l = fmaf(ex2(wml[(w * kDecodeRows + row) * 2] - base), wml[(w * kDecodeRows + row) * 2 + 1], l);
+                peer_store2(peer_addr(sbase + L::kOffInMl + (row * p.cluster + rank) * 8, e & (p.cluster - 1)), m, l);
+            }
+        }
         const bool whole = is_whole(sg);
         const int slot = part_slot(sg);
         // four finished values of a row to the output
@@ -391,10 +423,8 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
                 acc.z = fmaf(a, v.z, acc.z);
                 acc.w = fmaf(a, v.w, acc.w);
             }
-            if (p.cluster > 1) {
-                *reinterpret_cast<float4 *>(smem + L::kOffSum + (row * D + c) * 4) = acc;
-                if (c == 0)
-                    *reinterpret_cast<float2 *>(smem + L::kOffSum + (kDecodeRows * D + 2 * row) * 4) = make_float2(m, l);
+            if (p.cluster > 1) {   // four values to the block that joins them
+                peer_store4(peer_addr(sbase + L::kOffIn + ((e >> log2_blocks) * p.cluster + rank) * 16, e & (p.cluster - 1)), acc);
             } else if (whole) {
                 store(row, c, m, l, acc);
             } else {
@@ -405,32 +435,21 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
             }
         }
         if (p.cluster > 1) {
-            // the blocks' parts meet, each block joins its share of the values
-            cluster_sync();
-            const int rank = blockIdx.x % p.cluster;
-            for (int e = tid * p.cluster + rank; e < r.rows * (D / 4); e += p.cluster * kDecThreads) {
-                const int row = e / (D / 4), c = 4 * (e % (D / 4));
-                const uint32_t ml_at = sbase + L::kOffSum + (kDecodeRows * D + 2 * row) * 4;
-                const uint32_t o_at = sbase + L::kOffSum + (row * D + c) * 4;
+            // each block joins its share of the values.  They have been sent to it: reading
+            // them from the others takes a second meeting, before which no block may leave,
+            // and 1 us more.
+            cluster_arrive();
+            cluster_wait();
+            for (int i = tid; i < (r.rows * (D / 4)) >> log2_blocks; i += kDecThreads) {
+                const int e = (i << log2_blocks) + rank, row = e / (D / 4), c = 4 * (e % (D / 4));
+                const float4 *v = reinterpret_cast<const float4 *>(smem + L::kOffIn) + (i << log2_blocks);
+                const float2 *ml = reinterpret_cast<const float2 *>(smem + L::kOffInMl) + (row << log2_blocks);
                 float m = -INFINITY, l = 0.f;
                 float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                float2 ml[kMaxCluster];      // all reads are under way together
-                float4 v[kMaxCluster];
-#pragma unroll
-                for (int b = 0; b < kMaxCluster; ++b) {
-                    ml[b] = make_float2(-INFINITY, 0.f);
-                    v[b] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (b < p.cluster) {
-                        ml[b] = peer_load2(peer_addr(ml_at, b));
-                        v[b] = peer_load4(peer_addr(o_at, b));
-                    }
-                }
-#pragma unroll
-                for (int b = 0; b < kMaxCluster; ++b)
+                for (int b = 0; b < p.cluster; ++b)
                     m = fmaxf(m, ml[b].x);
                 const float base = m == -INFINITY ? 0.f : m;
-#pragma unroll
-                for (int b = 0; b < kMaxCluster; ++b) {
+                for (int b = 0; b < p.cluster; ++b) {
                     const float w = ex2(ml[b].x - base);
                     l = fmaf(w, ml[b].y, l);
                     acc.x = fmaf(w, v[b].x, acc.x);
@@ -440,7 +459,6 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
                 }
                 store(row, c, m, l, acc);
             }
-            cluster_sync();   // no block leaves while another still reads from it
             return;
         }
         if (tid == 0 && is_last_part(sg))

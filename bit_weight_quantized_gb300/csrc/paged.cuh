@@ -68,10 +68,9 @@ __device__ __forceinline__ int2 seq_tokens(const qmm_paged_kv &kv, int b)
     return make_int2(t0, t1 - t0);
 }
 
-// Keys of sequence b, held to what its row of the block table can hold.
-__device__ __forceinline__ int seq_keys(const qmm_paged_kv &kv, int b, int *status)
+// A sequence's number of keys, held to what its row of the block table can hold.
+__device__ __forceinline__ int seq_keys(const qmm_paged_kv &kv, int n, int *status)
 {
-    const int n = kv.kv_len[b];
     const long long most = static_cast<long long>(kv.blocks) * kv.page_size;
     if (n > most) {
         record_error(status, QMM_ERR_INDEX);
@@ -117,12 +116,13 @@ __device__ __forceinline__ RowTile row_tile(const AttnParams &p, int i)
     RowTile r;
     r.b = p.by_tiles(i);
     r.row0 = (i - r.b * p.row_tiles) * p.tile_rows;
+    const int keys = p.kv.kv_len[r.b];   // (the lengths' loads are under way together)
     const int2 tn = seq_tokens(p.kv, r.b);
     r.t0 = tn.x;
     r.n = tn.y;
     const long long all = static_cast<long long>(r.n) * p.group;
     r.rows = static_cast<int>(min(static_cast<long long>(p.tile_rows), max(0LL, all - r.row0)));
-    r.kv = seq_keys(p.kv, r.b, p.status);
+    r.kv = seq_keys(p.kv, keys, p.status);
     r.lo = r.hi = r.unit0 = r.units = 0;
     if (r.rows == 0)
         return r;
