@@ -154,6 +154,21 @@ __device__ __forceinline__ void tmem_ld32_start(uint32_t taddr, uint32_t *r)
         : "r"(taddr));
 }
 
+// The same, and the largest of the 32 as fp32 values (NaN left out), without waiting
+__device__ __forceinline__ void tmem_ld32_max_start(uint32_t taddr, uint32_t *r, float &most)
+{
+    asm volatile(
+        "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, %32, [%33];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+          "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=f"(most)
+        : "r"(taddr));
+}
+
 // 5-D tiled load of a box into shared memory, completing on `bar`.
 __device__ __forceinline__ void tma_load_5d(uint32_t dst, const void *tmap, uint64_t *bar, int c3, int c4)
 {
@@ -420,24 +435,16 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                     tmem_st_wait();
                 }
                 uint32_t v[kChunkKeys];
+                float mx[kChunkKeys / 32];
 #pragma unroll
                 for (int c = 0; c < kChunkKeys; c += 32)
-                    tmem_ld32_start(ts + c, v + c);
+                    tmem_ld32_max_start(ts + c, v + c, mx[c / 32]);
                 tmem_ld_wait();
 #pragma unroll
-                for (int c = 0; c < kChunkKeys; c += 32)
+                for (int c = 0; c < kChunkKeys; c += 32) {
                     pin32(v + c);
-                float mx[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    mx[e] = __uint_as_float(v[e]);
-#pragma unroll
-                for (int c = 4; c + 8 <= kChunkKeys; c += 8)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        mx[e] = max3(mx[e], __uint_as_float(v[c + 2 * e]), __uint_as_float(v[c + 2 * e + 1]));
-                mx[0] = max3(mx[0], __uint_as_float(v[kChunkKeys - 4]), __uint_as_float(v[kChunkKeys - 3]));
-                mx[1] = max3(mx[1], __uint_as_float(v[kChunkKeys - 2]), __uint_as_float(v[kChunkKeys - 1]));
+                    asm volatile("" : "+f"(mx[c / 32]));
+                }
                 const float m = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * p.scale_log2;
                 const bool up = m > mref + kChunkGrow;
                 if (__any_sync(0xffffffffu, up)) {
