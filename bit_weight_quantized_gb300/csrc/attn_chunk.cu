@@ -73,8 +73,8 @@ struct ChunkLayout {
     static constexpr int kOffV = kOffK + kKRing * kTile;
     static constexpr int kOffBar = kOffV + kVRing * kTile;
     // full / empty of both rings, patch, per stream q_full, q_empty, s_full, p_full (two halves) and
-    // o_full, x_full, x_done, drain, full / empty of the segments
-    static constexpr int kNumBars = 2 * (kKRing + kVRing) + 16 + 2 * kSegs;
+    // pv_done, o_full, x_full, x_done, drain, full / empty of the segments
+    static constexpr int kNumBars = 2 * (kKRing + kVRing) + 18 + 2 * kSegs;
     static constexpr int kOffTmem = kOffBar + 8 * kNumBars;
     static constexpr int kOffShare = kOffTmem + 16;
     static constexpr int kOffRed = kOffShare + sizeof(Share);
@@ -85,10 +85,18 @@ struct ChunkLayout {
     static_assert(kBytes <= 227 * 1024, "shared memory per block");
 };
 
-// Tensor-memory columns of stream s: S (and P, half h of it), and O.
+// Tensor-memory columns of stream s: S, half h of P, and O.  At D = 64 there is room for
+// P beside S, so that the next scores are computed while the weights still are.
+template <int D>
+constexpr bool kBeside = D == 64;
 __device__ __forceinline__ uint32_t s_col(int s) { return static_cast<uint32_t>(s) * 128u; }
-__device__ __forceinline__ uint32_t p_col(int s, int h) { return s_col(s) + static_cast<uint32_t>(h) * 32u; }
-__device__ __forceinline__ uint32_t o_col(int s) { return 256u + static_cast<uint32_t>(s) * 128u; }
+template <int D>
+__device__ __forceinline__ uint32_t p_col(int s, int h)
+{
+    return (kBeside<D> ? 384u + static_cast<uint32_t>(s) * 64u : s_col(s)) + static_cast<uint32_t>(h) * 32u;
+}
+template <int D>
+__device__ __forceinline__ uint32_t o_col(int s) { return 256u + static_cast<uint32_t>(s * D); }
 
 // Query tiles lie as halves of 64 values, rows of 128 bytes, chunks of 16 bytes permuted
 // by the row (the 128-byte swizzle).
@@ -305,7 +313,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
     uint64_t *v_full = k_empty + L::kKRing, *v_empty = v_full + L::kVRing, *patch = v_empty + L::kVRing;
     uint64_t *q_full = patch + 1, *q_empty = q_full + 2, *s_full = q_empty + 2, *p_full = s_full + 2, *o_full = p_full + 4;
     uint64_t *x_full = o_full + 2, *x_done = x_full + 1, *drain = x_done + 1;
-    uint64_t *seg_full = drain + 1, *seg_empty = seg_full + kSegs;
+    uint64_t *pv_done = drain + 1, *seg_full = pv_done + 2, *seg_empty = seg_full + kSegs;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kOffTmem);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -331,6 +339,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
             mbar_init(&p_full[2 * s], kSoftWarps);
             mbar_init(&p_full[2 * s + 1], kSoftWarps);
             mbar_init(&o_full[s], 1);
+            mbar_init(&pv_done[s], 1);
         }
         mbar_init(x_full, kSoftWarps);
         mbar_init(x_done, kSoftWarps);
@@ -374,10 +383,12 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
         const int s = warp / kSoftWarps, quarter = warp % kSoftWarps;
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-        const uint32_t ts = tmem + lanes + s_col(s), to = tmem + lanes + o_col(s);
+        const uint32_t ts = tmem + lanes + s_col(s), to = tmem + lanes + o_col<D>(s);
+        const uint32_t tp = tmem + lanes + p_col<D>(s, 0);
         float2 *x_ml = reinterpret_cast<float2 *>(smem + L::kOffX);
         uint32_t ph = 0;         // parity of the next S
         uint32_t oph = 0;        // parity of the next O
+        uint32_t dph = 1;        // parity of the last tile's products into O (none at first)
         uint32_t xph = 0;        // parity of the next exchange between the streams
         for (int n = 0;; ++n) {
             const Segment &sg = segment(n);
@@ -446,12 +457,20 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                     asm volatile("" : "+f"(mx[c / 32]));
                 }
                 const float m = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * p.scale_log2;
+                bool done = !kBeside<D>;     // whether the last tile's products are known to be complete
+                auto pv_complete = [&]() {
+                    if (!done)
+                        ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[s], dph, p.status));
+                    done = true;
+                    tc_fence_after();
+                };
                 const bool up = m > mref + kChunkGrow;
                 if (__any_sync(0xffffffffu, up)) {
                     const float a = up ? ex2(mref - m) : 1.f;
                     mref = up ? m : mref;
                     l *= a;
                     if (j > j0) {
+                        pv_complete();
 #pragma unroll 1
                         for (int c = 0; c < D; c += 32) {
                             uint32_t o[32];
@@ -482,7 +501,9 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                         sum[e & 1] = add2(sum[e & 1], pair(__float_as_uint(p0), __float_as_uint(p1)));
                         w[e] = pack16<BF16>(p0, p1);
                     }
-                    tmem_st16(ts + 16 * c, w);
+                    if (kBeside<D> && c == 2)    // (its place may still be read)
+                        pv_complete();
+                    tmem_st16(tp + 16 * c, w);
                     if (c & 1) {
                         tmem_st_wait();
                         tc_fence_before();
@@ -494,6 +515,9 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                 float s0, s1;
                 unpair(add2(sum[0], sum[1]), s0, s1);
                 l += s0 + s1;
+                dph ^= 1u;
+                if (!ok)
+                    break;
             }
             if (ok)
                 ok = __all_sync(0xffffffffu, mbar_wait(&o_full[s], oph, p.status));
@@ -550,7 +574,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                 pin32(o);
                 if (two) {
                     uint32_t o1[32];
-                    tmem_ld32_start(tmem + lanes + o_col(1) + c, o1);
+                    tmem_ld32_start(tmem + lanes + o_col<D>(1) + c, o1);
                     tmem_ld_wait();
                     pin32(o1);
 #pragma unroll
@@ -639,23 +663,25 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                 }
                 __syncwarp();
             };
-            // O of stream s (+)= P V, V in slot vs, half by half as the weights come
-            auto pv = [&](int s, int vs, bool first, bool last) {
+            // O of stream s (+)= P V for half h of a tile, V in slot vs, when its weights have
+            // come
+            auto pv = [&](int s, int h, int vs, bool first, bool last) {
+                wait(&p_full[2 * s + h], pph >> s & 1u);
+                const uint64_t b = v_desc + static_cast<uint32_t>((vs * L::kTile + h * (L::kTile / 2)) >> 4);
+                if (elect_one()) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    wait(&p_full[2 * s + h], pph >> s & 1u);
-                    const uint64_t b = v_desc + static_cast<uint32_t>((vs * L::kTile + h * (L::kTile / 2)) >> 4);
-                    if (elect_one()) {
-#pragma unroll
-                        for (int e = 0; e < kHalf / 16; ++e)
-                            tc_mma_ts(tmem + o_col(s), tmem + p_col(s, h) + 8 * e, b + e * (2 * D * 16 / 16), id_pv,
-                                      h > 0 || e > 0 || !first ? 1u : 0u);
-                        if (h == 1 && last)
-                            tc_commit(&v_empty[vs]);
-                    }
+                    for (int e = 0; e < kHalf / 16; ++e)
+                        tc_mma_ts(tmem + o_col<D>(s), tmem + p_col<D>(s, h) + 8 * e, b + e * (2 * D * 16 / 16), id_pv,
+                                  h > 0 || e > 0 || !first ? 1u : 0u);
+                    if (kBeside<D> && h == 1)
+                        tc_commit(&pv_done[s]);
+                    if (h == 1 && last)
+                        tc_commit(&v_empty[vs]);
                 }
-                __syncwarp();
-                pph ^= 1u << s;
+                if (h == 1) {
+                    __syncwarp();
+                    pph ^= 1u << s;
+                }
             };
             auto finish = [&](int s) {   // stream s's last product of the segment
                 if (elect_one())
@@ -688,10 +714,15 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                         for (int s = 0; s < 2; ++s) {
                             const int j = j0 + s;
                             if (j < units) {
-                                pv(s, v_landed(j), j0 == 0, true);
+                                const int vs = v_landed(j);
+                                pv(s, 0, vs, j0 == 0, true);
+                                if (!kBeside<D>)
+                                    pv(s, 1, vs, j0 == 0, true);
                                 if (j + 2 < units)
                                     qk(s, 0, k_landed(j + 2), true, j + 3 == units);
-                                else
+                                if (kBeside<D>)
+                                    pv(s, 1, vs, j0 == 0, true);
+                                if (j + 2 >= units)
                                     finish(s);
                             }
                         }
@@ -708,14 +739,18 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                         const bool more = j + 1 < units;
 #pragma unroll
                         for (int s = 0; s < 2; ++s) {
-                            pv(s, vs, j == 0, s == 1);
+                            pv(s, 0, vs, j == 0, s == 1);
+                            if (!kBeside<D>)
+                                pv(s, 1, vs, j == 0, s == 1);
                             if (more) {
                                 if (s == 0)
                                     ks = k_landed(j + 1);
                                 qk(s, s, ks, s == 1, j + 2 == units);
-                            } else {
-                                finish(s);
                             }
+                            if (kBeside<D>)
+                                pv(s, 1, vs, j == 0, s == 1);
+                            if (!more)
+                                finish(s);
                         }
                     }
                 }
