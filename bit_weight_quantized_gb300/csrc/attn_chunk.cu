@@ -38,11 +38,13 @@
 // The running maximum is replaced only when it grows by more than 2^8: the output
 // accumulator in tensor memory is then read, scaled and written back by its
 // stream's own threads, a few times per item.  S's arrival says that the product
-// before it into O is complete, so that needs no signal of its own.
+// before it into O is complete, so that needs no signal of its own (D = 64, where the
+// next S is computed under it: pv_done).
 //
-// Bound by the tensor cores at D = 128 (4096 x 4096 x 32 heads: 1480 TFLOP/s, 79% of
-// the measured bf16 rate; products and signals alone, the softmax left out, 1687), by
-// the softmax at D = 64 (844 and 1261).
+// Bound by the tensor cores at D = 128 (a causal prompt of 8192 tokens x 64 heads: 1655
+// TFLOP/s, 88% of the measured bf16 burst rate, until the power limit brings it to 1500;
+// products and signals alone, the softmax left out, 1687 for 4096 x 4096 x 32), by the
+// issuing warp and the softmax at D = 64 (4096 x 4096 x 32 heads: 132 us, 1041).
 #include "gemm.cuh"
 #include "paged.cuh"
 
