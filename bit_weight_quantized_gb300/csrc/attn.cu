@@ -216,14 +216,19 @@ size_t scratch_bytes(bool few, int head_dim, int num_sms)
 }
 
 // Work a block takes at least, in units: below this a split costs more (a second
-// kernel, the partial results) than the longer walk.
-constexpr int kMinDecodeUnits = 5, kMinChunkUnits = 6;
+// kernel, the partial results) than the longer walk.  (Chunk kernel, 30 items of up to 12
+// units: 18.1 us, with 6 20.4.)
+constexpr int kMinDecodeUnits = 5, kMinChunkUnits = 4;
 
 // Work of the longest item (setup and units) up to which blocks of the chunk kernel take
 // whole items: no joining kernel, against blocks of unequal work by up to one item.  Four
 // sequences of up to 1000 tokens, work 10: 47.8 us, split 49.5; seven chunks with a
 // window of 1000, work 12: 35.6, split 36.8; prompts of 2048, work 18: 49.9, split 41.6.
 constexpr int kUnsplitWork = 12;
+
+// The same where every item has a block of its own (20 items of up to 6 units: 14.6 us,
+// split 19.3).
+constexpr int kWholeWork = 10;
 
 // Whole items in clusters against a split over all blocks: a cluster's block walks
 // units / c, a split one units * items / blocks and the joining kernel's time, some 5
@@ -232,28 +237,44 @@ constexpr int kUnsplitWork = 12;
 // (16) 18.9 and 14.6; eight over 3000 (12) 15.8 and 18.4.
 constexpr int kJoinUnits = 5, kMostUnits = 12;
 
+// What starting an item costs a block, in units, and the items (in 16 keys at head size
+// 128) that are short enough for one block however many they are.  Blocks of one warp take
+// four times the units of those of four and fit seven to an SM instead of two: 1728 items
+// of 4 keys 8.0 us against 20.5, 2048 of 256 keys 44 against 51, 512 of 256 keys 16.4
+// against 13.2.
+constexpr int kStartUnits = 3, kWholeKeys = 16;
+
 // Blocks per item of the decode kernel, and their warps, where every item gets a cluster
 // (or block) of its own: clusters of the largest size that all run at once (eight
 // clusters of eight on 64 SMs do, sixteen on 128 do not: 12.0 us for 24 rows over 1000
 // keys, 7.9 in sixteen of four).  Eight warps a block where an SM is free for each: one
 // token over 2000 keys 6.2 us against 7.4 with four, over 4000 8.1 against 10.4.  Items
-// short enough for one block go there however many they are.  0: the axis is split over
-// all blocks.
+// short enough for one block go there however many they are, to blocks of four warps or of
+// one.  0: the axis is split over all blocks.  A window bounds the items' keys (16 tokens,
+// the last 500 of 4000 keys: 8.1 us, 11.9 without).
 int decode_cluster(const AttnParams &p, long long items, long long max_kv, int num_sms, int *warps)
 {
     const bool bf16 = p.kv.dtype == QMM_BF16;
+    // an item's keys at most, and one unit more where a window may start inside one
+    const long long span = p.window > 0 ? std::min(max_kv, static_cast<long long>(p.window) + kDecodeRows / p.group + 1) : max_kv;
+    const int more = span < max_kv;
     for (*warps = 8; *warps >= 4; *warps /= 2) {
         const int keys = decode_keys(p.kv.head_dim, *warps);
-        const long long units = (max_kv + keys - 1) / keys, blocks = *warps == 8 ? num_sms : kDecodeBlocksPerSm * num_sms;
+        const long long units = (span + keys - 1) / keys + more, blocks = *warps == 8 ? num_sms : kDecodeBlocksPerSm * num_sms;
         for (int c = kMaxCluster; c >= 1; c /= 2)
             if (items * c <= blocks && (c == 1 || c / 2 < units) && (units + c - 1) / c <= kMostUnits &&
                 (units + c - 1) / c <= items * units / blocks + kJoinUnits &&
                 (c == 1 || items <= attn_decode_clusters(p.kv.head_dim, bf16, *warps, c)))
                 return c;
     }
-    *warps = 4;
-    const int keys = decode_keys(p.kv.head_dim, 4);
-    return (max_kv + keys - 1) / keys + kDecodeSetup <= kMinDecodeUnits && items <= 0x7fffffff ? 1 : 0;
+    // more items than blocks at once: each costs its block a start and its units
+    const auto rounds = [&](int w, int blocks_per_sm) {
+        const int keys = decode_keys(p.kv.head_dim, w);
+        const long long blocks = static_cast<long long>(blocks_per_sm) * num_sms;
+        return (items + blocks - 1) / blocks * (kStartUnits + (span + keys - 1) / keys + more);
+    };
+    *warps = rounds(1, kNarrowBlocksPerSm) < rounds(4, kDecodeBlocksPerSm) ? 1 : 4;
+    return span <= kWholeKeys * decode_keys(p.kv.head_dim, 1) && items <= 0x7fffffff ? 1 : 0;
 }
 
 }  // namespace
@@ -297,7 +318,7 @@ cudaError_t attn_dispatch(AttnParams &p, int max_q, long long max_kv, void *work
     // one block or cluster per item where no item is long enough to be split over more
     p.cluster = few && cluster > 0 ? cluster : 1;
     int grid = attn_grid(few, num_sms);
-    p.whole = few ? cluster > 0 : items <= grid ? longest + setup <= p.min_chunk : longest + setup <= kUnsplitWork;
+    p.whole = few ? cluster > 0 : items <= grid ? longest + setup <= kWholeWork : longest + setup <= kUnsplitWork;
     p.unsplit = !few && p.whole && items > grid;
     if (p.whole && !p.unsplit)
         grid = static_cast<int>(items) * p.cluster;

@@ -45,7 +45,7 @@ struct DecLayout {
     // [row][block] maximum and sum
     static constexpr int kOffIn = kOffQ + kDecodeRows * D * 2;
     static constexpr int kOffInMl = kOffIn + kDecodeRows * D * 4;
-    static constexpr int kBytes = kOffInMl + kDecodeRows * kMaxCluster * 8;
+    static constexpr int kBytes = WARPS == 1 ? kOffIn : kOffInMl + kDecodeRows * kMaxCluster * 8;   // (one warp: no clusters)
     static constexpr int kPitch = D + 8;                                  // floats per row of a warp's output
     static constexpr int kOffMl = WARPS * kDecodeRows * kPitch * 4;   // the warps' maxima and sums
     static_assert(kOffMl + WARPS * kDecodeRows * 8 <= kOffQ, "the warps' outputs reuse the rings");
@@ -110,9 +110,10 @@ __device__ __forceinline__ void peer_store4(uint32_t addr, const float4 &v)
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-// WARPS = 4: two blocks per SM; 8: one, for clusters where every block has an SM.
+// WARPS = 4: two blocks per SM; 8: one, for clusters where every block has an SM; 1:
+// seven, for many short items.
 template <int D, bool BF16, int WARPS>
-__global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? kDecodeBlocksPerSm : 1)
+__global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? kDecodeBlocksPerSm : WARPS == 8 ? 1 : kNarrowBlocksPerSm)
 attn_decode_kernel(const __grid_constant__ AttnParams p)
 {
     using L = DecLayout<D, WARPS>;
@@ -131,7 +132,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
     const int g = lane >> 2, t = lane & 3;
     if (tid == 0)
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (p.cluster > 1)
+    if (WARPS > 1 && p.cluster > 1)
         cluster_arrive();   // (waited for before anything is sent to another block)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     find_share<kKeys, kDecodeSetup, kDecThreads>(p, red, &share);
@@ -160,7 +161,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
         sg.off = rank * all / p.cluster;
         sg.units = (rank + 1) * all / p.cluster - sg.off;
     }
-    if (!more && p.cluster > 1)
+    if (WARPS > 1 && !more && p.cluster > 1)
         cluster_wait();
     for (; more; more = !p.whole && walk.next(p, sg)) {
         const RowTile &r = sg.r;
@@ -375,7 +376,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
         }
         __syncthreads();
         const int rank = blockIdx.x % p.cluster, log2_blocks = 31 - __clz(p.cluster);
-        if (p.cluster > 1) {
+        if (WARPS > 1 && p.cluster > 1) {
             cluster_wait();      // every block of the cluster has started
             // the block's maxima and sums of all rows to every block
             for (int e = tid; e < r.rows << log2_blocks; e += kDecThreads) {
@@ -423,7 +424,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
                 acc.z = fmaf(a, v.z, acc.z);
                 acc.w = fmaf(a, v.w, acc.w);
             }
-            if (p.cluster > 1) {   // four values to the block that joins them
+            if (WARPS > 1 && p.cluster > 1) {   // four values to the block that joins them
                 peer_store4(peer_addr(sbase + L::kOffIn + ((e >> log2_blocks) * p.cluster + rank) * 16, e & (p.cluster - 1)), acc);
             } else if (whole) {
                 store(row, c, m, l, acc);
@@ -434,7 +435,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
                         make_float2(m, l);
             }
         }
-        if (p.cluster > 1) {
+        if (WARPS > 1 && p.cluster > 1) {
             // each block joins its share of the values.  They have been sent to it: reading
             // them from the others takes a second meeting, before which no block may leave,
             // and 1 us more.
@@ -528,7 +529,9 @@ int active_clusters(int cluster)
 template <int D, bool BF16>
 cudaError_t launch_decode_width(const AttnParams &p, int grid, cudaStream_t stream)
 {
-    return p.warps == 8 ? launch_decode_attn<D, BF16, 8>(p, grid, stream) : launch_decode_attn<D, BF16, 4>(p, grid, stream);
+    return p.warps == 8   ? launch_decode_attn<D, BF16, 8>(p, grid, stream)
+           : p.warps == 4 ? launch_decode_attn<D, BF16, 4>(p, grid, stream)
+                          : launch_decode_attn<D, BF16, 1>(p, grid, stream);
 }
 
 }  // namespace

@@ -75,7 +75,7 @@ struct AttnParams {
     int whole;                     // every item in one cluster or block: no partial results
     int unsplit;                   // whole items, several per block (chunk kernel)
     int cluster;                   // blocks per cluster (decode kernel, whole items)
-    int warps;                     // of a block of the decode kernel: 4 or 8
+    int warps;                     // of a block of the decode kernel: 1, 4 or 8
     int same_page;                 // every warp tile of the decode kernel lies in one page
     int min_chunk;                 // work a block takes at least, in units
 };
@@ -95,8 +95,8 @@ constexpr int kDecodeSetup = 1, kChunkSetup = 2;
 // Blocks per cluster of the decode kernel at most.
 constexpr int kMaxCluster = 8;
 
-// Blocks of the decode kernel per SM (it is sized for two).
-constexpr int kDecodeBlocksPerSm = 2;
+// Blocks of the decode kernel per SM (what it is sized for), of four warps and of one.
+constexpr int kDecodeBlocksPerSm = 2, kNarrowBlocksPerSm = 7;
 
 // Clusters of `cluster` (2, 4, 8) blocks of `warps` warps of the decode kernel that run at
 // once on the current device.

@@ -131,6 +131,15 @@ def test_wide_items_between_narrow_ones(q, D):
     check(q, Batch(ql, ql, 8, 8, D, "f16", seed=7))
 
 
+# more short items than run at once, some without keys, some with a window
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("most", [5, 100, 250])
+def test_many_short_items(q, D, most):
+    kl = [i * 7 % (most + 1) for i in range(150)]
+    check(q, Batch([1] * 150, kl, 16, 8, D, "f16", seed=most))
+    check(q, Batch([1] * 150, [900 + k for k in kl], 16, 8, D, "bf16", seed=most + 1), window=most)
+
+
 # ragged batches: long and short items on the same blocks
 @pytest.mark.parametrize("n", [1, 48])
 def test_ragged(q, n):
