@@ -289,6 +289,8 @@ cudaError_t attn_dispatch(AttnParams &p, int max_q, long long max_kv, void *work
     const long long most = static_cast<long long>(p.kv.blocks) * p.kv.page_size, q_rows = static_cast<long long>(max_q) * p.group;
     if (max_kv <= 0 || max_kv > most)
         max_kv = most;
+    if (p.window >= most)   // no position lies further back
+        p.window = 0;
     // the decode kernel's items
     const long long dtiles = (q_rows + kDecodeRows - 1) / kDecodeRows, ditems = p.kv.batch * dtiles * p.kv.kv_heads;
     int warps;

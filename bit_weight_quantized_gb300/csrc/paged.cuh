@@ -110,6 +110,10 @@ struct RowTile {
     int unit0, units;
 };
 
+// First key that a row at position pos sees under a window (> 0).  Compared before the
+// difference is taken: pos may be negative (padding) and the window as large as an int.
+__host__ __device__ __forceinline__ int window_start(int pos, int window) { return pos >= window ? pos - window + 1 : 0; }
+
 template <int KEYS>
 __device__ __forceinline__ RowTile row_tile(const AttnParams &p, int i)
 {
@@ -129,7 +133,7 @@ __device__ __forceinline__ RowTile row_tile(const AttnParams &p, int i)
     const int first = r.kv - r.n + p.by_group(r.row0);                     // position of the first row
     const int last = r.kv - r.n + p.by_group(r.row0 + r.rows - 1);
     r.hi = p.causal ? min(r.kv, max(0, last + 1)) : r.kv;
-    r.lo = p.window > 0 ? min(r.hi, max(0, first - p.window + 1)) : 0;
+    r.lo = p.window > 0 ? min(r.hi, window_start(first, p.window)) : 0;
     r.unit0 = r.lo / KEYS;
     r.units = max(1, (r.hi + KEYS - 1) / KEYS - r.unit0);
     return r;
@@ -142,7 +146,7 @@ __device__ __forceinline__ int2 row_keys(const AttnParams &p, const RowTile &r, 
     if (row >= r.row0 + r.rows)
         return make_int2(0, -1);
     const int pos = r.kv - r.n + p.by_group(row);
-    return make_int2(p.window > 0 ? max(0, pos - p.window + 1) : 0, p.causal ? min(r.kv - 1, pos) : r.kv - 1);
+    return make_int2(p.window > 0 ? window_start(pos, p.window) : 0, p.causal ? min(r.kv - 1, pos) : r.kv - 1);
 }
 
 // Where a block's share of the work starts.  All items of the call lie on one
