@@ -3,6 +3,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cstring>
 #include <mutex>
@@ -773,9 +774,9 @@ qmm_status qmm_paged_attn(const qmm_paged_kv *kv, const void *q, int64_t q_strid
         return QMM_ERR_NULL;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 16) || !aligned(lse, 4))
         return QMM_ERR_ALIGN;
-    // row tiles of the batch are counted in 32 bits
+    // row tiles of the batch are counted in 32 bits (no sequence has more than `tokens`)
     const int group = q_heads / kv->kv_heads;
-    if ((static_cast<long long>(max_q) * group / 16 + 1) * kv->batch > 0x7fffffffLL ||
+    if ((static_cast<long long>(std::min(max_q, kv->tokens)) * group / 16 + 1) * kv->batch > 0x7fffffffLL ||
         static_cast<long long>(kv->tokens) * group > 0x7fffffffLL)
         return QMM_ERR_UNSUPPORTED;
     const DeviceFacts *f = device_facts();

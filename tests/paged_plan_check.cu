@@ -38,7 +38,7 @@ cudaError_t launch_attn_chunk(const AttnParams &p, int grid, cudaStream_t)
 // clusters that run at once, as 152 SMs would have them in parts of 16
 int attn_decode_clusters(int, bool, int warps, int cluster) { return (warps == 8 ? 144 : 288) / cluster; }
 void attn_set_tma(AttnParams &p) { p.box = 0; }
-bool attn_set_q_tma(AttnParams &) { return q_map != 0; }
+bool attn_set_q_tma(AttnParams &p) { return q_map != 0 && p.group <= 128; }
 
 }  // namespace qmm
 

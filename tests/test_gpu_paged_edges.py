@@ -53,3 +53,50 @@ def test_window_of_any_size_beside_padding(q, n, window):
     bt = Batch([n, n + 3, 2 * n], [n // 2, 3, n + 300], 8, 2, 128, "bf16", seed=n)
     check(q, bt, window=window)
     check(q, bt, window=window, pad=4000, max_q=4000)
+
+
+# any bound on the new tokens will do, up to the largest integer
+@pytest.mark.parametrize("max_q", [2 ** 31 - 1, 2 ** 28, 70])
+@pytest.mark.parametrize("n", [1, 40])
+def test_max_q_of_any_size(q, n, max_q):
+    check(q, Batch([n, 1, n], [n + 300, 7, n], 16, 2, 64, "f16", seed=n), max_q=max_q)
+    check(q, Batch([n], [n + 2000], 8, 1, 128, "bf16", seed=n), max_q=max_q, max_kv=0)
+
+
+# The kernel for many rows on batches that the other one would take: rows of padding behind the
+# batch's tokens raise the bound on a sequence's tokens.
+MANY = dict(pad=8192, max_q=8192)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_many_rows_kernel_every_length(q, D, dtype):
+    kl = [1, 2, 3, 15, 16, 17, 31, 33, 63, 64, 65, 127, 128, 129, 200, 255, 256, 257, 511, 513]
+    check(q, Batch([1] * len(kl), kl, 8, 2, D, dtype, seed=D), **MANY)
+    check(q, Batch([3, 1, 20], [3, 9000, 500], 8, 2, D, dtype, seed=D), **MANY)
+
+
+@pytest.mark.parametrize("page,layout", [(1, "hnd"), (7, "nhd"), (8, "hnd"), (24, "gap"), (64, "nhd"), (128, "hnd"),
+                                         (200, "gap")])
+@pytest.mark.parametrize("n", [1, 70])
+def test_many_rows_kernel_pages_and_layouts(q, page, layout, n):
+    check(q, Batch([n, n, n], [n, n + 133, n + 470], 4, 2, 128, "f16", page=page, layout=layout, seed=page), **MANY)
+
+
+@pytest.mark.parametrize("heads", [(1, 1), (3, 3), (7, 1), (17, 1), (64, 1), (40, 8), (100, 1), (128, 1), (258, 2)])
+@pytest.mark.parametrize("n", [1, 4, 50])
+def test_many_rows_kernel_head_groups(q, heads, n):
+    check(q, Batch([n, n], [n + 77, n + 300], *heads, 64, "bf16", seed=heads[0]), **MANY)
+
+
+@pytest.mark.parametrize("window", [1, 16, 65, 130, 1000])
+@pytest.mark.parametrize("n", [1, 3, 150])
+def test_many_rows_kernel_window(q, window, n):
+    check(q, Batch([n, n, n], [n, n + 90, n + 700], 8, 4, 128, "bf16", seed=window), window=window, **MANY)
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_many_rows_kernel_rows_without_keys(q, n):
+    bt = Batch([n, n, 0, n, n], [0, n + 50, 30, n // 2, n], 4, 1, 128, "bf16", seed=n)
+    for kw in (dict(), dict(causal=False), dict(window=3)):
+        assert (check(q, bt, **kw, **MANY)[:n] == 0).all()

@@ -59,3 +59,19 @@ def test_window_start(program):
     out = subprocess.run([program, "start"], input="".join(f"{p} {w}\n" for p, w in pairs), capture_output=True,
                          text=True, check=True).stdout.split()
     assert [int(v) for v in out] == [max(0, p - w + 1) for p, w in pairs]
+
+
+# max_q may be any bound: row tiles cover the batch's tokens and no more, rows are counted in
+# 32 bits, and the scratch that the caller was asked for holds the parts.
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("q_map", [0, 1])
+def test_row_tiles_of_any_max_q(plan, D, q_map):
+    cases = [(b, t, hq, hk, D, 16, 600, 0, max_q, max_kv, q_map) for b in (1, 3, 40) for t in (1, 5, 64, 300, 9000)
+             for hq, hk in ((1, 1), (8, 1), (32, 8), (17, 1), (100, 1), (512, 1)) for max_kv in (0, 9000)
+             for max_q in (1, 4, 40, t, 8192, 1 << 24, INT_MAX)]
+    for c, p in zip(cases, plan(cases)):
+        rows = min(c[8], c[1]) * (c[2] // c[3])
+        assert (p.row_tiles - 1) * p.tile_rows < rows <= p.row_tiles * p.tile_rows, (c, p)
+        assert p.row_tiles * p.tile_rows < INT_MAX
+        assert p.part_end <= p.scratch, (c, p)
+        assert p.grid <= (2 if p.few else 1) * SMS or p.whole
