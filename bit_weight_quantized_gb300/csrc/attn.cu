@@ -267,14 +267,21 @@ int decode_cluster(const AttnParams &p, long long items, long long max_kv, int n
                 (c == 1 || items <= attn_decode_clusters(p.kv.head_dim, bf16, *warps, c)))
                 return c;
     }
-    // more items than blocks at once: each costs its block a start and its units
+    // longer: the axis is split over two blocks of four warps per SM, which the split's grid is
+    // sized for (128 sequences of 300 to 4096 keys, 8 key heads: 175 us; on as many blocks of
+    // one warp, a quarter of the copies in flight, 373)
+    *warps = 4;
+    if (span > kWholeKeys * decode_keys(p.kv.head_dim, 1) || items > 0x7fffffff)
+        return 0;
+    // more short items than blocks at once: each costs its block a start and its units
     const auto rounds = [&](int w, int blocks_per_sm) {
         const int keys = decode_keys(p.kv.head_dim, w);
         const long long blocks = static_cast<long long>(blocks_per_sm) * num_sms;
         return (items + blocks - 1) / blocks * (kStartUnits + (span + keys - 1) / keys + more);
     };
-    *warps = rounds(1, kNarrowBlocksPerSm) < rounds(4, kDecodeBlocksPerSm) ? 1 : 4;
-    return span <= kWholeKeys * decode_keys(p.kv.head_dim, 1) && items <= 0x7fffffff ? 1 : 0;
+    if (rounds(1, kNarrowBlocksPerSm) < rounds(4, kDecodeBlocksPerSm))
+        *warps = 1;
+    return 1;
 }
 
 }  // namespace

@@ -100,3 +100,12 @@ def test_many_rows_kernel_rows_without_keys(q, n):
     bt = Batch([n, n, 0, n, n], [0, n + 50, 30, n // 2, n], 4, 1, 128, "bf16", seed=n)
     for kw in (dict(), dict(causal=False), dict(window=3)):
         assert (check(q, bt, **kw, **MANY)[:n] == 0).all()
+
+
+# more items, each longer than a block takes whole, than run at once: the axis is split,
+# on the counts around one, two and three rounds of blocks
+@pytest.mark.parametrize("D,keys", [(64, 560), (128, 300)])
+@pytest.mark.parametrize("batch", [29, 33, 60, 93])
+def test_more_long_items_than_blocks(q, D, keys, batch):
+    kl = [keys + i * 37 % 200 for i in range(batch)]
+    check(q, Batch([1] * batch, kl, 64, 32, D, "bf16" if batch % 2 else "f16", page=32, seed=batch))

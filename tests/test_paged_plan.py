@@ -75,3 +75,26 @@ def test_row_tiles_of_any_max_q(plan, D, q_map):
         assert p.row_tiles * p.tile_rows < INT_MAX
         assert p.part_end <= p.scratch, (c, p)
         assert p.grid <= (2 if p.few else 1) * SMS or p.whole
+
+
+# An axis that is split runs on blocks of four warps, which its grid of two blocks per SM
+# is made for, whatever the number of items.
+@pytest.mark.parametrize("D", [64, 128])
+def test_split_decode_runs_on_four_warps(plan, D):
+    cases = [_decode(b, h, n, D, w) for h in (1, 2, 8, 16, 32) for n in (300, 520, 600, 1100, 2100, 4096, 30000)
+             for b in (1, 7, 29, 33, 58, 66, 100, 115, 128, 133, 200, 256, 400) for w in (0, 700)]
+    split = 0
+    for c, p in zip(cases, plan(cases)):
+        assert p.few
+        if not p.whole:
+            split += 1
+            assert p.warps == 4 and p.cluster == 1, c
+            assert p.grid <= 2 * SMS
+    assert split > 100
+
+
+def test_many_short_items_keep_their_narrow_blocks(plan):
+    got = plan([_decode(54, 32, 4), _decode(256, 8, 256), _decode(64, 8, 256)])
+    assert [p.whole for p in got] == [1, 1, 1]
+    assert [p.warps for p in got] == [1, 1, 4]
+    assert [p.grid for p in got] == [54 * 32, 2048, 512]
