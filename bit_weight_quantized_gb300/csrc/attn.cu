@@ -29,7 +29,6 @@ template <int D, bool BF16>
 __global__ void __launch_bounds__(128)
 join_decode_kernel(const __grid_constant__ AttnParams p)
 {
-    constexpr float kShift = BF16 ? 0.f : 7.f;
     constexpr int kVec = D / 32;
     __shared__ float so[4][D];
     __shared__ float2 sml[4];
@@ -109,10 +108,10 @@ join_decode_kernel(const __grid_constant__ AttnParams p)
             o1 = fmaf(a, so[w][2 * threadIdx.x + 1], o1);
         }
         const long long at = out_row(p, mt.z + row, mt.w, h);
-        const float inv = ll > 0.f ? 1.f / ll : 0.f;
+        const float inv = row_inverse(ll);
         reinterpret_cast<uint32_t *>(p.out + at * D)[threadIdx.x] = pack16<BF16>(o0 * inv, o1 * inv);
         if (p.lse && threadIdx.x == 0)
-            p.lse[at] = ll > 0.f ? (mm - kShift + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+            p.lse[at] = row_log_sum<BF16>(mm, ll);
     }
 }
 
@@ -122,7 +121,6 @@ template <int D, bool BF16>
 __global__ void __launch_bounds__(256)
 join_chunk_kernel(const __grid_constant__ AttnParams p)
 {
-    constexpr float kShift = BF16 ? 0.f : 7.f;
     constexpr int kQuads = D / 32;      // groups of four values per thread
     if (threadIdx.x == 0)
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -169,13 +167,13 @@ join_chunk_kernel(const __grid_constant__ AttnParams p)
         }
     }
     const long long at = out_row(p, mt.z + row, mt.w, h);
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = row_inverse(l);
     uint2 *dst = reinterpret_cast<uint2 *>(p.out + at * D + warp * (D / 8));
 #pragma unroll
     for (int e = 0; e < kQuads; ++e)
         dst[e] = make_uint2(pack16<BF16>(o[e].x * inv, o[e].y * inv), pack16<BF16>(o[e].z * inv, o[e].w * inv));
     if (p.lse && warp == 0)
-        p.lse[at] = l > 0.f ? (m - kShift + log2f(l)) * 0.6931471805599453f : -INFINITY;
+        p.lse[at] = row_log_sum<BF16>(m, l);
 }
 
 template <int D, bool BF16>

@@ -566,7 +566,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                 l = w0 * l + w1 * l1;
             }
             // rows to memory: the item's output, or this block's part of it
-            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const float inv = row_inverse(l);
             float *part = p.part_o + static_cast<long long>(slot) * (kChunkRows * D) + 4 * trow;
             const int tok = p.by_group(rr), sub = lane & 3;
             // this row's place in the output, and those of the group of four lanes
@@ -621,7 +621,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p)
                     *reinterpret_cast<float2 *>(p.part_ml + (static_cast<long long>(slot) * kChunkRows + trow) * 2) =
                         make_float2(mref, l);
                 else if (p.lse)
-                    p.lse[place / D] = l > 0.f ? (mref - kShift + log2f(l)) * 0.6931471805599453f : -INFINITY;
+                    p.lse[place / D] = row_log_sum<BF16>(mref, l);
             }
         }
     } else {

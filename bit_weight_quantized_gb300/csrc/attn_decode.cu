@@ -398,11 +398,11 @@ attn_decode_kernel(const __grid_constant__ AttnParams p)
         auto store = [&](int row, int c, float m, float l, const float4 &acc) {
             const int rr = r.row0 + row, tok = p.by_group(rr);
             const long long at = static_cast<long long>(r.t0 + tok) * p.q_heads + sg.h * p.group + rr - tok * p.group;
-            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const float inv = row_inverse(l);
             *reinterpret_cast<uint2 *>(p.out + at * D + c) =
                 make_uint2(pack16<BF16>(acc.x * inv, acc.y * inv), pack16<BF16>(acc.z * inv, acc.w * inv));
             if (p.lse && c == 0)
-                p.lse[at] = l > 0.f ? (m - kShift + log2f(l)) * 0.6931471805599453f : -INFINITY;
+                p.lse[at] = row_log_sum<BF16>(m, l);
         };
         for (int e = tid; e < r.rows * (D / 4); e += kDecThreads) {
             const int row = e / (D / 4), c = 4 * (e % (D / 4));

@@ -42,6 +42,19 @@ __device__ __forceinline__ float hi16(uint32_t w)
     return BF16 ? __uint_as_float(w & 0xFFFF0000u) : f16_bits_to_f32(static_cast<uint16_t>(w >> 16));
 }
 
+// ---- the end of a row -------------------------------------------------------------
+// A row's maximum m (in powers of two), its sum l of 2^(s - m + shift) and what they give.
+// l is zero only where the row sees no key (the largest weight is 2^-8 at least): its output
+// is zero and its log sum -infinity.  NaN and infinite scores leave NaN in l, and so in both.
+__device__ __forceinline__ float row_inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
+
+template <bool BF16>
+__device__ __forceinline__ float row_log_sum(float m, float l)
+{
+    constexpr float kShift = BF16 ? 0.f : 7.f;
+    return l == 0.f ? -INFINITY : (m - kShift + log2f(l)) * 0.6931471805599453f;
+}
+
 // ---- asynchronous copies --------------------------------------------------------
 // 16 bytes global -> shared through L2; with ok == false 16 zero bytes (nothing is
 // read, `src` only has to be a valid address).

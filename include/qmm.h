@@ -389,7 +389,8 @@ QMM_API qmm_status qmm_kv_append(const qmm_paged_kv *kv, const void *k, int64_t 
  *           0 <= j < kv_len[b];  j <= p when `causal`;  j > p - window when window > 0
  *   out   = sum_j exp(s_j - m) V_j / sum_j exp(s_j - m),   m = max_j s_j
  *   lse   = m + ln sum_j exp(s_j - m)
- * A row that sees no key (padding) gets out = 0 and lse = -infinity.  Scores, the
+ * A row that sees no key (padding) gets out = 0 and lse = -infinity; one that sees a
+ * NaN or +infinite score gets NaN in both.  Scores, the
  * running maximum, the sums and the accumulated output are fp32; the weights
  * exp(s_j - m) are rounded to dtype for the product with V, and out once at the
  * end.  Results are deterministic run to run.  Slots that no new token of the

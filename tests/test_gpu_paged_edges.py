@@ -109,3 +109,24 @@ def test_many_rows_kernel_rows_without_keys(q, n):
 def test_more_long_items_than_blocks(q, D, keys, batch):
     kl = [keys + i * 37 % 200 for i in range(batch)]
     check(q, Batch([1] * batch, kl, 64, 32, D, "bf16" if batch % 2 else "f16", page=32, seed=batch))
+
+
+# NaN and infinite scores: every row that sees such a key gets NaN, as log sum too; the rows
+# before it, and the other sequences, are as without it
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("n,kv,key", [(1, 40, 20), (1, 3000, 2000), (1, 40000, 77), (30, 400, 380), (200, 900, 800),
+                                      (130, 6000, 5950)])
+def test_nan_reaches_output_and_log_sum(q, n, kv, key, dtype, bad):
+    bt = Batch([n, n], [kv, kv - n // 2], 2, 1, 64, dtype, page=16, seed=kv)
+    bt.q[..., 0] = 1.0
+    clean = attention(bt)
+    bt.k_cache[bt.table[0, key // 16], key % 16, 0, 0] = bad
+    for pad in (0, 8192):
+        out, lse = attend(q, bt, pad=pad, max_q=max(n, pad))
+        pos = torch.arange(kv - n, kv, device="cuda")
+        hit = torch.cat([pos >= key, torch.zeros(n, dtype=torch.bool, device="cuda")])
+        assert torch.isnan(out[hit]).all() and torch.isnan(lse[hit]).all()
+        ref, tol, ls, ltol = clean
+        assert ((out.double() - ref).abs() <= tol)[~hit].all()
+        assert ((lse.double() - ls).abs() <= ltol)[~hit].all()
