@@ -768,7 +768,7 @@ qmm_status qmm_paged_attn(const qmm_paged_kv *kv, const void *q, int64_t q_strid
         return QMM_ERR_SHAPE;
     if (kv->tokens > 1 && q_stride % 8)
         return QMM_ERR_ALIGN;
-    if (kv->batch == 0 || kv->tokens == 0 || max_q == 0)
+    if (kv->batch == 0 || kv->tokens == 0)
         return QMM_OK;
     if (!q || !out || !workspace)
         return QMM_ERR_NULL;
@@ -779,9 +779,12 @@ qmm_status qmm_paged_attn(const qmm_paged_kv *kv, const void *q, int64_t q_strid
     if ((static_cast<long long>(std::min(max_q, kv->tokens)) * group / 16 + 1) * kv->batch > 0x7fffffffLL ||
         static_cast<long long>(kv->tokens) * group > 0x7fffffffLL)
         return QMM_ERR_UNSUPPORTED;
+    // max_q = 0 says that no sequence has a token, so that there is nothing to do; that is for
+    // the device to check, where there is one, as for every other bound: one token is
+    // answered, more are recorded
     const DeviceFacts *f = device_facts();
     if (!f || f->usable != QMM_OK)
-        return QMM_ERR_DEVICE;
+        return max_q == 0 ? QMM_OK : QMM_ERR_DEVICE;
     if (workspace_bytes < attn_workspace_bytes(q_heads, kv->kv_heads, kv->head_dim, max_q, f->num_sms))
         return QMM_ERR_SHAPE;
     AttnParams p;

@@ -286,14 +286,14 @@ int decode_cluster(const AttnParams &p, long long items, long long max_kv, int n
 
 size_t attn_workspace_bytes(int q_heads, int kv_heads, int head_dim, int max_q, int num_sms)
 {
-    return scratch_bytes(few_rows(max_q, q_heads / kv_heads), head_dim, num_sms);
+    return scratch_bytes(few_rows(std::max(1, max_q), q_heads / kv_heads), head_dim, num_sms);
 }
 
 cudaError_t attn_dispatch(AttnParams &p, int max_q, long long max_kv, void *workspace, int num_sms, cudaStream_t stream)
 {
     // no sequence has more tokens than the batch: a caller's large bound adds no row tiles, and
     // the rows of a sequence are counted in 32 bits (qmm_paged_attn checks tokens * group)
-    max_q = std::min(max_q, p.kv.tokens);
+    max_q = std::max(1, std::min(max_q, p.kv.tokens));
     const long long most = static_cast<long long>(p.kv.blocks) * p.kv.page_size, q_rows = static_cast<long long>(max_q) * p.group;
     if (max_kv <= 0 || max_kv > most)
         max_kv = most;

@@ -404,7 +404,7 @@ QMM_API qmm_status qmm_kv_append(const qmm_paged_kv *kv, const void *k, int64_t 
  *   window   0 (none) or the number of keys a token sees, its own included;
  *            window > 0 needs causal.
  *   max_q    at least the longest sequence's number of new tokens (any larger number
- *            will do; more than `tokens` counts as `tokens`): it chooses the
+ *            will do; more than `tokens` counts as `tokens`, 0 as 1): it chooses the
  *            kernel and sizes the split (a longer sequence records QMM_ERR_INDEX).
  *   max_kv   at least the longest kv_len, or 0 if unknown: a hint for the split.
  *   workspace  (device) 16-byte aligned scratch of at least

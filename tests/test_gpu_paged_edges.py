@@ -18,6 +18,16 @@ def q():
     return q
 
 
+@pytest.fixture(params=["extension", "ctypes"])
+def route(q, request, monkeypatch):
+    """Either route of the binding to the library."""
+    if request.param == "ctypes":
+        monkeypatch.setattr(q, "_fast_append", None)
+        monkeypatch.setattr(q, "_fast_attn", None)
+    elif q._fast_attn is None:
+        pytest.skip("extension not built")
+
+
 def attend(q, bt, window=0, causal=True, max_q=None, max_kv=None, pad=0):
     """out, lse of one call; `pad` rows of NaN follow the batch's queries, which belong to
     no sequence and whose output must stay as it was."""
@@ -130,3 +140,15 @@ def test_nan_reaches_output_and_log_sum(q, n, kv, key, dtype, bad):
         ref, tol, ls, ltol = clean
         assert ((out.double() - ref).abs() <= tol)[~hit].all()
         assert ((lse.double() - ls).abs() <= ltol)[~hit].all()
+
+
+# max_q = 0 in a batch that has tokens: single tokens are answered, more are reported
+def test_max_q_of_zero(q, route):
+    bt = Batch([1, 1, 1], [90, 5, 700], 8, 2, 64, seed=5)
+    check(q, bt, max_q=0)
+    wide = Batch([1, 1], [90, 400], 40, 2, 64, seed=6)      # more rows than the decode kernel's tile
+    check(q, wide, max_q=0)
+    bt = Batch([9, 1], [90, 5], 4, 2, 64, seed=5)
+    q.qmm_paged_attn(bt.q, *bt.args(), 0, 90)
+    assert q.qmm_device_status() == 10
+    assert q.qmm_device_status() == 0

@@ -68,9 +68,9 @@ def test_window_start(program):
 def test_row_tiles_of_any_max_q(plan, D, q_map):
     cases = [(b, t, hq, hk, D, 16, 600, 0, max_q, max_kv, q_map) for b in (1, 3, 40) for t in (1, 5, 64, 300, 9000)
              for hq, hk in ((1, 1), (8, 1), (32, 8), (17, 1), (100, 1), (512, 1)) for max_kv in (0, 9000)
-             for max_q in (1, 4, 40, t, 8192, 1 << 24, INT_MAX)]
+             for max_q in (0, 1, 4, 40, t, 8192, 1 << 24, INT_MAX)]
     for c, p in zip(cases, plan(cases)):
-        rows = min(c[8], c[1]) * (c[2] // c[3])
+        rows = max(1, min(c[8], c[1])) * (c[2] // c[3])
         assert (p.row_tiles - 1) * p.tile_rows < rows <= p.row_tiles * p.tile_rows, (c, p)
         assert p.row_tiles * p.tile_rows < INT_MAX
         assert p.part_end <= p.scratch, (c, p)
