@@ -432,6 +432,13 @@ def qmm_quantize_act(x, xq=None, sa=None):
     return xq, sa
 
 
+def _int32(**values):
+    # sizes and bounds that the library takes as C ints: ctypes would cut them silently
+    for name, v in values.items():
+        if not -2 ** 31 <= v < 2 ** 31:
+            raise ValueError(f"{name} must fit in 32 bits, got {v}")
+
+
 def _paged_checks(k_cache, v_cache, block_table, cu_q, kv_len, rows):
     # the argument checks of the paged cache calls, one by one
     for name, t, dt, nd in (("k_cache", k_cache, None, 4), ("v_cache", v_cache, None, 4),
@@ -452,6 +459,8 @@ def _paged_checks(k_cache, v_cache, block_table, cu_q, kv_len, rows):
     if cu_q.shape[0] != kv_len.shape[0] + 1 or block_table.shape[0] != kv_len.shape[0]:
         raise ValueError("cu_q must have one entry more than kv_len, block_table as many rows")
     D = k_cache.shape[3]
+    _int32(pages=k_cache.shape[0], page_size=k_cache.shape[1], kv_heads=k_cache.shape[2], head_dim=D,
+           sequences=kv_len.shape[0], blocks=block_table.shape[1])
     for name, t, heads in rows:
         if not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor")
@@ -463,6 +472,7 @@ def _paged_checks(k_cache, v_cache, block_table, cu_q, kv_len, rows):
             raise ValueError(f"{name}: the heads of a token must be contiguous")
         if t.shape[0] != rows[0][1].shape[0]:
             raise ValueError(f"{name} must have as many tokens as {rows[0][0]}")
+        _int32(tokens=t.shape[0], heads=t.shape[1])
 
 
 def _paged_kv(k_cache, v_cache, block_table, cu_q, kv_len, tokens):
@@ -500,6 +510,7 @@ def qmm_kv_append(k, v, k_cache, v_cache, block_table, cu_q, kv_len, q=None, q_o
         if cos_sin.dim() != 2:
             raise ValueError("cos_sin must be [positions][rot]")
         rope_len, rot = cos_sin.shape
+        _int32(positions=rope_len, rot=rot)
     if q is not None:
         heads = q.shape[1]
         if q_out is None:
@@ -517,6 +528,7 @@ def qmm_kv_append(k, v, k_cache, v_cache, block_table, cu_q, kv_len, q=None, q_o
 def qmm_paged_attn_workspace(q_heads: int, kv_heads: int, head_dim: int, max_q: int) -> int:
     """Bytes of scratch a qmm_paged_attn call of these sizes needs (0 for sizes it
     does not take)."""
+    _int32(q_heads=q_heads, kv_heads=kv_heads, head_dim=head_dim, max_q=max_q)
     return int(load().qmm_paged_attn_workspace(q_heads, kv_heads, head_dim, max_q))
 
 
@@ -542,6 +554,7 @@ def qmm_paged_attn(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q, max_kv
         if r > 0:
             raise QmmError(r, "qmm_paged_attn")
     _paged_checks(k_cache, v_cache, block_table, cu_q, kv_len, [("q", q, None)])
+    _int32(max_q=max_q, max_kv=max_kv, window=window)
     T, heads, D = q.shape
     if out is None:
         out = torch.empty((T, heads, D), dtype=q.dtype, device=q.device)

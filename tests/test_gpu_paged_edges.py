@@ -152,3 +152,22 @@ def test_max_q_of_zero(q, route):
     q.qmm_paged_attn(bt.q, *bt.args(), 0, 90)
     assert q.qmm_device_status() == 10
     assert q.qmm_device_status() == 0
+
+
+# numbers past 32 bits are refused, not cut
+def test_numbers_past_32_bits_are_refused(q, route):
+    bt = Batch([2], [10], 4, 2, 64)
+    a = bt.args()
+    k = torch.zeros(2, 2, 64, device="cuda", dtype=bt.dt)
+    big = 2 ** 32 + 5
+    for kw in (dict(window=big), dict(max_kv=big), dict(max_q=big)):
+        with pytest.raises(ValueError):
+            q.qmm_paged_attn(bt.q, *a, **dict(dict(max_q=2, max_kv=10), **kw))
+    many = [t[:1].expand(big, -1, -1, -1) for t in a[:2]]
+    with pytest.raises(ValueError):
+        q.qmm_paged_attn(bt.q, *many, *a[2:], 2, 10)
+    with pytest.raises(ValueError):
+        q.qmm_kv_append(k, k, *many, *a[2:])
+    with pytest.raises(ValueError):
+        q.qmm_paged_attn_workspace(8, 2, 64, big)
+    assert q.qmm_device_status() == 0
