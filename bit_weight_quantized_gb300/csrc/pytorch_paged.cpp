@@ -10,12 +10,14 @@
 #include <Python.h>
 
 #include <cstdint>
+#include <exception>
 
 #include <ATen/EmptyTensor.h>
 #include <ATen/core/Tensor.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "../../include/qmm.h"
@@ -111,6 +113,14 @@ F address(PyObject *o)
 
 PyObject *mismatch() { return PyLong_FromLong(-1); }
 
+// The exception being handled as torch raises it in Python: torch.OutOfMemoryError from the
+// allocator, for one.
+PyObject *raise_current()
+{
+    torch::translate_exception_to_python(std::current_exception());
+    return nullptr;
+}
+
 using append_fn = decltype(&qmm_kv_append);
 using attn_fn = decltype(&qmm_paged_attn);
 using scratch_fn = decltype(&qmm_paged_attn_workspace);
@@ -170,9 +180,8 @@ PyObject *kv_append(PyObject *, PyObject *const *a, Py_ssize_t n)
             return THPVariable_Wrap(std::move(made));
         Py_INCREF(a[9]);
         return a[9];   // q_out or None
-    } catch (const std::exception &e) {
-        PyErr_SetString(PyExc_RuntimeError, e.what());
-        return nullptr;
+    } catch (...) {
+        return raise_current();
     }
 }
 
@@ -245,9 +254,8 @@ PyObject *paged_attn(PyObject *, PyObject *const *a, Py_ssize_t n)
         Py_DECREF(o);
         Py_XDECREF(l);
         return pair;
-    } catch (const std::exception &e) {
-        PyErr_SetString(PyExc_RuntimeError, e.what());
-        return nullptr;
+    } catch (...) {
+        return raise_current();
     }
 }
 

@@ -171,3 +171,21 @@ def test_numbers_past_32_bits_are_refused(q, route):
     with pytest.raises(ValueError):
         q.qmm_paged_attn_workspace(8, 2, 64, big)
     assert q.qmm_device_status() == 0
+
+
+# no memory for the output is torch's own error, by either route
+def test_out_of_memory_is_torchs_error(q, route):
+    bt = Batch([1], [10], 8, 2, 128)
+    query = bt.q[:1].expand(1 << 16, -1, -1)       # an output of 128 MB
+    fused = torch.zeros(1, 2, 128, device="cuda", dtype=bt.dt).expand(1 << 16, -1, -1)
+    torch.cuda.empty_cache()
+    total = torch.cuda.get_device_properties(0).total_memory
+    torch.cuda.set_per_process_memory_fraction((torch.cuda.memory_reserved() + (32 << 20)) / total)
+    try:
+        with pytest.raises(torch.cuda.OutOfMemoryError):
+            q.qmm_paged_attn(query, *bt.args(), 1, 10)
+        with pytest.raises(torch.cuda.OutOfMemoryError):
+            q.qmm_kv_append(fused, fused, *bt.args(), q=query)
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    check(q, bt)
