@@ -104,6 +104,15 @@ bool as_int(PyObject *o, int &v)
     return true;
 }
 
+// The truth of an argument; -1 where it has none (the binding's own checks say so).
+int truth(PyObject *o)
+{
+    const int t = PyObject_IsTrue(o);
+    if (t < 0)
+        PyErr_Clear();
+    return t;
+}
+
 template <typename F>
 F address(PyObject *o)
 {
@@ -138,7 +147,7 @@ PyObject *kv_append(PyObject *, PyObject *const *a, Py_ssize_t n)
         const Tensor *k = tensor(a[1], ok), *v = tensor(a[2], ok), *kc = tensor(a[3], ok), *vc = tensor(a[4], ok),
                      *table = tensor(a[5], ok), *cu = tensor(a[6], ok), *len = tensor(a[7], ok), *q = tensor(a[8], ok),
                      *q_out = tensor(a[9], ok), *cs = tensor(a[10], ok);
-        const int inter = PyObject_IsTrue(a[11]);
+        const int inter = truth(a[11]);
         if (!ok || !k || !v || !kc || !vc || !table || !cu || !len || inter < 0 || k->dim() != 3)
             return mismatch();
         qmm_paged_kv kv;
@@ -199,7 +208,7 @@ PyObject *paged_attn(PyObject *, PyObject *const *a, Py_ssize_t n)
         const Tensor *q = tensor(a[2], ok), *kc = tensor(a[3], ok), *vc = tensor(a[4], ok), *table = tensor(a[5], ok),
                      *cu = tensor(a[6], ok), *len = tensor(a[7], ok), *out = tensor(a[14], ok), *ws = tensor(a[15], ok);
         int max_q, max_kv, window;
-        const int causal = PyObject_IsTrue(a[11]), want_lse = PyObject_IsTrue(a[13]);
+        const int causal = truth(a[11]), want_lse = truth(a[13]);
         if (!ok || !q || !kc || !vc || !table || !cu || !len || causal < 0 || want_lse < 0 || q->dim() != 3 ||
             !as_int(a[8], max_q) || !as_int(a[9], max_kv) || !as_int(a[12], window))
             return mismatch();

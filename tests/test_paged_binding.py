@@ -18,3 +18,18 @@ def test_sizes_past_32_bits_are_refused(at, big):
     args[at] = big
     with pytest.raises(ValueError, match="32 bits"):
         q.qmm_paged_attn_workspace(*args)
+
+
+# something that is neither true nor false: its own error, not one of the interpreter
+def test_flags_without_a_truth_value():
+    import numpy as np
+    import torch
+    c = torch.zeros(2, 16, 2, 64, dtype=torch.float16)
+    i = torch.zeros(1, dtype=torch.int32)
+    k = torch.zeros(1, 2, 64, dtype=torch.float16)
+    both = np.array([True, False])
+    with pytest.raises(ValueError):
+        q.qmm_kv_append(k, k, c, c, i.view(1, 1), torch.zeros(2, dtype=torch.int32), i, interleaved=both)
+    for kw in (dict(causal=both), dict(return_lse=both)):
+        with pytest.raises(ValueError):
+            q.qmm_paged_attn(k, c, c, i.view(1, 1), torch.zeros(2, dtype=torch.int32), i, 1, **kw)
