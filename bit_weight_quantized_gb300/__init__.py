@@ -99,17 +99,18 @@ def _load_fastcall(lib):
 
 # The optional extension with the hot path of the paged cache calls
 # (csrc/pytorch_paged.cpp): their checks and allocations in C++.
-PAGED_PATH = os.path.join(_HERE, "lib", "_qmmpaged" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 _fast_append = _fast_attn = None
 _append_addr = _attn_addr = _scratch_addr = 0   # function addresses for it, filled by load()
 
 
 def _load_paged(lib):
     global _fast_append, _fast_attn, _append_addr, _attn_addr, _scratch_addr
-    if not os.path.exists(PAGED_PATH):
+    from .build import paged_path
+    path = paged_path()
+    if not os.path.exists(path):
         return
     try:
-        spec = importlib.util.spec_from_file_location("_qmmpaged", PAGED_PATH)
+        spec = importlib.util.spec_from_file_location("_qmmpaged", path)
         mod = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(mod)
     except (ImportError, OSError):

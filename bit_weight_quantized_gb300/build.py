@@ -133,8 +133,12 @@ PAGED_SRC = os.path.join(CSRC, "pytorch_paged.cpp")
 
 
 def paged_path() -> str:
-    """Where the paged cache calls' extension (csrc/pytorch_paged.cpp) is built."""
-    return os.path.join(LIBDIR, "_qmmpaged" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
+    """Where the paged cache calls' extension (csrc/pytorch_paged.cpp) is built.  It is
+    compiled against torch's internal headers, so the name holds the torch build: one made for
+    another is never loaded, and the calls go through ctypes until it is built again."""
+    import torch
+    made_for = f"{torch.__version__}-{(torch.version.git_version or '')[:12]}-abi{int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
+    return os.path.join(LIBDIR, f"_qmmpaged-{made_for}" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 
 
 def build_paged(verbose: bool = False) -> Optional[str]:

@@ -33,3 +33,26 @@ def test_flags_without_a_truth_value():
     for kw in (dict(causal=both), dict(return_lse=both)):
         with pytest.raises(ValueError):
             q.qmm_paged_attn(k, c, c, i.view(1, 1), torch.zeros(2, dtype=torch.int32), i, 1, **kw)
+
+
+# compiled against one torch, it is not loaded by another: neither a newer version nor another
+# build of the same one
+@pytest.mark.parametrize("what", ["version", "build"])
+def test_extension_of_another_torch_is_not_loaded(lib, what, monkeypatch):
+    import torch
+    if qbuild.build_paged() is None:
+        pytest.skip("no C++ compiler or headers here")
+    try:
+        if what == "version":
+            monkeypatch.setattr(torch, "__version__", "99.0.0")
+        else:
+            monkeypatch.setattr(torch.version, "git_version", "0123456789abcdef")
+        monkeypatch.setattr(q, "_fast_append", None)
+        monkeypatch.setattr(q, "_fast_attn", None)
+        q._load_paged(lib)
+        assert q._fast_append is None and q._fast_attn is None
+        monkeypatch.undo()
+        q._load_paged(lib)
+        assert q._fast_append is not None and q._fast_attn is not None
+    finally:
+        monkeypatch.undo()
