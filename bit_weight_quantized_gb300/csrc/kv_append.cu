@@ -129,7 +129,7 @@ kv_append_kernel(const __grid_constant__ AppendParams p)
     const int pos = keys - (end - t);
     if (pos < 0)
         return;                                          // padding
-    if (pos >= static_cast<long long>(kv.blocks) * kv.page_size || (p.rot > 0 && pos >= p.rope_len)) {
+    if (pos >= table_keys(kv) || (p.rot > 0 && pos >= p.rope_len)) {
         if (threadIdx.x == 0)
             record_error(p.status, QMM_ERR_INDEX);
         return;

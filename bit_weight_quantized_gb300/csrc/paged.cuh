@@ -81,13 +81,23 @@ __device__ __forceinline__ int2 seq_tokens(const qmm_paged_kv &kv, int b)
     return make_int2(t0, t1 - t0);
 }
 
-// A sequence's number of keys, held to what its row of the block table can hold.
+// Keys of a sequence at most: the kernels look up to a few thousand keys past a sequence's
+// end (whole tiles, those loaded ahead) before they see that nothing is there.
+constexpr int kMostKeys = 0x7fffffff - 16383;
+
+// What a sequence's row of the block table can hold.
+__device__ __forceinline__ int table_keys(const qmm_paged_kv &kv)
+{
+    return static_cast<int>(min(static_cast<long long>(kv.blocks) * kv.page_size, static_cast<long long>(kMostKeys)));
+}
+
+// A sequence's number of keys, held to that.
 __device__ __forceinline__ int seq_keys(const qmm_paged_kv &kv, int n, int *status)
 {
-    const long long most = static_cast<long long>(kv.blocks) * kv.page_size;
+    const int most = table_keys(kv);
     if (n > most) {
         record_error(status, QMM_ERR_INDEX);
-        return static_cast<int>(most);
+        return most;
     }
     return max(n, 0);
 }

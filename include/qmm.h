@@ -335,7 +335,7 @@ QMM_API qmm_status qmm_quantize_act(const void *x, int8_t *xq, void *sa, int M, 
  *                strides (in elements) are multiples of 8.
  *   block_table  (device) int32 [batch][blocks], rows `blocks` apart.
  *   cu_q         (device) int32 [batch + 1], cu_q[0] = 0, non-decreasing.
- *   kv_len       (device) int32 [batch].  A token whose position is negative
+ *   kv_len       (device) int32 [batch], at most 2^31 - 16384 keys.  A token whose position is negative
  *                (kv_len[b] < n_b, for example kv_len[b] = 0 in an unused place
  *                of a padded batch) is padding.
  *   page_size    any size >= 1.   head_dim: 64 or 128.   kv_heads >= 1.

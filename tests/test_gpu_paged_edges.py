@@ -189,3 +189,39 @@ def test_out_of_memory_is_torchs_error(q, route):
     finally:
         torch.cuda.set_per_process_memory_fraction(1.0)
     check(q, bt)
+
+
+# a sequence of as many keys as there may be (the table names two pages again and again), of
+# which the window leaves the last; one key more is reported
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [1, 40])
+def test_longest_sequence(q, n, D):
+    most, page, w = 2 ** 31 - 16384, 1 << 20, 300
+    g = torch.Generator(device="cuda")
+    g.manual_seed(n + D)
+    k, v = (torch.randn((2, page, 1, D), generator=g, device="cuda", dtype=torch.float16) for _ in range(2))
+    table = (torch.arange(2048, dtype=torch.int32, device="cuda") % 2).view(1, -1)
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    length = torch.tensor([most], dtype=torch.int32, device="cuda")
+    x = torch.randn((n, 4, D), generator=g, device="cuda", dtype=torch.float16)
+    j = torch.arange(most - n - w, most, device="cuda")
+    kk, vv = (t[(j // page) % 2, j % page, 0].double() for t in (k, v))
+    pos = torch.arange(most - n, most, device="cuda")[:, None, None]
+    see = (j <= pos) & (j > pos - w)
+    s = (torch.einsum("thd,jd->thj", x.double(), kk) * D ** -0.5).masked_fill(~see, -math.inf)
+    p = torch.softmax(s, -1)
+    ref = p @ vv
+    tol = 2.0 ** -11 * ref.abs() + (2.0 ** -11 + 2.0 ** -14) * (p @ vv.abs()) + 1e-7      # as in paged_ref
+    padded = torch.cat([x, torch.full((8192, 4, D), math.nan, device="cuda", dtype=x.dtype)])
+    for x, max_q, max_kv in ((x, n, most), (x, n, 0), (padded, 8192, most)):
+        out = q.qmm_paged_attn(x, k, v, table, cu, length, max_q, max_kv, window=w)
+        torch.cuda.synchronize()
+        assert q.qmm_device_status() == 0
+        assert ((out[:n].double() - ref).abs() <= tol).all()
+    q.qmm_kv_append(k[0, :n], v[0, :n], k, v, table, cu, length)
+    assert q.qmm_device_status() == 0
+    q.qmm_paged_attn(x, k, v, table, cu, length + 1, n, 0, window=w)
+    assert q.qmm_device_status() == 10
+    q.qmm_kv_append(k[0, :n], v[0, :n], k, v, table, cu, length + 1)
+    assert q.qmm_device_status() == 10
+    assert q.qmm_device_status() == 0
