@@ -126,7 +126,7 @@ kv_append_kernel(const __grid_constant__ AppendParams p)
     find_sequence(kv, t, lane, seq, end, keys);
     if (seq >= kv.batch)
         return;                                          // past the last sequence: padding
-    const int pos = keys - (end - t);
+    const int pos = max(keys, 0) - (end - t);            // (a length may be any integer)
     if (pos < 0)
         return;                                          // padding
     if (pos >= table_keys(kv) || (p.rot > 0 && pos >= p.rope_len)) {

@@ -225,3 +225,23 @@ def test_longest_sequence(q, n, D):
     q.qmm_kv_append(k[0, :n], v[0, :n], k, v, table, cu, length + 1)
     assert q.qmm_device_status() == 10
     assert q.qmm_device_status() == 0
+
+
+# lengths below zero, down to the smallest integer: padding, as zero is
+@pytest.mark.parametrize("length", [-1, -2 ** 31 + 2, -2 ** 31])
+def test_negative_lengths_are_padding(q, length):
+    bt = Batch([3, 5], [20, 40], 4, 2, 64, seed=4)
+    bt.kv_len[1] = length
+    k = torch.ones(8, 2, 64, device="cuda", dtype=bt.dt)
+    before, sentinel = bt.k_cache.clone(), torch.full_like(bt.q, 7.0)
+    q.qmm_kv_append(k, k, *bt.args(), q=bt.q, q_out=sentinel)
+    torch.cuda.synchronize()
+    assert q.qmm_device_status() == 0
+    assert (sentinel[3:] == 7.0).all() and torch.equal(sentinel[:3], bt.q[:3])
+    changed = torch.nan_to_num(bt.k_cache.double(), nan=5e5) != torch.nan_to_num(before.double(), nan=5e5)
+    assert int(changed.any(-1).sum()) == 6          # 3 slots of 2 heads
+    out, lse = q.qmm_paged_attn(bt.q[3:], bt.k_cache, bt.v_cache, bt.table[1:], bt.cu_q[1:] - 3, bt.kv_len[1:], 5, 40,
+                                return_lse=True)
+    torch.cuda.synchronize()
+    assert q.qmm_device_status() == 0
+    assert (out == 0).all() and (lse == -math.inf).all()
