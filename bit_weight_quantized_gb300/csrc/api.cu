@@ -743,7 +743,7 @@ qmm_status qmm_kv_append(const qmm_paged_kv *kv, const void *k, int64_t k_stride
     p.rope_len = rope_len;
     p.interleaved = interleaved != 0;
     p.by_page = fast_div(kv->page_size);
-    return from_cuda(launch_kv_append(p, f->num_sms, stream));
+    return from_cuda(launch_kv_append(p, stream));
 }
 
 size_t qmm_paged_attn_workspace(int q_heads, int kv_heads, int head_dim, int max_q)

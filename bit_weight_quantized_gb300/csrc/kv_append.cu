@@ -197,7 +197,7 @@ cudaError_t launch_append(const AppendParams &p, cudaStream_t stream)
 
 }  // namespace
 
-cudaError_t launch_kv_append(const AppendParams &p, int, cudaStream_t stream)
+cudaError_t launch_kv_append(const AppendParams &p, cudaStream_t stream)
 {
     const bool bf16 = p.kv.dtype == QMM_BF16;
     if (p.kv.head_dim == 128)

@@ -48,7 +48,7 @@ struct AppendParams {
     FastDiv by_page;
 };
 
-cudaError_t launch_kv_append(const AppendParams &p, int num_sms, cudaStream_t stream);
+cudaError_t launch_kv_append(const AppendParams &p, cudaStream_t stream);
 
 struct AttnParams {
     // the cache as [page and head][slot / 8][d / 64][slot % 8][d % 64] for tensor copies
