@@ -214,8 +214,10 @@ size_t scratch_bytes(bool few, int head_dim, int num_sms)
 }
 
 // Work a block takes at least, in units: below this a split costs more (a second
-// kernel, the partial results) than the longer walk.  (Chunk kernel, 30 items of up to 12
-// units: 18.1 us, with 6 20.4.)
+// kernel, the partial results) than the longer walk.  Decode kernel (blocks of four warps): one
+// token over 30000 keys of one key head 12.5 us, with 2 units 16.1, 8 13.2, 12 15.4; over 16000
+// of four 12.9, with 2 12.0, 8 13.5, 12 16.6.  Chunk kernel, 30 items of up to 12 units: 18.1 us,
+// with 6 20.4.
 constexpr int kMinDecodeUnits = 5, kMinChunkUnits = 4;
 
 // Work of the longest item (setup and units) up to which blocks of the chunk kernel take

@@ -20,7 +20,8 @@
 //
 // The running maximum is replaced only when it grows by more than 2^8 (the scale
 // factors stay within fp32 and fp16 range either way), so the output is rescaled
-// a few times per segment rather than in every tile.  fp16 weights are scaled by
+// a few times per segment rather than in every tile: a published refinement of the running
+// softmax; the bound is this file's, by the fp16 range below.  fp16 weights are scaled by
 // 2^7: 2^(s' - m + 7) <= 2^15 stays finite and weights down to 2^-21 of the maximum
 // keep all their bits (fp16 loses bits below 2^-14).
 #include <atomic>

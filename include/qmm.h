@@ -339,8 +339,10 @@ QMM_API qmm_status qmm_quantize_act(const void *x, int8_t *xq, void *sa, int M, 
  *                (kv_len[b] < n_b, for example kv_len[b] = 0 in an unused place
  *                of a padded batch) is padding.
  *   page_size    any size >= 1.   head_dim: 64 or 128.   kv_heads >= 1.
- * Tokens cu_q[batch] .. tokens - 1, if any, are padding too: nothing of them is
- * read or written.
+ * Tokens cu_q[batch] .. tokens - 1, if any, are padding too.  The rows of padding tokens
+ * must exist in every buffer (the kernels may read them); what they hold does not
+ * matter, and nothing is stored for them (qmm_paged_attn writes zeros for those that
+ * belong to a sequence, see there).
  * The lengths, tables and page numbers are data in device memory, so the host
  * cannot check them.  The kernels do: a page number outside [0, num_pages) or a
  * position past the table (or past the rotation table) reads and writes nothing
@@ -406,7 +408,11 @@ QMM_API qmm_status qmm_kv_append(const qmm_paged_kv *kv, const void *k, int64_t 
  *   max_q    at least the longest sequence's number of new tokens (any larger number
  *            will do; more than `tokens` counts as `tokens`, 0 as 1): it chooses the
  *            kernel and sizes the split (a longer sequence records QMM_ERR_INDEX).
- *   max_kv   at least the longest kv_len, or 0 if unknown: a hint for the split.
+ *   max_kv   at least the longest kv_len, or 0 if unknown (as long as the table):
+ *            a hint that chooses the split and, for short axes, the form without a
+ *            joining kernel.  Results do not depend on it beyond the rounding of the
+ *            order of sums; a bound far above the lengths costs a short axis some 4 us
+ *            (one token over 517 keys 4.9 us, in a table of 131072 with 0 9.2).
  *   workspace  (device) 16-byte aligned scratch of at least
  *            qmm_paged_attn_workspace() bytes; its contents need not survive, and
  *            calls on one stream may share it.

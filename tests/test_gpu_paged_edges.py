@@ -245,3 +245,32 @@ def test_negative_lengths_are_padding(q, length):
     torch.cuda.synchronize()
     assert q.qmm_device_status() == 0
     assert (out == 0).all() and (lse == -math.inf).all()
+
+
+# rows of padding behind the batch may hold anything, and nothing is stored for them
+def test_append_leaves_padding_alone(q):
+    bt = Batch([2, 3], [20, 30], 4, 2, 64, seed=4)
+    fused = torch.full((400, 8, 64), math.nan, device="cuda", dtype=bt.dt)
+    fused[:5] = torch.randn(5, 8, 64, device="cuda").to(bt.dt)
+    other = Batch([2, 3], [20, 30], 4, 2, 64, seed=4)
+    want = q.qmm_kv_append(fused[:5, 4:6], fused[:5, 6:], *other.args(), q=fused[:5, :4])
+    out = torch.full((400, 4, 64), 7.0, device="cuda", dtype=bt.dt)
+    q.qmm_kv_append(fused[:, 4:6], fused[:, 6:], *bt.args(), q=fused[:, :4], q_out=out)
+    torch.cuda.synchronize()
+    assert q.qmm_device_status() == 0
+    assert torch.equal(out[:5], want) and (out[5:] == 7.0).all()
+    for a, b in ((bt.k_cache, other.k_cache), (bt.v_cache, other.v_cache)):
+        assert torch.equal(torch.nan_to_num(a.double(), nan=9e9), torch.nan_to_num(b.double(), nan=9e9))
+
+
+# a table without columns holds no keys
+@pytest.mark.parametrize("n", [1, 40, 600])
+def test_empty_table(q, n):
+    bt = Batch([n], [0], 16, 2, 64, seed=4)
+    none = torch.empty(1, 0, dtype=torch.int32, device="cuda")
+    for window in (0, 5):
+        out = q.qmm_paged_attn(bt.q, bt.k_cache, bt.v_cache, none, bt.cu_q, bt.kv_len, n, 0, window=window)
+        torch.cuda.synchronize()
+        assert (out == 0).all() and q.qmm_device_status() == 0
+    q.qmm_paged_attn(bt.q, bt.k_cache, bt.v_cache, none, bt.cu_q, bt.kv_len + 1, n, 0)
+    assert q.qmm_device_status() == 10
