@@ -31,7 +31,8 @@ class QuantizedLinear:
     def __init__(self, weight):
         N, K = weight.shape
         w = weight.float().view(N, K // GROUP, GROUP)
-        lo, hi = w.amin(-1), w.amax(-1)
+        # the grid holds zero: the zero point is a code of its own, 0 to 255
+        lo, hi = w.amin(-1).clamp(max=0), w.amax(-1).clamp(min=0)
         scale = ((hi - lo) / (2 ** BITS - 1)).clamp(min=1e-6).half()
         zero = (-lo / scale.float()).round().clamp(0, 255)
         codes = (w / scale.float()[..., None] + zero[..., None]).round().clamp(0, 2 ** BITS - 1)
