@@ -359,7 +359,8 @@ def work(case):
 def _exact_scale(x, bits, least):
     """The smallest number of so many significant bits that is not below x (not below `least`'s multiples)."""
     m, e = torch.frexp(x)
-    y = torch.ldexp(torch.ceil(m * 2.0 ** bits), e - bits)
+    # (torch.ldexp multiplies by a power of two computed in 32 bits, on the GPU not exactly)
+    y = torch.ceil(m * 2.0 ** bits) * ((e.long() - bits + 1023) << 52).view(torch.float64)
     return torch.where(y < 2.0 ** bits * least, torch.ceil(x / least) * least, y)
 
 
