@@ -45,6 +45,12 @@ class PagedKV(ctypes.Structure):
                 ("blocks", _I), ("batch", _I), ("tokens", _I), ("kv_heads", _I), ("head_dim", _I), ("dtype", _I)]
 
 
+class PagedKV4(ctypes.Structure):
+    """qmm_paged_kv4 of qmm.h: a paged key / value cache in 4 bits and the batch that uses it."""
+    _fields_ = PagedKV._fields_ + [("scales", _P), ("scale_page_stride", _L), ("scale_slot_stride", _L),
+                                   ("scale_head_stride", _L)]
+
+
 SIGNATURES = {
     "qmm_pack": ([_P, _P, _I, _I, _I, _P, _P], _I),
     "qmm_unpack": ([_P, _P, _I, _I, _I, _P], _I),
@@ -63,6 +69,10 @@ SIGNATURES = {
     "qmm_kv_append": ([_P, _P, _L, _P, _L, _P, _L, _P, _I, _P, _I, _I, _I, _P], _I),
     "qmm_paged_attn": ([_P, _P, _L, _I, _F, _I, _I, _P, _P, _I, _I, _P, _SZ, _P], _I),
     "qmm_paged_attn_workspace": ([_I, _I, _I, _I], _SZ),
+    "qmm_kv4_append": ([_P, _P, _L, _P, _L, _P, _L, _P, _I, _P, _I, _I, _I, _P, _P, _F, _P], _I),
+    "qmm_kv4_read": ([_P, _P, _P, _P], _I),
+    "qmm_kv4_attn": ([_P, _P, _L, _I, _F, _I, _I, _I, _P, _P, _I, _I, _P, _SZ, _P], _I),
+    "qmm_kv4_attn_workspace": ([_I, _I, _I, _I], _SZ),
     "qmm_device_status": ([_P], _I),
     "qmm_watchdog_selftest": ([_P], _I),
     "qmm_status_string": ([_I], ctypes.c_char_p),
@@ -569,6 +579,172 @@ def qmm_paged_attn(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q, max_kv
     _check(_lib.qmm_paged_attn(ctypes.byref(kv), _ptr(q), q.stride(0), heads, scale, 1 if causal else 0, window,
                                _ptr(out), _ptr(lse), max_q, max_kv, _ptr(workspace), workspace.numel(),
                                _stream(q.device)), "qmm_paged_attn")
+    return (out, lse) if return_lse else out
+
+
+def _kv4_checks(k_cache, v_cache, scales, block_table, cu_q, kv_len, rows):
+    # the argument checks of the 4-bit cache calls, one by one
+    for name, t, dt, nd in (("k_cache", k_cache, _U8, 4), ("v_cache", v_cache, _U8, 4), ("scales", scales, None, 4),
+                            ("block_table", block_table, torch.int32, 2), ("cu_q", cu_q, torch.int32, 1),
+                            ("kv_len", kv_len, torch.int32, 1)):
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.device != k_cache.device:
+            raise ValueError(f"{name} must be on {k_cache.device}")
+        if t.dim() != nd:
+            raise ValueError(f"{name} must have {nd} dimensions")
+        if dt is not None and t.dtype != dt:
+            raise ValueError(f"{name} must be {dt}")
+        if nd < 4 and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    if scales.dtype not in _DT:
+        raise ValueError("scales must be float16 or bfloat16")
+    if v_cache.shape != k_cache.shape or v_cache.stride() != k_cache.stride():
+        raise ValueError("k_cache and v_cache must have the same shape and strides")
+    D = 2 * k_cache.shape[3]
+    if D not in (64, 128):
+        raise ValueError("k_cache must hold 32 or 64 bytes a head (head sizes 64 and 128)")
+    if tuple(scales.shape) != (*k_cache.shape[:3], D // 32):
+        raise ValueError(f"scales must have shape {(*k_cache.shape[:3], D // 32)}, got {tuple(scales.shape)}")
+    if k_cache.stride(3) != 1 or scales.stride(3) != 1:
+        raise ValueError("the cache's last dimension must be contiguous")
+    if cu_q.shape[0] != kv_len.shape[0] + 1 or block_table.shape[0] != kv_len.shape[0]:
+        raise ValueError("cu_q must have one entry more than kv_len, block_table as many rows")
+    _int32(pages=k_cache.shape[0], page_size=k_cache.shape[1], kv_heads=k_cache.shape[2],
+           sequences=kv_len.shape[0], blocks=block_table.shape[1])
+    for name, t, heads in rows:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.device != k_cache.device:
+            raise ValueError(f"{name} must be on {k_cache.device}")
+        if t.dim() != 3 or t.shape[2] != D or t.dtype != scales.dtype:
+            raise ValueError(f"{name} must be [tokens][heads][{D}] of {scales.dtype}")
+        if heads is not None and t.shape[1] != heads:
+            raise ValueError(f"{name} must have {heads} heads")
+        if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != D):
+            raise ValueError(f"{name}: the heads of a token must be contiguous")
+        if t.shape[0] != rows[0][1].shape[0]:
+            raise ValueError(f"{name} must have as many tokens as {rows[0][0]}")
+        _int32(tokens=t.shape[0], heads=t.shape[1])
+
+
+def _kv4(k_cache, v_cache, scales, block_table, cu_q, kv_len, tokens):
+    s0, s1, s2, _ = k_cache.stride()
+    c0, c1, c2, _ = scales.stride()
+    pages, page, hk, row = k_cache.shape
+    return PagedKV4(_ptr(k_cache), _ptr(v_cache), s0, s1, s2, _ptr(block_table), _ptr(cu_q), _ptr(kv_len), pages, page,
+                    block_table.shape[1], kv_len.shape[0], tokens, hk, 2 * row, _DT[scales.dtype], _ptr(scales), c0, c1, c2)
+
+
+def qmm_kv4_append(k, v, k_cache, v_cache, scales, block_table, cu_q, kv_len, q=None, q_out=None, cos_sin=None,
+                   interleaved=False, q_norm=None, k_norm=None, eps=1e-6):
+    """qmm_kv_append for a cache in 4 bits: k_cache and v_cache hold codes (uint8
+    [pages][page_size][kv_heads][D / 2] by index, any strides with the last dimension
+    contiguous), scales [pages][page_size][kv_heads][D / 32] of the rows' type the scale
+    patterns of 64 values each, the key's and then the value's.  With q_norm or k_norm
+    ([D], the rows' type) the queries' or keys' heads are normed before the rotation.  See
+    qmm_kv4_append in qmm.h."""
+    if _lib is None:
+        load()
+    hk = k_cache.shape[2] if k_cache.dim() == 4 else None
+    rows = [("k", k, hk), ("v", v, hk)] + ([("q", q, None)] if q is not None else [])
+    _kv4_checks(k_cache, v_cache, scales, block_table, cu_q, kv_len, rows)
+    T, hk, D = k.shape
+    rot = rope_len = heads = 0
+    if cos_sin is not None:
+        _dev(cos_sin, "cos_sin", torch.float32)
+        if cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be [positions][rot]")
+        rope_len, rot = cos_sin.shape
+        _int32(positions=rope_len, rot=rot)
+    for name, t in (("q_norm", q_norm), ("k_norm", k_norm)):
+        if t is not None:
+            _dev(t, name, k.dtype, (D,))
+    for name, t in (("cos_sin", cos_sin), ("q_norm", q_norm), ("k_norm", k_norm), ("q_out", q_out)):
+        if t is not None and t.device != k.device:
+            raise ValueError(f"{name} must be on {k.device}")
+    if q is not None:
+        heads = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty((T, heads, D), dtype=q.dtype, device=q.device)
+        _dev(q_out, "q_out", q.dtype, (T, heads, D))
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    elif q_norm is not None:
+        raise ValueError("q_norm without q")
+    kv = _kv4(k_cache, v_cache, scales, block_table, cu_q, kv_len, T)
+    with torch.cuda.device(k.device):
+        _check(_lib.qmm_kv4_append(ctypes.byref(kv), _ptr(k), k.stride(0), _ptr(v), v.stride(0), _ptr(q),
+                                   0 if q is None else q.stride(0), _ptr(q_out), heads, _ptr(cos_sin), rot, rope_len,
+                                   1 if interleaved else 0, _ptr(q_norm), _ptr(k_norm), eps, _stream(k.device)),
+               "qmm_kv4_append")
+    return q_out
+
+
+def qmm_kv4_read(k_cache, v_cache, scales, block_table, cu_q, kv_len, tokens, k_out=None, v_out=None):
+    """The values that the cache holds for the last cu_q[b + 1] - cu_q[b] keys of every
+    sequence b (arguments as for qmm_kv4_append; tokens: the rows of the outputs, cu_q's
+    last entry): (k_out, v_out), [tokens][kv_heads][D] of scales' type.  Rows of padding
+    tokens are left as they were.  See qmm_kv4_read in qmm.h."""
+    if _lib is None:
+        load()
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must have 4 dimensions")
+    if tokens < 0:
+        raise ValueError(f"tokens must not be negative, got {tokens}")
+    _kv4_checks(k_cache, v_cache, scales, block_table, cu_q, kv_len, [])
+    _int32(tokens=tokens)
+    shape = (tokens, k_cache.shape[2], 2 * k_cache.shape[3])
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=scales.dtype, device=scales.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=scales.dtype, device=scales.device)
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        _dev(t, name, scales.dtype, shape)
+        if t.device != k_cache.device:
+            raise ValueError(f"{name} must be on {k_cache.device}")
+    kv = _kv4(k_cache, v_cache, scales, block_table, cu_q, kv_len, tokens)
+    with torch.cuda.device(k_cache.device):
+        _check(_lib.qmm_kv4_read(ctypes.byref(kv), _ptr(k_out), _ptr(v_out), _stream(k_cache.device)), "qmm_kv4_read")
+    return k_out, v_out
+
+
+def qmm_kv4_attn_workspace(q_heads: int, kv_heads: int, head_dim: int, max_q: int) -> int:
+    """Bytes of scratch a qmm_kv4_attn call of these sizes needs (0 for sizes it does
+    not take)."""
+    _int32(q_heads=q_heads, kv_heads=kv_heads, head_dim=head_dim, max_q=max_q)
+    return int(load().qmm_kv4_attn_workspace(q_heads, kv_heads, head_dim, max_q))
+
+
+def qmm_kv4_attn(q, k_cache, v_cache, scales, block_table, cu_q, kv_len, max_q, max_kv=0, scale=None, causal=True,
+                 window=0, sinks=0, return_lse=False, out=None, workspace=None):
+    """qmm_paged_attn over a cache in 4 bits (k_cache, v_cache and scales as for
+    qmm_kv4_append).  With a window, sinks: first tokens that stay visible to every
+    token.  workspace: uint8 scratch of qmm_kv4_attn_workspace() bytes, allocated if
+    None.  See qmm_kv4_attn in qmm.h."""
+    if _lib is None:
+        load()
+    if scale is None:
+        scale = q.shape[-1] ** -0.5
+    _kv4_checks(k_cache, v_cache, scales, block_table, cu_q, kv_len, [("q", q, None)])
+    _int32(max_q=max_q, max_kv=max_kv, window=window, sinks=sinks)
+    T, heads, D = q.shape
+    if out is None:
+        out = torch.empty((T, heads, D), dtype=q.dtype, device=q.device)
+    _dev(out, "out", q.dtype, (T, heads, D))
+    lse = torch.empty((T, heads), dtype=torch.float32, device=q.device) if return_lse else None
+    with torch.cuda.device(q.device):
+        if workspace is None:
+            nbytes = qmm_kv4_attn_workspace(heads, k_cache.shape[2], D, max_q)
+            workspace = torch.empty(max(nbytes, 16), dtype=_U8, device=q.device)
+        _dev(workspace, "workspace", _U8)
+        for name, t in (("out", out), ("workspace", workspace)):
+            if t.device != q.device:
+                raise ValueError(f"{name} must be on {q.device}")
+        kv = _kv4(k_cache, v_cache, scales, block_table, cu_q, kv_len, T)
+        _check(_lib.qmm_kv4_attn(ctypes.byref(kv), _ptr(q), q.stride(0), heads, scale, 1 if causal else 0, window, sinks,
+                                 _ptr(out), _ptr(lse), max_q, max_kv, _ptr(workspace), workspace.numel(),
+                                 _stream(q.device)), "qmm_kv4_attn")
     return (out, lse) if return_lse else out
 
 

@@ -13,6 +13,7 @@
 #include "gemv.h"
 #include "w4a8.h"
 #include "gemm.h"
+#include "kv4.h"
 #include "paged.h"
 
 namespace qmm {
@@ -280,6 +281,36 @@ static qmm_status check_paged(const qmm_paged_kv *kv)
         return QMM_ERR_NULL;
     if (!aligned(kv->k, 16) || !aligned(kv->v, 16) || !aligned(kv->block_table, 4) || !aligned(kv->cu_q, 4) ||
         !aligned(kv->kv_len, 4))
+        return QMM_ERR_ALIGN;
+    return QMM_OK;
+}
+
+// Shared checks of the 4-bit cache calls; fills what the kernels take.  A batch without tokens
+// or sequences passes with the sizes alone.
+static qmm_status check_kv4(const qmm_paged_kv4 *kv, qmm_paged_kv *codes, Kv4Scales *sc)
+{
+    if (!kv)
+        return QMM_ERR_NULL;
+    // (the members up to dtype are qmm_paged_kv's; strides of 16 bytes pass as multiples of 8)
+    *codes = {kv->k, kv->v, kv->page_stride, kv->slot_stride, kv->head_stride, kv->block_table, kv->cu_q, kv->kv_len,
+              kv->num_pages, kv->page_size, kv->blocks, kv->batch, kv->tokens, kv->kv_heads, kv->head_dim, kv->dtype};
+    *sc = {static_cast<uint16_t *>(kv->scales), kv->scale_page_stride, kv->scale_slot_stride, kv->scale_head_stride};
+    if (const qmm_status st = check_paged(codes); st != QMM_OK)
+        return st;
+    if (kv->kv_heads > 65536)
+        return QMM_ERR_UNSUPPORTED;
+    if ((kv->num_pages > 1 && sc->page < 0) || (kv->page_size > 1 && sc->slot < 0) || (kv->kv_heads > 1 && sc->head < 0))
+        return QMM_ERR_SHAPE;
+    const int step = kv->head_dim / 32;   // a key's scale patterns
+    if ((kv->num_pages > 1 && (kv->page_stride % 16 || sc->page % step)) ||
+        (kv->page_size > 1 && (kv->slot_stride % 16 || sc->slot % step)) ||
+        (kv->kv_heads > 1 && (kv->head_stride % 16 || sc->head % step)))
+        return QMM_ERR_ALIGN;
+    if (kv->batch == 0 || kv->tokens == 0)
+        return QMM_OK;
+    if (kv->blocks > 0 && kv->num_pages > 0 && !kv->scales)
+        return QMM_ERR_NULL;
+    if (!aligned(kv->scales, 2 * step))
         return QMM_ERR_ALIGN;
     return QMM_OK;
 }
@@ -801,6 +832,136 @@ qmm_status qmm_paged_attn(const qmm_paged_kv *kv, const void *q, int64_t q_strid
     p.causal = causal != 0;
     p.window = window;
     return from_cuda(attn_dispatch(p, max_q, max_kv, workspace, f->num_sms, stream));
+}
+
+qmm_status qmm_kv4_append(const qmm_paged_kv4 *kv, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                          const void *q, int64_t q_stride, void *q_out, int q_heads, const float *cos_sin, int rot,
+                          int rope_len, int interleaved, const void *q_norm, const void *k_norm, float eps,
+                          cudaStream_t stream)
+{
+    Kv4AppendParams p;
+    std::memset(&p, 0, sizeof(p));
+    const qmm_status st = check_kv4(kv, &p.kv, &p.sc);
+    if (st != QMM_OK)
+        return st;
+    if (rot < 0 || rot > kv->head_dim || rot % 16 || rope_len < 0 || q_heads < 0 || !(eps >= 0.f) || !(eps < INFINITY))
+        return QMM_ERR_SHAPE;
+    if (q_heads > 65536)
+        return QMM_ERR_UNSUPPORTED;
+    if (kv->tokens > 1 && (k_stride < 0 || v_stride < 0 || (q && q_stride < 0)))
+        return QMM_ERR_SHAPE;
+    if (kv->tokens > 1 && (k_stride % 8 || v_stride % 8 || (q && q_stride % 8)))
+        return QMM_ERR_ALIGN;
+    if (kv->batch == 0 || kv->tokens == 0)
+        return QMM_OK;
+    if (!k || !v || (rot > 0 && !cos_sin) || !q != !q_out)
+        return QMM_ERR_NULL;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(q, 16) || !aligned(q_out, 16) || !aligned(cos_sin, 16) ||
+        !aligned(q_norm, 16) || !aligned(k_norm, 16))
+        return QMM_ERR_ALIGN;
+    const DeviceFacts *f = device_facts();
+    if (!f || f->usable != QMM_OK)
+        return QMM_ERR_DEVICE;
+    p.k = static_cast<const uint16_t *>(k);
+    p.v = static_cast<const uint16_t *>(v);
+    p.q = static_cast<const uint16_t *>(q);
+    p.q_out = static_cast<uint16_t *>(q_out);
+    p.cos_sin = cos_sin;
+    p.status = f->status;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.q_stride = q_stride;
+    p.q_heads = q ? q_heads : 0;
+    p.rot = rot;
+    p.rope_len = rope_len;
+    p.interleaved = interleaved != 0;
+    p.by_page = fast_div(kv->page_size);
+    p.q_norm = static_cast<const uint16_t *>(q_norm);
+    p.k_norm = static_cast<const uint16_t *>(k_norm);
+    p.eps = eps;
+    return from_cuda(launch_kv4_append(p, stream));
+}
+
+qmm_status qmm_kv4_read(const qmm_paged_kv4 *kv, void *k_out, void *v_out, cudaStream_t stream)
+{
+    Kv4ReadParams p;
+    std::memset(&p, 0, sizeof(p));
+    const qmm_status st = check_kv4(kv, &p.kv, &p.sc);
+    if (st != QMM_OK)
+        return st;
+    if (kv->batch == 0 || kv->tokens == 0)
+        return QMM_OK;
+    if (!k_out || !v_out)
+        return QMM_ERR_NULL;
+    if (!aligned(k_out, 16) || !aligned(v_out, 16))
+        return QMM_ERR_ALIGN;
+    const DeviceFacts *f = device_facts();
+    if (!f || f->usable != QMM_OK)
+        return QMM_ERR_DEVICE;
+    p.k = static_cast<uint16_t *>(k_out);
+    p.v = static_cast<uint16_t *>(v_out);
+    p.status = f->status;
+    p.by_page = fast_div(kv->page_size);
+    p.by_heads = fast_div(kv->kv_heads);
+    return from_cuda(launch_kv4_read(p, f->num_sms, stream));
+}
+
+size_t qmm_kv4_attn_workspace(int q_heads, int kv_heads, int head_dim, int max_q)
+{
+    if (q_heads < 1 || kv_heads < 1 || q_heads > 65536 || q_heads % kv_heads || (head_dim != 64 && head_dim != 128) || max_q < 0)
+        return 0;
+    const DeviceFacts *f = device_facts();
+    if (!f || f->usable != QMM_OK)
+        return 0;
+    return kv4_attn_workspace_bytes(q_heads, kv_heads, head_dim, max_q, f->num_sms);
+}
+
+qmm_status qmm_kv4_attn(const qmm_paged_kv4 *kv, const void *q, int64_t q_stride, int q_heads, float scale, int causal,
+                        int window, int sinks, void *out, float *lse, int max_q, int max_kv, void *workspace,
+                        size_t workspace_bytes, cudaStream_t stream)
+{
+    Kv4AttnParams p;
+    std::memset(&p, 0, sizeof(p));
+    const qmm_status st = check_kv4(kv, &p.kv, &p.sc);
+    if (st != QMM_OK)
+        return st;
+    if (q_heads < 1 || q_heads % kv->kv_heads || window < 0 || (window > 0 && !causal) || sinks < 0 ||
+        (sinks > 0 && window == 0) || max_q < 0 || max_kv < 0 || !(scale > 0.f) || !(scale <= 2.0e38f) ||
+        (kv->tokens > 1 && q_stride < 0))   // scale log2(e) is finite
+        return QMM_ERR_SHAPE;
+    if (q_heads > 65536)
+        return QMM_ERR_UNSUPPORTED;
+    if (kv->tokens > 1 && q_stride % 8)
+        return QMM_ERR_ALIGN;
+    if (kv->batch == 0 || kv->tokens == 0)
+        return QMM_OK;
+    if (!q || !out || !workspace)
+        return QMM_ERR_NULL;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 16) || !aligned(lse, 4))
+        return QMM_ERR_ALIGN;
+    // row tiles of the batch are counted in 32 bits (no sequence has more than `tokens`)
+    const int group = q_heads / kv->kv_heads;
+    if ((static_cast<long long>(std::min(max_q, kv->tokens)) * group / 8 + 1) * kv->batch > 0x7fffffffLL ||
+        static_cast<long long>(kv->tokens) * group > 0x7fffffffLL)
+        return QMM_ERR_UNSUPPORTED;
+    // (max_q = 0: as for qmm_paged_attn)
+    const DeviceFacts *f = device_facts();
+    if (!f || f->usable != QMM_OK)
+        return max_q == 0 ? QMM_OK : QMM_ERR_DEVICE;
+    if (workspace_bytes < kv4_attn_workspace_bytes(q_heads, kv->kv_heads, kv->head_dim, max_q, f->num_sms))
+        return QMM_ERR_SHAPE;
+    p.q = static_cast<const uint16_t *>(q);
+    p.out = static_cast<uint16_t *>(out);
+    p.lse = lse;
+    p.status = f->status;
+    p.q_stride = q_stride;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.q_heads = q_heads;
+    p.group = group;
+    p.causal = causal != 0;
+    p.window = window;
+    p.sinks = sinks;
+    return from_cuda(kv4_attn_dispatch(p, max_q, max_kv, workspace, f->num_sms, stream));
 }
 
 qmm_status qmm_watchdog_selftest(cudaStream_t stream)

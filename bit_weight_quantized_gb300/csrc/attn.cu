@@ -192,6 +192,8 @@ cudaError_t launch_join(const AttnParams &p, int grid, bool few, int max_rows, c
                : cudaLaunchKernelEx(&cfg, join_chunk_kernel<D, BF16>, p);
 }
 
+}  // namespace
+
 cudaError_t launch_attn_join(const AttnParams &p, int grid, bool few, int max_rows, cudaStream_t stream)
 {
     const bool bf16 = p.kv.dtype == QMM_BF16;
@@ -201,6 +203,8 @@ cudaError_t launch_attn_join(const AttnParams &p, int grid, bool few, int max_ro
     return bf16 ? launch_join<64, true>(p, grid, few, max_rows, stream)
                 : launch_join<64, false>(p, grid, few, max_rows, stream);
 }
+
+namespace {
 
 // The decode kernel holds 16 query rows per key head.
 bool few_rows(int max_q, int group) { return static_cast<long long>(max_q) * group <= kDecodeRows; }

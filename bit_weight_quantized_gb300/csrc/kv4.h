@@ -1,0 +1,60 @@
+// kv4.h -- host interface of the 4-bit paged key / value cache kernels
+// (qmm_kv4_append, qmm_kv4_read, qmm_kv4_attn).
+#pragma once
+
+#include "paged.h"
+
+namespace qmm {
+
+// Values that share a scale and a zero.
+constexpr int kKv4Group = 64;
+
+// The scales of a 4-bit cache: element (page, slot, head) at page * page_stride + ...; a
+// key's scales, then its value's, one per group.  (The codes are qmm_paged_kv's k and v, with
+// strides in bytes.)
+struct Kv4Scales {
+    uint16_t *base;
+    long long page, slot, head;
+};
+
+struct Kv4AppendParams : AppendParams {
+    Kv4Scales sc;
+    const uint16_t *q_norm, *k_norm;   // weights of the norms, or nullptr
+    float eps;
+};
+
+struct Kv4ReadParams {
+    qmm_paged_kv kv;
+    Kv4Scales sc;
+    uint16_t *k, *v;                   // dense [tokens][kv_heads][D]
+    int *status;
+    int rows;                          // tokens per block
+    FastDiv by_page, by_heads;
+};
+
+struct Kv4AttnParams : AttnParams {
+    Kv4Scales sc;
+};
+
+cudaError_t launch_kv4_append(const Kv4AppendParams &p, cudaStream_t stream);
+cudaError_t launch_kv4_read(Kv4ReadParams &p, int num_sms, cudaStream_t stream);
+
+// Keys per unit of the kernel for few rows: a warp's stage holds 4 KB of codes.
+__host__ __device__ constexpr int kv4_keys(int head_dim, int warps) { return 4096 / head_dim * warps; }
+// Blocks of it per SM, of four or eight warps (16 rows take 168 registers a thread, 8 rows 128).
+__host__ __device__ constexpr int kv4_blocks_per_sm(int rows, int warps)
+{
+    return warps == 4 ? (rows == 8 ? 4 : 3) : rows == 8 ? 2 : 1;
+}
+
+// Clusters of `cluster` blocks of eight warps that run at once on the current device.
+int kv4_decode_clusters(int head_dim, bool bf16, int rows, int cluster);
+
+// p.warps: 4 or 8; p.tile_rows: 8 or 16.
+cudaError_t launch_kv4_decode(const Kv4AttnParams &p, int grid, cudaStream_t stream);
+
+size_t kv4_attn_workspace_bytes(int q_heads, int kv_heads, int head_dim, int max_q, int num_sms);
+cudaError_t kv4_attn_dispatch(Kv4AttnParams &p, int max_q, long long max_kv, void *workspace, int num_sms,
+                              cudaStream_t stream);
+
+}  // namespace qmm

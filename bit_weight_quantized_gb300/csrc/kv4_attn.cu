@@ -1,0 +1,91 @@
+// kv4_attn.cu -- qmm_kv4_attn: kernel choice and split sizes.
+#include <algorithm>
+
+#include "kv4.h"
+#include "paged.cuh"
+
+namespace qmm {
+
+namespace {
+
+// Blocks of four warps that a split goes over.
+int grid_of(int rows, int num_sms) { return kv4_blocks_per_sm(rows, 4) * num_sms; }
+
+// Work a block takes at least, in units: below this a split costs more (a second kernel,
+// the partial results) than the longer walk.
+constexpr int kMinUnits = 3;
+
+// Whole items in clusters against a split over all blocks: a cluster's block walks
+// units / c, a split one units * items / blocks and the joining kernel's time, some
+// kJoinUnits; and not more than kMostUnits, since whole items are not balanced where
+// lengths differ.
+constexpr int kJoinUnits = 4, kMostUnits = 10;
+
+// Blocks of eight warps per item where every item gets a cluster (or block) of its own:
+// clusters of the largest size that all run at once; 0: the axis is split over all blocks.
+int cluster_of(const Kv4AttnParams &p, long long items, long long span, int num_sms)
+{
+    const int keys = kv4_keys(p.kv.head_dim, 8), blocks = kv4_blocks_per_sm(p.tile_rows, 8) * num_sms;
+    const long long units = (span + keys - 1) / keys;
+    for (int c = kMaxCluster; c >= 1; c /= 2)
+        if (items * c <= blocks && (c == 1 || c / 2 < units) && (units + c - 1) / c <= kMostUnits &&
+            (units + c - 1) / c <= items * units / blocks + kJoinUnits &&
+            (c == 1 || items <= kv4_decode_clusters(p.kv.head_dim, p.kv.dtype == QMM_BF16, p.tile_rows, c)))
+            return c;
+    return 0;
+}
+
+}  // namespace
+
+size_t kv4_attn_workspace_bytes(int, int, int head_dim, int, int num_sms)
+{
+    const size_t g = grid_of(8, num_sms);
+    return g * 32 + 2 * g * kDecodeRows * (head_dim + 2) * 4;
+}
+
+cudaError_t kv4_attn_dispatch(Kv4AttnParams &p, int max_q, long long max_kv, void *workspace, int num_sms,
+                              cudaStream_t stream)
+{
+    // no sequence has more tokens than the batch: a caller's large bound adds no row tiles
+    max_q = std::max(1, std::min(max_q, p.kv.tokens));
+    const long long most = static_cast<long long>(p.kv.blocks) * p.kv.page_size, q_rows = static_cast<long long>(max_q) * p.group;
+    if (max_kv <= 0 || max_kv > most)
+        max_kv = most;
+    if (p.window >= most)   // no position lies further back
+        p.window = 0;
+    if (p.window == 0)
+        p.sinks = 0;
+    p.tile_rows = q_rows <= 8 ? 8 : 16;
+    p.row_tiles = static_cast<int>((q_rows + p.tile_rows - 1) / p.tile_rows);
+    p.by_group = fast_div(p.group);
+    p.by_tiles = fast_div(p.row_tiles);
+    p.by_page = fast_div(p.kv.page_size);
+    p.min_chunk = kMinUnits;
+    // keys of an item at most, and units more where its parts begin and end inside one
+    const long long seen = static_cast<long long>(p.window) + p.sinks + p.tile_rows / p.group + 1;
+    const bool part = p.window > 0 && seen < max_kv;
+    const long long span = part ? seen : max_kv;
+    const long long items = static_cast<long long>(p.kv.batch) * p.row_tiles * p.kv.kv_heads;
+    const int cluster = cluster_of(p, items, span, num_sms);
+    p.whole = cluster > 0;
+    p.cluster = std::max(cluster, 1);
+    p.warps = p.whole ? 8 : 4;
+    const int keys = kv4_keys(p.kv.head_dim, p.warps);
+    const long long longest = (span + keys - 1) / keys + (part ? 2 : 0);
+    int grid = grid_of(p.tile_rows, num_sms);
+    if (p.whole)
+        grid = static_cast<int>(items) * p.cluster;
+    else if (items * (longest + kDecodeSetup) < static_cast<long long>(grid) * p.min_chunk)
+        grid = static_cast<int>((items * (longest + kDecodeSetup) + p.min_chunk - 1) / p.min_chunk);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    const size_t g = grid_of(8, num_sms);
+    p.meta = reinterpret_cast<int4 *>(ws);
+    p.part_ml = reinterpret_cast<float *>(ws + g * 32);
+    p.part_o = p.part_ml + 2 * g * kDecodeRows * 2;
+    const cudaError_t e = launch_kv4_decode(p, grid, stream);
+    if (e != cudaSuccess || p.whole)
+        return e;
+    return launch_attn_join(p, grid, true, static_cast<int>(std::min(static_cast<long long>(p.tile_rows), q_rows)), stream);
+}
+
+}  // namespace qmm

@@ -1,0 +1,614 @@
+// kv4_decode.cu -- attention over the 4-bit paged cache for few query rows per key head:
+// at most 16 rows (token, query head of the key head) per work item.
+//
+//   K_j = (c_j - z) s per 64 values, likewise V_j:
+//   S_j = sum_g s_jg (sum_d q_d c_jd - z_jg sum_d q_d),  O = sum_j p_j s_jg (c_jd - z_jg)
+//
+// The codes themselves are the matrix instructions' operands; scales and zeros meet the
+// scores and the weights, of which there are D times fewer.  A code in the low four bits of
+// an fp16 pattern is the (subnormal) number c 2^-24, in the next four c 2^-20, both exact: a
+// word of eight codes becomes four operand words by a shift and four masks.  Which d a
+// place along an operand's axis stands for is free, so the queries are loaded in that
+// order, those against c 2^-20 scaled by 2^-4.  The tile is turned over (keys are the rows
+// of the scores' product, d those of the output's), so that 8 query rows, the most that a
+// single token of most models has per key head, fill an instruction: as columns.
+//
+// A product with a subnormal operand is aligned by its exponent field, so that sums keep
+// 2^-14 of a step s instead of fp32's precision: measured 2^-15 of a weight times s, where
+// the cache's own error is s / 2.  (Codes as 64 + c, normal numbers, would take 7
+// instructions for 8 codes instead of 5.)
+//
+// Queries are scaled per row by a power of two to below 2^15 and are then fp16 (bf16 has
+// 8 bits, so only values 2^-25 times the row's largest lose any).  A weight times its V
+// scale is rounded once to fp16, 2^-12 relative, with a power of two taken out that follows
+// the largest scale seen as the maximum follows the scores; that the zeros' share is
+// subtracted by the same rounded weights comes from one more product, of the zeros.
+//
+// Bound by the cache's bytes (D + D / 16 per key and head) and nearly as much by
+// instruction issue: some 250 instructions a warp for 16 keys of 128 (2176 bytes, which
+// the copy rate brings in 93 cycles).  Each of a block's warps walks its own keys with its
+// own ring of asynchronous copies, maximum, sum and output, as in attn_decode.cu, whose
+// split, clusters and end this has.
+#include <atomic>
+
+#include "attn_rows.cuh"
+#include "kv4.cuh"
+
+namespace qmm {
+
+namespace {
+
+constexpr float kGrow = 8.f;                         // log2 of the growth that replaces the maximum
+
+template <int D, int WARPS, int NB>
+struct Layout {
+    static constexpr int kRows = 8 * NB;
+    static constexpr int kWarpKeys = kv4_keys(D, 1);                      // a warp's keys of a unit
+    static constexpr int kKeys = kv4_keys(D, WARPS);
+    static constexpr int kRow = D / 2, kScaleRow = D / 16;                // bytes of a key's codes, and of both its scales
+    static constexpr int kCodes = kWarpKeys * kRow;                       // 2 KB
+    static constexpr int kStage = 2 * kCodes + kWarpKeys * kScaleRow;
+    static constexpr int kStages = 3;
+    static constexpr int kWarpBytes = kStages * kStage;
+    static constexpr int kOffIn = WARPS * kWarpBytes;                     // clusters: what the other blocks send
+    static constexpr int kOffInMl = kOffIn + kRows * D * 4;
+    static constexpr int kBytes = kOffIn, kClusterBytes = kOffInMl + kRows * kMaxCluster * 8;
+    static constexpr int kPitch = D + 8;
+    static constexpr int kOffMl = WARPS * kRows * kPitch * 4;
+    static_assert(kOffMl + WARPS * kRows * 8 <= kOffIn, "the warps' outputs reuse the rings");
+};
+
+// 8 or 4 bytes global -> shared (zeros where !ok)
+template <int BYTES>
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void *src, bool ok)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(ok ? BYTES : 0)
+                 : "memory");
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t addr)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint2 lds64(uint32_t addr)
+{
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+
+// An 8 x 8 matrix of 16-bit values, row g of it in lane group g: turned over.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v)
+{
+    uint32_t d;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+    return d;
+}
+
+// The key (row of a 16-key step, eight by eight) that index k of an operand's axis stands
+// for: with it and the swizzle below, neither the K reads (keys k = 0 .. 3 or 4 .. 7 at once)
+// nor the V reads (even or odd k) meet in a bank.
+__device__ __forceinline__ int key_row(int k) { return (k >> 1 & 1) | ((k ^ k >> 2) & 1) << 1 | (k & 4) | (k & 8); }
+
+// Byte of 16-byte chunk c of row r of a tile of codes.
+template <int D>
+__device__ __forceinline__ uint32_t code_addr(int r, int c)
+{
+    return static_cast<uint32_t>(r * (D / 2) + ((D == 128 ? c ^ (r & 2) : c) << 4));
+}
+
+template <int D, bool BF16, int WARPS, int NB>
+__global__ void __launch_bounds__(32 * WARPS, kv4_blocks_per_sm(8 * NB, WARPS))
+kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p)
+{
+    using L = Layout<D, WARPS, NB>;
+    constexpr int kThreads = 32 * WARPS, kKeys = L::kKeys, kWarpKeys = L::kWarpKeys, kRows = L::kRows;
+    constexpr int kGroups = D / kKv4Group, kSteps = kWarpKeys / 16;
+    constexpr int kChunks = D / 32;                    // 16-byte chunks of a key's codes
+    constexpr int kRowsPerCopy = 32 / kChunks, kCopies = kWarpKeys / kRowsPerCopy;
+    constexpr int kLook = kWarpKeys / 32;              // keys whose place a lane looks up, per tile
+    // weights are 2^(s - m + kShift); with their V scale, over the power of two, at most 2^15
+    constexpr float kShift = BF16 ? 0.f : 7.f;
+    constexpr float kLift = BF16 ? 128.f : 1.f;
+    constexpr uint32_t kM0 = 0x000f000fu, kM1 = 0x00f000f0u;
+
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ Share share;
+    __shared__ long long red[WARPS];
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g = lane >> 2, t = lane & 3;
+    if (tid == 0)
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (p.cluster > 1)
+        cluster_arrive();   // (waited for before anything is sent to another block)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    find_share<kKeys, kDecodeSetup, kThreads, true>(p, red, &share);
+
+    const uint32_t ring = smem_u32(smem) + warp * L::kWarpBytes;
+    const int crow = lane / kChunks, cchunk = lane % kChunks;
+
+    if (!p.whole && tid == 0)
+        p.meta[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
+
+    Walk<kKeys, kDecodeSetup, true> walk;
+    walk.begin(share);
+    Segment sg;
+    bool more = p.whole ? share.end > 0 : walk.next(p, sg);
+    if (p.whole && more) {   // the whole item; a cluster's blocks take a stretch each
+        const int rank = blockIdx.x % p.cluster, all = share.r.units;
+        sg.r = share.r;
+        sg.h = share.h;
+        sg.start = 0;
+        sg.off = rank * all / p.cluster;
+        sg.units = (rank + 1) * all / p.cluster - sg.off;
+    }
+    if (!more && p.cluster > 1)
+        cluster_wait();
+    for (; more; more = !p.whole && walk.next(p, sg)) {
+        const RowTile &r = sg.r;
+        const uint8_t *kbase = static_cast<const uint8_t *>(p.kv.k) + sg.h * p.kv.head_stride;
+        const uint8_t *vbase = static_cast<const uint8_t *>(p.kv.v) + sg.h * p.kv.head_stride;
+        const uint16_t *sbase = p.sc.base + sg.h * p.sc.head;
+        // the warp's first key of tile j
+        auto tile_key = [&](int j) { return unit_key<kKeys>(p, r, sg.off + j) + warp * kWarpKeys; };
+        auto reads = [&](int j, int key) { return j < sg.units && key < r.hi && (key >= r.lo || key < p.sinks); };
+        // The pages of the lane's keys of a tile (lane, lane + 32) are looked up one tile ahead
+        // and not looked at before the tile is loaded: the warp would wait for the table here.
+        struct Look {
+            int page[kLook];
+        };
+        auto look_up = [&](int j) {
+            Look k;
+            const int kb = j < sg.units ? tile_key(j) : 0;
+#pragma unroll
+            for (int i = 0; i < kLook; ++i)
+                k.page[i] = reads(j, kb + lane + 32 * i) ?
+                    p.kv.block_table[static_cast<long long>(r.b) * p.kv.blocks + p.by_page(kb + lane + 32 * i)] : 0;
+            return k;
+        };
+        auto load = [&](int j, const Look &look) {
+            const uint32_t dst = ring + (j % L::kStages) * L::kStage;
+            const int kb = tile_key(j);
+            long long off[kLook];
+#pragma unroll
+            for (int i = 0; i < kLook; ++i) {
+                const int key = kb + lane + 32 * i, slot = key - p.by_page(key) * p.kv.page_size, page = look.page[i];
+                bool ok = reads(j, key);
+                if (ok && (page < 0 || page >= p.kv.num_pages)) {
+                    record_error(p.status, QMM_ERR_INDEX);
+                    ok = false;
+                }
+                off[i] = ok ? page * p.kv.page_stride + slot * p.kv.slot_stride : -1;
+                // (a key that nobody sees gets scales of zero; its codes do not matter)
+                cp_async_small<L::kScaleRow>(dst + 2 * L::kCodes + (lane + 32 * i) * L::kScaleRow,
+                                             ok ? sbase + scale_offset(p.sc, page, slot) : p.sc.base, ok);
+            }
+#pragma unroll
+            for (int c = 0; c < kCopies; ++c) {
+                const int row = c * kRowsPerCopy + crow;
+                const long long o = __shfl_sync(0xffffffffu, off[c * kRowsPerCopy / 32], row & 31);
+                const bool ok = o >= 0;
+                const long long e = ok ? o + cchunk * 16 : 0;
+                cp_async16_or_zero(dst + code_addr<D>(row, cchunk), kbase + e, ok);
+                cp_async16_or_zero(dst + L::kCodes + code_addr<D>(row, cchunk), vbase + e, ok);
+            }
+        };
+
+        Look first[L::kStages - 1];
+#pragma unroll
+        for (int j = 0; j < L::kStages - 1; ++j)
+            first[j] = look_up(j);
+        Look ahead = look_up(L::kStages - 1);
+
+        // queries in operand order: row g, values 16 t .. 16 t + 15 of every group
+        uint32_t qf[NB][kGroups][4][2];
+        float qs[NB][kGroups][2], rowf[NB][2];       // of rows 2 t, 2 t + 1: sums over the groups, factor of the scores
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            const int row = 8 * nb + g, rr = r.row0 + row, tok = p.by_group(rr);
+            uint32_t x[kGroups][8];
+            const uint16_t *src = p.q + (r.t0 + tok) * p.q_stride + static_cast<long long>(sg.h * p.group + rr - tok * p.group) * D;
+#pragma unroll
+            for (int gr = 0; gr < kGroups; ++gr)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                    if (row < r.rows)
+                        v = *reinterpret_cast<const uint4 *>(src + gr * kKv4Group + 16 * t + 8 * i);
+                    x[gr][4 * i] = v.x; x[gr][4 * i + 1] = v.y; x[gr][4 * i + 2] = v.z; x[gr][4 * i + 3] = v.w;
+                }
+            float most = 0.f;
+#pragma unroll
+            for (int gr = 0; gr < kGroups; ++gr)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    most = fmaxf(most, fmaxf(fabsf(lo16<BF16>(x[gr][i])), fabsf(hi16<BF16>(x[gr][i]))));
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+            // a power of two that brings the largest to 2^14 .. 2^15 (exponents kept where both
+            // it and its inverse with the codes' 2^24 are normal numbers)
+            const uint32_t ex = min(max(__float_as_uint(most) >> 23, 15u), 243u);
+            const float down = __uint_as_float((268u - ex) << 23), up = __uint_as_float((ex + 10u) << 23);
+            float sum[kGroups];
+#pragma unroll
+            for (int gr = 0; gr < kGroups; ++gr) {
+                sum[gr] = 0.f;
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {        // d = 8 w .. 8 w + 7 of the sixteen
+                    float v[8];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        v[2 * i] = lo16<BF16>(x[gr][4 * w + i]) * down;
+                        v[2 * i + 1] = hi16<BF16>(x[gr][4 * w + i]) * down;
+                        sum[gr] += v[2 * i] + v[2 * i + 1];
+                    }
+                    qf[nb][gr][2 * w][0] = pack16<false>(v[0], v[4]);
+                    qf[nb][gr][2 * w][1] = pack16<false>(v[2], v[6]);
+                    qf[nb][gr][2 * w + 1][0] = pack16<false>(v[1] * 0.0625f, v[5] * 0.0625f);
+                    qf[nb][gr][2 * w + 1][1] = pack16<false>(v[3] * 0.0625f, v[7] * 0.0625f);
+                }
+                sum[gr] += __shfl_xor_sync(0xffffffffu, sum[gr], 1);
+                sum[gr] += __shfl_xor_sync(0xffffffffu, sum[gr], 2);
+                sum[gr] *= 5.9604644775390625e-8f;   // 2^-24, as the codes are
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    qs[nb][gr][e] = __shfl_sync(0xffffffffu, sum[gr], 8 * t + 4 * e);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                rowf[nb][e] = __shfl_sync(0xffffffffu, up, 8 * t + 4 * e) * p.scale_log2;
+        }
+
+#pragma unroll
+        for (int j = 0; j < L::kStages - 1; ++j) {
+            if (j < sg.units)
+                load(j, first[j]);
+            cp_async_commit();
+        }
+
+        // keys that the lane's rows see, and that every row of the tile sees (rows past the
+        // tile do not count)
+        int2 see[NB][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                see[nb][e] = row_keys(p, r, r.row0 + 8 * nb + 2 * t + e);
+        const int all_lo = row_keys(p, r, r.row0 + r.rows - 1).x, all_hi = row_keys(p, r, r.row0).y;
+
+        float o[NB][kGroups][4][4], oz[NB][kGroups][4];   // [tile of d][fragment]; the zeros' share
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int gr = 0; gr < kGroups; ++gr)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    oz[nb][gr][e] = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        o[nb][gr][i][e] = 0.f;
+                }
+        float m[NB][2], l[NB][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+            m[nb][0] = m[nb][1] = -INFINITY, l[nb][0] = l[nb][1] = 0.f;
+        float vmost = 0.f, vdown = kLift;            // V scales are below vmost; what brings that to one
+
+#pragma unroll 1
+        for (int j = 0; j < sg.units; ++j) {
+            if (j + L::kStages - 1 < sg.units)
+                load(j + L::kStages - 1, ahead);
+            cp_async_commit();
+            ahead = look_up(j + L::kStages);
+            cp_async_wait_group<L::kStages - 1>();
+            __syncwarp();
+            const int kb = tile_key(j);
+            if (kb < r.hi && (kb + kWarpKeys > r.lo || kb < p.sinks)) {
+                const uint32_t ks = ring + (j % L::kStages) * L::kStage, vs = ks + L::kCodes, ss = vs + L::kCodes;
+                const bool masked = (kb < all_lo && kb + kWarpKeys > p.sinks) || kb + kWarpKeys - 1 > all_hi;
+#pragma unroll
+                for (int st = 0; st < kSteps; ++st) {
+                    // scores: rows are keys, columns query rows
+                    const int k0 = 16 * st + key_row(g), k1 = k0 + 8;
+                    float s[NB][4];
+                    uint32_t sc0[kGroups], sc1[kGroups];     // the keys' scale words: K's groups, V's groups
+                    if constexpr (kGroups == 2) {
+                        const uint2 a = lds64(ss + k0 * L::kScaleRow), b = lds64(ss + k1 * L::kScaleRow);
+                        sc0[0] = a.x; sc0[1] = a.y; sc1[0] = b.x; sc1[1] = b.y;
+                    } else {
+                        sc0[0] = lds32(ss + k0 * L::kScaleRow);
+                        sc1[0] = lds32(ss + k1 * L::kScaleRow);
+                    }
+                    // pattern i of a key's scales: K's 0 .. kGroups - 1, then V's
+                    auto pattern = [](const uint32_t (&w)[kGroups], int i) { return i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xffffu; };
+#pragma unroll
+                    for (int gr = 0; gr < kGroups; ++gr) {
+                        const uint2 a = lds64(ks + code_addr<D>(k0, 2 * gr + (t >> 1)) + 8 * (t & 1));
+                        const uint2 b = lds64(ks + code_addr<D>(k1, 2 * gr + (t >> 1)) + 8 * (t & 1));
+                        const uint32_t aw[2] = {a.x, a.y}, bw[2] = {b.x, b.y};
+                        float acc[NB][4];
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                acc[nb][e] = 0.f;
+#pragma unroll
+                        for (int w = 0; w < 2; ++w) {
+                            const uint32_t a8 = aw[w] >> 8, b8 = bw[w] >> 8;
+#pragma unroll
+                            for (int nb = 0; nb < NB; ++nb) {
+                                mma_f16_16816(acc[nb], aw[w] & kM0, bw[w] & kM0, a8 & kM0, b8 & kM0, qf[nb][gr][2 * w][0],
+                                              qf[nb][gr][2 * w][1]);
+                                mma_f16_16816(acc[nb], aw[w] & kM1, bw[w] & kM1, a8 & kM1, b8 & kM1, qf[nb][gr][2 * w + 1][0],
+                                              qf[nb][gr][2 * w + 1][1]);
+                            }
+                        }
+                        const uint32_t u0 = pattern(sc0, gr), u1 = pattern(sc1, gr);
+                        const float s0 = scale_of<BF16>(u0), s1 = scale_of<BF16>(u1);
+                        const float z0 = __uint_as_float(0x4b000000u | (u0 & 15u)) - 8388608.f;
+                        const float z1 = __uint_as_float(0x4b000000u | (u1 & 15u)) - 8388608.f;
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float x = fmaf(-(e < 2 ? z0 : z1), qs[nb][gr][e & 1], acc[nb][e]) * (e < 2 ? s0 : s1);
+                                s[nb][e] = gr == 0 ? x : s[nb][e] + x;
+                            }
+                    }
+                    float vsc[kGroups][2];
+                    bool up = false;
+#pragma unroll
+                    for (int gr = 0; gr < kGroups; ++gr) {
+                        vsc[gr][0] = scale_of<BF16>(pattern(sc0, kGroups + gr));
+                        vsc[gr][1] = scale_of<BF16>(pattern(sc1, kGroups + gr));
+                        up |= vsc[gr][0] > vmost || vsc[gr][1] > vmost;
+                    }
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            s[nb][e] *= rowf[nb][e & 1];
+                        if (masked) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int key = kb + (e < 2 ? k0 : k1);
+                                if ((key < see[nb][e & 1].x && key >= p.sinks) || key > see[nb][e & 1].y)
+                                    s[nb][e] = -INFINITY;
+                            }
+                        }
+                        up |= fmaxf(s[nb][0], s[nb][2]) > m[nb][0] + kGrow || fmaxf(s[nb][1], s[nb][3]) > m[nb][1] + kGrow;
+                    }
+                    if (__any_sync(0xffffffffu, up)) {
+                        // a new maximum of some row, or a larger V scale
+                        float big = 0.f;
+#pragma unroll
+                        for (int gr = 0; gr < kGroups; ++gr)
+                            big = fmaxf(big, fmaxf(vsc[gr][0], vsc[gr][1]));
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1)
+                            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
+                        float vf = 1.f;
+                        if (big > vmost) {
+                            const uint32_t ex = min(max(__float_as_uint(big) >> 23, 1u), 245u);
+                            const float down = __uint_as_float((253u - ex) << 23) * kLift;
+                            vf = down / vdown;               // (powers of two; nothing is there before the first)
+                            if (vmost == 0.f)
+                                vf = 0.f;
+                            vdown = down;
+                            vmost = __uint_as_float((ex + 1u) << 23);
+                        }
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb) {
+                            float f[2];
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                float x = fmaxf(s[nb][e], s[nb][2 + e]);
+#pragma unroll
+                                for (int d = 4; d < 32; d <<= 1)
+                                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+                                const bool grow = x > m[nb][e] + kGrow;
+                                const float a = grow ? ex2(m[nb][e] - x) : 1.f;
+                                m[nb][e] = grow ? x : m[nb][e];
+                                l[nb][e] *= a;
+                                f[e] = a * vf;
+                            }
+#pragma unroll
+                            for (int gr = 0; gr < kGroups; ++gr)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    oz[nb][gr][e] *= f[e & 1];
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i)
+                                        o[nb][gr][i][e] *= f[e & 1];
+                                }
+                        }
+                    }
+                    // weights, times their keys' V scales, as the right operand
+                    uint32_t pf[NB][kGroups][2];
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) {
+                        const float n0 = kShift - (m[nb][0] == -INFINITY ? 0.f : m[nb][0]);
+                        const float n1 = kShift - (m[nb][1] == -INFINITY ? 0.f : m[nb][1]);
+                        const float w0 = ex2(s[nb][0] + n0), w1 = ex2(s[nb][1] + n1);
+                        const float w2 = ex2(s[nb][2] + n0), w3 = ex2(s[nb][3] + n1);
+                        l[nb][0] += w0 + w2;
+                        l[nb][1] += w1 + w3;
+#pragma unroll
+                        for (int gr = 0; gr < kGroups; ++gr) {
+                            const float a = vsc[gr][0] * vdown, b = vsc[gr][1] * vdown;
+                            pf[nb][gr][0] = transpose8(pack16<false>(w0 * a, w1 * a));
+                            pf[nb][gr][1] = transpose8(pack16<false>(w2 * b, w3 * b));
+                        }
+                    }
+                    // output: rows are d, columns query rows
+                    const int r0 = 16 * st + key_row(2 * t), r1 = 16 * st + key_row(2 * t + 1);
+                    uint32_t zw[4];                          // the V scale words of the keys 2 t, 2 t + 1, + 8
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        zw[i] = lds32(ss + ((i & 1 ? r1 : r0) + 8 * (i >> 1)) * L::kScaleRow + (kGroups == 2 ? 4 : 0));
+#pragma unroll
+                    for (int gr = 0; gr < kGroups; ++gr) {
+                        const uint32_t sel = kGroups == 2 && gr == 0 ? 0x5410u : 0x7632u;
+                        const uint32_t z0 = __byte_perm(zw[0], zw[1], sel) & kM0, z1 = __byte_perm(zw[2], zw[3], sel) & kM0;
+                        uint32_t v[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            v[i] = lds32(vs + code_addr<D>((i & 1 ? r1 : r0) + 8 * (i >> 1), 2 * gr + (g >> 2)) + 4 * (g & 3));
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {   // codes 0 .. 3, 4 .. 7 of the word
+                            const uint32_t hs = half ? 0x7632u : 0x5410u;
+                            const uint32_t a = __byte_perm(v[0], v[1], hs), b = __byte_perm(v[2], v[3], hs);
+                            const uint32_t a8 = a >> 8, b8 = b >> 8;
+#pragma unroll
+                            for (int nb = 0; nb < NB; ++nb) {
+                                mma_f16_16816(o[nb][gr][2 * half], a & kM0, a & kM1, b & kM0, b & kM1, pf[nb][gr][0], pf[nb][gr][1]);
+                                mma_f16_16816(o[nb][gr][2 * half + 1], a8 & kM0, a8 & kM1, b8 & kM0, b8 & kM1, pf[nb][gr][0],
+                                              pf[nb][gr][1]);
+                            }
+                        }
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb)
+                            mma_f16_16816(oz[nb][gr], z0, 0u, z1, 0u, pf[nb][gr][0], pf[nb][gr][1]);
+                    }
+                }
+            }
+            __syncwarp();   // every lane has read the slot before it is filled again
+        }
+        cp_async_wait_group<0>();
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1)
+                    l[nb][e] += __shfl_xor_sync(0xffffffffu, l[nb][e], d);
+
+        // the warps' maxima, sums and outputs meet in shared memory (over the rings)
+        __syncthreads();
+        float *wo = reinterpret_cast<float *>(smem);
+        float *wml = reinterpret_cast<float *>(smem + L::kOffMl);
+        const float unit = 16777216.f / vdown;       // 2^24 for the codes
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int row = warp * kRows + 8 * nb + 2 * t + e;
+#pragma unroll
+                for (int gr = 0; gr < kGroups; ++gr) {
+                    float *w = wo + row * L::kPitch + gr * kKv4Group + 8 * g;
+                    float v[8];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {    // values 2 i (c 2^-24) and 2 i + 1 (c 2^-20)
+                        v[2 * i] = (o[nb][gr][i][e] - oz[nb][gr][e]) * unit;
+                        v[2 * i + 1] = fmaf(o[nb][gr][i][2 + e], 0.0625f, -oz[nb][gr][e]) * unit;
+                    }
+                    *reinterpret_cast<float4 *>(w) = make_float4(v[0], v[1], v[2], v[3]);
+                    *reinterpret_cast<float4 *>(w + 4) = make_float4(v[4], v[5], v[6], v[7]);
+                }
+                if (g == 0)
+                    *reinterpret_cast<float2 *>(wml + row * 2) = make_float2(m[nb][e], l[nb][e]);
+            }
+        __syncthreads();
+        if (finish_rows<L, D, BF16, WARPS, kRows>(p, sg, smem))
+            return;
+        if (tid == 0 && is_last_part(sg))
+            write_meta<kDecodeSetup>(p, sg, share.chunk);
+        __syncthreads();   // the rings are free again
+    }
+}
+
+template <int D, bool BF16, int WARPS, int NB>
+cudaError_t decode_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute (&attr)[2], int grid, int cluster,
+                          cudaStream_t stream)
+{
+    using L = Layout<D, WARPS, NB>;
+    static SmemLimit limit;
+    if (const cudaError_t e = ensure_smem_limit(limit, kv4_decode_kernel<D, BF16, WARPS, NB>, L::kClusterBytes, true);
+        e != cudaSuccess)
+        return e;
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(32 * WARPS);
+    cfg.dynamicSmemBytes = cluster > 1 ? L::kClusterBytes : L::kBytes;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaSuccess;
+}
+
+template <int D, bool BF16, int WARPS, int NB>
+cudaError_t launch_width(const Kv4AttnParams &p, int grid, cudaStream_t stream)
+{
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    if (const cudaError_t e = decode_config<D, BF16, WARPS, NB>(cfg, attr, grid, p.cluster, stream); e != cudaSuccess)
+        return e;
+    return cudaLaunchKernelEx(&cfg, kv4_decode_kernel<D, BF16, WARPS, NB>, p);
+}
+
+// Clusters of 2, 4 or 8 blocks that run at once on the current device: fewer than its
+// blocks' number would give, since a cluster lies in one part of the device.
+template <int D, bool BF16, int NB>
+int active_clusters(int cluster)
+{
+    static std::atomic<int> known[64][4] = {};   // + 1; per device and log2 of the size
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
+        return 0;
+    std::atomic<int> &k = known[dev][cluster == 2 ? 1 : cluster == 4 ? 2 : 3];
+    if ((n = k.load(std::memory_order_relaxed)) > 0)
+        return n - 1;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    if (decode_config<D, BF16, 8, NB>(cfg, attr, cluster, cluster, nullptr) != cudaSuccess)
+        return 0;
+    cfg.attrs = attr + 1;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kv4_decode_kernel<D, BF16, 8, NB>, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        n = 0;
+    }
+    k.store(n + 1, std::memory_order_relaxed);
+    return n;
+}
+
+template <int D, bool BF16>
+cudaError_t launch_decode(const Kv4AttnParams &p, int grid, cudaStream_t stream)
+{
+    if (p.tile_rows == 8)
+        return p.warps == 8 ? launch_width<D, BF16, 8, 1>(p, grid, stream) : launch_width<D, BF16, 4, 1>(p, grid, stream);
+    return p.warps == 8 ? launch_width<D, BF16, 8, 2>(p, grid, stream) : launch_width<D, BF16, 4, 2>(p, grid, stream);
+}
+
+template <int D, bool BF16>
+int clusters_of(int rows, int cluster)
+{
+    return rows == 8 ? active_clusters<D, BF16, 1>(cluster) : active_clusters<D, BF16, 2>(cluster);
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_decode(const Kv4AttnParams &p, int grid, cudaStream_t stream)
+{
+    const bool bf16 = p.kv.dtype == QMM_BF16;
+    if (p.kv.head_dim == 128)
+        return bf16 ? launch_decode<128, true>(p, grid, stream) : launch_decode<128, false>(p, grid, stream);
+    return bf16 ? launch_decode<64, true>(p, grid, stream) : launch_decode<64, false>(p, grid, stream);
+}
+
+int kv4_decode_clusters(int head_dim, bool bf16, int rows, int cluster)
+{
+    if (head_dim == 128)
+        return bf16 ? clusters_of<128, true>(rows, cluster) : clusters_of<128, false>(rows, cluster);
+    return bf16 ? clusters_of<64, true>(rows, cluster) : clusters_of<64, false>(rows, cluster);
+}
+
+}  // namespace qmm

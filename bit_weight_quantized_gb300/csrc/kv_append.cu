@@ -55,29 +55,6 @@ __device__ __forceinline__ void rotate_pairs(uint4 &a, uint4 &b, const float (&c
     b = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
-// The sequence that owns token t (the number of sequences that end at or before
-// t), its end cu_q[b + 1] and its key count, by one warp: lanes look at 32
-// sequences at a time.  b = batch if no sequence owns it.
-__device__ __forceinline__ void find_sequence(const qmm_paged_kv &kv, int t, int lane, int &b, int &end, int &keys)
-{
-    for (int b0 = 0; b0 < kv.batch; b0 += 32) {
-        const int i = b0 + lane;
-        int e = 0x7fffffff, k = 0;
-        if (i < kv.batch) {
-            e = kv.cu_q[i + 1];
-            k = kv.kv_len[i];
-        }
-        const int cnt = __popc(__ballot_sync(0xffffffffu, e <= t));
-        if (cnt < 32) {
-            b = b0 + cnt;
-            end = __shfl_sync(0xffffffffu, e, cnt);
-            keys = __shfl_sync(0xffffffffu, k, cnt);
-            return;
-        }
-    }
-    b = kv.batch;
-}
-
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kAppendThreads)
 kv_append_kernel(const __grid_constant__ AppendParams p)

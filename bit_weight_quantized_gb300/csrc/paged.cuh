@@ -117,6 +117,29 @@ __device__ __forceinline__ long long key_offset(const qmm_paged_kv &kv, const Fa
     return page * kv.page_stride + slot * kv.slot_stride;
 }
 
+// The sequence that owns token t (the number of sequences that end at or before
+// t), its end cu_q[b + 1] and its key count, by one warp: lanes look at 32
+// sequences at a time.  b = batch if no sequence owns it.
+__device__ __forceinline__ void find_sequence(const qmm_paged_kv &kv, int t, int lane, int &b, int &end, int &keys)
+{
+    for (int b0 = 0; b0 < kv.batch; b0 += 32) {
+        const int i = b0 + lane;
+        int e = 0x7fffffff, k = 0;
+        if (i < kv.batch) {
+            e = kv.cu_q[i + 1];
+            k = kv.kv_len[i];
+        }
+        const int cnt = __popc(__ballot_sync(0xffffffffu, e <= t));
+        if (cnt < 32) {
+            b = b0 + cnt;
+            end = __shfl_sync(0xffffffffu, e, cnt);
+            keys = __shfl_sync(0xffffffffu, k, cnt);
+            return;
+        }
+    }
+    b = kv.batch;
+}
+
 // ---- the split of an attention call --------------------------------------------------
 // An item is one row tile of one sequence with one key head: tile_rows consecutive rows
 // of the sequence's (token, query head of the key head) pairs, token-major, with the
@@ -137,7 +160,21 @@ struct RowTile {
 // difference is taken: pos may be negative (padding) and the window as large as an int.
 __host__ __device__ __forceinline__ int window_start(int pos, int window) { return pos >= window ? pos - window + 1 : 0; }
 
+// With first tokens that stay visible (SINKS), the units that hold them and lie before the
+// window's come first: unit u of the item holds keys from unit_key(p, r, u).
 template <int KEYS>
+__device__ __forceinline__ int sink_units(const AttnParams &p, const RowTile &r)
+{
+    return min(r.lo / KEYS, p.sinks / KEYS + (p.sinks % KEYS != 0));
+}
+
+template <int KEYS>
+__device__ __forceinline__ int unit_key(const AttnParams &p, const RowTile &r, int u)
+{
+    return (u < sink_units<KEYS>(p, r) ? u : r.unit0 + u) * KEYS;
+}
+
+template <int KEYS, bool SINKS = false>
 __device__ __forceinline__ RowTile row_tile(const AttnParams &p, int i)
 {
     RowTile r;
@@ -159,6 +196,11 @@ __device__ __forceinline__ RowTile row_tile(const AttnParams &p, int i)
     r.lo = p.window > 0 ? min(r.hi, window_start(first, p.window)) : 0;
     r.unit0 = r.lo / KEYS;
     r.units = max(1, (r.hi + KEYS - 1) / KEYS - r.unit0);
+    if constexpr (SINKS) {
+        const int first_units = sink_units<KEYS>(p, r);
+        r.unit0 -= first_units;
+        r.units += first_units;
+    }
     return r;
 }
 
@@ -198,14 +240,14 @@ __device__ __forceinline__ long long divide(long long a, long long b)
 
 // Called by all THREADS threads of the block; `red` is scratch of THREADS / 32
 // words of 8 bytes, `out` the shared result.
-template <int KEYS, int SETUP, int THREADS>
+template <int KEYS, int SETUP, int THREADS, bool SINKS = false>
 __device__ __forceinline__ void find_share(const AttnParams &p, long long *red, Share *out)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (p.whole && !p.unsplit) {   // cluster (or block) c holds item c
         if (tid == 0) {
             const int item = blockIdx.x / p.cluster, i = item / p.kv.kv_heads;
-            const RowTile r = row_tile<KEYS>(p, i);
+            const RowTile r = row_tile<KEYS, SINKS>(p, i);
             out->i = i;
             out->r = r;
             out->h = item - i * p.kv.kv_heads;
@@ -224,7 +266,7 @@ __device__ __forceinline__ void find_share(const AttnParams &p, long long *red, 
     long long sum = 0;
     RowTile r;
     for (int i = i0; i < i1; ++i) {
-        r = row_tile<KEYS>(p, i);
+        r = row_tile<KEYS, SINKS>(p, i);
         sum += static_cast<long long>(r.units ? SETUP + r.units : 0) * p.kv.kv_heads;
         if (r.row0 == 0 && static_cast<long long>(r.n) * p.group > static_cast<long long>(p.row_tiles) * p.tile_rows)
             record_error(p.status, QMM_ERR_INDEX);   // more new tokens than max_q
@@ -258,7 +300,7 @@ __device__ __forceinline__ void find_share(const AttnParams &p, long long *red, 
         long long start = before;
         for (int i = i0; i < i1; ++i) {
             if (per > 1)
-                r = row_tile<KEYS>(p, i);
+                r = row_tile<KEYS, SINKS>(p, i);
             const int len = r.units ? SETUP + r.units : 0;
             const long long all = static_cast<long long>(len) * p.kv.kv_heads;
             if (at < start + all) {
@@ -285,7 +327,7 @@ struct Segment {
 };
 
 // Walks a share.  next() gives its segments in order.
-template <int KEYS, int SETUP>
+template <int KEYS, int SETUP, bool SINKS = false>
 struct Walk {
     long long at, end, chunk, start;
     int i, h;
@@ -309,7 +351,7 @@ struct Walk {
             do {
                 if (++i >= p.kv.batch * p.row_tiles)
                     return false;
-                r = row_tile<KEYS>(p, i);
+                r = row_tile<KEYS, SINKS>(p, i);
             } while (r.units == 0);
         }
         return true;

@@ -69,6 +69,7 @@ struct AttnParams {
     float scale_log2;              // scale * log2(e): the softmax works in powers of two
     int q_heads, group;            // query heads, query heads per key head
     int causal, window;
+    int sinks;                     // first tokens that a window leaves visible (4-bit cache)
     int tile_rows;                 // rows per tile
     int row_tiles;                 // row tiles per sequence (of the longest one)
     FastDiv by_group, by_tiles, by_page;   // divisions by group, row_tiles, page_size
@@ -104,6 +105,8 @@ int attn_decode_clusters(int head_dim, bool bf16, int warps, int cluster);
 
 cudaError_t launch_attn_decode(const AttnParams &p, int grid, cudaStream_t stream);
 cudaError_t launch_attn_chunk(const AttnParams &p, int grid, cudaStream_t stream);
+// Joins the partial results of a split call of `grid` blocks; few: parts of the decode kernel.
+cudaError_t launch_attn_join(const AttnParams &p, int grid, bool few, int max_rows, cudaStream_t stream);
 
 // Sets p.box and the tensor maps where the cache takes tensor copies.
 void attn_set_tma(AttnParams &p);

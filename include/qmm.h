@@ -426,6 +426,78 @@ QMM_API qmm_status qmm_paged_attn(const qmm_paged_kv *kv, const void *q, int64_t
  * device (an upper bound over every batch), or 0 for sizes it does not take. */
 QMM_API size_t qmm_paged_attn_workspace(int q_heads, int kv_heads, int head_dim, int max_q);
 
+/* ---- The paged cache in 4 bits ------------------------------------------------
+ *
+ * The same paged cache and batch (qmm_paged_kv above: sequences, lengths, block
+ * table, page sizes, padding, device-side checks) with 4.25 bits a value.  64 values of a
+ * head share a scale s and a zero z; code c, 0 .. 15, stands for
+ *     (c - z) * s
+ * as the weights' codes do.  s has 4 significant bits in bf16 and 7 in fp16, so that every
+ * value the cache stands for is exact in its type.
+ *   k, v     (device) codes: bytes page * page_stride + slot * slot_stride + head *
+ *            head_stride + 0 .. head_dim / 2 - 1; byte i holds codes 2 i (low half) and
+ *            2 i + 1.  16-byte aligned; strides in bytes, multiples of 16.
+ *   scales   (device) 16-bit patterns: elements page * scale_page_stride + slot *
+ *            scale_slot_stride + head * scale_head_stride + 0 .. head_dim / 32 - 1: the
+ *            key's scales, one per 64 values, then the value's.  A pattern is s's with z
+ *            in the low four bits.  Aligned to head_dim / 16 bytes; strides multiples of
+ *            head_dim / 32.
+ * kv_heads and query heads: at most 65536. */
+typedef struct {
+    void *k, *v;                                       /* (device) codes            */
+    int64_t page_stride, slot_stride, head_stride;     /* in bytes                  */
+    const int32_t *block_table, *cu_q, *kv_len;        /* (device)                  */
+    int num_pages, page_size, blocks;
+    int batch, tokens;
+    int kv_heads, head_dim;
+    int dtype;                                         /* of scales and rows        */
+    void *scales;                                      /* (device)                  */
+    int64_t scale_page_stride, scale_slot_stride, scale_head_stride;   /* in elements */
+} qmm_paged_kv4;
+
+/* Stores the new tokens' keys and values in the 4-bit cache.  Keys, and the queries beside
+ * them, are normed per head and rotated by their positions on the way:
+ *   y = x / sqrt(mean x^2 + eps) * w               (mean over the head; where there are weights)
+ * then the rotation of qmm_kv_append, in fp32, with one rounding to dtype at the end.  The
+ * rounded keys and the values are quantized, 64 at a time:
+ *   lo = min(0, min x), hi = max(0, max x), s = (hi - lo) / 15 rounded up to its bits,
+ *   z = rint(-lo / s), c = clamp(rint(x / s) + z, 0, 15)      (z = c = 0 where s = 0)
+ * so that a value is off by at most s / 2 (and a code whose value would pass the
+ * largest finite number is one nearer to z).  64 values that hold a NaN or an infinity read
+ * back as NaN.
+ *   q_norm, k_norm   (device) [head_dim] weights of the queries' and the keys' norms, dtype,
+ *            16-byte aligned; NULL: no norm.  eps >= 0 and finite.
+ * The other arguments, padding and errors are qmm_kv_append's. */
+QMM_API qmm_status qmm_kv4_append(const qmm_paged_kv4 *kv, const void *k, int64_t k_stride, const void *v,
+                                  int64_t v_stride, const void *q, int64_t q_stride, void *q_out, int q_heads,
+                                  const float *cos_sin, int rot, int rope_len, int interleaved, const void *q_norm,
+                                  const void *k_norm, float eps, cudaStream_t stream);
+
+/* Reads the cache back: the values that the codes of the batch's tokens (the last n_b keys
+ * of sequence b; all of them with n_b = kv_len[b]) stand for.
+ *   k_out, v_out   (device) dense [tokens][kv_heads][head_dim], dtype, 16-byte aligned.
+ * Rows of padding tokens are left as they were.  Errors as for qmm_kv4_append. */
+QMM_API qmm_status qmm_kv4_read(const qmm_paged_kv4 *kv, void *k_out, void *v_out, cudaStream_t stream);
+
+/* qmm_paged_attn over the 4-bit cache, with first tokens that stay visible: key j is visible
+ * to the token at position p where
+ *           0 <= j < kv_len[b];  j <= p when `causal`;
+ *           j > p - window or j < sinks when window > 0.
+ *   sinks    0, or the number of first tokens that a window leaves visible (sinks > 0
+ *            needs window > 0).
+ * Queries must be finite (a NaN or an infinity makes its row NaN), in bf16 below 2^116.
+ * Scores, maximum, sums and output are fp32.  Up to 16 query rows per key head (q_heads /
+ * kv_heads * new tokens) the codes are multiplied as they are and the weights rounded to
+ * fp16 once; for more the values, exact in dtype, are, and the weights are rounded to dtype.
+ * Everything else, the workspace (qmm_kv4_attn_workspace) among it, is qmm_paged_attn's. */
+QMM_API qmm_status qmm_kv4_attn(const qmm_paged_kv4 *kv, const void *q, int64_t q_stride, int q_heads, float scale,
+                                int causal, int window, int sinks, void *out, float *lse, int max_q, int max_kv,
+                                void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Bytes of scratch a qmm_kv4_attn call of these sizes needs on the current device (an
+ * upper bound over every batch), or 0 for sizes it does not take. */
+QMM_API size_t qmm_kv4_attn_workspace(int q_heads, int kv_heads, int head_dim, int max_q);
+
 /* Synchronizes `stream`, then returns and clears the first device-side error
  * recorded by any qmm kernel on the current device (QMM_OK if none).  A
  * pending asynchronous CUDA error is reported as QMM_ERR_CUDA. */
