@@ -111,10 +111,14 @@ def _load_fastcall(lib):
 # (csrc/pytorch_paged.cpp): their checks and allocations in C++.
 _fast_append = _fast_attn = None
 _append_addr = _attn_addr = _scratch_addr = 0   # function addresses for it, filled by load()
+_fast_kv4_append = _fast_kv4_read = _fast_kv4_attn = None
+_kv4_append_addr = _kv4_read_addr = _kv4_attn_addr = _kv4_scratch_addr = 0
 
 
 def _load_paged(lib):
     global _fast_append, _fast_attn, _append_addr, _attn_addr, _scratch_addr
+    global _fast_kv4_append, _fast_kv4_read, _fast_kv4_attn
+    global _kv4_append_addr, _kv4_read_addr, _kv4_attn_addr, _kv4_scratch_addr
     from .build import paged_path
     path = paged_path()
     if not os.path.exists(path):
@@ -129,6 +133,10 @@ def _load_paged(lib):
     _attn_addr = ctypes.cast(lib.qmm_paged_attn, ctypes.c_void_p).value
     _scratch_addr = ctypes.cast(lib.qmm_paged_attn_workspace, ctypes.c_void_p).value
     _fast_append, _fast_attn = mod.kv_append, mod.paged_attn
+    _kv4_append_addr, _kv4_read_addr, _kv4_attn_addr, _kv4_scratch_addr = (
+        ctypes.cast(f, ctypes.c_void_p).value
+        for f in (lib.qmm_kv4_append, lib.qmm_kv4_read, lib.qmm_kv4_attn, lib.qmm_kv4_attn_workspace))
+    _fast_kv4_append, _fast_kv4_read, _fast_kv4_attn = mod.kv4_append, mod.kv4_read, mod.kv4_attn
 
 
 class QmmError(RuntimeError):
@@ -646,6 +654,13 @@ def qmm_kv4_append(k, v, k_cache, v_cache, scales, block_table, cu_q, kv_len, q=
     qmm_kv4_append in qmm.h."""
     if _lib is None:
         load()
+    if _fast_kv4_append is not None:
+        r = _fast_kv4_append(_kv4_append_addr, k, v, k_cache, v_cache, scales, block_table, cu_q, kv_len, q, q_out,
+                             cos_sin, interleaved, q_norm, k_norm, eps)
+        if type(r) is not int:
+            return r
+        if r > 0:
+            raise QmmError(r, "qmm_kv4_append")
     hk = k_cache.shape[2] if k_cache.dim() == 4 else None
     rows = [("k", k, hk), ("v", v, hk)] + ([("q", q, None)] if q is not None else [])
     _kv4_checks(k_cache, v_cache, scales, block_table, cu_q, kv_len, rows)
@@ -688,6 +703,12 @@ def qmm_kv4_read(k_cache, v_cache, scales, block_table, cu_q, kv_len, tokens, k_
     tokens are left as they were.  See qmm_kv4_read in qmm.h."""
     if _lib is None:
         load()
+    if _fast_kv4_read is not None:
+        r = _fast_kv4_read(_kv4_read_addr, k_cache, v_cache, scales, block_table, cu_q, kv_len, tokens, k_out, v_out)
+        if type(r) is not int:
+            return r
+        if r > 0:
+            raise QmmError(r, "qmm_kv4_read")
     if k_cache.dim() != 4:
         raise ValueError("k_cache must have 4 dimensions")
     if tokens < 0:
@@ -726,6 +747,13 @@ def qmm_kv4_attn(q, k_cache, v_cache, scales, block_table, cu_q, kv_len, max_q, 
         load()
     if scale is None:
         scale = q.shape[-1] ** -0.5
+    if _fast_kv4_attn is not None:
+        r = _fast_kv4_attn(_kv4_attn_addr, _kv4_scratch_addr, q, k_cache, v_cache, scales, block_table, cu_q, kv_len, max_q,
+                           max_kv, scale, causal, window, sinks, return_lse, out, workspace)
+        if type(r) is not int:
+            return r
+        if r > 0:
+            raise QmmError(r, "qmm_kv4_attn")
     _kv4_checks(k_cache, v_cache, scales, block_table, cu_q, kv_len, [("q", q, None)])
     _int32(max_q=max_q, max_kv=max_kv, window=window, sinks=sinks)
     T, heads, D = q.shape

@@ -53,6 +53,8 @@ int kv4_decode_clusters(int head_dim, bool bf16, int rows, int cluster);
 // p.warps: 4 or 8; p.tile_rows: 8 or 16.
 cudaError_t launch_kv4_decode(const Kv4AttnParams &p, int grid, cudaStream_t stream);
 
+cudaError_t launch_kv4_chunk(const Kv4AttnParams &p, int grid, cudaStream_t stream);
+
 size_t kv4_attn_workspace_bytes(int q_heads, int kv_heads, int head_dim, int max_q, int num_sms);
 cudaError_t kv4_attn_dispatch(Kv4AttnParams &p, int max_q, long long max_kv, void *workspace, int num_sms,
                               cudaStream_t stream);

@@ -8,12 +8,12 @@ namespace qmm {
 
 namespace {
 
-// Blocks of four warps that a split goes over.
-int grid_of(int rows, int num_sms) { return kv4_blocks_per_sm(rows, 4) * num_sms; }
+// Blocks that a split goes over: of four warps of the kernel for few rows, or one per SM.
+int grid_of(bool few, int rows, int num_sms) { return few ? kv4_blocks_per_sm(rows, 4) * num_sms : num_sms; }
 
 // Work a block takes at least, in units: below this a split costs more (a second kernel,
 // the partial results) than the longer walk.
-constexpr int kMinUnits = 3;
+constexpr int kMinUnits = 3, kMinChunkUnits = 4;
 
 // Whole items in clusters against a split over all blocks: a cluster's block walks
 // units / c, a split one units * items / blocks and the joining kernel's time, some
@@ -21,26 +21,38 @@ constexpr int kMinUnits = 3;
 // lengths differ.
 constexpr int kJoinUnits = 4, kMostUnits = 10;
 
+// Work of the longest item (setup and units) up to which blocks of the kernel for many rows
+// take whole items, and the same where every item has a block of its own (as attn.cu).
+constexpr int kUnsplitWork = 12, kWholeWork = 10;
+
+// Rows (token, query head) per key head up to which the kernel for few rows takes the call.
+constexpr int kFewRows = 32;
+
 // Blocks of eight warps per item where every item gets a cluster (or block) of its own:
 // clusters of the largest size that all run at once; 0: the axis is split over all blocks.
-int cluster_of(const Kv4AttnParams &p, long long items, long long span, int num_sms)
+int cluster_of(const Kv4AttnParams &p, int rows, long long items, long long span, int num_sms)
 {
-    const int keys = kv4_keys(p.kv.head_dim, 8), blocks = kv4_blocks_per_sm(p.tile_rows, 8) * num_sms;
+    const int keys = kv4_keys(p.kv.head_dim, 8), blocks = kv4_blocks_per_sm(rows, 8) * num_sms;
     const long long units = (span + keys - 1) / keys;
     for (int c = kMaxCluster; c >= 1; c /= 2)
         if (items * c <= blocks && (c == 1 || c / 2 < units) && (units + c - 1) / c <= kMostUnits &&
             (units + c - 1) / c <= items * units / blocks + kJoinUnits &&
-            (c == 1 || items <= kv4_decode_clusters(p.kv.head_dim, p.kv.dtype == QMM_BF16, p.tile_rows, c)))
+            (c == 1 || items <= kv4_decode_clusters(p.kv.head_dim, p.kv.dtype == QMM_BF16, rows, c)))
             return c;
     return 0;
+}
+
+size_t scratch_bytes(bool few, int head_dim, int num_sms)
+{
+    const size_t g = grid_of(few, 8, num_sms), rows = few ? kDecodeRows : kChunkRows;
+    return g * 32 + 2 * g * rows * (head_dim + 2) * 4;
 }
 
 }  // namespace
 
 size_t kv4_attn_workspace_bytes(int, int, int head_dim, int, int num_sms)
 {
-    const size_t g = grid_of(8, num_sms);
-    return g * 32 + 2 * g * kDecodeRows * (head_dim + 2) * 4;
+    return std::max(scratch_bytes(true, head_dim, num_sms), scratch_bytes(false, head_dim, num_sms));
 }
 
 cudaError_t kv4_attn_dispatch(Kv4AttnParams &p, int max_q, long long max_kv, void *workspace, int num_sms,
@@ -55,37 +67,43 @@ cudaError_t kv4_attn_dispatch(Kv4AttnParams &p, int max_q, long long max_kv, voi
         p.window = 0;
     if (p.window == 0)
         p.sinks = 0;
-    p.tile_rows = q_rows <= 8 ? 8 : 16;
+    // (and queries that the other kernel's tensor copies do not take)
+    const bool few = q_rows <= kFewRows || !attn_set_q_tma(p);
+    p.tile_rows = few ? (q_rows <= 8 ? 8 : 16) : 2 * chunk_stream_rows(p.group);
     p.row_tiles = static_cast<int>((q_rows + p.tile_rows - 1) / p.tile_rows);
     p.by_group = fast_div(p.group);
     p.by_tiles = fast_div(p.row_tiles);
     p.by_page = fast_div(p.kv.page_size);
-    p.min_chunk = kMinUnits;
-    // keys of an item at most, and units more where its parts begin and end inside one
+    p.min_chunk = few ? kMinUnits : kMinChunkUnits;
+    // keys of an item at most: a window's, the first tokens, and those its tokens see beyond each other
     const long long seen = static_cast<long long>(p.window) + p.sinks + p.tile_rows / p.group + 1;
     const bool part = p.window > 0 && seen < max_kv;
     const long long span = part ? seen : max_kv;
     const long long items = static_cast<long long>(p.kv.batch) * p.row_tiles * p.kv.kv_heads;
-    const int cluster = cluster_of(p, items, span, num_sms);
-    p.whole = cluster > 0;
-    p.cluster = std::max(cluster, 1);
-    p.warps = p.whole ? 8 : 4;
-    const int keys = kv4_keys(p.kv.head_dim, p.warps);
+    const int cluster = few ? cluster_of(p, p.tile_rows, items, span, num_sms) : 0;
+    p.warps = cluster > 0 ? 8 : 4;
+    const int keys = few ? kv4_keys(p.kv.head_dim, p.warps) : kChunkKeys, setup = few ? kDecodeSetup : kChunkSetup;
+    // (its parts may begin and end inside a unit)
     const long long longest = (span + keys - 1) / keys + (part ? 2 : 0);
-    int grid = grid_of(p.tile_rows, num_sms);
-    if (p.whole)
+    int grid = grid_of(few, p.tile_rows, num_sms);
+    p.whole = few ? cluster > 0 : items <= grid ? longest + setup <= kWholeWork : longest + setup <= kUnsplitWork;
+    p.unsplit = !few && p.whole && items > grid;
+    p.cluster = std::max(cluster, 1);
+    if (p.whole && !p.unsplit)
         grid = static_cast<int>(items) * p.cluster;
-    else if (items * (longest + kDecodeSetup) < static_cast<long long>(grid) * p.min_chunk)
-        grid = static_cast<int>((items * (longest + kDecodeSetup) + p.min_chunk - 1) / p.min_chunk);
+    else if (p.unsplit)
+        p.min_chunk = 1;
+    else if (items * (longest + setup) < static_cast<long long>(grid) * p.min_chunk)
+        grid = static_cast<int>((items * (longest + setup) + p.min_chunk - 1) / p.min_chunk);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    const size_t g = grid_of(8, num_sms);
+    const size_t g = grid_of(few, 8, num_sms);
     p.meta = reinterpret_cast<int4 *>(ws);
     p.part_ml = reinterpret_cast<float *>(ws + g * 32);
-    p.part_o = p.part_ml + 2 * g * kDecodeRows * 2;
-    const cudaError_t e = launch_kv4_decode(p, grid, stream);
+    p.part_o = p.part_ml + 2 * g * (few ? kDecodeRows : kChunkRows) * 2;
+    const cudaError_t e = few ? launch_kv4_decode(p, grid, stream) : launch_kv4_chunk(p, grid, stream);
     if (e != cudaSuccess || p.whole)
         return e;
-    return launch_attn_join(p, grid, true, static_cast<int>(std::min(static_cast<long long>(p.tile_rows), q_rows)), stream);
+    return launch_attn_join(p, grid, few, static_cast<int>(std::min(static_cast<long long>(p.tile_rows), q_rows)), stream);
 }
 
 }  // namespace qmm
