@@ -41,6 +41,14 @@
 // before it into O is complete, so that needs no signal of its own (D = 64, where the
 // next S is computed under it: pv_done).
 //
+// The 4-bit cache (Q4) has the same tiles out of codes: two warps copy codes and scale
+// patterns as they lie in the cache into a ring, four turn them into values (exact in the
+// type) in the K and V rings.  Four warps that fetched codes by plain loads took 4500 cycles for
+// a pair of tiles, half of it for ten loads in a queue behind the softmax's instructions (512
+// tokens over 16384 keys 126 us, now 107; 97 without the conversions, as over the 16-bit
+// cache).  Not kept: eight converting warps (133; fewer registers for the softmax),
+// exponentials by a polynomial on the FMA pipe for every fourth weight (140).
+//
 // Bound by the tensor cores at D = 128 (a causal prompt of 8192 tokens x 64 heads: 1655
 // TFLOP/s, 88% of the measured bf16 burst rate, until the power limit brings it to 1500;
 // products and signals alone, the softmax left out, 1687 for 4096 x 4096 x 32), by the
@@ -61,37 +69,42 @@ constexpr int kSegs = 4;                            // segments found ahead
 constexpr float kChunkGrow = 8.f;
 constexpr int kHalf = kChunkKeys / 2;               // the weights are handed over by halves of a tile
 // The 16-bit cache's form and the 4-bit cache's (Q4).  Registers per thread after the split:
-// 256 x 200 + 128 x 104 = 384 x 168, what the launch gives; Q4 256 x (176 + 80) or (at D = 64,
-// where the softmax keeps its scores) 256 x (192 + 64) = 512 x 128.
+// 256 x 200 + 128 x 104 = 384 x 168, what the launch gives; Q4 256 x 192 + 256 x 64 = 512 x 128.
 template <int D, bool Q4>
 struct ChunkForm {
     using Params = AttnParams;
     static constexpr int kThreads = 384, kSoftRegs = 200, kOtherRegs = 104;
-    static constexpr int kLoaders = 1;                  // warps that fill a K or V tile
+    static constexpr int kFillers = 1;                  // arrivals that make a K or V tile full
     static constexpr int kReaders = 2 * kSoftWarps + 3; // warps that go through the segments
+    static constexpr int kKRing = D == 64 ? 5 : 3, kVRing = D == 64 ? 5 : 2, kRaw = 0;   // tiles of each ring
     static_assert(256 * kSoftRegs + 128 * kOtherRegs == kThreads * 168, "register split");
 };
 template <int D>
 struct ChunkForm<D, true> {
     using Params = Kv4AttnParams;
-    static constexpr int kThreads = 512, kSoftRegs = D == 64 ? 192 : 176, kOtherRegs = 256 - kSoftRegs;
-    static constexpr int kLoaders = 4;
-    static constexpr int kReaders = 2 * kSoftWarps + 5;
+    static constexpr int kThreads = 512, kSoftRegs = 192, kOtherRegs = 64;
+    static constexpr int kFillers = 4;
+    static constexpr int kReaders = 2 * kSoftWarps + 7;
+    static constexpr int kKRing = D == 64 ? 5 : 2, kVRing = D == 64 ? 5 : 2, kRaw = D == 64 ? 6 : 3;
     static_assert(256 * kSoftRegs + 256 * kOtherRegs == kThreads * 128, "register split");
 };
-constexpr int kDequantWarp = 12;                        // Q4: the first of the four
+constexpr int kRawWarp = 10, kDequantWarp = 12;         // Q4: the first of the two and of the four
 
-template <int D>
+template <int D, bool Q4>
 struct ChunkLayout {
+    using Form = ChunkForm<D, Q4>;
     static constexpr int kTile = 128 * D * 2;       // 128 rows of D values: D / 64 halves of [128][64]
     static constexpr int kOffQ = 0;                 // two streams
-    static constexpr int kKRing = D == 64 ? 5 : 3, kVRing = D == 64 ? 5 : 2;   // tiles of each ring
+    static constexpr int kKRing = Form::kKRing, kVRing = Form::kVRing;
     static constexpr int kOffK = 2 * kTile;
     static constexpr int kOffV = kOffK + kKRing * kTile;
-    static constexpr int kOffBar = kOffV + kVRing * kTile;
+    // Q4: codes of a K or V tile as they lie in the cache, and a word of patterns per key
+    static constexpr int kRawCodes = 128 * D / 2, kRawStage = kRawCodes + 128 * 4;
+    static constexpr int kOffRaw = kOffV + kVRing * kTile;
+    static constexpr int kOffBar = kOffRaw + Form::kRaw * kRawStage;
     // full / empty of both rings, patch, per stream q_full, q_empty, s_full, p_full (two halves) and
-    // pv_done, o_full, x_full, x_done, drain, full / empty of the segments
-    static constexpr int kNumBars = 2 * (kKRing + kVRing) + 18 + 2 * kSegs;
+    // pv_done, o_full, x_full, x_done, drain, full / empty of the segments and of the raw ring
+    static constexpr int kNumBars = 2 * (kKRing + kVRing) + 18 + 2 * kSegs + 2 * Form::kRaw;
     static constexpr int kOffTmem = kOffBar + 8 * kNumBars;
     static constexpr int kOffShare = kOffTmem + 16;
     static constexpr int kOffRed = kOffShare + sizeof(Share);
@@ -124,6 +137,13 @@ template <int D>
 __device__ __forceinline__ uint32_t kv_addr(int r, int c)
 {
     return static_cast<uint32_t>((r >> 3) * (D * 16) + (c >> 3) * 1024 + (r & 7) * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+// Byte of 16-byte piece c of key r in a tile of codes (Q4).
+template <int D>
+__device__ __forceinline__ uint32_t raw_addr(int r, int c)
+{
+    return static_cast<uint32_t>(r * (D / 2) + ((D == 128 ? c ^ (r >> 1 & 3) : c ^ (r >> 2 & 1)) << 4));
 }
 
 // Operand descriptor with the 128-byte swizzle.  `stride`: bytes between groups of 8
@@ -317,7 +337,7 @@ template <int D, bool BF16, bool Q4>
 __global__ void __launch_bounds__(ChunkForm<D, Q4>::kThreads, 1)
 attn_chunk_kernel(const __grid_constant__ typename ChunkForm<D, Q4>::Params p)
 {
-    using L = ChunkLayout<D>;
+    using L = ChunkLayout<D, Q4>;
     using Form = ChunkForm<D, Q4>;
     constexpr int kChunks = D / 8;                     // 16-byte chunks per row
     constexpr int kRowsPerCopy = 32 / kChunks;
@@ -332,6 +352,7 @@ attn_chunk_kernel(const __grid_constant__ typename ChunkForm<D, Q4>::Params p)
     uint64_t *q_full = patch + 1, *q_empty = q_full + 2, *s_full = q_empty + 2, *p_full = s_full + 2, *o_full = p_full + 4;
     uint64_t *x_full = o_full + 2, *x_done = x_full + 1, *drain = x_done + 1;
     uint64_t *pv_done = drain + 1, *seg_full = pv_done + 2, *seg_empty = seg_full + kSegs;
+    [[maybe_unused]] uint64_t *raw_full = seg_empty + kSegs, *raw_empty = raw_full + Form::kRaw;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kOffTmem);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -342,11 +363,11 @@ attn_chunk_kernel(const __grid_constant__ typename ChunkForm<D, Q4>::Params p)
     }
     if (threadIdx.x == 0) {
         for (int i = 0; i < L::kKRing; ++i) {
-            mbar_init(&k_full[i], Form::kLoaders);
+            mbar_init(&k_full[i], Form::kFillers);
             mbar_init(&k_empty[i], 1);
         }
         for (int i = 0; i < L::kVRing; ++i) {
-            mbar_init(&v_full[i], Form::kLoaders);
+            mbar_init(&v_full[i], Form::kFillers);
             mbar_init(&v_empty[i], 1);
         }
         mbar_init(patch, 1);
@@ -365,6 +386,10 @@ attn_chunk_kernel(const __grid_constant__ typename ChunkForm<D, Q4>::Params p)
         for (int i = 0; i < kSegs; ++i) {
             mbar_init(&seg_full[i], 1);
             mbar_init(&seg_empty[i], Form::kReaders);   // softmax, issue and loading warps
+        }
+        for (int i = 0; i < Form::kRaw; ++i) {
+            mbar_init(&raw_full[i], 64);                    // the threads that copy
+            mbar_init(&raw_empty[i], 4);
         }
         fence_barrier_init();
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -846,15 +871,15 @@ attn_chunk_kernel(const __grid_constant__ typename ChunkForm<D, Q4>::Params p)
             }
             __syncwarp();
         } else if constexpr (Q4) {
-            // ================= K and V tiles out of codes (warps 12 - 15) =================
-            // Thread r brings key r of every tile: its codes by 16-byte loads half a tile's
-            // time ahead (its page two tiles ahead), its values by 16-byte stores, which eight
-            // threads side by side make without a bank twice.  Keys that nobody sees get a
-            // scale of zero.
-            if (warp >= kDequantWarp) {
-                constexpr int kGroups = D / kKv4Group, kVecs = D / 32;
-                const int row = threadIdx.x - 32 * kDequantWarp;
-                unsigned tile = 0;             // tiles of each ring so far
+            if (warp < kDequantWarp) {
+                // ================= codes (warps 10 and 11) =================
+                // Lane l of a warp copies keys l and l + 32 of its half of every tile as they lie in
+                // the cache, K and V in turn, and their words of patterns (zeros for keys that
+                // nobody sees).  Pages are looked up a tile ahead.  16-byte pieces are permuted by
+                // the key, so that eight threads that read a piece of a key each meet no bank twice.
+                constexpr int kVecs = D / 32;
+                const int row0 = 64 * (warp - kRawWarp) + lane;
+                unsigned stage = 0;            // stages so far
                 for (int n = 0; ok; ++n) {
                     const Segment &sg = segment(n);
                     const RowTile r = sg.r;
@@ -862,104 +887,109 @@ attn_chunk_kernel(const __grid_constant__ typename ChunkForm<D, Q4>::Params p)
                     if (!ok || units == 0)
                         break;
                     leave(n);
-                    const uint8_t *kbase = static_cast<const uint8_t *>(p.kv.k) + h * p.kv.head_stride;
-                    const uint8_t *vbase = static_cast<const uint8_t *>(p.kv.v) + h * p.kv.head_stride;
                     const uint16_t *sbase = p.sc.base + h * p.sc.head;
-                    // the key of tile j, -1 where nobody sees it, and its page
-                    auto key_of = [&](int j) {
+                    // key i of the lane in tile j, -1 where nobody sees it, and its page
+                    auto key_of = [&](int j, int i) {
                         if (j >= units)
                             return -1;
-                        const int key = unit_key<kChunkKeys>(p, r, off + j) + row;
+                        const int key = unit_key<kChunkKeys>(p, r, off + j) + row0 + 32 * i;
                         return key < r.hi && (key >= r.lo || key < p.sinks) ? key : -1;
                     };
                     auto look_up = [&](int key) {
                         return key >= 0 ? p.kv.block_table[static_cast<long long>(r.b) * p.kv.blocks + p.by_page(key)] : 0;
                     };
-                    struct Codes {
-                        uint4 w[kVecs];
-                    };
-                    auto load = [&](const uint8_t *base, long long at) {
-                        Codes c;
+                    int page[2] = {look_up(key_of(0, 0)), look_up(key_of(0, 1))};
+                    for (int j = 0; j < units && ok; ++j) {
+                        long long at[2], sat[2];
 #pragma unroll
-                        for (int i = 0; i < kVecs; ++i)
-                            c.w[i] = at >= 0 ? reinterpret_cast<const uint4 *>(base + at)[i] : make_uint4(0u, 0u, 0u, 0u);
-                        return c;
-                    };
-                    uint32_t pats[kGroups];    // the key's patterns: K's, then V's
-                    auto place = [&](int key, int page) -> long long {
-#pragma unroll
-                        for (int i = 0; i < kGroups; ++i)
-                            pats[i] = 0;
-                        if (key < 0)
-                            return -1;
-                        if (page < 0 || page >= p.kv.num_pages) {
-                            record_error(p.status, QMM_ERR_INDEX);
-                            return -1;
+                        for (int i = 0; i < 2; ++i) {
+                            const int key = key_of(j, i);
+                            at[i] = -1;
+                            sat[i] = 0;
+                            if (key >= 0) {
+                                if (page[i] < 0 || page[i] >= p.kv.num_pages) {
+                                    record_error(p.status, QMM_ERR_INDEX);
+                                } else {
+                                    const int slot = key - p.by_page(key) * p.kv.page_size;
+                                    at[i] = page[i] * p.kv.page_stride + slot * p.kv.slot_stride + h * p.kv.head_stride;
+                                    sat[i] = scale_offset(p.sc, page[i], slot);
+                                }
+                            }
+                            page[i] = look_up(key_of(j + 1, i));
                         }
-                        const int slot = key - p.by_page(key) * p.kv.page_size;
-                        const uint16_t *s = sbase + scale_offset(p.sc, page, slot);
-                        if constexpr (kGroups == 2) {
-                            const uint2 u = *reinterpret_cast<const uint2 *>(s);
-                            pats[0] = u.x;
-                            pats[1] = u.y;
-                        } else {
-                            pats[0] = *reinterpret_cast<const uint32_t *>(s);
-                        }
-                        return page * p.kv.page_stride + slot * p.kv.slot_stride;
-                    };
-                    auto store = [&](uint8_t *dst, const Codes &c, const uint32_t *pat) {
-#pragma unroll
-                        for (int gr = 0; gr < kGroups; ++gr) {
-                            const GroupScale<BF16> sc(pat[gr]);
+#pragma unroll 1
+                        for (int kk = 0; kk < 2; ++kk, ++stage) {
+                            const unsigned slot = stage % Form::kRaw;
+                            if (stage >= Form::kRaw &&
+                                !(ok = __all_sync(0xffffffffu, mbar_wait(&raw_empty[slot], (stage / Form::kRaw - 1) & 1u, p.status))))
+                                break;
+                            const uint8_t *base = static_cast<const uint8_t *>(kk ? p.kv.v : p.kv.k);
+                            const uint32_t dst = smem_u32(smem + L::kOffRaw) + slot * L::kRawStage;
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
-                                const uint4 w = c.w[2 * gr + i];
-                                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+                                const int row = row0 + 32 * i;
+                                const bool in = at[i] >= 0;
+                                const uint8_t *src = in ? base + at[i] : base;
+#pragma unroll
+                                for (int v = 0; v < kVecs; ++v)
+                                    cp_async16_or_zero(dst + raw_addr<D>(row, v), src + 16 * v, in);
+                                cp_async_small<4>(dst + L::kRawCodes + 4 * row,
+                                                  sbase + sat[i] + (D == 128 && kk ? 2 : 0), in);
+                            }
+                            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&raw_full[slot])) : "memory");
+                        }
+                    }
+                }
+                cp_async_wait_all();   // no copy may still be landing when the block exits
+            } else {
+                // ================= K and V tiles out of codes (warps 12 - 15) =================
+                // Thread r turns key r of every tile into values; 16-byte stores that eight threads
+                // side by side make meet no bank twice.
+                constexpr int kGroups = D / kKv4Group, kVecs = D / 32;
+                const int row = threadIdx.x - 32 * kDequantWarp;
+                unsigned tile = 0;             // tiles of each ring so far
+                for (int n = 0; ok; ++n) {
+                    const int units = segment(n).units;
+                    if (!ok || units == 0)
+                        break;
+                    leave(n);
+                    for (int i = 0; i < 2 * units; ++i) {
+                        const bool v = i & 1;
+                        const unsigned stage = 2 * tile + (v ? 1u : 0u), rs = stage % Form::kRaw;
+                        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&raw_full[rs], stage / Form::kRaw & 1u, p.status))))
+                            break;
+                        const uint8_t *raw = smem + L::kOffRaw + rs * L::kRawStage;
+                        uint4 w[kVecs];
+#pragma unroll
+                        for (int c = 0; c < kVecs; ++c)
+                            w[c] = *reinterpret_cast<const uint4 *>(raw + raw_addr<D>(row, c));
+                        const uint32_t pats = *reinterpret_cast<const uint32_t *>(raw + L::kRawCodes + 4 * row);
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(&raw_empty[rs]);
+                        const unsigned ring = v ? L::kVRing : L::kKRing;
+                        const unsigned slot = v ? tile % L::kVRing : tile % L::kKRing, use = v ? tile / L::kVRing : tile / L::kKRing;
+                        if (tile >= ring &&
+                            !(ok = __all_sync(0xffffffffu, mbar_wait(v ? &v_empty[slot] : &k_empty[slot], (use - 1) & 1u, p.status))))
+                            break;
+                        uint8_t *dst = smem + (v ? L::kOffV : L::kOffK) + slot * L::kTile;
+#pragma unroll
+                        for (int gr = 0; gr < kGroups; ++gr) {
+                            const GroupScale<BF16> sc((kGroups == 2 ? gr == 1 : v) ? pats >> 16 : pats & 0xffffu);
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                const uint4 x = w[2 * gr + c];
+                                const uint32_t u[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                                 for (int e = 0; e < 4; ++e)
-                                    *reinterpret_cast<uint4 *>(dst + kv_addr<D>(row, 8 * gr + 4 * i + e)) = sc.values(u[e]);
+                                    *reinterpret_cast<uint4 *>(dst + kv_addr<D>(row, 8 * gr + 4 * c + e)) = sc.values(u[e]);
                             }
                         }
-                    };
-                    auto announce = [&](uint64_t *bar) {
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0)
-                            mbar_arrive(bar);
-                    };
-                    int key = key_of(0);
-                    long long at = place(key, look_up(key));
-                    Codes kc = load(kbase, at);
-                    key = key_of(1);
-                    int page = look_up(key);
-                    for (int j = 0; j < units; ++j, ++tile) {
-                        const Codes vc = load(vbase, at);
-                        uint32_t kp[kGroups], vp[kGroups];
-                        if constexpr (kGroups == 2) {
-                            kp[0] = pats[0] & 0xffffu;
-                            kp[1] = pats[0] >> 16;
-                            vp[0] = pats[1] & 0xffffu;
-                            vp[1] = pats[1] >> 16;
-                        } else {
-                            kp[0] = pats[0] & 0xffffu;
-                            vp[0] = pats[0] >> 16;
-                        }
-                        const unsigned ks = tile % L::kKRing, vs = tile % L::kVRing;
-                        if (tile >= L::kKRing &&
-                            !(ok = __all_sync(0xffffffffu, mbar_wait(&k_empty[ks], (tile / L::kKRing - 1) & 1u, p.status))))
-                            break;
-                        store(smem + L::kOffK + ks * L::kTile, kc, kp);
-                        announce(&k_full[ks]);
-                        // the next tile's keys, on their way under this one's values
-                        at = place(key, page);
-                        kc = load(kbase, at);
-                        key = key_of(j + 2);
-                        page = look_up(key);
-                        if (tile >= L::kVRing &&
-                            !(ok = __all_sync(0xffffffffu, mbar_wait(&v_empty[vs], (tile / L::kVRing - 1) & 1u, p.status))))
-                            break;
-                        store(smem + L::kOffV + vs * L::kTile, vc, vp);
-                        announce(&v_full[vs]);
+                            mbar_arrive(v ? &v_full[slot] : &k_full[slot]);
+                        tile += v ? 1 : 0;
                     }
                 }
             }
@@ -1096,7 +1126,7 @@ attn_chunk_kernel(const __grid_constant__ typename ChunkForm<D, Q4>::Params p)
 template <int D, bool BF16, bool Q4>
 cudaError_t launch_chunk(const typename ChunkForm<D, Q4>::Params &p, int grid, cudaStream_t stream)
 {
-    constexpr int smem = ChunkLayout<D>::kBytes;
+    constexpr int smem = ChunkLayout<D, Q4>::kBytes;
     static SmemLimit limit;
     if (const cudaError_t e = ensure_smem_limit(limit, attn_chunk_kernel<D, BF16, Q4>, smem, true); e != cudaSuccess)
         return e;

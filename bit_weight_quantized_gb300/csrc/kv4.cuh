@@ -67,6 +67,16 @@ struct GroupScale {
     }
 };
 
+// 8 or 4 bytes global -> shared (zeros where !ok)
+template <int BYTES>
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void *src, bool ok)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(ok ? BYTES : 0)
+                 : "memory");
+}
+
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // Element offset of the scales of (page, slot, head 0).
 __device__ __forceinline__ long long scale_offset(const Kv4Scales &sc, int page, int slot)
 {

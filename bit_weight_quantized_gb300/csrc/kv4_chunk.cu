@@ -1,5 +1,5 @@
-// kv4_chunk.cu -- the kernel for many query rows over the 4-bit paged cache: four warps more,
-// which turn codes into the tiles that tensor copies bring from a 16-bit cache.
+// kv4_chunk.cu -- the kernel for many query rows over the 4-bit paged cache: six warps copy codes
+// and turn them into the tiles that tensor copies bring from a 16-bit cache.
 #include "attn_chunk.cuh"
 
 namespace qmm {

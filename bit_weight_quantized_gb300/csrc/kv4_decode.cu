@@ -58,14 +58,6 @@ struct Layout {
     static_assert(kOffMl + WARPS * kRows * 8 <= kOffIn, "the warps' outputs reuse the rings");
 };
 
-// 8 or 4 bytes global -> shared (zeros where !ok)
-template <int BYTES>
-__device__ __forceinline__ void cp_async_small(uint32_t dst, const void *src, bool ok)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(ok ? BYTES : 0)
-                 : "memory");
-}
-
 __device__ __forceinline__ uint32_t lds32(uint32_t addr)
 {
     uint32_t v;
