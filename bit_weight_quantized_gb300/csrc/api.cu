@@ -299,6 +299,12 @@ static qmm_status check_kv4(const qmm_paged_kv4 *kv, qmm_paged_kv *codes, Kv4Sca
         return st;
     if (kv->kv_heads > 65536)
         return QMM_ERR_UNSUPPORTED;
+    // (the kernels multiply page and slot numbers by 32-bit strides)
+    const int64_t most = 0x7fffffff, slots = kv->page_size - 1, heads = kv->kv_heads - 1;
+    if ((kv->num_pages > 1 && (kv->page_stride > most || sc->page > most)) ||
+        (slots > 0 && (kv->slot_stride > most / slots || sc->slot > most / slots)) ||
+        (heads > 0 && (kv->head_stride > most || sc->head > most)))
+        return QMM_ERR_UNSUPPORTED;
     if ((kv->num_pages > 1 && sc->page < 0) || (kv->page_size > 1 && sc->slot < 0) || (kv->kv_heads > 1 && sc->head < 0))
         return QMM_ERR_SHAPE;
     const int step = kv->head_dim / 32;   // a key's scale patterns

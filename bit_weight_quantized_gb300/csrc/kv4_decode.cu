@@ -30,6 +30,7 @@
 // own ring of asynchronous copies, maximum, sum and output, as in attn_decode.cu, whose
 // split, clusters and end this has.
 #include <atomic>
+#include <cuda_fp16.h>
 
 #include "attn_rows.cuh"
 #include "kv4.cuh"
@@ -58,18 +59,13 @@ struct Layout {
     static_assert(kOffMl + WARPS * kRows * 8 <= kOffIn, "the warps' outputs reuse the rings");
 };
 
-__device__ __forceinline__ uint32_t lds32(uint32_t addr)
-{
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-    return v;
-}
+// (plain loads: the compiler moves them between the waits, which are barriers to it)
+__device__ __forceinline__ uint32_t lds32(const uint8_t *p) { return *reinterpret_cast<const uint32_t *>(p); }
+__device__ __forceinline__ uint2 lds64(const uint8_t *p) { return *reinterpret_cast<const uint2 *>(p); }
 
-__device__ __forceinline__ uint2 lds64(uint32_t addr)
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src)
 {
-    uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
-    return v;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
 // An 8 x 8 matrix of 16-bit values, row g of it in lane group g: turned over.
@@ -92,6 +88,20 @@ __device__ __forceinline__ uint32_t code_addr(int r, int c)
     return static_cast<uint32_t>(r * (D / 2) + ((D == 128 ? c ^ (r & 2) : c) << 4));
 }
 
+// Both halves of a word as numbers: 16-bit floats of the type, or fp16.
+template <bool BF16>
+__device__ __forceinline__ void halves(uint32_t w, float &lo, float &hi)
+{
+    if constexpr (BF16) {
+        lo = __uint_as_float(w << 16);
+        hi = __uint_as_float(w & 0xffff0000u);
+    } else {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+        lo = f.x;
+        hi = f.y;
+    }
+}
+
 template <int D, bool BF16, int WARPS, int NB>
 __global__ void __launch_bounds__(32 * WARPS, kv4_blocks_per_sm(8 * NB, WARPS))
 kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p)
@@ -102,10 +112,10 @@ kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p)
     constexpr int kChunks = D / 32;                    // 16-byte chunks of a key's codes
     constexpr int kRowsPerCopy = 32 / kChunks, kCopies = kWarpKeys / kRowsPerCopy;
     constexpr int kLook = kWarpKeys / 32;              // keys whose place a lane looks up, per tile
-    // weights are 2^(s - m + kShift); with their V scale, over the power of two, at most 2^15
-    constexpr float kShift = BF16 ? 0.f : 7.f;
-    constexpr float kLift = BF16 ? 128.f : 1.f;
-    constexpr uint32_t kM0 = 0x000f000fu, kM1 = 0x00f000f0u;
+    // weights are 2^(s - m + 7), at most 2^15: times a V scale over a power of two above it, rounded to fp16
+    constexpr float kShift = 7.f;
+    constexpr uint32_t kM0 = 0x000f000fu, kM1 = 0x00f000f0u, kScaleBits = 0xfff0fff0u;
+    constexpr int kExpBits = BF16 ? 7 : 10, kBias = BF16 ? 127 : 15, kMostExp = BF16 ? 253 : 30;   // of a scale pattern
 
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Share share;
@@ -120,8 +130,22 @@ kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     find_share<kKeys, kDecodeSetup, kThreads, true>(p, red, &share);
 
-    const uint32_t ring = smem_u32(smem) + warp * L::kWarpBytes;
+    uint8_t *const ring = smem + warp * L::kWarpBytes, *const ring_end = ring + L::kWarpBytes;
     const int crow = lane / kChunks, cchunk = lane % kChunks;
+    // the lane's places in a stage: K words of key g (of 16) and their scales, V words of keys
+    // 2 t and 2 t + 1 and their zeros, the scales of key `lane`
+    uint32_t at_k[kGroups], at_v[2][kGroups], at_z[2];
+#pragma unroll
+    for (int gr = 0; gr < kGroups; ++gr)
+        at_k[gr] = code_addr<D>(key_row(g), 2 * gr + (t >> 1)) + 8 * (t & 1);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int gr = 0; gr < kGroups; ++gr)
+            at_v[e][gr] = L::kCodes + code_addr<D>(key_row(2 * t + e), 2 * gr + (g >> 2)) + 4 * (g & 3);
+        at_z[e] = 2 * L::kCodes + key_row(2 * t + e) * L::kScaleRow + (kGroups == 2 ? 4 : 0);
+    }
+    const uint32_t at_s = 2 * L::kCodes + key_row(g) * L::kScaleRow;
 
     if (!p.whole && tid == 0)
         p.meta[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
@@ -142,12 +166,17 @@ kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p)
         cluster_wait();
     for (; more; more = !p.whole && walk.next(p, sg)) {
         const RowTile &r = sg.r;
-        const uint8_t *kbase = static_cast<const uint8_t *>(p.kv.k) + sg.h * p.kv.head_stride;
-        const uint8_t *vbase = static_cast<const uint8_t *>(p.kv.v) + sg.h * p.kv.head_stride;
+        const int page_stride = static_cast<int>(p.kv.page_stride), slot_stride = static_cast<int>(p.kv.slot_stride);
+        const int s_page = static_cast<int>(p.sc.page), s_slot = static_cast<int>(p.sc.slot);
+        const uint8_t *kbase = static_cast<const uint8_t *>(p.kv.k) + sg.h * p.kv.head_stride + cchunk * 16;
+        const uint8_t *vbase = static_cast<const uint8_t *>(p.kv.v) + sg.h * p.kv.head_stride + cchunk * 16;
         const uint16_t *sbase = p.sc.base + sg.h * p.sc.head;
-        // the warp's first key of tile j
-        auto tile_key = [&](int j) { return unit_key<kKeys>(p, r, sg.off + j) + warp * kWarpKeys; };
-        auto reads = [&](int j, int key) { return j < sg.units && key < r.hi && (key >= r.lo || key < p.sinks); };
+        const int32_t *pages = p.kv.block_table + static_cast<long long>(r.b) * p.kv.blocks;
+        // the warp's first key of tile j (unit_key, with what does not change taken out)
+        const int first_tiles = sink_units<kKeys>(p, r) - sg.off, key0 = sg.off * kKeys + warp * kWarpKeys;
+        const int past = r.unit0 * kKeys;
+        auto tile_key = [&](int j) { return key0 + j * kKeys + (j < first_tiles ? 0 : past); };
+        auto reads = [&](int key) { return key < r.hi && (key >= r.lo || key < p.sinks); };
         // The pages of the lane's keys of a tile (lane, lane + 32) are looked up one tile ahead
         // and not looked at before the tile is loaded: the warp would wait for the table here.
         struct Look {
@@ -155,38 +184,45 @@ kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p)
         };
         auto look_up = [&](int j) {
             Look k;
-            const int kb = j < sg.units ? tile_key(j) : 0;
+            const int kb = tile_key(j) + lane;
 #pragma unroll
             for (int i = 0; i < kLook; ++i)
-                k.page[i] = reads(j, kb + lane + 32 * i) ?
-                    p.kv.block_table[static_cast<long long>(r.b) * p.kv.blocks + p.by_page(kb + lane + 32 * i)] : 0;
+                k.page[i] = j < sg.units && reads(kb + 32 * i) ? pages[p.by_page(kb + 32 * i)] : 0;
             return k;
         };
-        auto load = [&](int j, const Look &look) {
-            const uint32_t dst = ring + (j % L::kStages) * L::kStage;
-            const int kb = tile_key(j);
+        auto load = [&](int j, const Look &look, uint8_t *stage) {
+            const uint32_t dst = smem_u32(stage);
+            const int kb = tile_key(j) + lane;
             long long off[kLook];
+            bool all = true;
 #pragma unroll
             for (int i = 0; i < kLook; ++i) {
-                const int key = kb + lane + 32 * i, slot = key - p.by_page(key) * p.kv.page_size, page = look.page[i];
-                bool ok = reads(j, key);
-                if (ok && (page < 0 || page >= p.kv.num_pages)) {
+                const int key = kb + 32 * i, slot = key - p.by_page(key) * p.kv.page_size, page = look.page[i];
+                bool ok = reads(key);
+                if (ok && static_cast<unsigned>(page) >= static_cast<unsigned>(p.kv.num_pages)) {
                     record_error(p.status, QMM_ERR_INDEX);
                     ok = false;
                 }
-                off[i] = ok ? page * p.kv.page_stride + slot * p.kv.slot_stride : -1;
+                off[i] = ok ? static_cast<long long>(page) * page_stride + slot * slot_stride : -1;
+                all = all && ok;
                 // (a key that nobody sees gets scales of zero; its codes do not matter)
                 cp_async_small<L::kScaleRow>(dst + 2 * L::kCodes + (lane + 32 * i) * L::kScaleRow,
-                                             ok ? sbase + scale_offset(p.sc, page, slot) : p.sc.base, ok);
+                                             sbase + (ok ? static_cast<long long>(page) * s_page + slot * s_slot : 0), ok);
             }
+            all = __all_sync(0xffffffffu, all);
 #pragma unroll
             for (int c = 0; c < kCopies; ++c) {
                 const int row = c * kRowsPerCopy + crow;
                 const long long o = __shfl_sync(0xffffffffu, off[c * kRowsPerCopy / 32], row & 31);
-                const bool ok = o >= 0;
-                const long long e = ok ? o + cchunk * 16 : 0;
-                cp_async16_or_zero(dst + code_addr<D>(row, cchunk), kbase + e, ok);
-                cp_async16_or_zero(dst + L::kCodes + code_addr<D>(row, cchunk), vbase + e, ok);
+                const uint32_t to = dst + code_addr<D>(row, cchunk);
+                if (all) {
+                    cp_async16(to, kbase + o);
+                    cp_async16(to + L::kCodes, vbase + o);
+                } else {
+                    const bool ok = o >= 0;
+                    cp_async16_or_zero(to, kbase + (ok ? o : 0), ok);
+                    cp_async16_or_zero(to + L::kCodes, vbase + (ok ? o : 0), ok);
+                }
             }
         };
 
@@ -245,21 +281,24 @@ kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p)
                 }
                 sum[gr] += __shfl_xor_sync(0xffffffffu, sum[gr], 1);
                 sum[gr] += __shfl_xor_sync(0xffffffffu, sum[gr], 2);
-                sum[gr] *= 5.9604644775390625e-8f;   // 2^-24, as the codes are
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
-                    qs[nb][gr][e] = __shfl_sync(0xffffffffu, sum[gr], 8 * t + 4 * e);
+                    qs[nb][gr][e] = -__shfl_sync(0xffffffffu, sum[gr], 8 * t + 4 * e);
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-                rowf[nb][e] = __shfl_sync(0xffffffffu, up, 8 * t + 4 * e) * p.scale_log2;
+                // (not zero, which times a hidden score, -infinity, is NaN)
+                rowf[nb][e] = fmaxf(__shfl_sync(0xffffffffu, up, 8 * t + 4 * e) * p.scale_log2, 1.17549435e-38f);
         }
 
+        uint8_t *wr = ring, *rd = ring;              // the stages written and read next
+        auto next_stage = [&](uint8_t *a) { return a + L::kStage == ring_end ? ring : a + L::kStage; };
 #pragma unroll
         for (int j = 0; j < L::kStages - 1; ++j) {
             if (j < sg.units)
-                load(j, first[j]);
+                load(j, first[j], wr);
             cp_async_commit();
+            wr = next_stage(wr);
         }
 
         // keys that the lane's rows see, and that every row of the tile sees (rows past the
@@ -284,43 +323,39 @@ kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p)
                     for (int i = 0; i < 4; ++i)
                         o[nb][gr][i][e] = 0.f;
                 }
-        float m[NB][2], l[NB][2];
+        float m[NB][2], l[NB][2];                    // maximum (a power of two), sum
+        float limit[NB][2], minus[NB][2];            // the score past which it is replaced, kShift - maximum
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
-            m[nb][0] = m[nb][1] = -INFINITY, l[nb][0] = l[nb][1] = 0.f;
-        float vmost = 0.f, vdown = kLift;            // V scales are below vmost; what brings that to one
+            m[nb][0] = m[nb][1] = limit[nb][0] = limit[nb][1] = -INFINITY, l[nb][0] = l[nb][1] = 0.f, minus[nb][0] = minus[nb][1] = kShift;
+        uint32_t vlimit = 0;                         // V's patterns so far are below this power of two's
+        float vdown = 1.f;                           // its inverse
 
 #pragma unroll 1
         for (int j = 0; j < sg.units; ++j) {
             if (j + L::kStages - 1 < sg.units)
-                load(j + L::kStages - 1, ahead);
+                load(j + L::kStages - 1, ahead, wr);
             cp_async_commit();
+            wr = next_stage(wr);
             ahead = look_up(j + L::kStages);
             cp_async_wait_group<L::kStages - 1>();
             __syncwarp();
             const int kb = tile_key(j);
             if (kb < r.hi && (kb + kWarpKeys > r.lo || kb < p.sinks)) {
-                const uint32_t ks = ring + (j % L::kStages) * L::kStage, vs = ks + L::kCodes, ss = vs + L::kCodes;
-                const bool masked = (kb < all_lo && kb + kWarpKeys > p.sinks) || kb + kWarpKeys - 1 > all_hi;
+                // scores: rows are keys, columns query rows
+                float s[kSteps][NB][4];
 #pragma unroll
                 for (int st = 0; st < kSteps; ++st) {
-                    // scores: rows are keys, columns query rows
-                    const int k0 = 16 * st + key_row(g), k1 = k0 + 8;
-                    float s[NB][4];
-                    uint32_t sc0[kGroups], sc1[kGroups];     // the keys' scale words: K's groups, V's groups
-                    if constexpr (kGroups == 2) {
-                        const uint2 a = lds64(ss + k0 * L::kScaleRow), b = lds64(ss + k1 * L::kScaleRow);
-                        sc0[0] = a.x; sc0[1] = a.y; sc1[0] = b.x; sc1[1] = b.y;
-                    } else {
-                        sc0[0] = lds32(ss + k0 * L::kScaleRow);
-                        sc1[0] = lds32(ss + k1 * L::kScaleRow);
-                    }
-                    // pattern i of a key's scales: K's 0 .. kGroups - 1, then V's
-                    auto pattern = [](const uint32_t (&w)[kGroups], int i) { return i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xffffu; };
+                    // the scale words of keys g and g + 8: K's (D = 64: K's and V's)
+                    const uint32_t u0 = lds32(rd + at_s + 16 * st * L::kScaleRow), u1 = lds32(rd + at_s + (16 * st + 8) * L::kScaleRow);
+                    float s0[2], s1[2], z0[2], z1[2];    // scales; zeros, as the codes are, times 2^-24
+                    halves<BF16>(u0 & kScaleBits, s0[0], s0[1]);
+                    halves<BF16>(u1 & kScaleBits, s1[0], s1[1]);
+                    halves<false>(u0 & kM0, z0[0], z0[1]);
+                    halves<false>(u1 & kM0, z1[0], z1[1]);
 #pragma unroll
                     for (int gr = 0; gr < kGroups; ++gr) {
-                        const uint2 a = lds64(ks + code_addr<D>(k0, 2 * gr + (t >> 1)) + 8 * (t & 1));
-                        const uint2 b = lds64(ks + code_addr<D>(k1, 2 * gr + (t >> 1)) + 8 * (t & 1));
+                        const uint2 a = lds64(rd + at_k[gr] + 16 * st * L::kRow), b = lds64(rd + at_k[gr] + (16 * st + 8) * L::kRow);
                         const uint32_t aw[2] = {a.x, a.y}, bw[2] = {b.x, b.y};
                         float acc[NB][4];
 #pragma unroll
@@ -339,109 +374,115 @@ kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p)
                                               qf[nb][gr][2 * w + 1][1]);
                             }
                         }
-                        const uint32_t u0 = pattern(sc0, gr), u1 = pattern(sc1, gr);
-                        const float s0 = scale_of<BF16>(u0), s1 = scale_of<BF16>(u1);
-                        const float z0 = __uint_as_float(0x4b000000u | (u0 & 15u)) - 8388608.f;
-                        const float z1 = __uint_as_float(0x4b000000u | (u1 & 15u)) - 8388608.f;
 #pragma unroll
                         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                const float x = fmaf(-(e < 2 ? z0 : z1), qs[nb][gr][e & 1], acc[nb][e]) * (e < 2 ? s0 : s1);
-                                s[nb][e] = gr == 0 ? x : s[nb][e] + x;
+                                const float x = fmaf(e < 2 ? z0[gr] : z1[gr], qs[nb][gr][e & 1], acc[nb][e]);
+                                s[st][nb][e] = gr == 0 ? x * (e < 2 ? s0[gr] : s1[gr]) : fmaf(x, e < 2 ? s0[gr] : s1[gr], s[st][nb][e]);
                             }
                     }
-                    float vsc[kGroups][2];
-                    bool up = false;
+                }
+                if ((kb < all_lo && kb + kWarpKeys > p.sinks) || kb + kWarpKeys - 1 > all_hi) {
 #pragma unroll
-                    for (int gr = 0; gr < kGroups; ++gr) {
-                        vsc[gr][0] = scale_of<BF16>(pattern(sc0, kGroups + gr));
-                        vsc[gr][1] = scale_of<BF16>(pattern(sc1, kGroups + gr));
-                        up |= vsc[gr][0] > vmost || vsc[gr][1] > vmost;
-                    }
+                    for (int st = 0; st < kSteps; ++st)
 #pragma unroll
-                    for (int nb = 0; nb < NB; ++nb) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            s[nb][e] *= rowf[nb][e & 1];
-                        if (masked) {
+                        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                const int key = kb + (e < 2 ? k0 : k1);
+                                const int key = kb + 16 * st + key_row(g) + (e < 2 ? 0 : 8);
                                 if ((key < see[nb][e & 1].x && key >= p.sinks) || key > see[nb][e & 1].y)
-                                    s[nb][e] = -INFINITY;
+                                    s[st][nb][e] = -INFINITY;
                             }
-                        }
-                        up |= fmaxf(s[nb][0], s[nb][2]) > m[nb][0] + kGrow || fmaxf(s[nb][1], s[nb][3]) > m[nb][1] + kGrow;
+                }
+                // a new maximum of some row, or a larger V scale?
+                float most[NB][2];
+                bool up = false;
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        most[nb][e] = fmaxf(s[0][nb][e], s[0][nb][2 + e]);
+#pragma unroll
+                        for (int st = 1; st < kSteps; ++st)
+                            most[nb][e] = fmaxf(most[nb][e], fmaxf(s[st][nb][e], s[st][nb][2 + e]));
+                        up |= most[nb][e] > limit[nb][e];
                     }
-                    if (__any_sync(0xffffffffu, up)) {
-                        // a new maximum of some row, or a larger V scale
-                        float big = 0.f;
+                uint32_t big = 0;
 #pragma unroll
-                        for (int gr = 0; gr < kGroups; ++gr)
-                            big = fmaxf(big, fmaxf(vsc[gr][0], vsc[gr][1]));
-#pragma unroll
-                        for (int d = 4; d < 32; d <<= 1)
-                            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
-                        float vf = 1.f;
-                        if (big > vmost) {
-                            const uint32_t ex = min(max(__float_as_uint(big) >> 23, 1u), 245u);
-                            const float down = __uint_as_float((253u - ex) << 23) * kLift;
-                            vf = down / vdown;               // (powers of two; nothing is there before the first)
-                            if (vmost == 0.f)
-                                vf = 0.f;
-                            vdown = down;
-                            vmost = __uint_as_float((ex + 1u) << 23);
-                        }
-#pragma unroll
-                        for (int nb = 0; nb < NB; ++nb) {
-                            float f[2];
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                float x = fmaxf(s[nb][e], s[nb][2 + e]);
-#pragma unroll
-                                for (int d = 4; d < 32; d <<= 1)
-                                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-                                const bool grow = x > m[nb][e] + kGrow;
-                                const float a = grow ? ex2(m[nb][e] - x) : 1.f;
-                                m[nb][e] = grow ? x : m[nb][e];
-                                l[nb][e] *= a;
-                                f[e] = a * vf;
-                            }
-#pragma unroll
-                            for (int gr = 0; gr < kGroups; ++gr)
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    oz[nb][gr][e] *= f[e & 1];
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i)
-                                        o[nb][gr][i][e] *= f[e & 1];
-                                }
-                        }
+                for (int i = 0; i < kLook; ++i) {
+                    const uint32_t u = lds32(rd + 2 * L::kCodes + (lane + 32 * i) * L::kScaleRow + (kGroups == 2 ? 4 : 0));
+                    big = max(big, u >> 16);
+                    if (kGroups == 2)
+                        big = max(big, u & 0xffffu);
+                }
+                if (__any_sync(0xffffffffu, up || big >= vlimit)) {
+                    constexpr uint32_t kInf = BF16 ? 0x7f80u : 0x7c00u;      // (patterns of groups that hold NaN lie above)
+                    big = __reduce_max_sync(0xffffffffu, big >= kInf ? 0u : big);
+                    float vf = 1.f;
+                    if (big >= vlimit) {
+                        const int ex = min(static_cast<int>(big >> kExpBits) + 1, kMostExp);
+                        const float down = __uint_as_float(static_cast<uint32_t>(127 + kBias - ex) << 23);
+                        vf = vlimit == 0 ? 0.f : down / vdown;   // (powers of two; nothing is there before the first)
+                        vdown = down;
+                        vlimit = static_cast<uint32_t>(ex) << kExpBits;
                     }
-                    // weights, times their keys' V scales, as the right operand
-                    uint32_t pf[NB][kGroups][2];
 #pragma unroll
                     for (int nb = 0; nb < NB; ++nb) {
-                        const float n0 = kShift - (m[nb][0] == -INFINITY ? 0.f : m[nb][0]);
-                        const float n1 = kShift - (m[nb][1] == -INFINITY ? 0.f : m[nb][1]);
-                        const float w0 = ex2(s[nb][0] + n0), w1 = ex2(s[nb][1] + n1);
-                        const float w2 = ex2(s[nb][2] + n0), w3 = ex2(s[nb][3] + n1);
+                        float f[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float x = most[nb][e];
+#pragma unroll
+                            for (int d = 4; d < 32; d <<= 1)
+                                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+                            const bool grow = x > limit[nb][e];
+                            x *= rowf[nb][e];
+                            const float a = grow ? ex2(m[nb][e] - x) : 1.f;
+                            if (grow) {
+                                m[nb][e] = x;
+                                limit[nb][e] = (x + kGrow) / rowf[nb][e];
+                                minus[nb][e] = kShift - x;
+                            }
+                            l[nb][e] *= a;
+                            f[e] = a * vf;
+                        }
+#pragma unroll
+                        for (int gr = 0; gr < kGroups; ++gr)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                oz[nb][gr][e] *= f[e & 1];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    o[nb][gr][i][e] *= f[e & 1];
+                            }
+                    }
+                }
+#pragma unroll
+                for (int st = 0; st < kSteps; ++st) {
+                    // weights, times their keys' V scales, as the right operand
+                    uint32_t pf[NB][kGroups][2];
+                    float v0[2], v1[2];
+                    halves<BF16>(lds32(rd + at_s + 16 * st * L::kScaleRow + (kGroups == 2 ? 4 : 0)) & kScaleBits, v0[0], v0[1]);
+                    halves<BF16>(lds32(rd + at_s + (16 * st + 8) * L::kScaleRow + (kGroups == 2 ? 4 : 0)) & kScaleBits, v1[0], v1[1]);
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) {
+                        const float w0 = ex2(fmaf(s[st][nb][0], rowf[nb][0], minus[nb][0])), w1 = ex2(fmaf(s[st][nb][1], rowf[nb][1], minus[nb][1]));
+                        const float w2 = ex2(fmaf(s[st][nb][2], rowf[nb][0], minus[nb][0])), w3 = ex2(fmaf(s[st][nb][3], rowf[nb][1], minus[nb][1]));
                         l[nb][0] += w0 + w2;
                         l[nb][1] += w1 + w3;
 #pragma unroll
                         for (int gr = 0; gr < kGroups; ++gr) {
-                            const float a = vsc[gr][0] * vdown, b = vsc[gr][1] * vdown;
+                            const float a = v0[kGroups == 2 ? gr : 1] * vdown, b = v1[kGroups == 2 ? gr : 1] * vdown;
                             pf[nb][gr][0] = transpose8(pack16<false>(w0 * a, w1 * a));
                             pf[nb][gr][1] = transpose8(pack16<false>(w2 * b, w3 * b));
                         }
                     }
                     // output: rows are d, columns query rows
-                    const int r0 = 16 * st + key_row(2 * t), r1 = 16 * st + key_row(2 * t + 1);
                     uint32_t zw[4];                          // the V scale words of the keys 2 t, 2 t + 1, + 8
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        zw[i] = lds32(ss + ((i & 1 ? r1 : r0) + 8 * (i >> 1)) * L::kScaleRow + (kGroups == 2 ? 4 : 0));
+                        zw[i] = lds32(rd + at_z[i & 1] + (16 * st + 8 * (i >> 1)) * L::kScaleRow);
 #pragma unroll
                     for (int gr = 0; gr < kGroups; ++gr) {
                         const uint32_t sel = kGroups == 2 && gr == 0 ? 0x5410u : 0x7632u;
@@ -449,7 +490,7 @@ kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p)
                         uint32_t v[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            v[i] = lds32(vs + code_addr<D>((i & 1 ? r1 : r0) + 8 * (i >> 1), 2 * gr + (g >> 2)) + 4 * (g & 3));
+                            v[i] = lds32(rd + at_v[i & 1][gr] + (16 * st + 8 * (i >> 1)) * L::kRow);
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {   // codes 0 .. 3, 4 .. 7 of the word
                             const uint32_t hs = half ? 0x7632u : 0x5410u;
@@ -469,21 +510,26 @@ kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p)
                 }
             }
             __syncwarp();   // every lane has read the slot before it is filled again
+            rd = next_stage(rd);
         }
         cp_async_wait_group<0>();
+        // (a row's sum and output count 2^(s - m) in bf16, 2^7 times that in fp16: row_log_sum)
+        constexpr float kUnshift = BF16 ? 0.0078125f : 1.f;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
+            for (int e = 0; e < 2; ++e) {
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1)
                     l[nb][e] += __shfl_xor_sync(0xffffffffu, l[nb][e], d);
+                l[nb][e] *= kUnshift;
+            }
 
         // the warps' maxima, sums and outputs meet in shared memory (over the rings)
         __syncthreads();
         float *wo = reinterpret_cast<float *>(smem);
         float *wml = reinterpret_cast<float *>(smem + L::kOffMl);
-        const float unit = 16777216.f / vdown;       // 2^24 for the codes
+        const float unit = 16777216.f * kUnshift / vdown;       // 2^24 for the codes
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll

@@ -38,6 +38,10 @@ KV_CASES = [
     (dict(kv_heads=1, head_stride=-3, scale_head_stride=1), DEVICE),
     (dict(page_stride=1032), ALIGN), (dict(slot_stride=8), ALIGN), (dict(head_stride=24), ALIGN),
     (dict(scale_page_stride=2), ALIGN), (dict(scale_slot_stride=6), ALIGN), (dict(scale_head_stride=1), ALIGN),
+    (dict(page_stride=1 << 31), UNSUPPORTED), (dict(scale_page_stride=1 << 40), UNSUPPORTED),
+    (dict(page_stride=(1 << 31) - 16), DEVICE), (dict(slot_stride=1 << 27, page_size=17), UNSUPPORTED),
+    (dict(slot_stride=1 << 27, page_size=16), DEVICE), (dict(scale_slot_stride=1 << 28), UNSUPPORTED),
+    (dict(head_stride=1 << 31), UNSUPPORTED), (dict(scale_head_stride=1 << 31), UNSUPPORTED),
     (dict(k=None), NULL), (dict(v=None), NULL), (dict(scales=None), NULL), (dict(block_table=None), NULL),
     (dict(cu_q=None), NULL), (dict(kv_len=None), NULL), (dict(k=A + 8), ALIGN), (dict(v=A + 2), ALIGN),
     (dict(scales=A + 4), ALIGN), (dict(scales=A + 8), DEVICE), (dict(head_dim=64, scales=A + 4), DEVICE),
