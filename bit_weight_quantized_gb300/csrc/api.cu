@@ -945,6 +945,8 @@ qmm_status qmm_kv4_attn(const qmm_paged_kv4 *kv, const void *q, int64_t q_stride
         return QMM_ERR_NULL;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 16) || !aligned(lse, 4))
         return QMM_ERR_ALIGN;
+    if (!kv4_set_units(p))
+        return QMM_ERR_UNSUPPORTED;
     // row tiles of the batch are counted in 32 bits (no sequence has more than `tokens`)
     const int group = q_heads / kv->kv_heads;
     if ((static_cast<long long>(std::min(max_q, kv->tokens)) * group / 8 + 1) * kv->batch > 0x7fffffffLL ||

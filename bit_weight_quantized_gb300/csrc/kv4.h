@@ -34,6 +34,9 @@ struct Kv4ReadParams {
 
 struct Kv4AttnParams : AttnParams {
     Kv4Scales sc;
+    // places of codes in 32 bits (kernel for few rows): the strides in units of `unit` bytes, the
+    // largest power of two that divides them
+    uint32_t unit, page_units, slot_units;
 };
 
 cudaError_t launch_kv4_append(const Kv4AppendParams &p, cudaStream_t stream);
@@ -55,6 +58,8 @@ cudaError_t launch_kv4_decode(const Kv4AttnParams &p, int grid, cudaStream_t str
 
 cudaError_t launch_kv4_chunk(const Kv4AttnParams &p, int grid, cudaStream_t stream);
 
+// Sets the units; false where places do not fit.
+bool kv4_set_units(Kv4AttnParams &p);
 size_t kv4_attn_workspace_bytes(int q_heads, int kv_heads, int head_dim, int max_q, int num_sms);
 cudaError_t kv4_attn_dispatch(Kv4AttnParams &p, int max_q, long long max_kv, void *workspace, int num_sms,
                               cudaStream_t stream);

@@ -50,6 +50,19 @@ size_t scratch_bytes(bool few, int head_dim, int num_sms)
 
 }  // namespace
 
+bool kv4_set_units(Kv4AttnParams &p)
+{
+    const unsigned long long page = p.kv.num_pages > 1 ? p.kv.page_stride : 0, slot = p.kv.page_size > 1 ? p.kv.slot_stride : 0;
+    unsigned long long unit = 16;
+    while (unit < 1u << 20 && (page | slot) % (2 * unit) == 0)
+        unit *= 2;
+    p.unit = static_cast<uint32_t>(unit);
+    p.page_units = static_cast<uint32_t>(page / unit);
+    p.slot_units = static_cast<uint32_t>(slot / unit);
+    // (the last place is kept for "none")
+    return (std::max(0, p.kv.num_pages - 1) * page + (p.kv.page_size - 1) * slot) / unit < 0xffffffffull;
+}
+
 size_t kv4_attn_workspace_bytes(int, int, int head_dim, int, int num_sms)
 {
     return std::max(scratch_bytes(true, head_dim, num_sms), scratch_bytes(false, head_dim, num_sms));

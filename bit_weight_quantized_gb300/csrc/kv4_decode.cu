@@ -51,12 +51,15 @@ struct Layout {
     static constexpr int kStage = 2 * kCodes + kWarpKeys * kScaleRow;
     static constexpr int kStages = 3;
     static constexpr int kWarpBytes = kStages * kStage;
-    static constexpr int kOffIn = WARPS * kWarpBytes;                     // clusters: what the other blocks send
+    // queries in operand order; per row minus its groups' sums and the factor of its scores
+    static constexpr int kOffQ = WARPS * kWarpBytes;
+    static constexpr int kOffRow = kOffQ + kRows * D * 2;
+    static constexpr int kOffIn = kOffRow + kRows * 16;                   // clusters: what the other blocks send
     static constexpr int kOffInMl = kOffIn + kRows * D * 4;
     static constexpr int kBytes = kOffIn, kClusterBytes = kOffInMl + kRows * kMaxCluster * 8;
     static constexpr int kPitch = D + 8;
     static constexpr int kOffMl = WARPS * kRows * kPitch * 4;
-    static_assert(kOffMl + WARPS * kRows * 8 <= kOffIn, "the warps' outputs reuse the rings");
+    static_assert(kOffMl + WARPS * kRows * 8 <= kOffQ, "the warps' outputs reuse the rings");
 };
 
 // (plain loads: the compiler moves them between the waits, which are barriers to it)
@@ -114,7 +117,7 @@ kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p)
     constexpr int kLook = kWarpKeys / 32;              // keys whose place a lane looks up, per tile
     // weights are 2^(s - m + 7), at most 2^15: times a V scale over a power of two above it, rounded to fp16
     constexpr float kShift = 7.f;
-    constexpr uint32_t kM0 = 0x000f000fu, kM1 = 0x00f000f0u, kScaleBits = 0xfff0fff0u;
+    constexpr uint32_t kM0 = 0x000f000fu, kM1 = 0x00f000f0u, kMB = 0x00ff00ffu, kScaleBits = 0xfff0fff0u;
     constexpr int kExpBits = BF16 ? 7 : 10, kBias = BF16 ? 127 : 15, kMostExp = BF16 ? 253 : 30;   // of a scale pattern
 
     extern __shared__ __align__(128) uint8_t smem[];
@@ -166,7 +169,6 @@ kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p)
         cluster_wait();
     for (; more; more = !p.whole && walk.next(p, sg)) {
         const RowTile &r = sg.r;
-        const int page_stride = static_cast<int>(p.kv.page_stride), slot_stride = static_cast<int>(p.kv.slot_stride);
         const int s_page = static_cast<int>(p.sc.page), s_slot = static_cast<int>(p.sc.slot);
         const uint8_t *kbase = static_cast<const uint8_t *>(p.kv.k) + sg.h * p.kv.head_stride + cchunk * 16;
         const uint8_t *vbase = static_cast<const uint8_t *>(p.kv.v) + sg.h * p.kv.head_stride + cchunk * 16;
@@ -177,51 +179,56 @@ kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p)
         const int past = r.unit0 * kKeys;
         auto tile_key = [&](int j) { return key0 + j * kKeys + (j < first_tiles ? 0 : past); };
         auto reads = [&](int key) { return key < r.hi && (key >= r.lo || key < p.sinks); };
-        // The pages of the lane's keys of a tile (lane, lane + 32) are looked up one tile ahead
-        // and not looked at before the tile is loaded: the warp would wait for the table here.
+        // The places of the lane's keys of a tile (lane, lane + 32; slot -1: nobody sees it) are
+        // looked up one tile ahead and not looked at before the tile is loaded: the warp would wait
+        // for the table here.
         struct Look {
-            int page[kLook];
+            int page[kLook], slot[kLook];
         };
         auto look_up = [&](int j) {
             Look k;
             const int kb = tile_key(j) + lane;
 #pragma unroll
-            for (int i = 0; i < kLook; ++i)
-                k.page[i] = j < sg.units && reads(kb + 32 * i) ? pages[p.by_page(kb + 32 * i)] : 0;
+            for (int i = 0; i < kLook; ++i) {
+                const int key = kb + 32 * i, blk = p.by_page(key);
+                const bool in = j < sg.units && reads(key);
+                k.slot[i] = in ? key - blk * p.kv.page_size : -1;
+                k.page[i] = in ? pages[blk] : 0;
+            }
             return k;
         };
-        auto load = [&](int j, const Look &look, uint8_t *stage) {
+        auto load = [&](const Look &look, uint8_t *stage) {
             const uint32_t dst = smem_u32(stage);
-            const int kb = tile_key(j) + lane;
-            long long off[kLook];
-            bool all = true;
+            uint32_t off[kLook];                     // of the key's codes, in p.unit bytes
+            bool all = true, good[kLook];
 #pragma unroll
             for (int i = 0; i < kLook; ++i) {
-                const int key = kb + 32 * i, slot = key - p.by_page(key) * p.kv.page_size, page = look.page[i];
-                bool ok = reads(key);
-                if (ok && static_cast<unsigned>(page) >= static_cast<unsigned>(p.kv.num_pages)) {
+                const int page = look.page[i], slot = look.slot[i];
+                good[i] = slot >= 0;
+                if (good[i] && static_cast<unsigned>(page) >= static_cast<unsigned>(p.kv.num_pages)) {
                     record_error(p.status, QMM_ERR_INDEX);
-                    ok = false;
+                    good[i] = false;
                 }
-                off[i] = ok ? static_cast<long long>(page) * page_stride + slot * slot_stride : -1;
-                all = all && ok;
+                off[i] = good[i] ? page * p.page_units + slot * p.slot_units : ~0u;
+                all = all && good[i];
                 // (a key that nobody sees gets scales of zero; its codes do not matter)
-                cp_async_small<L::kScaleRow>(dst + 2 * L::kCodes + (lane + 32 * i) * L::kScaleRow,
-                                             sbase + (ok ? static_cast<long long>(page) * s_page + slot * s_slot : 0), ok);
+                const uint16_t *src = sbase + static_cast<long long>(good[i] ? page : 0) * s_page + (good[i] ? slot * s_slot : 0);
+                cp_async_small<L::kScaleRow>(dst + 2 * L::kCodes + (lane + 32 * i) * L::kScaleRow, src, good[i]);
             }
             all = __all_sync(0xffffffffu, all);
 #pragma unroll
             for (int c = 0; c < kCopies; ++c) {
                 const int row = c * kRowsPerCopy + crow;
-                const long long o = __shfl_sync(0xffffffffu, off[c * kRowsPerCopy / 32], row & 31);
+                const uint32_t o = __shfl_sync(0xffffffffu, off[c * kRowsPerCopy / 32], row & 31);
                 const uint32_t to = dst + code_addr<D>(row, cchunk);
                 if (all) {
-                    cp_async16(to, kbase + o);
-                    cp_async16(to + L::kCodes, vbase + o);
+                    cp_async16(to, kbase + static_cast<uint64_t>(o) * p.unit);
+                    cp_async16(to + L::kCodes, vbase + static_cast<uint64_t>(o) * p.unit);
                 } else {
-                    const bool ok = o >= 0;
-                    cp_async16_or_zero(to, kbase + (ok ? o : 0), ok);
-                    cp_async16_or_zero(to + L::kCodes, vbase + (ok ? o : 0), ok);
+                    const bool ok = o != ~0u;
+                    const uint64_t e = ok ? static_cast<uint64_t>(o) * p.unit : 0;
+                    cp_async16_or_zero(to, kbase + e, ok);
+                    cp_async16_or_zero(to + L::kCodes, vbase + e, ok);
                 }
             }
         };
@@ -232,73 +239,92 @@ kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p)
             first[j] = look_up(j);
         Look ahead = look_up(L::kStages - 1);
 
-        // queries in operand order: row g, values 16 t .. 16 t + 15 of every group
-        uint32_t qf[NB][kGroups][4][2];
-        float qs[NB][kGroups][2], rowf[NB][2];       // of rows 2 t, 2 t + 1: sums over the groups, factor of the scores
+        // Queries in operand order, eight values a thread: 16 bytes of a row, gone through by half a
+        // warp (D = 64: a quarter).  By all warps, since code that runs once per segment has to be
+        // fetched, at several cycles an instruction: every warp's own fragments, straight from
+        // memory, took some 500 instructions.
+        constexpr int kWords = D / 8, kItems = kRows * kWords;
+        uint4 raw[(kItems + kThreads - 1) / kThreads];
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            const int row = 8 * nb + g, rr = r.row0 + row, tok = p.by_group(rr);
-            uint32_t x[kGroups][8];
-            const uint16_t *src = p.q + (r.t0 + tok) * p.q_stride + static_cast<long long>(sg.h * p.group + rr - tok * p.group) * D;
+        for (int i = 0; i * kThreads < kItems; ++i) {
+            const int e = i * kThreads + tid, row = e / kWords, rr = r.row0 + row, tok = p.by_group(rr);
+            raw[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (e < kItems && row < r.rows)
+                raw[i] = *reinterpret_cast<const uint4 *>(p.q + (r.t0 + tok) * p.q_stride +
+                                                          static_cast<long long>(sg.h * p.group + rr - tok * p.group) * D + 8 * (e % kWords));
+        }
+        uint8_t *wr = ring, *rd = ring;              // the stages written and read next
+        auto next_stage = [&](uint8_t *a) { return a + L::kStage == ring_end ? ring : a + L::kStage; };
+#pragma unroll 1
+        for (int j = 0; j < L::kStages - 1; ++j) {
+            if (j < sg.units)
+                load(first[0], wr);
+            cp_async_commit();
+            wr = next_stage(wr);
 #pragma unroll
-            for (int gr = 0; gr < kGroups; ++gr)
+            for (int i = 0; i + 1 < L::kStages - 1; ++i)
+                first[i] = first[i + 1];
+        }
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if (row < r.rows)
-                        v = *reinterpret_cast<const uint4 *>(src + gr * kKv4Group + 16 * t + 8 * i);
-                    x[gr][4 * i] = v.x; x[gr][4 * i + 1] = v.y; x[gr][4 * i + 2] = v.z; x[gr][4 * i + 3] = v.w;
-                }
-            float most = 0.f;
+        for (int i = 0; i * kThreads < kItems; ++i) {
+            const int e = i * kThreads + tid;
+            if (e >= kItems)                         // (whole warps)
+                break;
+            const uint32_t x[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+            float v[8], most = 0.f, sum = 0.f;
 #pragma unroll
-            for (int gr = 0; gr < kGroups; ++gr)
+            for (int k = 0; k < 4; ++k) {
+                v[2 * k] = lo16<BF16>(x[k]);
+                v[2 * k + 1] = hi16<BF16>(x[k]);
+                most = fmaxf(most, fmaxf(fabsf(v[2 * k]), fabsf(v[2 * k + 1])));
+            }
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    most = fmaxf(most, fmaxf(fabsf(lo16<BF16>(x[gr][i])), fabsf(hi16<BF16>(x[gr][i]))));
-            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
-            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+            for (int d = 1; d < kWords; d <<= 1)
+                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
             // a power of two that brings the largest to 2^14 .. 2^15 (exponents kept where both
             // it and its inverse with the codes' 2^24 are normal numbers)
             const uint32_t ex = min(max(__float_as_uint(most) >> 23, 15u), 243u);
-            const float down = __uint_as_float((268u - ex) << 23), up = __uint_as_float((ex + 10u) << 23);
-            float sum[kGroups];
+            const float down = __uint_as_float((268u - ex) << 23);
 #pragma unroll
-            for (int gr = 0; gr < kGroups; ++gr) {
-                sum[gr] = 0.f;
-#pragma unroll
-                for (int w = 0; w < 2; ++w) {        // d = 8 w .. 8 w + 7 of the sixteen
-                    float v[8];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        v[2 * i] = lo16<BF16>(x[gr][4 * w + i]) * down;
-                        v[2 * i + 1] = hi16<BF16>(x[gr][4 * w + i]) * down;
-                        sum[gr] += v[2 * i] + v[2 * i + 1];
-                    }
-                    qf[nb][gr][2 * w][0] = pack16<false>(v[0], v[4]);
-                    qf[nb][gr][2 * w][1] = pack16<false>(v[2], v[6]);
-                    qf[nb][gr][2 * w + 1][0] = pack16<false>(v[1] * 0.0625f, v[5] * 0.0625f);
-                    qf[nb][gr][2 * w + 1][1] = pack16<false>(v[3] * 0.0625f, v[7] * 0.0625f);
-                }
-                sum[gr] += __shfl_xor_sync(0xffffffffu, sum[gr], 1);
-                sum[gr] += __shfl_xor_sync(0xffffffffu, sum[gr], 2);
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    qs[nb][gr][e] = -__shfl_sync(0xffffffffu, sum[gr], 8 * t + 4 * e);
+            for (int k = 0; k < 8; ++k) {
+                v[k] *= down;
+                sum += v[k];
             }
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-                // (not zero, which times a hidden score, -infinity, is NaN)
-                rowf[nb][e] = fmaxf(__shfl_sync(0xffffffffu, up, 8 * t + 4 * e) * p.scale_log2, 1.17549435e-38f);
+            for (int d = 1; d < 8; d <<= 1)
+                sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            *reinterpret_cast<uint4 *>(smem + L::kOffQ + 16 * e) =
+                make_uint4(pack16<false>(v[0], v[4]), pack16<false>(v[2], v[6]), pack16<false>(v[1] * 0.0625f, v[5] * 0.0625f),
+                           pack16<false>(v[3] * 0.0625f, v[7] * 0.0625f));
+            float *rows = reinterpret_cast<float *>(smem + L::kOffRow) + 4 * (e / kWords);
+            if (e % 8 == 0)                          // minus the group's sum, the scores' factor
+                rows[e % kWords / 8] = -sum;
+            if (e % kWords == 0)                     // (not zero, which times a hidden score, -infinity, is NaN)
+                rows[2] = fmaxf(__uint_as_float((ex + 10u) << 23) * p.scale_log2, 1.17549435e-38f);
         }
-
-        uint8_t *wr = ring, *rd = ring;              // the stages written and read next
-        auto next_stage = [&](uint8_t *a) { return a + L::kStage == ring_end ? ring : a + L::kStage; };
+        __syncthreads();
+        uint32_t qf[NB][kGroups][4][2];
+        float qs[NB][kGroups][2], rowf[NB][2];       // of rows 2 t, 2 t + 1
 #pragma unroll
-        for (int j = 0; j < L::kStages - 1; ++j) {
-            if (j < sg.units)
-                load(j, first[j], wr);
-            cp_async_commit();
-            wr = next_stage(wr);
+        for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+            for (int gr = 0; gr < kGroups; ++gr)
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    const uint4 u = *reinterpret_cast<const uint4 *>(smem + L::kOffQ + 16 * ((8 * nb + g) * kWords + 8 * gr + 2 * t + w));
+                    qf[nb][gr][2 * w][0] = u.x;
+                    qf[nb][gr][2 * w][1] = u.y;
+                    qf[nb][gr][2 * w + 1][0] = u.z;
+                    qf[nb][gr][2 * w + 1][1] = u.w;
+                }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float4 u = reinterpret_cast<const float4 *>(smem + L::kOffRow)[8 * nb + 2 * t + e];
+                qs[nb][0][e] = u.x;
+                if (kGroups == 2)
+                    qs[nb][kGroups - 1][e] = u.y;
+                rowf[nb][e] = u.z;
+            }
         }
 
         // keys that the lane's rows see, and that every row of the tile sees (rows past the
@@ -334,7 +360,7 @@ kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p)
 #pragma unroll 1
         for (int j = 0; j < sg.units; ++j) {
             if (j + L::kStages - 1 < sg.units)
-                load(j + L::kStages - 1, ahead, wr);
+                load(ahead, wr);
             cp_async_commit();
             wr = next_stage(wr);
             ahead = look_up(j + L::kStages);
@@ -495,12 +521,11 @@ kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p)
                         for (int half = 0; half < 2; ++half) {   // codes 0 .. 3, 4 .. 7 of the word
                             const uint32_t hs = half ? 0x7632u : 0x5410u;
                             const uint32_t a = __byte_perm(v[0], v[1], hs), b = __byte_perm(v[2], v[3], hs);
-                            const uint32_t a8 = a >> 8, b8 = b >> 8;
+                            const uint32_t a8 = __byte_perm(a, 0u, 0x4341u), b8 = __byte_perm(b, 0u, 0x4341u);
 #pragma unroll
                             for (int nb = 0; nb < NB; ++nb) {
-                                mma_f16_16816(o[nb][gr][2 * half], a & kM0, a & kM1, b & kM0, b & kM1, pf[nb][gr][0], pf[nb][gr][1]);
-                                mma_f16_16816(o[nb][gr][2 * half + 1], a8 & kM0, a8 & kM1, b8 & kM0, b8 & kM1, pf[nb][gr][0],
-                                              pf[nb][gr][1]);
+                                mma_f16_16816(o[nb][gr][2 * half], a & kM0, a & kMB, b & kM0, b & kMB, pf[nb][gr][0], pf[nb][gr][1]);
+                                mma_f16_16816(o[nb][gr][2 * half + 1], a8 & kM0, a8, b8 & kM0, b8, pf[nb][gr][0], pf[nb][gr][1]);
                             }
                         }
 #pragma unroll
@@ -540,9 +565,9 @@ kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p)
                     float *w = wo + row * L::kPitch + gr * kKv4Group + 8 * g;
                     float v[8];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {    // values 2 i (c 2^-24) and 2 i + 1 (c 2^-20)
+                    for (int i = 0; i < 4; ++i) {    // values 2 i (of c), 2 i + 1 (of 16 c and the c before it)
                         v[2 * i] = (o[nb][gr][i][e] - oz[nb][gr][e]) * unit;
-                        v[2 * i + 1] = fmaf(o[nb][gr][i][2 + e], 0.0625f, -oz[nb][gr][e]) * unit;
+                        v[2 * i + 1] = fmaf(o[nb][gr][i][2 + e] - o[nb][gr][i][e], 0.0625f, -oz[nb][gr][e]) * unit;
                     }
                     *reinterpret_cast<float4 *>(w) = make_float4(v[0], v[1], v[2], v[3]);
                     *reinterpret_cast<float4 *>(w + 4) = make_float4(v[4], v[5], v[6], v[7]);

@@ -443,7 +443,8 @@ QMM_API size_t qmm_paged_attn_workspace(int q_heads, int kv_heads, int head_dim,
  *            in the low four bits.  Aligned to head_dim / 16 bytes; strides multiples of
  *            head_dim / 32.
  * kv_heads and query heads: at most 65536.  Page and head strides, and a page's slots times
- * the slot stride, below 2^31 (QMM_ERR_UNSUPPORTED). */
+ * the slot stride, below 2^31; for qmm_kv4_attn codes within 2^32 - 1 times the largest power of
+ * two (up to 2^20) that divides page and slot stride (QMM_ERR_UNSUPPORTED). */
 typedef struct {
     void *k, *v;                                       /* (device) codes            */
     int64_t page_stride, slot_stride, head_stride;     /* in bytes                  */

@@ -69,6 +69,9 @@ ATTN_CASES = [
     (dict(workspace=None), NULL), (dict(q=A + 4), ALIGN), (dict(out=A + 8), ALIGN), (dict(workspace=A + 8), ALIGN),
     (dict(lse=A + 2), ALIGN), (dict(max_q=0), 0),
 ]
+# places of codes are counted in units of the strides' largest power of two
+UNIT_CASES = [(dict(num_pages=2 ** 31 - 1, page_stride=48), UNSUPPORTED), (dict(num_pages=2 ** 31 - 1, page_stride=32, slot_stride=32), DEVICE),
+              (dict(num_pages=2 ** 20, page_stride=2 ** 20 + 16), UNSUPPORTED), (dict(num_pages=2 ** 18, page_stride=2 ** 20), DEVICE)]
 
 
 @pytest.fixture(scope="module")
@@ -94,6 +97,14 @@ def test_cache_and_batch(lib, name, case):
 def test_arguments(lib, name, cases):
     for kw, want in cases:
         assert call(lib, name, {}, dict(CALLS[name], **kw)) == want, kw
+
+
+@host_only
+@pytest.mark.parametrize("case", range(len(UNIT_CASES)))
+def test_units(lib, case):
+    kw, want = UNIT_CASES[case]
+    assert call(lib, "qmm_kv4_attn", dict(kw, kv_heads=1), ATTN) == want
+    assert call(lib, "qmm_kv4_read", dict(kw, kv_heads=1), READ) == DEVICE
 
 
 @host_only
