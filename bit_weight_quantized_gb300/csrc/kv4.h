@@ -44,11 +44,8 @@ cudaError_t launch_kv4_read(Kv4ReadParams &p, int num_sms, cudaStream_t stream);
 
 // Keys per unit of the kernel for few rows: a warp's stage holds 4 KB of codes.
 __host__ __device__ constexpr int kv4_keys(int head_dim, int warps) { return 4096 / head_dim * warps; }
-// Blocks of it per SM, of four or eight warps (16 rows take 168 registers a thread, 8 rows 128).
-__host__ __device__ constexpr int kv4_blocks_per_sm(int rows, int warps)
-{
-    return warps == 4 ? (rows == 8 ? 4 : 3) : rows == 8 ? 2 : 1;
-}
+// Blocks of it per SM, of four or eight warps (8 rows take 128 registers a thread, 16 all 255).
+__host__ __device__ constexpr int kv4_blocks_per_sm(int rows, int warps) { return (rows == 8 ? 16 : 8) / warps; }
 
 // Clusters of `cluster` blocks of eight warps that run at once on the current device.
 int kv4_decode_clusters(int head_dim, bool bf16, int rows, int cluster);

@@ -115,10 +115,11 @@ kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p)
     constexpr int kChunks = D / 32;                    // 16-byte chunks of a key's codes
     constexpr int kRowsPerCopy = 32 / kChunks, kCopies = kWarpKeys / kRowsPerCopy;
     constexpr int kLook = kWarpKeys / 32;              // keys whose place a lane looks up, per tile
-    // weights are 2^(s - m + 7), at most 2^15: times a V scale over a power of two above it, rounded to fp16
+    // weights are 2^(s - m + 7), at most 2^15: times a V scale over a power of two above it, they
+    // are rounded to fp16
     constexpr float kShift = 7.f;
     constexpr uint32_t kM0 = 0x000f000fu, kM1 = 0x00f000f0u, kMB = 0x00ff00ffu, kScaleBits = 0xfff0fff0u;
-    constexpr int kExpBits = BF16 ? 7 : 10, kBias = BF16 ? 127 : 15, kMostExp = BF16 ? 253 : 30;   // of a scale pattern
+    constexpr int kExpBits = BF16 ? 7 : 10, kBias = BF16 ? 127 : 15, kLeastExp = BF16 ? 63 : 1, kMostExp = BF16 ? 253 : 30;   // of a scale pattern
 
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Share share;
@@ -215,21 +216,24 @@ kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p)
                 const uint16_t *src = sbase + static_cast<long long>(good[i] ? page : 0) * s_page + (good[i] ? slot * s_slot : 0);
                 cp_async_small<L::kScaleRow>(dst + 2 * L::kCodes + (lane + 32 * i) * L::kScaleRow, src, good[i]);
             }
-            all = __all_sync(0xffffffffu, all);
+            const uint32_t to = dst + code_addr<D>(crow, cchunk);   // (its permutation has the period of a copy's rows)
+            if (__all_sync(0xffffffffu, all)) {
 #pragma unroll
-            for (int c = 0; c < kCopies; ++c) {
-                const int row = c * kRowsPerCopy + crow;
-                const uint32_t o = __shfl_sync(0xffffffffu, off[c * kRowsPerCopy / 32], row & 31);
-                const uint32_t to = dst + code_addr<D>(row, cchunk);
-                if (all) {
-                    cp_async16(to, kbase + static_cast<uint64_t>(o) * p.unit);
-                    cp_async16(to + L::kCodes, vbase + static_cast<uint64_t>(o) * p.unit);
-                } else {
-                    const bool ok = o != ~0u;
-                    const uint64_t e = ok ? static_cast<uint64_t>(o) * p.unit : 0;
-                    cp_async16_or_zero(to, kbase + e, ok);
-                    cp_async16_or_zero(to + L::kCodes, vbase + e, ok);
+                for (int c = 0; c < kCopies; ++c) {
+                    const uint32_t o = __shfl_sync(0xffffffffu, off[c * kRowsPerCopy / 32], (c * kRowsPerCopy + crow) & 31);
+                    cp_async16(to + c * kRowsPerCopy * L::kRow, kbase + static_cast<uint64_t>(o) * p.unit);
+                    cp_async16(to + c * kRowsPerCopy * L::kRow + L::kCodes, vbase + static_cast<uint64_t>(o) * p.unit);
                 }
+                return;
+            }
+#pragma unroll 1
+            for (int c = 0; c < kCopies; ++c) {
+                const uint32_t o = __shfl_sync(0xffffffffu, kLook == 2 && c * kRowsPerCopy >= 32 ? off[kLook - 1] : off[0],
+                                               (c * kRowsPerCopy + crow) & 31);
+                const bool ok = o != ~0u;
+                const uint64_t e = ok ? static_cast<uint64_t>(o) * p.unit : 0;
+                cp_async16_or_zero(to + c * kRowsPerCopy * L::kRow, kbase + e, ok);
+                cp_async16_or_zero(to + c * kRowsPerCopy * L::kRow + L::kCodes, vbase + e, ok);
             }
         };
 
@@ -354,8 +358,10 @@ kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p)
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
             m[nb][0] = m[nb][1] = limit[nb][0] = limit[nb][1] = -INFINITY, l[nb][0] = l[nb][1] = 0.f, minus[nb][0] = minus[nb][1] = kShift;
-        uint32_t vlimit = 0;                         // V's patterns so far are below this power of two's
-        float vdown = 1.f;                           // its inverse
+        // V's patterns so far are below that of 2^(vex - kBias); weights and their sums are taken
+        // times its inverse, which leaves a weight times its V scale at 2^15 at most
+        uint32_t vlimit = 0;
+        int vex = kBias;
 
 #pragma unroll 1
         for (int j = 0; j < sg.units; ++j) {
@@ -447,10 +453,9 @@ kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p)
                     big = __reduce_max_sync(0xffffffffu, big >= kInf ? 0u : big);
                     float vf = 1.f;
                     if (big >= vlimit) {
-                        const int ex = min(static_cast<int>(big >> kExpBits) + 1, kMostExp);
-                        const float down = __uint_as_float(static_cast<uint32_t>(127 + kBias - ex) << 23);
-                        vf = vlimit == 0 ? 0.f : down / vdown;   // (powers of two; nothing is there before the first)
-                        vdown = down;
+                        const int ex = min(max(static_cast<int>(big >> kExpBits) + 1, kLeastExp), kMostExp);
+                        vf = __uint_as_float(static_cast<uint32_t>(max(127 + vex - ex, 0)) << 23);
+                        vex = ex;
                         vlimit = static_cast<uint32_t>(ex) << kExpBits;
                     }
 #pragma unroll
@@ -468,10 +473,10 @@ kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p)
                             if (grow) {
                                 m[nb][e] = x;
                                 limit[nb][e] = (x + kGrow) / rowf[nb][e];
-                                minus[nb][e] = kShift - x;
                             }
-                            l[nb][e] *= a;
+                            minus[nb][e] = kShift + static_cast<float>(kBias - vex) - (m[nb][e] == -INFINITY ? 0.f : m[nb][e]);
                             f[e] = a * vf;
+                            l[nb][e] *= f[e];
                         }
 #pragma unroll
                         for (int gr = 0; gr < kGroups; ++gr)
@@ -499,7 +504,7 @@ kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p)
                         l[nb][1] += w1 + w3;
 #pragma unroll
                         for (int gr = 0; gr < kGroups; ++gr) {
-                            const float a = v0[kGroups == 2 ? gr : 1] * vdown, b = v1[kGroups == 2 ? gr : 1] * vdown;
+                            const float a = v0[kGroups == 2 ? gr : 1], b = v1[kGroups == 2 ? gr : 1];
                             pf[nb][gr][0] = transpose8(pack16<false>(w0 * a, w1 * a));
                             pf[nb][gr][1] = transpose8(pack16<false>(w2 * b, w3 * b));
                         }
@@ -538,8 +543,8 @@ kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p)
             rd = next_stage(rd);
         }
         cp_async_wait_group<0>();
-        // (a row's sum and output count 2^(s - m) in bf16, 2^7 times that in fp16: row_log_sum)
-        constexpr float kUnshift = BF16 ? 0.0078125f : 1.f;
+        // a row's sum and output count 2^(s - m) in bf16, 2^7 times that in fp16 (row_log_sum)
+        const float unshift = __uint_as_float(static_cast<uint32_t>(127 + vex - kBias - (BF16 ? 7 : 0)) << 23);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -547,14 +552,14 @@ kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p)
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1)
                     l[nb][e] += __shfl_xor_sync(0xffffffffu, l[nb][e], d);
-                l[nb][e] *= kUnshift;
+                l[nb][e] *= unshift;
             }
 
         // the warps' maxima, sums and outputs meet in shared memory (over the rings)
         __syncthreads();
         float *wo = reinterpret_cast<float *>(smem);
         float *wml = reinterpret_cast<float *>(smem + L::kOffMl);
-        const float unit = 16777216.f * kUnshift / vdown;       // 2^24 for the codes
+        const float unit = 16777216.f * unshift;       // 2^24 for the codes
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
