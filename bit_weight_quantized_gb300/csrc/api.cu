@@ -885,6 +885,7 @@ qmm_status qmm_kv4_append(const qmm_paged_kv4 *kv, const void *k, int64_t k_stri
     p.q_norm = static_cast<const uint16_t *>(q_norm);
     p.k_norm = static_cast<const uint16_t *>(k_norm);
     p.eps = eps;
+    p.one = 1.f;
     return from_cuda(launch_kv4_append(p, stream));
 }
 

@@ -20,7 +20,7 @@ struct Kv4Scales {
 struct Kv4AppendParams : AppendParams {
     Kv4Scales sc;
     const uint16_t *q_norm, *k_norm;   // weights of the norms, or nullptr
-    float eps;
+    float eps, one;                    // one: 1
 };
 
 struct Kv4ReadParams {
@@ -29,6 +29,7 @@ struct Kv4ReadParams {
     uint16_t *k, *v;                   // dense [tokens][kv_heads][D]
     int *status;
     int rows;                          // tokens per block
+    int wide;                          // outputs take 32-byte stores
     FastDiv by_page, by_heads;
 };
 

@@ -48,21 +48,55 @@ __device__ __forceinline__ uint32_t max16x2(uint32_t a, uint32_t b)
     return d;
 }
 
+// Two fp32 values in one 64-bit register: the FMA pipe takes both in one instruction.
+__device__ __forceinline__ uint64_t pair(float lo, float hi)
+{
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+
+__device__ __forceinline__ float2 unpair(uint64_t v)
+{
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+}
+
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+// Eight 16-bit values as four pairs.
 template <bool BF16>
-__device__ __forceinline__ void unpack8(const uint4 &w, float *x)
+__device__ __forceinline__ void unpack8(const uint4 &w, uint64_t *x)
 {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = lo16<BF16>(u[i]);
-        x[2 * i + 1] = hi16<BF16>(u[i]);
-    }
+    for (int i = 0; i < 4; ++i)
+        x[i] = pair(lo16<BF16>(u[i]), hi16<BF16>(u[i]));
 }
 
 template <bool BF16>
-__device__ __forceinline__ uint4 pack8(const float *x)
+__device__ __forceinline__ uint4 pack8(const uint64_t *x)
 {
-    return make_uint4(pack16<BF16>(x[0], x[1]), pack16<BF16>(x[2], x[3]), pack16<BF16>(x[4], x[5]), pack16<BF16>(x[6], x[7]));
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = unpair(x[i]);
+        u[i] = pack16<BF16>(f.x, f.y);
+    }
+    return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
 // (min, max) of a chunk with zero, one in each half of a word's place.
@@ -99,6 +133,16 @@ struct Quant {
         if (s == 0.f)
             z = 0.f;
     }
+    // what the neighbouring thread worked out (the whole warp)
+    __device__ __forceinline__ Quant swapped() const
+    {
+        Quant q = *this;
+        q.s = __shfl_xor_sync(0xffffffffu, s, 1);
+        q.z = __shfl_xor_sync(0xffffffffu, z, 1);
+        q.pattern = __shfl_xor_sync(0xffffffffu, pattern, 1);
+        q.large = __shfl_xor_sync(0xffffffffu, large, 1);
+        return q;
+    }
     __device__ __forceinline__ uint32_t code(float x) const
     {
         constexpr float kMost = BF16 ? 3.3895313892515355e38f : 65504.f;
@@ -109,25 +153,42 @@ struct Quant {
         }
         return static_cast<uint32_t>(c);
     }
-    // eight 16-bit values to a word of codes
+    // Eight 16-bit values to a word of codes.  The quotient by the correctly rounded reciprocal
+    // and one correction (Markstein, "Computation of elementary functions on the IBM RISC System
+    // / 6000": it is the correctly rounded one), which leaves out what a division does for
+    // numbers at the ends of the range; those go by the division.
     __device__ __forceinline__ uint32_t codes(const uint4 &w) const
     {
-        float x[8];
-        unpack8<BF16>(w, x);
+        constexpr float kMagic = 12582912.f;                                // 1.5 2^23: integers in its low bits
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
         uint32_t d = 0;
+        if (large || s < 1e-30f) {                                          // (zeros, and NaN among the values, too)
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t v = i < 2 ? u[0] : i < 4 ? u[1] : i < 6 ? u[2] : u[3];
+                d |= code(i & 1 ? hi16<BF16>(v) : lo16<BF16>(v)) << (4 * i);
+            }
+            return d;
+        }
+        const float inv = __frcp_rn(s);
+        const int base = static_cast<int>(z) - 0x4b400000;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            d |= code(x[i]) << (4 * i);
+        for (int i = 0; i < 8; ++i) {
+            const float x = i & 1 ? hi16<BF16>(u[i / 2]) : lo16<BF16>(u[i / 2]);
+            float q = __fmul_rn(x, inv);
+            q = fmaf(fmaf(-q, s, x), inv, q);
+            d += static_cast<uint32_t>(min(max(__float_as_int(__fadd_rn(q, kMagic)) + base, 0), 15)) << (4 * i);
+        }
         return d;
     }
 };
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 7)
 kv4_append_kernel(const __grid_constant__ Kv4AppendParams p)
 {
     constexpr int kItems = D / 16;                       // threads per head
-    constexpr int kCols = kThreads / kItems;             // heads in flight
+    constexpr int kCols = kThreads / kItems;             // heads side by side
     constexpr int kGroups = D / kKv4Group;
     if (threadIdx.x == 0)
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -136,7 +197,7 @@ kv4_append_kernel(const __grid_constant__ Kv4AppendParams p)
     const qmm_paged_kv &kv = p.kv;
     const int t = blockIdx.x;
     const int lane = threadIdx.x & 31;
-    const int item = threadIdx.x % kItems;
+    const int item = threadIdx.x % kItems, col = threadIdx.x / kItems;
     const int hq = p.q_heads, hk = kv.kv_heads;
     const int rot_items = p.rot / 16;
     const bool turn = item < rot_items;
@@ -146,37 +207,36 @@ kv4_append_kernel(const __grid_constant__ Kv4AppendParams p)
         c0 = item;
         c1 = item + rot_items;
     }
-    // heads: queries 0 .. hq - 1, keys, values
-    const int heads = hq + 2 * hk;
-    auto source = [&](int h) {
-        return h < hq ? p.q + t * p.q_stride + static_cast<long long>(h) * D
-             : h < hq + hk ? p.k + t * p.k_stride + static_cast<long long>(h - hq) * D
-                           : p.v + t * p.v_stride + static_cast<long long>(h - hq - hk) * D;
-    };
-    // kBatch heads' chunks at a time; the first ones are under way before the rest is known
-    int h = threadIdx.x / kItems;
-    uint4 a[kBatch], b[kBatch];
-    auto fetch = [&]() {
+    // Queries come first, kBatch heads at a time, then keys and values, in one row of 2 hk heads.
+    // The first of both are under way before the rest is known.
+    const uint16_t *qsrc = p.q + t * p.q_stride + col * D;
+    uint4 qa[kBatch], qb[kBatch], ka = {}, kb = {};
+    auto fetch_q = [&](int h) {
 #pragma unroll
         for (int u = 0; u < kBatch; ++u)
-            if (h + u * kCols < heads) {
-                const uint16_t *src = source(h + u * kCols);
-                a[u] = __ldcs(reinterpret_cast<const uint4 *>(src + 8 * c0));
-                b[u] = __ldcs(reinterpret_cast<const uint4 *>(src + 8 * c1));
-            } else {
-                a[u] = b[u] = make_uint4(0u, 0u, 0u, 0u);
+            if (h + u * kCols < hq) {
+                qa[u] = __ldcs(reinterpret_cast<const uint4 *>(qsrc + u * (kCols * D) + 8 * c0));
+                qb[u] = __ldcs(reinterpret_cast<const uint4 *>(qsrc + u * (kCols * D) + 8 * c1));
             }
+        qsrc += kBatch * kCols * D;
     };
-    fetch();
-    uint4 wq0 = {}, wq1 = {}, wk0 = {}, wk1 = {};
-    if (p.q_norm) {
-        wq0 = *reinterpret_cast<const uint4 *>(p.q_norm + 8 * c0);
-        wq1 = *reinterpret_cast<const uint4 *>(p.q_norm + 8 * c1);
-    }
-    if (p.k_norm) {
-        wk0 = *reinterpret_cast<const uint4 *>(p.k_norm + 8 * c0);
-        wk1 = *reinterpret_cast<const uint4 *>(p.k_norm + 8 * c1);
-    }
+    auto fetch_kv = [&](int h) {
+        if (h < 2 * hk) {
+            const uint16_t *src = h < hk ? p.k + t * p.k_stride + h * D : p.v + t * p.v_stride + (h - hk) * D;
+            ka = __ldcs(reinterpret_cast<const uint4 *>(src + 8 * c0));
+            kb = __ldcs(reinterpret_cast<const uint4 *>(src + 8 * c1));
+        }
+    };
+    fetch_q(col);
+    fetch_kv(col);
+    uint64_t wa[4], wb[4];                               // the norm's weights
+    auto weights = [&](const uint16_t *w) {
+        if (w) {
+            unpack8<BF16>(*reinterpret_cast<const uint4 *>(w + 8 * c0), wa);
+            unpack8<BF16>(*reinterpret_cast<const uint4 *>(w + 8 * c1), wb);
+        }
+    };
+    weights(p.q_norm);
 
     int seq = 0, end = 0, keys = 0;
     find_sequence(kv, t, lane, seq, end, keys);
@@ -190,124 +250,146 @@ kv4_append_kernel(const __grid_constant__ Kv4AppendParams p)
             record_error(p.status, QMM_ERR_INDEX);
         return;
     }
-    float cs[8], sn[8];
+    uint64_t cs[4], sn[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        cs[i] = 1.f;
-        sn[i] = 0.f;
+    for (int i = 0; i < 4; ++i) {
+        cs[i] = pair(1.f, 1.f);
+        sn[i] = 0;
     }
     if (turn) {
-        const float4 *row = reinterpret_cast<const float4 *>(p.cos_sin + static_cast<long long>(pos) * p.rot + 8 * item);
-        const float4 *rows = reinterpret_cast<const float4 *>(p.cos_sin + static_cast<long long>(pos) * p.rot +
-                                                              p.rot / 2 + 8 * item);
-        const float4 u0 = row[0], u1 = row[1], w0 = rows[0], w1 = rows[1];
-        cs[0] = u0.x; cs[1] = u0.y; cs[2] = u0.z; cs[3] = u0.w;
-        cs[4] = u1.x; cs[5] = u1.y; cs[6] = u1.z; cs[7] = u1.w;
-        sn[0] = w0.x; sn[1] = w0.y; sn[2] = w0.z; sn[3] = w0.w;
-        sn[4] = w1.x; sn[5] = w1.y; sn[6] = w1.z; sn[7] = w1.w;
+        const ulonglong2 *row = reinterpret_cast<const ulonglong2 *>(p.cos_sin + static_cast<long long>(pos) * p.rot + 8 * item);
+        const ulonglong2 *rows = reinterpret_cast<const ulonglong2 *>(p.cos_sin + static_cast<long long>(pos) * p.rot +
+                                                                      p.rot / 2 + 8 * item);
+        const ulonglong2 u0 = row[0], u1 = row[1], w0 = rows[0], w1 = rows[1];
+        cs[0] = u0.x; cs[1] = u0.y; cs[2] = u1.x; cs[3] = u1.y;
+        sn[0] = w0.x; sn[1] = w0.y; sn[2] = w1.x; sn[3] = w1.y;
     }
     int page, slot;
     const bool place = find_slot(kv, p.by_page, seq, pos, p.status, page, slot);
-    const long long at = page * kv.page_stride + slot * kv.slot_stride;
-    const long long sat = scale_offset(p.sc, page, slot);
 
-    // norm and rotation of a head's chunks, rounded to the type
-    auto turned = [&](uint4 &xa, uint4 &xb, bool norm, const uint4 &w0, const uint4 &w1) {
-        float x[8], y[8];
-        unpack8<BF16>(xa, x);
-        unpack8<BF16>(xb, y);
+    // (sums of rounded products: written as sums they came out fused, so they are products with
+    // ones that the compiler does not know)
+    const uint64_t plus = pair(p.one, p.one), minus = pair(-p.one, -p.one);
+    // Norm and rotation of a head's chunks, rounded to the type.  The whole warp comes here together;
+    // what its columns without a head hold does not matter.
+    auto turned = [&](uint4 &a, uint4 &b, bool norm) {
+        uint64_t x[4], y[4];
+        unpack8<BF16>(a, x);
+        unpack8<BF16>(b, y);
         if (norm) {
-            float ss = 0.f;
+            uint64_t s2 = mul2(x[0], x[0]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                ss += x[i] * x[i] + y[i] * y[i];
+            for (int i = 1; i < 4; ++i)
+                s2 = fma2(x[i], x[i], s2);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                s2 = fma2(y[i], y[i], s2);
+            const float2 f = unpair(s2);
+            float ss = f.x + f.y;
 #pragma unroll
             for (int d = 1; d < kItems; d <<= 1)
                 ss += __shfl_xor_sync(0xffffffffu, ss, d);
-            const float r = __frsqrt_rn(__fadd_rn(ss * (1.f / D), p.eps));
-            float u[8], v[8];
-            unpack8<BF16>(w0, u);
-            unpack8<BF16>(w1, v);
+            const float r = rsqrtf(fmaf(ss, 1.f / D, p.eps));
+            const uint64_t r2 = pair(r, r);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                x[i] = __fmul_rn(__fmul_rn(x[i], r), u[i]);
-                y[i] = __fmul_rn(__fmul_rn(y[i], r), v[i]);
+            for (int i = 0; i < 4; ++i) {
+                x[i] = mul2(mul2(x[i], r2), wa[i]);
+                y[i] = mul2(mul2(y[i], r2), wb[i]);
             }
         }
-        if (turn) {
-            if (p.interleaved) {
+        if (p.rot > 0 && p.interleaved) {
+            if (turn) {
+                // pairs side by side
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    float &e = i < 4 ? x[2 * i] : y[2 * i - 8], &o = i < 4 ? x[2 * i + 1] : y[2 * i - 7];
-                    const float e0 = e, o0 = o;
-                    e = __fsub_rn(__fmul_rn(e0, cs[i]), __fmul_rn(o0, sn[i]));
-                    o = __fadd_rn(__fmul_rn(o0, cs[i]), __fmul_rn(e0, sn[i]));
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float x0 = x[i], y0 = y[i];
-                    x[i] = __fsub_rn(__fmul_rn(x0, cs[i]), __fmul_rn(y0, sn[i]));
-                    y[i] = __fadd_rn(__fmul_rn(y0, cs[i]), __fmul_rn(x0, sn[i]));
+                    uint64_t &z = i < 4 ? x[i & 3] : y[i & 3];
+                    const float2 cc = unpair(cs[i / 2]), ss = unpair(sn[i / 2]), f = unpair(z);
+                    const float c = i & 1 ? cc.y : cc.x, s = i & 1 ? ss.y : ss.x;
+                    z = pair(__fsub_rn(__fmul_rn(f.x, c), __fmul_rn(f.y, s)), __fadd_rn(__fmul_rn(f.y, c), __fmul_rn(f.x, s)));
                 }
             }
+        } else if (p.rot > 0) {                          // (threads that do not turn: by cosines of one)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint64_t x0 = x[i], y0 = y[i];
+                x[i] = fma2(mul2(y0, sn[i]), minus, mul2(x0, cs[i]));
+                y[i] = fma2(mul2(x0, sn[i]), plus, mul2(y0, cs[i]));
+            }
         }
-        xa = pack8<BF16>(x);
-        xb = pack8<BF16>(y);
+        a = pack8<BF16>(x);
+        b = pack8<BF16>(y);
     };
-    // the whole warp goes through this together: the heads' columns exchange values
-    const int last = (heads + kBatch * kCols - 1) / (kBatch * kCols);
-    for (int round = 0; round < last; ++round) {
+
+    const int first = (threadIdx.x & ~31) / kItems;      // the warp's first column
+    uint16_t *dst = p.q_out + (static_cast<long long>(t) * hq + col) * D;
+    const bool work = p.rot > 0 || p.q_norm;
+    for (int h0 = first; h0 < hq;) {
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
-            const int hu = h + u * kCols;
-            const bool is_q = hu < hq, is_k = hu >= hq && hu < hq + hk;
-            const bool norm = (is_q && p.q_norm) || (is_k && p.k_norm);
-            // (the columns of a warp may hold queries, keys and values side by side)
-            if (__any_sync(0xffffffffu, norm)) {
-                uint4 xa = a[u], xb = b[u];
-                turned(xa, xb, true, is_q ? wq0 : wk0, is_q ? wq1 : wk1);
-                if (norm) {
-                    a[u] = xa;
-                    b[u] = xb;
-                }
+            if (h0 + u * kCols >= hq)
+                break;
+            if (work)
+                turned(qa[u], qb[u], p.q_norm != nullptr);
+            if (h0 + u * kCols + (col - first) < hq) {
+                *reinterpret_cast<uint4 *>(dst + u * (kCols * D) + 8 * c0) = qa[u];
+                *reinterpret_cast<uint4 *>(dst + u * (kCols * D) + 8 * c1) = qb[u];
             }
-            if (!norm && turn && (is_q || is_k))
-                turned(a[u], b[u], false, wq0, wq1);
-            if (is_q && hu < heads) {
-                uint16_t *dst = p.q_out + (static_cast<long long>(t) * hq + hu) * D;
-                *reinterpret_cast<uint4 *>(dst + 8 * c0) = a[u];
-                *reinterpret_cast<uint4 *>(dst + 8 * c1) = b[u];
+        }
+        dst += kBatch * kCols * D;
+        h0 += kBatch * kCols;
+        fetch_q(h0 + (col - first));
+    }
+    if (!place)
+        return;
+    const long long at = page * kv.page_stride + slot * kv.slot_stride;
+    const long long sat = scale_offset(p.sc, page, slot);
+    if (p.k_norm != p.q_norm)
+        weights(p.k_norm);
+    for (int h0 = first; h0 < 2 * hk; h0 += kCols) {
+        const int h = h0 + (col - first);
+        const bool is_k = h < hk;
+        if (h0 < hk && (p.rot > 0 || p.k_norm)) {        // (a warp may hold keys and values side by side)
+            uint4 a = ka, b = kb;
+            turned(a, b, p.k_norm != nullptr);
+            if (is_k) {
+                ka = a;
+                kb = b;
             }
-            if (!__any_sync(0xffffffffu, hu >= hq && hu < heads))
-                continue;
-            // extremes of the groups, group g in half g of a word
-            uint32_t lo0, hi0, lo1, hi1;
-            extremes<BF16>(a[u], lo0, hi0);
-            extremes<BF16>(b[u], lo1, hi1);
-            uint32_t lo, hi;
-            if constexpr (kGroups == 2) {
-                const uint32_t m0 = c0 >> 3 ? 0xffff0000u : 0xffffu, m1 = c1 >> 3 ? 0xffff0000u : 0xffffu;
-                lo = min16x2<BF16>(lo0 & m0, lo1 & m1);
-                hi = max16x2<BF16>(hi0 & m0, hi1 & m1);
-            } else {
-                lo = min16x2<BF16>(lo0, lo1);
-                hi = max16x2<BF16>(hi0, hi1);
-            }
+        }
+        // extremes of the groups, group g in half g of a word
+        uint32_t lo0, hi0, lo1, hi1;
+        extremes<BF16>(ka, lo0, hi0);
+        extremes<BF16>(kb, lo1, hi1);
+        uint32_t lo, hi;
+        if constexpr (kGroups == 2) {
+            const uint32_t m0 = c0 >> 3 ? 0xffff0000u : 0xffffu, m1 = c1 >> 3 ? 0xffff0000u : 0xffffu;
+            lo = min16x2<BF16>(lo0 & m0, lo1 & m1);
+            hi = max16x2<BF16>(hi0 & m0, hi1 & m1);
+        } else {
+            lo = min16x2<BF16>(lo0, lo1);
+            hi = max16x2<BF16>(hi0, hi1);
+        }
 #pragma unroll
-            for (int d = 1; d < kItems; d <<= 1) {
-                lo = min16x2<BF16>(lo, __shfl_xor_sync(0xffffffffu, lo, d));
-                hi = max16x2<BF16>(hi, __shfl_xor_sync(0xffffffffu, hi, d));
-            }
-            if (is_q || hu >= heads || !place)
-                continue;
-            const Quant<BF16> g0(lo16<BF16>(lo), lo16<BF16>(hi)), g1(hi16<BF16>(lo), hi16<BF16>(hi));
-            const uint32_t w0 = (kGroups == 2 && c0 >> 3 ? g1 : g0).codes(a[u]);
-            const uint32_t w1 = (kGroups == 2 && c1 >> 3 ? g1 : g0).codes(b[u]);
-            const int head = is_k ? hu - hq : hu - hq - hk;
-            uint8_t *dst = static_cast<uint8_t *>(is_k ? kv.k : kv.v) + at + head * kv.head_stride;
-            *reinterpret_cast<uint32_t *>(dst + 4 * c0) = w0;
-            *reinterpret_cast<uint32_t *>(dst + 4 * c1) = w1;
+        for (int d = 1; d < kItems; d <<= 1) {
+            lo = min16x2<BF16>(lo, __shfl_xor_sync(0xffffffffu, lo, d));
+            hi = max16x2<BF16>(hi, __shfl_xor_sync(0xffffffffu, hi, d));
+        }
+        // a thread works out one group's scale, its pair's first thread the first's
+        const bool second = kGroups == 2 && item & 1;
+        const Quant<BF16> mine(second ? hi16<BF16>(lo) : lo16<BF16>(lo), second ? hi16<BF16>(hi) : lo16<BF16>(hi));
+        Quant<BF16> g0 = mine, g1 = mine;
+        if constexpr (kGroups == 2) {
+            const Quant<BF16> other = mine.swapped();
+            g0 = second ? other : mine;
+            g1 = second ? mine : other;
+        }
+        if (h < 2 * hk) {
+            const uint32_t w0 = (kGroups == 2 && c0 >> 3 ? g1 : g0).codes(ka);
+            const uint32_t w1 = (kGroups == 2 && c1 >> 3 ? g1 : g0).codes(kb);
+            const int head = is_k ? h : h - hk;
+            uint8_t *to = static_cast<uint8_t *>(is_k ? kv.k : kv.v) + at + head * kv.head_stride;
+            *reinterpret_cast<uint32_t *>(to + 4 * c0) = w0;
+            *reinterpret_cast<uint32_t *>(to + 4 * c1) = w1;
             if (item == 0) {
                 uint16_t *sd = p.sc.base + sat + head * p.sc.head + (is_k ? 0 : kGroups);
                 if constexpr (kGroups == 2)
@@ -316,9 +398,7 @@ kv4_append_kernel(const __grid_constant__ Kv4AppendParams p)
                     *sd = static_cast<uint16_t>(g0.pattern);
             }
         }
-        h += kBatch * kCols;
-        if (round + 1 < last)
-            fetch();
+        fetch_kv(h + kCols);
     }
 }
 

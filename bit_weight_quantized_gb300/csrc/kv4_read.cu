@@ -1,9 +1,10 @@
 // kv4_read.cu -- reading the 4-bit paged cache back: (c - z) s for the last tokens of every
 // sequence, exact in 16 bits.
 //
-// Bound by memory: 4.25 bits a value come in, 16 go out.  A thread turns eight codes (a
-// word) into a 16-byte store, so that a warp's loads and stores are whole lines; a block
-// finds the places of its tokens first, and takes four words a thread at a time.
+// Bound by memory: 4.25 bits a value come in, 16 go out.  A thread turns sixteen codes into a
+// 32-byte store (or two of 16, where the output is aligned to less), so that a warp's loads and
+// stores are whole lines; a block finds the places of its tokens first, and has kFlight loads a
+// thread under way.
 #include <algorithm>
 
 #include "kv4.cuh"
@@ -13,8 +14,8 @@ namespace qmm {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMostRows = 16;                            // tokens per block
-constexpr int kFlight = 4;                               // words in flight per thread
+constexpr int kMostRows = 8;                             // tokens per block
+constexpr int kFlight = 2;                               // loads in flight per thread
 
 struct Place {
     long long codes, scales;                             // offsets of (page, slot), -1: nothing to read
@@ -24,7 +25,7 @@ template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreads)
 kv4_read_kernel(const __grid_constant__ Kv4ReadParams p)
 {
-    constexpr int kWords = D / 8;                        // words of codes per head
+    constexpr int kPieces = D / 16;                      // of a head
     constexpr int kGroups = D / kKv4Group;
     __shared__ Place places[kMostRows];
     if (threadIdx.x == 0)
@@ -52,34 +53,45 @@ kv4_read_kernel(const __grid_constant__ Kv4ReadParams p)
         }
     }
     __syncthreads();
-    // words of a token: [key, value][head][word]
-    const int per = 2 * kv.kv_heads * kWords, all = rows * per;
-    const int word = threadIdx.x % kWords;
+    // pieces of a token, 16 codes: [key, value][head][piece]
+    const int all = rows * 2 * kv.kv_heads * kPieces;
+    const int piece = threadIdx.x % kPieces;
     for (int e0 = threadIdx.x; e0 < all; e0 += kFlight * kThreads) {
-        uint32_t w[kFlight], pattern[kFlight];
+        uint2 w[kFlight];
+        uint32_t pattern[kFlight];
         uint16_t *dst[kFlight];
 #pragma unroll
         for (int u = 0; u < kFlight; ++u) {
             const int e = e0 + u * kThreads;
             dst[u] = nullptr;
-            w[u] = pattern[u] = 0;
+            w[u] = make_uint2(0u, 0u);
+            pattern[u] = 0;
             if (e < all) {
-                // (token, key or value, head): e / kWords in the heads' base
-                const int row = p.by_heads(e / kWords), i = row >> 1, head = e / kWords - row * kv.kv_heads;
+                const int row = p.by_heads(e / kPieces), i = row >> 1, head = e / kPieces - row * kv.kv_heads;
                 const bool is_v = row & 1;
                 const Place at = places[i];
                 if (at.codes >= 0) {
                     const uint8_t *src = static_cast<const uint8_t *>(is_v ? kv.v : kv.k) + at.codes + head * kv.head_stride;
-                    w[u] = __ldcs(reinterpret_cast<const uint32_t *>(src) + word);
-                    pattern[u] = p.sc.base[at.scales + head * p.sc.head + (is_v ? kGroups : 0) + (word >> 3)];
-                    dst[u] = (is_v ? p.v : p.k) + (static_cast<long long>(t0 + i) * kv.kv_heads + head) * D + 8 * word;
+                    w[u] = __ldcs(reinterpret_cast<const uint2 *>(src) + piece);
+                    pattern[u] = p.sc.base[at.scales + head * p.sc.head + (is_v ? kGroups : 0) + piece / 4];
+                    dst[u] = (is_v ? p.v : p.k) + (static_cast<long long>(t0 + i) * kv.kv_heads + head) * D + 16 * piece;
                 }
             }
         }
 #pragma unroll
         for (int u = 0; u < kFlight; ++u)
-            if (dst[u])
-                __stcs(reinterpret_cast<uint4 *>(dst[u]), GroupScale<BF16>(pattern[u]).values(w[u]));
+            if (dst[u]) {
+                const GroupScale<BF16> sc(pattern[u]);
+                const uint4 a = sc.values(w[u].x), b = sc.values(w[u].y);
+                if (p.wide) {
+                    asm volatile("st.global.cs.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst[u]), "r"(a.x),
+                                 "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                                 : "memory");
+                } else {
+                    reinterpret_cast<uint4 *>(dst[u])[0] = a;
+                    reinterpret_cast<uint4 *>(dst[u])[1] = b;
+                }
+            }
     }
 }
 
@@ -106,6 +118,7 @@ cudaError_t launch_kv4_read(Kv4ReadParams &p, int num_sms, cudaStream_t stream)
     // the words of a block's tokens are counted in 32 bits
     while (p.rows > 1 && static_cast<long long>(p.rows) * p.kv.kv_heads > (1 << 24))
         p.rows /= 2;
+    p.wide = (reinterpret_cast<uintptr_t>(p.k) | reinterpret_cast<uintptr_t>(p.v)) % 32 == 0;
     const bool bf16 = p.kv.dtype == QMM_BF16;
     if (p.kv.head_dim == 128)
         return bf16 ? launch_read<128, true>(p, stream) : launch_read<128, false>(p, stream);

@@ -300,6 +300,18 @@ def test_read(q, D, layout, ql, kl, page, hk):
     assert (k[bt.T:] == 7.0).all() and (v[bt.T:] == 7.0).all()
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_read_into_rows_aligned_to_16_bytes(q, D):
+    bt = Batch4([5], [40], 3, 3, D, "f16")
+    a, b = (torch.full((5 * 3 * D + 16,), 7.0, dtype=bt.dt, device="cuda") for _ in range(2))
+    k, v = a[8:8 + 5 * 3 * D].view(5, 3, D), b[8:8 + 5 * 3 * D].view(5, 3, D)
+    q.qmm_kv4_read(*bt.args(), 5, k_out=k, v_out=v)
+    assert status(q) == 0
+    assert torch.equal(k.double(), bt.k64[0][35:]) and torch.equal(v.double(), bt.v64[0][35:])
+    for x in (a, b):
+        assert (x[:8] == 7.0).all() and (x[-8:] == 7.0).all()
+
+
 def test_padding_is_left_alone(q):
     bt = Batch4([1, 2, 1], [0, 1, 3], 4, 2, 128, "bf16", fill=False, extra_blocks=1)
     g = torch.randn(bt.T + 2, 8, 128, device="cuda").bfloat16()
