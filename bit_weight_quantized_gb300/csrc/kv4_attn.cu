@@ -15,21 +15,33 @@ int grid_of(bool few, int rows, int num_sms) { return few ? kv4_blocks_per_sm(ro
 // the partial results) than the longer walk.
 constexpr int kMinUnits = 3, kMinChunkUnits = 4;
 
-// Whole items in clusters against a split over all blocks: a cluster's block walks
+// Few rows, whole items in clusters against a split over all blocks: a cluster's block walks
 // units / c, a split one units * items / blocks and the joining kernel's time, some
 // kJoinUnits; and not more than kMostUnits, since whole items are not balanced where
-// lengths differ.
+// lengths differ.  One token over 4000 keys of 8 heads 8.3 us in clusters of 8 (4: 10.6, 1:
+// 25.4, split 10.9); 16 over 2000 14.5 in 2 (split 18.7), 32 over 4000 41.0 in 1 (42.9).
 constexpr int kJoinUnits = 4, kMostUnits = 10;
 
-// Work of the longest item (setup and units) up to which blocks of the kernel for many rows
-// take whole items, and the same where every item has a block of its own (as attn.cu).
+// Few rows, whole items in blocks of four warps, more of them than run at once: blocks start as
+// others end, without a joining kernel and with fewer items cut in two; at the end the
+// last ones run alone, which costs the more the longer the items and the fewer they are.  Up
+// to kWholeUnits units and kMoreUnits for each time that the blocks are filled: 512 items of 700
+// keys 18.9 us (split 23.3), of 140 .. 1400 29.1 (29.1), of 280 .. 2800 50.9 (42.0); 2048 of
+// 1400 96.1 (102.8), of 280 .. 2800 130 (129), of 560 .. 5600 244 (237).
+constexpr int kWholeUnits = 6, kMoreUnits = 5;
+
+// Many rows: work of the longest item (setup and units) up to which blocks take whole items,
+// and the same where every item has a block of its own (as attn.cu).
 constexpr int kUnsplitWork = 12, kWholeWork = 10;
 
-// Rows (token, query head) per key head up to which the kernel for few rows takes the call.
-constexpr int kFewRows = 32;
+// Rows (token, query head) per key head of the kernel for few rows: two column tiles of the
+// matrix instructions.  More go to it, sixteen at a time, where these items all run at once in
+// clusters (128 rows over 2000 keys 13.3 us, many-row kernel 16.7; but 32 over 2000 of 64
+// sequences 114 and 108).
+constexpr int kFewRows = 16;
 
 // Blocks of eight warps per item where every item gets a cluster (or block) of its own:
-// clusters of the largest size that all run at once; 0: the axis is split over all blocks.
+// clusters of the largest size that all run at once; 0: there are none.
 int cluster_of(const Kv4AttnParams &p, int rows, long long items, long long span, int num_sms)
 {
     const int keys = kv4_keys(p.kv.head_dim, 8), blocks = kv4_blocks_per_sm(rows, 8) * num_sms;
@@ -80,28 +92,31 @@ cudaError_t kv4_attn_dispatch(Kv4AttnParams &p, int max_q, long long max_kv, voi
         p.window = 0;
     if (p.window == 0)
         p.sinks = 0;
+    // keys of an item at most: a window's, the first tokens, and those its tokens see beyond each
+    // other; its parts may then begin and end inside a unit
+    const auto span_of = [&](int rows) {
+        return p.window > 0 ? std::min(max_kv, static_cast<long long>(p.window) + p.sinks + rows / p.group + 1) : max_kv;
+    };
+    const int few_rows = q_rows <= 8 ? 8 : 16;
+    const long long few_items = p.kv.batch * ((q_rows + few_rows - 1) / few_rows) * p.kv.kv_heads;
+    const int cluster = cluster_of(p, few_rows, few_items, span_of(few_rows), num_sms);
     // (and queries that the other kernel's tensor copies do not take)
-    const bool few = q_rows <= kFewRows || !attn_set_q_tma(p);
-    p.tile_rows = few ? (q_rows <= 8 ? 8 : 16) : 2 * chunk_stream_rows(p.group);
+    const bool few = q_rows <= kFewRows || cluster > 0 || !attn_set_q_tma(p);
+    p.tile_rows = few ? few_rows : 2 * chunk_stream_rows(p.group);
     p.row_tiles = static_cast<int>((q_rows + p.tile_rows - 1) / p.tile_rows);
     p.by_group = fast_div(p.group);
     p.by_tiles = fast_div(p.row_tiles);
     p.by_page = fast_div(p.kv.page_size);
     p.min_chunk = few ? kMinUnits : kMinChunkUnits;
-    // keys of an item at most: a window's, the first tokens, and those its tokens see beyond each other
-    const long long seen = static_cast<long long>(p.window) + p.sinks + p.tile_rows / p.group + 1;
-    const bool part = p.window > 0 && seen < max_kv;
-    const long long span = part ? seen : max_kv;
-    const long long items = static_cast<long long>(p.kv.batch) * p.row_tiles * p.kv.kv_heads;
-    const int cluster = few ? cluster_of(p, p.tile_rows, items, span, num_sms) : 0;
-    p.warps = cluster > 0 ? 8 : 4;
+    const long long items = static_cast<long long>(p.kv.batch) * p.row_tiles * p.kv.kv_heads, span = span_of(p.tile_rows);
+    p.cluster = few && cluster > 0 ? cluster : 1;
+    p.warps = few && cluster > 0 ? 8 : 4;
     const int keys = few ? kv4_keys(p.kv.head_dim, p.warps) : kChunkKeys, setup = few ? kDecodeSetup : kChunkSetup;
-    // (its parts may begin and end inside a unit)
-    const long long longest = (span + keys - 1) / keys + (part ? 2 : 0);
+    const long long longest = (span + keys - 1) / keys + (span < max_kv ? 2 : 0);
     int grid = grid_of(few, p.tile_rows, num_sms);
-    p.whole = few ? cluster > 0 : items <= grid ? longest + setup <= kWholeWork : longest + setup <= kUnsplitWork;
+    p.whole = few ? cluster > 0 || (longest <= kWholeUnits + kMoreUnits * items / grid && items <= 0x7fffffff)
+                  : items <= grid ? longest + setup <= kWholeWork : longest + setup <= kUnsplitWork;
     p.unsplit = !few && p.whole && items > grid;
-    p.cluster = std::max(cluster, 1);
     if (p.whole && !p.unsplit)
         grid = static_cast<int>(items) * p.cluster;
     else if (p.unsplit)
