@@ -7,6 +7,9 @@ the page lists):
     attend over the paged cache        qmm_paged_attn
     y    = x + heads . W_o^T           qmm_gemm / qmm_gemv
 
+or, over a cache in 4 bits, with queries and keys normed per head, a window and first
+tokens that stay visible: qmm_kv4_append and qmm_kv4_attn.
+
     python examples/attention_layer.py
 
 Three conversations share one pool of pages.  Their prompts go in in chunks, all in
@@ -70,8 +73,23 @@ class PagedCache:
         return table.to(dev), cu.to(dev), torch.tensor(self.lengths, dtype=torch.int32, device=dev)
 
 
+class PagedCache4(PagedCache):
+    """The same in 4 bits: codes, and a scale pattern per 64 values."""
+
+    def __init__(self, pages, page, kv_heads, head_dim, batch, dtype, device):
+        super().__init__(0, page, kv_heads, head_dim, batch, dtype, device)
+        self.k, self.v = (torch.zeros(pages, kv_heads, page, head_dim // 2, dtype=torch.uint8, device=device).permute(0, 2, 1, 3)
+                          for _ in range(2))
+        self.scales = torch.zeros(pages, kv_heads, page, head_dim // 32, dtype=dtype, device=device).permute(0, 2, 1, 3)
+        self.free = list(range(pages))
+
+
 class AttentionLayer:
-    def __init__(self, hidden=1024, q_heads=8, kv_heads=2, head_dim=128, max_len=4096, device="cuda", seed=0):
+    """norm: queries and keys are normed per head; window, sinks: tokens that a token sees (both
+    over a cache in 4 bits)."""
+
+    def __init__(self, hidden=1024, q_heads=8, kv_heads=2, head_dim=128, max_len=4096, device="cuda", seed=0, norm=False,
+                 window=0, sinks=0):
         g = torch.Generator(device=device)
         g.manual_seed(seed)
         self.heads, self.kv_heads, self.D = q_heads, kv_heads, head_dim
@@ -84,23 +102,32 @@ class AttentionLayer:
         freq = 10000.0 ** (-torch.arange(head_dim // 2, device=device, dtype=torch.float64) * 2 / head_dim)
         ang = torch.arange(max_len, device=device, dtype=torch.float64)[:, None] * freq
         self.cos_sin = torch.cat([ang.cos(), ang.sin()], 1).float().contiguous()
+        self.window, self.sinks = window, sinks
+        self.q_norm = self.k_norm = None
+        if norm:
+            self.q_norm, self.k_norm = (1 + torch.randn(2, head_dim, generator=g, device=device) / 4).half()
 
     def __call__(self, x, cache, new):
         """x [tokens][hidden] (fp16): new[b] tokens of every conversation b, packed."""
         T, hq, hk = x.shape[0], self.heads, self.kv_heads
         table, cu_q, kv_len = cache.grow(new)
         qkv = self.qkv(x).view(T, hq + 2 * hk, self.D)
+        if isinstance(cache, PagedCache4):
+            cached = cache.k, cache.v, cache.scales, table, cu_q, kv_len
+            turned = q.qmm_kv4_append(qkv[:, hq:hq + hk], qkv[:, hq + hk:], *cached, q=qkv[:, :hq], cos_sin=self.cos_sin,
+                                      q_norm=self.q_norm, k_norm=self.k_norm)
+            heads = q.qmm_kv4_attn(turned, *cached, max(new), max(cache.lengths), window=self.window, sinks=self.sinks)
+            return x + self.out(heads.view(T, hq * self.D))
         rotated = q.qmm_kv_append(qkv[:, hq:hq + hk], qkv[:, hq + hk:], cache.k, cache.v, table, cu_q, kv_len,
                                   q=qkv[:, :hq], cos_sin=self.cos_sin)
         heads = q.qmm_paged_attn(rotated, cache.k, cache.v, table, cu_q, kv_len, max(new), max(cache.lengths))
         return x + self.out(heads.view(T, hq * self.D))
 
 
-def main():
+def run(layer, kind):
     dev = torch.device("cuda")
-    layer = AttentionLayer(device=dev)
     prompts, chunk, steps = [700, 45, 300], 256, 16
-    cache = PagedCache(128, 16, 2, 128, len(prompts), torch.float16, dev)
+    cache = kind(128, 16, 2, 128, len(prompts), torch.float16, dev)
     left = list(prompts)
     while any(left):
         new = [min(n, chunk) for n in left]
@@ -114,8 +141,13 @@ def main():
     torch.cuda.synchronize()
     t = (time.perf_counter() - t) / steps
     assert q.qmm_device_status() == 0
-    print(f"prompts of {prompts} tokens in, {steps} steps of {len(prompts)} tokens: {t * 1e6:.0f} us a step "
+    print(f"{kind.__name__}: prompts of {prompts} tokens in, {steps} steps of {len(prompts)} tokens: {t * 1e6:.0f} us a step "
           f"(one layer, host work and page lists included); keys now {cache.lengths}")
+
+
+def main():
+    run(AttentionLayer(), PagedCache)
+    run(AttentionLayer(norm=True, window=512, sinks=4), PagedCache4)
 
 
 if __name__ == "__main__":
