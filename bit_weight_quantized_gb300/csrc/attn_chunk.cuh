@@ -437,7 +437,6 @@ attn_chunk_kernel(const __grid_constant__ typename ChunkForm<D, Q4>::Params p)
             const Segment &sg = segment(n);
             const RowTile r = sg.r;
             const int h = sg.h, units = sg.units, kb0 = (r.unit0 + sg.off) * kChunkKeys, slot = part_slot(sg);
-            [[maybe_unused]] const int sg_off = sg.off;
             const bool two = in_two(sg, srows), whole = is_whole(sg);
             if (!ok || units == 0)
                 break;
@@ -449,7 +448,7 @@ attn_chunk_kernel(const __grid_constant__ typename ChunkForm<D, Q4>::Params p)
             const int row = quarter * 32 + lane, trow = (two ? 0 : srows * s) + row;   // row in the stream, in the item
             const bool mine = row < srows && trow < r.rows;   // (the others hold anything)
             const int rr = r.row0 + trow;
-            const int2 see = row_keys(p, r, rr);
+            const int2 see = Q4 ? row_places(p, r, rr) : row_keys(p, r, rr);   // (Q4: kb and these are places)
             float mref = -INFINITY, l = 0.f;
             const uint64_t scale2 = pair(__float_as_uint(p.scale_log2), __float_as_uint(p.scale_log2));
             const int j0 = two ? s : 0, step = two ? 2 : 1;
@@ -465,7 +464,7 @@ attn_chunk_kernel(const __grid_constant__ typename ChunkForm<D, Q4>::Params p)
                     break;
                 ph ^= 1u;
                 tc_fence_after();
-                const int kb = Q4 ? unit_key<kChunkKeys>(p, r, sg_off + j) : kb0 + j * kChunkKeys;
+                const int kb = kb0 + j * kChunkKeys;
                 // (Q4: the first tokens, before the window, are seen by all)
                 auto all_see = [&](int k, int n) {
                     return (k >= all_lo || (Q4 && k + n <= p.sinks)) && k + n - 1 <= all_hi;
@@ -892,8 +891,8 @@ attn_chunk_kernel(const __grid_constant__ typename ChunkForm<D, Q4>::Params p)
                     auto key_of = [&](int j, int i) {
                         if (j >= units)
                             return -1;
-                        const int key = unit_key<kChunkKeys>(p, r, off + j) + row0 + 32 * i;
-                        return key < r.hi && (key >= r.lo || key < p.sinks) ? key : -1;
+                        const int place = (off + j) * kChunkKeys + row0 + 32 * i;
+                        return place < r.hi ? place + (place < p.sinks ? 0 : r.lo) : -1;
                     };
                     auto look_up = [&](int key) {
                         return key >= 0 ? p.kv.block_table[static_cast<long long>(r.b) * p.kv.blocks + p.by_page(key)] : 0;

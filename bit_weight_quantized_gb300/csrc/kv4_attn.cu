@@ -92,8 +92,7 @@ cudaError_t kv4_attn_dispatch(Kv4AttnParams &p, int max_q, long long max_kv, voi
         p.window = 0;
     if (p.window == 0)
         p.sinks = 0;
-    // keys of an item at most: a window's, the first tokens, and those its tokens see beyond each
-    // other; its parts may then begin and end inside a unit
+    // keys of an item at most: a window's, the first tokens, and those its tokens see beyond each other
     const auto span_of = [&](int rows) {
         return p.window > 0 ? std::min(max_kv, static_cast<long long>(p.window) + p.sinks + rows / p.group + 1) : max_kv;
     };
@@ -112,7 +111,7 @@ cudaError_t kv4_attn_dispatch(Kv4AttnParams &p, int max_q, long long max_kv, voi
     p.cluster = few && cluster > 0 ? cluster : 1;
     p.warps = few && cluster > 0 ? 8 : 4;
     const int keys = few ? kv4_keys(p.kv.head_dim, p.warps) : kChunkKeys, setup = few ? kDecodeSetup : kChunkSetup;
-    const long long longest = (span + keys - 1) / keys + (span < max_kv ? 2 : 0);
+    const long long longest = (span + keys - 1) / keys;
     int grid = grid_of(few, p.tile_rows, num_sms);
     p.whole = few ? cluster > 0 || (longest <= kWholeUnits + kMoreUnits * items / grid && items <= 0x7fffffff)
                   : items <= grid ? longest + setup <= kWholeWork : longest + setup <= kUnsplitWork;

@@ -175,11 +175,9 @@ kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p)
         const uint8_t *vbase = static_cast<const uint8_t *>(p.kv.v) + sg.h * p.kv.head_stride + cchunk * 16;
         const uint16_t *sbase = p.sc.base + sg.h * p.sc.head;
         const int32_t *pages = p.kv.block_table + static_cast<long long>(r.b) * p.kv.blocks;
-        // the warp's first key of tile j (unit_key, with what does not change taken out)
-        const int first_tiles = sink_units<kKeys>(p, r) - sg.off, key0 = sg.off * kKeys + warp * kWarpKeys;
-        const int past = r.unit0 * kKeys;
-        auto tile_key = [&](int j) { return key0 + j * kKeys + (j < first_tiles ? 0 : past); };
-        auto reads = [&](int key) { return key < r.hi && (key >= r.lo || key < p.sinks); };
+        // the warp's first place of tile j (places, not keys: see row_tile)
+        const int place0 = sg.off * kKeys + warp * kWarpKeys;
+        auto tile_place = [&](int j) { return place0 + j * kKeys; };
         // The places of the lane's keys of a tile (lane, lane + 32; slot -1: nobody sees it) are
         // looked up one tile ahead and not looked at before the tile is loaded: the warp would wait
         // for the table here.
@@ -188,11 +186,10 @@ kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p)
         };
         auto look_up = [&](int j) {
             Look k;
-            const int kb = tile_key(j) + lane;
 #pragma unroll
             for (int i = 0; i < kLook; ++i) {
-                const int key = kb + 32 * i, blk = p.by_page(key);
-                const bool in = j < sg.units && reads(key);
+                const int place = tile_place(j) + lane + 32 * i, key = place + (place < p.sinks ? 0 : r.lo), blk = p.by_page(key);
+                const bool in = j < sg.units && place < r.hi;
                 k.slot[i] = in ? key - blk * p.kv.page_size : -1;
                 k.page[i] = in ? pages[blk] : 0;
             }
@@ -331,15 +328,15 @@ kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p)
             }
         }
 
-        // keys that the lane's rows see, and that every row of the tile sees (rows past the
+        // places that the lane's rows see, and that every row of the tile sees (rows past the
         // tile do not count)
         int2 see[NB][2];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-                see[nb][e] = row_keys(p, r, r.row0 + 8 * nb + 2 * t + e);
-        const int all_lo = row_keys(p, r, r.row0 + r.rows - 1).x, all_hi = row_keys(p, r, r.row0).y;
+                see[nb][e] = row_places(p, r, r.row0 + 8 * nb + 2 * t + e);
+        const int all_lo = row_places(p, r, r.row0 + r.rows - 1).x, all_hi = row_places(p, r, r.row0).y;
 
         float o[NB][kGroups][4][4], oz[NB][kGroups][4];   // [tile of d][fragment]; the zeros' share
 #pragma unroll
@@ -372,8 +369,8 @@ kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p)
             ahead = look_up(j + L::kStages);
             cp_async_wait_group<L::kStages - 1>();
             __syncwarp();
-            const int kb = tile_key(j);
-            if (kb < r.hi && (kb + kWarpKeys > r.lo || kb < p.sinks)) {
+            const int kb = tile_place(j);
+            if (kb < r.hi) {
                 // scores: rows are keys, columns query rows
                 float s[kSteps][NB][4];
 #pragma unroll
@@ -422,8 +419,8 @@ kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p)
                         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                const int key = kb + 16 * st + key_row(g) + (e < 2 ? 0 : 8);
-                                if ((key < see[nb][e & 1].x && key >= p.sinks) || key > see[nb][e & 1].y)
+                                const int place = kb + 16 * st + key_row(g) + (e < 2 ? 0 : 8);
+                                if ((place < see[nb][e & 1].x && place >= p.sinks) || place > see[nb][e & 1].y)
                                     s[st][nb][e] = -INFINITY;
                             }
                 }

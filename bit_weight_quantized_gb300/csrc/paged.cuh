@@ -152,7 +152,7 @@ struct RowTile {
     int row0;       // first row of the tile
     int rows;       // rows in the tile (0: the tile does not exist)
     int kv;         // keys of the sequence
-    int lo, hi;     // keys some row of the tile sees
+    int lo, hi;     // keys some row of the tile sees (SINKS: see row_tile)
     int unit0, units;
 };
 
@@ -160,20 +160,10 @@ struct RowTile {
 // difference is taken: pos may be negative (padding) and the window as large as an int.
 __host__ __device__ __forceinline__ int window_start(int pos, int window) { return pos >= window ? pos - window + 1 : 0; }
 
-// With first tokens that stay visible (SINKS), the units that hold them and lie before the
-// window's come first: unit u of the item holds keys from unit_key(p, r, u).
-template <int KEYS>
-__device__ __forceinline__ int sink_units(const AttnParams &p, const RowTile &r)
-{
-    return min(r.lo / KEYS, p.sinks / KEYS + (p.sinks % KEYS != 0));
-}
-
-template <int KEYS>
-__device__ __forceinline__ int unit_key(const AttnParams &p, const RowTile &r, int u)
-{
-    return (u < sink_units<KEYS>(p, r) ? u : r.unit0 + u) * KEYS;
-}
-
+// With first tokens that stay visible (SINKS, p.sinks) an item's keys are numbered along an
+// axis without the hidden ones between those and the window: places 0 .. hi, which the units
+// count along, place i being key i + (i < p.sinks ? 0 : lo).  Every row of a tile that has such
+// a gap sees the first tokens (its position lies past the window's start).
 template <int KEYS, bool SINKS = false>
 __device__ __forceinline__ RowTile row_tile(const AttnParams &p, int i)
 {
@@ -194,13 +184,14 @@ __device__ __forceinline__ RowTile row_tile(const AttnParams &p, int i)
     const int last = r.kv - r.n + p.by_group(r.row0 + r.rows - 1);
     r.hi = p.causal ? min(r.kv, max(0, last + 1)) : r.kv;
     r.lo = p.window > 0 ? min(r.hi, window_start(first, p.window)) : 0;
+    if constexpr (SINKS) {
+        r.lo = max(0, r.lo - p.sinks);
+        r.hi -= r.lo;
+        r.units = max(1, (r.hi + KEYS - 1) / KEYS);
+        return r;
+    }
     r.unit0 = r.lo / KEYS;
     r.units = max(1, (r.hi + KEYS - 1) / KEYS - r.unit0);
-    if constexpr (SINKS) {
-        const int first_units = sink_units<KEYS>(p, r);
-        r.unit0 -= first_units;
-        r.units += first_units;
-    }
     return r;
 }
 
@@ -212,6 +203,13 @@ __device__ __forceinline__ int2 row_keys(const AttnParams &p, const RowTile &r, 
         return make_int2(0, -1);
     const int pos = r.kv - r.n + p.by_group(row);
     return make_int2(p.window > 0 ? window_start(pos, p.window) : 0, p.causal ? min(r.kv - 1, pos) : r.kv - 1);
+}
+
+// The same in places (SINKS).
+__device__ __forceinline__ int2 row_places(const AttnParams &p, const RowTile &r, int row)
+{
+    const int2 k = row_keys(p, r, row);
+    return make_int2(k.x - r.lo, k.y - r.lo);
 }
 
 // Where a block's share of the work starts.  All items of the call lie on one
