@@ -8,14 +8,16 @@
 //   s = (hi - lo) / 15 rounded up to 4 (bf16) or 7 (fp16) significant bits,
 //   z = rint(-lo / s),  c = clamp(rint(x / s) + z, 0, 15)
 //
-// in fp32 with IEEE division and without fused multiply-adds, so that a plain computation
-// step by step gives the same codes.  x / s is a tie exactly when the division says so: x and
-// s have 11 and 7 bits at most, and a quotient that is no tie is further from one than
-// fp32 rounds.
+// in fp32 with correctly rounded quotients and, in the rotation, without fused multiply-adds, so
+// that a plain computation step by step gives the same codes.  x / s is a tie exactly when the
+// division says so: x and s have 11 and 7 bits at most, and a quotient that is no tie is
+// further from one than fp32 rounds.
 //
-// Bound by memory, like kv_append.cu, whose layout this has: a block serves a token,
-// thread i of a column of head_dim / 16 owns two 8-value chunks of a head.  The sums and the
-// extremes of a head meet by shuffles within the column.
+// Bound by memory, like kv_append.cu, whose layout this has, and nearly as much by
+// instructions: a block serves a token, thread i of a column of head_dim / 16 owns two 8-value
+// chunks of a head.  The sums and the extremes of a head meet by shuffles within the column.
+// 8192 tokens of 80 heads of 128: 63 us with norms, 55 without (4.9 and 5.7 TB/s); with
+// divisions and one loop over all heads 93.
 #include "kv4.cuh"
 
 namespace qmm {

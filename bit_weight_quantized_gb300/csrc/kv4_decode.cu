@@ -24,11 +24,12 @@
 // the largest scale seen as the maximum follows the scores; that the zeros' share is
 // subtracted by the same rounded weights comes from one more product, of the zeros.
 //
-// Bound by the cache's bytes (D + D / 16 per key and head) and nearly as much by
-// instruction issue: some 250 instructions a warp for 16 keys of 128 (2176 bytes, which
-// the copy rate brings in 93 cycles).  Each of a block's warps walks its own keys with its
-// own ring of asynchronous copies, maximum, sum and output, as in attn_decode.cu, whose
-// split, clusters and end this has.
+// Bound by instruction issue as much as by the cache's bytes (D + D / 16 per key and head): 300
+// instructions a warp for 16 keys of 128 in the loop, 2176 bytes, which the copy rate brings in
+// 93 cycles, 372 issue slots.  64 sequences of 300 to 4096 keys, 8 key heads: 51.7 us (copies
+// alone 36, the first form of this kernel 58.5); one token over 131072 keys 44.5.  Each of a
+// block's warps walks its own keys with its own ring of asynchronous copies, maximum, sum and
+// output, as in attn_decode.cu, whose split, clusters and end this has.
 #include <atomic>
 #include <cuda_fp16.h>
 

@@ -487,7 +487,8 @@ QMM_API qmm_status qmm_kv4_read(const qmm_paged_kv4 *kv, void *k_out, void *v_ou
  *           j > p - window or j < sinks when window > 0.
  *   sinks    0, or the number of first tokens that a window leaves visible (sinks > 0
  *            needs window > 0).
- * Queries must be finite (a NaN or an infinity makes its row NaN), in bf16 below 2^116.
+ * Queries must be finite (a NaN or an infinity makes its row NaN), in bf16 below 2^116;
+ * bf16 values below 2^-80 lose bits.
  * Scores, maximum, sums and output are fp32.  Up to 16 query rows per key head (q_heads /
  * kv_heads * new tokens) the codes are multiplied as they are and the weights rounded to
  * fp16 once; for more the values, exact in dtype, are, and the weights are rounded to dtype.
