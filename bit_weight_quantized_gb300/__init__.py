@@ -73,6 +73,7 @@ SIGNATURES = {
     "qmm_kv4_read": ([_P, _P, _P, _P], _I),
     "qmm_kv4_attn": ([_P, _P, _L, _I, _F, _I, _I, _I, _P, _P, _I, _I, _P, _SZ, _P], _I),
     "qmm_kv4_attn_workspace": ([_I, _I, _I, _I], _SZ),
+    "qmm_kv4_attn_more_workspace": ([_I, _I, _I, _I, _I, _I, _I], _SZ),
     "qmm_device_status": ([_P], _I),
     "qmm_watchdog_selftest": ([_P], _I),
     "qmm_status_string": ([_I], ctypes.c_char_p),
@@ -112,13 +113,13 @@ def _load_fastcall(lib):
 _fast_append = _fast_attn = None
 _append_addr = _attn_addr = _scratch_addr = 0   # function addresses for it, filled by load()
 _fast_kv4_append = _fast_kv4_read = _fast_kv4_attn = None
-_kv4_append_addr = _kv4_read_addr = _kv4_attn_addr = _kv4_scratch_addr = 0
+_kv4_append_addr = _kv4_read_addr = _kv4_attn_addr = _kv4_scratch_addr = _kv4_more_addr = 0
 
 
 def _load_paged(lib):
     global _fast_append, _fast_attn, _append_addr, _attn_addr, _scratch_addr
     global _fast_kv4_append, _fast_kv4_read, _fast_kv4_attn
-    global _kv4_append_addr, _kv4_read_addr, _kv4_attn_addr, _kv4_scratch_addr
+    global _kv4_append_addr, _kv4_read_addr, _kv4_attn_addr, _kv4_scratch_addr, _kv4_more_addr
     from .build import paged_path
     path = paged_path()
     if not os.path.exists(path):
@@ -133,9 +134,10 @@ def _load_paged(lib):
     _attn_addr = ctypes.cast(lib.qmm_paged_attn, ctypes.c_void_p).value
     _scratch_addr = ctypes.cast(lib.qmm_paged_attn_workspace, ctypes.c_void_p).value
     _fast_append, _fast_attn = mod.kv_append, mod.paged_attn
-    _kv4_append_addr, _kv4_read_addr, _kv4_attn_addr, _kv4_scratch_addr = (
+    _kv4_append_addr, _kv4_read_addr, _kv4_attn_addr, _kv4_scratch_addr, _kv4_more_addr = (
         ctypes.cast(f, ctypes.c_void_p).value
-        for f in (lib.qmm_kv4_append, lib.qmm_kv4_read, lib.qmm_kv4_attn, lib.qmm_kv4_attn_workspace))
+        for f in (lib.qmm_kv4_append, lib.qmm_kv4_read, lib.qmm_kv4_attn, lib.qmm_kv4_attn_workspace,
+                  lib.qmm_kv4_attn_more_workspace))
     _fast_kv4_append, _fast_kv4_read, _fast_kv4_attn = mod.kv4_append, mod.kv4_read, mod.kv4_attn
 
 
@@ -737,19 +739,28 @@ def qmm_kv4_attn_workspace(q_heads: int, kv_heads: int, head_dim: int, max_q: in
     return int(load().qmm_kv4_attn_workspace(q_heads, kv_heads, head_dim, max_q))
 
 
+def qmm_kv4_attn_more_workspace(batch: int, q_heads: int, kv_heads: int, head_dim: int, max_q: int, max_kv: int,
+                                sinks: int = 0) -> int:
+    """Bytes beyond qmm_kv4_attn_workspace() with which a qmm_kv4_attn call of these sizes
+    converts its keys once (0: such a call has no use for more)."""
+    _int32(batch=batch, q_heads=q_heads, kv_heads=kv_heads, head_dim=head_dim, max_q=max_q, max_kv=max_kv, sinks=sinks)
+    return int(load().qmm_kv4_attn_more_workspace(batch, q_heads, kv_heads, head_dim, max_q, max_kv, sinks))
+
+
 def qmm_kv4_attn(q, k_cache, v_cache, scales, block_table, cu_q, kv_len, max_q, max_kv=0, scale=None, causal=True,
                  window=0, sinks=0, return_lse=False, out=None, workspace=None):
     """qmm_paged_attn over a cache in 4 bits (k_cache, v_cache and scales as for
     qmm_kv4_append).  With a window, sinks: first tokens that stay visible to every
-    token.  workspace: uint8 scratch of qmm_kv4_attn_workspace() bytes, allocated if
-    None.  See qmm_kv4_attn in qmm.h."""
+    token.  workspace: uint8 scratch of qmm_kv4_attn_workspace() bytes (and
+    qmm_kv4_attn_more_workspace() for long prompts), allocated if None.  See
+    qmm_kv4_attn in qmm.h."""
     if _lib is None:
         load()
     if scale is None:
         scale = q.shape[-1] ** -0.5
     if _fast_kv4_attn is not None:
-        r = _fast_kv4_attn(_kv4_attn_addr, _kv4_scratch_addr, q, k_cache, v_cache, scales, block_table, cu_q, kv_len, max_q,
-                           max_kv, scale, causal, window, sinks, return_lse, out, workspace)
+        r = _fast_kv4_attn(_kv4_attn_addr, _kv4_scratch_addr, _kv4_more_addr, q, k_cache, v_cache, scales, block_table,
+                           cu_q, kv_len, max_q, max_kv, scale, causal, window, sinks, return_lse, out, workspace)
         if type(r) is not int:
             return r
         if r > 0:
@@ -764,6 +775,7 @@ def qmm_kv4_attn(q, k_cache, v_cache, scales, block_table, cu_q, kv_len, max_q, 
     with torch.cuda.device(q.device):
         if workspace is None:
             nbytes = qmm_kv4_attn_workspace(heads, k_cache.shape[2], D, max_q)
+            nbytes += qmm_kv4_attn_more_workspace(kv_len.shape[0], heads, k_cache.shape[2], D, max_q, max_kv, sinks)
             workspace = torch.empty(max(nbytes, 16), dtype=_U8, device=q.device)
         _dev(workspace, "workspace", _U8)
         for name, t in (("out", out), ("workspace", workspace)):

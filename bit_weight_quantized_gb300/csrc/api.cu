@@ -923,6 +923,13 @@ size_t qmm_kv4_attn_workspace(int q_heads, int kv_heads, int head_dim, int max_q
     return kv4_attn_workspace_bytes(q_heads, kv_heads, head_dim, max_q, f->num_sms);
 }
 
+size_t qmm_kv4_attn_more_workspace(int batch, int q_heads, int kv_heads, int head_dim, int max_q, int max_kv, int sinks)
+{
+    if (batch < 1 || sinks < 0 || max_kv < 0 || qmm_kv4_attn_workspace(q_heads, kv_heads, head_dim, max_q) == 0)
+        return 0;
+    return kv4_attn_unpack_bytes(batch, q_heads / kv_heads, kv_heads, head_dim, max_q, max_kv, sinks);
+}
+
 qmm_status qmm_kv4_attn(const qmm_paged_kv4 *kv, const void *q, int64_t q_stride, int q_heads, float scale, int causal,
                         int window, int sinks, void *out, float *lse, int max_q, int max_kv, void *workspace,
                         size_t workspace_bytes, cudaStream_t stream)
@@ -957,8 +964,11 @@ qmm_status qmm_kv4_attn(const qmm_paged_kv4 *kv, const void *q, int64_t q_stride
     const DeviceFacts *f = device_facts();
     if (!f || f->usable != QMM_OK)
         return max_q == 0 ? QMM_OK : QMM_ERR_DEVICE;
-    if (workspace_bytes < kv4_attn_workspace_bytes(q_heads, kv->kv_heads, kv->head_dim, max_q, f->num_sms))
+    const size_t need = kv4_attn_workspace_bytes(q_heads, kv->kv_heads, kv->head_dim, max_q, f->num_sms);
+    if (workspace_bytes < need)
         return QMM_ERR_SHAPE;
+    // (tensor copies read the converted keys from multiples of 128 bytes of the scratch)
+    const size_t more = aligned(workspace, 128) ? workspace_bytes - need : 0;
     p.q = static_cast<const uint16_t *>(q);
     p.out = static_cast<uint16_t *>(out);
     p.lse = lse;
@@ -970,7 +980,7 @@ qmm_status qmm_kv4_attn(const qmm_paged_kv4 *kv, const void *q, int64_t q_stride
     p.causal = causal != 0;
     p.window = window;
     p.sinks = sinks;
-    return from_cuda(kv4_attn_dispatch(p, max_q, max_kv, workspace, f->num_sms, stream));
+    return from_cuda(kv4_attn_dispatch(p, max_q, max_kv, workspace, more, f->num_sms, stream));
 }
 
 qmm_status qmm_watchdog_selftest(cudaStream_t stream)

@@ -30,6 +30,9 @@ struct Kv4ReadParams {
     int *status;
     int rows;                          // tokens per block
     int wide;                          // outputs take 32-byte stores
+    // all visible keys (kv4_unpack): room per sequence and head, window, the block table to write
+    int32_t *table;
+    int cap, window;
     FastDiv by_page, by_heads;
 };
 
@@ -41,6 +44,7 @@ struct Kv4AttnParams : AttnParams {
 };
 
 cudaError_t launch_kv4_append(const Kv4AppendParams &p, cudaStream_t stream);
+// The batch's tokens, or with p.table all keys that they see, laid out for attn_chunk.cuh.
 cudaError_t launch_kv4_read(Kv4ReadParams &p, int num_sms, cudaStream_t stream);
 
 // Keys per unit of the kernel for few rows: a warp's stage holds 4 KB of codes.
@@ -59,7 +63,10 @@ cudaError_t launch_kv4_chunk(const Kv4AttnParams &p, int grid, cudaStream_t stre
 // Sets the units; false where places do not fit.
 bool kv4_set_units(Kv4AttnParams &p);
 size_t kv4_attn_workspace_bytes(int q_heads, int kv_heads, int head_dim, int max_q, int num_sms);
-cudaError_t kv4_attn_dispatch(Kv4AttnParams &p, int max_q, long long max_kv, void *workspace, int num_sms,
+// What a call of these sizes takes beyond that to convert its keys once; 0 where it would not.
+size_t kv4_attn_unpack_bytes(int batch, int group, int kv_heads, int head_dim, int max_q, long long max_kv, int sinks);
+// workspace: as many bytes as kv4_attn_workspace_bytes() says, and `more`.
+cudaError_t kv4_attn_dispatch(Kv4AttnParams &p, int max_q, long long max_kv, void *workspace, size_t more, int num_sms,
                               cudaStream_t stream);
 
 }  // namespace qmm

@@ -40,6 +40,40 @@ constexpr int kUnsplitWork = 12, kWholeWork = 10;
 // sequences 114 and 108).
 constexpr int kFewRows = 16;
 
+// Where keys are converted once, into scratch, and read by the 16-bit form of the kernel for many
+// rows, in place of by every row tile that sees them: it costs a launch and a pass over the keys,
+// and saves some of each tile's time per key.  So from so many row tiles, and so much work, tiles
+// x keys over all heads and sequences, on (us, by every tile and once; D 128):
+//   heads  new  keys    tiles  work      every    once
+//   64/8   128  16384   4      2^19      63.1     70.8
+//   64/8   256  16384   8      2^20      108.6    106.6
+//   8/8    2048 8192    8      2^19      58.5     58.8
+//   8/8    2048 16384   8      2^20      103.5    102.1
+//   64/8   1024 1024    32     2^18      38.5     39.2
+//   32/8   1024 4096    16     2^19      62.8     60.3
+//   32/8   2048 2048    32     2^19      51.9     47.8
+//   8/1    2048 2048    64     2^17      24.1     24.9
+//   8/1    1024 16384   32     2^19      61.1     57.0
+//   64/8   2048 16384   64     2^23      718.7    574.1
+constexpr int kUnpackTiles = 8;
+constexpr long long kUnpackWork = 1LL << 19;
+// Bytes of converted keys at most.
+constexpr long long kUnpackMost = 1LL << 30;
+
+// (keys: what a row tile sees at most)
+bool unpack_pays(int batch, int group, int kv_heads, int max_q, long long keys)
+{
+    const long long rows = 2 * chunk_stream_rows(group);
+    const long long tiles = (static_cast<long long>(max_q) * group + rows - 1) / rows;
+    return tiles >= kUnpackTiles && static_cast<double>(tiles) * keys * kv_heads * batch >= kUnpackWork;
+}
+
+// Places per sequence of the converted keys.
+long long unpack_cap(long long max_kv) { return (max_kv + 127) / 128 * 128; }
+
+// The block table of the converted keys, a page per sequence, before them.
+size_t table_bytes(int batch) { return (static_cast<size_t>(batch) * 4 + 127) / 128 * 128; }
+
 // Blocks of eight warps per item where every item gets a cluster (or block) of its own:
 // clusters of the largest size that all run at once; 0: there are none.
 int cluster_of(const Kv4AttnParams &p, int rows, long long items, long long span, int num_sms)
@@ -60,6 +94,12 @@ size_t scratch_bytes(bool few, int head_dim, int num_sms)
     return g * 32 + 2 * g * rows * (head_dim + 2) * 4;
 }
 
+// (a multiple of 16 bytes; the converted keys follow from a multiple of 128)
+size_t scratch_bytes_most(int head_dim, int num_sms)
+{
+    return (std::max(scratch_bytes(true, head_dim, num_sms), scratch_bytes(false, head_dim, num_sms)) + 127) / 128 * 128;
+}
+
 }  // namespace
 
 bool kv4_set_units(Kv4AttnParams &p)
@@ -77,10 +117,19 @@ bool kv4_set_units(Kv4AttnParams &p)
 
 size_t kv4_attn_workspace_bytes(int, int, int head_dim, int, int num_sms)
 {
-    return std::max(scratch_bytes(true, head_dim, num_sms), scratch_bytes(false, head_dim, num_sms));
+    return scratch_bytes_most(head_dim, num_sms);
 }
 
-cudaError_t kv4_attn_dispatch(Kv4AttnParams &p, int max_q, long long max_kv, void *workspace, int num_sms,
+size_t kv4_attn_unpack_bytes(int batch, int group, int kv_heads, int head_dim, int max_q, long long max_kv, int sinks)
+{
+    if (sinks > 0 || max_kv <= 0 || max_kv > 0x7fffff00LL || group > 128 || batch > 65535 ||
+        !unpack_pays(batch, group, kv_heads, max_q, max_kv))
+        return 0;
+    const double bytes = 4.0 * unpack_cap(max_kv) * kv_heads * head_dim * batch;
+    return bytes > kUnpackMost ? 0 : table_bytes(batch) + static_cast<size_t>(bytes);
+}
+
+cudaError_t kv4_attn_dispatch(Kv4AttnParams &p, int max_q, long long max_kv, void *workspace, size_t more, int num_sms,
                               cudaStream_t stream)
 {
     // no sequence has more tokens than the batch: a caller's large bound adds no row tiles
@@ -127,6 +176,39 @@ cudaError_t kv4_attn_dispatch(Kv4AttnParams &p, int max_q, long long max_kv, voi
     p.meta = reinterpret_cast<int4 *>(ws);
     p.part_ml = reinterpret_cast<float *>(ws + g * 32);
     p.part_o = p.part_ml + 2 * g * (few ? kDecodeRows : kChunkRows) * 2;
+    const size_t unpack = few ? 0 : kv4_attn_unpack_bytes(p.kv.batch, p.group, p.kv.kv_heads, p.kv.head_dim, max_q, max_kv, p.sinks);
+    if (unpack > 0 && unpack <= more && unpack_pays(p.kv.batch, p.group, p.kv.kv_heads, max_q, span)) {
+        Kv4ReadParams u = {};
+        u.kv = p.kv;
+        u.sc = p.sc;
+        u.status = p.status;
+        u.by_page = p.by_page;
+        u.by_heads = fast_div(p.kv.kv_heads);
+        u.cap = static_cast<int>(unpack_cap(max_kv));
+        u.window = p.window;
+        u.table = reinterpret_cast<int32_t *>(ws + scratch_bytes_most(p.kv.head_dim, num_sms));
+        u.k = reinterpret_cast<uint16_t *>(reinterpret_cast<uint8_t *>(u.table) + table_bytes(p.kv.batch));
+        const long long head = static_cast<long long>(u.cap) * p.kv.head_dim, page = head * p.kv.kv_heads;
+        u.v = u.k + page * p.kv.batch;
+        if (const cudaError_t e = launch_kv4_read(u, num_sms, stream); e != cudaSuccess)
+            return e;
+        AttnParams q = p;
+        q.kv.k = u.k;
+        q.kv.v = u.v;
+        q.kv.block_table = u.table;
+        q.kv.page_stride = page;
+        q.kv.slot_stride = p.kv.head_dim;
+        q.kv.head_stride = head;
+        q.kv.num_pages = p.kv.batch;
+        q.kv.page_size = u.cap;
+        q.kv.blocks = 1;
+        q.by_page = fast_div(u.cap);
+        attn_set_tma(q);
+        const cudaError_t e = launch_attn_chunk(q, grid, stream);
+        if (e != cudaSuccess || p.whole)
+            return e;
+        return launch_attn_join(q, grid, false, static_cast<int>(std::min(static_cast<long long>(p.tile_rows), q_rows)), stream);
+    }
     const cudaError_t e = few ? launch_kv4_decode(p, grid, stream) : launch_kv4_chunk(p, grid, stream);
     if (e != cudaSuccess || p.whole)
         return e;

@@ -328,6 +328,7 @@ bool is_weight(const Tensor *t, at::ScalarType dt, int64_t n, c10::DeviceIndex d
 using append4_fn = decltype(&qmm_kv4_append);
 using read4_fn = decltype(&qmm_kv4_read);
 using attn4_fn = decltype(&qmm_kv4_attn);
+using more_fn = decltype(&qmm_kv4_attn_more_workspace);
 
 // kv4_append(fn, k, v, k_cache, v_cache, scales, block_table, cu_q, kv_len, q, q_out, cos_sin,
 //            interleaved, q_norm, k_norm, eps) -> q_out or None; a status (> 0); -1: mismatch
@@ -448,32 +449,32 @@ PyObject *kv4_read(PyObject *, PyObject *const *a, Py_ssize_t n)
     }
 }
 
-// kv4_attn(fn, scratch_fn, q, k_cache, v_cache, scales, block_table, cu_q, kv_len, max_q,
+// kv4_attn(fn, scratch_fn, more_fn, q, k_cache, v_cache, scales, block_table, cu_q, kv_len, max_q,
 //          max_kv, scale, causal, window, sinks, return_lse, out, workspace)
 //   -> out or (out, lse); a status (> 0); -1: mismatch
 PyObject *kv4_attn(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
-    if (n != 18) {
-        PyErr_SetString(PyExc_TypeError, "kv4_attn takes 18 arguments");
+    if (n != 19) {
+        PyErr_SetString(PyExc_TypeError, "kv4_attn takes 19 arguments");
         return nullptr;
     }
     try {
         bool ok = true;
-        const Tensor *q = tensor(a[2], ok), *out = tensor(a[16], ok), *ws = tensor(a[17], ok);
+        const Tensor *q = tensor(a[3], ok), *out = tensor(a[17], ok), *ws = tensor(a[18], ok);
         int max_q, max_kv, window, sinks;
-        const int causal = truth(a[12]), want_lse = truth(a[15]);
-        if (!ok || !q || causal < 0 || want_lse < 0 || q->dim() != 3 || !as_int(a[9], max_q) || !as_int(a[10], max_kv) ||
-            !as_int(a[13], window) || !as_int(a[14], sinks))
+        const int causal = truth(a[13]), want_lse = truth(a[16]);
+        if (!ok || !q || causal < 0 || want_lse < 0 || q->dim() != 3 || !as_int(a[10], max_q) || !as_int(a[11], max_kv) ||
+            !as_int(a[14], window) || !as_int(a[15], sinks))
             return mismatch();
         qmm_paged_kv4 kv;
         c10::DeviceIndex dev;
         const int64_t T = q->size(0), heads = q->size(1), D = q->size(2);
-        if (!fill4(kv, a + 3, T, dev) || kv.head_dim != D || heads > kIntMax)
+        if (!fill4(kv, a + 4, T, dev) || kv.head_dim != D || heads > kIntMax)
             return mismatch();
         const at::ScalarType dt = kv.dtype == QMM_BF16 ? at::kBFloat16 : at::kHalf;
         if (!is_rows(*q, dt, T, D) || q->get_device() != dev)
             return mismatch();
-        const double scale = PyFloat_AsDouble(a[11]);
+        const double scale = PyFloat_AsDouble(a[12]);
         if (scale == -1.0 && PyErr_Occurred()) {
             PyErr_Clear();
             return mismatch();
@@ -494,6 +495,8 @@ PyObject *kv4_attn(PyObject *, PyObject *const *a, Py_ssize_t n)
             bytes = static_cast<size_t>(ws->numel());
         } else {
             bytes = address<scratch_fn>(a[1])(static_cast<int>(heads), kv.kv_heads, static_cast<int>(D), max_q);
+            bytes += address<more_fn>(a[2])(kv.batch, static_cast<int>(heads), kv.kv_heads, static_cast<int>(D), max_q, max_kv,
+                                            sinks);
             scratch = c10::cuda::CUDACachingAllocator::get()->allocate(bytes ? bytes : 16);
         }
         const auto stream = c10::cuda::getCurrentCUDAStream(dev).stream();
@@ -503,7 +506,7 @@ PyObject *kv4_attn(PyObject *, PyObject *const *a, Py_ssize_t n)
             max_kv, ws ? ws->data_ptr() : scratch.get(), bytes, stream);
         if (st != QMM_OK)
             return PyLong_FromLong(st);
-        PyObject *o = out ? a[16] : THPVariable_Wrap(std::move(made));
+        PyObject *o = out ? a[17] : THPVariable_Wrap(std::move(made));
         if (out)
             Py_INCREF(o);
         if (!want_lse || !o)
@@ -530,7 +533,7 @@ PyMethodDef methods[] = {
     {"kv4_read", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(kv4_read)), METH_FASTCALL,
      "kv4_read(fn, k_cache, v_cache, scales, block_table, cu_q, kv_len, tokens, k_out, v_out)"},
     {"kv4_attn", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(kv4_attn)), METH_FASTCALL,
-     "kv4_attn(fn, scratch_fn, q, k_cache, v_cache, scales, block_table, cu_q, kv_len, max_q, max_kv, scale, causal, "
+     "kv4_attn(fn, scratch_fn, more_fn, q, k_cache, v_cache, scales, block_table, cu_q, kv_len, max_q, max_kv, scale, causal, "
      "window, sinks, return_lse, out, workspace)"},
     {nullptr, nullptr, 0, nullptr},
 };

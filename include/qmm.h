@@ -501,6 +501,15 @@ QMM_API qmm_status qmm_kv4_attn(const qmm_paged_kv4 *kv, const void *q, int64_t 
  * upper bound over every batch), or 0 for sizes it does not take. */
 QMM_API size_t qmm_kv4_attn_workspace(int q_heads, int kv_heads, int head_dim, int max_q);
 
+/* Bytes beyond those with which a call of these sizes (max_kv: what it is called with) converts
+ * its keys to 16 bits once, in the workspace, instead of once per 256 query rows: many new
+ * tokens over many keys, without first tokens, up to 1 GB; 0 for other calls and for a max_kv of
+ * 0.  The workspace is then 128-byte aligned.  A call that gets less does without; results differ
+ * by the order of sums at most, under a window.  Keys from max_kv, rounded up to 128, on are
+ * not seen, and QMM_ERR_INDEX is recorded. */
+QMM_API size_t qmm_kv4_attn_more_workspace(int batch, int q_heads, int kv_heads, int head_dim, int max_q, int max_kv,
+                                           int sinks);
+
 /* Synchronizes `stream`, then returns and clears the first device-side error
  * recorded by any qmm kernel on the current device (QMM_OK if none).  A
  * pending asynchronous CUDA error is reported as QMM_ERR_CUDA. */

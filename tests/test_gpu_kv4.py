@@ -88,6 +88,47 @@ def test_split_axes(q, D, batch, n):
     check(q, bt, max_kv=2 ** 31 - 1, max_q=2 ** 31 - 1)
 
 
+# Long prompts: keys converted once in the workspace, against converted by every block, and
+# against the plain form.
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D,heads,ql,kl,page,layout", [
+    (128, (64, 8), [1030], [2100], 16, "hnd"), (64, (32, 4), [600, 3, 0, 1030], [900, 3, 5, 3000], 7, "nhd"),
+    (128, (24, 8), [1300, 1200], [1641, 5000], 48, "gaps")])
+@pytest.mark.parametrize("window,causal", [(0, True), (0, False), (2000, True)])
+def test_keys_converted_once(q, dtype, D, heads, ql, kl, page, layout, window, causal):
+    bt = Batch4(ql, kl, *heads, D, dtype, page=page, layout=layout)
+    more = q.qmm_kv4_attn_more_workspace(len(ql), *heads, D, max(ql), max(kl))
+    assert more >= 4 * len(ql) * max(kl) * heads[1] * D
+    a = check(q, bt, window=window, causal=causal)
+    ws = torch.empty(q.qmm_kv4_attn_workspace(*heads, D, max(ql)), dtype=torch.uint8, device="cuda")
+    b = q.qmm_kv4_attn(bt.q, *bt.args(), max(ql), max(kl), window=window, causal=causal, workspace=ws)
+    assert status(q) == 0
+    if not window:
+        assert torch.equal(a, b)
+    ref, tol, _, _ = attention4(bt, None, causal, window)
+    assert ((b.double() - ref).abs() <= tol).all()
+    # a workspace of the caller's, aligned to less than the converted keys need
+    full = torch.empty(ws.numel() + more + 16, dtype=torch.uint8, device="cuda")
+    for at in (0, 16):
+        full.fill_(255)
+        c = q.qmm_kv4_attn(bt.q, *bt.args(), max(ql), max(kl), window=window, causal=causal, workspace=full[at:])
+        assert status(q) == 0 and torch.equal(c, a if at == 0 else b)
+
+
+def test_longer_than_max_kv_is_recorded(q):
+    bt = Batch4([1100], [2500], 64, 8, 128, "bf16")
+    assert q.qmm_kv4_attn_more_workspace(1, 64, 8, 128, 1100, 1920) > 0
+    q.qmm_kv4_attn(bt.q, *bt.args(), 1100, 4000)
+    assert status(q) == 0
+    # than the table
+    short = q.qmm_kv4_attn(bt.q, *bt.args()[:3], bt.table[:, :120].contiguous(), *bt.args()[4:], 1100, 4000)
+    assert status(q) == 10 and torch.isfinite(short).all()
+    # than max_kv
+    assert q.qmm_kv4_attn_more_workspace(1, 64, 8, 128, 1100, 2300) > 0
+    q.qmm_kv4_attn(bt.q, *bt.args(), 1100, 2300)
+    assert status(q) == 10
+
+
 def test_padding(q):
     bt = Batch4([1, 0, 2, 1], [0, 5, 1, 50], 8, 2, 128, "bf16", extra_blocks=3)
     check(q, bt, pad=5)

@@ -119,6 +119,13 @@ def test_workspace_sizes_refused(lib):
         assert lib.qmm_kv4_attn_workspace(*a) == 0
 
 
+def test_more_workspace(lib):
+    assert lib.qmm_kv4_attn_more_workspace(0, 32, 8, 128, 2048, 2048, 0) == 0
+    assert lib.qmm_kv4_attn_more_workspace(1, 32, 7, 128, 2048, 2048, 0) == 0
+    with pytest.raises(ValueError, match="32 bits"):
+        q.qmm_kv4_attn_more_workspace(1, 32, 8, 128, 2048, 2 ** 31)
+
+
 def cpu_batch():
     i = torch.zeros(1, dtype=torch.int32)
     return (torch.zeros(2, 16, 2, 32, dtype=torch.uint8), torch.zeros(2, 16, 2, 32, dtype=torch.uint8),

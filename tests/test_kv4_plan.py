@@ -29,8 +29,9 @@ def plan(tmp_path_factory):
                    check=True, capture_output=True)
 
     def run(batches):
-        """Launches of (batch, tokens, q_heads, kv_heads, D, page, blocks, window, sinks, max_q, max_kv, q_map)."""
-        text = "".join(" ".join(str(int(v)) for v in b) + "\n" for b in batches)
+        """Launches of (batch, tokens, q_heads, kv_heads, D, page, blocks, window, sinks, max_q, max_kv, q_map), with
+        the scratch to convert keys once where a 13th number says so."""
+        text = "".join(" ".join(str(int(v)) for v in (*b, 0)[:13]) + "\n" for b in batches)
         out = subprocess.run([exe], input=text, capture_output=True, text=True, check=True).stdout.splitlines()
         assert len(out) == 2 * len(batches)
         return [Launch(*map(int, out[2 * i].split()), int(out[2 * i + 1])) for i in range(len(batches))]
@@ -64,6 +65,16 @@ def test_queries_without_a_tensor_map(plan):
     assert a.few and b.few
 
 
+# Keys are converted once for long prompts without first tokens, where there is scratch.
+def test_converted_keys(plan):
+    prompt = (1, 2048, 32, 8, 128, 16, 128, 0, 0, 2048, 2048, 1)
+    got = plan([prompt, (*prompt, 1), (*prompt[:7], 1990, 0, *prompt[9:], 1), (*prompt[:7], 100, 0, *prompt[9:], 1),
+                (*prompt[:7], 1990, 4, *prompt[9:], 1),
+                (*prompt[:9], 100, 2048, 1, 1), (*prompt[:10], 0, 1, 1)])
+    assert [p.few for p in got] == [0, 2, 2, 0, 0, 0, 0]
+    assert got[1].scratch - got[0].scratch >= 2 * 2 * 2048 * 8 * 128
+
+
 # Partial results stay inside the scratch that is asked for, and numbers in their ranges,
 # whatever the batch.
 def test_scratch_and_ranges(plan):
@@ -82,12 +93,15 @@ def test_scratch_and_ranges(plan):
         max_kv = r.choice([0, 1, 100, 10000, INT_MAX])
         if (min(max_q, tokens) * group // 8 + 1) * batch > INT_MAX or tokens * group > INT_MAX:
             continue
-        batches.append((batch, tokens, hk * group, hk, r.choice([64, 128]), page, blocks, window, sinks, max_q, max_kv, 1))
-    for b, p in zip(batches, plan(batches)):
-        assert p.part_end <= p.scratch, b
+        batches.append((batch, tokens, hk * group, hk, r.choice([64, 128]), page, blocks, window, sinks, max_q, max_kv, 1,
+                        r.choice([0, 1])))
+    plans = plan(batches)
+    assert {p.few for p in plans} == {0, 1, 2}
+    for b, p in zip(batches, plans):
+        assert 0 <= p.part_end <= p.scratch, b
         assert 1 <= p.grid <= INT_MAX and p.cluster in (1, 2, 4, 8), b
         assert p.row_tiles * p.tile_rows >= min(max(b[9], 1), b[1]) * (b[2] // b[3]), b
-        if p.few:
+        if p.few == 1:
             assert p.tile_rows in (8, 16) and p.warps in (4, 8) and (p.cluster == 1 or p.warps == 8), b
         else:
             assert p.tile_rows <= 256 and p.tile_rows % (b[2] // b[3]) == 0, b
