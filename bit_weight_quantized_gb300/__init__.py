@@ -73,7 +73,7 @@ SIGNATURES = {
     "qmm_kv4_read": ([_P, _P, _P, _P], _I),
     "qmm_kv4_attn": ([_P, _P, _L, _I, _F, _I, _I, _I, _P, _P, _I, _I, _P, _SZ, _P], _I),
     "qmm_kv4_attn_workspace": ([_I, _I, _I, _I], _SZ),
-    "qmm_kv4_attn_more_workspace": ([_I, _I, _I, _I, _I, _I, _I], _SZ),
+    "qmm_kv4_attn_more_workspace": ([_I, _I, _I, _I, _I, _I, _I, _I], _SZ),
     "qmm_device_status": ([_P], _I),
     "qmm_watchdog_selftest": ([_P], _I),
     "qmm_status_string": ([_I], ctypes.c_char_p),
@@ -739,12 +739,12 @@ def qmm_kv4_attn_workspace(q_heads: int, kv_heads: int, head_dim: int, max_q: in
     return int(load().qmm_kv4_attn_workspace(q_heads, kv_heads, head_dim, max_q))
 
 
-def qmm_kv4_attn_more_workspace(batch: int, q_heads: int, kv_heads: int, head_dim: int, max_q: int, max_kv: int,
-                                sinks: int = 0) -> int:
+def qmm_kv4_attn_more_workspace(batch: int, tokens: int, q_heads: int, kv_heads: int, head_dim: int, max_q: int,
+                                max_kv: int, sinks: int = 0) -> int:
     """Bytes beyond qmm_kv4_attn_workspace() with which a qmm_kv4_attn call of these sizes
     converts its keys once (0: such a call has no use for more)."""
-    _int32(batch=batch, q_heads=q_heads, kv_heads=kv_heads, head_dim=head_dim, max_q=max_q, max_kv=max_kv, sinks=sinks)
-    return int(load().qmm_kv4_attn_more_workspace(batch, q_heads, kv_heads, head_dim, max_q, max_kv, sinks))
+    _int32(batch=batch, tokens=tokens, q_heads=q_heads, kv_heads=kv_heads, head_dim=head_dim, max_q=max_q, max_kv=max_kv, sinks=sinks)
+    return int(load().qmm_kv4_attn_more_workspace(batch, tokens, q_heads, kv_heads, head_dim, max_q, max_kv, sinks))
 
 
 def qmm_kv4_attn(q, k_cache, v_cache, scales, block_table, cu_q, kv_len, max_q, max_kv=0, scale=None, causal=True,
@@ -774,9 +774,15 @@ def qmm_kv4_attn(q, k_cache, v_cache, scales, block_table, cu_q, kv_len, max_q, 
     lse = torch.empty((T, heads), dtype=torch.float32, device=q.device) if return_lse else None
     with torch.cuda.device(q.device):
         if workspace is None:
-            nbytes = qmm_kv4_attn_workspace(heads, k_cache.shape[2], D, max_q)
-            nbytes += qmm_kv4_attn_more_workspace(kv_len.shape[0], heads, k_cache.shape[2], D, max_q, max_kv, sinks)
-            workspace = torch.empty(max(nbytes, 16), dtype=_U8, device=q.device)
+            hk = k_cache.shape[2]
+            nbytes = qmm_kv4_attn_workspace(heads, hk, D, max_q)
+            more = qmm_kv4_attn_more_workspace(kv_len.shape[0], T, heads, hk, D, max_q, max_kv, sinks)
+            try:
+                workspace = torch.empty(max(nbytes + more, 16), dtype=_U8, device=q.device)
+            except torch.OutOfMemoryError:
+                if more == 0:
+                    raise
+                workspace = torch.empty(nbytes, dtype=_U8, device=q.device)   # it does without
         _dev(workspace, "workspace", _U8)
         for name, t in (("out", out), ("workspace", workspace)):
             if t.device != q.device:

@@ -923,11 +923,12 @@ size_t qmm_kv4_attn_workspace(int q_heads, int kv_heads, int head_dim, int max_q
     return kv4_attn_workspace_bytes(q_heads, kv_heads, head_dim, max_q, f->num_sms);
 }
 
-size_t qmm_kv4_attn_more_workspace(int batch, int q_heads, int kv_heads, int head_dim, int max_q, int max_kv, int sinks)
+size_t qmm_kv4_attn_more_workspace(int batch, int tokens, int q_heads, int kv_heads, int head_dim, int max_q, int max_kv,
+                                   int sinks)
 {
-    if (batch < 1 || sinks < 0 || max_kv < 0 || qmm_kv4_attn_workspace(q_heads, kv_heads, head_dim, max_q) == 0)
+    if (batch < 1 || tokens < 1 || sinks < 0 || max_kv < 0 || qmm_kv4_attn_workspace(q_heads, kv_heads, head_dim, max_q) == 0)
         return 0;
-    return kv4_attn_unpack_bytes(batch, q_heads / kv_heads, kv_heads, head_dim, max_q, max_kv, sinks);
+    return kv4_attn_unpack_bytes(batch, tokens, q_heads / kv_heads, kv_heads, head_dim, max_q, max_kv, sinks);
 }
 
 qmm_status qmm_kv4_attn(const qmm_paged_kv4 *kv, const void *q, int64_t q_stride, int q_heads, float scale, int causal,

@@ -64,7 +64,8 @@ cudaError_t launch_kv4_chunk(const Kv4AttnParams &p, int grid, cudaStream_t stre
 bool kv4_set_units(Kv4AttnParams &p);
 size_t kv4_attn_workspace_bytes(int q_heads, int kv_heads, int head_dim, int max_q, int num_sms);
 // What a call of these sizes takes beyond that to convert its keys once; 0 where it would not.
-size_t kv4_attn_unpack_bytes(int batch, int group, int kv_heads, int head_dim, int max_q, long long max_kv, int sinks);
+size_t kv4_attn_unpack_bytes(int batch, int tokens, int group, int kv_heads, int head_dim, int max_q, long long max_kv,
+                             int sinks);
 // workspace: as many bytes as kv4_attn_workspace_bytes() says, and `more`.
 cudaError_t kv4_attn_dispatch(Kv4AttnParams &p, int max_q, long long max_kv, void *workspace, size_t more, int num_sms,
                               cudaStream_t stream);

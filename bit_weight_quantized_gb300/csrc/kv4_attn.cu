@@ -60,12 +60,13 @@ constexpr long long kUnpackWork = 1LL << 19;
 // Bytes of converted keys at most.
 constexpr long long kUnpackMost = 1LL << 30;
 
-// (keys: what a row tile sees at most)
-bool unpack_pays(int batch, int group, int kv_heads, int max_q, long long keys)
+// (Row tiles per sequence on average: a prompt beside many sequences of a token each would have
+// all their keys converted for few rows.  keys: what a row tile sees at most.)
+bool unpack_pays(int batch, int tokens, int group, int kv_heads, int max_q, long long keys)
 {
-    const long long rows = 2 * chunk_stream_rows(group);
-    const long long tiles = (static_cast<long long>(max_q) * group + rows - 1) / rows;
-    return tiles >= kUnpackTiles && static_cast<double>(tiles) * keys * kv_heads * batch >= kUnpackWork;
+    const double rows = 2 * chunk_stream_rows(group);
+    const double tiles = std::min(static_cast<double>(max_q), static_cast<double>(tokens) / batch) * group / rows;
+    return tiles > kUnpackTiles - 1 && tiles * static_cast<double>(keys) * kv_heads * batch >= kUnpackWork;
 }
 
 // Places per sequence of the converted keys.
@@ -120,10 +121,10 @@ size_t kv4_attn_workspace_bytes(int, int, int head_dim, int, int num_sms)
     return scratch_bytes_most(head_dim, num_sms);
 }
 
-size_t kv4_attn_unpack_bytes(int batch, int group, int kv_heads, int head_dim, int max_q, long long max_kv, int sinks)
+size_t kv4_attn_unpack_bytes(int batch, int tokens, int group, int kv_heads, int head_dim, int max_q, long long max_kv, int sinks)
 {
     if (sinks > 0 || max_kv <= 0 || max_kv > 0x7fffff00LL || group > 128 || batch > 65535 ||
-        !unpack_pays(batch, group, kv_heads, max_q, max_kv))
+        !unpack_pays(batch, tokens, group, kv_heads, max_q, max_kv))
         return 0;
     const double bytes = 4.0 * unpack_cap(max_kv) * kv_heads * head_dim * batch;
     return bytes > kUnpackMost ? 0 : table_bytes(batch) + static_cast<size_t>(bytes);
@@ -176,8 +177,9 @@ cudaError_t kv4_attn_dispatch(Kv4AttnParams &p, int max_q, long long max_kv, voi
     p.meta = reinterpret_cast<int4 *>(ws);
     p.part_ml = reinterpret_cast<float *>(ws + g * 32);
     p.part_o = p.part_ml + 2 * g * (few ? kDecodeRows : kChunkRows) * 2;
-    const size_t unpack = few ? 0 : kv4_attn_unpack_bytes(p.kv.batch, p.group, p.kv.kv_heads, p.kv.head_dim, max_q, max_kv, p.sinks);
-    if (unpack > 0 && unpack <= more && unpack_pays(p.kv.batch, p.group, p.kv.kv_heads, max_q, span)) {
+    const size_t unpack = few ? 0 : kv4_attn_unpack_bytes(p.kv.batch, p.kv.tokens, p.group, p.kv.kv_heads, p.kv.head_dim,
+                                                              max_q, max_kv, p.sinks);
+    if (unpack > 0 && unpack <= more && unpack_pays(p.kv.batch, p.kv.tokens, p.group, p.kv.kv_heads, max_q, span)) {
         Kv4ReadParams u = {};
         u.kv = p.kv;
         u.sc = p.sc;

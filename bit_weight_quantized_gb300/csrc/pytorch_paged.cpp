@@ -495,9 +495,17 @@ PyObject *kv4_attn(PyObject *, PyObject *const *a, Py_ssize_t n)
             bytes = static_cast<size_t>(ws->numel());
         } else {
             bytes = address<scratch_fn>(a[1])(static_cast<int>(heads), kv.kv_heads, static_cast<int>(D), max_q);
-            bytes += address<more_fn>(a[2])(kv.batch, static_cast<int>(heads), kv.kv_heads, static_cast<int>(D), max_q, max_kv,
-                                            sinks);
-            scratch = c10::cuda::CUDACachingAllocator::get()->allocate(bytes ? bytes : 16);
+            const size_t more = address<more_fn>(a[2])(kv.batch, kv.tokens, static_cast<int>(heads), kv.kv_heads,
+                                                       static_cast<int>(D), max_q, max_kv, sinks);
+            auto *allocator = c10::cuda::CUDACachingAllocator::get();
+            try {
+                scratch = allocator->allocate(bytes + more ? bytes + more : 16);
+                bytes += more;
+            } catch (const c10::OutOfMemoryError &) {
+                if (more == 0)
+                    throw;
+                scratch = allocator->allocate(bytes);   // it does without
+            }
         }
         const auto stream = c10::cuda::getCurrentCUDAStream(dev).stream();
         const qmm_status st = address<attn4_fn>(a[0])(

@@ -503,12 +503,12 @@ QMM_API size_t qmm_kv4_attn_workspace(int q_heads, int kv_heads, int head_dim, i
 
 /* Bytes beyond those with which a call of these sizes (max_kv: what it is called with) converts
  * its keys to 16 bits once, in the workspace, instead of once per 256 query rows: many new
- * tokens over many keys, without first tokens, up to 1 GB; 0 for other calls and for a max_kv of
- * 0.  The workspace is then 128-byte aligned.  A call that gets less does without; results differ
+ * tokens (of the batch's `tokens`, over all sequences) over many keys, without first tokens, up
+ * to 1 GB; 0 for other calls and for a max_kv of 0.  The workspace is then 128-byte aligned.  A call that gets less does without; results differ
  * by the order of sums at most, under a window.  Keys from max_kv, rounded up to 128, on are
  * not seen, and QMM_ERR_INDEX is recorded. */
-QMM_API size_t qmm_kv4_attn_more_workspace(int batch, int q_heads, int kv_heads, int head_dim, int max_q, int max_kv,
-                                           int sinks);
+QMM_API size_t qmm_kv4_attn_more_workspace(int batch, int tokens, int q_heads, int kv_heads, int head_dim,
+                                           int max_q, int max_kv, int sinks);
 
 /* Synchronizes `stream`, then returns and clears the first device-side error
  * recorded by any qmm kernel on the current device (QMM_OK if none).  A

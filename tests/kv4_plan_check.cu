@@ -80,7 +80,7 @@ int main()
         p.causal = 1;
         p.window = window;
         p.sinks = sinks;
-        const size_t extra = more ? kv4_attn_unpack_bytes(batch, p.group, hk, D, max_q, max_kv, sinks) : 0;
+        const size_t extra = more ? kv4_attn_unpack_bytes(batch, tokens, p.group, hk, D, max_q, max_kv, sinks) : 0;
         kv4_attn_dispatch(p, max_q, max_kv, nullptr, extra, 152, nullptr);
         std::printf("%zu\n", kv4_attn_workspace_bytes(hq, hk, D, max_q, 152) + extra);
     }

@@ -94,10 +94,10 @@ def test_split_axes(q, D, batch, n):
 @pytest.mark.parametrize("D,heads,ql,kl,page,layout", [
     (128, (64, 8), [1030], [2100], 16, "hnd"), (64, (32, 4), [600, 3, 0, 1030], [900, 3, 5, 3000], 7, "nhd"),
     (128, (24, 8), [1300, 1200], [1641, 5000], 48, "gaps")])
-@pytest.mark.parametrize("window,causal", [(0, True), (0, False), (2000, True)])
+@pytest.mark.parametrize("window,causal", [(0, True), (0, False), (2700, True)])
 def test_keys_converted_once(q, dtype, D, heads, ql, kl, page, layout, window, causal):
     bt = Batch4(ql, kl, *heads, D, dtype, page=page, layout=layout)
-    more = q.qmm_kv4_attn_more_workspace(len(ql), *heads, D, max(ql), max(kl))
+    more = q.qmm_kv4_attn_more_workspace(len(ql), sum(ql), *heads, D, max(ql), max(kl))
     assert more >= 4 * len(ql) * max(kl) * heads[1] * D
     a = check(q, bt, window=window, causal=causal)
     ws = torch.empty(q.qmm_kv4_attn_workspace(*heads, D, max(ql)), dtype=torch.uint8, device="cuda")
@@ -115,16 +115,45 @@ def test_keys_converted_once(q, dtype, D, heads, ql, kl, page, layout, window, c
         assert status(q) == 0 and torch.equal(c, a if at == 0 else b)
 
 
+# A prompt beside sequences of a token: its keys alone would be worth it.
+def test_keys_of_mixed_batches_stay(q):
+    assert q.qmm_kv4_attn_more_workspace(1, 2048, 64, 8, 128, 2048, 8192) > 0
+    assert q.qmm_kv4_attn_more_workspace(16, 2048 + 15, 64, 8, 128, 2048, 8192) == 0
+
+
+# Where memory is short, a call does without the scratch for converted keys.
+@pytest.mark.parametrize("fast", [True, False])
+def test_converted_keys_without_memory(q, fast, monkeypatch):
+    if not fast:
+        monkeypatch.setattr(q, "_fast_kv4_attn", None)
+    bt = Batch4([1030], [8000], 64, 8, 128, "bf16")
+    want = q.qmm_kv4_attn(bt.q, *bt.args(), 1030, 8000)
+    more = q.qmm_kv4_attn_more_workspace(1, 1030, 64, 8, 128, 1030, 8000)
+    base = q.qmm_kv4_attn_workspace(64, 8, 128, 1030)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    total = torch.cuda.get_device_properties(0).total_memory
+    try:
+        room = torch.cuda.memory_reserved() + want.nbytes + base + more // 2
+        torch.cuda.set_per_process_memory_fraction(room / total)
+        got = q.qmm_kv4_attn(bt.q, *bt.args(), 1030, 8000)
+        with pytest.raises(torch.OutOfMemoryError):
+            torch.empty(base + more, dtype=torch.uint8, device="cuda")
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    assert status(q) == 0 and torch.equal(got, want)
+
+
 def test_longer_than_max_kv_is_recorded(q):
     bt = Batch4([1100], [2500], 64, 8, 128, "bf16")
-    assert q.qmm_kv4_attn_more_workspace(1, 64, 8, 128, 1100, 1920) > 0
+    assert q.qmm_kv4_attn_more_workspace(1, 1100, 64, 8, 128, 1100, 1920) > 0
     q.qmm_kv4_attn(bt.q, *bt.args(), 1100, 4000)
     assert status(q) == 0
     # than the table
     short = q.qmm_kv4_attn(bt.q, *bt.args()[:3], bt.table[:, :120].contiguous(), *bt.args()[4:], 1100, 4000)
     assert status(q) == 10 and torch.isfinite(short).all()
     # than max_kv
-    assert q.qmm_kv4_attn_more_workspace(1, 64, 8, 128, 1100, 2300) > 0
+    assert q.qmm_kv4_attn_more_workspace(1, 1100, 64, 8, 128, 1100, 2300) > 0
     q.qmm_kv4_attn(bt.q, *bt.args(), 1100, 2300)
     assert status(q) == 10
 

@@ -120,10 +120,10 @@ def test_workspace_sizes_refused(lib):
 
 
 def test_more_workspace(lib):
-    assert lib.qmm_kv4_attn_more_workspace(0, 32, 8, 128, 2048, 2048, 0) == 0
-    assert lib.qmm_kv4_attn_more_workspace(1, 32, 7, 128, 2048, 2048, 0) == 0
+    assert lib.qmm_kv4_attn_more_workspace(0, 2048, 32, 8, 128, 2048, 2048, 0) == 0
+    assert lib.qmm_kv4_attn_more_workspace(1, 2048, 32, 7, 128, 2048, 2048, 0) == 0
     with pytest.raises(ValueError, match="32 bits"):
-        q.qmm_kv4_attn_more_workspace(1, 32, 8, 128, 2048, 2 ** 31)
+        q.qmm_kv4_attn_more_workspace(1, 2048, 32, 8, 128, 2048, 2 ** 31)
 
 
 def cpu_batch():

@@ -70,8 +70,8 @@ def test_converted_keys(plan):
     prompt = (1, 2048, 32, 8, 128, 16, 128, 0, 0, 2048, 2048, 1)
     got = plan([prompt, (*prompt, 1), (*prompt[:7], 1990, 0, *prompt[9:], 1), (*prompt[:7], 100, 0, *prompt[9:], 1),
                 (*prompt[:7], 1990, 4, *prompt[9:], 1),
-                (*prompt[:9], 100, 2048, 1, 1), (*prompt[:10], 0, 1, 1)])
-    assert [p.few for p in got] == [0, 2, 2, 0, 0, 0, 0]
+                (*prompt[:9], 100, 2048, 1, 1), (*prompt[:10], 0, 1, 1), (16, 2063, *prompt[2:], 1)])
+    assert [p.few for p in got] == [0, 2, 2, 0, 0, 0, 0, 0]
     assert got[1].scratch - got[0].scratch >= 2 * 2 * 2048 * 8 * 128
 
 
