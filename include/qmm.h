@@ -490,8 +490,9 @@ QMM_API qmm_status qmm_kv4_read(const qmm_paged_kv4 *kv, void *k_out, void *v_ou
  * Queries must be finite (a NaN or an infinity makes its row NaN), in bf16 below 2^116;
  * bf16 values below 2^-80 lose bits.
  * Scores, maximum, sums and output are fp32.  Up to 16 query rows per key head (q_heads /
- * kv_heads * new tokens) the codes are multiplied as they are and the weights rounded to
- * fp16 once; for more the values, exact in dtype, are, and the weights are rounded to dtype.
+ * kv_heads * new tokens), and more in small batches, the codes are multiplied as they are and
+ * the weights rounded to fp16 once; for more the values, exact in dtype, are, and the weights
+ * are rounded to dtype.
  * Everything else, the workspace (qmm_kv4_attn_workspace) among it, is qmm_paged_attn's. */
 QMM_API qmm_status qmm_kv4_attn(const qmm_paged_kv4 *kv, const void *q, int64_t q_stride, int q_heads, float scale,
                                 int causal, int window, int sinks, void *out, float *lse, int max_q, int max_kv,
