@@ -115,6 +115,30 @@ def test_keys_converted_once(q, dtype, D, heads, ql, kl, page, layout, window, c
         assert status(q) == 0 and torch.equal(c, a if at == 0 else b)
 
 
+# Captured: every replay converts the keys that lie in the cache then, for two calls that share
+# their workspace and on another stream than the capture's.
+def test_converted_keys_in_a_graph(q):
+    bt, other = Batch4([1030], [2100], 64, 8, 128, "bf16"), Batch4([1030], [2100], 64, 8, 128, "bf16", seed=5)
+    more = q.qmm_kv4_attn_more_workspace(1, 1030, 64, 8, 128, 1030, 2100)
+    ws = torch.empty(q.qmm_kv4_attn_workspace(64, 8, 128, 1030) + more, dtype=torch.uint8, device="cuda")
+    run = lambda b: q.qmm_kv4_attn(b.q, *b.args(), 1030, 2100, workspace=ws)
+    want = [run(b) for b in (bt, other)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = [run(b) for b in (bt, other)]
+    graph.replay()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    for a, b in ((bt.k_cache, other.k_cache), (bt.v_cache, other.v_cache), (bt.scales, other.scales), (bt.q, other.q),
+                 (bt.table, other.table)):
+        a.copy_(b)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        graph.replay()
+    side.synchronize()
+    assert status(q) == 0 and torch.equal(got[0], want[1]) and torch.equal(got[1], want[1])
+
+
 # A prompt beside sequences of a token: its keys alone would be worth it.
 def test_keys_of_mixed_batches_stay(q):
     assert q.qmm_kv4_attn_more_workspace(1, 2048, 64, 8, 128, 2048, 8192) > 0
