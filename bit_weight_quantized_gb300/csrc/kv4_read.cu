@@ -16,65 +16,18 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMostRows = 8;                             // tokens per block
-constexpr int kFlight = 2;                               // loads in flight per thread
+constexpr int kFlight = 2, kAhead = 4;                   // loads in flight per thread
 
 struct Place {
     long long codes, scales;                             // offsets of (page, slot), -1: nothing to read
 };
 
-// All heads' keys and values of `rows` places to rows of D, by the whole block.
-template <int D, bool BF16, typename F>
-__device__ __forceinline__ void convert(const Kv4ReadParams &p, const Place *places, int rows, F row_of)
-{
-    constexpr int kPieces = D / 16;                      // of a head
-    constexpr int kGroups = D / kKv4Group;
-    const qmm_paged_kv &kv = p.kv;
-    // pieces of a token, 16 codes: [key, value][head][piece]
-    const int all = rows * 2 * kv.kv_heads * kPieces;
-    const int piece = threadIdx.x % kPieces;
-    for (int e0 = threadIdx.x; e0 < all; e0 += kFlight * kThreads) {
-        uint2 w[kFlight];
-        uint32_t pattern[kFlight];
-        uint16_t *dst[kFlight];
-#pragma unroll
-        for (int u = 0; u < kFlight; ++u) {
-            const int e = e0 + u * kThreads;
-            dst[u] = nullptr;
-            w[u] = make_uint2(0u, 0u);
-            pattern[u] = 0;
-            if (e < all) {
-                const int row = p.by_heads(e / kPieces), i = row >> 1, head = e / kPieces - row * kv.kv_heads;
-                const bool is_v = row & 1;
-                const Place at = places[i];
-                if (at.codes >= 0) {
-                    const uint8_t *src = static_cast<const uint8_t *>(is_v ? kv.v : kv.k) + at.codes + head * kv.head_stride;
-                    w[u] = __ldcs(reinterpret_cast<const uint2 *>(src) + piece);
-                    pattern[u] = p.sc.base[at.scales + head * p.sc.head + (is_v ? kGroups : 0) + piece / 4];
-                    dst[u] = row_of(i, head, is_v) + 16 * piece;
-                }
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < kFlight; ++u)
-            if (dst[u]) {
-                const GroupScale<BF16> sc(pattern[u]);
-                const uint4 a = sc.values(w[u].x), b = sc.values(w[u].y);
-                if (p.wide) {
-                    asm volatile("st.global.cs.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst[u]), "r"(a.x),
-                                 "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
-                                 : "memory");
-                } else {
-                    reinterpret_cast<uint4 *>(dst[u])[0] = a;
-                    reinterpret_cast<uint4 *>(dst[u])[1] = b;
-                }
-            }
-    }
-}
-
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreads)
 kv4_read_kernel(const __grid_constant__ Kv4ReadParams p)
 {
+    constexpr int kPieces = D / 16;                      // of a head
+    constexpr int kGroups = D / kKv4Group;
     __shared__ Place places[kMostRows];
     if (threadIdx.x == 0)
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -101,50 +54,121 @@ kv4_read_kernel(const __grid_constant__ Kv4ReadParams p)
         }
     }
     __syncthreads();
-    convert<D, BF16>(p, places, rows, [&](int i, int head, bool is_v) {
-        return (is_v ? p.v : p.k) + (static_cast<long long>(t0 + i) * kv.kv_heads + head) * D;
-    });
+    // pieces of a token, 16 codes: [key, value][head][piece]
+    const int all = rows * 2 * kv.kv_heads * kPieces;
+    const int piece = threadIdx.x % kPieces;
+    for (int e0 = threadIdx.x; e0 < all; e0 += kFlight * kThreads) {
+        uint2 w[kFlight];
+        uint32_t pattern[kFlight];
+        uint16_t *dst[kFlight];
+#pragma unroll
+        for (int u = 0; u < kFlight; ++u) {
+            const int e = e0 + u * kThreads;
+            dst[u] = nullptr;
+            w[u] = make_uint2(0u, 0u);
+            pattern[u] = 0;
+            if (e < all) {
+                const int row = p.by_heads(e / kPieces), i = row >> 1, head = e / kPieces - row * kv.kv_heads;
+                const bool is_v = row & 1;
+                const Place at = places[i];
+                if (at.codes >= 0) {
+                    const uint8_t *src = static_cast<const uint8_t *>(is_v ? kv.v : kv.k) + at.codes + head * kv.head_stride;
+                    w[u] = __ldcs(reinterpret_cast<const uint2 *>(src) + piece);
+                    pattern[u] = p.sc.base[at.scales + head * p.sc.head + (is_v ? kGroups : 0) + piece / 4];
+                    dst[u] = (is_v ? p.v : p.k) + (static_cast<long long>(t0 + i) * kv.kv_heads + head) * D + 16 * piece;
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kFlight; ++u)
+            if (dst[u]) {
+                const GroupScale<BF16> sc(pattern[u]);
+                const uint4 a = sc.values(w[u].x), b = sc.values(w[u].y);
+                if (p.wide) {
+                    asm volatile("st.global.cs.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst[u]), "r"(a.x),
+                                 "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                                 : "memory");
+                } else {
+                    reinterpret_cast<uint4 *>(dst[u])[0] = a;
+                    reinterpret_cast<uint4 *>(dst[u])[1] = b;
+                }
+            }
+    }
 }
 
-// The keys of a sequence that the call's new tokens see, in 16 bits: blocks (x, y) take p.rows
+// The keys of a sequence that the call's new tokens see, in 16 bits: blocks (x, y) take kMostRows
 // keys of sequence y at a time.  Keys lie [sequence][head][p.cap keys][D], a page per sequence to
-// attn_chunk.cuh, whose block table is written here, too.
+// attn_chunk.cuh, whose block table is written here, too.  A thread keeps a key and a piece of 16
+// values and goes through the heads.  Bound by latency (lengths and page, codes, stores: 16.6 us
+// for 16384 keys of 8 heads alone, where memory would take 3 and L2 10); with the lengths, then
+// the page, then two loads at a time 17.4.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreads)
 kv4_unpack_kernel(const __grid_constant__ Kv4ReadParams p)
 {
-    __shared__ Place places[kMostRows];
+    constexpr int kPieces = D / 16, kGroups = D / kKv4Group;
+    constexpr int kSide = kThreads / (kPieces * kMostRows);          // heads side by side
     if (threadIdx.x == 0)
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const qmm_paged_kv &kv = p.kv;
-    const int b = blockIdx.y;
+    const int b = blockIdx.y, heads = kv.kv_heads;
     if (blockIdx.x == 0 && threadIdx.x == 0)
         p.table[b] = b;
+    // (pages are looked up beside the lengths, and ahead)
+    const int piece = threadIdx.x % kPieces, side = threadIdx.x / (kPieces * kMostRows), most = table_keys(kv);
+    const long long step = static_cast<long long>(gridDim.x) * kMostRows;
+    const int32_t *row = kv.block_table + static_cast<long long>(b) * kv.blocks;
+    auto page_of = [&](long long key) { return key < most ? row[p.by_page(static_cast<int>(key))] : -1; };
+    long long key = static_cast<long long>(blockIdx.x) * kMostRows + threadIdx.x / kPieces % kMostRows;
     const int count = kv.kv_len[b], tokens = seq_tokens(kv, b).y;
+    if (p.window > 0)
+        key += window_start(min(max(count, 0), p.cap) - tokens, p.window);
+    int page = page_of(key), next;
     if (tokens == 0)
         return;
-    // (zeros for keys past the table: the length that is wrong is recorded, and what follows
-    // reads nothing but what was written here)
+    // (zeros for keys past the table and of pages that are not there: what is wrong is recorded,
+    // and what follows reads nothing but what was written here)
     const int known = seq_keys(kv, count, p.status), keys = min(count, p.cap);
-    const int lo = p.window > 0 ? window_start(keys - tokens, p.window) : 0;
-    for (long long from = lo + static_cast<long long>(blockIdx.x) * p.rows; from < keys; from += static_cast<long long>(gridDim.x) * p.rows) {
-        const int key0 = static_cast<int>(from), rows = min(p.rows, keys - key0);
-        __syncthreads();                                 // the last keys' places have been read
-        if (static_cast<int>(threadIdx.x) < rows) {
-            Place at = {-1, -1};
-            int page, slot;
-            const int key = key0 + threadIdx.x;
-            if (key < known && find_slot(kv, p.by_page, b, key, p.status, page, slot)) {
-                at.codes = page * kv.page_stride + slot * kv.slot_stride;
-                at.scales = scale_offset(p.sc, page, slot);
-            }
-            places[threadIdx.x] = at;
+    for (; key < keys; key += step, page = next) {
+        next = page_of(key + step);
+        bool in = key < known;
+        if (in && (page < 0 || page >= kv.num_pages)) {
+            record_error(p.status, QMM_ERR_INDEX);
+            in = false;
         }
-        __syncthreads();
-        convert<D, BF16>(p, places, rows, [&](int i, int head, bool is_v) {
-            return (is_v ? p.v : p.k) + ((static_cast<long long>(b) * kv.kv_heads + head) * p.cap + key0 + i) * D;
-        });
+        const int slot = static_cast<int>(key) - p.by_page(static_cast<int>(key)) * kv.page_size;
+        const long long at = in ? page * kv.page_stride + slot * kv.slot_stride + 8 * piece : 0;
+        const uint16_t *pattern_at = p.sc.base + (in ? scale_offset(p.sc, page, slot) + piece / 4 : 0);
+        const long long head = static_cast<long long>(p.cap) * D, to = b * heads * head + key * D + 16 * piece;
+        // keys' heads and then values', kAhead loads under way
+        for (int e0 = side; e0 < 2 * heads; e0 += kAhead * kSide) {
+            uint2 w[kAhead];
+            uint32_t pattern[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int e = e0 + u * kSide, h = e < heads ? e : e - heads;
+                w[u] = make_uint2(0u, 0u);
+                pattern[u] = 0;
+                if (in && e < 2 * heads) {
+                    const uint8_t *src = static_cast<const uint8_t *>(e < heads ? kv.k : kv.v) + at + h * kv.head_stride;
+                    w[u] = __ldcs(reinterpret_cast<const uint2 *>(src));
+                    pattern[u] = pattern_at[(e < heads ? 0 : kGroups) + h * p.sc.head];
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int e = e0 + u * kSide;
+                if (e >= 2 * heads)
+                    break;
+                const GroupScale<BF16> sc(pattern[u]);
+                const uint4 x = sc.values(w[u].x), y = sc.values(w[u].y);
+                uint16_t *dst = e < heads ? p.k + to + e * head : p.v + to + (e - heads) * head;
+                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(x.x), "r"(x.y),
+                             "r"(x.z), "r"(x.w), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
+                             : "memory");
+            }
+        }
     }
 }
 

@@ -174,8 +174,19 @@ def test_longer_than_max_kv_is_recorded(q):
     q.qmm_kv4_attn(bt.q, *bt.args(), 1100, 4000)
     assert status(q) == 0
     # than the table
-    short = q.qmm_kv4_attn(bt.q, *bt.args()[:3], bt.table[:, :120].contiguous(), *bt.args()[4:], 1100, 4000)
+    ws = torch.empty(q.qmm_kv4_attn_workspace(64, 8, 128, 1100) +
+                     q.qmm_kv4_attn_more_workspace(1, 1100, 64, 8, 128, 1100, 2500), dtype=torch.uint8, device="cuda")
+    run = lambda table: q.qmm_kv4_attn(bt.q, *bt.args()[:3], table, *bt.args()[4:], 1100, 2500, workspace=ws.fill_(255))
+    short = run(bt.table[:, :120].contiguous())
     assert status(q) == 10 and torch.isfinite(short).all()
+    # pages that are not there: keys and values of zeros
+    bad = bt.table.clone()
+    bad[0, 3] = -1
+    bad[0, 7] = bt.k_cache.shape[0]
+    got = run(bad)
+    assert status(q) == 10
+    direct = q.qmm_kv4_attn(bt.q, *bt.args()[:3], bad, *bt.args()[4:], 1100, 2500, workspace=ws[:-4096])
+    assert status(q) == 10 and torch.equal(got, direct)
     # than max_kv
     assert q.qmm_kv4_attn_more_workspace(1, 1100, 64, 8, 128, 1100, 2300) > 0
     q.qmm_kv4_attn(bt.q, *bt.args(), 1100, 2300)
