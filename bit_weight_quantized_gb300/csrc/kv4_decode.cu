@@ -20,14 +20,17 @@
 //
 // Queries are scaled per row by a power of two to below 2^15 and are then fp16 (bf16 has
 // 8 bits, so only values 2^-25 times the row's largest lose any).  A weight times its V
-// scale is rounded once to fp16, 2^-12 relative, with a power of two taken out that follows
-// the largest scale seen as the maximum follows the scores; that the zeros' share is
-// subtracted by the same rounded weights comes from one more product, of the zeros.
+// scale is rounded once to fp16, 2^-12 relative, times a power of two of its row and group that
+// follows the largest such product so far (2^7 to 2^16 then), as the maximum follows the scores:
+// what a key's large values take from the others' bits depends on its weight, in the group that
+// holds them and the rows that see it.  (One power of two per warp, from the largest scale, left
+// nothing of keys 2^-32 times that scale, whatever its weight; 64 sequences 51.4 us with it, 52.1.)
+// That the zeros' share is subtracted by the same rounded weights comes from one more product, of the zeros.
 //
 // Bound by instruction issue as much as by the cache's bytes (D + D / 16 per key and head): 300
 // instructions a warp for 16 keys of 128 in the loop, 2176 bytes, which the copy rate brings in
-// 93 cycles, 372 issue slots.  64 sequences of 300 to 4096 keys, 8 key heads: 51.7 us (copies
-// alone 36, the first form of this kernel 58.5); one token over 131072 keys 44.5.  Each of a
+// 93 cycles, 372 issue slots.  64 sequences of 300 to 4096 keys, 8 key heads: 52.1 us (copies
+// alone 36, the first form of this kernel 58.5); one token over 131072 keys 44.7.  Each of a
 // block's warps walks its own keys with its own ring of asynchronous copies, maximum, sum and
 // output, as in attn_decode.cu, whose split, clusters and end this has.
 #include <atomic>
@@ -106,6 +109,26 @@ __device__ __forceinline__ void halves(uint32_t w, float &lo, float &hi)
     }
 }
 
+__device__ __forceinline__ uint32_t max16x2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// Column e of a group's output fragments, and of the zeros' share, times 2^ex (ex <= 0).
+__device__ __forceinline__ void scale_output(float (&o)[4][4], float (&oz)[4], int e, int ex)
+{
+    const float by = __uint_as_float(static_cast<uint32_t>(max(127 + ex, 0)) << 23);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        o[i][e] *= by;
+        o[i][2 + e] *= by;
+    }
+    oz[e] *= by;
+    oz[2 + e] *= by;
+}
+
 template <int D, bool BF16, int WARPS, int NB>
 __global__ void __launch_bounds__(32 * WARPS, kv4_blocks_per_sm(8 * NB, WARPS))
 kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p)
@@ -116,11 +139,10 @@ kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p)
     constexpr int kChunks = D / 32;                    // 16-byte chunks of a key's codes
     constexpr int kRowsPerCopy = 32 / kChunks, kCopies = kWarpKeys / kRowsPerCopy;
     constexpr int kLook = kWarpKeys / 32;              // keys whose place a lane looks up, per tile
-    // weights are 2^(s - m + 7), at most 2^15: times a V scale over a power of two above it, they
-    // are rounded to fp16
+    // weights are 2^(s - m + 7), at most 2^15: times a V scale and f, they are rounded to fp16
     constexpr float kShift = 7.f;
     constexpr uint32_t kM0 = 0x000f000fu, kM1 = 0x00f000f0u, kMB = 0x00ff00ffu, kScaleBits = 0xfff0fff0u;
-    constexpr int kExpBits = BF16 ? 7 : 10, kBias = BF16 ? 127 : 15, kLeastExp = BF16 ? 63 : 1, kMostExp = BF16 ? 253 : 30;   // of a scale pattern
+    constexpr int kMostF = 127 + 112;                  // f's exponent field at most: 2^15 times it is a number
 
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Share share;
@@ -351,15 +373,20 @@ kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p)
                     for (int i = 0; i < 4; ++i)
                         o[nb][gr][i][e] = 0.f;
                 }
-        float m[NB][2], l[NB][2];                    // maximum (a power of two), sum
-        float limit[NB][2], minus[NB][2];            // the score past which it is replaced, kShift - maximum
+        // kShift - the maximum (a whole number), the score past which it is replaced (-infinity: there
+        // is none yet), the sum; per group f, the power of two by which weights times V scales are taken
+        float minus[NB][2], limit[NB][2], l[NB][2], f[NB][kGroups][2];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
-            m[nb][0] = m[nb][1] = limit[nb][0] = limit[nb][1] = -INFINITY, l[nb][0] = l[nb][1] = 0.f, minus[nb][0] = minus[nb][1] = kShift;
-        // V's patterns so far are below that of 2^(vex - kBias); weights and their sums are taken
-        // times its inverse, which leaves a weight times its V scale at 2^15 at most
-        uint32_t vlimit = 0;
-        int vex = kBias;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                minus[nb][e] = kShift;
+                limit[nb][e] = -INFINITY;
+                l[nb][e] = 0.f;
+#pragma unroll
+                for (int gr = 0; gr < kGroups; ++gr)
+                    f[nb][gr][e] = __uint_as_float(kMostF << 23);
+            }
 
 #pragma unroll 1
         for (int j = 0; j < sg.units; ++j) {
@@ -425,7 +452,7 @@ kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p)
                                     s[st][nb][e] = -INFINITY;
                             }
                 }
-                // a new maximum of some row, or a larger V scale?
+                // a new maximum of some row?
                 float most[NB][2];
                 bool up = false;
 #pragma unroll
@@ -438,75 +465,128 @@ kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p)
                             most[nb][e] = fmaxf(most[nb][e], fmaxf(s[st][nb][e], s[st][nb][2 + e]));
                         up |= most[nb][e] > limit[nb][e];
                     }
-                uint32_t big = 0;
+                if (__any_sync(0xffffffffu, up)) {
+                    // exponents of the V scales (of a step's keys g and g + 8): a row's first f follows from them
+                    // and the scores (by the pass below, like later ones, 64 sequences took 53.4 us)
+                    float ea[kSteps][2][kGroups];
 #pragma unroll
-                for (int i = 0; i < kLook; ++i) {
-                    const uint32_t u = lds32(rd + 2 * L::kCodes + (lane + 32 * i) * L::kScaleRow + (kGroups == 2 ? 4 : 0));
-                    big = max(big, u >> 16);
-                    if (kGroups == 2)
-                        big = max(big, u & 0xffffu);
-                }
-                if (__any_sync(0xffffffffu, up || big >= vlimit)) {
-                    constexpr uint32_t kInf = BF16 ? 0x7f80u : 0x7c00u;      // (patterns of groups that hold NaN lie above)
-                    big = __reduce_max_sync(0xffffffffu, big >= kInf ? 0u : big);
-                    float vf = 1.f;
-                    if (big >= vlimit) {
-                        const int ex = min(max(static_cast<int>(big >> kExpBits) + 1, kLeastExp), kMostExp);
-                        vf = __uint_as_float(static_cast<uint32_t>(max(127 + vex - ex, 0)) << 23);
-                        vex = ex;
-                        vlimit = static_cast<uint32_t>(ex) << kExpBits;
-                    }
+                    for (int st = 0; st < kSteps; ++st)
 #pragma unroll
-                    for (int nb = 0; nb < NB; ++nb) {
-                        float f[2];
+                        for (int k = 0; k < 2; ++k) {
+                            float a[2];
+                            halves<BF16>(lds32(rd + at_s + (16 * st + 8 * k) * L::kScaleRow + (kGroups == 2 ? 4 : 0)) & kScaleBits, a[0], a[1]);
+#pragma unroll
+                            for (int gr = 0; gr < kGroups; ++gr)
+                                ea[st][k][gr] = static_cast<float>(static_cast<int>(__float_as_uint(a[kGroups == 2 ? gr : 1]) >> 23) - 127);
+                        }
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            float x = most[nb][e];
+                            float x = most[nb][e], c[kGroups];
 #pragma unroll
-                            for (int d = 4; d < 32; d <<= 1)
-                                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-                            const bool grow = x > limit[nb][e];
-                            x *= rowf[nb][e];
-                            const float a = grow ? ex2(m[nb][e] - x) : 1.f;
-                            if (grow) {
-                                m[nb][e] = x;
-                                limit[nb][e] = (x + kGrow) / rowf[nb][e];
+                            for (int gr = 0; gr < kGroups; ++gr) {
+                                c[gr] = -INFINITY;
+#pragma unroll
+                                for (int st = 0; st < kSteps; ++st)
+                                    c[gr] = fmaxf(c[gr], fmaxf(fmaf(s[st][nb][e], rowf[nb][e], ea[st][0][gr]), fmaf(s[st][nb][2 + e], rowf[nb][e], ea[st][1][gr])));
                             }
-                            minus[nb][e] = kShift + static_cast<float>(kBias - vex) - (m[nb][e] == -INFINITY ? 0.f : m[nb][e]);
-                            f[e] = a * vf;
-                            l[nb][e] *= f[e];
+#pragma unroll
+                            for (int d = 4; d < 32; d <<= 1) {
+                                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+#pragma unroll
+                                for (int gr = 0; gr < kGroups; ++gr)
+                                    c[gr] = fmaxf(c[gr], __shfl_xor_sync(0xffffffffu, c[gr], d));
+                            }
+                            if (x > limit[nb][e]) {
+                                x = ceilf(x * rowf[nb][e]);
+                                const bool none = limit[nb][e] == -INFINITY;
+                                // the sum falls; the output stays, and f rises (as far as it goes)
+                                const float by = none ? 0.f : fminf(fmaxf(x + minus[nb][e] - kShift, 0.f), 1024.f);
+                                l[nb][e] *= ex2(-by);
+                                minus[nb][e] = kShift - x;
+                                limit[nb][e] = (x + kGrow) / rowf[nb][e];
+#pragma unroll
+                                for (int gr = 0; gr < kGroups; ++gr) {
+                                    const int ex = none ? 127 + 6 - static_cast<int>(fminf(fmaxf(c[gr] + minus[nb][e], 6 - 112.f), 120.f))
+                                                        : static_cast<int>(__float_as_uint(f[nb][gr][e]) >> 23) + static_cast<int>(by);
+                                    f[nb][gr][e] = __uint_as_float(static_cast<uint32_t>(min(ex, kMostF)) << 23);
+                                    if (ex > kMostF)
+                                        scale_output(o[nb][gr], oz[nb][gr], e, kMostF - ex);
+                                }
+                            }
                         }
+                }
+                // weights; times their keys' V scales the right operand, turned over below
+                uint32_t pf[kSteps][NB][kGroups][2];
+                auto weighted = [&](bool first) {
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int st = 0; st < kSteps; ++st) {
+                        float v0[2], v1[2];              // V scales of keys g and g + 8
+                        halves<BF16>(lds32(rd + at_s + 16 * st * L::kScaleRow + (kGroups == 2 ? 4 : 0)) & kScaleBits, v0[0], v0[1]);
+                        halves<BF16>(lds32(rd + at_s + (16 * st + 8) * L::kScaleRow + (kGroups == 2 ? 4 : 0)) & kScaleBits, v1[0], v1[1]);
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb) {
+                            float(&w)[4] = s[st][nb];
+                            if (first) {
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    w[e] = ex2(fmaf(w[e], rowf[nb][e & 1], minus[nb][e & 1]));
+                                l[nb][0] += w[0] + w[2];
+                                l[nb][1] += w[1] + w[3];
+                            }
+#pragma unroll
+                            for (int gr = 0; gr < kGroups; ++gr) {
+                                const float a = v0[kGroups == 2 ? gr : 1], b = v1[kGroups == 2 ? gr : 1];
+                                pf[st][nb][gr][0] = pack16<false>(w[0] * f[nb][gr][0] * a, w[1] * f[nb][gr][1] * a);
+                                pf[st][nb][gr][1] = pack16<false>(w[2] * f[nb][gr][0] * b, w[3] * f[nb][gr][1] * b);
+                                top = max16x2(top, max16x2(pf[st][nb][gr][0], pf[st][nb][gr][1]));
+                            }
+                        }
+                    }
+                    return top;
+                };
+                // one that does not fit (an infinity): f comes down, and the output with it
+                if (__any_sync(0xffffffffu, (weighted(true) + 0x04000400u) & 0x80008000u)) {
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                         for (int gr = 0; gr < kGroups; ++gr)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                oz[nb][gr][e] *= f[e & 1];
+                            for (int e = 0; e < 2; ++e) {
+                                // the largest, times 2^-16 (products of weights up to 2^15 and scales stay numbers)
+                                float x = 0.f;
 #pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    o[nb][gr][i][e] *= f[e & 1];
+                                for (int st = 0; st < kSteps; ++st)
+#pragma unroll
+                                    for (int k = 0; k < 2; ++k) {
+                                        float a[2];
+                                        halves<BF16>(lds32(rd + at_s + (16 * st + 8 * k) * L::kScaleRow + (kGroups == 2 ? 4 : 0)) & kScaleBits,
+                                                     a[0], a[1]);
+                                        x = fmaxf(x, s[st][nb][2 * k + e] * 1.52587890625e-5f * a[kGroups == 2 ? gr : 1]);
+                                    }
+#pragma unroll
+                                for (int d = 4; d < 32; d <<= 1)
+                                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+                                const int ex = static_cast<int>(__float_as_uint(x) >> 23), was = static_cast<int>(__float_as_uint(f[nb][gr][e]) >> 23);
+                                if (ex + was >= 15 + 127 + 127 - 16) {   // 2^15 or more: to 2^7
+                                    const int now = max(7 + 127 + 127 - 16 - ex, 1);
+                                    f[nb][gr][e] = __uint_as_float(static_cast<uint32_t>(now) << 23);
+                                    scale_output(o[nb][gr], oz[nb][gr], e, now - was);
+                                }
                             }
-                    }
+                    weighted(false);
                 }
 #pragma unroll
                 for (int st = 0; st < kSteps; ++st) {
-                    // weights, times their keys' V scales, as the right operand
-                    uint32_t pf[NB][kGroups][2];
-                    float v0[2], v1[2];
-                    halves<BF16>(lds32(rd + at_s + 16 * st * L::kScaleRow + (kGroups == 2 ? 4 : 0)) & kScaleBits, v0[0], v0[1]);
-                    halves<BF16>(lds32(rd + at_s + (16 * st + 8) * L::kScaleRow + (kGroups == 2 ? 4 : 0)) & kScaleBits, v1[0], v1[1]);
 #pragma unroll
-                    for (int nb = 0; nb < NB; ++nb) {
-                        const float w0 = ex2(fmaf(s[st][nb][0], rowf[nb][0], minus[nb][0])), w1 = ex2(fmaf(s[st][nb][1], rowf[nb][1], minus[nb][1]));
-                        const float w2 = ex2(fmaf(s[st][nb][2], rowf[nb][0], minus[nb][0])), w3 = ex2(fmaf(s[st][nb][3], rowf[nb][1], minus[nb][1]));
-                        l[nb][0] += w0 + w2;
-                        l[nb][1] += w1 + w3;
+                    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                         for (int gr = 0; gr < kGroups; ++gr) {
-                            const float a = v0[kGroups == 2 ? gr : 1], b = v1[kGroups == 2 ? gr : 1];
-                            pf[nb][gr][0] = transpose8(pack16<false>(w0 * a, w1 * a));
-                            pf[nb][gr][1] = transpose8(pack16<false>(w2 * b, w3 * b));
+                            pf[st][nb][gr][0] = transpose8(pf[st][nb][gr][0]);
+                            pf[st][nb][gr][1] = transpose8(pf[st][nb][gr][1]);
                         }
-                    }
                     // output: rows are d, columns query rows
                     uint32_t zw[4];                          // the V scale words of the keys 2 t, 2 t + 1, + 8
 #pragma unroll
@@ -527,13 +607,13 @@ kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p)
                             const uint32_t a8 = __byte_perm(a, 0u, 0x4341u), b8 = __byte_perm(b, 0u, 0x4341u);
 #pragma unroll
                             for (int nb = 0; nb < NB; ++nb) {
-                                mma_f16_16816(o[nb][gr][2 * half], a & kM0, a & kMB, b & kM0, b & kMB, pf[nb][gr][0], pf[nb][gr][1]);
-                                mma_f16_16816(o[nb][gr][2 * half + 1], a8 & kM0, a8, b8 & kM0, b8, pf[nb][gr][0], pf[nb][gr][1]);
+                                mma_f16_16816(o[nb][gr][2 * half], a & kM0, a & kMB, b & kM0, b & kMB, pf[st][nb][gr][0], pf[st][nb][gr][1]);
+                                mma_f16_16816(o[nb][gr][2 * half + 1], a8 & kM0, a8, b8 & kM0, b8, pf[st][nb][gr][0], pf[st][nb][gr][1]);
                             }
                         }
 #pragma unroll
                         for (int nb = 0; nb < NB; ++nb)
-                            mma_f16_16816(oz[nb][gr], z0, 0u, z1, 0u, pf[nb][gr][0], pf[nb][gr][1]);
+                            mma_f16_16816(oz[nb][gr], z0, 0u, z1, 0u, pf[st][nb][gr][0], pf[st][nb][gr][1]);
                     }
                 }
             }
@@ -542,7 +622,7 @@ kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p)
         }
         cp_async_wait_group<0>();
         // a row's sum and output count 2^(s - m) in bf16, 2^7 times that in fp16 (row_log_sum)
-        const float unshift = __uint_as_float(static_cast<uint32_t>(127 + vex - kBias - (BF16 ? 7 : 0)) << 23);
+        constexpr float unshift = BF16 ? 1.f / 128 : 1.f;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -557,7 +637,7 @@ kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p)
         __syncthreads();
         float *wo = reinterpret_cast<float *>(smem);
         float *wml = reinterpret_cast<float *>(smem + L::kOffMl);
-        const float unit = 16777216.f * unshift;       // 2^24 for the codes
+        constexpr float unit = 16777216.f * unshift;   // 2^24 for the codes
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -565,18 +645,19 @@ kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p)
                 const int row = warp * kRows + 8 * nb + 2 * t + e;
 #pragma unroll
                 for (int gr = 0; gr < kGroups; ++gr) {
+                    const float back = __uint_as_float((254u << 23) - __float_as_uint(f[nb][gr][e]));   // 1 / f
                     float *w = wo + row * L::kPitch + gr * kKv4Group + 8 * g;
                     float v[8];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {    // values 2 i (of c), 2 i + 1 (of 16 c and the c before it)
-                        v[2 * i] = (o[nb][gr][i][e] - oz[nb][gr][e]) * unit;
-                        v[2 * i + 1] = fmaf(o[nb][gr][i][2 + e] - o[nb][gr][i][e], 0.0625f, -oz[nb][gr][e]) * unit;
+                        v[2 * i] = (o[nb][gr][i][e] - oz[nb][gr][e]) * unit * back;
+                        v[2 * i + 1] = fmaf(o[nb][gr][i][2 + e] - o[nb][gr][i][e], 0.0625f, -oz[nb][gr][e]) * unit * back;
                     }
                     *reinterpret_cast<float4 *>(w) = make_float4(v[0], v[1], v[2], v[3]);
                     *reinterpret_cast<float4 *>(w + 4) = make_float4(v[4], v[5], v[6], v[7]);
                 }
                 if (g == 0)
-                    *reinterpret_cast<float2 *>(wml + row * 2) = make_float2(m[nb][e], l[nb][e]);
+                    *reinterpret_cast<float2 *>(wml + row * 2) = make_float2(limit[nb][e] == -INFINITY ? -INFINITY : kShift - minus[nb][e], l[nb][e]);
             }
         __syncthreads();
         if (finish_rows<L, D, BF16, WARPS, kRows>(p, sg, smem))
