@@ -185,7 +185,9 @@ struct Quant {
     }
 };
 
-template <int D, bool BF16>
+// PART: only some of a head's threads rotate (0 < rot < D); the others' values are copied.  A kernel of
+// its own: with the choice in one, whole heads took 5 us more (8192 tokens of 80 heads).
+template <int D, bool BF16, bool PART>
 __global__ void __launch_bounds__(kThreads, 7)
 kv4_append_kernel(const __grid_constant__ Kv4AppendParams p)
 {
@@ -254,10 +256,8 @@ kv4_append_kernel(const __grid_constant__ Kv4AppendParams p)
     }
     uint64_t cs[4], sn[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        cs[i] = pair(1.f, 1.f);
-        sn[i] = 0;
-    }
+    for (int i = 0; i < 4; ++i)
+        cs[i] = sn[i] = 0;
     if (turn) {
         const ulonglong2 *row = reinterpret_cast<const ulonglong2 *>(p.cos_sin + static_cast<long long>(pos) * p.rot + 8 * item);
         const ulonglong2 *rows = reinterpret_cast<const ulonglong2 *>(p.cos_sin + static_cast<long long>(pos) * p.rot +
@@ -275,6 +275,8 @@ kv4_append_kernel(const __grid_constant__ Kv4AppendParams p)
     // Norm and rotation of a head's chunks, rounded to the type.  The whole warp comes here together;
     // what its columns without a head hold does not matter.
     auto turned = [&](uint4 &a, uint4 &b, bool norm) {
+        if (PART && !turn && !norm)
+            return;                                      // the same bits
         uint64_t x[4], y[4];
         unpack8<BF16>(a, x);
         unpack8<BF16>(b, y);
@@ -310,7 +312,7 @@ kv4_append_kernel(const __grid_constant__ Kv4AppendParams p)
                     z = pair(__fsub_rn(__fmul_rn(f.x, c), __fmul_rn(f.y, s)), __fadd_rn(__fmul_rn(f.y, c), __fmul_rn(f.x, s)));
                 }
             }
-        } else if (p.rot > 0) {                          // (threads that do not turn: by cosines of one)
+        } else if (PART ? turn : p.rot > 0) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint64_t x0 = x[i], y0 = y[i];
@@ -404,8 +406,8 @@ kv4_append_kernel(const __grid_constant__ Kv4AppendParams p)
     }
 }
 
-template <int D, bool BF16>
-cudaError_t launch_append(const Kv4AppendParams &p, cudaStream_t stream)
+template <int D, bool BF16, bool PART>
+cudaError_t launch_part(const Kv4AppendParams &p, cudaStream_t stream)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p.kv.tokens);
@@ -416,7 +418,13 @@ cudaError_t launch_append(const Kv4AppendParams &p, cudaStream_t stream)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kv4_append_kernel<D, BF16>, p);
+    return cudaLaunchKernelEx(&cfg, kv4_append_kernel<D, BF16, PART>, p);
+}
+
+template <int D, bool BF16>
+cudaError_t launch_append(const Kv4AppendParams &p, cudaStream_t stream)
+{
+    return p.rot > 0 && p.rot < D ? launch_part<D, BF16, true>(p, stream) : launch_part<D, BF16, false>(p, stream);
 }
 
 }  // namespace
