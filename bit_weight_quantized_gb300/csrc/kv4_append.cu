@@ -9,14 +9,15 @@
 //   z = rint(-lo / s),  c = clamp(rint(x / s) + z, 0, 15)
 //
 // in fp32 with correctly rounded quotients and, in the rotation, without fused multiply-adds, so
-// that a plain computation step by step gives the same codes.  x / s is a tie exactly when the
+// that a plain computation step by step gives the same codes where there are no norms (whose sum of
+// squares has an order of its own, and whose root is rsqrtf's).  x / s is a tie exactly when the
 // division says so: x and s have 11 and 7 bits at most, and a quotient that is no tie is
 // further from one than fp32 rounds.
 //
 // Bound by memory, like kv_append.cu, whose layout this has, and nearly as much by
 // instructions: a block serves a token, thread i of a column of head_dim / 16 owns two 8-value
 // chunks of a head.  The sums and the extremes of a head meet by shuffles within the column.
-// 8192 tokens of 80 heads of 128: 63 us with norms, 55 without (4.9 and 5.7 TB/s); with
+// 8192 tokens of 80 heads of 128: 61.4 us with norms, 53.9 without (5.1 and 5.8 TB/s); with
 // divisions and one loop over all heads 93.
 #include "kv4.cuh"
 
@@ -281,19 +282,34 @@ kv4_append_kernel(const __grid_constant__ Kv4AppendParams p)
         unpack8<BF16>(a, x);
         unpack8<BF16>(b, y);
         if (norm) {
-            uint64_t s2 = mul2(x[0], x[0]);
+            auto squares = [&] {
+                uint64_t s2 = mul2(x[0], x[0]);
 #pragma unroll
-            for (int i = 1; i < 4; ++i)
-                s2 = fma2(x[i], x[i], s2);
+                for (int i = 1; i < 4; ++i)
+                    s2 = fma2(x[i], x[i], s2);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                s2 = fma2(y[i], y[i], s2);
-            const float2 f = unpair(s2);
-            float ss = f.x + f.y;
+                for (int i = 0; i < 4; ++i)
+                    s2 = fma2(y[i], y[i], s2);
+                const float2 f = unpair(s2);
+                float ss = f.x + f.y;
 #pragma unroll
-            for (int d = 1; d < kItems; d <<= 1)
-                ss += __shfl_xor_sync(0xffffffffu, ss, d);
-            const float r = rsqrtf(fmaf(ss, 1.f / D, p.eps));
+                for (int d = 1; d < kItems; d <<= 1)
+                    ss += __shfl_xor_sync(0xffffffffu, ss, d);
+                return ss;
+            };
+            float mean = fmaf(squares(), 1.f / D, p.eps);
+            // bf16 heads whose squares leave fp32's range: times a power of two first
+            if (BF16 && __any_sync(0xffffffffu, !(mean < 0x1p120f) || mean < 0x1p-80f)) {
+                const float c = mean < 0x1p-80f ? 0x1p100f : mean < 0x1p120f ? 1.f : 0x1p-70f;
+                const uint64_t c2 = pair(c, c);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[i] = mul2(x[i], c2);
+                    y[i] = mul2(y[i], c2);
+                }
+                mean = fmaf(squares(), 1.f / D, p.eps * c * c);
+            }
+            const float r = rsqrtf(mean);
             const uint64_t r2 = pair(r, r);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {

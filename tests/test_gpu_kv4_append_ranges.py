@@ -45,3 +45,40 @@ def test_what_is_not_rotated_is_copied(q, dtype, D, rot, interleaved):
         ref = rotate(x[..., :rot], torch.arange(4, 9, device="cuda"), cs, interleaved)
         near = x[..., :rot].double().abs().amax(-1, keepdim=True)
         assert ((got[..., :rot].double() - ref).abs() <= torch.finfo(bt.dt).eps / 2 * ref.abs() + 2.0 ** -22 * near).all()
+
+
+# Heads so large or small that their squares are no fp32 numbers, beside ordinary ones in a token.
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype,size,eps", [
+    ("bf16", 2.0 ** 62, 1e-6), ("bf16", 1e20, 1e-6), ("bf16", 1e37, 1e-6), ("bf16", 1e20, 0.0), ("bf16", 1e-18, 0.0),
+    ("bf16", 1e-25, 0.0), ("bf16", 1e-37, 0.0), ("bf16", 1e-25, 1e-6), ("bf16", 1e-25, 1e-45), ("bf16", 1e-25, 1e-30),
+    ("bf16", 1e15, 1e37), ("f16", 1e4, 1e-6), ("f16", 1e-6, 0.0)])
+@pytest.mark.parametrize("rot", [0, 32, 64])
+def test_norms_of_large_and_small_heads(q, dtype, size, eps, D, rot):
+    bt = Batch4([6], [9], 6, 2, D, dtype, fill=False)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(D + rot)
+    qkv = torch.randn((6, 10, D), generator=g, device="cuda").double()
+    qkv[::2, ::2] *= size
+    qkv[1, 5] *= size
+    qkv[2, 4, ::2] = 0.0
+    qkv = qkv.to(bt.dt)
+    w = [(1 + torch.randn(D, generator=g, device="cuda") / 4).to(bt.dt) for _ in range(2)]
+    cs = cos_sin_table(9, rot) if rot else None
+    got = q.qmm_kv4_append(qkv[:, 6:8], qkv[:, 8:], *bt.args(), q=qkv[:, :6], cos_sin=cs, q_norm=w[0], k_norm=w[1], eps=eps)
+    k = q.qmm_kv4_read(*bt.args(), 6)[0]
+    assert status(q) == 0
+    for x, weight, y in ((qkv[:, :6], w[0], got), (qkv[:, 6:8], w[1], k)):
+        eps32 = float(torch.tensor(eps))                         # what the call takes
+        x = x.double()
+        ref = x / torch.sqrt(x.square().mean(-1, keepdim=True) + eps32) * weight.double()
+        ref = rotate(ref, torch.arange(3, 9, device="cuda"), cs, False)
+        # as with ordinary heads: D / 2 + 8 roundings of 2^-24, a rotated value below 2 max |x|; the output's rounding,
+        # half a step of the type's smallest numbers at least
+        f = torch.finfo(bt.dt)
+        tol = f.eps / 2 * ref.abs() + 2 * (D / 2 + 8) * 2.0 ** -24 * ref.abs().amax(-1, keepdim=True) + f.tiny * f.eps / 2
+        if y is k:                                               # read back: within half a step, (hi - lo) / 15 and 9 / 8 of it
+            near = ref.unflatten(-1, (-1, 64))
+            step = (near.amax(-1).clamp(min=0) - near.amin(-1).clamp(max=0)) / 15 * 9 / 8 + 2.0 ** (-129 if dtype == "bf16" else -20)
+            tol = tol + step.repeat_interleave(64, -1) * (0.5 + 2.0 ** -6)
+        assert ((y.double() - ref).abs() <= tol).all()
