@@ -122,10 +122,15 @@ struct Quant {
     {
         constexpr uint32_t kLow = BF16 ? (1u << 20) - 1 : (1u << 17) - 1;   // the bits that s does not have
         constexpr float kLarge = BF16 ? 1.5e38f : 32000.f;
-        const float x = __fdiv_rn(__fsub_rn(hi * 0.5f, lo * 0.5f), 7.5f);   // (hi - lo may overflow)
+        // (half of hi - lo, which may overflow, rounded up; an s times 7.5 is exact)
+        const float d = __fsub_ru(hi * 0.5f, lo * 0.5f), x = __fmul_rz(d, 0x1.11111p-3f);   // 1 / 7.5 and x are cut off
         s = __uint_as_float((__float_as_uint(x) + kLow) & ~kLow);
-        if (!BF16 && x < 6.103515625e-5f)                                   // below the normal numbers: steps of 2^-20
+        float next = __uint_as_float(__float_as_uint(s) + kLow + 1);
+        if (!BF16 && x < 6.103515625e-5f) {                                 // below the normal numbers: steps of 2^-20
             s = ceilf(x * 1048576.f) * 9.5367431640625e-7f;
+            next = s + 9.5367431640625e-7f;
+        }
+        s = s * 7.5f < d ? next : s;                                        // where the quotient lies just above the cut one
         z = s > 0.f ? fminf(rintf(__fdiv_rn(-lo, s)), 15.f) : 0.f;
         large = hi > kLarge || lo < -kLarge;
         pattern = (pack16<BF16>(s, 0.f) & 0xfff0u) | static_cast<uint32_t>(z);

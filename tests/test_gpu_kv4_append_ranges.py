@@ -5,7 +5,7 @@ import math
 import pytest
 import torch
 
-from kv4_ref import Batch4, rotate
+from kv4_ref import Batch4, pack, patterns, quantize, rotate, values
 from paged_ref import cos_sin_table
 
 pytestmark = pytest.mark.gpu
@@ -82,3 +82,30 @@ def test_norms_of_large_and_small_heads(q, dtype, size, eps, D, rot):
             step = (near.amax(-1).clamp(min=0) - near.amin(-1).clamp(max=0)) / 15 * 9 / 8 + 2.0 ** (-129 if dtype == "bf16" else -20)
             tol = tol + step.repeat_interleave(64, -1) * (0.5 + 2.0 ** -6)
         assert ((y.double() - ref).abs() <= tol).all()
+
+
+# Groups whose (hi - lo) / 15 is a number of the scale's bits, or above one by less than fp32 can tell.
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_scales_next_to_a_step(q, dtype, D):
+    bt = Batch4([60], [60], 1, 1, D, dtype, fill=False)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    hi, size = torch.arange(1, 16, device="cuda").double(), (0.25 if dtype == "bf16" else 128.0)
+    v = torch.zeros((60, 1, D), dtype=torch.float64, device="cuda")
+    for i in range(60):
+        top = float(hi[i % 15]) * (15 if i < 30 else 1) * size
+        x = torch.rand(D, generator=g, device="cuda").double() * top
+        x[::64] = top
+        if i % 2:
+            x[7::64] = -top * 2.0 ** (i % 15 - 30) if dtype == "bf16" else -2.0 ** -24
+        v[i, 0] = -x if i % 4 > 1 else x
+    v = v.to(bt.dt)
+    q.qmm_kv4_append(v, v, *bt.args())
+    got = q.qmm_kv4_read(*bt.args(), 60)[1]
+    assert status(q) == 0
+    c, s, z = quantize(v)
+    seq_page = bt.table.long()[0, torch.arange(60, device="cuda") // bt.page]
+    pats = bt.scales.view(torch.int16)[seq_page, torch.arange(60, device="cuda") % bt.page][..., D // 64:]
+    assert torch.equal(pats, patterns(s, z, bt.dt).view(torch.int16))
+    assert torch.equal(got.double(), values(pack(c), patterns(s, z, bt.dt)))
