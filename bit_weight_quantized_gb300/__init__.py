@@ -751,9 +751,11 @@ def qmm_kv4_attn(q, k_cache, v_cache, scales, block_table, cu_q, kv_len, max_q, 
                  window=0, sinks=0, return_lse=False, out=None, workspace=None):
     """qmm_paged_attn over a cache in 4 bits (k_cache, v_cache and scales as for
     qmm_kv4_append).  With a window, sinks: first tokens that stay visible to every
-    token.  workspace: uint8 scratch of qmm_kv4_attn_workspace() bytes (and
-    qmm_kv4_attn_more_workspace() for long prompts), allocated if None.  See
-    qmm_kv4_attn in qmm.h."""
+    token.  max_kv: at least the longest kv_len, or 0 (unknown); a bound here, not a
+    hint, since long prompts may see no keys past it (the device status says so).
+    workspace: uint8 scratch of qmm_kv4_attn_workspace() bytes and, for long prompts,
+    qmm_kv4_attn_more_workspace() (up to 1 GB); allocated if None.  See qmm_kv4_attn in
+    qmm.h."""
     if _lib is None:
         load()
     if scale is None:

@@ -487,6 +487,10 @@ QMM_API qmm_status qmm_kv4_read(const qmm_paged_kv4 *kv, void *k_out, void *v_ou
  *           j > p - window or j < sinks when window > 0.
  *   sinks    0, or the number of first tokens that a window leaves visible (sinks > 0
  *            needs window > 0).
+ *   max_kv   at least the longest kv_len, or 0 if unknown.  A bound, where qmm_paged_attn has a
+ *            hint: a call whose workspace has room for converted keys
+ *            (qmm_kv4_attn_more_workspace) takes a longer sequence as one of max_kv keys,
+ *            rounded up to 128, and records QMM_ERR_INDEX.
  * Queries must be finite (a NaN or an infinity makes its row NaN), in bf16 below 2^116;
  * bf16 values below 2^-80 lose bits.
  * Scores, maximum, sums and output are fp32.  Up to 16 query rows per key head (q_heads /
@@ -505,9 +509,9 @@ QMM_API size_t qmm_kv4_attn_workspace(int q_heads, int kv_heads, int head_dim, i
 /* Bytes beyond those with which a call of these sizes (max_kv: what it is called with) converts
  * its keys to 16 bits once, in the workspace, instead of once per 256 query rows: many new
  * tokens (of the batch's `tokens`, over all sequences) over many keys, without first tokens, up
- * to 1 GB; 0 for other calls and for a max_kv of 0.  The workspace is then 128-byte aligned.  A call that gets less does without; results differ
- * by the order of sums at most, under a window.  Keys from max_kv, rounded up to 128, on are
- * not seen, and QMM_ERR_INDEX is recorded. */
+ * to 1 GB; 0 for other calls and for a max_kv of 0.  The workspace is then 128-byte aligned.  A
+ * call that gets less does without; results differ by the order of sums at most, under a window,
+ * as long as max_kv is the bound that it has to be (see there). */
 QMM_API size_t qmm_kv4_attn_more_workspace(int batch, int tokens, int q_heads, int kv_heads, int head_dim,
                                            int max_q, int max_kv, int sinks);
 

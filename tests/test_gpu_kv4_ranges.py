@@ -219,3 +219,16 @@ def test_many_rows(q, dtype, base, r, D, ql, kl, heads, window, sinks):
         v[n - 1] *= 2.0 ** min(r, 20)
         store(bt, b, k.to(bt.dt), v.to(bt.dt))
     check(q, bt, few=False, window=window, sinks=sinks)
+
+
+# Where keys are converted once, max_kv bounds them: a longer sequence counts as one of so many, in whole tiles of 128.
+def test_longer_than_max_kv_counts_as_max_kv(q):
+    bt = Batch4([1100, 3], [2500, 40], 64, 8, 128, "bf16")
+    assert q.qmm_kv4_attn_more_workspace(2, 1103, 64, 8, 128, 1100, 2300) > 0
+    got = q.qmm_kv4_attn(bt.q, *bt.args(), 1100, 2300)
+    torch.cuda.synchronize()
+    assert q.qmm_device_status() == 10
+    bt.kv_len[0] = 2304
+    want = q.qmm_kv4_attn(bt.q, *bt.args(), 1100, 2304)
+    torch.cuda.synchronize()
+    assert q.qmm_device_status() == 0 and torch.equal(got, want)
