@@ -491,12 +491,14 @@ QMM_API qmm_status qmm_kv4_read(const qmm_paged_kv4 *kv, void *k_out, void *v_ou
  *            hint: a call whose workspace has room for converted keys
  *            (qmm_kv4_attn_more_workspace) takes a longer sequence as one of max_kv keys,
  *            rounded up to 128, and records QMM_ERR_INDEX.
- * Queries must be finite (a NaN or an infinity makes its row NaN), in bf16 below 2^116;
- * bf16 values below 2^-80 lose bits.
- * Scores, maximum, sums and output are fp32.  Up to 16 query rows per key head (q_heads /
+ * Queries must be finite (a NaN or an infinity makes its row NaN), in bf16 below 2^116.
+ * Maximum, sums and output are fp32.  Up to 16 query rows per key head (q_heads /
  * kv_heads * new tokens), and more in small batches, the codes are multiplied as they are and
- * the weights rounded to fp16 once; for more the values, exact in dtype, are, and the weights
- * are rounded to dtype.
+ * the weights, times the values' scales, rounded to fp16 once.  Of a product with a code 2^-14 of
+ * a step s is kept: a score is off by head_dim 2^-14 s max |q| scale at most, an output by 2^-9 of
+ * the weighted mean of its group's steps (by some 2^-15 as measured; the codes' own rounding is s / 2).
+ * For more rows the values, exact in dtype, are multiplied, with scores in fp32, and the weights rounded
+ * to dtype.
  * Everything else, the workspace (qmm_kv4_attn_workspace) among it, is qmm_paged_attn's. */
 QMM_API qmm_status qmm_kv4_attn(const qmm_paged_kv4 *kv, const void *q, int64_t q_stride, int q_heads, float scale,
                                 int causal, int window, int sinks, void *out, float *lse, int max_q, int max_kv,
