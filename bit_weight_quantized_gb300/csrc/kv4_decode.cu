@@ -324,7 +324,7 @@ kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p)
             if (e % 8 == 0)                          // minus the group's sum, the scores' factor
                 rows[e % kWords / 8] = -sum;
             if (e % kWords == 0)                     // (not zero, which times a hidden score, -infinity, is NaN)
-                rows[2] = fmaxf(__uint_as_float((ex + 10u) << 23) * p.scale_log2, 1.17549435e-38f);
+                rows[2] = fmaxf(__uint_as_float((ex + 10u) << 23) * p.scale_log2, __uint_as_float(1));
         }
         __syncthreads();
         uint32_t qf[NB][kGroups][4][2];

@@ -491,7 +491,8 @@ QMM_API qmm_status qmm_kv4_read(const qmm_paged_kv4 *kv, void *k_out, void *v_ou
  *            hint: a call whose workspace has room for converted keys
  *            (qmm_kv4_attn_more_workspace) takes a longer sequence as one of max_kv keys,
  *            rounded up to 128, and records QMM_ERR_INDEX.
- * Queries must be finite (a NaN or an infinity makes its row NaN), in bf16 below 2^116.
+ * Queries must be finite (a NaN or an infinity makes its row NaN), they and their products with
+ * scale below 2^116.
  * Maximum, sums and output are fp32.  Up to 16 query rows per key head (q_heads /
  * kv_heads * new tokens), and more in small batches, the codes are multiplied as they are and
  * the weights, times the values' scales, rounded to fp16 once.  Of a product with a code 2^-14 of

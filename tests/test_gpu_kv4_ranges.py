@@ -221,6 +221,27 @@ def test_many_rows(q, dtype, base, r, D, ql, kl, heads, window, sinks):
     check(q, bt, few=False, window=window, sinks=sinks)
 
 
+# Scores of ordinary size from sizes at the ends of the type's.
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("ql", [[1], [3]])
+@pytest.mark.parametrize("q_e,k_e,scale_e", [(-70, 124, -70), (-110, 120, -29), (100, -110, -1), (-100, -20, 115), (10, -122, 104)])
+def test_scores_of_large_and_small_factors(q, D, ql, q_e, k_e, scale_e):
+    bt = Batch4(ql, [300], 8, 2, D, "bf16", fill=False)
+    bt.k64, bt.v64 = [None], [None]
+    g = torch.Generator(device="cuda")
+    g.manual_seed(D)
+    k, v = (torch.randn((300, 2, D), generator=g, device="cuda").clamp(-3, 3) for _ in range(2))
+    store(bt, 0, (k.double() * 2.0 ** k_e).to(bt.dt), v.to(bt.dt))
+    bt.q = (bt.q.double().clamp(-3, 3) * 2.0 ** q_e).to(bt.dt)
+    got, lse = q.qmm_kv4_attn(bt.q, *bt.args(), ql[0], 300, scale=2.0 ** scale_e, return_lse=True)
+    torch.cuda.synchronize()
+    assert q.qmm_device_status() == 0
+    # (the reference's scale is D^-0.5)
+    bt.q = bt.q.double() * 2.0 ** scale_e * D ** 0.5
+    ref, tol, ls, ltol = reference(bt, True)
+    assert ((got.double() - ref).abs() <= tol).all() and ((lse.double() - ls).abs() <= ltol).all()
+
+
 # Where keys are converted once, max_kv bounds them: a longer sequence counts as one of so many, in whole tiles of 128.
 def test_longer_than_max_kv_counts_as_max_kv(q):
     bt = Batch4([1100, 3], [2500, 40], 64, 8, 128, "bf16")
