@@ -46,7 +46,7 @@
 // type) in the K and V rings.  Four warps that fetched codes by plain loads took 4500 cycles for
 // a pair of tiles, half of it for ten loads in a queue behind the softmax's instructions (512
 // tokens over 16384 keys 126 us, now 107; 97 without the conversions, as over the 16-bit
-// cache).  Not kept: eight converting warps (133; fewer registers for the softmax),
+// cache).  Not kept: eight converting warps (120; fewer registers for the softmax),
 // exponentials by a polynomial on the FMA pipe for every fourth weight (140).
 //
 // Bound by the tensor cores at D = 128 (a causal prompt of 8192 tokens x 64 heads: 1655

@@ -18,16 +18,16 @@ constexpr int kMinUnits = 3, kMinChunkUnits = 4;
 // Few rows, whole items in clusters against a split over all blocks: a cluster's block walks
 // units / c, a split one units * items / blocks and the joining kernel's time, some
 // kJoinUnits; and not more than kMostUnits, since whole items are not balanced where
-// lengths differ.  One token over 4000 keys of 8 heads 8.3 us in clusters of 8 (4: 10.6, 1:
-// 25.4, split 10.9); 16 over 2000 14.5 in 2 (split 18.7), 32 over 4000 41.0 in 1 (42.9).
+// lengths differ.  One token over 4000 keys of 8 heads 7.6 us in clusters of 8 (4: 9.9, 1:
+// 24.6, split 11.1); 16 over 2000 15.1 in 2 (split 19.3), 32 over 4000 40.4 in 1 (42.5).
 constexpr int kJoinUnits = 4, kMostUnits = 10;
 
 // Few rows, whole items in blocks of four warps, more of them than run at once: blocks start as
 // others end, without a joining kernel and with fewer items cut in two; at the end the
 // last ones run alone, which costs the more the longer the items and the fewer they are.  Up
 // to kWholeUnits units and kMoreUnits for each time that the blocks are filled: 512 items of 700
-// keys 18.9 us (split 23.3), of 140 .. 1400 29.1 (29.1), of 280 .. 2800 50.9 (42.0); 2048 of
-// 1400 96.1 (102.8), of 280 .. 2800 130 (129), of 560 .. 5600 244 (237).
+// keys 19.1 us (split 24.3), of 140 .. 1400 27.0 (27.0), of 280 .. 2800 49.2 (41.6); 2048 of
+// 1400 95.4 (105.9), of 280 .. 2800 115.5 (117.2), of 560 .. 5600 223 (213).
 constexpr int kWholeUnits = 6, kMoreUnits = 5;
 
 // Many rows: work of the longest item (setup and units) up to which blocks take whole items,
@@ -36,25 +36,26 @@ constexpr int kUnsplitWork = 12, kWholeWork = 10;
 
 // Rows (token, query head) per key head of the kernel for few rows: two column tiles of the
 // matrix instructions.  More go to it, sixteen at a time, where these items all run at once in
-// clusters (128 rows over 2000 keys 13.3 us, many-row kernel 16.7; but 32 over 2000 of 64
-// sequences 114 and 108).
+// clusters (128 rows over 2000 keys 13.1 us, many-row kernel 16.3; but 32 over 2000 of 64
+// sequences 110 and 103).
 constexpr int kFewRows = 16;
 
 // Where keys are converted once, into scratch, and read by the 16-bit form of the kernel for many
 // rows, in place of by every row tile that sees them: it costs a launch and a pass over the keys,
 // and saves some of each tile's time per key.  So from so many row tiles, and so much work, tiles
-// x keys over all heads and sequences, on (us, by every tile and once; D 128):
-//   heads  new  keys    tiles  work      every    once
-//   64/8   128  16384   4      2^19      63.1     70.8
-//   64/8   256  16384   8      2^20      108.6    106.6
-//   8/8    2048 8192    8      2^19      58.5     58.8
-//   8/8    2048 16384   8      2^20      103.5    102.1
-//   64/8   1024 1024    32     2^18      38.5     39.2
-//   32/8   1024 4096    16     2^19      62.8     60.3
-//   32/8   2048 2048    32     2^19      51.9     47.8
-//   8/1    2048 2048    64     2^17      24.1     24.9
-//   8/1    1024 16384   32     2^19      61.1     57.0
-//   64/8   2048 16384   64     2^23      718.7    574.1
+// x keys over all heads and sequences, on (us, by every tile and once, for heads of 64 and of 128; in a
+// graph, codes at random; called one by one the launch costs some 2 us more):
+//   heads  new  keys    tiles  work      64: every  once     128: every  once
+//   64/8   128  16384   4      2^19      50.9       50.8     69.8        69.6
+//   64/8   256  16384   8      2^20      86.5       78.4     119.3       105.9
+//   8/8    2048 8192    8      2^19      46.4       44.3     64.8        58.7
+//   8/8    2048 16384   8      2^20      82.9       76.0     113.9       101.5
+//   64/8   1024 1024    32     2^18      32.3       29.5     42.0        37.0
+//   32/8   1024 4096    16     2^19      49.2       44.8     68.5        59.3
+//   32/8   2048 2048    32     2^19      37.9       34.8     54.9        47.2
+//   8/1    2048 2048    64     2^17      20.1       20.1     25.0        25.5
+//   8/1    1024 16384   32     2^19      48.1       46.0     61.3        59.2
+//   64/8   2048 16384   64     2^23      558        452      786         587
 constexpr int kUnpackTiles = 8;
 constexpr long long kUnpackWork = 1LL << 19;
 // Bytes of converted keys at most.

@@ -27,12 +27,13 @@
 // nothing of keys 2^-32 times that scale, whatever its weight; 64 sequences 51.4 us with it, 52.1.)
 // That the zeros' share is subtracted by the same rounded weights comes from one more product, of the zeros.
 //
-// Bound by instruction issue as much as by the cache's bytes (D + D / 16 per key and head): 300
-// instructions a warp for 16 keys of 128 in the loop, 2176 bytes, which the copy rate brings in
-// 93 cycles, 372 issue slots.  64 sequences of 300 to 4096 keys, 8 key heads: 52.1 us (copies
-// alone 36, the first form of this kernel 58.5); one token over 131072 keys 44.7.  Each of a
-// block's warps walks its own keys with its own ring of asynchronous copies, maximum, sum and
-// output, as in attn_decode.cu, whose split, clusters and end this has.
+// Bound by latency, with no unit full (DRAM 50%, issue 50%, logic pipe 51%, tensor 19% of a launch, of
+// which start and join take a third): a warp's tile goes from scores to maximum, weights and output in
+// order, with four warps a scheduler to cover it.  The loop takes some 307 instructions a warp for 16
+// keys of 128, 2176 bytes, which the copy rate brings in 372 issue slots.  64 sequences of 300 to 4096
+// keys, 8 key heads: 52.1 us (copies alone 36, the first form of this kernel 58.5); one token over 131072
+// keys 44.7.  Each of a block's warps walks its own keys with its own ring of asynchronous copies,
+// maximum, sum and output, as in attn_decode.cu, whose split, clusters and end this has.
 #include <atomic>
 #include <cuda_fp16.h>
 
