@@ -24,14 +24,14 @@
 // follows the largest such product so far (2^7 to 2^16 then), as the maximum follows the scores:
 // what a key's large values take from the others' bits depends on its weight, in the group that
 // holds them and the rows that see it.  (One power of two per warp, from the largest scale, left
-// nothing of keys 2^-32 times that scale, whatever its weight; 64 sequences 51.4 us with it, 52.1.)
+// nothing of keys 2^-32 times that scale, whatever its weight; 64 sequences 51.4 us with it, 52.4.)
 // That the zeros' share is subtracted by the same rounded weights comes from one more product, of the zeros.
 //
 // Bound by latency, with no unit full (DRAM 50%, issue 50%, logic pipe 51%, tensor 19% of a launch, of
 // which start and join take a third): a warp's tile goes from scores to maximum, weights and output in
 // order, with four warps a scheduler to cover it.  The loop takes some 307 instructions a warp for 16
 // keys of 128, 2176 bytes, which the copy rate brings in 372 issue slots.  64 sequences of 300 to 4096
-// keys, 8 key heads: 52.1 us (copies alone 36, the first form of this kernel 58.5); one token over 131072
+// keys, 8 key heads: 52.4 us (copies alone 36, the first form of this kernel 58.5); one token over 131072
 // keys 44.7.  Each of a block's warps walks its own keys with its own ring of asynchronous copies,
 // maximum, sum and output, as in attn_decode.cu, whose split, clusters and end this has.
 #include <atomic>
@@ -117,10 +117,9 @@ __device__ __forceinline__ uint32_t max16x2(uint32_t a, uint32_t b)
     return d;
 }
 
-// Column e of a group's output fragments, and of the zeros' share, times 2^ex (ex <= 0).
-__device__ __forceinline__ void scale_output(float (&o)[4][4], float (&oz)[4], int e, int ex)
+// Column e of a group's output fragments, and of the zeros' share, times `by`.
+__device__ __forceinline__ void scale_output(float (&o)[4][4], float (&oz)[4], int e, float by)
 {
-    const float by = __uint_as_float(static_cast<uint32_t>(max(127 + ex, 0)) << 23);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         o[i][e] *= by;
@@ -374,7 +373,7 @@ kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p)
                     for (int i = 0; i < 4; ++i)
                         o[nb][gr][i][e] = 0.f;
                 }
-        // kShift - the maximum (a whole number), the score past which it is replaced (-infinity: there
+        // kShift - the maximum, the score past which it is replaced (-infinity: there
         // is none yet), the sum; per group f, the power of two by which weights times V scales are taken
         float minus[NB][2], limit[NB][2], l[NB][2], f[NB][kGroups][2];
 #pragma unroll
@@ -500,20 +499,22 @@ kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p)
                                     c[gr] = fmaxf(c[gr], __shfl_xor_sync(0xffffffffu, c[gr], d));
                             }
                             if (x > limit[nb][e]) {
-                                x = ceilf(x * rowf[nb][e]);
+                                x *= rowf[nb][e];
                                 const bool none = limit[nb][e] == -INFINITY;
-                                // the sum falls; the output stays, and f rises (as far as it goes)
+                                // the largest score itself, so that its weight is a power of two and its product with a
+                                // scale exact.  The sum falls; f rises by whole powers of two, the output falls by the rest
                                 const float by = none ? 0.f : fminf(fmaxf(x + minus[nb][e] - kShift, 0.f), 1024.f);
                                 l[nb][e] *= ex2(-by);
                                 minus[nb][e] = kShift - x;
                                 limit[nb][e] = (x + kGrow) / rowf[nb][e];
 #pragma unroll
                                 for (int gr = 0; gr < kGroups; ++gr) {
-                                    const int ex = none ? 127 + 6 - static_cast<int>(fminf(fmaxf(c[gr] + minus[nb][e], 6 - 112.f), 120.f))
-                                                        : static_cast<int>(__float_as_uint(f[nb][gr][e]) >> 23) + static_cast<int>(by);
-                                    f[nb][gr][e] = __uint_as_float(static_cast<uint32_t>(min(ex, kMostF)) << 23);
-                                    if (ex > kMostF)
-                                        scale_output(o[nb][gr], oz[nb][gr], e, kMostF - ex);
+                                    const int was = static_cast<int>(__float_as_uint(f[nb][gr][e]) >> 23);
+                                    const int now = none ? 127 + 6 - static_cast<int>(fminf(fmaxf(c[gr] + minus[nb][e], 6 - 112.f), 120.f))
+                                                         : min(was + static_cast<int>(by), kMostF);
+                                    f[nb][gr][e] = __uint_as_float(static_cast<uint32_t>(now) << 23);
+                                    if (!none)
+                                        scale_output(o[nb][gr], oz[nb][gr], e, ex2(static_cast<float>(now - was) - by));
                                 }
                             }
                         }
@@ -574,7 +575,7 @@ kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p)
                                 if (ex + was >= 15 + 127 + 127 - 16) {   // 2^15 or more: to 2^7
                                     const int now = max(7 + 127 + 127 - 16 - ex, 1);
                                     f[nb][gr][e] = __uint_as_float(static_cast<uint32_t>(now) << 23);
-                                    scale_output(o[nb][gr], oz[nb][gr], e, now - was);
+                                    scale_output(o[nb][gr], oz[nb][gr], e, __uint_as_float(static_cast<uint32_t>(max(127 + now - was, 0)) << 23));
                                 }
                             }
                     weighted(false);

@@ -242,6 +242,20 @@ def test_scores_of_large_and_small_factors(q, D, ql, q_e, k_e, scale_e):
     assert ((got.double() - ref).abs() <= tol).all() and ((lse.double() - ls).abs() <= ltol).all()
 
 
+# A row that sees one key gives its value: the largest weight is rounded to nothing else than itself.
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("ql,kl,heads,window", [([1], [1], (8, 2), 0), ([1, 2], [500, 40], (8, 2), 1), ([4], [2000], (4, 1), 1),
+                                                ([400], [700], (8, 1), 1)])
+def test_one_key_gives_its_value(q, dtype, D, ql, kl, heads, window):
+    bt = Batch4(ql, kl, *heads, D, dtype)
+    out = q.qmm_kv4_attn(bt.q, *bt.args(), max(ql), max(kl), window=window)
+    torch.cuda.synchronize()
+    assert q.qmm_device_status() == 0
+    want = torch.cat([v[n - m:] for v, m, n in zip(bt.v64, ql, kl)]).repeat_interleave(heads[0] // heads[1], 1)
+    assert torch.equal(out.double(), want)
+
+
 # Where keys are converted once, max_kv bounds them: a longer sequence counts as one of so many, in whole tiles of 128.
 def test_longer_than_max_kv_counts_as_max_kv(q):
     bt = Batch4([1100, 3], [2500, 40], 64, 8, 128, "bf16")
